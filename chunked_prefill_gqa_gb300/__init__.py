@@ -36,11 +36,17 @@ ATTN_ESCRATCH = -11
 DECODE_SCRATCH_BYTES = 4 << 20
 MAX_TOKENS = 1 << 24
 PAGE = 16
+TREE_ROWS = 64     # drafted rows of one sequence
+F32, BF16 = 0, 1   # element types of the calls that take more than one
+ROPE_HALVES, ROPE_PAIRS = 0, 1   # the rotation turns dims (i, i + 32), or (2 i, 2 i + 1)
 
 # Every symbol the header declares (the CPU tests check the library exports them).
 EXPORTS = ("attn_prefill", "attn_prefill_bf16x3", "attn_prefill_bf16kv", "attn_prefill_host",
            "attn_prefill_bf16x3_host", "attn_prefill_bf16kv_host", "attn_full_causal", "attn_prefill_paged", "attn_decode_paged",
            "attn_decode_workspace_bytes", "attn_decode_paged_noalloc",
+           "attn_rope_table", "attn_qk_norm_rope", "attn_append_paged", "attn_append_paged_bf16kv",
+           "attn_tree_paged", "attn_tree_paged_bf16kv", "attn_tree_workspace_bytes",
+           "attn_compact_paged", "attn_compact_paged_bf16kv",
            "attn_naive_workspace_bytes", "attn_naive_scores", "attn_naive_softmax", "attn_naive_weighted_sum",
            "attn_naive_prefill", "attn_prefill_ffma", "attn_reference_prefill", "attn_selftest_timeout",
            "attn_selftest_decode_timeout", "attn_tensor_peak", "attn_get_device_error", "attn_strerror",
@@ -92,6 +98,26 @@ def load():
             lib.attn_decode_paged_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
             lib.attn_decode_workspace_bytes.restype = ctypes.c_size_t
             lib.attn_decode_workspace_bytes.argtypes = [ci, ci, ci]
+            cl, cf, cs = ctypes.c_longlong, ctypes.c_float, ctypes.c_size_t
+            lib.attn_rope_table.restype = ci
+            lib.attn_rope_table.argtypes = [vp, vp, ci, vp]
+            lib.attn_qk_norm_rope.restype = ci
+            lib.attn_qk_norm_rope.argtypes = [vp, vp, ci, cl, cl, vp, vp, cf, vp, vp, ci, ci, vp, vp, ci, ci, vp]
+            for name in ("attn_append_paged", "attn_append_paged_bf16kv"):
+                fn = getattr(lib, name)
+                fn.restype = ci
+                fn.argtypes = [vp, vp, vp, ci, cl, cl, cl, vp, vp, cf, vp, vp, ci, ci, vp, vp, vp, vp, vp, vp,
+                               ci, ci, ci, ci, vp]
+            for name in ("attn_tree_paged", "attn_tree_paged_bf16kv"):
+                fn = getattr(lib, name)
+                fn.restype = ci
+                fn.argtypes = [vp] * 8 + [ci] * 7 + [vp, cs, vp]
+            lib.attn_tree_workspace_bytes.restype = cs
+            lib.attn_tree_workspace_bytes.argtypes = [ci] * 5
+            for name in ("attn_compact_paged", "attn_compact_paged_bf16kv"):
+                fn = getattr(lib, name)
+                fn.restype = ci
+                fn.argtypes = [vp] * 6 + [ci] * 5 + [vp]
             lib.attn_naive_workspace_bytes.restype = ctypes.c_size_t
             lib.attn_naive_workspace_bytes.argtypes = [ci, ci]
             lib.attn_naive_scores.restype = ci
@@ -364,6 +390,242 @@ def attn_decode_paged_noalloc(q, kPages, vPages, blockTable, contextLens, out, m
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode_paged_noalloc")
     return out
+
+
+def _device_tensor(name, t, dtype, shape):
+    """t: a contiguous CUDA tensor of this dtype and shape (None in a shape: any)."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    got = t.shape
+    if len(got) != len(shape) or any(w is not None and w != n for n, w in zip(got, shape)):
+        raise ValueError(f"{name} has shape {tuple(got)}, expected {list(shape)}")
+    return t.data_ptr()
+
+
+def _rows(name, t, heads, n, dtype):
+    """t: [n][heads][64], heads packed, any stride between rows; returns (pointer, stride)."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != n or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {[n, heads, D]}")
+    if stride[2] != 1 or stride[1] != D:
+        raise ValueError(f"{name}: the heads of a row must be packed")
+    return t.data_ptr(), stride[0] if n > 1 else heads * D
+
+
+def _in_type(t):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("k must be a torch.Tensor")
+    if t.dtype == torch.float32:
+        return torch.float32, F32
+    if t.dtype == torch.bfloat16:
+        return torch.bfloat16, BF16
+    raise ValueError(f"k must be float32 or bfloat16, got {t.dtype}")
+
+
+def _same_device(k, *tensors):
+    """Every tensor of a call lives on k's device, which is the current one."""
+    import torch
+    dev = k.device.index
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors are on another device than the current one")
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError("the tensors are on different devices")
+
+
+def attn_rope_table(cosSin, theta: float = 10000.0, invFreq=None, stream=None):
+    """Fill the rotation table cosSin [numPositions][64] fp32 (cosines, then
+    sines). The 32 frequencies are theta^(-i / 32), or ``invFreq`` (any sequence
+    of 32 floats) for scaled rotations."""
+    import torch
+    ptr = _device_tensor("cosSin", cosSin, torch.float32, (None, D))
+    _same_device(cosSin)
+    freq = [float(theta) ** (-i / 32.0) for i in range(D // 2)] if invFreq is None else [float(f) for f in invFreq]
+    if len(freq) != D // 2:
+        raise ValueError(f"invFreq must hold {D // 2} frequencies")
+    host = (ctypes.c_double * (D // 2))(*freq)
+    rc = load().attn_rope_table(host, ptr, cosSin.shape[0], _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope_table")
+    return cosSin
+
+
+def _weights_and_table(qWeight, kWeight, cosSin, positions, n):
+    import torch
+    qw = None if qWeight is None else _device_tensor("qWeight", qWeight, torch.float32, (D,))
+    kw = None if kWeight is None else _device_tensor("kWeight", kWeight, torch.float32, (D,))
+    cs, count = None, 0
+    if cosSin is not None:
+        cs, count = _device_tensor("cosSin", cosSin, torch.float32, (None, D)), cosSin.shape[0]
+    pos = None if positions is None else _device_tensor("positions", positions, torch.int32, (n,))
+    return qw, kw, cs, pos, count
+
+
+def attn_qk_norm_rope(q, k, positions, cosSin, qOut, kOut, qWeight=None, kWeight=None, eps: float = 1e-6,
+                      pairing: int = ROPE_HALVES, stream=None):
+    """Per-head RMS norm of q and k and the position rotation, in one pass.
+
+    q [N][32][64] and k [N][8][64], fp32 or bf16 (both the same), rows may be
+    views into a wider projection; q may be None (with qOut None). qOut fp32
+    [N][32][64], kOut fp32 or bf16 [N][8][64], contiguous. qWeight, kWeight fp32
+    [64] or None (not normed); positions int32 [N] into cosSin (attn_rope_table),
+    both None for no rotation. Returns (qOut, kOut)."""
+    import torch
+    dtype, code = _in_type(k)
+    n = k.shape[0]
+    kp, ks = _rows("k", k, HKV, n, dtype)
+    qp, qs, qo = None, 0, None
+    if q is not None:
+        qp, qs = _rows("q", q, HQ, n, dtype)
+        qo = _device_tensor("qOut", qOut, torch.float32, (n, HQ, D))
+    out = BF16 if kOut.dtype == torch.bfloat16 else F32
+    ko = _device_tensor("kOut", kOut, torch.bfloat16 if out else torch.float32, (n, HKV, D))
+    qw, kw, cs, pos, count = _weights_and_table(qWeight, kWeight, cosSin, positions, n)
+    _same_device(k, q, positions, cosSin, qOut, kOut, qWeight, kWeight)
+    rc = load().attn_qk_norm_rope(qp, kp, code, qs, ks, qw, kw, eps, cs, pos, count, pairing, qo, ko, out, n,
+                                  _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_qk_norm_rope")
+    return qOut, kOut
+
+
+def _batch(kPages, vPages, blockTable, contextLens, page_dtype, B):
+    import torch
+    pages = kPages.shape[0]
+    kp = _device_tensor("kPages", kPages, page_dtype, (None, PAGE, HKV, D))
+    vp = _device_tensor("vPages", vPages, page_dtype, (pages, PAGE, HKV, D))
+    bt = _device_tensor("blockTable", blockTable, torch.int32, (B, None))
+    cl = _device_tensor("contextLens", contextLens, torch.int32, (B,))
+    return kp, vp, bt, cl, blockTable.shape[1], pages
+
+
+def _append(name, page_dtype, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin, positions, kWeight, q,
+            qOut, qWeight, eps, pairing, stream):
+    import torch
+    dtype, code = _in_type(k)
+    n, B = k.shape[0], contextLens.shape[0]
+    kp, ks = _rows("k", k, HKV, n, dtype)
+    vp, vs = _rows("v", v, HKV, n, dtype)
+    qp, qs, qo = None, 0, None
+    if q is not None:
+        qp, qs = _rows("q", q, HQ, n, dtype)
+        qo = _device_tensor("qOut", qOut, torch.float32, (n, HQ, D))
+    kpg, vpg, bt, cl, max_blocks, pages = _batch(kPages, vPages, blockTable, contextLens, page_dtype, B)
+    rs = _device_tensor("rowStart", rowStart, torch.int32, (B + 1,))
+    qw, kw, cs, pos, count = _weights_and_table(qWeight, kWeight, cosSin, positions, n)
+    _same_device(k, v, q, kPages, vPages, blockTable, contextLens, rowStart, cosSin, positions, kWeight, qOut, qWeight)
+    rc = getattr(load(), name)(qp, kp, vp, code, qs, ks, vs, qw, kw, eps, cs, pos, count, pairing, qo, kpg, vpg, bt,
+                               cl, rs, B, n, max_blocks, pages, _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, name)
+    return qOut
+
+
+def attn_append_paged(k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin=None, positions=None,
+                      kWeight=None, q=None, qOut=None, qWeight=None, eps: float = 1e-6, pairing: int = ROPE_HALVES,
+                      stream=None):
+    """Append a batch's rows to its paged cache: keys normed (kWeight) and rotated
+    (cosSin), values as they are, and with ``q`` the queries normed and rotated
+    into qOut, all in one launch.
+
+    k, v [N][8][64] (q [N][32][64]), fp32 or bf16, rows may be views; kPages,
+    vPages [numPages][16][8][64] fp32; blockTable int32 [B][maxBlocks],
+    contextLens int32 [B] (tokens in the cache before these rows), rowStart int32
+    [B + 1]. positions int32 [N], or None for consecutive ones. Returns qOut."""
+    import torch
+    return _append("attn_append_paged", torch.float32, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin,
+                   positions, kWeight, q, qOut, qWeight, eps, pairing, stream)
+
+
+def attn_append_paged_bf16kv(k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin=None, positions=None,
+                             kWeight=None, q=None, qOut=None, qWeight=None, eps: float = 1e-6,
+                             pairing: int = ROPE_HALVES, stream=None):
+    """attn_append_paged into bfloat16 pages."""
+    import torch
+    return _append("attn_append_paged_bf16kv", torch.bfloat16, k, v, kPages, vPages, blockTable, contextLens, rowStart,
+                   cosSin, positions, kWeight, q, qOut, qWeight, eps, pairing, stream)
+
+
+def attn_tree_workspace_bytes(B: int, N: int, max_rows: int, max_context: int, num_splits: int = 0) -> int:
+    """Bytes of workspace attn_tree_paged (either page type) needs on the current device."""
+    return int(load().attn_tree_workspace_bytes(int(B), int(N), int(max_rows), int(max_context), int(num_splits)))
+
+
+def _tree(name, page_dtype, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows, max_context,
+          num_splits, workspace, stream):
+    import torch
+    n, B = q.shape[0], contextLens.shape[0]
+    qp = _device_tensor("q", q, torch.float32, (n, HQ, D))
+    op = _device_tensor("out", out, torch.float32, (n, HQ, D))
+    kp, vp, bt, cl, max_blocks, pages = _batch(kPages, vPages, blockTable, contextLens, page_dtype, B)
+    rs = _device_tensor("rowStart", rowStart, torch.int32, (B + 1,))
+    mp = None if masks is None else _device_tensor("masks", masks, torch.int64, (n,))
+    _same_device(q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, workspace)
+    wp, wb = None, 0
+    if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        wp, wb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = getattr(load(), name)(qp, kp, vp, bt, cl, rs, mp, op, B, n, max_rows, max_blocks, pages, max_context,
+                               num_splits, wp, wb, _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, name)
+    return out
+
+
+def attn_tree_paged(q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows: int, max_context: int,
+                    num_splits: int = 0, workspace=None, stream=None):
+    """Attention of drafted rows over their sequences' paged caches.
+
+    q, out fp32 [N][32][64]; masks int64 [N] (bit j: the row sees row j of its
+    sequence) or None for a chain; the rows' keys and values are already in the
+    pages at tokens contextLens[b] + i. max_rows (<= 64) and max_context bound
+    the batch. ``workspace``: a CUDA tensor of at least
+    attn_tree_workspace_bytes(B, N, max_rows, max_context, num_splits) bytes, or
+    None when none is needed."""
+    import torch
+    return _tree("attn_tree_paged", torch.float32, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out,
+                 max_rows, max_context, num_splits, workspace, stream)
+
+
+def attn_tree_paged_bf16kv(q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows: int,
+                           max_context: int, num_splits: int = 0, workspace=None, stream=None):
+    """attn_tree_paged against bfloat16 pages, used exactly as stored."""
+    import torch
+    return _tree("attn_tree_paged_bf16kv", torch.bfloat16, q, kPages, vPages, blockTable, contextLens, rowStart, masks,
+                 out, max_rows, max_context, num_splits, workspace, stream)
+
+
+def _compact(name, page_dtype, kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows, stream):
+    import torch
+    B = contextLens.shape[0]
+    kp, vp, bt, cl, max_blocks, pages = _batch(kPages, vPages, blockTable, contextLens, page_dtype, B)
+    ke = _device_tensor("keep", keep, torch.int32, (B, None))
+    kc = _device_tensor("keepCounts", keepCounts, torch.int32, (B,))
+    _same_device(kPages, vPages, blockTable, contextLens, keep, keepCounts)
+    rc = getattr(load(), name)(kp, vp, bt, cl, ke, kc, B, keep.shape[1], max_rows, max_blocks, pages,
+                               _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, name)
+
+
+def attn_compact_paged(kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows: int, stream=None):
+    """Move the accepted drafted rows' keys and values to the front of the rows:
+    row keep[b][i] to token contextLens[b] + i, i < keepCounts[b]. keep int32
+    [B][maxKeep], rising in each row, entries below max_rows; keepCounts int32 [B]."""
+    import torch
+    _compact("attn_compact_paged", torch.float32, kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows,
+             stream)
+
+
+def attn_compact_paged_bf16kv(kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows: int, stream=None):
+    """attn_compact_paged on bfloat16 pages."""
+    import torch
+    _compact("attn_compact_paged_bf16kv", torch.bfloat16, kPages, vPages, blockTable, contextLens, keep, keepCounts,
+             max_rows, stream)
 
 
 def attn_naive_workspace_bytes(C: int, P: int) -> int:

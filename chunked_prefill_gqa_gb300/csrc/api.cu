@@ -384,6 +384,238 @@ extern "C" int attn_decode_paged_noalloc(const float* q, const float* kPages, co
                        split_len, splits, st->err, stream);
 }
 
+namespace attn {
+namespace {
+
+bool aligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
+
+// A tensor of `heads` heads a row with `stride` elements between rows: every
+// row has to start on 16 bytes.
+int row_stride_ok(long long stride, int heads, int type) {
+  if (stride < (long long)heads * ATTN_D) return ATTN_EINVAL;
+  return (stride * (type == ATTN_BF16 ? 2 : 4)) % 16 == 0 ? ATTN_OK : ATTN_EALIGN;
+}
+
+// What attn_qk_norm_rope and the appends check alike.
+int rows_ok(const RowCall& c) {
+  if (c.N < 0 || (c.in_type != ATTN_F32 && c.in_type != ATTN_BF16) ||
+      (c.out_type != ATTN_F32 && c.out_type != ATTN_BF16))
+    return ATTN_EINVAL;
+  if (c.pairing != ATTN_ROPE_HALVES && c.pairing != ATTN_ROPE_PAIRS) return ATTN_EINVAL;
+  if (c.N > ATTN_MAX_TOKENS) return ATTN_ERANGE;
+  if (c.N == 0) return ATTN_OK;
+  if (!c.k || !c.k_out || (c.q && !c.q_out)) return ATTN_EINVAL;
+  if (!(c.eps >= 0.f) || c.eps > 3.4e38f) return ATTN_EINVAL;  // NaN, negative or infinite
+  if (c.cos_sin && c.num_positions < 1) return ATTN_EINVAL;
+  int rc = row_stride_ok(c.k_stride, ATTN_HKV, c.in_type);
+  if (rc == ATTN_OK && c.q) rc = row_stride_ok(c.q_stride, ATTN_HQ, c.in_type);
+  if (rc == ATTN_OK && c.v) rc = row_stride_ok(c.v_stride, ATTN_HKV, c.in_type);
+  if (rc != ATTN_OK) return rc;
+  if (!aligned16(c.q) || !aligned16(c.k) || !aligned16(c.v) || !aligned16(c.q_weight) || !aligned16(c.k_weight) ||
+      !aligned16(c.cos_sin) || !aligned4(c.positions) || !aligned16(c.q_out) || !aligned16(c.k_out) ||
+      !aligned16(c.v_out))
+    return ATTN_EALIGN;
+  return ATTN_OK;
+}
+
+// Shape checks shared by the calls on a batch of sequences over paged caches.
+int batch_ok(int B, int N, int maxBlocks, int numPages) {
+  if (B < 0 || N < 0 || maxBlocks < 1 || numPages < 1) return ATTN_EINVAL;
+  if (B > 65535 || N > ATTN_MAX_TOKENS || (long long)maxBlocks * ATTN_PAGE > ATTN_MAX_TOKENS ||
+      numPages > ATTN_MAX_TOKENS / ATTN_PAGE)
+    return ATTN_ERANGE;
+  return ATTN_OK;
+}
+
+int append_paged(const RowCall& c, cudaStream_t stream) {
+  int rc = batch_ok(c.B, c.N, c.max_blocks, c.num_pages);
+  if (rc != ATTN_OK) return rc;
+  if ((rc = rows_ok(c)) != ATTN_OK || c.N == 0 || c.B == 0) return rc;
+  if (!c.v || !c.v_out || !c.table || !c.ctx_lens || !c.row_start) return ATTN_EINVAL;
+  if (!aligned4(c.table) || !aligned4(c.ctx_lens) || !aligned4(c.row_start)) return ATTN_EALIGN;
+  DeviceState* st = nullptr;
+  if ((rc = current_device(&st)) != ATTN_OK) return rc;
+  return from_cuda(launch_rows(c, st->err, stream));
+}
+
+int tree_ok(int B, int N, int maxRows, int maxBlocks, int numPages, int maxContext, int numSplits) {
+  const int rc = batch_ok(B, N, maxBlocks, numPages);
+  if (rc != ATTN_OK) return rc;
+  if (maxRows < 1 || maxContext < 0 || numSplits < 0) return ATTN_EINVAL;
+  if (maxRows > ATTN_TREE_ROWS || maxContext > maxBlocks * ATTN_PAGE)
+    return ATTN_ERANGE;
+  return ATTN_OK;
+}
+
+int tree_paged(TreeCall c, int numSplits, void* workspace, size_t workspaceBytes, cudaStream_t stream) {
+  int rc = tree_ok(c.B, c.N, c.max_rows, c.max_blocks, c.num_pages, c.max_context, numSplits);
+  if (rc != ATTN_OK || c.B == 0 || c.N == 0) return rc;
+  if (!c.q || !c.k_pages || !c.v_pages || !c.table || !c.ctx_lens || !c.row_start || !c.out) return ATTN_EINVAL;
+  if (!aligned16(c.q) || !aligned16(c.k_pages) || !aligned16(c.v_pages) || !aligned16(c.out) || !aligned4(c.table) ||
+      !aligned4(c.ctx_lens) || !aligned4(c.row_start) || (reinterpret_cast<uintptr_t>(c.masks) & 7u))
+    return ATTN_EALIGN;
+  DeviceState* st = nullptr;
+  if ((rc = current_device(&st)) != ATTN_OK) return rc;
+  if ((rc = tree_splits(c.type == ATTN_BF16, c.B, c.max_rows, c.max_context, numSplits, &c.splits, &c.split_len)) !=
+      ATTN_OK)
+    return rc;
+  const size_t need = tree_workspace_bytes(c.N, c.splits);
+  if (need > 0) {
+    if (!workspace || workspaceBytes < need) return ATTN_ESPACE;
+    if (!aligned16(workspace)) return ATTN_EALIGN;
+  }
+  c.parts = static_cast<float*>(workspace);
+  return launch_tree(c, st->err, stream);
+}
+
+int compact_paged(void* kPages, void* vPages, int type, const int* blockTable, const int* contextLens,
+                  const int* keep, const int* keepCounts, int B, int maxKeep, int maxRows, int maxBlocks,
+                  int numPages, cudaStream_t stream) {
+  int rc = batch_ok(B, 0, maxBlocks, numPages);
+  if (rc != ATTN_OK) return rc;
+  if (maxKeep < 0 || maxRows < 1) return ATTN_EINVAL;
+  if (maxRows > ATTN_TREE_ROWS || maxKeep > maxRows) return ATTN_ERANGE;
+  if (B == 0 || maxKeep == 0) return ATTN_OK;
+  if (!kPages || !vPages || !blockTable || !contextLens || !keep || !keepCounts) return ATTN_EINVAL;
+  if (!aligned16(kPages) || !aligned16(vPages) || !aligned4(blockTable) || !aligned4(contextLens) || !aligned4(keep) ||
+      !aligned4(keepCounts))
+    return ATTN_EALIGN;
+  DeviceState* st = nullptr;
+  if ((rc = current_device(&st)) != ATTN_OK) return rc;
+  return from_cuda(launch_compact(kPages, vPages, type, blockTable, contextLens, keep, keepCounts, B, maxKeep, maxRows,
+                                  maxBlocks, numPages, st->err, stream));
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" int attn_rope_table(const double* invFreq, float* cosSin, int numPositions, cudaStream_t stream) {
+  if (numPositions < 0) return ATTN_EINVAL;
+  if (numPositions > ATTN_MAX_TOKENS) return ATTN_ERANGE;
+  if (numPositions == 0) return ATTN_OK;
+  if (!invFreq || !cosSin) return ATTN_EINVAL;
+  if (!aligned16(cosSin)) return ATTN_EALIGN;
+  DeviceState* st = nullptr;
+  const int rc = current_device(&st);
+  if (rc != ATTN_OK) return rc;
+  return from_cuda(launch_rope_table(invFreq, cosSin, numPositions, stream));
+}
+
+extern "C" int attn_qk_norm_rope(const void* q, const void* k, int inType, long long qStride, long long kStride,
+                                 const float* qWeight, const float* kWeight, float eps, const float* cosSin,
+                                 const int* positions, int numPositions, int pairing, float* qOut, void* kOut,
+                                 int kOutType, int N, cudaStream_t stream) {
+  RowCall c{};
+  c.q = q;
+  c.k = k;
+  c.in_type = inType;
+  c.out_type = kOutType;
+  c.q_stride = qStride;
+  c.k_stride = kStride;
+  c.q_weight = qWeight;
+  c.k_weight = kWeight;
+  c.eps = eps;
+  c.cos_sin = cosSin;
+  c.positions = positions;
+  c.num_positions = numPositions;
+  c.pairing = pairing;
+  c.q_out = qOut;
+  c.k_out = kOut;
+  c.N = N;
+  int rc = rows_ok(c);
+  if (rc != ATTN_OK || N == 0) return rc;
+  if (cosSin && !positions) return ATTN_EINVAL;
+  DeviceState* st = nullptr;
+  if ((rc = current_device(&st)) != ATTN_OK) return rc;
+  return from_cuda(launch_rows(c, st->err, stream));
+}
+
+namespace attn {
+namespace {
+RowCall append_call(const void* q, const void* k, const void* v, int inType, long long qStride, long long kStride,
+                    long long vStride, const float* qWeight, const float* kWeight, float eps, const float* cosSin,
+                    const int* positions, int numPositions, int pairing, float* qOut, void* kPages, void* vPages,
+                    int pageType, const int* blockTable, const int* contextLens, const int* rowStart, int B, int N,
+                    int maxBlocks, int numPages) {
+  return RowCall{q,        k,       v,         qStride,   kStride,      vStride, inType,  pageType,
+                 qWeight,  kWeight, eps,       cosSin,    positions,    numPositions, pairing, qOut,
+                 kPages,   vPages,  blockTable, contextLens, rowStart,  B,       N,       maxBlocks, numPages};
+}
+}  // namespace
+}  // namespace attn
+
+extern "C" int attn_append_paged(const void* q, const void* k, const void* v, int inType, long long qStride,
+                                 long long kStride, long long vStride, const float* qWeight, const float* kWeight,
+                                 float eps, const float* cosSin, const int* positions, int numPositions, int pairing,
+                                 float* qOut, float* kPages, float* vPages, const int* blockTable,
+                                 const int* contextLens, const int* rowStart, int B, int N, int maxBlocks,
+                                 int numPages, cudaStream_t stream) {
+  return append_paged(append_call(q, k, v, inType, qStride, kStride, vStride, qWeight, kWeight, eps, cosSin, positions,
+                                  numPositions, pairing, qOut, kPages, vPages, ATTN_F32, blockTable, contextLens,
+                                  rowStart, B, N, maxBlocks, numPages),
+                      stream);
+}
+
+extern "C" int attn_append_paged_bf16kv(const void* q, const void* k, const void* v, int inType, long long qStride,
+                                        long long kStride, long long vStride, const float* qWeight,
+                                        const float* kWeight, float eps, const float* cosSin, const int* positions,
+                                        int numPositions, int pairing, float* qOut, uint16_t* kPages,
+                                        uint16_t* vPages, const int* blockTable, const int* contextLens,
+                                        const int* rowStart, int B, int N, int maxBlocks, int numPages,
+                                        cudaStream_t stream) {
+  return append_paged(append_call(q, k, v, inType, qStride, kStride, vStride, qWeight, kWeight, eps, cosSin, positions,
+                                  numPositions, pairing, qOut, kPages, vPages, ATTN_BF16, blockTable, contextLens,
+                                  rowStart, B, N, maxBlocks, numPages),
+                      stream);
+}
+
+extern "C" size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxContext, int numSplits) {
+  if (B <= 0 || N <= 0 || maxRows < 1 || maxRows > ATTN_TREE_ROWS || maxContext < 0 ||
+      maxContext > ATTN_MAX_TOKENS - maxRows || numSplits < 0 || B > 65535 || N > ATTN_MAX_TOKENS)
+    return 0;
+  size_t most = 0;
+  for (int bf16 = 0; bf16 < 2; ++bf16) {  // either page type may be called with it
+    int splits = 0, len = 0;
+    if (tree_splits(bf16 != 0, B, maxRows, maxContext, numSplits, &splits, &len) != ATTN_OK) return 0;
+    const size_t need = tree_workspace_bytes(N, splits);
+    if (need > most) most = need;
+  }
+  return most;
+}
+
+extern "C" int attn_tree_paged(const float* q, const float* kPages, const float* vPages, const int* blockTable,
+                               const int* contextLens, const int* rowStart, const long long* masks, float* out, int B,
+                               int N, int maxRows, int maxBlocks, int numPages, int maxContext, int numSplits,
+                               void* workspace, size_t workspaceBytes, cudaStream_t stream) {
+  return tree_paged(TreeCall{q, kPages, vPages, ATTN_F32, blockTable, contextLens, rowStart, masks, out, nullptr, B, N,
+                             maxRows, maxBlocks, numPages, maxContext, 0, 0},
+                    numSplits, workspace, workspaceBytes, stream);
+}
+
+extern "C" int attn_tree_paged_bf16kv(const float* q, const uint16_t* kPages, const uint16_t* vPages,
+                                      const int* blockTable, const int* contextLens, const int* rowStart,
+                                      const long long* masks, float* out, int B, int N, int maxRows, int maxBlocks,
+                                      int numPages, int maxContext, int numSplits, void* workspace,
+                                      size_t workspaceBytes, cudaStream_t stream) {
+  return tree_paged(TreeCall{q, kPages, vPages, ATTN_BF16, blockTable, contextLens, rowStart, masks, out, nullptr, B,
+                             N, maxRows, maxBlocks, numPages, maxContext, 0, 0},
+                    numSplits, workspace, workspaceBytes, stream);
+}
+
+extern "C" int attn_compact_paged(float* kPages, float* vPages, const int* blockTable, const int* contextLens,
+                                  const int* keep, const int* keepCounts, int B, int maxKeep, int maxRows,
+                                  int maxBlocks, int numPages, cudaStream_t stream) {
+  return compact_paged(kPages, vPages, ATTN_F32, blockTable, contextLens, keep, keepCounts, B, maxKeep, maxRows,
+                       maxBlocks, numPages, stream);
+}
+
+extern "C" int attn_compact_paged_bf16kv(uint16_t* kPages, uint16_t* vPages, const int* blockTable,
+                                         const int* contextLens, const int* keep, const int* keepCounts, int B,
+                                         int maxKeep, int maxRows, int maxBlocks, int numPages, cudaStream_t stream) {
+  return compact_paged(kPages, vPages, ATTN_BF16, blockTable, contextLens, keep, keepCounts, B, maxKeep, maxRows,
+                       maxBlocks, numPages, stream);
+}
+
 extern "C" size_t attn_naive_workspace_bytes(int C, int P) {
   if (C < 0 || P < 0 || (long long)P + C > ATTN_MAX_TOKENS) return 0;
   return naive_workspace_bytes(C, P);
@@ -471,15 +703,16 @@ extern "C" const char* attn_strerror(int code) {
     case ATTN_EINVAL: return "invalid argument (a NULL pointer, or a size below what the call accepts)";
     case ATTN_EALIGN: return "a tensor pointer is not 16-byte aligned";
     case ATTN_ERANGE:
-      return "a size is out of range (C or P + C above ATTN_MAX_TOKENS, numPages above ATTN_MAX_TOKENS / 16, "
-             "B above 65535, or maxContext above 16 * maxBlocks)";
+      return "a size is out of range (C, N or P + C above ATTN_MAX_TOKENS, numPages above ATTN_MAX_TOKENS / 16, "
+             "B above 65535, maxContext above 16 * maxBlocks, maxRows above ATTN_TREE_ROWS, or maxKeep above maxRows)";
     case ATTN_ELAUNCH: return "kernel launch failed";
     case ATTN_ETIMEOUT: return "a device-side bounded wait expired";
     case ATTN_EBOUNDS: return "a device-side bounds check failed";
     case ATTN_EDEVICE: return "the current device is not sm_103 (GB300)";
     case ATTN_ETMA: return "a TMA tensor map could not be encoded";
     case ATTN_ECUDA: return "a CUDA runtime call failed";
-    case ATTN_ESPACE: return "the workspace is missing or smaller than attn_decode_workspace_bytes()";
+    case ATTN_ESPACE:
+      return "the workspace is missing or smaller than attn_decode_workspace_bytes() or attn_tree_workspace_bytes()";
     case ATTN_ESCRATCH:
       return "the decode partials exceed the library's fixed scratch (ATTN_DECODE_SCRATCH_BYTES): "
              "use fewer splits or attn_decode_paged with a workspace";
@@ -488,5 +721,5 @@ extern "C" const char* attn_strerror(int code) {
 }
 
 extern "C" const char* attn_version(void) {
-  return "libattnprefill: tcgen05 split-TF32 prefill (contiguous and paged), tcgen05 bf16-K/V prefill, split-KV GQA decode, FFMA, score-matrix and reference kernels, sm_103a";
+  return "libattnprefill: tcgen05 split-TF32 prefill (contiguous and paged), tcgen05 bf16-K/V prefill, split-KV GQA decode, drafted-tree attention, norm/rotation/append rows, FFMA, score-matrix and reference kernels, sm_103a";
 }

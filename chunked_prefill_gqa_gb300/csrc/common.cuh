@@ -79,6 +79,43 @@ int launch_tc_bf16x3(const Problem& p, cudaStream_t stream);
 // Paged K/V: p.k / p.v point at [num_pages * 16][8][64] page pools.
 int launch_tc_paged(const Problem& p, const int* table, int num_pages, cudaStream_t stream);
 
+// Rows between the projections and attention (rows.cu): norm, rotation and the
+// store into a contiguous destination (table == nullptr) or a paged cache.
+struct RowCall {
+  const void *q, *k, *v;  // q and v may be nullptr
+  long long q_stride, k_stride, v_stride;
+  int in_type, out_type;  // ATTN_F32 or ATTN_BF16: of q, k, v; of k_out, v_out
+  const float *q_weight, *k_weight;
+  float eps;
+  const float* cos_sin;
+  const int* positions;
+  int num_positions, pairing;
+  float* q_out;
+  void *k_out, *v_out;
+  const int *table, *ctx_lens, *row_start;
+  int B, N, max_blocks, num_pages;
+};
+cudaError_t launch_rows(const RowCall& c, unsigned* err, cudaStream_t stream);
+cudaError_t launch_rope_table(const double* inv_freq, float* table, int num_positions, cudaStream_t stream);
+cudaError_t launch_compact(void* k_pages, void* v_pages, int type, const int* table, const int* ctx_lens,
+                           const int* keep, const int* counts, int B, int max_keep, int max_rows, int max_blocks,
+                           int num_pages, unsigned* err, cudaStream_t stream);
+
+// Attention of drafted rows over a paged cache (tree.cu): the segments of a
+// call, the workspace of its partials, launch. int results are ATTN_* codes.
+struct TreeCall {
+  const float* q;
+  const void *k_pages, *v_pages;
+  int type;  // ATTN_F32 or ATTN_BF16 pages
+  const int *table, *ctx_lens, *row_start;
+  const long long* masks;
+  float *out, *parts;
+  int B, N, max_rows, max_blocks, num_pages, max_context, split_len, splits;
+};
+int tree_splits(bool bf16, int B, int max_rows, int max_context, int splits_hint, int* splits, int* split_len);
+size_t tree_workspace_bytes(int N, int splits);
+int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream);
+
 // Tensor-pipe rate measurement (peak.cu): `ctas` CTAs each issue `iters`
 // dense M = 128, N = n MMAs (kind::tf32, or kind::f16 with bf16 operands).
 int launch_tensor_peak(int bf16, int n, int iters, int ctas, unsigned* err, cudaStream_t stream);

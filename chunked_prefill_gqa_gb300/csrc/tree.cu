@@ -1,0 +1,847 @@
+// tree.cu -- attention of drafted tokens over a paged cache: each of B
+// sequences has up to 64 drafted rows whose keys and values already lie in its
+// cache behind the ctx_b accepted tokens, and row i sees all of those and the
+// drafted rows j whose bit is set in its mask (itself and its ancestors in the
+// tree of drafts):
+//   K_i = {0 .. ctx-1} u {ctx + j : bit j of mask_i, j < T}
+//   out_i = sum_{j in K_i} softmax_j(q_i . k_j / 8) v_j,   zeros for an empty K_i
+//
+// One pass over the cache per sequence and KV head: a block owns (key segment,
+// KV head, row tile, sequence) and all four query heads of that KV head, 16 MT
+// rows of 4 MT drafted tokens. Its warps share nothing until the end. Each
+// walks its own 16-token pages through its own ring of TMA boxes, with its own
+// running maximum, sum and accumulator, and the warps' (and then the segments')
+// partials merge with the split-K rule: m = max m_s, out = sum e^(m_s - m) O_s /
+// sum e^(m_s - m) l_s.
+//
+// The products run on mma.sync (16 query rows x 8 keys), in fp32 precision:
+//   fp32 pages: each operand as two tf32 terms x = hi + lo (hi = x with its 13
+//     low mantissa bits cleared), hi hi + hi lo + lo hi, as in the prefill kernel;
+//   bf16 pages: K and V exactly as stored, q and the probabilities as three bf16
+//     terms each (24 bits), so nothing of q or p is lost to the cache's precision.
+// The reference maximum of a row moves only when a score passes it by 2^8 (p
+// stays below 2^8, far from fp32's range), so in the steady state a page costs
+// one vote instead of a reduction over lanes and a rescaled accumulator.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kC = kScale * kLog2e;     // scores in log2 units
+constexpr float kStale = 8.f;             // log2: how far a score may pass the reference maximum
+constexpr int kMaxSplits = 64;
+
+// Variants: MT m-tiles of 16 rows (4 MT drafted tokens). Warps, ring depth and
+// blocks per SM keep at least 128 KB of copies in flight on an SM, twice what
+// its share of the memory bandwidth needs.
+template <bool kBf16, int MT>
+struct Cfg {
+  static constexpr int kWarps = (!kBf16 && MT > 1) ? 8 : 4;
+  static constexpr int kStages = !kBf16 ? 3 : MT == 4 ? 5 : 6;
+  static constexpr int kBoxes = kBf16 ? 1 : 2;                    // boxes of 128 bytes x 16 tokens per operand
+  static constexpr uint32_t kBox = ATTN_PAGE * 128;
+  static constexpr uint32_t kStage = 2 * kBoxes * kBox;           // K, then V
+  static constexpr int kSteps = kBf16 ? 4 : 8;                    // k-steps of q . k
+  static constexpr int kTerms = kBf16 ? 3 : 2;                    // q's terms
+  static constexpr uint32_t kQBytes = MT * kSteps * kTerms * 512;  // fragments, 16 bytes a lane
+  static constexpr uint32_t kRing = kWarps * kStages * kStage;
+  static constexpr uint32_t kSmemQ = kRing;
+  static constexpr uint32_t kSmemMask = kSmemQ + kQBytes;
+  static constexpr uint32_t kSmemBar = kSmemMask + 4 * MT * 8;
+  static constexpr uint32_t kSmemTotal = kSmemBar + kWarps * kStages * 8;
+  static constexpr uint32_t kSmemAlloc = kSmemTotal + 1024;
+  static constexpr int kBlocks = 233472 / (kSmemAlloc + 1024);
+  static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
+  static_assert(16 * MT * kD * 4 <= kStages * kStage, "a warp's accumulator fits its own ring");
+  static_assert(kWarps * 16 * MT * 8 <= kQBytes, "the warps' maxima and sums fit where q was");
+};
+
+struct TreeArgs {
+  const float* q;            // [N][32][64]
+  const int* table;          // [B][max_blocks]
+  const int* ctx_lens;       // [B]
+  const int* row_start;      // [B + 1]
+  const long long* masks;    // [N], or nullptr: a chain (row i sees rows 0 .. i)
+  float* out;                // [N][32][64]
+  float* parts;              // [N][32][splits][64], then [N][32][splits][2] (log2 maximum, sum)
+  int B, N, max_rows, max_blocks, num_pages, max_context, split_len, splits;
+  unsigned* err;
+  unsigned long long timeout_ns;
+};
+
+// One sequence of the batch, its lengths checked.
+struct Seq {
+  int ctx, first, rows, keys;
+  bool ok;
+};
+__device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b) {
+  Seq s;
+  s.ctx = __ldg(a.ctx_lens + b);
+  s.first = __ldg(a.row_start + b);
+  const int end = __ldg(a.row_start + b + 1);
+  s.ok = true;
+  const int room = min((long long)a.max_blocks * ATTN_PAGE, (long long)ATTN_MAX_TOKENS);
+  if (s.ctx < 0 || s.ctx > a.max_context) {
+    s.ok = false;
+    s.ctx = s.ctx < 0 ? 0 : a.max_context;
+  }
+  if (s.first < 0 || end < s.first || end > a.N || (long long)end - s.first > a.max_rows) {
+    s.ok = false;
+    s.first = min(max(s.first, 0), a.N);
+    s.rows = min(min(max(end, s.first), a.N) - s.first, a.max_rows);
+  } else {
+    s.rows = end - s.first;
+  }
+  if (s.ctx + s.rows > room) {
+    s.ok = false;
+    s.ctx = min(s.ctx, room);
+  }
+  s.keys = min(s.ctx + s.rows, room);
+  return s;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t hi_of(float x) { return __float_as_uint(x) & 0xffffe000u; }
+__device__ __forceinline__ uint32_t lo_of(float x) { return __float_as_uint(x - __uint_as_float(hi_of(x))); }
+// Three bf16 terms of a pair: two truncated, the last rounded to nearest: 24
+// bits, all of an fp32 value whose last term does not underflow.
+__device__ __forceinline__ void split3(float x, float y, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
+  t0 = tc::pack_bf16_trunc(x, y);
+  const float rx = x - tc::bf16_trunc(x), ry = y - tc::bf16_trunc(y);
+  t1 = tc::pack_bf16_trunc(rx, ry);
+  t2 = tc::pack_bf16_rn(rx - tc::bf16_trunc(rx), ry - tc::bf16_trunc(ry));
+}
+__device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+
+// The tensor core's own accumulation does not round to nearest: over a long key
+// range its error would all lean one way. Each page's product starts at zero
+// and is added here, rounded to nearest.
+__device__ __forceinline__ void add4(float (&o)[4], const float (&x)[4]) {
+  tc::add2(o[0], o[1], o[0], o[1], x[0], x[1]);
+  tc::add2(o[2], o[3], o[2], o[3], x[2], x[3]);
+}
+
+// Inside an 8-row group the order of keys, and inside a 32-dim group the order
+// of 16-byte chunks, is free as long as both sides of a product use one order.
+// This one (0 4 1 5 2 6 3 7 backwards: bit 0 to bit 2) makes every 128-bit load
+// of a fragment touch all eight chunk positions of the swizzle once.
+__device__ __forceinline__ int turn(int n) { return (n >> 1) | ((n & 1) << 2); }
+
+template <bool kBf16, int MT>
+__global__ void __launch_bounds__(32 * Cfg<kBf16, MT>::kWarps, Cfg<kBf16, MT>::kBlocks)
+tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
+  using F = Cfg<kBf16, MT>;
+  constexpr int kWarps = F::kWarps, kStages = F::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, c = lane & 3;  // fragment row (or key), fragment column
+  const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
+
+  const Seq seq = load_seq(a, b);
+  const int i0 = rt * 4 * MT;               // the tile's first drafted row
+  const int nrows = min(4 * MT, seq.rows - i0);
+  const int k0 = s * a.split_len;
+  const int k1 = min(k0 + a.split_len, seq.keys);
+  if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+  if (nrows <= 0) return;
+  if (k0 >= k1) {
+    // Past the sequence: the merge counts its segments from the lengths. A
+    // sequence without any key (only a refused one) gets zeros.
+    if (s == 0)
+      for (int e = tid; e < nrows * kGroup * kD; e += 32 * kWarps)
+        a.out[((size_t)(seq.first + i0 + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
+    return;
+  }
+  const bool whole = seq.keys <= a.split_len;  // one segment: the output is written here
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F::kSmemBar);
+  unsigned long long* masks = reinterpret_cast<unsigned long long*>(smem + F::kSmemMask);
+  uint8_t* const ring = smem + warp * (kStages * F::kStage);
+  uint64_t* const full = bars + warp * kStages;
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
+    tc::fence_mbar_init();
+  }
+  if (tid < 4 * MT) {
+    unsigned long long m = 0;
+    const int i = i0 + tid;
+    if (tid < nrows) m = a.masks ? (unsigned long long)__ldg(a.masks + seq.first + i) : ~0ull >> (63 - i);
+    masks[tid] = m;
+  }
+  __syncwarp();
+
+  // This warp's pages: pages warp, warp + kWarps, ... of the segment. Lane l
+  // holds the table entry of its l-th page from the last multiple of 32.
+  const int npages = (k1 - k0 + ATTN_PAGE - 1) / ATTN_PAGE;
+  const int mine = warp < npages ? (npages - warp + kWarps - 1) / kWarps : 0;
+  const int* trow = a.table + (size_t)b * a.max_blocks + k0 / ATTN_PAGE + warp;
+  int entries = 0;
+  auto issue = [&](int n) {
+    if ((n & 31) == 0) entries = n + lane < mine ? __ldg(trow + (size_t)(n + lane) * kWarps) : 0;
+    int page = __shfl_sync(kFull, entries, n & 31);
+    if (lane == 0) {
+      if (page < 0 || page >= a.num_pages) {  // reads as zeros: past the pool's end
+        record_error(a.err, kDevErrBounds);
+        page = a.num_pages;
+      }
+      const int st = n % kStages;
+      uint8_t* dst = ring + st * F::kStage;
+      tc::mbar_arrive_expect_tx(&full[st], F::kStage);
+#pragma unroll
+      for (int x = 0; x < F::kBoxes; ++x) {
+        tc::tma_load_2d(dst + x * F::kBox, &mk, &full[st], head * kD + x * 32, page * ATTN_PAGE);
+        tc::tma_load_2d(dst + (F::kBoxes + x) * F::kBox, &mv, &full[st], head * kD + x * 32, page * ATTN_PAGE);
+      }
+    }
+  };
+  int issued = 0;
+  for (; issued < kStages && issued < mine; ++issued) issue(issued);
+
+  // q's fragments, split into their terms: in shared memory in the order the
+  // lanes read them, or with one m-tile in registers.
+  uint4* const qs = reinterpret_cast<uint4*>(smem + F::kSmemQ);
+  for (int e = warp; e < MT * 4; e += kWarps) {  // (m-tile, 16 dims)
+    const int mt = e >> 2, j = e & 3;
+    float x[2][4];  // rows g and g + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = 4 * mt + 2 * h + (g >> 2);
+      const float* src = a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (g & 3)) * kD + 16 * j;
+      if (i < nrows) {
+        if constexpr (kBf16) {  // dims 2c, 2c+1, 2c+8, 2c+9
+          const float2 u = __ldg(reinterpret_cast<const float2*>(src + 2 * c));
+          const float2 v = __ldg(reinterpret_cast<const float2*>(src + 2 * c + 8));
+          x[h][0] = u.x, x[h][1] = u.y, x[h][2] = v.x, x[h][3] = v.y;
+        } else {  // dims 4c .. 4c + 3
+          const float4 u = __ldg(reinterpret_cast<const float4*>(src + 4 * c));
+          x[h][0] = u.x, x[h][1] = u.y, x[h][2] = u.z, x[h][3] = u.w;
+        }
+      } else {
+        x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.f;
+      }
+    }
+    if constexpr (kBf16) {
+      uint32_t t[3][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          split3(x[h][2 * u], x[h][2 * u + 1], t[0][2 * u + h], t[1][2 * u + h], t[2][2 * u + h]);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        qs[((mt * 4 + j) * 3 + k) * 32 + lane] = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {  // k-step 2 j + u: k = c is dim 4c + 2u, k = c + 4 the next
+        uint4* dst = qs + ((mt * 8 + 2 * j + u) * 2) * 32 + lane;
+        dst[0] = make_uint4(hi_of(x[0][2 * u]), hi_of(x[1][2 * u]), hi_of(x[0][2 * u + 1]), hi_of(x[1][2 * u + 1]));
+        dst[32] = make_uint4(lo_of(x[0][2 * u]), lo_of(x[1][2 * u]), lo_of(x[0][2 * u + 1]), lo_of(x[1][2 * u + 1]));
+      }
+    }
+  }
+  __syncthreads();
+  uint4 qreg[MT == 1 ? F::kSteps * F::kTerms : 1];
+  if constexpr (MT == 1) {
+#pragma unroll
+    for (int e = 0; e < F::kSteps * F::kTerms; ++e) qreg[e] = qs[e * 32 + lane];
+  }
+  auto qfrag = [&](int mt, int step, int term, uint32_t (&r)[4]) {
+    uint4 v;
+    if constexpr (MT == 1) v = qreg[step * F::kTerms + term];
+    else v = qs[((mt * F::kSteps + step) * F::kTerms + term) * 32 + lane];
+    r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
+  };
+
+  // State of this warp's partial: rows g and g + 8 of every m-tile. The sums
+  // are this lane's columns' alone until the end.
+  float top[MT][2], sum[MT][2], o[MT][8][4];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    top[mt][0] = top[mt][1] = -INFINITY;
+    sum[mt][0] = sum[mt][1] = 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) o[mt][u][0] = o[mt][u][1] = o[mt][u][2] = o[mt][u][3] = 0.f;
+  }
+
+  bool failed = false;
+  int n = 0;
+  for (; n < mine; ++n) {
+    const int st = n % kStages;
+    if (!__all_sync(kFull, tc::mbar_wait(&full[st], (n / kStages) & 1, a.timeout_ns))) {
+      failed = true;
+      break;
+    }
+    const uint8_t* kt = ring + st * F::kStage;
+    const uint8_t* vt = kt + F::kBoxes * F::kBox;
+    const int t0 = k0 + (warp + n * kWarps) * ATTN_PAGE;
+    const bool tail = t0 + ATTN_PAGE > seq.ctx;  // holds drafted keys, or slots past them
+
+    // Scores: sc[mt][nt], columns 2c and 2c + 1 of 8-key group nt. Column n is
+    // key turn(n) of the group (fp32 pages) or key n (bf16 pages).
+    float sc[MT][2][4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.f;
+      if constexpr (kBf16) {
+        uint32_t kb[2][4];
+        const int r = nt * 8 + (lane & 7);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          ldsm4(kb[h], tc::smem_u32(kt) + r * 128 + (((h * 4 + (lane >> 3)) ^ (r & 7)) << 4));
+#pragma unroll
+        for (int st4 = 0; st4 < 4; ++st4) {
+          const uint32_t b0 = kb[st4 >> 1][(st4 & 1) * 2], b1 = kb[st4 >> 1][(st4 & 1) * 2 + 1];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int k = 2; k >= 0; --k) {
+              uint32_t qa[4];
+              qfrag(mt, st4, k, qa);
+              mma_bf16(sc[mt][nt], qa, b0, b1);
+            }
+        }
+      } else {
+        const int r = nt * 8 + turn(g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 x = *reinterpret_cast<const float4*>(kt + (j >> 1) * F::kBox + r * 128 +
+                                                            ((((j & 1) * 4 + c) ^ (r & 7)) << 4));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float e0 = u ? x.z : x.x, e1 = u ? x.w : x.y;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t qh[4], ql[4];
+              qfrag(mt, 2 * j + u, 0, qh);
+              qfrag(mt, 2 * j + u, 1, ql);
+              mma_tf32(sc[mt][nt], ql, hi_of(e0), hi_of(e1));
+              mma_tf32(sc[mt][nt], qh, lo_of(e0), lo_of(e1));
+              mma_tf32(sc[mt][nt], qh, hi_of(e0), hi_of(e1));
+            }
+          }
+        }
+      }
+    }
+
+    if (tail) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int col = 2 * c + (e & 1);
+            const int pos = t0 + nt * 8 + (kBf16 ? col : turn(col));
+            const int at = pos - seq.ctx;
+            const bool seen = pos < k1 && (at < 0 || (masks[4 * mt + 2 * (e >> 1) + (g >> 2)] >> at & 1));
+            if (!seen) sc[mt][nt][e] = -INFINITY;
+          }
+    }
+
+    // Does a score pass its row's reference by more than 2^8? (Any score does
+    // while the reference is -inf.)
+    bool over = false;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float most = fmaxf(fmaxf(sc[mt][0][2 * h], sc[mt][0][2 * h + 1]),
+                                 fmaxf(sc[mt][1][2 * h], sc[mt][1][2 * h + 1]));
+        over |= most * kC > top[mt][h] + kStale;
+      }
+    if (__any_sync(kFull, over)) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float most = fmaxf(fmaxf(sc[mt][0][2 * h], sc[mt][0][2 * h + 1]),
+                             fmaxf(sc[mt][1][2 * h], sc[mt][1][2 * h + 1]));
+          most = fmaxf(most, __shfl_xor_sync(kFull, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(kFull, most, 2));
+          const float next = fmaxf(top[mt][h], most * kC);
+          const float alpha = next == -INFINITY ? 1.f : ex2(top[mt][h] - next);
+          top[mt][h] = next;
+          sum[mt][h] *= alpha;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            o[mt][u][2 * h] *= alpha;
+            o[mt][u][2 * h + 1] *= alpha;
+          }
+        }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float ref = top[mt][h] == -INFINITY ? 0.f : top[mt][h];  // a row that has seen no key yet
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int e = 2 * h; e < 2 * h + 2; ++e) {
+            sc[mt][nt][e] = ex2(fmaf(sc[mt][nt][e], kC, -ref));
+            sum[mt][h] += sc[mt][nt][e];
+          }
+      }
+
+    // Drafted values that are not finite reach only the rows that see them; a
+    // product with a zero probability would spread NaN. They are taken out of
+    // the operand and added row by row. Slots past the last key count as zeros.
+    if constexpr (kBf16) {
+      uint32_t pf[MT][3][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)  // a0 a1: group 0, rows g and g + 8; a2 a3: group 1
+          split3(sc[mt][e >> 1][(e & 1) * 2], sc[mt][e >> 1][(e & 1) * 2 + 1], pf[mt][0][e], pf[mt][1][e],
+                 pf[mt][2][e]);
+      bool odd = false;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // 16 dims: two n-tiles
+        uint32_t vb[4];
+        const int r = ((lane >> 3) & 1) * 8 + (lane & 7);
+        ldsm4_t(vb, tc::smem_u32(vt) + r * 128 + (((2 * j + (lane >> 4)) ^ (r & 7)) << 4));
+        if (tail) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int pos = t0 + (e & 1) * 8 + 2 * c;
+            if ((vb[e] & 0x7f80u) == 0x7f80u) odd |= pos < k1 && pos >= seq.ctx;
+            if ((vb[e] & 0x7f800000u) == 0x7f800000u) odd |= pos + 1 < k1 && pos + 1 >= seq.ctx;
+            if (pos >= k1 || (pos >= seq.ctx && (vb[e] & 0x7f80u) == 0x7f80u)) vb[e] &= 0xffff0000u;
+            if (pos + 1 >= k1 || (pos + 1 >= seq.ctx && (vb[e] & 0x7f800000u) == 0x7f800000u)) vb[e] &= 0xffffu;
+          }
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int k = 2; k >= 0; --k) {
+            mma_bf16(x0, pf[mt][k], vb[0], vb[1]);
+            mma_bf16(x1, pf[mt][k], vb[2], vb[3]);
+          }
+          add4(o[mt][2 * j], x0);
+          add4(o[mt][2 * j + 1], x1);
+        }
+      }
+      if (tail && __any_sync(kFull, odd)) {
+#pragma unroll 1
+        for (int key = 0; key < ATTN_PAGE; ++key) {
+          const int at = t0 + key - seq.ctx;
+          if (at < 0 || t0 + key >= k1) continue;
+          const int from = (lane & ~3) | ((key & 7) >> 1);  // the lane of this row's column `key`
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float p0 = __shfl_sync(kFull, key < 8 ? sc[mt][0][2 * h] : sc[mt][1][2 * h], from);
+              const float p1 = __shfl_sync(kFull, key < 8 ? sc[mt][0][2 * h + 1] : sc[mt][1][2 * h + 1], from);
+              const float p = (key & 1) ? p1 : p0;
+              const bool seen = masks[4 * mt + 2 * h + (g >> 2)] >> at & 1;
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int d = 8 * u + 2 * c + e;
+                  const uint16_t raw = *reinterpret_cast<const uint16_t*>(
+                      vt + key * 128 + ((((d >> 3) ^ (key & 7)) << 4) | ((d & 7) * 2)));
+                  const float v = __uint_as_float((uint32_t)raw << 16);
+                  if (seen && !finite(v)) o[mt][u][2 * h + e] += p * v;
+                }
+            }
+        }
+      }
+    } else {
+      bool odd = false;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        float va[2][2][4];  // keys c and c + 4 of each group, dims 32 hh + 4 turn(g) ..
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int r = nt * 8 + c + 4 * y;
+            const float4 x =
+                *reinterpret_cast<const float4*>(vt + hh * F::kBox + r * 128 + ((turn(g) ^ (r & 7)) << 4));
+            va[nt][y][0] = x.x, va[nt][y][1] = x.y, va[nt][y][2] = x.z, va[nt][y][3] = x.w;
+            if (tail) {
+              const int pos = t0 + r;
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                if (pos >= k1) va[nt][y][u] = 0.f;
+                if (pos >= seq.ctx && !finite(va[nt][y][u])) {
+                  odd = true;
+                  va[nt][y][u] = 0.f;
+                }
+              }
+            }
+          }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t ph[2][4], pl[2][4];
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {  // a0 a1: column 2c (key c), rows g, g + 8; a2 a3: column 2c + 1 (key c + 4)
+              const float p = sc[mt][nt][(e & 1) * 2 + (e >> 1)];
+              ph[nt][e] = hi_of(p);
+              pl[nt][e] = lo_of(p);
+            }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+              mma_tf32(x, pl[nt], hi_of(va[nt][0][u]), hi_of(va[nt][1][u]));
+              mma_tf32(x, ph[nt], lo_of(va[nt][0][u]), lo_of(va[nt][1][u]));
+            }
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) mma_tf32(x, ph[nt], hi_of(va[nt][0][u]), hi_of(va[nt][1][u]));
+            add4(o[mt][hh * 4 + u], x);
+          }
+        }
+      }
+      if (tail && __any_sync(kFull, odd)) {
+#pragma unroll 1
+        for (int key = 0; key < ATTN_PAGE; ++key) {
+          const int at = t0 + key - seq.ctx;
+          if (at < 0 || t0 + key >= k1) continue;
+          const int from = (lane & ~3) | (key & 3);  // the lane of this row's columns of keys c and c + 4
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float p0 = __shfl_sync(kFull, key < 8 ? sc[mt][0][2 * h] : sc[mt][1][2 * h], from);
+              const float p1 = __shfl_sync(kFull, key < 8 ? sc[mt][0][2 * h + 1] : sc[mt][1][2 * h + 1], from);
+              const float p = (key & 4) ? p1 : p0;
+              const bool seen = masks[4 * mt + 2 * h + (g >> 2)] >> at & 1;
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int chunk = c + 4 * e;  // turn(2c + e)
+                  const float v = *reinterpret_cast<const float*>(vt + (u >> 2) * F::kBox + key * 128 +
+                                                                  ((chunk ^ (key & 7)) << 4) + (u & 3) * 4);
+                  if (seen && !finite(v)) o[mt][u][2 * h + e] += p * v;
+                }
+            }
+        }
+      }
+    }
+    __syncwarp();  // the stage is read: refill it
+    if (issued < mine) issue(issued++);
+  }
+
+  if (failed) {
+    // A page did not land in time: record it, give the copies still in flight
+    // a bounded wait before the block's shared memory is released.
+    if (lane == 0) record_error(a.err, kDevErrTimeout);
+    for (int i = n; i < issued; ++i) tc::mbar_wait(&full[i % kStages], (i / kStages) & 1, a.timeout_ns);
+  }
+
+  // The warp's partial: sums over its lanes, the accumulator into its own ring
+  // (every copy into it has landed and been read), row-major with the 16-byte
+  // chunks of a row turned by the row.
+  float* const acc = reinterpret_cast<float*>(ring);
+  auto acc_at = [](int row, int d) { return row * kD + ((((d >> 2) ^ row) & 7) | ((d >> 2) & 8)) * 4 + (d & 3); };
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = 16 * mt + 8 * h + g;
+      sum[mt][h] += __shfl_xor_sync(kFull, sum[mt][h], 1);
+      sum[mt][h] += __shfl_xor_sync(kFull, sum[mt][h], 2);
+      if constexpr (kBf16) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          *reinterpret_cast<float2*>(acc + acc_at(row, 8 * u + 2 * c)) =
+              make_float2(o[mt][u][2 * h], o[mt][u][2 * h + 1]);
+      } else {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4*>(acc + acc_at(row, 32 * hh + 16 * e + 4 * c)) =
+                make_float4(o[mt][4 * hh][2 * h + e], o[mt][4 * hh + 1][2 * h + e], o[mt][4 * hh + 2][2 * h + e],
+                            o[mt][4 * hh + 3][2 * h + e]);
+      }
+    }
+  const bool any_failed = __syncthreads_or(failed);  // and q's fragments are no longer read
+  float2* const ml = reinterpret_cast<float2*>(smem + F::kSmemQ);  // [warp][row]
+  if (c == 0) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        ml[warp * 16 * MT + 16 * mt + 8 * h + g] = make_float2(top[mt][h], sum[mt][h]);
+  }
+  __syncthreads();
+  for (int e = tid; e < nrows * kGroup * 16; e += 32 * kWarps) {  // (row, 16-byte chunk)
+    const int row = e >> 4, d = (e & 15) * 4;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * 16 * MT + row].x);
+    float den = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 p = ml[w * 16 * MT + row];
+      // A warp that saw no key of the row has no weight; a sum that is NaN (a
+      // row whose scores are) stays NaN.
+      const float wt = p.x == -INFINITY ? 0.f : ex2(p.x - m);
+      den = fmaf(wt, p.y, den);
+      if (wt == 0.f) continue;
+      const float4 y = *reinterpret_cast<const float4*>(
+          reinterpret_cast<const float*>(smem + w * (kStages * F::kStage)) + acc_at(row, d));
+      x.x = fmaf(wt, y.x, x.x);
+      x.y = fmaf(wt, y.y, x.y);
+      x.z = fmaf(wt, y.z, x.z);
+      x.w = fmaf(wt, y.w, x.w);
+    }
+    const size_t at = (size_t)(seq.first + i0 + row / kGroup) * kHQ + head * kGroup + row % kGroup;
+    if (whole) {
+      if (any_failed) continue;  // left unwritten
+      const float inv = den == 0.f ? 0.f : 1.f / den;  // no key: zeros
+      *reinterpret_cast<float4*>(a.out + at * kD + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    } else {
+      // after a failed wait the segment counts as empty
+      float* part = a.parts + (at * a.splits + s) * kD + d;
+      *reinterpret_cast<float4*>(part) = x;
+      if (d == 0) {
+        float2* mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+        mls[at * a.splits + s] = any_failed ? make_float2(-INFINITY, 0.f) : make_float2(m, den);
+      }
+    }
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Merge: block (drafted row, sequence), a warp per four heads in turn, two dims a lane.
+// Lane s holds segment s's maximum and sum, 32 segments at a time.
+constexpr int kMergeWarps = 8;
+__global__ void __launch_bounds__(32 * kMergeWarps)
+tree_merge_kernel(const TreeArgs a) {
+  const int b = blockIdx.y, i = blockIdx.x, lane = threadIdx.x & 31;
+  const Seq seq = load_seq(a, b);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (i >= seq.rows || seq.keys <= a.split_len) return;
+  const int active = (seq.keys + a.split_len - 1) / a.split_len;
+  const float2* mls = reinterpret_cast<const float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+  for (int h = threadIdx.x >> 5; h < kHQ; h += kMergeWarps) {
+    const size_t at = (size_t)(seq.first + i) * kHQ + h;
+    float2 p[kMaxSplits / 32];
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 32; ++k) {
+      p[k] = make_float2(-INFINITY, 0.f);
+      if (k * 32 + lane < active) p[k] = mls[at * a.splits + k * 32 + lane];
+      m = fmaxf(m, p[k].x);
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+    float den = 0.f;
+    float2 x = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMaxSplits / 32; ++k) {
+      const float w = p[k].x == -INFINITY ? 0.f : ex2(p[k].x - m);
+      const int most = min(32, active - k * 32);
+      den = fmaf(w, p[k].y, den);
+      for (int t = 0; t < most; ++t) {
+        const float wt = __shfl_sync(kFull, w, t);
+        const float2 y = *reinterpret_cast<const float2*>(a.parts + (at * a.splits + k * 32 + t) * kD + 2 * lane);
+        if (wt != 0.f) {  // an empty segment's accumulator has no weight, whatever it holds
+          x.x = fmaf(wt, y.x, x.x);
+          x.y = fmaf(wt, y.y, x.y);
+        }
+      }
+    }
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(kFull, den, off);
+    const float inv = den == 0.f ? 0.f : 1.f / den;  // no key: zeros
+    *reinterpret_cast<float2*>(a.out + at * kD + 2 * lane) = make_float2(x.x * inv, x.y * inv);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// A page pool [num_pages * 16][8][64] as the 2-D tensor (head * 64 + d, row); a
+// box is 128 bytes (64 bf16, or 32 fp32) of the 16 rows of a page.
+int encode_pool(const void* base, int num_pages, bool bf16, CUtensorMap* map) {
+  auto enc = encoder();
+  if (!enc) return ATTN_ETMA;
+  const cuuint32_t ones[2] = {1, 1};
+  const cuuint64_t dims[2] = {(cuuint64_t)kHKV * kD, (cuuint64_t)num_pages * ATTN_PAGE};
+  const cuuint64_t strides[1] = {(cuuint64_t)kHKV * kD * (bf16 ? 2 : 4)};
+  const cuuint32_t box[2] = {bf16 ? 64u : 32u, ATTN_PAGE};
+  if (enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
+          dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return ATTN_ETMA;
+  return ATTN_OK;
+}
+
+using Kernel = void (*)(CUtensorMap, CUtensorMap, TreeArgs);
+struct Variant {
+  Kernel kernel;
+  int tokens, threads;  // drafted rows a block takes
+  uint32_t smem;
+};
+template <bool kBf16, int MT>
+Variant make_variant() {
+  return {tree_kernel<kBf16, MT>, 4 * MT, 32 * Cfg<kBf16, MT>::kWarps, Cfg<kBf16, MT>::kSmemAlloc};
+}
+const Variant kVariants[2][3] = {
+    {make_variant<false, 1>(), make_variant<false, 2>(), make_variant<false, 4>()},
+    {make_variant<true, 1>(), make_variant<true, 2>(), make_variant<true, 4>()}};
+
+int variant_of(int max_rows) { return max_rows <= 4 ? 0 : max_rows <= 8 ? 1 : 2; }
+
+// Per device: the shared-memory opt-ins and how many blocks of each variant fit at once.
+struct TreeDevice {
+  bool ready = false;
+  int slots[2][3] = {};
+};
+int tree_device(TreeDevice** out) {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static TreeDevice devs[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return ATTN_ECUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  TreeDevice& d = devs[dev];
+  if (!d.ready) {
+    int sms = 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return ATTN_ECUDA;
+    for (int t = 0; t < 2; ++t)
+      for (int v = 0; v < 3; ++v) {
+        const Variant& x = kVariants[t][v];
+        int per_sm = 0;
+        if (cudaFuncSetAttribute(x.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, x.kernel, x.threads, x.smem) != cudaSuccess)
+          return ATTN_ECUDA;
+        d.slots[t][v] = sms * (per_sm > 0 ? per_sm : 1);
+      }
+    d.ready = true;
+  }
+  *out = &d;
+  return ATTN_OK;
+}
+
+}  // namespace
+
+int tree_splits(bool bf16, int B, int max_rows, int max_context, int splits_hint, int* splits, int* split_len) {
+  TreeDevice* d = nullptr;
+  const int rc = tree_device(&d);
+  if (rc != ATTN_OK) return rc;
+  const int v = variant_of(max_rows);
+  const int keys = max_context + max_rows;
+  int n = splits_hint < kMaxSplits ? splits_hint : kMaxSplits;
+  if (n <= 0) {
+    // Segments of at least 128 keys, as many as fill the resident blocks best:
+    // blocks / (waves x slots), less 0.04 for each extra wave.
+    const int tokens = kVariants[bf16][v].tokens, slots = d->slots[bf16][v];
+    const long long units = (long long)B * kHKV * ((max_rows + tokens - 1) / tokens);
+    const int most = (keys + 127) / 128;
+    const int limit = most < kMaxSplits ? most : kMaxSplits;
+    double best = -1.0;
+    n = 1;
+    for (int s = 1; s <= limit; ++s) {
+      const long long blocks = units * s;
+      const long long waves = (blocks + slots - 1) / slots;
+      const double score = (double)blocks / (double)(waves * slots) - 0.04 * (double)(waves - 1);
+      if (score > best + 1e-9) {
+        best = score;
+        n = s;
+      }
+    }
+  }
+  const int per = (keys + n - 1) / n;
+  *split_len = (per + 127) / 128 * 128;
+  *splits = (keys + *split_len - 1) / *split_len;
+  return ATTN_OK;
+}
+
+size_t tree_workspace_bytes(int N, int splits) {
+  return splits <= 1 ? 0 : (size_t)N * kHQ * splits * (kD + 2) * sizeof(float);
+}
+
+int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
+  TreeDevice* d = nullptr;
+  int rc = tree_device(&d);
+  if (rc != ATTN_OK) return rc;
+  const bool bf16 = c.type == ATTN_BF16;
+  alignas(64) CUtensorMap mk, mv;
+  if ((rc = encode_pool(c.k_pages, c.num_pages, bf16, &mk)) != ATTN_OK ||
+      (rc = encode_pool(c.v_pages, c.num_pages, bf16, &mv)) != ATTN_OK)
+    return rc;
+  const TreeArgs a{c.q, c.table, c.ctx_lens, c.row_start, c.masks, c.out, c.splits > 1 ? c.parts : nullptr,
+                   c.B, c.N, c.max_rows, c.max_blocks, c.num_pages, c.max_context, c.split_len, c.splits,
+                   err, 2000000000ull};
+  const Variant& x = kVariants[bf16][variant_of(c.max_rows)];
+  const int row_tiles = (c.max_rows + x.tokens - 1) / x.tokens;
+  x.kernel<<<dim3(c.splits, kHKV * row_tiles, c.B), x.threads, x.smem, stream>>>(mk, mv, a);
+  if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;
+  if (c.splits > 1) {
+    // The merge starts as the split blocks leave (programmatic dependent launch).
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c.max_rows, c.B);
+    cfg.blockDim = dim3(32 * kMergeWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, tree_merge_kernel, a) != cudaSuccess) return ATTN_ELAUNCH;
+  }
+  return ATTN_OK;
+}
+
+}  // namespace attn

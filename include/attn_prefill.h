@@ -63,6 +63,15 @@ extern "C" {
 #define ATTN_D 64
 #define ATTN_MAX_TOKENS (1 << 24)
 #define ATTN_PAGE 16        /* tokens per page of a paged K/V cache */
+#define ATTN_TREE_ROWS 64   /* drafted rows of one sequence: bits of a row's mask */
+
+/* Element types of the calls that take more than one. */
+#define ATTN_F32 0
+#define ATTN_BF16 1         /* 16-bit patterns, as attn_prefill_bf16kv's caches */
+
+/* Which two dims of a head the position rotation turns together. */
+#define ATTN_ROPE_HALVES 0  /* (i, i + 32) */
+#define ATTN_ROPE_PAIRS 1   /* (2 i, 2 i + 1) */
 
 /* Return codes. */
 #define ATTN_OK 0
@@ -303,6 +312,167 @@ int attn_decode_paged_noalloc(const float *q, const float *kPages, const float *
                               const int *blockTable, const int *contextLens, float *out, int B,
                               int maxBlocks, int numPages, int maxContext, int numSplits,
                               cudaStream_t stream);
+
+/*
+ * The serving step around a paged cache. A batch is B sequences: sequence b has
+ * contextLens[b] tokens in its cache and the packed rows rowStart[b] ..
+ * rowStart[b + 1] - 1 of the step's tensors (rowStart non-decreasing, B + 1
+ * entries; a sequence may have no row). Its row i belongs to its token
+ * contextLens[b] + i: one row a sequence is a decode step, many are a prefill
+ * chunk, a tree of drafted tokens or a mixture. Rows of the N that lie behind
+ * the last sequence (padding) are neither read into a cache nor written.
+ * A step that drafts trees is:
+ *   attn_append_paged (norms, rotation, keys and values into the pages)
+ *   attn_tree_paged (each row over its sequence's cache and its ancestors)
+ *   attn_compact_paged (the accepted path's rows moved behind the context)
+ * All of it is enqueued on `stream`, allocates nothing and may be captured into
+ * a graph.
+ *
+ * attn_rope_table -- the table of the position rotation, for the calls below:
+ * cosSin [numPositions][64] fp32, of position p the cosines of p * invFreq[i],
+ * i = 0 .. 31, then the sines, computed in double and rounded once (at position
+ * 2^24 the product in fp32 would be off by a radian). invFreq is a HOST array
+ * of 32 doubles, read before the call returns, so any scaling of the
+ * frequencies is the caller's; a table made another way serves as well. Made
+ * once, it is only read afterwards. Errors: ATTN_EINVAL (NULL, numPositions <
+ * 0), ATTN_ERANGE (above ATTN_MAX_TOKENS), ATTN_EALIGN. numPositions == 0 is a
+ * no-op.
+ */
+int attn_rope_table(const double *invFreq, float *cosSin, int numPositions, cudaStream_t stream);
+
+/*
+ * attn_qk_norm_rope -- RMS norm of every query and key head and the position
+ * rotation, in one pass:
+ *   y[d] = x[d] w[d] / sqrt(sum_e x[e]^2 / 64 + eps)
+ *   (y[a], y[b]) -> (y[a] cos - y[b] sin, y[b] cos + y[a] sin)
+ * (a, b) = (i, i + 32) for ATTN_ROPE_HALVES, (2 i, 2 i + 1) for ATTN_ROPE_PAIRS,
+ * cos and sin of frequency i from row positions[n] of cosSin. fp32 arithmetic,
+ * one rounding at the store.
+ *   q, k       N rows of 32 and 8 heads of 64, fp32 or bf16 (inType), qStride
+ *              and kStride elements between rows (views into a wider projection
+ *              are fine; every row starts on 16 bytes). q may be NULL.
+ *   qWeight, kWeight  [64] fp32; NULL: that tensor is not normed
+ *   cosSin     [numPositions][64] fp32 (attn_rope_table); NULL: no rotation
+ *   positions  int32 [N]; one outside [0, numPositions) is recorded as
+ *              ATTN_EBOUNDS in the device error word and clamped
+ *   qOut       [N][32][64] fp32, the query of the attention calls
+ *   kOut       [N][8][64], fp32 or bf16 (kOutType): the cache precision; it may
+ *              be the rows P .. P + N - 1 of a contiguous kCache
+ * qOut may be q and kOut may be k when type and strides are the same (in
+ * place); any other overlap is undefined. Errors: ATTN_EINVAL (a NULL k, kOut or
+ * qOut, cosSin without positions, a stride shorter than a row, an unknown type
+ * or pairing, numPositions < 1 with a table, eps negative or not finite, N < 0),
+ * ATTN_ERANGE (N above ATTN_MAX_TOKENS), ATTN_EALIGN (pointers and row strides
+ * of 16 bytes). N == 0 is a no-op.
+ */
+int attn_qk_norm_rope(const void *q, const void *k, int inType, long long qStride, long long kStride,
+                      const float *qWeight, const float *kWeight, float eps, const float *cosSin,
+                      const int *positions, int numPositions, int pairing, float *qOut, void *kOut, int kOutType,
+                      int N, cudaStream_t stream);
+
+/*
+ * attn_append_paged, attn_append_paged_bf16kv -- the rows of a batch appended to
+ * its paged cache: keys normed and rotated as by attn_qk_norm_rope, values as
+ * they are, each to slot t % 16 of page blockTable[b * maxBlocks + t / 16], t =
+ * contextLens[b] + i; and the queries, normed and rotated, to qOut. Layouts of
+ * pages and table as attn_decode_paged; the second call's pages are bf16
+ * patterns, to which fp32 rows are rounded once (to nearest even). contextLens
+ * is not advanced. q, k, v, their type and strides, weights, cosSin and pairing
+ * as above (v [N] rows of 8 heads, vStride; q NULL: keys and values only).
+ *   positions  int32 [N], or NULL: row i of sequence b stands at contextLens[b]
+ *              + i. Drafted rows of a tree stand at their depth instead: their
+ *              slot goes by the row, their rotation by the position.
+ * A row whose token lies at or past 16 * maxBlocks, whose page is outside [0,
+ * numPages) or whose context is negative is recorded as ATTN_EBOUNDS and its
+ * key and value are not stored (its query is). Two rows of one slot (sequences
+ * that share a page they write) leave either's. Errors: as attn_qk_norm_rope
+ * (positions may be NULL), ATTN_EINVAL (NULL v, page, table, contextLens or
+ * rowStart, maxBlocks or numPages < 1, B < 0), ATTN_ERANGE (B above 65535, 16 *
+ * maxBlocks or 16 * numPages above ATTN_MAX_TOKENS). B == 0 or N == 0 is a
+ * no-op.
+ */
+int attn_append_paged(const void *q, const void *k, const void *v, int inType, long long qStride, long long kStride,
+                      long long vStride, const float *qWeight, const float *kWeight, float eps, const float *cosSin,
+                      const int *positions, int numPositions, int pairing, float *qOut, float *kPages,
+                      float *vPages, const int *blockTable, const int *contextLens, const int *rowStart, int B,
+                      int N, int maxBlocks, int numPages, cudaStream_t stream);
+int attn_append_paged_bf16kv(const void *q, const void *k, const void *v, int inType, long long qStride,
+                             long long kStride, long long vStride, const float *qWeight, const float *kWeight,
+                             float eps, const float *cosSin, const int *positions, int numPositions, int pairing,
+                             float *qOut, uint16_t *kPages, uint16_t *vPages, const int *blockTable,
+                             const int *contextLens, const int *rowStart, int B, int N, int maxBlocks, int numPages,
+                             cudaStream_t stream);
+
+/*
+ * attn_tree_paged, attn_tree_paged_bf16kv -- attention of up to 64 drafted rows
+ * per sequence over its paged cache, the rows' own keys and values already in
+ * it (attn_append_paged). Row i of sequence b sees the contextLens[b] tokens
+ * before the rows and, of the rows, those j whose bit is set in its mask:
+ *   out[r][h][:] = sum_{j in K} softmax_j(q[r][h] . k_b[j][h/4] / 8) v_b[j][h/4][:]
+ *   q, out     [N][32][64] fp32, the batch's packed rows
+ *   masks      int64 [N], bit j for row j of the same sequence (itself included
+ *              or not, as set; bits past its rows are ignored). NULL: a chain,
+ *              row i sees rows 0 .. i (one row a sequence: a decode step)
+ *   maxRows    at most 64, maxContext: bounds of the batch's row counts and
+ *              context lengths
+ * A row that sees nothing gets zeros. What a row does not see has no influence
+ * on it, not even values that are infinite or NaN; one that it does see makes
+ * its output not finite. Slots past a sequence's last row may hold anything.
+ * q stays in fp32 precision on both caches (bf16 pages are used as stored, q and
+ * the probabilities split into three bf16 terms).
+ * numSplits: segments per sequence, 0 = chosen so that the blocks fill the
+ * device (segments of at least 128 keys, at most 64 of them; larger hints count
+ * as 64). With more than one segment the partials need `workspace`, a device
+ * buffer of at least attn_tree_workspace_bytes(B, N, maxRows, maxContext,
+ * numSplits) bytes, 16-byte aligned, owned by the caller, overwritten by the
+ * call; calls that may overlap (other streams, graphs that run at the same
+ * time) need one each. Nothing in it needs to start at zero.
+ * A context length outside [0, maxContext], rows that run past N, 16 *
+ * maxBlocks tokens or maxRows, and a page index outside [0, numPages) are
+ * recorded as ATTN_EBOUNDS and clamped / read as zeros. Errors: ATTN_EINVAL
+ * (NULL pointer, negative size, maxRows, maxBlocks or numPages < 1),
+ * ATTN_ERANGE (maxRows above 64, maxContext above 16 * maxBlocks, the bounds of
+ * attn_append_paged), ATTN_EALIGN, ATTN_ESPACE, ATTN_ETMA. B == 0 or
+ * N == 0 is a no-op.
+ */
+int attn_tree_paged(const float *q, const float *kPages, const float *vPages, const int *blockTable,
+                    const int *contextLens, const int *rowStart, const long long *masks, float *out, int B, int N,
+                    int maxRows, int maxBlocks, int numPages, int maxContext, int numSplits, void *workspace,
+                    size_t workspaceBytes, cudaStream_t stream);
+int attn_tree_paged_bf16kv(const float *q, const uint16_t *kPages, const uint16_t *vPages, const int *blockTable,
+                           const int *contextLens, const int *rowStart, const long long *masks, float *out, int B,
+                           int N, int maxRows, int maxBlocks, int numPages, int maxContext, int numSplits,
+                           void *workspace, size_t workspaceBytes, cudaStream_t stream);
+
+/*
+ * attn_tree_workspace_bytes -- the workspace the two calls above need for the
+ * same sizes on the current device (enough for either); 0 when one segment
+ * suffices (or for invalid arguments).
+ */
+size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxContext, int numSplits);
+
+/*
+ * attn_compact_paged, attn_compact_paged_bf16kv -- after the check of a drafted
+ * tree: the keys and values of the accepted rows moved to the front, so that
+ * they lie at tokens contextLens[b] .. contextLens[b] + keepCounts[b] - 1 and
+ * the next step's context is contextLens[b] + keepCounts[b].
+ *   keep        int32 [B][maxKeep]: the accepted rows of sequence b, rising, each
+ *               in [0, maxRows); entries from keepCounts[b] on are not read
+ *   keepCounts  int32 [B], each in [0, maxKeep]
+ * keep[b][i] >= i, so the moves run in place. Tokens that no accepted row moves
+ * to stay as they are. A sequence whose list is not as above, or whose tokens or
+ * pages are out of range, is recorded as ATTN_EBOUNDS and left as it is. Pages
+ * and table as attn_append_paged; sequences must not share the pages of their
+ * rows. Errors: ATTN_EINVAL (NULL pointer, negative size, maxRows, maxBlocks or
+ * numPages < 1), ATTN_ERANGE (maxRows above 64, maxKeep above maxRows, the
+ * bounds of attn_append_paged), ATTN_EALIGN. B == 0 or maxKeep == 0 is a no-op.
+ */
+int attn_compact_paged(float *kPages, float *vPages, const int *blockTable, const int *contextLens,
+                       const int *keep, const int *keepCounts, int B, int maxKeep, int maxRows, int maxBlocks,
+                       int numPages, cudaStream_t stream);
+int attn_compact_paged_bf16kv(uint16_t *kPages, uint16_t *vPages, const int *blockTable, const int *contextLens,
+                              const int *keep, const int *keepCounts, int B, int maxKeep, int maxRows,
+                              int maxBlocks, int numPages, cudaStream_t stream);
 
 /*
  * The score-matrix pipeline ("Inference Attention 1: The Full Score Matrix",

@@ -15,8 +15,8 @@
 // sum e^(m_s - m) l_s.
 //
 // The products run on mma.sync (16 query rows x 8 keys), in fp32 precision:
-//   fp32 pages: each operand as two tf32 terms x = hi + lo (hi = x with its 13
-//     low mantissa bits cleared), hi hi + hi lo + lo hi, as in the prefill kernel;
+//   fp32 pages: each operand as two tf32 terms x = hi + lo (hi = x rounded to 11
+//     bits), hi hi + hi lo + lo hi;
 //   bf16 pages: K and V exactly as stored, q and the probabilities as three bf16
 //     terms each (24 bits), so nothing of q or p is lost to the cache's precision.
 // The reference maximum of a row moves only when a score passes it by 2^8 (p
@@ -134,7 +134,10 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ uint32_t hi_of(float x) { return __float_as_uint(x) & 0xffffe000u; }
+// The tf32 terms: hi rounded to nearest (half the remainder of a truncation,
+// and of either sign, so what the products drop does not lean one way), lo the
+// exact rest, of which the tensor core reads the upper 11 bits.
+__device__ __forceinline__ uint32_t hi_of(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
 __device__ __forceinline__ uint32_t lo_of(float x) { return __float_as_uint(x - __uint_as_float(hi_of(x))); }
 // Three bf16 terms of a pair: two truncated, the last rounded to nearest: 24
 // bits, all of an fp32 value whose last term does not underflow.
@@ -148,7 +151,8 @@ __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0
 
 // The tensor core's own accumulation does not round to nearest: over a long key
 // range its error would all lean one way. Each page's product starts at zero
-// and is added here, rounded to nearest.
+// and is added here, rounded to nearest; a score's small terms have a chain of
+// their own for the same reason.
 __device__ __forceinline__ void add4(float (&o)[4], const float (&x)[4]) {
   tc::add2(o[0], o[1], o[0], o[1], x[0], x[1]);
   tc::add2(o[2], o[3], o[2], o[3], x[2], x[3]);
@@ -317,6 +321,9 @@ tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUte
     for (int nt = 0; nt < 2; ++nt) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.f;
+      float low[MT][4];  // the small terms' own chain
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) low[mt][0] = low[mt][1] = low[mt][2] = low[mt][3] = 0.f;
       if constexpr (kBf16) {
         uint32_t kb[2][4];
         const int r = nt * 8 + (lane & 7);
@@ -332,7 +339,7 @@ tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUte
             for (int k = 2; k >= 0; --k) {
               uint32_t qa[4];
               qfrag(mt, st4, k, qa);
-              mma_bf16(sc[mt][nt], qa, b0, b1);
+              mma_bf16(k ? low[mt] : sc[mt][nt], qa, b0, b1);
             }
         }
       } else {
@@ -349,13 +356,15 @@ tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUte
               uint32_t qh[4], ql[4];
               qfrag(mt, 2 * j + u, 0, qh);
               qfrag(mt, 2 * j + u, 1, ql);
-              mma_tf32(sc[mt][nt], ql, hi_of(e0), hi_of(e1));
-              mma_tf32(sc[mt][nt], qh, lo_of(e0), lo_of(e1));
+              mma_tf32(low[mt], ql, hi_of(e0), hi_of(e1));
+              mma_tf32(low[mt], qh, lo_of(e0), lo_of(e1));
               mma_tf32(sc[mt][nt], qh, hi_of(e0), hi_of(e1));
             }
           }
         }
       }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) add4(sc[mt][nt], low[mt]);
     }
 
     if (tail) {

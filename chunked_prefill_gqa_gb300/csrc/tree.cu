@@ -29,13 +29,13 @@
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
+#include "tree.cuh"
 
 namespace attn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr float kC = kScale * kLog2e;     // scores in log2 units
-constexpr float kStale = 8.f;             // log2: how far a score may pass the reference maximum
+constexpr float kC = kTreeC, kStale = kTreeStale;
 constexpr int kMaxSplits = 64;
 
 // Variants: MT m-tiles of 16 rows (4 MT drafted tokens). Warps, ring depth and
@@ -62,50 +62,6 @@ struct Cfg {
   static_assert(16 * MT * kD * 4 <= kStages * kStage, "a warp's accumulator fits its own ring");
   static_assert(kWarps * 16 * MT * 8 <= kQBytes, "the warps' maxima and sums fit where q was");
 };
-
-struct TreeArgs {
-  const float* q;            // [N][32][64]
-  const int* table;          // [B][max_blocks]
-  const int* ctx_lens;       // [B]
-  const int* row_start;      // [B + 1]
-  const long long* masks;    // [N], or nullptr: a chain (row i sees rows 0 .. i)
-  float* out;                // [N][32][64]
-  float* parts;              // [N][32][splits][64], then [N][32][splits][2] (log2 maximum, sum)
-  int B, N, max_rows, max_blocks, num_pages, max_context, split_len, splits;
-  unsigned* err;
-  unsigned long long timeout_ns;
-};
-
-// One sequence of the batch, its lengths checked.
-struct Seq {
-  int ctx, first, rows, keys;
-  bool ok;
-};
-__device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b) {
-  Seq s;
-  s.ctx = __ldg(a.ctx_lens + b);
-  s.first = __ldg(a.row_start + b);
-  const int end = __ldg(a.row_start + b + 1);
-  s.ok = true;
-  const int room = min((long long)a.max_blocks * ATTN_PAGE, (long long)ATTN_MAX_TOKENS);
-  if (s.ctx < 0 || s.ctx > a.max_context) {
-    s.ok = false;
-    s.ctx = s.ctx < 0 ? 0 : a.max_context;
-  }
-  if (s.first < 0 || end < s.first || end > a.N || (long long)end - s.first > a.max_rows) {
-    s.ok = false;
-    s.first = min(max(s.first, 0), a.N);
-    s.rows = min(min(max(end, s.first), a.N) - s.first, a.max_rows);
-  } else {
-    s.rows = end - s.first;
-  }
-  if (s.ctx + s.rows > room) {
-    s.ok = false;
-    s.ctx = min(s.ctx, room);
-  }
-  s.keys = min(s.ctx + s.rows, room);
-  return s;
-}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -139,14 +95,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 // exact rest, of which the tensor core reads the upper 11 bits.
 __device__ __forceinline__ uint32_t hi_of(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
 __device__ __forceinline__ uint32_t lo_of(float x) { return __float_as_uint(x - __uint_as_float(hi_of(x))); }
-// Three bf16 terms of a pair: two truncated, the last rounded to nearest: 24
-// bits, all of an fp32 value whose last term does not underflow.
-__device__ __forceinline__ void split3(float x, float y, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
-  t0 = tc::pack_bf16_trunc(x, y);
-  const float rx = x - tc::bf16_trunc(x), ry = y - tc::bf16_trunc(y);
-  t1 = tc::pack_bf16_trunc(rx, ry);
-  t2 = tc::pack_bf16_rn(rx - tc::bf16_trunc(rx), ry - tc::bf16_trunc(ry));
-}
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // The tensor core's own accumulation does not round to nearest: over a long key
@@ -736,19 +684,14 @@ int encode_pool(const void* base, int num_pages, bool bf16, CUtensorMap* map) {
   return ATTN_OK;
 }
 
-using Kernel = void (*)(CUtensorMap, CUtensorMap, TreeArgs);
-struct Variant {
-  Kernel kernel;
-  int tokens, threads;  // drafted rows a block takes
-  uint32_t smem;
-};
+using Variant = TreeVariant;
 template <bool kBf16, int MT>
 Variant make_variant() {
   return {tree_kernel<kBf16, MT>, 4 * MT, 32 * Cfg<kBf16, MT>::kWarps, Cfg<kBf16, MT>::kSmemAlloc};
 }
 const Variant kVariants[2][3] = {
     {make_variant<false, 1>(), make_variant<false, 2>(), make_variant<false, 4>()},
-    {make_variant<true, 1>(), make_variant<true, 2>(), make_variant<true, 4>()}};
+    {tree_tc_variant(0), tree_tc_variant(1), tree_tc_variant(2)}};
 
 int variant_of(int max_rows) { return max_rows <= 4 ? 0 : max_rows <= 8 ? 1 : 2; }
 
@@ -830,7 +773,7 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
   if ((rc = encode_pool(c.k_pages, c.num_pages, bf16, &mk)) != ATTN_OK ||
       (rc = encode_pool(c.v_pages, c.num_pages, bf16, &mv)) != ATTN_OK)
     return rc;
-  const TreeArgs a{c.q, c.table, c.ctx_lens, c.row_start, c.masks, c.out, c.splits > 1 ? c.parts : nullptr,
+  const TreeArgs a{c.q, c.v_pages, c.table, c.ctx_lens, c.row_start, c.masks, c.out, c.splits > 1 ? c.parts : nullptr,
                    c.B, c.N, c.max_rows, c.max_blocks, c.num_pages, c.max_context, c.split_len, c.splits,
                    err, 2000000000ull};
   const Variant& x = kVariants[bf16][variant_of(c.max_rows)];

@@ -1,0 +1,619 @@
+// tree_tc.cu -- the drafted-tree attention of tree.cu on the tcgen05 tensor
+// cores, for bf16 pages.
+//
+// The few query rows of a (sequence, KV head) are the N side of both products
+// and the keys the M side, so a tile is always 128 full keys whatever the
+// number of rows, and the three bf16 terms of q (and of the probabilities) that
+// keep them in fp32 precision cost narrow instructions, or stack along N:
+//   S^T [128 keys][R] = K [128][64] . (q3, q2, q1)^T         12 MMAs of N = R
+//   O^T [64 dims][3 R] += V^T [64][128] . [p1 | p2 | p3]      8 MMAs of N = 3 R
+// with R = 4 x the drafted rows of a block (16, 32 or 64 columns). K is a
+// K-major operand as it lies in the page, V^T an MN-major one, also as it lies;
+// nothing of the cache is converted or transposed. p goes through shared memory,
+// written by the thread that owns its key: one row of N per key, which is an
+// MN-major operand again. The accumulators are in tensor memory: S^T in lanes =
+// keys, O^T (M = 64) in lanes 0-15 of each lane quarter.
+//
+// A thread owns one key and 16 columns, so the softmax over keys runs across
+// threads. It needs no maximum in the steady state: a row's reference moves only
+// when a score passes it by 2^8, which each thread checks on its own values; one
+// barrier with a vote per tile decides. Sums stay per thread until the end. The
+// tensor core's accumulation does not round to nearest, and over a long key
+// range that error would lean one way: every 8 tiles (and when a reference
+// moves, which then costs nothing more) O is added to fp32 sums in shared
+// memory and starts anew.
+//
+// Roles: the softmax warps; one warp for TMA (16-token pages through the block
+// table, 8 boxes each of K and V a tile); one thread for the MMAs. S(n+1) is
+// issued as soon as S(n) has been read into registers, so it runs under the
+// softmax of tile n, and PV(n) under the first half of that of tile n + 1.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+#include "tree.cuh"
+
+namespace attn {
+namespace {
+
+using namespace tc;
+
+constexpr int kKeys = 128;                          // keys of a tile: M of S^T
+constexpr int kPages = kKeys / ATTN_PAGE;
+constexpr uint32_t kOperand = kKeys * kD * 2;       // 16 KB: a tile of K, of V, or an N atom of p
+constexpr uint32_t kStageBytes = 2 * kOperand;
+constexpr uint32_t kBox = ATTN_PAGE * 128;
+constexpr float kUnseen = -3e38f;                   // reference of a row that has seen no key
+
+constexpr int kCols = 16;                           // columns of a softmax thread
+constexpr int kFlush = 8;                           // tiles between two flushes of O
+
+template <int R>
+struct Lay {
+  static constexpr int kParts = R / kCols;          // warps on one lane quarter
+  static constexpr int kSoft = 4 * kParts;          // softmax warps
+  static constexpr int kTmaWarp = kSoft, kMmaWarp = kSoft + 1;
+  static constexpr int kThreads = 32 * (kSoft + 2);
+  static constexpr int kBlocks = R == 64 ? 1 : 2;   // per SM
+  static constexpr int kStages = R == 64 ? 4 : 2;
+  static constexpr int kN = 3 * R;
+  static constexpr uint32_t kColS = 0, kColO = 2 * R;                // two S buffers, then O's three terms
+  static constexpr uint32_t kTmem = R == 64 ? 512 : R == 32 ? 256 : 128;
+  static constexpr uint32_t kSmemQ = kStages * kStageBytes;          // [3 R rows][128 bytes]
+  static constexpr uint32_t kSmemP = kSmemQ + ((kN * 128 + 1023) / 1024) * 1024;
+  // O so far, [R][64] fp32: for 64 rows its own 16 KB; for 32 and 16 the bytes
+  // that the last atom of p leaves free in each of its 128 rows (64 or 32: just
+  // as many), so that two blocks fit an SM.
+  static constexpr uint32_t kFree = R == 64 ? 0 : 4 * R / 2;
+  static constexpr uint32_t kSmemAcc = kSmemP + (R == 64 ? 3 : (kN + 63) / 64 - 1) * kOperand;
+  static constexpr uint32_t kSmemMask = kSmemAcc + kOperand;
+  static_assert(R == 64 ? R * kD * 4 == kOperand : kKeys * kFree == R * kD * 4 && (kN % 64) * 2 + kFree <= 128, "acc");
+  static constexpr uint32_t kSmemMax = kSmemMask + (R / 4) * 8;      // [4 quarters][R]
+  static constexpr uint32_t kSmemBar = kSmemMax + 4 * R * 4;
+  static constexpr int kNumBars = 4 * kStages + 7;
+  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2), fresh (2)
+  static constexpr uint32_t kSmemAlloc = kSmemWords + 32 + 1024;
+  static_assert(kBlocks * (kSmemAlloc + 1024) <= 233472 && kSmemAlloc <= 232448, "shared memory of an SM");
+  static_assert(kColO + kN <= kTmem && kBlocks * kTmem <= 512, "TMEM layout");
+};
+
+// kind::f16, bf16 operands, fp32 accumulate; A K-major (S) or MN-major (PV).
+__host__ __device__ constexpr uint32_t idesc_tree(int M, int N, bool mn_major) {
+  return idesc_bf16(M, N, mn_major) | (mn_major ? 1u << 15 : 0u);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+// All softmax threads of the block meet; returns how many warps failed a wait,
+// and in `over` how many saw a score that moves a reference. (A hardware
+// barrier: it can hang only if a warp stays away, so none ever does. A warp
+// whose wait failed still meets, and all leave together.)
+__device__ __forceinline__ int meet(int threads, bool mine_over, bool failed, int lane, int* over) {
+  int count;
+  const int p = lane == 0 ? failed : mine_over;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, 1, %2, p;\n\t}"
+      : "=r"(count)
+      : "r"(p), "r"(threads)
+      : "memory");
+  *over = count / 31;
+  return count % 31;
+}
+__device__ __forceinline__ void meet(int threads) {
+  asm volatile("barrier.cta.sync.aligned 1, %0;" ::"r"(threads) : "memory");
+}
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+struct Wait {
+  unsigned* err;
+  unsigned long long timeout_ns;
+  volatile int* abort_flag;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+      if (*abort_flag) return false;
+      if (globaltimer_ns() - t0 > timeout_ns) {
+        record_error(err, kDevErrTimeout);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(bar, parity));
+  }
+};
+
+// Where column j of dim d is kept.
+template <int R>
+__device__ __forceinline__ float* acc_at(uint8_t* smem, int j, int d) {
+  uint8_t* const base = smem + Lay<R>::kSmemAcc;
+  if constexpr (R == 64) {
+    return reinterpret_cast<float*>(base) + j * kD + d;
+  } else {
+    constexpr uint32_t kFree = Lay<R>::kFree;
+    const uint32_t at = (uint32_t)(j * kD + d) * 4u;
+    return reinterpret_cast<float*>(base + sw128(at / kFree * 128u + 128u - kFree + at % kFree));
+  }
+}
+
+template <int R>
+__global__ void __launch_bounds__(Lay<R>::kThreads, Lay<R>::kBlocks)
+tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
+  using L = Lay<R>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: descriptors in uniform registers
+  const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
+
+  const Seq seq = load_seq(a, b);
+  const int i0 = rt * (R / 4);  // the block's first drafted row
+  const int nrows = min(R / 4, seq.rows - i0);
+  const int k0 = s * a.split_len;
+  const int k1 = min(k0 + a.split_len, seq.keys);
+  if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+  if (nrows <= 0) return;
+  if (k0 >= k1) {
+    // Past the sequence: the merge counts its segments from the lengths. A
+    // sequence without any key (only a refused one) gets zeros.
+    if (s == 0)
+      for (int e = tid; e < nrows * kGroup * kD; e += L::kThreads)
+        a.out[((size_t)(seq.first + i0 + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
+    return;
+  }
+  const bool whole = seq.keys <= a.split_len;  // one segment: the output is written here
+  const int ntiles = (k1 - k0 + kKeys - 1) / kKeys;
+
+  uint64_t* const kfull = reinterpret_cast<uint64_t*>(smem + L::kSmemBar);  // [stage] K landed
+  uint64_t* const vfull = kfull + kStages;                                  // [stage] V landed
+  uint64_t* const kempty = vfull + kStages;                                 // [stage] S done with K
+  uint64_t* const vempty = kempty + kStages;                                // [stage] PV done with V
+  uint64_t* const sfull = vempty + kStages;                                // [2] S written
+  uint64_t* const sread = sfull + 2;                                       // [2] S read into registers
+  uint64_t* const pfull = sread + 2;                                       // p written (and O rescaled)
+  uint64_t* const odone = pfull + 1;                                       // PV complete
+  uint64_t* const drain = odone + 1;                                       // MMAs in flight on abort
+  uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
+  uint32_t* const odd = words + 2;                 // [2] drafted rows whose value is not finite
+  volatile uint32_t* const fresh = words + 4;      // [2] tile n starts O anew, at n % 2
+  unsigned long long* const masks = reinterpret_cast<unsigned long long*>(smem + L::kSmemMask);
+  const Wait wait{a.err, a.timeout_ns, abort_flag};
+
+  // The TMA warp: 8 lanes load the 8 pages of a tile of K, or of V.
+  const int* const trow = a.table + (size_t)b * a.max_blocks;
+  auto page_of = [&](int n) -> int {  // -1: no page there; out of range: num_pages (reads as zeros)
+    const int t = k0 + n * kKeys + lane * ATTN_PAGE;
+    if (lane >= kPages || n >= ntiles || t >= k1) return -1;
+    const int p = __ldg(trow + t / ATTN_PAGE);
+    if (p >= 0 && p < a.num_pages) return p;
+    record_error(a.err, kDevErrBounds);
+    return a.num_pages;
+  };
+  auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t operand, int n, int page) {
+    const int st = n % kStages;
+    const unsigned boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * kBox);
+    __syncwarp();
+    if (page >= 0)
+      tma_load_2d(smem + st * kStageBytes + operand + lane * kBox, map, &full[st], head * kD, page * ATTN_PAGE);
+  };
+  // K(n + 1) goes before V(n): its stage is free earlier.
+  int page_v = -1, page_k = -1, page_next = -1, ahead = 0;
+  auto load_next = [&]() -> bool {  // V(ahead) and K(ahead + 1)
+    const int n = ahead;
+    if (n + 1 < ntiles) {
+      if (n + 1 >= kStages && !wait.warp(&kempty[(n + 1) % kStages], ((n + 1) / kStages - 1) & 1)) return false;
+      load(&mk, kfull, 0, n + 1, page_k);
+    }
+    if (n >= kStages && !wait.warp(&vempty[n % kStages], (n / kStages - 1) & 1)) return false;
+    load(&mv, vfull, kOperand, n, page_v);
+    page_v = page_k;
+    page_k = page_next;
+    page_next = page_of(n + 3);
+    ++ahead;
+    return true;
+  };
+  if (warp == L::kTmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < 4 * kStages; ++i) mbar_init(&kfull[i], 1);
+      mbar_init(&sfull[0], 1);
+      mbar_init(&sfull[1], 1);
+      mbar_init(&sread[0], L::kSoft);
+      mbar_init(&sread[1], L::kSoft);
+      mbar_init(pfull, L::kSoft);
+      mbar_init(odone, 1);
+      mbar_init(drain, 1);
+      fence_mbar_init();
+      *abort_flag = 0;
+      odd[0] = odd[1] = 0;
+    }
+    __syncwarp();
+    // The first tiles are on their way before the block has met.
+    page_v = page_of(0);
+    page_k = page_of(1);
+    page_next = page_of(2);
+    load(&mk, kfull, 0, 0, page_v);
+    while (ahead < kStages - 1 && ahead < ntiles) load_next();
+  } else if (warp == L::kMmaWarp) {
+    tmem_alloc(words, L::kTmem);
+    tmem_relinquish();
+  } else {
+    // q's terms: row t R + r of 128 bytes holds term t of row r.
+    for (int e = tid; e < R * 8; e += 32 * L::kSoft) {  // (row, 8 dims)
+      const int r = e >> 3, c8 = e & 7, i = r >> 2;
+      float x[8];
+      if (i < nrows) {
+        const float4* src = reinterpret_cast<const float4*>(
+            a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (r & 3)) * kD + c8 * 8);
+        const float4 u = __ldg(src), v = __ldg(src + 1);
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = 0.f;
+      }
+      uint32_t w[3][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) split3(x[2 * k], x[2 * k + 1], w[0][k], w[1][k], w[2][k]);
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        *reinterpret_cast<uint4*>(smem + L::kSmemQ + sw128((uint32_t)(t * R + r) * 128u + c8 * 16u)) =
+            make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+    }
+    for (int i = tid; i < R / 4; i += 32 * L::kSoft)
+      masks[i] = i >= nrows ? 0ull
+                 : a.masks  ? (unsigned long long)__ldg(a.masks + seq.first + i0 + i)
+                            : ~0ull >> (63 - (i0 + i));
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = words[0];
+
+  if (warp == L::kTmaWarp) {
+    while (ahead < ntiles && load_next()) {
+    }
+    if (*abort_flag) {
+      // Copies still in flight land before the block's shared memory is
+      // released (K(ahead) and, where its wait ran out, K(ahead + 1) at most).
+      for (int i = max(0, ahead - kStages); i < min(ahead + 2, ntiles); ++i)
+        mbar_wait(&kfull[i % kStages], (i / kStages) & 1, 1000000);
+      for (int i = max(0, ahead - kStages); i < ahead; ++i) mbar_wait(&vfull[i % kStages], (i / kStages) & 1, 1000000);
+    }
+    __syncwarp();
+  } else if (warp == L::kMmaWarp) {
+    constexpr uint32_t kIdS = idesc_tree(128, R, false), kIdPV = idesc_tree(64, L::kN, true);
+    const uint32_t base = smem_u32(smem);
+    const uint64_t qd = sdesc_sw128(base + L::kSmemQ), pd = sdesc_sw128_mn(base + L::kSmemP, kOperand);
+    auto issue_s = [&](int n) -> bool {
+      const int st = n % kStages;
+      if (!wait.warp(&kfull[st], (n / kStages) & 1)) return false;
+      if (n > 1 && !wait.warp(&sread[n & 1], ((n >> 1) - 1) & 1)) return false;  // S(n - 2) is in registers
+      tc_fence_after();
+      const uint64_t kd = sdesc_sw128(base + st * kStageBytes);
+      const uint32_t dst = tmem + L::kColS + (n & 1) * R;
+      if (elect()) {
+        // The smallest term first: only the last four accumulations are at
+        // the score's own size.
+#pragma unroll
+        for (int t = 2; t >= 0; --t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            mma_f16_ss(dst, kd + x * 2, qd + t * (R * 8) + x * 2, kIdS, t < 2 || x > 0);
+        mma_commit(&sfull[n & 1]);
+        mma_commit(&kempty[st]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = issue_s(0);
+    for (int n = 0; ok && n < ntiles; ++n) {
+      if (n + 1 < ntiles && !(ok = issue_s(n + 1))) break;
+      const int st = n % kStages;
+      if (!(ok = wait.warp(pfull, n & 1) && wait.warp(&vfull[st], (n / kStages) & 1))) break;
+      tc_fence_after();
+      const uint64_t vd = sdesc_sw128_mn(base + st * kStageBytes + kOperand);
+      const uint32_t old = n > 0 && !fresh[n & 1];
+      if (elect()) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x)  // 16 keys a step: 2048 bytes of rows
+          mma_f16_ss(tmem + L::kColO, vd + x * 128, pd + x * 128, kIdPV, x > 0 ? 1u : old);
+        mma_commit(&vempty[st]);
+        mma_commit(odone);
+      }
+      __syncwarp();
+    }
+    if (*abort_flag) {
+      if (elect()) {
+        mma_commit(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < a.timeout_ns) {
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int quarter = warp & 3, part = warp >> 2;
+    const int key = quarter * 32 + lane;       // this thread's key of a tile
+    const int col0 = part * kCols;             // its first column
+    const uint32_t lane_tmem = tmem + ((uint32_t)(quarter * 32) << 16);
+    constexpr int kMeet = 32 * L::kSoft;
+    float* const maxima = reinterpret_cast<float*>(smem + L::kSmemMax);
+    const int d = quarter * 16 + lane;         // lanes 0-15 hold the dims of O^T
+    float sum[kCols], neg[kCols];  // this key's share of the sums; minus the references
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+      sum[j] = 0.f;
+      neg[j] = -kUnseen;
+    }
+    float ref = kUnseen;  // lane j (and 16 + j): the reference of column col0 + j
+    bool failed = false, kept = false;  // kept: acc holds something
+    // Eight columns of O^T at this thread's dim, from tensor memory: the three
+    // terms added, the smallest first.
+    auto read_o = [&](int h, float (&o)[8]) {
+      float o1[8];
+      tmem_ld8(lane_tmem + L::kColO + 2 * R + col0 + h, o);
+      tmem_ld8(lane_tmem + L::kColO + R + col0 + h, o1);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += o1[j];
+      tmem_ld8(lane_tmem + L::kColO + col0 + h, o1);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] += o1[j];
+    };
+
+    int n = 0;
+    for (; n < ntiles; ++n) {
+      failed |= !wait.warp(&sfull[n & 1], (n >> 1) & 1);
+      tc_fence_after();
+      const uint32_t s_tmem = lane_tmem + L::kColS + (n & 1) * R + col0;
+      float x[kCols];
+      tmem_ld16(s_tmem, x);
+      tmem_wait_ld();
+      const int pos = k0 + n * kKeys + key;
+      const int at = pos - seq.ctx;  // >= 0: a drafted row, or a slot past the last
+      const bool tail = k0 + (n + 1) * kKeys > seq.ctx;
+      uint32_t hidden = 0;  // columns that do not see this key
+      if (tail) {
+        if (at >= 0) {
+          const bool past = pos >= k1;
+          hidden = past ? ~0u : 0u;
+          if (!past)
+#pragma unroll
+            for (int i = 0; i < kCols / 4; ++i)
+              if (!(masks[col0 / 4 + i] >> at & 1)) hidden |= 15u << (4 * i);
+          // The value row of this key: zeros past the last key (its slot may hold
+          // anything), and no infinity or NaN of a drafted row into a product
+          // with the zero probability of a row that does not see it.
+          if (!wait(&vfull[n % kStages], (n / kStages) & 1)) failed = true;
+          uint8_t* v = smem + (n % kStages) * kStageBytes + kOperand;
+          for (int c8 = part; c8 < 8; c8 += L::kParts) {
+            uint4* p = reinterpret_cast<uint4*>(v + sw128((uint32_t)key * 128u + c8 * 16u));
+            uint4 u = past ? make_uint4(0, 0, 0, 0) : *p;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+            bool bad = past;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, bad = true;
+              if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu, bad = true;
+            }
+            if (bad) *p = u;
+            if (bad && !past) atomicOr(odd + (at >> 5), 1u << (at & 31));
+          }
+        }
+        failed = __any_sync(0xffffffffu, failed);
+      }
+      // Scores relative to the references, in log2 units. Does one pass 2^8?
+      auto relative = [&]() -> float {
+        float most = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kCols; j += 2) {
+          fma2(x[j], x[j + 1], x[j], x[j + 1], kTreeC, kTreeC, neg[j], neg[j + 1]);
+          if (tail) {
+            if (hidden >> j & 1) x[j] = -INFINITY;
+            if (hidden >> (j + 1) & 1) x[j + 1] = -INFINITY;
+          }
+          most = max3(most, x[j], x[j + 1]);
+        }
+        return most;
+      };
+      const float most = relative();
+      int over;
+      if (meet(kMeet, __any_sync(0xffffffffu, most > kTreeStale), failed, lane, &over)) {
+        failed = true;
+        break;
+      }
+      float alpha = 1.f;
+      if (over) {
+        tmem_ld16(s_tmem, x);  // the scores again
+        tmem_wait_ld();
+        float mine = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          const float m = warp_max(hidden >> j & 1 ? -INFINITY : x[j]);
+          if ((lane & 15) == j) mine = m;
+        }
+        const int c = col0 + (lane & 15);
+        if (lane < kCols) maxima[quarter * R + c] = mine;
+        meet(kMeet);
+        mine = fmaxf(fmaxf(maxima[c], maxima[R + c]), fmaxf(maxima[2 * R + c], maxima[3 * R + c]));
+        const float next = fmaxf(ref, mine * kTreeC);
+        alpha = ex2(ref - next);
+        ref = next;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          neg[j] = -__shfl_sync(0xffffffffu, next, j);
+          sum[j] *= __shfl_sync(0xffffffffu, alpha, j);
+        }
+        relative();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sread[n & 1]);
+      uint32_t w[3][kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols; j += 2) {
+        const float p0 = ex2(x[j]), p1 = ex2(x[j + 1]);
+        add2(sum[j], sum[j + 1], sum[j], sum[j + 1], p0, p1);
+        split3(p0, p1, w[0][j / 2], w[1][j / 2], w[2][j / 2]);
+      }
+      // PV(n-1) has read p, and its O is complete.
+      if (n > 0) {
+        failed |= !wait.warp(odone, (n - 1) & 1);
+        if (over || n % kFlush == 0) {
+          // O moves to fp32 sums that round to nearest, with the references' change.
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < kCols; h += 8) {
+            float o[8];
+            read_o(h, o);
+            if (kept && lane < 16) {
+              float old[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) old[j] = *acc_at<R>(smem, col0 + h + j, d);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] += old[j];
+            }
+            if (over) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] *= __shfl_sync(0xffffffffu, alpha, h + j);
+            }
+            if (lane < 16) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) *acc_at<R>(smem, col0 + h + j, d) = o[j];
+            }
+          }
+          kept = true;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 3; ++t) {
+        const int c = t * R + col0;  // 64 columns an atom, 8 a 16-byte chunk
+        uint8_t* row = smem + L::kSmemP + (c >> 6) * kOperand;
+#pragma unroll
+        for (int k = 0; k < kCols / 8; ++k)
+          *reinterpret_cast<uint4*>(row + sw128((uint32_t)key * 128u + ((c & 63) / 8 + k) * 16u)) =
+              make_uint4(w[t][4 * k], w[t][4 * k + 1], w[t][4 * k + 2], w[t][4 * k + 3]);
+      }
+      if (tid == 0) fresh[n & 1] = over || n % kFlush == 0;
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pfull);
+    }
+
+    // ------------------------------------------------------------ epilogue
+    if (!failed) failed = !wait.warp(odone, (ntiles - 1) & 1);
+    {
+      float l = 0.f;  // lanes j and 16 + j: the sum of column col0 + j
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) {
+        float v = sum[j];
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+        if ((lane & 15) == j) l = v;
+      }
+      const int c = col0 + (lane & 15);
+      int over;
+      // The maxima of the last tile may still be read: meet before they become sums.
+      if (meet(kMeet, false, failed, lane, &over)) goto done;
+      if (lane < kCols) maxima[quarter * R + c] = l;
+      meet(kMeet);
+      l = (maxima[c] + maxima[R + c]) + (maxima[2 * R + c] + maxima[3 * R + c]);
+      tc_fence_after();
+      float o[kCols];
+#pragma unroll
+      for (int h = 0; h < kCols; h += 8) read_o(h, reinterpret_cast<float (&)[8]>(o[h]));
+      if (kept && lane < 16) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) o[j] += *acc_at<R>(smem, col0 + j, d);
+      }
+      unsigned long long rest = ((unsigned long long)odd[1] << 32) | odd[0];
+      while (rest) {  // drafted values that are not finite reach the rows that see them
+        const int j0 = __ffsll((long long)rest) - 1;
+        rest &= rest - 1;
+        const int page = __ldg(trow + (seq.ctx + j0) / ATTN_PAGE);
+        if (lane < 16 && page >= 0 && page < a.num_pages) {
+          const uint16_t raw = __ldg(static_cast<const uint16_t*>(a.v_pages) +
+                                     (((size_t)page * ATTN_PAGE + (seq.ctx + j0) % ATTN_PAGE) * kHKV + head) * kD + d);
+          if ((raw & 0x7f80u) == 0x7f80u)
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+              if (masks[(col0 + j) >> 2] >> j0 & 1) o[j] += __uint_as_float((uint32_t)raw << 16);
+        }
+      }
+      const size_t at0 = (size_t)(seq.first + i0) * kHQ + head * kGroup;  // row r: + (r / 4) * 32 + r % 4
+      if (whole) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          const float f = __shfl_sync(0xffffffffu, inv, j);
+          const int r = col0 + j;
+          if (lane < 16 && (r >> 2) < nrows) a.out[(at0 + (r >> 2) * kHQ + (r & 3)) * kD + d] = o[j] * f;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) {
+          const int r = col0 + j;
+          if (lane < 16 && (r >> 2) < nrows)
+            a.parts[((at0 + (r >> 2) * kHQ + (r & 3)) * a.splits + s) * kD + d] = o[j];
+        }
+        float2* mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+        if (quarter == 0 && lane < kCols && (c >> 2) < nrows)
+          mls[(at0 + (c >> 2) * kHQ + (c & 3)) * a.splits + s] = make_float2(ref == kUnseen ? -INFINITY : ref, l);
+      }
+    }
+  done:;
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*abort_flag && !whole) {  // after a failed wait the segment counts as empty
+    float2* mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+    for (int r = tid; r < nrows * kGroup; r += L::kThreads)
+      mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
+          make_float2(-INFINITY, 0.f);
+  }
+  if (warp == L::kMmaWarp) tmem_dealloc(tmem, L::kTmem);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace
+
+TreeVariant tree_tc_variant(int which) {
+  switch (which) {
+    case 0: return {tree_tc_kernel<16>, 4, Lay<16>::kThreads, Lay<16>::kSmemAlloc};
+    case 1: return {tree_tc_kernel<32>, 8, Lay<32>::kThreads, Lay<32>::kSmemAlloc};
+    default: return {tree_tc_kernel<64>, 16, Lay<64>::kThreads, Lay<64>::kSmemAlloc};
+  }
+}
+
+}  // namespace attn

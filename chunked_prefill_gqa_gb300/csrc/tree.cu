@@ -63,11 +63,6 @@ struct Cfg {
   static_assert(kWarps * 16 * MT * 8 <= kQBytes, "the warps' maxima and sums fit where q was");
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -670,7 +665,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 
 // A page pool [num_pages * 16][8][64] as the 2-D tensor (head * 64 + d, row); a
 // box is 128 bytes (64 bf16, or 32 fp32) of the 16 rows of a page.
-int encode_pool(const void* base, int num_pages, bool bf16, CUtensorMap* map) {
+int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtensorMap* map) {
   auto enc = encoder();
   if (!enc) return ATTN_ETMA;
   const cuuint32_t ones[2] = {1, 1};
@@ -678,8 +673,8 @@ int encode_pool(const void* base, int num_pages, bool bf16, CUtensorMap* map) {
   const cuuint64_t strides[1] = {(cuuint64_t)kHKV * kD * (bf16 ? 2 : 4)};
   const cuuint32_t box[2] = {bf16 ? 64u : 32u, ATTN_PAGE};
   if (enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
-          dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+          dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return ATTN_ETMA;
   return ATTN_OK;
 }
@@ -687,11 +682,12 @@ int encode_pool(const void* base, int num_pages, bool bf16, CUtensorMap* map) {
 using Variant = TreeVariant;
 template <bool kBf16, int MT>
 Variant make_variant() {
-  return {tree_kernel<kBf16, MT>, 4 * MT, 32 * Cfg<kBf16, MT>::kWarps, Cfg<kBf16, MT>::kSmemAlloc};
+  return {tree_kernel<kBf16, MT>, 4 * MT, 32 * Cfg<kBf16, MT>::kWarps, Cfg<kBf16, MT>::kSmemAlloc,
+          Cfg<kBf16, MT>::kBlocks, false, 0};
 }
 const Variant kVariants[2][3] = {
-    {make_variant<false, 1>(), make_variant<false, 2>(), make_variant<false, 4>()},
-    {tree_tc_variant(0), tree_tc_variant(1), tree_tc_variant(2)}};
+    {make_variant<false, 1>(), tree_wide_variant(false), tree_wide_variant(false)},
+    {tree_tc_variant(true, 0), tree_tc_variant(true, 1), tree_wide_variant(true)}};
 
 int variant_of(int max_rows) { return max_rows <= 4 ? 0 : max_rows <= 8 ? 1 : 2; }
 
@@ -714,11 +710,14 @@ int tree_device(TreeDevice** out) {
     for (int t = 0; t < 2; ++t)
       for (int v = 0; v < 3; ++v) {
         const Variant& x = kVariants[t][v];
-        int per_sm = 0;
-        if (cudaFuncSetAttribute(x.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.smem) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, x.kernel, x.threads, x.smem) != cudaSuccess)
+        if (cudaFuncSetAttribute(x.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.smem) != cudaSuccess)
           return ATTN_ECUDA;
-        d.slots[t][v] = sms * (per_sm > 0 ? per_sm : 1);
+        if (x.regs) {  // a split that adds up to more than the launch has would wait forever
+          cudaFuncAttributes fa;
+          if (cudaFuncGetAttributes(&fa, x.kernel) != cudaSuccess) return ATTN_ECUDA;
+          if (fa.numRegs < x.regs) return ATTN_ELAUNCH;
+        }
+        d.slots[t][v] = sms * x.blocks;
       }
     d.ready = true;
   }
@@ -736,20 +735,20 @@ int tree_splits(bool bf16, int B, int max_rows, int max_context, int splits_hint
   const int keys = max_context + max_rows;
   int n = splits_hint < kMaxSplits ? splits_hint : kMaxSplits;
   if (n <= 0) {
-    // Segments of at least 128 keys, as many as fill the resident blocks best:
-    // blocks / (waves x slots), less 0.04 for each extra wave.
+    // The segments that take the least time: rounds of resident blocks, each as
+    // long as its tiles of 128 keys and what a block costs besides them (measured:
+    // six tiles' time), and the merge of several (three).
     const int tokens = kVariants[bf16][v].tokens, slots = d->slots[bf16][v];
     const long long units = (long long)B * kHKV * ((max_rows + tokens - 1) / tokens);
-    const int most = (keys + 127) / 128;
-    const int limit = most < kMaxSplits ? most : kMaxSplits;
-    double best = -1.0;
+    const int tiles = (keys + 127) / 128;
+    const int limit = tiles < kMaxSplits ? tiles : kMaxSplits;
+    long long best = 0;
     n = 1;
     for (int s = 1; s <= limit; ++s) {
-      const long long blocks = units * s;
-      const long long waves = (blocks + slots - 1) / slots;
-      const double score = (double)blocks / (double)(waves * slots) - 0.04 * (double)(waves - 1);
-      if (score > best + 1e-9) {
-        best = score;
+      const long long rounds = (units * s + slots - 1) / slots;
+      const long long cost = rounds * ((tiles + s - 1) / s + 6) + (s > 1 ? 3 : 0);
+      if (s == 1 || cost < best) {
+        best = cost;
         n = s;
       }
     }
@@ -770,13 +769,13 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
   if (rc != ATTN_OK) return rc;
   const bool bf16 = c.type == ATTN_BF16;
   alignas(64) CUtensorMap mk, mv;
-  if ((rc = encode_pool(c.k_pages, c.num_pages, bf16, &mk)) != ATTN_OK ||
-      (rc = encode_pool(c.v_pages, c.num_pages, bf16, &mv)) != ATTN_OK)
+  const Variant& x = kVariants[bf16][variant_of(c.max_rows)];
+  if ((rc = encode_pool(c.k_pages, c.num_pages, bf16, false, &mk)) != ATTN_OK ||
+      (rc = encode_pool(c.v_pages, c.num_pages, bf16, x.v_atom32, &mv)) != ATTN_OK)
     return rc;
-  const TreeArgs a{c.q, c.v_pages, c.table, c.ctx_lens, c.row_start, c.masks, c.out, c.splits > 1 ? c.parts : nullptr,
+  const TreeArgs a{c.q, c.k_pages, c.v_pages, c.table, c.ctx_lens, c.row_start, c.masks, c.out, c.splits > 1 ? c.parts : nullptr,
                    c.B, c.N, c.max_rows, c.max_blocks, c.num_pages, c.max_context, c.split_len, c.splits,
                    err, 2000000000ull};
-  const Variant& x = kVariants[bf16][variant_of(c.max_rows)];
   const int row_tiles = (c.max_rows + x.tokens - 1) / x.tokens;
   x.kernel<<<dim3(c.splits, kHKV * row_tiles, c.B), x.threads, x.smem, stream>>>(mk, mv, a);
   if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;

@@ -15,7 +15,7 @@ constexpr float kTreeStale = 8.f;          // log2: how far a score may pass its
 
 struct TreeArgs {
   const float* q;            // [N][32][64]
-  const void* v_pages;       // [num_pages][16][8][64]
+  const void *k_pages, *v_pages;  // [num_pages][16][8][64]
   const int* table;          // [B][max_blocks]
   const int* ctx_lens;       // [B]
   const int* row_start;      // [B + 1]
@@ -69,12 +69,75 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& t0, uint32_t&
   t2 = tc::pack_bf16_rn(rx, ry);
 }
 
-// A kernel of the family: drafted rows a block takes, threads, shared memory.
+// ---- pieces of the tcgen05 kernels
+constexpr float kUnseen = -3e38f;  // reference of a row that has seen no key: any score passes it
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// All softmax threads of the block meet; returns how many warps failed a wait,
+// and in `over` how many saw a score that moves a reference. (A hardware
+// barrier: it can hang only if a warp stays away, so none ever does. A warp
+// whose wait failed still meets, and all leave together.)
+__device__ __forceinline__ int meet(int threads, bool mine_over, bool failed, int lane, int* over) {
+  int count;
+  const int p = lane == 0 ? failed : mine_over;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, 1, %2, p;\n\t}"
+      : "=r"(count)
+      : "r"(p), "r"(threads)
+      : "memory");
+  *over = count / 31;
+  return count % 31;
+}
+__device__ __forceinline__ void meet(int threads) {
+  asm volatile("barrier.cta.sync.aligned 1, %0;" ::"r"(threads) : "memory");
+}
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+struct Wait {
+  unsigned* err;
+  unsigned long long timeout_ns;
+  volatile int* abort_flag;
+  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = tc::globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i)
+        if (tc::mbar_try_wait(bar, parity)) return true;
+      if (*abort_flag) return false;
+      if (tc::globaltimer_ns() - t0 > timeout_ns) {
+        record_error(err, kDevErrTimeout);
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(bar, parity));
+  }
+};
+
+// A kernel of the family: drafted rows a block takes, threads, shared memory,
+// resident blocks of an SM.
 struct TreeVariant {
   void (*kernel)(CUtensorMap, CUtensorMap, TreeArgs);
   int tokens, threads;
   uint32_t smem;
+  int blocks;
+  bool v_atom32;  // fp32 V in the 128-byte swizzle of 32-byte chunks
+  int regs;       // registers a thread at least at launch (what its register split adds up to)
 };
-TreeVariant tree_tc_variant(int which);  // 0, 1, 2: 4, 8, 16 drafted rows (bf16 pages)
+TreeVariant tree_tc_variant(bool bf16, int which);  // 0, 1, 2: 4, 8, 16 drafted rows a block
+TreeVariant tree_wide_variant(bool bf16);           // 32 drafted rows a block
 
 }  // namespace attn

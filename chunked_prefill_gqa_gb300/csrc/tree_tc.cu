@@ -44,21 +44,25 @@ using namespace tc;
 constexpr int kKeys = 128;                          // keys of a tile: M of S^T
 constexpr int kPages = kKeys / ATTN_PAGE;
 constexpr uint32_t kOperand = kKeys * kD * 2;       // 16 KB: a tile of K, of V, or an N atom of p
-constexpr uint32_t kStageBytes = 2 * kOperand;
 constexpr uint32_t kBox = ATTN_PAGE * 128;
-constexpr float kUnseen = -3e38f;                   // reference of a row that has seen no key
 
 constexpr int kCols = 16;                           // columns of a softmax thread
 constexpr int kFlush = 8;                           // tiles between two flushes of O
 
-template <int R>
+constexpr int kConvWarps = 8;                       // fp32 pages: load and split K and V
+constexpr int kUnits = kKeys * 8 / (32 * kConvWarps);  // (key, 8 dims) of an operand a thread splits
+
+template <bool kF32, int R>
 struct Lay {
   static constexpr int kParts = R / kCols;          // warps on one lane quarter
   static constexpr int kSoft = 4 * kParts;          // softmax warps
-  static constexpr int kTmaWarp = kSoft, kMmaWarp = kSoft + 1;
-  static constexpr int kThreads = 32 * (kSoft + 2);
-  static constexpr int kBlocks = R == 64 ? 1 : 2;   // per SM
-  static constexpr int kStages = R == 64 ? 4 : 2;
+  static constexpr int kLoadWarps = kF32 ? kConvWarps : 1;
+  static constexpr int kMmaWarp = kSoft + kLoadWarps;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr int kBlocks = kF32 || R == 64 ? 1 : 2;  // per SM
+  static constexpr int kStages = kF32 ? 1 : R == 64 ? 4 : 2;
+  static constexpr int kTerms = kF32 ? 3 : 1;       // of K and V
+  static constexpr uint32_t kStageBytes = 2 * kTerms * kOperand;     // K's terms, then V's
   static constexpr int kN = 3 * R;
   static constexpr uint32_t kColS = 0, kColO = 2 * R;                // two S buffers, then O's three terms
   static constexpr uint32_t kTmem = R == 64 ? 512 : R == 32 ? 256 : 128;
@@ -71,8 +75,8 @@ struct Lay {
   static constexpr uint32_t kSmemAcc = kSmemP + (R == 64 ? 3 : (kN + 63) / 64 - 1) * kOperand;
   static constexpr uint32_t kSmemMask = kSmemAcc + kOperand;
   static_assert(R == 64 ? R * kD * 4 == kOperand : kKeys * kFree == R * kD * 4 && (kN % 64) * 2 + kFree <= 128, "acc");
-  static constexpr uint32_t kSmemMax = kSmemMask + (R / 4) * 8;      // [4 quarters][R]
-  static constexpr uint32_t kSmemBar = kSmemMax + 4 * R * 4;
+  static constexpr uint32_t kSmemMax = kSmemMask + (R / 4) * 8;      // [4 quarters][R], then [R] for the end
+  static constexpr uint32_t kSmemBar = kSmemMax + 5 * R * 4;
   static constexpr int kNumBars = 4 * kStages + 7;
   static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2), fresh (2)
   static constexpr uint32_t kSmemAlloc = kSmemWords + 32 + 1024;
@@ -85,84 +89,30 @@ __host__ __device__ constexpr uint32_t idesc_tree(int M, int N, bool mn_major) {
   return idesc_bf16(M, N, mn_major) | (mn_major ? 1u << 15 : 0u);
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float warp_max(float x) {
   float y;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
-// All softmax threads of the block meet; returns how many warps failed a wait,
-// and in `over` how many saw a score that moves a reference. (A hardware
-// barrier: it can hang only if a warp stays away, so none ever does. A warp
-// whose wait failed still meets, and all leave together.)
-__device__ __forceinline__ int meet(int threads, bool mine_over, bool failed, int lane, int* over) {
-  int count;
-  const int p = lane == 0 ? failed : mine_over;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %1, 0;\n\tbarrier.cta.red.popc.aligned.u32 %0, 1, %2, p;\n\t}"
-      : "=r"(count)
-      : "r"(p), "r"(threads)
-      : "memory");
-  *over = count / 31;
-  return count % 31;
-}
-__device__ __forceinline__ void meet(int threads) {
-  asm volatile("barrier.cta.sync.aligned 1, %0;" ::"r"(threads) : "memory");
-}
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect() {
-  uint32_t p;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
-struct Wait {
-  unsigned* err;
-  unsigned long long timeout_ns;
-  volatile int* abort_flag;
-  __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-#pragma unroll 1
-      for (int i = 0; i < 32; ++i)
-        if (mbar_try_wait(bar, parity)) return true;
-      if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > timeout_ns) {
-        record_error(err, kDevErrTimeout);
-        *abort_flag = 1;
-        return false;
-      }
-    }
-  }
-  __device__ __forceinline__ bool warp(uint64_t* bar, uint32_t parity) const {
-    return __all_sync(0xffffffffu, (*this)(bar, parity));
-  }
-};
-
 // Where column j of dim d is kept.
-template <int R>
+template <bool kF32, int R>
 __device__ __forceinline__ float* acc_at(uint8_t* smem, int j, int d) {
-  uint8_t* const base = smem + Lay<R>::kSmemAcc;
+  uint8_t* const base = smem + Lay<kF32, R>::kSmemAcc;
   if constexpr (R == 64) {
     return reinterpret_cast<float*>(base) + j * kD + d;
   } else {
-    constexpr uint32_t kFree = Lay<R>::kFree;
+    constexpr uint32_t kFree = Lay<kF32, R>::kFree;
     const uint32_t at = (uint32_t)(j * kD + d) * 4u;
     return reinterpret_cast<float*>(base + sw128(at / kFree * 128u + 128u - kFree + at % kFree));
   }
 }
 
-template <int R>
-__global__ void __launch_bounds__(Lay<R>::kThreads, Lay<R>::kBlocks)
+template <bool kF32, int R>
+__global__ void __launch_bounds__(Lay<kF32, R>::kThreads, Lay<kF32, R>::kBlocks)
 tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
-  using L = Lay<R>;
-  constexpr int kStages = L::kStages;
+  using L = Lay<kF32, R>;
+  constexpr int kStages = L::kStages, kTerms = L::kTerms;
+  constexpr uint32_t kStageBytes = L::kStageBytes, kV = kTerms * kOperand;  // V in a stage
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -203,43 +153,112 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   unsigned long long* const masks = reinterpret_cast<unsigned long long*>(smem + L::kSmemMask);
   const Wait wait{a.err, a.timeout_ns, abort_flag};
 
-  // The TMA warp: 8 lanes load the 8 pages of a tile of K, or of V.
   const int* const trow = a.table + (size_t)b * a.max_blocks;
-  auto page_of = [&](int n) -> int {  // -1: no page there; out of range: num_pages (reads as zeros)
-    const int t = k0 + n * kKeys + lane * ATTN_PAGE;
-    if (lane >= kPages || n >= ntiles || t >= k1) return -1;
-    const int p = __ldg(trow + t / ATTN_PAGE);
-    if (p >= 0 && p < a.num_pages) return p;
-    record_error(a.err, kDevErrBounds);
-    return a.num_pages;
+
+  // ---- bf16 pages: one warp, TMA boxes of a page each; 8 lanes load the 8 pages
+  // of a tile of K, or of V. Lane l holds the table's entry of page l of a group
+  // of four tiles, for V's group and for the next.
+  int entries = -1, entries_next = -1, group = 0, ahead = 0;
+  auto entry_at = [&](int g) -> int {
+    const int t = k0 + g * 4 * kKeys + lane * ATTN_PAGE;
+    return t < k1 ? __ldg(trow + t / ATTN_PAGE) : -1;
   };
-  auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t operand, int n, int page) {
+  auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t operand, int n) {
     const int st = n % kStages;
-    const unsigned boxes = __popc(__ballot_sync(0xffffffffu, page >= 0));
+    int page = __shfl_sync(0xffffffffu, (n >> 2) == group ? entries : entries_next, (n & 3) * kPages + (lane & 7));
+    const bool has = lane < kPages && k0 + n * kKeys + lane * ATTN_PAGE < k1;
+    if (has && (page < 0 || page >= a.num_pages)) {
+      record_error(a.err, kDevErrBounds);
+      page = a.num_pages;  // past the pool's end: reads as zeros
+    }
+    const unsigned boxes = __popc(__ballot_sync(0xffffffffu, has));
     if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * kBox);
     __syncwarp();
-    if (page >= 0)
+    if (has)
       tma_load_2d(smem + st * kStageBytes + operand + lane * kBox, map, &full[st], head * kD, page * ATTN_PAGE);
   };
-  // K(n + 1) goes before V(n): its stage is free earlier.
-  int page_v = -1, page_k = -1, page_next = -1, ahead = 0;
-  auto load_next = [&]() -> bool {  // V(ahead) and K(ahead + 1)
+  auto load_next = [&]() -> bool {  // K(ahead + 1), whose stage is free earlier, then V(ahead)
     const int n = ahead;
     if (n + 1 < ntiles) {
       if (n + 1 >= kStages && !wait.warp(&kempty[(n + 1) % kStages], ((n + 1) / kStages - 1) & 1)) return false;
-      load(&mk, kfull, 0, n + 1, page_k);
+      load(&mk, kfull, 0, n + 1);
     }
     if (n >= kStages && !wait.warp(&vempty[n % kStages], (n / kStages - 1) & 1)) return false;
-    load(&mv, vfull, kOperand, n, page_v);
-    page_v = page_k;
-    page_k = page_next;
-    page_next = page_of(n + 3);
+    load(&mv, vfull, kV, n);
     ++ahead;
+    if ((ahead >> 2) != group) {
+      group = ahead >> 2;
+      entries = entries_next;
+      entries_next = entry_at(group + 1);
+    }
     return true;
   };
-  if (warp == L::kTmaWarp) {
-    if (lane == 0) {
-      for (int i = 0; i < 4 * kStages; ++i) mbar_init(&kfull[i], 1);
+
+  // ---- fp32 pages: eight warps load K and V into registers a tile ahead, split
+  // each value into three bf16 terms and write those. A thread takes 8 dims of
+  // the keys row + 32 u, so a warp's loads are four whole rows of 256 bytes from
+  // one page. Lane 4 x + u holds the table's entry of unit u of tile x of a
+  // group of eight tiles.
+  const int ctid = tid - 32 * L::kSoft, crow = (ctid >> 3) & 31, c8 = ctid & 7;
+  float4 kx[kF32 ? 2 * kUnits : 1], vx[kF32 ? 2 * kUnits : 1];
+  auto centry = [&](int g) -> int {
+    const int t = k0 + (g * 8 + (lane >> 2)) * kKeys + (crow & ~3) + 32 * (lane & 3);
+    return t < k1 ? __ldg(trow + t / ATTN_PAGE) : -1;
+  };
+  auto fetch = [&](const void* pool, int n, int tab, int tab_next, int g, float4* x) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      const int page = __shfl_sync(0xffffffffu, (n >> 3) == g ? tab : tab_next, (n & 7) * 4 + u);
+      const int t = k0 + n * kKeys + crow + 32 * u;
+      x[2 * u] = x[2 * u + 1] = make_float4(0.f, 0.f, 0.f, 0.f);  // past the last key, or a bad page
+      if (t < k1) {
+        if (page >= 0 && page < a.num_pages) {
+          const float4* src = reinterpret_cast<const float4*>(
+              static_cast<const float*>(pool) + (((size_t)page * ATTN_PAGE + t % ATTN_PAGE) * kHKV + head) * kD + c8 * 8);
+          x[2 * u] = __ldg(src);
+          x[2 * u + 1] = __ldg(src + 1);
+        } else {
+          record_error(a.err, kDevErrBounds);
+        }
+      }
+    }
+  };
+  auto split_out = [&](const float4* x, uint32_t operand, int n, bool is_v) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      float y[8] = {x[2 * u].x, x[2 * u].y, x[2 * u].z, x[2 * u].w,
+                    x[2 * u + 1].x, x[2 * u + 1].y, x[2 * u + 1].z, x[2 * u + 1].w};
+      const int key = crow + 32 * u;
+      if (is_v && k0 + (n + 1) * kKeys > seq.ctx) {
+        // no infinity or NaN of a drafted row into a product with the zero
+        // probability of a row that does not see it
+        const int at = k0 + n * kKeys + key - seq.ctx;
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (at >= 0 && (__float_as_uint(y[k]) & 0x7f800000u) == 0x7f800000u) {
+            y[k] = 0.f;
+            bad = true;
+          }
+        if (bad) atomicOr(odd + (at >> 5), 1u << (at & 31));
+      }
+      uint32_t w[3][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) split3(y[2 * k], y[2 * k + 1], w[0][k], w[1][k], w[2][k]);
+#pragma unroll
+      for (int t = 0; t < 3; ++t)
+        *reinterpret_cast<uint4*>(smem + operand + t * kOperand + sw128((uint32_t)key * 128u + c8 * 16u)) =
+            make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(is_v ? vfull : kfull);
+  };
+
+  if (warp >= L::kSoft && warp < L::kMmaWarp) {
+    if (warp == L::kSoft && lane == 0) {
+      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kfull[i], kF32 ? kConvWarps : 1);  // and vfull
+      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kempty[i], 1);                     // and vempty
       mbar_init(&sfull[0], 1);
       mbar_init(&sfull[1], 1);
       mbar_init(&sread[0], L::kSoft);
@@ -253,11 +272,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
     __syncwarp();
     // The first tiles are on their way before the block has met.
-    page_v = page_of(0);
-    page_k = page_of(1);
-    page_next = page_of(2);
-    load(&mk, kfull, 0, 0, page_v);
-    while (ahead < kStages - 1 && ahead < ntiles) load_next();
+    if constexpr (kF32) {
+      entries = centry(0);
+      entries_next = centry(1);
+      fetch(a.k_pages, 0, entries, entries_next, 0, kx);
+      fetch(a.v_pages, 0, entries, entries_next, 0, vx);
+    } else {
+      entries = entry_at(0);
+      entries_next = entry_at(1);
+      load(&mk, kfull, 0, 0);
+      while (ahead < kStages - 1 && ahead < ntiles) load_next();
+    }
   } else if (warp == L::kMmaWarp) {
     tmem_alloc(words, L::kTmem);
     tmem_relinquish();
@@ -294,19 +319,41 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = words[0];
 
-  if (warp == L::kTmaWarp) {
-    while (ahead < ntiles && load_next()) {
-    }
-    if (*abort_flag) {
-      // Copies still in flight land before the block's shared memory is
-      // released (K(ahead) and, where its wait ran out, K(ahead + 1) at most).
-      for (int i = max(0, ahead - kStages); i < min(ahead + 2, ntiles); ++i)
-        mbar_wait(&kfull[i % kStages], (i / kStages) & 1, 1000000);
-      for (int i = max(0, ahead - kStages); i < ahead; ++i) mbar_wait(&vfull[i % kStages], (i / kStages) & 1, 1000000);
+  if (warp >= L::kSoft && warp < L::kMmaWarp) {
+    if constexpr (kF32) {
+      // K(n) as soon as S(n - 1) has read the terms before it, then V(n - 1) after PV(n - 2).
+      for (int n = 0; n <= ntiles; ++n) {
+        if (n < ntiles) {
+          if (n > 0 && !wait.warp(kempty, (n - 1) & 1)) break;
+          split_out(kx, 0, n, false);
+          if (n + 1 < ntiles) fetch(a.k_pages, n + 1, entries, entries_next, group, kx);
+        }
+        if (n > 0) {
+          if (n > 1 && !wait.warp(vempty, n & 1)) break;
+          split_out(vx, kV, n - 1, true);
+          if (n < ntiles) fetch(a.v_pages, n, entries, entries_next, group, vx);
+          if ((n >> 3) != group) {  // V's next tile starts a group
+            group = n >> 3;
+            entries = entries_next;
+            entries_next = centry(group + 1);
+          }
+        }
+      }
+    } else {
+      while (ahead < ntiles && load_next()) {
+      }
+      if (*abort_flag) {
+        // Copies still in flight land before the block's shared memory is
+        // released (K up to ahead + 1, V up to ahead - 1 may have been issued).
+        for (int i = max(0, ahead - kStages); i < min(ahead + 2, ntiles); ++i)
+          mbar_wait(&kfull[i % kStages], (i / kStages) & 1, 1000000);
+        for (int i = max(0, ahead - kStages); i < ahead; ++i)
+          mbar_wait(&vfull[i % kStages], (i / kStages) & 1, 1000000);
+      }
     }
     __syncwarp();
   } else if (warp == L::kMmaWarp) {
-    constexpr uint32_t kIdS = idesc_tree(128, R, false), kIdPV = idesc_tree(64, L::kN, true);
+    constexpr uint32_t kIdS = idesc_tree(128, R, false);
     const uint32_t base = smem_u32(smem);
     const uint64_t qd = sdesc_sw128(base + L::kSmemQ), pd = sdesc_sw128_mn(base + L::kSmemP, kOperand);
     auto issue_s = [&](int n) -> bool {
@@ -317,13 +364,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       const uint64_t kd = sdesc_sw128(base + st * kStageBytes);
       const uint32_t dst = tmem + L::kColS + (n & 1) * R;
       if (elect()) {
-        // The smallest term first: only the last four accumulations are at
-        // the score's own size.
+        // Products of terms i + j <= 2, the smallest first: only the last four
+        // accumulations are at the score's own size.
 #pragma unroll
-        for (int t = 2; t >= 0; --t)
+        for (int order = 2; order >= 0; --order)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            mma_f16_ss(dst, kd + x * 2, qd + t * (R * 8) + x * 2, kIdS, t < 2 || x > 0);
+          for (int kt = 0; kt < kTerms; ++kt)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (kt <= order)
+                mma_f16_ss(dst, kd + kt * (kOperand >> 4) + x * 2, qd + (order - kt) * (R * 8) + x * 2, kIdS,
+                           order < 2 || kt > 0 || x > 0);
         mma_commit(&sfull[n & 1]);
         mma_commit(&kempty[st]);
       }
@@ -336,12 +387,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       const int st = n % kStages;
       if (!(ok = wait.warp(pfull, n & 1) && wait.warp(&vfull[st], (n / kStages) & 1))) break;
       tc_fence_after();
-      const uint64_t vd = sdesc_sw128_mn(base + st * kStageBytes + kOperand);
+      const uint64_t vd = sdesc_sw128_mn(base + st * kStageBytes + kV);
       const uint32_t old = n > 0 && !fresh[n & 1];
       if (elect()) {
+        // V's term t takes the 3 - t largest terms of p, into their columns.
 #pragma unroll
-        for (int x = 0; x < 8; ++x)  // 16 keys a step: 2048 bytes of rows
-          mma_f16_ss(tmem + L::kColO, vd + x * 128, pd + x * 128, kIdPV, x > 0 ? 1u : old);
+        for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+          for (int x = 0; x < 8; ++x)  // 16 keys a step: 2048 bytes of rows
+            mma_f16_ss(tmem + L::kColO, vd + t * (kOperand >> 4) + x * 128, pd + x * 128,
+                       idesc_tree(64, L::kN - t * R, true), t > 0 || x > 0 ? 1u : old);
         mma_commit(&vempty[st]);
         mma_commit(odone);
       }
@@ -408,23 +463,25 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 #pragma unroll
             for (int i = 0; i < kCols / 4; ++i)
               if (!(masks[col0 / 4 + i] >> at & 1)) hidden |= 15u << (4 * i);
-          // The value row of this key: zeros past the last key (its slot may hold
-          // anything), and no infinity or NaN of a drafted row into a product
-          // with the zero probability of a row that does not see it.
-          if (!wait(&vfull[n % kStages], (n / kStages) & 1)) failed = true;
-          uint8_t* v = smem + (n % kStages) * kStageBytes + kOperand;
-          for (int c8 = part; c8 < 8; c8 += L::kParts) {
-            uint4* p = reinterpret_cast<uint4*>(v + sw128((uint32_t)key * 128u + c8 * 16u));
-            uint4 u = past ? make_uint4(0, 0, 0, 0) : *p;
-            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
-            bool bad = past;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, bad = true;
-              if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu, bad = true;
+          if constexpr (!kF32) {
+            // The value row of this key: zeros past the last key (its slot may hold
+            // anything), and no infinity or NaN of a drafted row into a product
+            // with the zero probability of a row that does not see it.
+            if (!wait(&vfull[n % kStages], (n / kStages) & 1)) failed = true;
+            uint8_t* v = smem + (n % kStages) * kStageBytes + kV;
+            for (int c8 = part; c8 < 8; c8 += L::kParts) {
+              uint4* p = reinterpret_cast<uint4*>(v + sw128((uint32_t)key * 128u + c8 * 16u));
+              uint4 u = past ? make_uint4(0, 0, 0, 0) : *p;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+              bool bad = past;
+  #pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((w[k] & 0x7f80u) == 0x7f80u) w[k] &= 0xffff0000u, bad = true;
+                if ((w[k] & 0x7f800000u) == 0x7f800000u) w[k] &= 0xffffu, bad = true;
+              }
+              if (bad) *p = u;
+              if (bad && !past) atomicOr(odd + (at >> 5), 1u << (at & 31));
             }
-            if (bad) *p = u;
-            if (bad && !past) atomicOr(odd + (at >> 5), 1u << (at & 31));
           }
         }
         failed = __any_sync(0xffffffffu, failed);
@@ -496,7 +553,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             if (kept && lane < 16) {
               float old[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) old[j] = *acc_at<R>(smem, col0 + h + j, d);
+              for (int j = 0; j < 8; ++j) old[j] = *acc_at<kF32, R>(smem, col0 + h + j, d);
 #pragma unroll
               for (int j = 0; j < 8; ++j) o[j] += old[j];
             }
@@ -506,7 +563,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             }
             if (lane < 16) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) *acc_at<R>(smem, col0 + h + j, d) = o[j];
+              for (int j = 0; j < 8; ++j) *acc_at<kF32, R>(smem, col0 + h + j, d) = o[j];
             }
           }
           kept = true;
@@ -531,28 +588,29 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     // ------------------------------------------------------------ epilogue
     if (!failed) failed = !wait.warp(odone, (ntiles - 1) & 1);
     {
-      float l = 0.f;  // lanes j and 16 + j: the sum of column col0 + j
+      // Sums over the warp's keys: halving the columns a lane holds each round,
+      // lanes j and 16 + j end with column col0 + j.
 #pragma unroll
-      for (int j = 0; j < kCols; ++j) {
-        float v = sum[j];
+      for (int w = 8; w >= 1; w >>= 1)
 #pragma unroll
-        for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-        if ((lane & 15) == j) l = v;
-      }
+        for (int j = 0; j < w; ++j) {
+          const bool up = lane & w;
+          const float give = up ? sum[j] : sum[j + w], keep = up ? sum[j + w] : sum[j];
+          sum[j] = keep + __shfl_xor_sync(0xffffffffu, give, w);
+        }
+      const float l = sum[0] + __shfl_xor_sync(0xffffffffu, sum[0], 16);
       const int c = col0 + (lane & 15);
       int over;
       // The maxima of the last tile may still be read: meet before they become sums.
       if (meet(kMeet, false, failed, lane, &over)) goto done;
       if (lane < kCols) maxima[quarter * R + c] = l;
-      meet(kMeet);
-      l = (maxima[c] + maxima[R + c]) + (maxima[2 * R + c] + maxima[3 * R + c]);
       tc_fence_after();
       float o[kCols];
 #pragma unroll
       for (int h = 0; h < kCols; h += 8) read_o(h, reinterpret_cast<float (&)[8]>(o[h]));
       if (kept && lane < 16) {
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) o[j] += *acc_at<R>(smem, col0 + j, d);
+        for (int j = 0; j < kCols; ++j) o[j] += *acc_at<kF32, R>(smem, col0 + j, d);
       }
       unsigned long long rest = ((unsigned long long)odd[1] << 32) | odd[0];
       while (rest) {  // drafted values that are not finite reach the rows that see them
@@ -560,33 +618,43 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         rest &= rest - 1;
         const int page = __ldg(trow + (seq.ctx + j0) / ATTN_PAGE);
         if (lane < 16 && page >= 0 && page < a.num_pages) {
-          const uint16_t raw = __ldg(static_cast<const uint16_t*>(a.v_pages) +
-                                     (((size_t)page * ATTN_PAGE + (seq.ctx + j0) % ATTN_PAGE) * kHKV + head) * kD + d);
-          if ((raw & 0x7f80u) == 0x7f80u)
+          const size_t at = (((size_t)page * ATTN_PAGE + (seq.ctx + j0) % ATTN_PAGE) * kHKV + head) * kD + d;
+          const float v = kF32 ? __ldg(static_cast<const float*>(a.v_pages) + at)
+                               : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.v_pages) + at) << 16);
+          if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u)
 #pragma unroll
             for (int j = 0; j < kCols; ++j)
-              if (masks[(col0 + j) >> 2] >> j0 & 1) o[j] += __uint_as_float((uint32_t)raw << 16);
+              if (masks[(col0 + j) >> 2] >> j0 & 1) o[j] += v;
         }
       }
+      // Rows to shared memory, so that they leave in 16-byte pieces. (p's atoms
+      // are free, and so is what the tiles occupied.)
+      float* const rows = reinterpret_cast<float*>(smem);  // [R][68]
+      if (lane < 16) {
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) rows[(col0 + j) * 68 + d] = o[j];
+      }
+      if (quarter == 0 && lane < kCols) maxima[4 * R + c] = ref;
+      meet(kMeet);
       const size_t at0 = (size_t)(seq.first + i0) * kHQ + head * kGroup;  // row r: + (r / 4) * 32 + r % 4
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: zeros
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          const float f = __shfl_sync(0xffffffffu, inv, j);
-          const int r = col0 + j;
-          if (lane < 16 && (r >> 2) < nrows) a.out[(at0 + (r >> 2) * kHQ + (r & 3)) * kD + d] = o[j] * f;
+      float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+#pragma unroll 1
+      for (int e = tid; e < nrows * kGroup * 16; e += kMeet) {  // (row, 4 dims)
+        const int r = e >> 4, d4 = (e & 15) * 4;
+        const float sl = (maxima[r] + maxima[R + r]) + (maxima[2 * R + r] + maxima[3 * R + r]);
+        float4 y = *reinterpret_cast<const float4*>(rows + r * 68 + d4);
+        const size_t at = at0 + (r >> 2) * kHQ + (r & 3);
+        if (whole) {
+          const float inv = sl == 0.f ? 0.f : 1.f / sl;  // no key: zeros
+          y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+          *reinterpret_cast<float4*>(a.out + at * kD + d4) = y;
+        } else {
+          *reinterpret_cast<float4*>(a.parts + (at * a.splits + s) * kD + d4) = y;
+          if (d4 == 0) {
+            const float m = maxima[4 * R + r];
+            mls[at * a.splits + s] = make_float2(m == kUnseen ? -INFINITY : m, sl);
+          }
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          const int r = col0 + j;
-          if (lane < 16 && (r >> 2) < nrows)
-            a.parts[((at0 + (r >> 2) * kHQ + (r & 3)) * a.splits + s) * kD + d] = o[j];
-        }
-        float2* mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
-        if (quarter == 0 && lane < kCols && (c >> 2) < nrows)
-          mls[(at0 + (c >> 2) * kHQ + (c & 3)) * a.splits + s] = make_float2(ref == kUnseen ? -INFINITY : ref, l);
       }
     }
   done:;
@@ -608,12 +676,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 
 }  // namespace
 
-TreeVariant tree_tc_variant(int which) {
-  switch (which) {
-    case 0: return {tree_tc_kernel<16>, 4, Lay<16>::kThreads, Lay<16>::kSmemAlloc};
-    case 1: return {tree_tc_kernel<32>, 8, Lay<32>::kThreads, Lay<32>::kSmemAlloc};
-    default: return {tree_tc_kernel<64>, 16, Lay<64>::kThreads, Lay<64>::kSmemAlloc};
-  }
+template <bool kF32, int R>
+TreeVariant variant() {
+  using L = Lay<kF32, R>;
+  return {tree_tc_kernel<kF32, R>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0};
+}
+
+TreeVariant tree_tc_variant(bool bf16, int which) {
+  if (!bf16) return which == 0 ? variant<true, 16>() : variant<true, 32>();
+  return which == 0 ? variant<false, 16>() : which == 1 ? variant<false, 32>() : variant<false, 64>();
 }
 
 }  // namespace attn

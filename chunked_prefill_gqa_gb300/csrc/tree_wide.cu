@@ -1,0 +1,599 @@
+// tree_wide.cu -- the drafted-tree attention of tree.cu for wide trees, on the
+// tcgen05 tensor cores with the query rows on the M side: 32 drafted rows x the
+// 4 query heads of a KV head fill the 128 lanes of tensor memory, a thread owns
+// one row, and nothing of the softmax crosses threads.
+//
+// Tiles of 64 keys go in turn to two softmax groups of four warps (tile n to
+// group n % 2), each with its own S, p and O in tensor memory and its own
+// reference maximum, sum and accumulator, so one group's softmax runs under the
+// other's products; the two partials merge at the end like two segments. The
+// tensor core's accumulation does not round to nearest: O of a tile starts at
+// zero, and the row's thread adds it to fp32 registers, rounded to nearest. A
+// reference that moves therefore costs a product in registers and no trip to
+// tensor memory.
+//
+//   bf16 pages (K and V as stored, q and p in three bf16 terms):
+//     S  = (q3, q2, q1) K^T        3 x 4 MMAs of 128 x 64 x 16
+//     O  = (p3, p2, p1) V          3 x 4 MMAs of 128 x 64 x 16
+//   fp32 pages (x = hi + lo, hi what the tensor core reads of x as tf32; four
+//   converter warps write K lo and V lo next to each landed tile):
+//     S  = q_lo K + q_hi K_lo + q_hi K       3 x 8 MMAs of 128 x 64 x 8
+//     O  = p_lo V + p_hi V_lo + p_hi V       3 x 8 MMAs of 128 x 64 x 8
+// q and p are tensor-memory operands (p overwrites the S it came from), K a
+// K-major and V an MN-major shared-memory operand as TMA lays them down.
+//
+// Roles: warps 0-3 and 4-7 softmax; (fp32) 8-11 converters; one warp for TMA
+// (16-token pages through the block table); one for the MMAs.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+#include "tree.cuh"
+
+namespace attn {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 32;                  // drafted rows of a block
+constexpr int kKeys = 64;                  // keys of a tile
+constexpr int kPages = kKeys / ATTN_PAGE;
+constexpr int kSoft = 8;                   // softmax warps, two groups of four
+constexpr uint32_t kHalf = kKeys * 128;    // 64 rows of 128 bytes
+
+template <bool kF32>
+struct Wide {
+  static constexpr int kConvWarp = kSoft, kConvWarps = kF32 ? 4 : 0;
+  static constexpr int kTmaWarp = kSoft + kConvWarps, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = kF32 ? 512 : 32 * (kMmaWarp + 1);  // fp32: whole warpgroups, for the register split
+  static constexpr uint32_t kOperand = kF32 ? 2 * kHalf : kHalf;     // a tile of K or V as stored
+  static constexpr uint32_t kStageBytes = (kF32 ? 4 : 2) * kOperand; // K (K lo) V (V lo)
+  static constexpr uint32_t kV = (kF32 ? 2 : 1) * kOperand;
+  static constexpr int kStages = kF32 ? 3 : 8;
+  // Tensor memory: q's terms, then per group S (p overwrites it) and the rest of
+  // p, then the groups' O.
+  static constexpr uint32_t kColQ = 0, kColS = kF32 ? 128 : 96, kGroupCols = kF32 ? 128 : 96;
+  static constexpr uint32_t kColO = kColS + 2 * kGroupCols;
+  static constexpr uint32_t kSmemMask = kStages * kStageBytes;
+  static constexpr uint32_t kSmemMl = kSmemMask + kRows * 8;         // [2 groups][128 rows] (reference, sum)
+  static constexpr uint32_t kSmemBar = kSmemMl + 2 * 128 * 8;
+  static constexpr int kNumBars = 6 * kStages + 6 + 2;
+  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2)
+  static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
+  static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
+  static_assert(kColO + 2 * kD <= 512, "TMEM layout");
+  static_assert(2 * 128 * 32 * 4 <= kStages * kStageBytes, "the groups' exchange fits the ring");
+};
+
+template <bool kF32>
+__global__ void __launch_bounds__(Wide<kF32>::kThreads, 1)
+tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
+  using L = Wide<kF32>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
+
+  const Seq seq = load_seq(a, b);
+  const int i0 = rt * kRows;  // the block's first drafted row
+  const int nrows = min(kRows, seq.rows - i0);
+  const int k0 = s * a.split_len;
+  const int k1 = min(k0 + a.split_len, seq.keys);
+  if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+  if (nrows <= 0) return;
+  if (k0 >= k1) {
+    // Past the sequence: the merge counts its segments from the lengths. A
+    // sequence without any key (only a refused one) gets zeros.
+    if (s == 0)
+      for (int e = tid; e < nrows * kGroup * kD; e += L::kThreads)
+        a.out[((size_t)(seq.first + i0 + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
+    return;
+  }
+  const bool whole = seq.keys <= a.split_len;  // one segment: the output is written here
+  const int ntiles = (k1 - k0 + kKeys - 1) / kKeys;
+  const int quarters = (nrows * kGroup + 31) / 32;  // lane quarters that hold rows
+
+  uint64_t* const kfull = reinterpret_cast<uint64_t*>(smem + L::kSmemBar);  // [stage] K landed
+  uint64_t* const vfull = kfull + kStages;                                  // [stage] V landed
+  uint64_t* const kready = vfull + kStages;                                 // [stage] K lo written (fp32)
+  uint64_t* const vready = kready + kStages;                                // [stage] V lo written (fp32)
+  uint64_t* const kempty = vready + kStages;                                // [stage] S done with K
+  uint64_t* const vempty = kempty + kStages;                                // [stage] PV done with V
+  uint64_t* const sfull = vempty + kStages;                                 // [group] S written
+  uint64_t* const pfull = sfull + 2;                                        // [group] p written, O read
+  uint64_t* const odone = pfull + 2;                                        // [group] PV complete
+  uint64_t* const qready = odone + 2;                                       // q's terms in tensor memory
+  uint64_t* const drain = qready + 1;                                       // MMAs in flight on abort
+  uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
+  uint32_t* const odd = words + 2;  // [2] drafted rows whose value is not finite
+  unsigned long long* const masks = reinterpret_cast<unsigned long long*>(smem + L::kSmemMask);
+  const Wait wait{a.err, a.timeout_ns, abort_flag};
+
+  // The TMA warp: lanes load the boxes of a tile of K, or of V: four pages, for
+  // fp32 in two halves of 32 dims. Lane l holds the table's entry of page l of a
+  // group of eight tiles, for V's group and for the next.
+  const int* const trow = a.table + (size_t)b * a.max_blocks;
+  int entries = -1, entries_next = -1, group8 = 0, ahead = 0;
+  auto entry_at = [&](int g) -> int {
+    const int t = k0 + g * 8 * kKeys + lane * ATTN_PAGE;
+    return t < k1 ? __ldg(trow + t / ATTN_PAGE) : -1;
+  };
+  auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t operand, int n) {
+    const int st = n % kStages, p = lane & (kPages - 1), half = lane / kPages;
+    int page = __shfl_sync(0xffffffffu, (n >> 3) == group8 ? entries : entries_next, (n & 7) * kPages + p);
+    const bool has = lane < (kF32 ? 2 : 1) * kPages && k0 + n * kKeys + p * ATTN_PAGE < k1;
+    if (has && (page < 0 || page >= a.num_pages)) {
+      record_error(a.err, kDevErrBounds);
+      page = a.num_pages;  // past the pool's end: reads as zeros
+    }
+    const unsigned boxes = __popc(__ballot_sync(0xffffffffu, has));
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * (ATTN_PAGE * 128));
+    __syncwarp();
+    if (has)
+      tma_load_2d(smem + st * L::kStageBytes + operand + half * kHalf + p * (ATTN_PAGE * 128), map, &full[st],
+                  head * kD + half * 32, page * ATTN_PAGE);
+  };
+  auto load_next = [&]() -> bool {  // K(ahead + 1), whose stage is free earlier, then V(ahead)
+    const int n = ahead;
+    if (n + 1 < ntiles) {
+      if (n + 1 >= kStages && !wait.warp(&kempty[(n + 1) % kStages], ((n + 1) / kStages - 1) & 1)) return false;
+      load(&mk, kfull, 0, n + 1);
+    }
+    if (n >= kStages && !wait.warp(&vempty[n % kStages], (n / kStages - 1) & 1)) return false;
+    load(&mv, vfull, L::kV, n);
+    ++ahead;
+    if ((ahead >> 3) != group8) {
+      group8 = ahead >> 3;
+      entries = entries_next;
+      entries_next = entry_at(group8 + 1);
+    }
+    return true;
+  };
+
+  if (warp == L::kTmaWarp) {
+    if (lane == 0) {
+      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kfull[i], 1);               // and vfull
+      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kready[i], L::kConvWarps + !kF32);  // and vready
+      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kempty[i], 1);              // and vempty
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sfull[i], 1);
+        mbar_init(&pfull[i], quarters);
+        mbar_init(&odone[i], 1);
+      }
+      mbar_init(qready, 2 * quarters);
+      mbar_init(drain, 1);
+      fence_mbar_init();
+      *abort_flag = 0;
+      odd[0] = odd[1] = 0;
+    }
+    __syncwarp();
+    // The first tiles are on their way before the block has met.
+    entries = entry_at(0);
+    entries_next = entry_at(1);
+    load(&mk, kfull, 0, 0);
+    while (ahead < kStages - 1 && ahead < ntiles) load_next();
+  } else if (warp == L::kMmaWarp) {
+    tmem_alloc(words, 512);
+    tmem_relinquish();
+  } else if (tid < kRows) {
+    const int rows_left = seq.rows;  // bits past the sequence's rows see nothing
+    unsigned long long m = 0;
+    if (tid < nrows)
+      m = (a.masks ? (unsigned long long)__ldg(a.masks + seq.first + i0 + tid) : ~0ull >> (63 - (i0 + tid))) &
+          (~0ull >> (64 - rows_left));
+    masks[tid] = m;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = words[0];
+
+  if (warp >= kSoft) {
+    // fp32: the loaders give registers to the softmax warps (launched with 128
+    // each: 8 warps x 168 + 4 x 88 + 4 x 80 = 16 x 126).
+    if constexpr (kF32) {
+      if (warp < L::kTmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    }
+    if (warp == L::kTmaWarp) {
+      while (ahead < ntiles && load_next()) {
+      }
+      if (*abort_flag) {
+        // Copies still in flight land before the block's shared memory is
+        // released (K up to ahead + 1, V up to ahead - 1 may have been issued).
+        for (int i = max(0, ahead - kStages); i < min(ahead + 2, ntiles); ++i)
+          mbar_wait(&kfull[i % kStages], (i / kStages) & 1, 1000000);
+        for (int i = max(0, ahead - kStages); i < ahead; ++i)
+          mbar_wait(&vfull[i % kStages], (i / kStages) & 1, 1000000);
+      }
+    } else if (warp == L::kMmaWarp) {
+      const uint32_t base = smem_u32(smem);
+      uint64_t* const kgo = kF32 ? kready : kfull;
+      uint64_t* const vgo = kF32 ? vready : vfull;
+      auto issue_s = [&](int n) -> bool {
+        const int st = n % kStages, g = n & 1;
+        if (!wait.warp(&kgo[st], (n / kStages) & 1)) return false;
+        tc_fence_after();
+        const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes);
+        const uint32_t d = tmem + L::kColS + g * L::kGroupCols, q = tmem + L::kColQ;
+        if (elect()) {
+          if constexpr (kF32) {
+            constexpr uint32_t id = idesc_tf32(128, kKeys);
+            constexpr uint64_t lo = L::kOperand >> 4;
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              mma_tf32_ts(d, q + 64 + x * 8, kd + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, x > 0);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              mma_tf32_ts(d, q + x * 8, kd + lo + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, 1);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              mma_tf32_ts(d, q + x * 8, kd + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, 1);
+          } else {
+            constexpr uint32_t id = idesc_bf16(128, kKeys, false);
+#pragma unroll
+            for (int t = 2; t >= 0; --t)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + t * 32 + x * 8, kd + x * 2, id, t < 2 || x > 0);
+          }
+          mma_commit(&sfull[g]);
+          mma_commit(&kempty[st]);
+        }
+        __syncwarp();
+        return true;
+      };
+      bool ok = wait.warp(qready, 0);
+      tc_fence_after();
+      ok = ok && issue_s(0) && (ntiles < 2 || issue_s(1));
+      for (int n = 0; ok && n < ntiles; ++n) {
+        const int st = n % kStages, g = n & 1;
+        if (!(ok = wait.warp(&pfull[g], (n >> 1) & 1) && wait.warp(&vgo[st], (n / kStages) & 1))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + L::kColO + g * kD, p = tmem + L::kColS + g * L::kGroupCols;
+        const uint32_t vb = base + st * L::kStageBytes + L::kV;
+        if (elect()) {
+          if constexpr (kF32) {
+            constexpr uint32_t id = idesc_tf32(128, kD, true);
+            const uint64_t vd = sdesc_sw128a32_mn(vb, kHalf);
+            constexpr uint64_t lo = L::kOperand >> 4;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + 64 + x * 8, vd + x * 64, id, x > 0);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + x * 8, vd + lo + x * 64, id, 1);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + x * 8, vd + x * 64, id, 1);
+          } else {
+            constexpr uint32_t id = idesc_bf16(128, kD, true);
+            const uint64_t vd = sdesc_sw128_mn(vb);
+#pragma unroll
+            for (int t = 2; t >= 0; --t)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mma_f16_ts(d, p + t * 32 + x * 8, vd + x * 128, id, t < 2 || x > 0);
+          }
+          mma_commit(&vempty[st]);
+          mma_commit(&odone[g]);
+        }
+        __syncwarp();
+        // S(n + 2) overwrites what PV(n) reads: MMAs of one thread run in order.
+        if (n + 2 < ntiles) ok = issue_s(n + 2);
+      }
+      if (*abort_flag) {
+        if (elect()) {
+          mma_commit(drain);
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < a.timeout_ns) {
+          }
+        }
+      }
+    } else if (kF32 && warp < L::kTmaWarp) {
+      // x lo = x - hi(x), element by element at the same offset of the next region.
+      const int ctid = tid - 32 * L::kConvWarp;
+      auto low = [](float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffffe000u); };
+      for (int n = 0; n < ntiles; ++n) {
+        const int st = n % kStages;
+        uint8_t* const stage = smem + st * L::kStageBytes;
+        if (!wait.warp(&kfull[st], (n / kStages) & 1)) break;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(stage + (ctid + (4 * h + i) * 128) * 16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(stage + L::kOperand + (ctid + (4 * h + i) * 128) * 16) =
+                make_float4(low(x[i].x), low(x[i].y), low(x[i].z), low(x[i].w));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kready[st]);
+        if (!wait.warp(&vfull[st], (n / kStages) & 1)) break;
+        const bool tail = k0 + (n + 1) * kKeys > seq.ctx;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            x[i] = *reinterpret_cast<const float4*>(stage + L::kV + (ctid + (4 * h + i) * 128) * 16);
+          if (tail) {
+            // Slots past the last key count as zeros, and no infinity or NaN of
+            // a drafted row meets the zero probability of a row that does not
+            // see it.
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int unit = ctid + (4 * h + i) * 128, pos = k0 + n * kKeys + ((unit >> 3) & (kKeys - 1));
+              const int at = pos - seq.ctx;
+              float* y = reinterpret_cast<float*>(&x[i]);
+              bool bad = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (pos >= k1 || (at >= 0 && (__float_as_uint(y[k]) & 0x7f800000u) == 0x7f800000u)) {
+                  y[k] = 0.f;
+                  bad = true;
+                }
+              if (bad) {
+                *reinterpret_cast<float4*>(stage + L::kV + unit * 16) = x[i];
+                if (pos < k1) atomicOr(odd + (at >> 5), 1u << (at & 31));
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(stage + L::kV + L::kOperand + (ctid + (4 * h + i) * 128) * 16) =
+                make_float4(low(x[i].x), low(x[i].y), low(x[i].z), low(x[i].w));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&vready[st]);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    if constexpr (kF32) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    constexpr int kMeet = 32 * kSoft;
+    const int quarter = warp & 3, g = warp >> 2;
+    const int row = quarter * 32 + lane;
+    const bool active = quarter < quarters;
+    const uint32_t lane_tmem = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_tmem = lane_tmem + L::kColS + g * L::kGroupCols, o_tmem = lane_tmem + L::kColO + g * kD;
+    float ref = kUnseen, l0 = 0.f, l1 = 0.f;
+    float o[kD];
+#pragma unroll
+    for (int i = 0; i < kD; ++i) o[i] = 0.f;
+    bool failed = false;
+
+    if (active) {
+      {  // this thread's 32 dims (32 g ..) of its row of q, in its terms
+        const int i = row >> 2;
+        const float* src = a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (row & 3)) * kD + g * 32;
+        float x[32];
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < nrows) v = __ldg(reinterpret_cast<const float4*>(src + k));
+          x[k] = v.x, x[k + 1] = v.y, x[k + 2] = v.z, x[k + 3] = v.w;
+        }
+        if constexpr (kF32) {
+          float hi[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            hi[k] = __uint_as_float((__float_as_uint(x[k]) + 0x1000u) & 0xffffe000u);  // to nearest
+            x[k] -= hi[k];
+          }
+          tmem_st32(lane_tmem + L::kColQ + g * 32, hi);
+          tmem_st32(lane_tmem + L::kColQ + 64 + g * 32, x);
+        } else {
+          uint32_t w[3][16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) split3(x[2 * k], x[2 * k + 1], w[0][k], w[1][k], w[2][k]);
+#pragma unroll
+          for (int t = 0; t < 3; ++t) tmem_st16(lane_tmem + L::kColQ + t * 32 + g * 16, w[t]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qready);
+      }
+      const unsigned long long mask = masks[row >> 2];
+
+      // O of the group's previous tile, once it is complete, joins the row's sums.
+      auto add_o = [&](int k) {
+        failed |= !wait.warp(&odone[g], k & 1);
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < kD; h += 32) {
+          float t[32];
+          tmem_ld32(o_tmem + h, t);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) add2(o[h + i], o[h + i + 1], o[h + i], o[h + i + 1], t[i], t[i + 1]);
+        }
+      };
+
+      int k = 0;  // the group's k-th tile
+      for (int n = g; n < ntiles; n += 2, ++k) {
+        failed |= !wait.warp(&sfull[g], k & 1);
+        tc_fence_after();
+        float x[kKeys];
+        tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(&x[0]));
+        tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
+        tmem_wait_ld();
+        const int t0 = k0 + n * kKeys;
+        if (t0 + kKeys > seq.ctx) {  // drafted keys, or slots past the last
+          const int at = t0 - seq.ctx;
+          unsigned long long see = at >= 0 ? mask >> at : -at >= 64 ? ~0ull : (mask << -at) | (~0ull >> (64 + at));
+          if (k1 - t0 < kKeys) see &= ~0ull >> (64 - (k1 - t0));
+#pragma unroll
+          for (int i = 0; i < kKeys; ++i)
+            if (!(see >> i & 1)) x[i] = -INFINITY;
+          if constexpr (!kF32) {
+            // The tile's value rows: zeros past the last key, and no infinity or
+            // NaN of a drafted row into a product with the zero probability of a
+            // row that does not see it. The group's threads share the rows.
+            failed |= !wait.warp(&vfull[n % kStages], (n / kStages) & 1);
+            uint8_t* v = smem + (n % kStages) * L::kStageBytes + L::kV;
+            for (int e = row; e < kKeys * 8; e += 32 * quarters) {
+              const int key = e >> 3, pos = t0 + key;
+              if (pos < seq.ctx) continue;
+              uint4* p = reinterpret_cast<uint4*>(v + sw128((uint32_t)key * 128u + (e & 7) * 16u));
+              uint4 u = pos >= k1 ? make_uint4(0, 0, 0, 0) : *p;
+              uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+              bool bad = pos >= k1;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if ((w[j] & 0x7f80u) == 0x7f80u) w[j] &= 0xffff0000u, bad = true;
+                if ((w[j] & 0x7f800000u) == 0x7f800000u) w[j] &= 0xffffu, bad = true;
+              }
+              if (bad) *p = u;
+              if (bad && pos < k1) atomicOr(odd + ((pos - seq.ctx) >> 5), 1u << ((pos - seq.ctx) & 31));
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        // The row's reference moves when a score passes it by 2^8.
+        float most = max3(x[0], x[1], x[2]);
+#pragma unroll
+        for (int i = 3; i < 63; i += 2) most = max3(most, x[i], x[i + 1]);
+        most = fmaxf(most, x[63]) * kTreeC;
+        float alpha = 1.f;
+        if (most > ref + kTreeStale) {
+          alpha = ex2(ref - most);
+          ref = most;
+        }
+        l0 *= alpha;
+        l1 *= alpha;
+        if (k > 0) {  // PV of the group's previous tile has read p, and its O is complete
+          failed |= !wait.warp(&odone[g], (k - 1) & 1);
+        }
+        const float neg = -ref;
+#pragma unroll
+        for (int h = 0; h < kKeys; h += 32) {
+          float* const y = x + h;
+          if constexpr (kF32) {
+            float lo[32];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              fma2(y[i], y[i + 1], y[i], y[i + 1], kTreeC, kTreeC, neg, neg);
+              y[i] = ex2(y[i]);
+              y[i + 1] = ex2(y[i + 1]);
+              add2(l0, l1, l0, l1, y[i], y[i + 1]);
+              // p hi is what the tensor core reads of p
+              fma2(lo[i], lo[i + 1], tf32_hi(y[i]), tf32_hi(y[i + 1]), -1.f, -1.f, y[i], y[i + 1]);
+            }
+            tmem_st32(s_tmem + h, *reinterpret_cast<float(*)[32]>(y));
+            tmem_st32(s_tmem + 64 + h, lo);
+          } else {
+            uint32_t w[3][16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              fma2(y[i], y[i + 1], y[i], y[i + 1], kTreeC, kTreeC, neg, neg);
+              y[i] = ex2(y[i]);
+              y[i + 1] = ex2(y[i + 1]);
+              add2(l0, l1, l0, l1, y[i], y[i + 1]);
+              split3(y[i], y[i + 1], w[0][i / 2], w[1][i / 2], w[2][i / 2]);
+            }
+#pragma unroll
+            for (int t = 0; t < 3; ++t) tmem_st16(s_tmem + t * 32 + h / 2, w[t]);
+          }
+        }
+        if (k > 0) add_o(k - 1);
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+          for (int i = 0; i < kD; ++i) o[i] *= alpha;
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[g]);
+      }
+      if (k > 0) add_o(k - 1);
+    }
+
+    // ------------------------------------------------------------ epilogue
+    // The groups exchange halves of their rows (dims 32 (1 - g) .. of this
+    // thread's) through the ring, which is idle once both have seen their last
+    // O, and each writes its half.
+    {
+      float l = l0 + l1;
+      int over;
+      if (meet(kMeet, false, failed, lane, &over)) goto done;
+      unsigned long long rest = ((unsigned long long)odd[1] << 32) | odd[0];
+      const unsigned long long mask = masks[row >> 2];
+      while (rest && g == 0) {  // drafted values that are not finite reach the rows that see them
+        const int j0 = __ffsll((long long)rest) - 1;
+        rest &= rest - 1;
+        const int page = __ldg(trow + (seq.ctx + j0) / ATTN_PAGE);
+        if (!(mask >> j0 & 1) || page < 0 || page >= a.num_pages) continue;
+        const size_t at = (((size_t)page * ATTN_PAGE + (seq.ctx + j0) % ATTN_PAGE) * kHKV + head) * kD;
+#pragma unroll
+        for (int i = 0; i < kD; ++i) {
+          const float v = kF32 ? __ldg(static_cast<const float*>(a.v_pages) + at + i)
+                               : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.v_pages) + at + i) << 16);
+          if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) o[i] += v;
+        }
+      }
+      float2* const ml = reinterpret_cast<float2*>(smem + L::kSmemMl);
+      uint8_t* const give = smem + ((1 - g) * 128 + row) * 128, * const take = smem + (g * 128 + row) * 128;
+      ml[g * 128 + row] = make_float2(ref, l);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = 4 * i;  // the other group's half
+        *reinterpret_cast<float4*>(give + ((i ^ (row & 7)) << 4)) =
+            g == 0 ? make_float4(o[32 + d], o[33 + d], o[34 + d], o[35 + d]) : make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+      }
+      meet(kMeet);
+      const float2 other = ml[(1 - g) * 128 + row];
+      const float m = fmaxf(ref, other.x);
+      const float w0 = ex2(ref - m), w1 = ex2(other.x - m);  // an unseen group's sums are zeros
+      l = fmaf(w0, l, w1 * other.y);
+      const bool mine = active && (row >> 2) < nrows;
+      const size_t at = (size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3);
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;  // no key: zeros
+      float* const dst = (whole ? a.out + at * kD : a.parts + (at * a.splits + s) * kD) + g * 32;
+      if (mine) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 y = *reinterpret_cast<const float4*>(take + ((i ^ (row & 7)) << 4));
+          const int d = 4 * i;
+          const float a0 = g ? o[32 + d] : o[d], a1 = g ? o[33 + d] : o[d + 1], a2 = g ? o[34 + d] : o[d + 2],
+                      a3 = g ? o[35 + d] : o[d + 3];
+          *reinterpret_cast<float4*>(dst + d) =
+              make_float4(fmaf(w0, a0, w1 * y.x) * inv, fmaf(w0, a1, w1 * y.y) * inv, fmaf(w0, a2, w1 * y.z) * inv,
+                          fmaf(w0, a3, w1 * y.w) * inv);
+        }
+        if (!whole && g == 0) {
+          float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+          mls[at * a.splits + s] = make_float2(m == kUnseen ? -INFINITY : m, l);
+        }
+      }
+    }
+  done:;
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*abort_flag && !whole) {  // after a failed wait the segment counts as empty
+    float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+    for (int r = tid; r < nrows * kGroup; r += L::kThreads)
+      mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
+          make_float2(-INFINITY, 0.f);
+  }
+  if (warp == L::kMmaWarp) tmem_dealloc(tmem, 512);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace
+
+TreeVariant tree_wide_variant(bool bf16) {
+  if (bf16) return {tree_wide_kernel<false>, kRows, Wide<false>::kThreads, Wide<false>::kSmemAlloc, 1, false, 0};
+  return {tree_wide_kernel<true>, kRows, Wide<true>::kThreads, Wide<true>::kSmemAlloc, 1, true, 126};
+}
+
+}  // namespace attn

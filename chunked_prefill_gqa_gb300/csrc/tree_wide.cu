@@ -22,8 +22,9 @@
 // q and p are tensor-memory operands (p overwrites the S it came from), K a
 // K-major and V an MN-major shared-memory operand as TMA lays them down.
 //
-// Roles: warps 0-3 and 4-7 softmax; (fp32) 8-11 converters; one warp for TMA
-// (16-token pages through the block table); one for the MMAs.
+// Roles: warps 0-3 and 4-7 softmax; (fp32) 8-11 converters; one warp each for the
+// TMA of K and of V (16-token pages through the block table); one each to issue
+// the products S and O.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -45,20 +46,23 @@ constexpr uint32_t kHalf = kKeys * 128;    // 64 rows of 128 bytes
 template <bool kF32>
 struct Wide {
   static constexpr int kConvWarp = kSoft, kConvWarps = kF32 ? 4 : 0;
-  static constexpr int kTmaWarp = kSoft + kConvWarps, kMmaWarp = kTmaWarp + 1;
-  static constexpr int kThreads = kF32 ? 512 : 32 * (kMmaWarp + 1);  // fp32: whole warpgroups, for the register split
+  static constexpr int kKWarp = kSoft + kConvWarps, kVWarp = kKWarp + 1, kQkWarp = kKWarp + 2, kPvWarp = kKWarp + 3;
+  static constexpr int kThreads = 32 * (kPvWarp + 1);
   static constexpr uint32_t kOperand = kF32 ? 2 * kHalf : kHalf;     // a tile of K or V as stored
   static constexpr uint32_t kStageBytes = (kF32 ? 4 : 2) * kOperand; // K (K lo) V (V lo)
   static constexpr uint32_t kV = (kF32 ? 2 : 1) * kOperand;
   static constexpr int kStages = kF32 ? 3 : 8;
-  // Tensor memory: q's terms, then per group S (p overwrites it) and the rest of
-  // p, then the groups' O.
-  static constexpr uint32_t kColQ = 0, kColS = kF32 ? 128 : 96, kGroupCols = kF32 ? 128 : 96;
-  static constexpr uint32_t kColO = kColS + 2 * kGroupCols;
+  // Tensor memory: q's terms, then buffers of S (p overwrites it) and the rest of
+  // p, then the groups' O. With bf16 pages there is room for a third buffer, so
+  // S(n + 2) runs ahead of PV(n) and a group finds it ready; with fp32 pages it
+  // follows PV(n), whose p it overwrites.
+  static constexpr int kBufs = kF32 ? 2 : 3;
+  static constexpr uint32_t kColQ = 0, kColS = kF32 ? 128 : 96, kBufCols = kF32 ? 128 : 96;
+  static constexpr uint32_t kColO = kColS + kBufs * kBufCols;
   static constexpr uint32_t kSmemMask = kStages * kStageBytes;
   static constexpr uint32_t kSmemMl = kSmemMask + kRows * 8;         // [2 groups][128 rows] (reference, sum)
   static constexpr uint32_t kSmemBar = kSmemMl + 2 * 128 * 8;
-  static constexpr int kNumBars = 6 * kStages + 6 + 2;
+  static constexpr int kNumBars = 6 * kStages + 2 * kBufs + 4 + 3;
   static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2)
   static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
   static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
@@ -77,6 +81,11 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
 
+  // The table's first entries are on their way while the lengths are: an entry
+  // past the sequence is read and not used.
+  const int first_page = s * (a.split_len / ATTN_PAGE) + lane;
+  int first_entries = -1;
+  if ((warp == L::kKWarp || warp == L::kVWarp) && first_page < a.max_blocks) first_entries = __ldg(a.table + (size_t)b * a.max_blocks + first_page);
   const Seq seq = load_seq(a, b);
   const int i0 = rt * kRows;  // the block's first drafted row
   const int nrows = min(kRows, seq.rows - i0);
@@ -102,81 +111,69 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   uint64_t* const vready = kready + kStages;                                // [stage] V lo written (fp32)
   uint64_t* const kempty = vready + kStages;                                // [stage] S done with K
   uint64_t* const vempty = kempty + kStages;                                // [stage] PV done with V
-  uint64_t* const sfull = vempty + kStages;                                 // [group] S written
-  uint64_t* const pfull = sfull + 2;                                        // [group] p written, O read
+  uint64_t* const sfull = vempty + kStages;                                 // [buffer] S written
+  uint64_t* const sfree = sfull + L::kBufs;                                 // [buffer] PV done with its p
+  uint64_t* const pfull = sfree + L::kBufs;                                        // [group] p written, O read
   uint64_t* const odone = pfull + 2;                                        // [group] PV complete
   uint64_t* const qready = odone + 2;                                       // q's terms in tensor memory
-  uint64_t* const drain = qready + 1;                                       // MMAs in flight on abort
+  uint64_t* const drain = qready + 1;                                       // [2] MMAs in flight on abort
   uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
   uint32_t* const odd = words + 2;  // [2] drafted rows whose value is not finite
   unsigned long long* const masks = reinterpret_cast<unsigned long long*>(smem + L::kSmemMask);
   const Wait wait{a.err, a.timeout_ns, abort_flag};
 
-  // The TMA warp: lanes load the boxes of a tile of K, or of V: four pages, for
-  // fp32 in two halves of 32 dims. Lane l holds the table's entry of page l of a
-  // group of eight tiles, for V's group and for the next.
+  // The TMA warps, one for K and one for V (a box of 16 rows costs its warp about
+  // 100 cycles): lanes load the four pages of a tile, for fp32 in two halves of 32
+  // dims. Lane l holds the table's entry of page l of a group of eight tiles.
   const int* const trow = a.table + (size_t)b * a.max_blocks;
-  int entries = -1, entries_next = -1, group8 = 0, ahead = 0;
+  int entries = -1, entries_next = -1;
   auto entry_at = [&](int g) -> int {
     const int t = k0 + g * 8 * kKeys + lane * ATTN_PAGE;
     return t < k1 ? __ldg(trow + t / ATTN_PAGE) : -1;
   };
   auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t operand, int n) {
     const int st = n % kStages, p = lane & (kPages - 1), half = lane / kPages;
-    int page = __shfl_sync(0xffffffffu, (n >> 3) == group8 ? entries : entries_next, (n & 7) * kPages + p);
-    const bool has = lane < (kF32 ? 2 : 1) * kPages && k0 + n * kKeys + p * ATTN_PAGE < k1;
+    int page = __shfl_sync(0xffffffffu, entries, (n & 7) * kPages + p);
+    const int pages = min(kPages, (k1 - k0 - n * kKeys + ATTN_PAGE - 1) / ATTN_PAGE);
+    const bool has = half < (kF32 ? 2 : 1) && p < pages;
     if (has && (page < 0 || page >= a.num_pages)) {
       record_error(a.err, kDevErrBounds);
       page = a.num_pages;  // past the pool's end: reads as zeros
     }
-    const unsigned boxes = __popc(__ballot_sync(0xffffffffu, has));
-    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * (ATTN_PAGE * 128));
+    if (lane == 0) mbar_arrive_expect_tx(&full[st], pages * (kF32 ? 2 : 1) * (ATTN_PAGE * 128));
     __syncwarp();
     if (has)
       tma_load_2d(smem + st * L::kStageBytes + operand + half * kHalf + p * (ATTN_PAGE * 128), map, &full[st],
                   head * kD + half * 32, page * ATTN_PAGE);
-  };
-  auto load_next = [&]() -> bool {  // K(ahead + 1), whose stage is free earlier, then V(ahead)
-    const int n = ahead;
-    if (n + 1 < ntiles) {
-      if (n + 1 >= kStages && !wait.warp(&kempty[(n + 1) % kStages], ((n + 1) / kStages - 1) & 1)) return false;
-      load(&mk, kfull, 0, n + 1);
-    }
-    if (n >= kStages && !wait.warp(&vempty[n % kStages], (n / kStages - 1) & 1)) return false;
-    load(&mv, vfull, L::kV, n);
-    ++ahead;
-    if ((ahead >> 3) != group8) {
-      group8 = ahead >> 3;
+    if ((n & 7) == 7) {
       entries = entries_next;
-      entries_next = entry_at(group8 + 1);
+      entries_next = entry_at((n >> 3) + 2);
     }
-    return true;
   };
 
-  if (warp == L::kTmaWarp) {
+  if (warp == L::kKWarp) {
+    for (int i = lane; i < L::kNumBars; i += 32) {
+      const int kind = i / kStages;  // kfull, vfull, kready, vready, kempty, vempty, then the single ones
+      mbar_init(&kfull[i], kind < 6 ? ((kind & ~1) == 2 && kF32 ? L::kConvWarps : 1)
+                           : &kfull[i] >= pfull && &kfull[i] < odone ? quarters
+                           : &kfull[i] == qready                     ? 2 * quarters
+                                                                     : 1);
+    }
+    fence_mbar_init();
     if (lane == 0) {
-      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kfull[i], 1);               // and vfull
-      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kready[i], L::kConvWarps + !kF32);  // and vready
-      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kempty[i], 1);              // and vempty
-      for (int i = 0; i < 2; ++i) {
-        mbar_init(&sfull[i], 1);
-        mbar_init(&pfull[i], quarters);
-        mbar_init(&odone[i], 1);
-      }
-      mbar_init(qready, 2 * quarters);
-      mbar_init(drain, 1);
-      fence_mbar_init();
       *abort_flag = 0;
       odd[0] = odd[1] = 0;
     }
     __syncwarp();
     // The first tiles are on their way before the block has met.
-    entries = entry_at(0);
+    entries = first_entries;
     entries_next = entry_at(1);
-    load(&mk, kfull, 0, 0);
-    while (ahead < kStages - 1 && ahead < ntiles) load_next();
-  } else if (warp == L::kMmaWarp) {
+    for (int n = 0; n < kStages && n < ntiles; ++n) load(&mk, kfull, 0, n);
+  } else if (warp == L::kVWarp) {
+    entries = first_entries;
+    entries_next = entry_at(1);
+  } else if (warp == L::kQkWarp) {
     tmem_alloc(words, 512);
     tmem_relinquish();
   } else if (tid < kRows) {
@@ -196,101 +193,104 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     // fp32: the loaders give registers to the softmax warps (launched with 128
     // each: 8 warps x 168 + 4 x 88 + 4 x 80 = 16 x 126).
     if constexpr (kF32) {
-      if (warp < L::kTmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+      if (warp < L::kKWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
       else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     }
-    if (warp == L::kTmaWarp) {
-      while (ahead < ntiles && load_next()) {
+    if (warp == L::kKWarp || warp == L::kVWarp) {
+      const bool is_k = warp == L::kKWarp;
+      uint64_t* const full = is_k ? kfull : vfull;
+      uint64_t* const empty = is_k ? kempty : vempty;
+      int n = is_k ? kStages : 0;
+      for (; n < ntiles; ++n) {
+        if (n >= kStages && !wait.warp(&empty[n % kStages], (n / kStages - 1) & 1)) break;
+        load(is_k ? &mk : &mv, full, is_k ? 0 : L::kV, n);
       }
-      if (*abort_flag) {
-        // Copies still in flight land before the block's shared memory is
-        // released (K up to ahead + 1, V up to ahead - 1 may have been issued).
-        for (int i = max(0, ahead - kStages); i < min(ahead + 2, ntiles); ++i)
-          mbar_wait(&kfull[i % kStages], (i / kStages) & 1, 1000000);
-        for (int i = max(0, ahead - kStages); i < ahead; ++i)
-          mbar_wait(&vfull[i % kStages], (i / kStages) & 1, 1000000);
-      }
-    } else if (warp == L::kMmaWarp) {
+      if (*abort_flag)  // copies still in flight land before the block's shared memory is released
+        for (int i = max(0, min(n, ntiles) - kStages); i < min(n, ntiles); ++i)
+          mbar_wait(&full[i % kStages], (i / kStages) & 1, 1000000);
+    } else if (warp == L::kQkWarp || warp == L::kPvWarp) {
+      // Two issuers, so that one's waits and issue run under the other's.
       const uint32_t base = smem_u32(smem);
-      uint64_t* const kgo = kF32 ? kready : kfull;
-      uint64_t* const vgo = kF32 ? vready : vfull;
-      auto issue_s = [&](int n) -> bool {
-        const int st = n % kStages, g = n & 1;
-        if (!wait.warp(&kgo[st], (n / kStages) & 1)) return false;
-        tc_fence_after();
-        const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes);
-        const uint32_t d = tmem + L::kColS + g * L::kGroupCols, q = tmem + L::kColQ;
-        if (elect()) {
-          if constexpr (kF32) {
-            constexpr uint32_t id = idesc_tf32(128, kKeys);
-            constexpr uint64_t lo = L::kOperand >> 4;
+      const bool qk = warp == L::kQkWarp;
+      uint64_t* const go = (kF32 ? kready : kfull) + (qk ? 0 : kStages);  // K, or V, ready
+      if (qk) {
+        bool ok = wait.warp(qready, 0);
+        for (int n = 0; ok && n < ntiles; ++n) {
+          const int st = n % kStages, buf = n % L::kBufs;
+          if (!(ok = wait.warp(&go[st], (n / kStages) & 1) &&
+                     (n < L::kBufs || wait.warp(&sfree[buf], (n / L::kBufs - 1) & 1))))
+            break;
+          tc_fence_after();
+          const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes);
+          const uint32_t d = tmem + L::kColS + buf * L::kBufCols, q = tmem + L::kColQ;
+          if (elect()) {
+            if constexpr (kF32) {
+              constexpr uint32_t id = idesc_tf32(128, kKeys);
+              constexpr uint64_t lo = L::kOperand >> 4;
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              mma_tf32_ts(d, q + 64 + x * 8, kd + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, x > 0);
+              for (int x = 0; x < 8; ++x)
+                mma_tf32_ts(d, q + 64 + x * 8, kd + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, x > 0);
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              mma_tf32_ts(d, q + x * 8, kd + lo + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, 1);
+              for (int x = 0; x < 8; ++x)
+                mma_tf32_ts(d, q + x * 8, kd + lo + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, 1);
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              mma_tf32_ts(d, q + x * 8, kd + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, 1);
-          } else {
-            constexpr uint32_t id = idesc_bf16(128, kKeys, false);
+              for (int x = 0; x < 8; ++x)
+                mma_tf32_ts(d, q + x * 8, kd + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, 1);
+            } else {
+              constexpr uint32_t id = idesc_bf16(128, kKeys, false);
 #pragma unroll
-            for (int t = 2; t >= 0; --t)
+              for (int t = 2; t >= 0; --t)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + t * 32 + x * 8, kd + x * 2, id, t < 2 || x > 0);
+                for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + t * 32 + x * 8, kd + x * 2, id, t < 2 || x > 0);
+            }
+            mma_commit(&sfull[buf]);
+            mma_commit(&kempty[st]);
           }
-          mma_commit(&sfull[g]);
-          mma_commit(&kempty[st]);
+          __syncwarp();
         }
-        __syncwarp();
-        return true;
-      };
-      bool ok = wait.warp(qready, 0);
-      tc_fence_after();
-      ok = ok && issue_s(0) && (ntiles < 2 || issue_s(1));
-      for (int n = 0; ok && n < ntiles; ++n) {
-        const int st = n % kStages, g = n & 1;
-        if (!(ok = wait.warp(&pfull[g], (n >> 1) & 1) && wait.warp(&vgo[st], (n / kStages) & 1))) break;
-        tc_fence_after();
-        const uint32_t d = tmem + L::kColO + g * kD, p = tmem + L::kColS + g * L::kGroupCols;
-        const uint32_t vb = base + st * L::kStageBytes + L::kV;
-        if (elect()) {
-          if constexpr (kF32) {
-            constexpr uint32_t id = idesc_tf32(128, kD, true);
-            const uint64_t vd = sdesc_sw128a32_mn(vb, kHalf);
-            constexpr uint64_t lo = L::kOperand >> 4;
+      } else {
+        for (int n = 0; n < ntiles; ++n) {
+          const int st = n % kStages, g = n & 1, buf = n % L::kBufs;
+          if (!wait.warp(&go[st], (n / kStages) & 1) || !wait.warp(&pfull[g], (n >> 1) & 1)) break;
+          tc_fence_after();
+          const uint32_t d = tmem + L::kColO + g * kD, p = tmem + L::kColS + buf * L::kBufCols;
+          const uint32_t vb = base + st * L::kStageBytes + L::kV;
+          if (elect()) {
+            if constexpr (kF32) {
+              constexpr uint32_t id = idesc_tf32(128, kD, true);
+              const uint64_t vd = sdesc_sw128a32_mn(vb, kHalf);
+              constexpr uint64_t lo = L::kOperand >> 4;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + 64 + x * 8, vd + x * 64, id, x > 0);
+              for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + 64 + x * 8, vd + x * 64, id, x > 0);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + x * 8, vd + lo + x * 64, id, 1);
+              for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + x * 8, vd + lo + x * 64, id, 1);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + x * 8, vd + x * 64, id, 1);
-          } else {
-            constexpr uint32_t id = idesc_bf16(128, kD, true);
-            const uint64_t vd = sdesc_sw128_mn(vb);
+              for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + x * 8, vd + x * 64, id, 1);
+            } else {
+              constexpr uint32_t id = idesc_bf16(128, kD, true);
+              const uint64_t vd = sdesc_sw128_mn(vb);
 #pragma unroll
-            for (int t = 2; t >= 0; --t)
+              for (int t = 2; t >= 0; --t)
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                mma_f16_ts(d, p + t * 32 + x * 8, vd + x * 128, id, t < 2 || x > 0);
+                for (int x = 0; x < 4; ++x)
+                  mma_f16_ts(d, p + t * 32 + x * 8, vd + x * 128, id, t < 2 || x > 0);
+            }
+            mma_commit(&odone[g]);
+            mma_commit(&sfree[buf]);
+            mma_commit(&vempty[st]);
           }
-          mma_commit(&vempty[st]);
-          mma_commit(&odone[g]);
+          __syncwarp();
         }
-        __syncwarp();
-        // S(n + 2) overwrites what PV(n) reads: MMAs of one thread run in order.
-        if (n + 2 < ntiles) ok = issue_s(n + 2);
       }
       if (*abort_flag) {
         if (elect()) {
-          mma_commit(drain);
+          mma_commit(&drain[!qk]);
           const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < a.timeout_ns) {
+          while (!mbar_try_wait(&drain[!qk], 0) && globaltimer_ns() - t0 < a.timeout_ns) {
           }
         }
       }
-    } else if (kF32 && warp < L::kTmaWarp) {
+    } else if (kF32 && warp < L::kKWarp) {
       // x lo = x - hi(x), element by element at the same offset of the next region.
       const int ctid = tid - 32 * L::kConvWarp;
       auto low = [](float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffffe000u); };
@@ -360,7 +360,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     const int row = quarter * 32 + lane;
     const bool active = quarter < quarters;
     const uint32_t lane_tmem = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t s_tmem = lane_tmem + L::kColS + g * L::kGroupCols, o_tmem = lane_tmem + L::kColO + g * kD;
+    const uint32_t o_tmem = lane_tmem + L::kColO + g * kD;
     float ref = kUnseen, l0 = 0.f, l1 = 0.f;
     float o[kD];
 #pragma unroll
@@ -417,7 +417,9 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 
       int k = 0;  // the group's k-th tile
       for (int n = g; n < ntiles; n += 2, ++k) {
-        failed |= !wait.warp(&sfull[g], k & 1);
+        const int buf = n % L::kBufs;
+        const uint32_t s_tmem = lane_tmem + L::kColS + buf * L::kBufCols;
+        failed |= !wait.warp(&sfull[buf], (n / L::kBufs) & 1);
         tc_fence_after();
         float x[kKeys];
         tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(&x[0]));
@@ -456,10 +458,14 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
           }
         }
         // The row's reference moves when a score passes it by 2^8.
-        float most = max3(x[0], x[1], x[2]);
+        float top[4];
 #pragma unroll
-        for (int i = 3; i < 63; i += 2) most = max3(most, x[i], x[i + 1]);
-        most = fmaxf(most, x[63]) * kTreeC;
+        for (int c = 0; c < 4; ++c) {  // four chains
+          top[c] = fmaxf(x[c], x[c + 4]);
+#pragma unroll
+          for (int i = 8; i < kKeys; i += 8) top[c] = max3(top[c], x[i + c], x[i + c + 4]);
+        }
+        const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * kTreeC;
         float alpha = 1.f;
         if (most > ref + kTreeStale) {
           alpha = ex2(ref - most);
@@ -467,9 +473,6 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
         l0 *= alpha;
         l1 *= alpha;
-        if (k > 0) {  // PV of the group's previous tile has read p, and its O is complete
-          failed |= !wait.warp(&odone[g], (k - 1) & 1);
-        }
         const float neg = -ref;
 #pragma unroll
         for (int h = 0; h < kKeys; h += 32) {
@@ -585,7 +588,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
           make_float2(-INFINITY, 0.f);
   }
-  if (warp == L::kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == L::kQkWarp) tmem_dealloc(tmem, 512);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 

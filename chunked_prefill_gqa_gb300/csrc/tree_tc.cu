@@ -19,7 +19,7 @@
 // when a score passes it by 2^8, which each thread checks on its own values; one
 // barrier with a vote per tile decides. Sums stay per thread until the end. The
 // tensor core's accumulation does not round to nearest, and over a long key
-// range that error would lean one way: every 8 tiles (and when a reference
+// range that error would lean one way: every 4 tiles (and when a reference
 // moves, which then costs nothing more) O is added to fp32 sums in shared
 // memory and starts anew.
 //
@@ -47,7 +47,7 @@ constexpr uint32_t kOperand = kKeys * kD * 2;       // 16 KB: a tile of K, of V,
 constexpr uint32_t kBox = ATTN_PAGE * 128;
 
 constexpr int kCols = 16;                           // columns of a softmax thread
-constexpr int kFlush = 8;                           // tiles between two flushes of O
+constexpr int kFlush = 4;                           // tiles between two flushes of O
 
 constexpr int kConvWarps = 8;                       // fp32 pages: load and split K and V
 constexpr int kUnits = kKeys * 8 / (32 * kConvWarps);  // (key, 8 dims) of an operand a thread splits

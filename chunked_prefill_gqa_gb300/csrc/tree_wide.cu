@@ -291,9 +291,19 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         }
       }
     } else if (kF32 && warp < L::kKWarp) {
-      // x lo = x - hi(x), element by element at the same offset of the next region.
+      // hi(x), rounded to nearest, in place and lo = x - hi(x) at the same offset of
+      // the next region, element by element. (Left as it landed, x would reach the
+      // tensor core truncated: a remainder of twice the size and of x's own sign.)
       const int ctid = tid - 32 * L::kConvWarp;
-      auto low = [](float x) { return x - __uint_as_float(__float_as_uint(x) & 0xffffe000u); };
+      auto split = [&](uint8_t* at, float4 x) {
+        float4 h;
+        h.x = __uint_as_float((__float_as_uint(x.x) + 0x1000u) & 0xffffe000u);
+        h.y = __uint_as_float((__float_as_uint(x.y) + 0x1000u) & 0xffffe000u);
+        h.z = __uint_as_float((__float_as_uint(x.z) + 0x1000u) & 0xffffe000u);
+        h.w = __uint_as_float((__float_as_uint(x.w) + 0x1000u) & 0xffffe000u);
+        *reinterpret_cast<float4*>(at) = h;
+        *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x.x - h.x, x.y - h.y, x.z - h.z, x.w - h.w);
+      };
       for (int n = 0; n < ntiles; ++n) {
         const int st = n % kStages;
         uint8_t* const stage = smem + st * L::kStageBytes;
@@ -304,9 +314,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(stage + (ctid + (4 * h + i) * 128) * 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(stage + L::kOperand + (ctid + (4 * h + i) * 128) * 16) =
-                make_float4(low(x[i].x), low(x[i].y), low(x[i].z), low(x[i].w));
+          for (int i = 0; i < 4; ++i) split(stage + (ctid + (4 * h + i) * 128) * 16, x[i]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -335,16 +343,11 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                   y[k] = 0.f;
                   bad = true;
                 }
-              if (bad) {
-                *reinterpret_cast<float4*>(stage + L::kV + unit * 16) = x[i];
-                if (pos < k1) atomicOr(odd + (at >> 5), 1u << (at & 31));
-              }
+              if (bad && pos < k1) atomicOr(odd + (at >> 5), 1u << (at & 31));
             }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4*>(stage + L::kV + L::kOperand + (ctid + (4 * h + i) * 128) * 16) =
-                make_float4(low(x[i].x), low(x[i].y), low(x[i].z), low(x[i].w));
+          for (int i = 0; i < 4; ++i) split(stage + L::kV + (ctid + (4 * h + i) * 128) * 16, x[i]);
         }
         fence_proxy_async_smem();
         __syncwarp();

@@ -392,116 +392,46 @@ def attn_decode_paged_noalloc(q, kPages, vPages, blockTable, contextLens, out, m
     return out
 
 
-# The calls of a serving step run once a layer: their checks are written to
-# cost little (one look at each property, no generic helpers).
-_torch = None
+def _native():
+    """The extension that checks and marshals the serving-step calls (binding.c):
+    they run once a layer, where doing that in Python would take longer than the
+    launch. It raises TypeError or ValueError for a tensor of another type, shape,
+    layout or device than stated; every tensor has to be on the current device."""
+    global _binding
+    if _binding is None:
+        load()
+        path = os.path.join(_HERE, "_build", "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m chunked_prefill_gqa_gb300.build`")
+        import importlib.machinery
+        import importlib.util
+        loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+        loader.exec_module(module)
+        _binding = module
+    return _binding
 
 
-def _t():
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch
-
-
-def _bad(name, t, dtype, shape, dev):
-    """Raise the error of a tensor that _ptr_of refused."""
-    torch = _t()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor, got {t.dtype} on {t.device}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    raise ValueError(f"{name} is on {t.device}, the call on CUDA device {dev}")
-
-
-def _ptr_of(name, t, dtype, shape, dev):
-    """The address of t, a contiguous tensor of this dtype and shape on device dev."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _bad(name, t, dtype, shape, dev)
-
-
-def _row_ptr(name, t, dtype, shape, dev):
-    """(address, elements between rows) of t [n][heads][64] on device dev, the
-    heads of a row packed, rows any distance apart."""
-    torch = _t()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, expected {dtype} {shape}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, the call on CUDA device {dev}")
-    n, heads, _ = shape
-    between, head, one = t.stride()
-    if one != 1 or head != D:
-        raise ValueError(f"{name}: the 64 values of a head and the heads of a row must be packed")
-    return t.data_ptr(), between if n > 1 else heads * D
-
-
-def _cuda_device():
-    """The current device; the tensors of a call have to be on it."""
-    torch = _t()
-    if not torch.cuda.is_initialized():
-        if not torch.cuda.is_available():
-            raise ValueError("the tensors must be on a CUDA device, and there is none")
-        torch.cuda.init()
-    return torch._C._cuda_getDevice()
-
-
-def _stream_on(stream, dev):
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+_binding = None
 
 
 def attn_rope_table(cosSin, theta: float = 10000.0, invFreq=None, stream=None):
     """Fill the rotation table cosSin [numPositions][64] fp32 (cosines, then
     sines). The 32 frequencies are theta^(-i / 32), or ``invFreq`` (any sequence
     of 32 floats) for scaled rotations."""
-    torch, dev = _t(), _cuda_device()
-    n = cosSin.shape[0]
-    ptr = _ptr_of("cosSin", cosSin, torch.float32, (n, D), dev)
+    import torch
+    if cosSin.dtype != torch.float32 or not cosSin.is_cuda or not cosSin.is_contiguous():
+        raise ValueError("cosSin must be a contiguous float32 CUDA tensor")
+    if cosSin.dim() != 2 or cosSin.shape[1] != D or cosSin.get_device() != torch.cuda.current_device():
+        raise ValueError(f"cosSin must be [numPositions][{D}] on the current device")
     freq = [float(theta) ** (-i / 32.0) for i in range(D // 2)] if invFreq is None else [float(f) for f in invFreq]
     if len(freq) != D // 2:
         raise ValueError(f"invFreq must hold {D // 2} frequencies")
     host = (ctypes.c_double * (D // 2))(*freq)
-    rc = load().attn_rope_table(host, ptr, n, _stream_on(stream, dev))
+    rc = load().attn_rope_table(host, _ptr(cosSin), cosSin.shape[0], _stream_handle(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope_table")
     return cosSin
-
-
-def _row_args(q, k, qOut, qWeight, kWeight, cosSin, positions, n, dev):
-    """What the row calls share: (element type, code, k's address and stride, q's,
-    qOut, the weights, the table, the positions, the table's rows)."""
-    torch = _torch
-    f32 = torch.float32
-    dtype = k.dtype
-    code = F32 if dtype is f32 else BF16
-    if code and dtype is not torch.bfloat16:
-        raise ValueError(f"k must be float32 or bfloat16, got {dtype}")
-    kp, ks = _row_ptr("k", k, dtype, (n, HKV, D), dev)
-    qp = qs = qo = qw = kw = cs = pos = None
-    count = 0
-    if q is not None:
-        qp, qs = _row_ptr("q", q, dtype, (n, HQ, D), dev)
-        qo = _ptr_of("qOut", qOut, f32, (n, HQ, D), dev)
-    if qWeight is not None:
-        qw = _ptr_of("qWeight", qWeight, f32, (D,), dev)
-    if kWeight is not None:
-        kw = _ptr_of("kWeight", kWeight, f32, (D,), dev)
-    if cosSin is not None:
-        count = cosSin.shape[0]
-        cs = _ptr_of("cosSin", cosSin, f32, (count, D), dev)
-    if positions is not None:
-        pos = _ptr_of("positions", positions, torch.int32, (n,), dev)
-    return dtype, code, kp, ks, qp, qs or 0, qo, qw, kw, cs, pos, count
 
 
 def attn_qk_norm_rope(q, k, positions, cosSin, qOut, kOut, qWeight=None, kWeight=None, eps: float = 1e-6,
@@ -513,48 +443,11 @@ def attn_qk_norm_rope(q, k, positions, cosSin, qOut, kOut, qWeight=None, kWeight
     [N][32][64], kOut fp32 or bf16 [N][8][64], contiguous. qWeight, kWeight fp32
     [64] or None (not normed); positions int32 [N] into cosSin (attn_rope_table),
     both None for no rotation. Returns (qOut, kOut)."""
-    torch = _t()
-    if not isinstance(k, torch.Tensor):
-        raise TypeError("k must be a torch.Tensor")
-    dev, n = _cuda_device(), k.shape[0]
-    _, code, kp, ks, qp, qs, qo, qw, kw, cs, pos, count = _row_args(q, k, qOut, qWeight, kWeight, cosSin, positions,
-                                                                    n, dev)
-    out = BF16 if kOut.dtype is torch.bfloat16 else F32
-    ko = _ptr_of("kOut", kOut, torch.bfloat16 if out else torch.float32, (n, HKV, D), dev)
-    rc = (_lib or load()).attn_qk_norm_rope(qp, kp, code, qs, ks, qw, kw, eps, cs, pos, count, pairing, qo, ko, out, n,
-                                            _stream_on(stream, dev))
-    if rc != ATTN_OK:
+    rc = (_binding or _native()).qk_norm_rope(q, k, positions, cosSin, qOut, kOut, qWeight, kWeight, eps, pairing,
+                                              stream)
+    if rc:
         raise AttnError(rc, "attn_qk_norm_rope")
     return qOut, kOut
-
-
-def _batch(kPages, vPages, blockTable, contextLens, dtype, dev):
-    """Addresses and sizes of a batch's paged cache: (pages, table, lengths, B, maxBlocks, numPages)."""
-    i32 = _torch.int32
-    B, (rows, blocks), pages = contextLens.shape[0], blockTable.shape, kPages.shape[0]
-    shape = (pages, PAGE, HKV, D)
-    return (_ptr_of("kPages", kPages, dtype, shape, dev), _ptr_of("vPages", vPages, dtype, shape, dev),
-            _ptr_of("blockTable", blockTable, i32, (B, blocks), dev),
-            _ptr_of("contextLens", contextLens, i32, (B,), dev), B, blocks, pages)
-
-
-def _append(name, bf16, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin, positions, kWeight, q, qOut,
-            qWeight, eps, pairing, stream):
-    torch = _t()
-    if not isinstance(k, torch.Tensor):
-        raise TypeError("k must be a torch.Tensor")
-    dev, n = _cuda_device(), k.shape[0]
-    dtype, code, kp, ks, qp, qs, qo, qw, kw, cs, pos, count = _row_args(q, k, qOut, qWeight, kWeight, cosSin,
-                                                                        positions, n, dev)
-    vp, vs = _row_ptr("v", v, dtype, (n, HKV, D), dev)
-    kpg, vpg, bt, cl, B, blocks, pages = _batch(kPages, vPages, blockTable, contextLens,
-                                                torch.bfloat16 if bf16 else torch.float32, dev)
-    rs = _ptr_of("rowStart", rowStart, torch.int32, (B + 1,), dev)
-    rc = getattr(_lib or load(), name)(qp, kp, vp, code, qs, ks, vs, qw, kw, eps, cs, pos, count, pairing, qo, kpg,
-                                       vpg, bt, cl, rs, B, n, blocks, pages, _stream_on(stream, dev))
-    if rc != ATTN_OK:
-        raise AttnError(rc, name)
-    return qOut
 
 
 def attn_append_paged(k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin=None, positions=None,
@@ -568,45 +461,27 @@ def attn_append_paged(k, v, kPages, vPages, blockTable, contextLens, rowStart, c
     vPages [numPages][16][8][64] fp32; blockTable int32 [B][maxBlocks],
     contextLens int32 [B] (tokens in the cache before these rows), rowStart int32
     [B + 1]. positions int32 [N], or None for consecutive ones. Returns qOut."""
-    return _append("attn_append_paged", False, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin,
-                   positions, kWeight, q, qOut, qWeight, eps, pairing, stream)
+    rc = (_binding or _native()).append_paged(False, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin,
+                                              positions, kWeight, q, qOut, qWeight, eps, pairing, stream)
+    if rc:
+        raise AttnError(rc, "attn_append_paged")
+    return qOut
 
 
 def attn_append_paged_bf16kv(k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin=None, positions=None,
                              kWeight=None, q=None, qOut=None, qWeight=None, eps: float = 1e-6,
                              pairing: int = ROPE_HALVES, stream=None):
     """attn_append_paged into bfloat16 pages."""
-    return _append("attn_append_paged_bf16kv", True, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin,
-                   positions, kWeight, q, qOut, qWeight, eps, pairing, stream)
+    rc = (_binding or _native()).append_paged(True, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin,
+                                              positions, kWeight, q, qOut, qWeight, eps, pairing, stream)
+    if rc:
+        raise AttnError(rc, "attn_append_paged_bf16kv")
+    return qOut
 
 
 def attn_tree_workspace_bytes(B: int, N: int, max_rows: int, max_context: int, num_splits: int = 0) -> int:
     """Bytes of workspace attn_tree_paged (either page type) needs on the current device."""
     return int(load().attn_tree_workspace_bytes(int(B), int(N), int(max_rows), int(max_context), int(num_splits)))
-
-
-def _tree(name, bf16, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows, max_context,
-          num_splits, workspace, stream):
-    torch = _t()
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    dev, n = _cuda_device(), q.shape[0]
-    shape = (n, HQ, D)
-    qp, op = _ptr_of("q", q, torch.float32, shape, dev), _ptr_of("out", out, torch.float32, shape, dev)
-    kp, vp, bt, cl, B, blocks, pages = _batch(kPages, vPages, blockTable, contextLens,
-                                              torch.bfloat16 if bf16 else torch.float32, dev)
-    rs = _ptr_of("rowStart", rowStart, torch.int32, (B + 1,), dev)
-    mp = None if masks is None else _ptr_of("masks", masks, torch.int64, (n,), dev)
-    wp, wb = None, 0
-    if workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on CUDA device {dev}")
-        wp, wb = workspace.data_ptr(), workspace.nbytes
-    rc = getattr(_lib or load(), name)(qp, kp, vp, bt, cl, rs, mp, op, B, n, max_rows, blocks, pages, max_context,
-                                       num_splits, wp, wb, _stream_on(stream, dev))
-    if rc != ATTN_OK:
-        raise AttnError(rc, name)
-    return out
 
 
 def attn_tree_paged(q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows: int, max_context: int,
@@ -619,41 +494,39 @@ def attn_tree_paged(q, kPages, vPages, blockTable, contextLens, rowStart, masks,
     the batch. ``workspace``: a CUDA tensor of at least
     attn_tree_workspace_bytes(B, N, max_rows, max_context, num_splits) bytes, or
     None when none is needed."""
-    return _tree("attn_tree_paged", False, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows,
-                 max_context, num_splits, workspace, stream)
+    rc = (_binding or _native()).tree_paged(False, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out,
+                                            max_rows, max_context, num_splits, workspace, stream)
+    if rc:
+        raise AttnError(rc, "attn_tree_paged")
+    return out
 
 
 def attn_tree_paged_bf16kv(q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows: int,
                            max_context: int, num_splits: int = 0, workspace=None, stream=None):
     """attn_tree_paged against bfloat16 pages, used exactly as stored."""
-    return _tree("attn_tree_paged_bf16kv", True, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out,
-                 max_rows, max_context, num_splits, workspace, stream)
-
-
-def _compact(name, bf16, kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows, stream):
-    torch, dev = _t(), _cuda_device()
-    kp, vp, bt, cl, B, blocks, pages = _batch(kPages, vPages, blockTable, contextLens,
-                                              torch.bfloat16 if bf16 else torch.float32, dev)
-    width = keep.shape[1]
-    ke = _ptr_of("keep", keep, torch.int32, (B, width), dev)
-    kc = _ptr_of("keepCounts", keepCounts, torch.int32, (B,), dev)
-    rc = getattr(_lib or load(), name)(kp, vp, bt, cl, ke, kc, B, width, max_rows, blocks, pages,
-                                       _stream_on(stream, dev))
-    if rc != ATTN_OK:
-        raise AttnError(rc, name)
+    rc = (_binding or _native()).tree_paged(True, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out,
+                                            max_rows, max_context, num_splits, workspace, stream)
+    if rc:
+        raise AttnError(rc, "attn_tree_paged_bf16kv")
+    return out
 
 
 def attn_compact_paged(kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows: int, stream=None):
     """Move the accepted drafted rows' keys and values to the front of the rows:
     row keep[b][i] to token contextLens[b] + i, i < keepCounts[b]. keep int32
     [B][maxKeep], rising in each row, entries below max_rows; keepCounts int32 [B]."""
-    _compact("attn_compact_paged", False, kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows, stream)
+    rc = (_binding or _native()).compact_paged(False, kPages, vPages, blockTable, contextLens, keep, keepCounts,
+                                               max_rows, stream)
+    if rc:
+        raise AttnError(rc, "attn_compact_paged")
 
 
 def attn_compact_paged_bf16kv(kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows: int, stream=None):
     """attn_compact_paged on bfloat16 pages."""
-    _compact("attn_compact_paged_bf16kv", True, kPages, vPages, blockTable, contextLens, keep, keepCounts, max_rows,
-             stream)
+    rc = (_binding or _native()).compact_paged(True, kPages, vPages, blockTable, contextLens, keep, keepCounts,
+                                               max_rows, stream)
+    if rc:
+        raise AttnError(rc, "attn_compact_paged_bf16kv")
 
 
 def attn_naive_workspace_bytes(C: int, P: int) -> int:

@@ -1,7 +1,8 @@
 """Build libattnprefill.so in-tree with nvcc for sm_103a.
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then nvcc links the
-shared library (CUDA runtime linked statically). Run as a module
+shared library (CUDA runtime linked statically), and gcc the small CPython
+extension that marshals the serving-step calls to it. Run as a module
 (``python -m chunked_prefill_gqa_gb300.build``) or call :func:`build`.
 """
 from __future__ import annotations
@@ -12,11 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libattnprefill.so")
+BINDING = os.path.join(OUT, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -35,14 +38,14 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(CSRC, "*.c"))) + \
         [os.path.join(INCLUDE, "attn_prefill.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -74,7 +77,23 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    build_binding(nvcc)
     return LIB
+
+
+def build_binding(nvcc: str) -> None:
+    """The CPython extension next to the library, which it finds by its own folder."""
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE, "-I", cuda,
+           "-I", sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "binding.c"), "-L", OUT,
+           "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on binding.c:\n{r.stderr}")
+    if r.stderr:
+        sys.stderr.write(r.stderr)
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":

@@ -456,10 +456,8 @@ int tree_paged(TreeCall c, int numSplits, void* workspace, size_t workspaceBytes
     return ATTN_EALIGN;
   DeviceState* st = nullptr;
   if ((rc = current_device(&st)) != ATTN_OK) return rc;
-  if ((rc = tree_splits(c.type == ATTN_BF16, c.B, c.max_rows, c.max_context, numSplits, &c.splits, &c.split_len)) !=
-      ATTN_OK)
-    return rc;
-  const size_t need = tree_workspace_bytes(c.N, c.splits);
+  if ((rc = tree_plan(c.type == ATTN_BF16, c.B, c.max_rows, c.max_context, numSplits, &c.plan)) != ATTN_OK) return rc;
+  const size_t need = tree_workspace_bytes(c.N, c.plan);
   if (need > 0) {
     if (!workspace || workspaceBytes < need) return ATTN_ESPACE;
     if (!aligned16(workspace)) return ATTN_EALIGN;
@@ -575,9 +573,9 @@ extern "C" size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxCo
     return 0;
   size_t most = 0;
   for (int bf16 = 0; bf16 < 2; ++bf16) {  // either page type may be called with it
-    int splits = 0, len = 0;
-    if (tree_splits(bf16 != 0, B, maxRows, maxContext, numSplits, &splits, &len) != ATTN_OK) return 0;
-    const size_t need = tree_workspace_bytes(N, splits);
+    TreePlan plan{};
+    if (tree_plan(bf16 != 0, B, maxRows, maxContext, numSplits, &plan) != ATTN_OK) return 0;
+    const size_t need = tree_workspace_bytes(N, plan);
     if (need > most) most = need;
   }
   return most;
@@ -588,7 +586,7 @@ extern "C" int attn_tree_paged(const float* q, const float* kPages, const float*
                                int N, int maxRows, int maxBlocks, int numPages, int maxContext, int numSplits,
                                void* workspace, size_t workspaceBytes, cudaStream_t stream) {
   return tree_paged(TreeCall{q, kPages, vPages, ATTN_F32, blockTable, contextLens, rowStart, masks, out, nullptr, B, N,
-                             maxRows, maxBlocks, numPages, maxContext, 0, 0},
+                             maxRows, maxBlocks, numPages, maxContext, {}},
                     numSplits, workspace, workspaceBytes, stream);
 }
 
@@ -598,7 +596,7 @@ extern "C" int attn_tree_paged_bf16kv(const float* q, const uint16_t* kPages, co
                                       int numPages, int maxContext, int numSplits, void* workspace,
                                       size_t workspaceBytes, cudaStream_t stream) {
   return tree_paged(TreeCall{q, kPages, vPages, ATTN_BF16, blockTable, contextLens, rowStart, masks, out, nullptr, B,
-                             N, maxRows, maxBlocks, numPages, maxContext, 0, 0},
+                             N, maxRows, maxBlocks, numPages, maxContext, {}},
                     numSplits, workspace, workspaceBytes, stream);
 }
 

@@ -101,8 +101,12 @@ cudaError_t launch_compact(void* k_pages, void* v_pages, int type, const int* ta
                            const int* keep, const int* counts, int B, int max_keep, int max_rows, int max_blocks,
                            int num_pages, unsigned* err, cudaStream_t stream);
 
-// Attention of drafted rows over a paged cache (tree.cu): the segments of a
-// call, the workspace of its partials, launch. int results are ATTN_* codes.
+// Attention of drafted rows over a paged cache (tree.cu): how a call is cut into
+// key segments, the workspace of its partials, launch. int results are ATTN_* codes.
+struct TreePlan {
+  int splits, split_len;
+  bool cluster;  // the segments of a unit are one cluster: no partials in memory
+};
 struct TreeCall {
   const float* q;
   const void *k_pages, *v_pages;
@@ -110,10 +114,11 @@ struct TreeCall {
   const int *table, *ctx_lens, *row_start;
   const long long* masks;
   float *out, *parts;
-  int B, N, max_rows, max_blocks, num_pages, max_context, split_len, splits;
+  int B, N, max_rows, max_blocks, num_pages, max_context;
+  TreePlan plan;
 };
-int tree_splits(bool bf16, int B, int max_rows, int max_context, int splits_hint, int* splits, int* split_len);
-size_t tree_workspace_bytes(int N, int splits);
+int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, TreePlan* plan);
+size_t tree_workspace_bytes(int N, const TreePlan& plan);
 int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream);
 
 // Tensor-pipe rate measurement (peak.cu): `ctas` CTAs each issue `iters`

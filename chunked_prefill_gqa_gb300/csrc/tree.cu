@@ -6,22 +6,25 @@
 //   K_i = {0 .. ctx-1} u {ctx + j : bit j of mask_i, j < T}
 //   out_i = sum_{j in K_i} softmax_j(q_i . k_j / 8) v_j,   zeros for an empty K_i
 //
-// One pass over the cache per sequence and KV head: a block owns (key segment,
-// KV head, row tile, sequence) and all four query heads of that KV head, 16 MT
-// rows of 4 MT drafted tokens. Its warps share nothing until the end. Each
-// walks its own 16-token pages through its own ring of TMA boxes, with its own
-// running maximum, sum and accumulator, and the warps' (and then the segments')
-// partials merge with the split-K rule: m = max m_s, out = sum e^(m_s - m) O_s /
-// sum e^(m_s - m) l_s.
+// Three kernels compute it, all in one pass over the cache with all four query
+// heads of a KV head at once, in fp32 precision on both page types:
+//   bf16 pages, up to 8 drafted rows: tree_tc.cu (keys on the M side of tcgen05)
+//   more rows, and fp32 pages from 5 on: tree_wide.cu (rows on the M side)
+//   fp32 pages, up to 4 rows: the kernel here
+// This file also holds what they share on the host: how a call is cut into key
+// segments, the launch, and the merge of segments that are not one cluster, with
+// the split-K rule m = max m_s, out = sum e^(m_s - m) O_s / sum e^(m_s - m) l_s.
 //
-// The products run on mma.sync (16 query rows x 8 keys), in fp32 precision:
-//   fp32 pages: each operand as two tf32 terms x = hi + lo (hi = x rounded to 11
-//     bits), hi hi + hi lo + lo hi;
-//   bf16 pages: K and V exactly as stored, q and the probabilities as three bf16
-//     terms each (24 bits), so nothing of q or p is lost to the cache's precision.
-// The reference maximum of a row moves only when a score passes it by 2^8 (p
-// stays below 2^8, far from fp32's range), so in the steady state a page costs
-// one vote instead of a reduction over lanes and a rescaled accumulator.
+// The kernel here: a block owns (key segment, KV head, sequence) and 16 query
+// rows, 4 drafted tokens, an m-tile of mma.sync (16 rows x 8 keys, so few rows
+// waste little, where a tcgen05 tile would be mostly padding and fp32 pages would
+// have to be split in shared memory first). Its warps share nothing until the
+// end: each walks its own 16-token pages through its own ring of TMA boxes, with
+// its own running maximum, sum and accumulator. Each operand is two tf32 terms
+// x = hi + lo (hi = x rounded to 11 bits), hi hi + hi lo + lo hi, split in
+// registers. The reference maximum of a row moves only when a score passes it by
+// 2^8 (p stays below 2^8, far from fp32's range), so in the steady state a page
+// costs one vote instead of a reduction over lanes and a rescaled accumulator.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -38,52 +41,27 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr float kC = kTreeC, kStale = kTreeStale;
 constexpr int kMaxSplits = 64;
 
-// Variants: MT m-tiles of 16 rows (4 MT drafted tokens). Warps, ring depth and
-// blocks per SM keep at least 128 KB of copies in flight on an SM, twice what
-// its share of the memory bandwidth needs.
-template <bool kBf16, int MT>
-struct Cfg {
-  static constexpr int kWarps = (!kBf16 && MT > 1) ? 8 : 4;
-  static constexpr int kStages = !kBf16 ? 3 : MT == 4 ? 5 : 6;
-  static constexpr int kBoxes = kBf16 ? 1 : 2;                    // boxes of 128 bytes x 16 tokens per operand
-  static constexpr uint32_t kBox = ATTN_PAGE * 128;
-  static constexpr uint32_t kStage = 2 * kBoxes * kBox;           // K, then V
-  static constexpr int kSteps = kBf16 ? 4 : 8;                    // k-steps of q . k
-  static constexpr int kTerms = kBf16 ? 3 : 2;                    // q's terms
-  static constexpr uint32_t kQBytes = MT * kSteps * kTerms * 512;  // fragments, 16 bytes a lane
-  static constexpr uint32_t kRing = kWarps * kStages * kStage;
-  static constexpr uint32_t kSmemQ = kRing;
-  static constexpr uint32_t kSmemMask = kSmemQ + kQBytes;
-  static constexpr uint32_t kSmemBar = kSmemMask + 4 * MT * 8;
-  static constexpr uint32_t kSmemTotal = kSmemBar + kWarps * kStages * 8;
-  static constexpr uint32_t kSmemAlloc = kSmemTotal + 1024;
-  static constexpr int kBlocks = 233472 / (kSmemAlloc + 1024);
-  static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
-  static_assert(16 * MT * kD * 4 <= kStages * kStage, "a warp's accumulator fits its own ring");
-  static_assert(kWarps * 16 * MT * 8 <= kQBytes, "the warps' maxima and sums fit where q was");
-};
+constexpr int kWarps = 4;
+constexpr int kStages = 3;                       // pages of a warp in flight: 96 KB a block, two blocks an SM
+constexpr int kRows = 16;
+constexpr int kRowStride = kD + 4;
+constexpr uint32_t kBox = ATTN_PAGE * 128;       // 32 dims of 16 tokens
+constexpr uint32_t kStage = 4 * kBox;            // a page of K, then of V
+constexpr int kSteps = 8;                        // k-steps of q . k
+constexpr uint32_t kSmemQ = kWarps * kStages * kStage;          // q's fragments, later the warps' maxima and sums
+constexpr uint32_t kSmemRows = kSmemQ + kSteps * 2 * 512;       // [16][kRowStride], for a cluster's merge
+constexpr uint32_t kSmemEnds = kSmemRows + kRows * kRowStride * 4;
+constexpr uint32_t kSmemMask = kSmemEnds + kRows * 8;
+constexpr uint32_t kSmemBar = kSmemMask + 4 * 8;
+constexpr uint32_t kSmemAlloc = kSmemBar + kWarps * kStages * 8 + 1024;
+constexpr int kBlocks = 2;
+static_assert(kBlocks * (kSmemAlloc + 1024) <= 233472, "shared memory of an SM");
+static_assert(kRows * kD * 4 <= kStages * kStage, "a warp's accumulator fits its own ring");
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
 }
 // The tf32 terms: hi rounded to nearest (half the remainder of a truncation,
 // and of either sign, so what the products drop does not lean one way), lo the
@@ -107,53 +85,49 @@ __device__ __forceinline__ void add4(float (&o)[4], const float (&x)[4]) {
 // of a fragment touch all eight chunk positions of the swizzle once.
 __device__ __forceinline__ int turn(int n) { return (n >> 1) | ((n & 1) << 2); }
 
-template <bool kBf16, int MT>
-__global__ void __launch_bounds__(32 * Cfg<kBf16, MT>::kWarps, Cfg<kBf16, MT>::kBlocks)
-tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
-  using F = Cfg<kBf16, MT>;
-  constexpr int kWarps = F::kWarps, kStages = F::kStages;
+__global__ void __launch_bounds__(32 * kWarps, kBlocks)
+tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;  // fragment row (or key), fragment column
-  const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
+  const int s = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
 
   const Seq seq = load_seq(a, b);
-  const int i0 = rt * 4 * MT;               // the tile's first drafted row
-  const int nrows = min(4 * MT, seq.rows - i0);
+  const int nrows = seq.rows;  // of at most four
   const int k0 = s * a.split_len;
   const int k1 = min(k0 + a.split_len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   if (nrows <= 0) return;
-  if (k0 >= k1) {
+  // Early: the merge's blocks may take their places; they wait for all of this grid.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (k0 >= k1 && !a.cluster) {
     // Past the sequence: the merge counts its segments from the lengths. A
     // sequence without any key (only a refused one) gets zeros.
     if (s == 0)
       for (int e = tid; e < nrows * kGroup * kD; e += 32 * kWarps)
-        a.out[((size_t)(seq.first + i0 + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
+        a.out[((size_t)(seq.first + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
     return;
   }
-  const bool whole = seq.keys <= a.split_len;  // one segment: the output is written here
+  const bool whole = !a.cluster && seq.keys <= a.split_len;  // one segment: the output is written here
 
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F::kSmemBar);
-  unsigned long long* masks = reinterpret_cast<unsigned long long*>(smem + F::kSmemMask);
-  uint8_t* const ring = smem + warp * (kStages * F::kStage);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kSmemBar);
+  unsigned long long* masks = reinterpret_cast<unsigned long long*>(smem + kSmemMask);
+  uint8_t* const ring = smem + warp * (kStages * kStage);
   uint64_t* const full = bars + warp * kStages;
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
     tc::fence_mbar_init();
   }
-  if (tid < 4 * MT) {
-    unsigned long long m = 0;
-    const int i = i0 + tid;
-    if (tid < nrows) m = a.masks ? (unsigned long long)__ldg(a.masks + seq.first + i) : ~0ull >> (63 - i);
-    masks[tid] = m;
-  }
+  if (tid < 4)
+    masks[tid] = tid >= nrows ? 0ull
+                 : a.masks    ? (unsigned long long)__ldg(a.masks + seq.first + tid)
+                              : ~0ull >> (63 - tid);
   __syncwarp();
 
   // This warp's pages: pages warp, warp + kWarps, ... of the segment. Lane l
   // holds the table entry of its l-th page from the last multiple of 32.
-  const int npages = (k1 - k0 + ATTN_PAGE - 1) / ATTN_PAGE;
+  const int npages = max(0, (k1 - k0 + ATTN_PAGE - 1) / ATTN_PAGE);
   const int mine = warp < npages ? (npages - warp + kWarps - 1) / kWarps : 0;
   const int* trow = a.table + (size_t)b * a.max_blocks + k0 / ATTN_PAGE + warp;
   int entries = 0;
@@ -166,83 +140,54 @@ tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUte
         page = a.num_pages;
       }
       const int st = n % kStages;
-      uint8_t* dst = ring + st * F::kStage;
-      tc::mbar_arrive_expect_tx(&full[st], F::kStage);
+      uint8_t* dst = ring + st * kStage;
+      tc::mbar_arrive_expect_tx(&full[st], kStage);
 #pragma unroll
-      for (int x = 0; x < F::kBoxes; ++x) {
-        tc::tma_load_2d(dst + x * F::kBox, &mk, &full[st], head * kD + x * 32, page * ATTN_PAGE);
-        tc::tma_load_2d(dst + (F::kBoxes + x) * F::kBox, &mv, &full[st], head * kD + x * 32, page * ATTN_PAGE);
+      for (int x = 0; x < 2; ++x) {
+        tc::tma_load_2d(dst + x * kBox, &mk, &full[st], head * kD + x * 32, page * ATTN_PAGE);
+        tc::tma_load_2d(dst + (2 + x) * kBox, &mv, &full[st], head * kD + x * 32, page * ATTN_PAGE);
       }
     }
   };
   int issued = 0;
   for (; issued < kStages && issued < mine; ++issued) issue(issued);
 
-  // q's fragments, split into their terms: in shared memory in the order the
-  // lanes read them, or with one m-tile in registers.
-  uint4* const qs = reinterpret_cast<uint4*>(smem + F::kSmemQ);
-  for (int e = warp; e < MT * 4; e += kWarps) {  // (m-tile, 16 dims)
-    const int mt = e >> 2, j = e & 3;
-    float x[2][4];  // rows g and g + 8
+  // q's fragments, split into their terms once for the block, in the order the
+  // lanes read them; then in registers.
+  uint4* const qs = reinterpret_cast<uint4*>(smem + kSmemQ);
+  {
+    const int j = warp;  // 16 dims
+    float x[2][4];       // rows g and g + 8, dims 4c .. 4c + 3
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int i = 4 * mt + 2 * h + (g >> 2);
-      const float* src = a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (g & 3)) * kD + 16 * j;
-      if (i < nrows) {
-        if constexpr (kBf16) {  // dims 2c, 2c+1, 2c+8, 2c+9
-          const float2 u = __ldg(reinterpret_cast<const float2*>(src + 2 * c));
-          const float2 v = __ldg(reinterpret_cast<const float2*>(src + 2 * c + 8));
-          x[h][0] = u.x, x[h][1] = u.y, x[h][2] = v.x, x[h][3] = v.y;
-        } else {  // dims 4c .. 4c + 3
-          const float4 u = __ldg(reinterpret_cast<const float4*>(src + 4 * c));
-          x[h][0] = u.x, x[h][1] = u.y, x[h][2] = u.z, x[h][3] = u.w;
-        }
-      } else {
-        x[h][0] = x[h][1] = x[h][2] = x[h][3] = 0.f;
-      }
+      const int i = 2 * h + (g >> 2);
+      float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < nrows)
+        u = __ldg(reinterpret_cast<const float4*>(a.q + ((size_t)(seq.first + i) * kHQ + head * kGroup + (g & 3)) * kD +
+                                                  16 * j + 4 * c));
+      x[h][0] = u.x, x[h][1] = u.y, x[h][2] = u.z, x[h][3] = u.w;
     }
-    if constexpr (kBf16) {
-      uint32_t t[3][4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          split3(x[h][2 * u], x[h][2 * u + 1], t[0][2 * u + h], t[1][2 * u + h], t[2][2 * u + h]);
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-        qs[((mt * 4 + j) * 3 + k) * 32 + lane] = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {  // k-step 2 j + u: k = c is dim 4c + 2u, k = c + 4 the next
-        uint4* dst = qs + ((mt * 8 + 2 * j + u) * 2) * 32 + lane;
-        dst[0] = make_uint4(hi_of(x[0][2 * u]), hi_of(x[1][2 * u]), hi_of(x[0][2 * u + 1]), hi_of(x[1][2 * u + 1]));
-        dst[32] = make_uint4(lo_of(x[0][2 * u]), lo_of(x[1][2 * u]), lo_of(x[0][2 * u + 1]), lo_of(x[1][2 * u + 1]));
-      }
+    for (int u = 0; u < 2; ++u) {  // k-step 2 j + u: k = c is dim 4c + 2u, k = c + 4 the next
+      uint4* dst = qs + ((2 * j + u) * 2) * 32 + lane;
+      dst[0] = make_uint4(hi_of(x[0][2 * u]), hi_of(x[1][2 * u]), hi_of(x[0][2 * u + 1]), hi_of(x[1][2 * u + 1]));
+      dst[32] = make_uint4(lo_of(x[0][2 * u]), lo_of(x[1][2 * u]), lo_of(x[0][2 * u + 1]), lo_of(x[1][2 * u + 1]));
     }
   }
   __syncthreads();
-  uint4 qreg[MT == 1 ? F::kSteps * F::kTerms : 1];
-  if constexpr (MT == 1) {
+  uint4 qreg[2 * kSteps];
 #pragma unroll
-    for (int e = 0; e < F::kSteps * F::kTerms; ++e) qreg[e] = qs[e * 32 + lane];
-  }
-  auto qfrag = [&](int mt, int step, int term, uint32_t (&r)[4]) {
-    uint4 v;
-    if constexpr (MT == 1) v = qreg[step * F::kTerms + term];
-    else v = qs[((mt * F::kSteps + step) * F::kTerms + term) * 32 + lane];
+  for (int e = 0; e < 2 * kSteps; ++e) qreg[e] = qs[e * 32 + lane];
+  auto qfrag = [&](int step, int term, uint32_t (&r)[4]) {
+    const uint4 v = qreg[step * 2 + term];
     r[0] = v.x, r[1] = v.y, r[2] = v.z, r[3] = v.w;
   };
 
-  // State of this warp's partial: rows g and g + 8 of every m-tile. The sums
-  // are this lane's columns' alone until the end.
-  float top[MT][2], sum[MT][2], o[MT][8][4];
+  // State of this warp's partial: rows g and g + 8. The sums are this lane's
+  // columns' alone until the end.
+  float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f}, o[8][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    top[mt][0] = top[mt][1] = -INFINITY;
-    sum[mt][0] = sum[mt][1] = 0.f;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) o[mt][u][0] = o[mt][u][1] = o[mt][u][2] = o[mt][u][3] = 0.f;
-  }
+  for (int u = 0; u < 8; ++u) o[u][0] = o[u][1] = o[u][2] = o[u][3] = 0.f;
 
   bool failed = false;
   int n = 0;
@@ -252,263 +197,154 @@ tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUte
       failed = true;
       break;
     }
-    const uint8_t* kt = ring + st * F::kStage;
-    const uint8_t* vt = kt + F::kBoxes * F::kBox;
+    const uint8_t* kt = ring + st * kStage;
+    const uint8_t* vt = kt + 2 * kBox;
     const int t0 = k0 + (warp + n * kWarps) * ATTN_PAGE;
     const bool tail = t0 + ATTN_PAGE > seq.ctx;  // holds drafted keys, or slots past them
 
-    // Scores: sc[mt][nt], columns 2c and 2c + 1 of 8-key group nt. Column n is
-    // key turn(n) of the group (fp32 pages) or key n (bf16 pages).
-    float sc[MT][2][4];
+    // Scores: sc[nt], columns 2c and 2c + 1 of 8-key group nt. Column n is key
+    // turn(n) of the group.
+    float sc[2][4];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt) {
+      sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      float low[4] = {0.f, 0.f, 0.f, 0.f};  // the small terms' own chain
+      const int r = nt * 8 + turn(g);
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.f;
-      float low[MT][4];  // the small terms' own chain
+      for (int j = 0; j < 4; ++j) {
+        const float4 x = *reinterpret_cast<const float4*>(kt + (j >> 1) * kBox + r * 128 +
+                                                          ((((j & 1) * 4 + c) ^ (r & 7)) << 4));
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) low[mt][0] = low[mt][1] = low[mt][2] = low[mt][3] = 0.f;
-      if constexpr (kBf16) {
-        uint32_t kb[2][4];
-        const int r = nt * 8 + (lane & 7);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          ldsm4(kb[h], tc::smem_u32(kt) + r * 128 + (((h * 4 + (lane >> 3)) ^ (r & 7)) << 4));
-#pragma unroll
-        for (int st4 = 0; st4 < 4; ++st4) {
-          const uint32_t b0 = kb[st4 >> 1][(st4 & 1) * 2], b1 = kb[st4 >> 1][(st4 & 1) * 2 + 1];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int k = 2; k >= 0; --k) {
-              uint32_t qa[4];
-              qfrag(mt, st4, k, qa);
-              mma_bf16(k ? low[mt] : sc[mt][nt], qa, b0, b1);
-            }
-        }
-      } else {
-        const int r = nt * 8 + turn(g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float4 x = *reinterpret_cast<const float4*>(kt + (j >> 1) * F::kBox + r * 128 +
-                                                            ((((j & 1) * 4 + c) ^ (r & 7)) << 4));
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float e0 = u ? x.z : x.x, e1 = u ? x.w : x.y;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              uint32_t qh[4], ql[4];
-              qfrag(mt, 2 * j + u, 0, qh);
-              qfrag(mt, 2 * j + u, 1, ql);
-              mma_tf32(low[mt], ql, hi_of(e0), hi_of(e1));
-              mma_tf32(low[mt], qh, lo_of(e0), lo_of(e1));
-              mma_tf32(sc[mt][nt], qh, hi_of(e0), hi_of(e1));
-            }
-          }
+        for (int u = 0; u < 2; ++u) {
+          const float e0 = u ? x.z : x.x, e1 = u ? x.w : x.y;
+          uint32_t qh[4], ql[4];
+          qfrag(2 * j + u, 0, qh);
+          qfrag(2 * j + u, 1, ql);
+          mma_tf32(low, ql, hi_of(e0), hi_of(e1));
+          mma_tf32(low, qh, lo_of(e0), lo_of(e1));
+          mma_tf32(sc[nt], qh, hi_of(e0), hi_of(e1));
         }
       }
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) add4(sc[mt][nt], low[mt]);
+      add4(sc[nt], low);
     }
 
     if (tail) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int col = 2 * c + (e & 1);
-            const int pos = t0 + nt * 8 + (kBf16 ? col : turn(col));
-            const int at = pos - seq.ctx;
-            const bool seen = pos < k1 && (at < 0 || (masks[4 * mt + 2 * (e >> 1) + (g >> 2)] >> at & 1));
-            if (!seen) sc[mt][nt][e] = -INFINITY;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int pos = t0 + nt * 8 + turn(2 * c + (e & 1));
+          const int at = pos - seq.ctx;
+          const bool seen = pos < k1 && (at < 0 || (masks[2 * (e >> 1) + (g >> 2)] >> at & 1));
+          if (!seen) sc[nt][e] = -INFINITY;
+        }
     }
 
     // Does a score pass its row's reference by more than 2^8? (Any score does
     // while the reference is -inf.)
     bool over = false;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float most = fmaxf(fmaxf(sc[mt][0][2 * h], sc[mt][0][2 * h + 1]),
-                                 fmaxf(sc[mt][1][2 * h], sc[mt][1][2 * h + 1]));
-        over |= most * kC > top[mt][h] + kStale;
-      }
+    for (int h = 0; h < 2; ++h) {
+      const float most = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+      over |= most * kC > top[h] + kStale;
+    }
     if (__any_sync(kFull, over)) {
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+      for (int h = 0; h < 2; ++h) {
+        float most = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
+        most = fmaxf(most, __shfl_xor_sync(kFull, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(kFull, most, 2));
+        const float next = fmaxf(top[h], most * kC);
+        const float alpha = next == -INFINITY ? 1.f : ex2(top[h] - next);
+        top[h] = next;
+        sum[h] *= alpha;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float most = fmaxf(fmaxf(sc[mt][0][2 * h], sc[mt][0][2 * h + 1]),
-                             fmaxf(sc[mt][1][2 * h], sc[mt][1][2 * h + 1]));
-          most = fmaxf(most, __shfl_xor_sync(kFull, most, 1));
-          most = fmaxf(most, __shfl_xor_sync(kFull, most, 2));
-          const float next = fmaxf(top[mt][h], most * kC);
-          const float alpha = next == -INFINITY ? 1.f : ex2(top[mt][h] - next);
-          top[mt][h] = next;
-          sum[mt][h] *= alpha;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            o[mt][u][2 * h] *= alpha;
-            o[mt][u][2 * h + 1] *= alpha;
-          }
+        for (int u = 0; u < 8; ++u) {
+          o[u][2 * h] *= alpha;
+          o[u][2 * h + 1] *= alpha;
         }
+      }
     }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int h = 0; h < 2; ++h) {
+      const float ref = top[h] == -INFINITY ? 0.f : top[h];  // a row that has seen no key yet
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float ref = top[mt][h] == -INFINITY ? 0.f : top[mt][h];  // a row that has seen no key yet
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 2 * h; e < 2 * h + 2; ++e) {
-            sc[mt][nt][e] = ex2(fmaf(sc[mt][nt][e], kC, -ref));
-            sum[mt][h] += sc[mt][nt][e];
-          }
-      }
+        for (int e = 2 * h; e < 2 * h + 2; ++e) {
+          sc[nt][e] = ex2(fmaf(sc[nt][e], kC, -ref));
+          sum[h] += sc[nt][e];
+        }
+    }
 
     // Drafted values that are not finite reach only the rows that see them; a
     // product with a zero probability would spread NaN. They are taken out of
     // the operand and added row by row. Slots past the last key count as zeros.
-    if constexpr (kBf16) {
-      uint32_t pf[MT][3][4];
+    bool odd = false;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+    for (int hh = 0; hh < 2; ++hh) {
+      float va[2][2][4];  // keys c and c + 4 of each group, dims 32 hh + 4 turn(g) ..
 #pragma unroll
-        for (int e = 0; e < 4; ++e)  // a0 a1: group 0, rows g and g + 8; a2 a3: group 1
-          split3(sc[mt][e >> 1][(e & 1) * 2], sc[mt][e >> 1][(e & 1) * 2 + 1], pf[mt][0][e], pf[mt][1][e],
-                 pf[mt][2][e]);
-      bool odd = false;
+      for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {  // 16 dims: two n-tiles
-        uint32_t vb[4];
-        const int r = ((lane >> 3) & 1) * 8 + (lane & 7);
-        ldsm4_t(vb, tc::smem_u32(vt) + r * 128 + (((2 * j + (lane >> 4)) ^ (r & 7)) << 4));
-        if (tail) {
+        for (int y = 0; y < 2; ++y) {
+          const int r = nt * 8 + c + 4 * y;
+          const float4 x = *reinterpret_cast<const float4*>(vt + hh * kBox + r * 128 + ((turn(g) ^ (r & 7)) << 4));
+          va[nt][y][0] = x.x, va[nt][y][1] = x.y, va[nt][y][2] = x.z, va[nt][y][3] = x.w;
+          if (tail) {
+            const int pos = t0 + r;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int pos = t0 + (e & 1) * 8 + 2 * c;
-            if ((vb[e] & 0x7f80u) == 0x7f80u) odd |= pos < k1 && pos >= seq.ctx;
-            if ((vb[e] & 0x7f800000u) == 0x7f800000u) odd |= pos + 1 < k1 && pos + 1 >= seq.ctx;
-            if (pos >= k1 || (pos >= seq.ctx && (vb[e] & 0x7f80u) == 0x7f80u)) vb[e] &= 0xffff0000u;
-            if (pos + 1 >= k1 || (pos + 1 >= seq.ctx && (vb[e] & 0x7f800000u) == 0x7f800000u)) vb[e] &= 0xffffu;
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float x0[4] = {0.f, 0.f, 0.f, 0.f}, x1[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 2; k >= 0; --k) {
-            mma_bf16(x0, pf[mt][k], vb[0], vb[1]);
-            mma_bf16(x1, pf[mt][k], vb[2], vb[3]);
-          }
-          add4(o[mt][2 * j], x0);
-          add4(o[mt][2 * j + 1], x1);
-        }
-      }
-      if (tail && __any_sync(kFull, odd)) {
-#pragma unroll 1
-        for (int key = 0; key < ATTN_PAGE; ++key) {
-          const int at = t0 + key - seq.ctx;
-          if (at < 0 || t0 + key >= k1) continue;
-          const int from = (lane & ~3) | ((key & 7) >> 1);  // the lane of this row's column `key`
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float p0 = __shfl_sync(kFull, key < 8 ? sc[mt][0][2 * h] : sc[mt][1][2 * h], from);
-              const float p1 = __shfl_sync(kFull, key < 8 ? sc[mt][0][2 * h + 1] : sc[mt][1][2 * h + 1], from);
-              const float p = (key & 1) ? p1 : p0;
-              const bool seen = masks[4 * mt + 2 * h + (g >> 2)] >> at & 1;
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int d = 8 * u + 2 * c + e;
-                  const uint16_t raw = *reinterpret_cast<const uint16_t*>(
-                      vt + key * 128 + ((((d >> 3) ^ (key & 7)) << 4) | ((d & 7) * 2)));
-                  const float v = __uint_as_float((uint32_t)raw << 16);
-                  if (seen && !finite(v)) o[mt][u][2 * h + e] += p * v;
-                }
-            }
-        }
-      }
-    } else {
-      bool odd = false;
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        float va[2][2][4];  // keys c and c + 4 of each group, dims 32 hh + 4 turn(g) ..
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const int r = nt * 8 + c + 4 * y;
-            const float4 x =
-                *reinterpret_cast<const float4*>(vt + hh * F::kBox + r * 128 + ((turn(g) ^ (r & 7)) << 4));
-            va[nt][y][0] = x.x, va[nt][y][1] = x.y, va[nt][y][2] = x.z, va[nt][y][3] = x.w;
-            if (tail) {
-              const int pos = t0 + r;
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                if (pos >= k1) va[nt][y][u] = 0.f;
-                if (pos >= seq.ctx && !finite(va[nt][y][u])) {
-                  odd = true;
-                  va[nt][y][u] = 0.f;
-                }
+            for (int u = 0; u < 4; ++u) {
+              if (pos >= k1) va[nt][y][u] = 0.f;
+              if (pos >= seq.ctx && !finite(va[nt][y][u])) {
+                odd = true;
+                va[nt][y][u] = 0.f;
               }
             }
           }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          uint32_t ph[2][4], pl[2][4];
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {  // a0 a1: column 2c (key c), rows g, g + 8; a2 a3: column 2c + 1 (key c + 4)
-              const float p = sc[mt][nt][(e & 1) * 2 + (e >> 1)];
-              ph[nt][e] = hi_of(p);
-              pl[nt][e] = lo_of(p);
-            }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-              mma_tf32(x, pl[nt], hi_of(va[nt][0][u]), hi_of(va[nt][1][u]));
-              mma_tf32(x, ph[nt], lo_of(va[nt][0][u]), lo_of(va[nt][1][u]));
-            }
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) mma_tf32(x, ph[nt], hi_of(va[nt][0][u]), hi_of(va[nt][1][u]));
-            add4(o[mt][hh * 4 + u], x);
-          }
         }
+      uint32_t ph[2][4], pl[2][4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // a0 a1: column 2c (key c), rows g, g + 8; a2 a3: column 2c + 1 (key c + 4)
+          const float p = sc[nt][(e & 1) * 2 + (e >> 1)];
+          ph[nt][e] = hi_of(p);
+          pl[nt][e] = lo_of(p);
+        }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          mma_tf32(x, pl[nt], hi_of(va[nt][0][u]), hi_of(va[nt][1][u]));
+          mma_tf32(x, ph[nt], lo_of(va[nt][0][u]), lo_of(va[nt][1][u]));
+        }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) mma_tf32(x, ph[nt], hi_of(va[nt][0][u]), hi_of(va[nt][1][u]));
+        add4(o[hh * 4 + u], x);
       }
-      if (tail && __any_sync(kFull, odd)) {
+    }
+    if (tail && __any_sync(kFull, odd)) {
 #pragma unroll 1
-        for (int key = 0; key < ATTN_PAGE; ++key) {
-          const int at = t0 + key - seq.ctx;
-          if (at < 0 || t0 + key >= k1) continue;
-          const int from = (lane & ~3) | (key & 3);  // the lane of this row's columns of keys c and c + 4
+      for (int key = 0; key < ATTN_PAGE; ++key) {
+        const int at = t0 + key - seq.ctx;
+        if (at < 0 || t0 + key >= k1) continue;
+        const int from = (lane & ~3) | (key & 3);  // the lane of this row's columns of keys c and c + 4
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < 2; ++h) {
+          const float p0 = __shfl_sync(kFull, key < 8 ? sc[0][2 * h] : sc[1][2 * h], from);
+          const float p1 = __shfl_sync(kFull, key < 8 ? sc[0][2 * h + 1] : sc[1][2 * h + 1], from);
+          const float p = (key & 4) ? p1 : p0;
+          const bool seen = masks[2 * h + (g >> 2)] >> at & 1;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float p0 = __shfl_sync(kFull, key < 8 ? sc[mt][0][2 * h] : sc[mt][1][2 * h], from);
-              const float p1 = __shfl_sync(kFull, key < 8 ? sc[mt][0][2 * h + 1] : sc[mt][1][2 * h + 1], from);
-              const float p = (key & 4) ? p1 : p0;
-              const bool seen = masks[4 * mt + 2 * h + (g >> 2)] >> at & 1;
+          for (int u = 0; u < 8; ++u)
 #pragma unroll
-              for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int chunk = c + 4 * e;  // turn(2c + e)
-                  const float v = *reinterpret_cast<const float*>(vt + (u >> 2) * F::kBox + key * 128 +
-                                                                  ((chunk ^ (key & 7)) << 4) + (u & 3) * 4);
-                  if (seen && !finite(v)) o[mt][u][2 * h + e] += p * v;
-                }
+            for (int e = 0; e < 2; ++e) {
+              const int chunk = c + 4 * e;  // turn(2c + e)
+              const float v = *reinterpret_cast<const float*>(vt + (u >> 2) * kBox + key * 128 +
+                                                              ((chunk ^ (key & 7)) << 4) + (u & 3) * 4);
+              if (seen && !finite(v)) o[u][2 * h + e] += p * v;
             }
         }
       }
@@ -530,75 +366,65 @@ tree_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUte
   float* const acc = reinterpret_cast<float*>(ring);
   auto acc_at = [](int row, int d) { return row * kD + ((((d >> 2) ^ row) & 7) | ((d >> 2) & 8)) * 4 + (d & 3); };
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+  for (int h = 0; h < 2; ++h) {
+    const int row = 8 * h + g;
+    sum[h] += __shfl_xor_sync(kFull, sum[h], 1);
+    sum[h] += __shfl_xor_sync(kFull, sum[h], 2);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int row = 16 * mt + 8 * h + g;
-      sum[mt][h] += __shfl_xor_sync(kFull, sum[mt][h], 1);
-      sum[mt][h] += __shfl_xor_sync(kFull, sum[mt][h], 2);
-      if constexpr (kBf16) {
+    for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-          *reinterpret_cast<float2*>(acc + acc_at(row, 8 * u + 2 * c)) =
-              make_float2(o[mt][u][2 * h], o[mt][u][2 * h + 1]);
-      } else {
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            *reinterpret_cast<float4*>(acc + acc_at(row, 32 * hh + 16 * e + 4 * c)) =
-                make_float4(o[mt][4 * hh][2 * h + e], o[mt][4 * hh + 1][2 * h + e], o[mt][4 * hh + 2][2 * h + e],
-                            o[mt][4 * hh + 3][2 * h + e]);
-      }
-    }
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<float4*>(acc + acc_at(row, 32 * hh + 16 * e + 4 * c)) =
+            make_float4(o[4 * hh][2 * h + e], o[4 * hh + 1][2 * h + e], o[4 * hh + 2][2 * h + e],
+                        o[4 * hh + 3][2 * h + e]);
+  }
   const bool any_failed = __syncthreads_or(failed);  // and q's fragments are no longer read
-  float2* const ml = reinterpret_cast<float2*>(smem + F::kSmemQ);  // [warp][row]
+  float2* const ml = reinterpret_cast<float2*>(smem + kSmemQ);  // [warp][row]
   if (c == 0) {
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        ml[warp * 16 * MT + 16 * mt + 8 * h + g] = make_float2(top[mt][h], sum[mt][h]);
+    for (int h = 0; h < 2; ++h) ml[warp * kRows + 8 * h + g] = make_float2(top[h], sum[h]);
   }
   __syncthreads();
+  float* const rows = reinterpret_cast<float*>(smem + kSmemRows);
+  float2* const ends = reinterpret_cast<float2*>(smem + kSmemEnds);
   for (int e = tid; e < nrows * kGroup * 16; e += 32 * kWarps) {  // (row, 16-byte chunk)
     const int row = e >> 4, d = (e & 15) * 4;
     float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * 16 * MT + row].x);
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w * kRows + row].x);
     float den = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 p = ml[w * 16 * MT + row];
+      const float2 p = ml[w * kRows + row];
       // A warp that saw no key of the row has no weight; a sum that is NaN (a
       // row whose scores are) stays NaN.
       const float wt = p.x == -INFINITY ? 0.f : ex2(p.x - m);
       den = fmaf(wt, p.y, den);
       if (wt == 0.f) continue;
-      const float4 y = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(smem + w * (kStages * F::kStage)) + acc_at(row, d));
+      const float4 y =
+          *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * (kStages * kStage)) + acc_at(row, d));
       x.x = fmaf(wt, y.x, x.x);
       x.y = fmaf(wt, y.y, x.y);
       x.z = fmaf(wt, y.z, x.z);
       x.w = fmaf(wt, y.w, x.w);
     }
-    const size_t at = (size_t)(seq.first + i0 + row / kGroup) * kHQ + head * kGroup + row % kGroup;
-    if (whole) {
+    const size_t at = (size_t)(seq.first + row / kGroup) * kHQ + head * kGroup + row % kGroup;
+    // after a failed wait the segment counts as empty
+    const float2 end = any_failed ? make_float2(-INFINITY, 0.f) : make_float2(m, den);
+    if (a.cluster) {
+      *reinterpret_cast<float4*>(rows + row * kRowStride + d) = x;
+      if (d == 0) ends[row] = end;
+    } else if (whole) {
       if (any_failed) continue;  // left unwritten
       const float inv = den == 0.f ? 0.f : 1.f / den;  // no key: zeros
       *reinterpret_cast<float4*>(a.out + at * kD + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
     } else {
-      // after a failed wait the segment counts as empty
-      float* part = a.parts + (at * a.splits + s) * kD + d;
-      *reinterpret_cast<float4*>(part) = x;
-      if (d == 0) {
-        float2* mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
-        mls[at * a.splits + s] = any_failed ? make_float2(-INFINITY, 0.f) : make_float2(m, den);
-      }
+      *reinterpret_cast<float4*>(a.parts + (at * a.splits + s) * kD + d) = x;
+      if (d == 0) reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD)[at * a.splits + s] = end;
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.cluster) cluster_merge(a, seq.first, nrows, head, rows, kRowStride, ends, tid, 32 * kWarps);
 }
 
 // Merge: block (drafted row, sequence), a warp per four heads in turn, two dims a lane.
@@ -679,22 +505,23 @@ int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtenso
   return ATTN_OK;
 }
 
+// Variants by page type and drafted rows: up to 4, up to 8, more. Measured on 16
+// sequences of 16384 tokens: bf16 pages, 8 rows, tree_tc 101 us and tree_wide 140;
+// 16 rows, 175 (as two tiles of 8: 200) and 143. fp32 pages, 4 rows, the kernel here
+// 205 us and tree_wide 250; 8 rows, 312 and 250.
 using Variant = TreeVariant;
-template <bool kBf16, int MT>
-Variant make_variant() {
-  return {tree_kernel<kBf16, MT>, 4 * MT, 32 * Cfg<kBf16, MT>::kWarps, Cfg<kBf16, MT>::kSmemAlloc,
-          Cfg<kBf16, MT>::kBlocks, false, 0};
-}
-const Variant kVariants[2][3] = {
-    {make_variant<false, 1>(), tree_wide_variant(false), tree_wide_variant(false)},
-    {tree_tc_variant(true, 0), tree_tc_variant(true, 1), tree_wide_variant(true)}};
+const Variant kNarrow = {tree_narrow_kernel, 4, 32 * kWarps, kSmemAlloc, kBlocks, false, 0};
+const Variant kVariants[2][3] = {{kNarrow, tree_wide_variant(false), tree_wide_variant(false)},
+                                 {tree_tc_variant(4), tree_tc_variant(8), tree_wide_variant(true)}};
 
 int variant_of(int max_rows) { return max_rows <= 4 ? 0 : max_rows <= 8 ? 1 : 2; }
 
-// Per device: the shared-memory opt-ins and how many blocks of each variant fit at once.
+// Per device and variant: how many blocks fit at once, and how many clusters of
+// each size.
 struct TreeDevice {
   bool ready = false;
   int slots[2][3] = {};
+  int clusters[2][3][kMaxCluster + 1] = {};
 };
 int tree_device(TreeDevice** out) {
   constexpr int kMaxDev = 64;
@@ -718,6 +545,25 @@ int tree_device(TreeDevice** out) {
           if (fa.numRegs < x.regs) return ATTN_ELAUNCH;
         }
         d.slots[t][v] = sms * x.blocks;
+        for (int size = 2; size <= kMaxCluster; ++size) {
+          cudaLaunchConfig_t cfg = {};
+          cfg.gridDim = dim3(size, kHKV);
+          cfg.blockDim = dim3(x.threads);
+          cfg.dynamicSmemBytes = x.smem;
+          cudaLaunchAttribute attr[1];
+          attr[0].id = cudaLaunchAttributeClusterDimension;
+          attr[0].val.clusterDim.x = size;
+          attr[0].val.clusterDim.y = 1;
+          attr[0].val.clusterDim.z = 1;
+          cfg.attrs = attr;
+          cfg.numAttrs = 1;
+          int n = 0;
+          if (cudaOccupancyMaxActiveClusters(&n, x.kernel, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;  // no such clusters: segments merge through memory
+          }
+          d.clusters[t][v][size] = n;
+        }
       }
     d.ready = true;
   }
@@ -727,17 +573,19 @@ int tree_device(TreeDevice** out) {
 
 }  // namespace
 
-int tree_splits(bool bf16, int B, int max_rows, int max_context, int splits_hint, int* splits, int* split_len) {
+int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, TreePlan* plan) {
   TreeDevice* d = nullptr;
   const int rc = tree_device(&d);
   if (rc != ATTN_OK) return rc;
   const int v = variant_of(max_rows);
+  const int* const clusters = d->clusters[bf16][v];
   const int keys = max_context + max_rows;
   int n = splits_hint < kMaxSplits ? splits_hint : kMaxSplits;
   if (n <= 0) {
-    // The segments that take the least time: rounds of resident blocks, each as
-    // long as its tiles of 128 keys and what a block costs besides them (measured:
-    // six tiles' time), and the merge of several (three).
+    // The segments that take the least time, counted in tiles of 128 keys: rounds
+    // of resident blocks, each as long as its tiles and what a block costs besides
+    // them (measured: six tiles' time), and the merge (two in a cluster, five
+    // through memory and a second kernel).
     const int tokens = kVariants[bf16][v].tokens, slots = d->slots[bf16][v];
     const long long units = (long long)B * kHKV * ((max_rows + tokens - 1) / tokens);
     const int tiles = (keys + 127) / 128;
@@ -745,8 +593,9 @@ int tree_splits(bool bf16, int B, int max_rows, int max_context, int splits_hint
     long long best = 0;
     n = 1;
     for (int s = 1; s <= limit; ++s) {
-      const long long rounds = (units * s + slots - 1) / slots;
-      const long long cost = rounds * ((tiles + s - 1) / s + 6) + (s > 1 ? 3 : 0);
+      const bool cluster = s > 1 && s <= kMaxCluster && clusters[s] > 0;
+      const long long rounds = cluster ? (units + clusters[s] - 1) / clusters[s] : (units * s + slots - 1) / slots;
+      const long long cost = rounds * ((tiles + s - 1) / s + 6) + (s == 1 ? 0 : cluster ? 2 : 5);
       if (s == 1 || cost < best) {
         best = cost;
         n = s;
@@ -754,13 +603,14 @@ int tree_splits(bool bf16, int B, int max_rows, int max_context, int splits_hint
     }
   }
   const int per = (keys + n - 1) / n;
-  *split_len = (per + 127) / 128 * 128;
-  *splits = (keys + *split_len - 1) / *split_len;
+  plan->split_len = (per + 127) / 128 * 128;
+  plan->splits = (keys + plan->split_len - 1) / plan->split_len;
+  plan->cluster = plan->splits > 1 && plan->splits <= kMaxCluster && clusters[plan->splits] > 0;
   return ATTN_OK;
 }
 
-size_t tree_workspace_bytes(int N, int splits) {
-  return splits <= 1 ? 0 : (size_t)N * kHQ * splits * (kD + 2) * sizeof(float);
+size_t tree_workspace_bytes(int N, const TreePlan& plan) {
+  return plan.splits <= 1 || plan.cluster ? 0 : (size_t)N * kHQ * plan.splits * (kD + 2) * sizeof(float);
 }
 
 int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
@@ -768,29 +618,43 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
   int rc = tree_device(&d);
   if (rc != ATTN_OK) return rc;
   const bool bf16 = c.type == ATTN_BF16;
-  alignas(64) CUtensorMap mk, mv;
   const Variant& x = kVariants[bf16][variant_of(c.max_rows)];
+  alignas(64) CUtensorMap mk, mv;
   if ((rc = encode_pool(c.k_pages, c.num_pages, bf16, false, &mk)) != ATTN_OK ||
       (rc = encode_pool(c.v_pages, c.num_pages, bf16, x.v_atom32, &mv)) != ATTN_OK)
     return rc;
-  const TreeArgs a{c.q, c.k_pages, c.v_pages, c.table, c.ctx_lens, c.row_start, c.masks, c.out, c.splits > 1 ? c.parts : nullptr,
-                   c.B, c.N, c.max_rows, c.max_blocks, c.num_pages, c.max_context, c.split_len, c.splits,
-                   err, 2000000000ull};
+  const TreePlan& p = c.plan;
+  const TreeArgs a{c.q, c.k_pages, c.v_pages, c.table, c.ctx_lens, c.row_start, c.masks, c.out, c.parts,
+                   c.B, c.N, c.max_rows, c.max_blocks, c.num_pages, c.max_context, p.split_len, p.splits,
+                   p.cluster, err, 2000000000ull};
   const int row_tiles = (c.max_rows + x.tokens - 1) / x.tokens;
-  x.kernel<<<dim3(c.splits, kHKV * row_tiles, c.B), x.threads, x.smem, stream>>>(mk, mv, a);
-  if (cudaGetLastError() != cudaSuccess) return ATTN_ELAUNCH;
-  if (c.splits > 1) {
-    // The merge starts as the split blocks leave (programmatic dependent launch).
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(c.max_rows, c.B);
-    cfg.blockDim = dim3(32 * kMergeWarps);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.splits, kHKV * row_tiles, c.B);
+  cfg.blockDim = dim3(x.threads);
+  cfg.dynamicSmemBytes = x.smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  cfg.attrs = attr;
+  if (p.cluster) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 1;
+  }
+  if (cudaLaunchKernelEx(&cfg, x.kernel, mk, mv, a) != cudaSuccess) return ATTN_ELAUNCH;
+  if (p.splits > 1 && !p.cluster) {
+    // The merge's blocks start as this grid's last ones run (programmatic
+    // dependent launch) and wait for its end.
+    cudaLaunchConfig_t mcfg = {};
+    mcfg.gridDim = dim3(c.max_rows, c.B);
+    mcfg.blockDim = dim3(32 * kMergeWarps);
+    mcfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, tree_merge_kernel, a) != cudaSuccess) return ATTN_ELAUNCH;
+    mcfg.attrs = attr;
+    mcfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&mcfg, tree_merge_kernel, a) != cudaSuccess) return ATTN_ELAUNCH;
   }
   return ATTN_OK;
 }

@@ -23,6 +23,7 @@ struct TreeArgs {
   float* out;                // [N][32][64]
   float* parts;              // [N][32][splits][64], then [N][32][splits][2] (log2 maximum, sum)
   int B, N, max_rows, max_blocks, num_pages, max_context, split_len, splits;
+  int cluster;               // the segments of a unit are one cluster and merge in shared memory
   unsigned* err;
   unsigned long long timeout_ns;
 };
@@ -127,6 +128,71 @@ struct Wait {
   }
 };
 
+// The segments of a unit as one cluster of blocks, up to kMaxCluster of them:
+// each leaves its rows ([4 nrows][stride], 64 used) and their (log2 maximum, sum)
+// in its own shared memory, and after a barrier of the cluster every block merges
+// and writes its share of the rows. No partial goes through memory, and no second
+// kernel waits for the first. Every block of a cluster comes here, also one
+// without keys or with a failed wait (its sums are then empty): none may leave
+// while another reads its shared memory. Called by the first `threads` threads
+// of every block; the others have left.
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ void cluster_merge(const TreeArgs& a, int first_row, int nrows, int head,
+                                              const float* rows, int stride, const float2* ml, int tid,
+                                              int threads) {
+  __syncwarp();
+  tc::cluster_sync_all();
+  for (int e = blockIdx.x * threads + tid; e < nrows * kGroup * 16; e += a.splits * threads) {  // (row, 4 dims)
+    const int r = e >> 4, d = (e & 15) * 4;
+    const uint32_t ml_at = tc::smem_u32(ml + r), row_at = tc::smem_u32(rows + r * stride + d);
+    float2 p[kMaxCluster];
+    float4 y[kMaxCluster];
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s)
+      if (s < a.splits) {
+        p[s] = ld_cluster2(tc::mapa_shared(ml_at, s));
+        y[s] = ld_cluster4(tc::mapa_shared(row_at, s));
+      }
+    float m = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s)
+      if (s < a.splits) m = fmaxf(m, p[s].x);
+    float den = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s)
+      if (s < a.splits) {
+        const float w = p[s].x == -INFINITY ? 0.f : ex2(p[s].x - m);
+        den = fmaf(w, p[s].y, den);
+        if (w != 0.f) {  // an empty segment's rows have no weight, whatever they hold
+          x.x = fmaf(w, y[s].x, x.x);
+          x.y = fmaf(w, y[s].y, x.y);
+          x.z = fmaf(w, y[s].z, x.z);
+          x.w = fmaf(w, y[s].w, x.w);
+        }
+      }
+    const float inv = den == 0.f ? 0.f : 1.f / den;  // no key: zeros
+    *reinterpret_cast<float4*>(a.out + ((size_t)(first_row + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * kD + d) =
+        make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  }
+  __syncwarp();
+  tc::cluster_sync_all();
+}
+
 // A kernel of the family: drafted rows a block takes, threads, shared memory,
 // resident blocks of an SM.
 struct TreeVariant {
@@ -137,7 +203,7 @@ struct TreeVariant {
   bool v_atom32;  // fp32 V in the 128-byte swizzle of 32-byte chunks
   int regs;       // registers a thread at least at launch (what its register split adds up to)
 };
-TreeVariant tree_tc_variant(bool bf16, int which);  // 0, 1, 2: 4, 8, 16 drafted rows a block
-TreeVariant tree_wide_variant(bool bf16);           // 32 drafted rows a block
+TreeVariant tree_tc_variant(int tokens);   // bf16 pages, 4 or 8 drafted rows a block
+TreeVariant tree_wide_variant(bool bf16);  // 32 drafted rows a block
 
 }  // namespace attn

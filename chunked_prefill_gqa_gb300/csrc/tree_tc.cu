@@ -7,7 +7,7 @@
 // keep them in fp32 precision cost narrow instructions, or stack along N:
 //   S^T [128 keys][R] = K [128][64] . (q3, q2, q1)^T         12 MMAs of N = R
 //   O^T [64 dims][3 R] += V^T [64][128] . [p1 | p2 | p3]      8 MMAs of N = 3 R
-// with R = 4 x the drafted rows of a block (16, 32 or 64 columns). K is a
+// with R = 4 x the drafted rows of a block (16 or 32 columns). K is a
 // K-major operand as it lies in the page, V^T an MN-major one, also as it lies;
 // nothing of the cache is converted or transposed. p goes through shared memory,
 // written by the thread that owns its key: one row of N per key, which is an
@@ -44,44 +44,42 @@ using namespace tc;
 constexpr int kKeys = 128;                          // keys of a tile: M of S^T
 constexpr int kPages = kKeys / ATTN_PAGE;
 constexpr uint32_t kOperand = kKeys * kD * 2;       // 16 KB: a tile of K, of V, or an N atom of p
+constexpr uint32_t kStageBytes = 2 * kOperand;
 constexpr uint32_t kBox = ATTN_PAGE * 128;
 
 constexpr int kCols = 16;                           // columns of a softmax thread
 constexpr int kFlush = 4;                           // tiles between two flushes of O
 
-constexpr int kConvWarps = 8;                       // fp32 pages: load and split K and V
-constexpr int kUnits = kKeys * 8 / (32 * kConvWarps);  // (key, 8 dims) of an operand a thread splits
+constexpr int kStages = 2;
+constexpr int kRowStride = kD + 4;                  // floats, for rows written a row a thread
 
-template <bool kF32, int R>
+template <int R>
 struct Lay {
   static constexpr int kParts = R / kCols;          // warps on one lane quarter
   static constexpr int kSoft = 4 * kParts;          // softmax warps
-  static constexpr int kLoadWarps = kF32 ? kConvWarps : 1;
-  static constexpr int kMmaWarp = kSoft + kLoadWarps;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  static constexpr int kBlocks = kF32 || R == 64 ? 1 : 2;  // per SM
-  static constexpr int kStages = kF32 ? 1 : R == 64 ? 4 : 2;
-  static constexpr int kTerms = kF32 ? 3 : 1;       // of K and V
-  static constexpr uint32_t kStageBytes = 2 * kTerms * kOperand;     // K's terms, then V's
+  static constexpr int kTmaWarp = kSoft, kMmaWarp = kSoft + 1;
+  static constexpr int kThreads = 32 * (kSoft + 2);
+  static constexpr int kBlocks = 2;                 // per SM
   static constexpr int kN = 3 * R;
   static constexpr uint32_t kColS = 0, kColO = 2 * R;                // two S buffers, then O's three terms
-  static constexpr uint32_t kTmem = R == 64 ? 512 : R == 32 ? 256 : 128;
+  static constexpr uint32_t kTmem = R == 32 ? 256 : 128;
   static constexpr uint32_t kSmemQ = kStages * kStageBytes;          // [3 R rows][128 bytes]
-  static constexpr uint32_t kSmemP = kSmemQ + ((kN * 128 + 1023) / 1024) * 1024;
-  // O so far, [R][64] fp32: for 64 rows its own 16 KB; for 32 and 16 the bytes
-  // that the last atom of p leaves free in each of its 128 rows (64 or 32: just
-  // as many), so that two blocks fit an SM.
-  static constexpr uint32_t kFree = R == 64 ? 0 : 4 * R / 2;
-  static constexpr uint32_t kSmemAcc = kSmemP + (R == 64 ? 3 : (kN + 63) / 64 - 1) * kOperand;
+  static constexpr uint32_t kSmemP = kSmemQ + kN * 128;
+  // O so far, [R][64] fp32, in the bytes that the last atom of p leaves free in
+  // each of its 128 rows (2 R of 128: just as many), so that two blocks fit an SM.
+  static constexpr uint32_t kFree = 2 * R;
+  static constexpr uint32_t kSmemAcc = kSmemP + ((kN + 63) / 64 - 1) * kOperand;
   static constexpr uint32_t kSmemMask = kSmemAcc + kOperand;
-  static_assert(R == 64 ? R * kD * 4 == kOperand : kKeys * kFree == R * kD * 4 && (kN % 64) * 2 + kFree <= 128, "acc");
+  static_assert(kKeys * kFree == R * kD * 4 && (kN % 64) * 2 + kFree <= 128 && kSmemP % 1024 == 0, "acc");
   static constexpr uint32_t kSmemMax = kSmemMask + (R / 4) * 8;      // [4 quarters][R], then [R] for the end
-  static constexpr uint32_t kSmemBar = kSmemMax + 5 * R * 4;
+  static constexpr uint32_t kSmemEnds = kSmemMax + 5 * R * 4;        // [R] (log2 maximum, sum)
+  static constexpr uint32_t kSmemBar = kSmemEnds + R * 8;
   static constexpr int kNumBars = 4 * kStages + 7;
   static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2), fresh (2)
   static constexpr uint32_t kSmemAlloc = kSmemWords + 32 + 1024;
-  static_assert(kBlocks * (kSmemAlloc + 1024) <= 233472 && kSmemAlloc <= 232448, "shared memory of an SM");
+  static_assert(kBlocks * (kSmemAlloc + 1024) <= 233472, "shared memory of an SM");
   static_assert(kColO + kN <= kTmem && kBlocks * kTmem <= 512, "TMEM layout");
+  static_assert(R * kRowStride * 4 <= kStages * kStageBytes, "the rows fit the ring");
 };
 
 // kind::f16, bf16 operands, fp32 accumulate; A K-major (S) or MN-major (PV).
@@ -95,30 +93,29 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 // Where column j of dim d is kept.
-template <bool kF32, int R>
+template <int R>
 __device__ __forceinline__ float* acc_at(uint8_t* smem, int j, int d) {
-  uint8_t* const base = smem + Lay<kF32, R>::kSmemAcc;
-  if constexpr (R == 64) {
-    return reinterpret_cast<float*>(base) + j * kD + d;
-  } else {
-    constexpr uint32_t kFree = Lay<kF32, R>::kFree;
-    const uint32_t at = (uint32_t)(j * kD + d) * 4u;
-    return reinterpret_cast<float*>(base + sw128(at / kFree * 128u + 128u - kFree + at % kFree));
-  }
+  constexpr uint32_t kFree = Lay<R>::kFree;
+  const uint32_t at = (uint32_t)(j * kD + d) * 4u;
+  return reinterpret_cast<float*>(smem + Lay<R>::kSmemAcc + sw128(at / kFree * 128u + 128u - kFree + at % kFree));
 }
 
-template <bool kF32, int R>
-__global__ void __launch_bounds__(Lay<kF32, R>::kThreads, Lay<kF32, R>::kBlocks)
+template <int R>
+__global__ void __launch_bounds__(Lay<R>::kThreads, Lay<R>::kBlocks)
 tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
-  using L = Lay<kF32, R>;
-  constexpr int kStages = L::kStages, kTerms = L::kTerms;
-  constexpr uint32_t kStageBytes = L::kStageBytes, kV = kTerms * kOperand;  // V in a stage
+  using L = Lay<R>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: descriptors in uniform registers
   const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
 
+  // The table's first entries are on their way while the lengths are: an entry
+  // past the sequence is read and not used.
+  const int first_page = s * (a.split_len / ATTN_PAGE) + lane;
+  int first_entries = -1;
+  if (warp == L::kTmaWarp && first_page < a.max_blocks)
+    first_entries = __ldg(a.table + (size_t)b * a.max_blocks + first_page);
   const Seq seq = load_seq(a, b);
   const int i0 = rt * (R / 4);  // the block's first drafted row
   const int nrows = min(R / 4, seq.rows - i0);
@@ -126,7 +123,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   const int k1 = min(k0 + a.split_len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   if (nrows <= 0) return;
-  if (k0 >= k1) {
+  // Early: the merge's blocks may take their places; they wait for all of this grid.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (k0 >= k1 && !a.cluster) {
     // Past the sequence: the merge counts its segments from the lengths. A
     // sequence without any key (only a refused one) gets zeros.
     if (s == 0)
@@ -134,8 +133,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         a.out[((size_t)(seq.first + i0 + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
     return;
   }
-  const bool whole = seq.keys <= a.split_len;  // one segment: the output is written here
-  const int ntiles = (k1 - k0 + kKeys - 1) / kKeys;
+  const bool whole = !a.cluster && seq.keys <= a.split_len;  // one segment: the output is written here
+  const int ntiles = max(0, (k1 - k0 + kKeys - 1) / kKeys);
 
   uint64_t* const kfull = reinterpret_cast<uint64_t*>(smem + L::kSmemBar);  // [stage] K landed
   uint64_t* const vfull = kfull + kStages;                                  // [stage] V landed
@@ -151,6 +150,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   uint32_t* const odd = words + 2;                 // [2] drafted rows whose value is not finite
   volatile uint32_t* const fresh = words + 4;      // [2] tile n starts O anew, at n % 2
   unsigned long long* const masks = reinterpret_cast<unsigned long long*>(smem + L::kSmemMask);
+  float2* const ends = reinterpret_cast<float2*>(smem + L::kSmemEnds);
   const Wait wait{a.err, a.timeout_ns, abort_flag};
 
   const int* const trow = a.table + (size_t)b * a.max_blocks;
@@ -184,7 +184,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       load(&mk, kfull, 0, n + 1);
     }
     if (n >= kStages && !wait.warp(&vempty[n % kStages], (n / kStages - 1) & 1)) return false;
-    load(&mv, vfull, kV, n);
+    load(&mv, vfull, kOperand, n);
     ++ahead;
     if ((ahead >> 2) != group) {
       group = ahead >> 2;
@@ -194,95 +194,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     return true;
   };
 
-  // ---- fp32 pages: eight warps load K and V into registers a tile ahead, split
-  // each value into three bf16 terms and write those. A thread takes 8 dims of
-  // the keys row + 32 u, so a warp's loads are four whole rows of 256 bytes from
-  // one page. Lane 4 x + u holds the table's entry of unit u of tile x of a
-  // group of eight tiles.
-  const int ctid = tid - 32 * L::kSoft, crow = (ctid >> 3) & 31, c8 = ctid & 7;
-  float4 kx[kF32 ? 2 * kUnits : 1], vx[kF32 ? 2 * kUnits : 1];
-  auto centry = [&](int g) -> int {
-    const int t = k0 + (g * 8 + (lane >> 2)) * kKeys + (crow & ~3) + 32 * (lane & 3);
-    return t < k1 ? __ldg(trow + t / ATTN_PAGE) : -1;
-  };
-  auto fetch = [&](const void* pool, int n, int tab, int tab_next, int g, float4* x) {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      const int page = __shfl_sync(0xffffffffu, (n >> 3) == g ? tab : tab_next, (n & 7) * 4 + u);
-      const int t = k0 + n * kKeys + crow + 32 * u;
-      x[2 * u] = x[2 * u + 1] = make_float4(0.f, 0.f, 0.f, 0.f);  // past the last key, or a bad page
-      if (t < k1) {
-        if (page >= 0 && page < a.num_pages) {
-          const float4* src = reinterpret_cast<const float4*>(
-              static_cast<const float*>(pool) + (((size_t)page * ATTN_PAGE + t % ATTN_PAGE) * kHKV + head) * kD + c8 * 8);
-          x[2 * u] = __ldg(src);
-          x[2 * u + 1] = __ldg(src + 1);
-        } else {
-          record_error(a.err, kDevErrBounds);
-        }
-      }
-    }
-  };
-  auto split_out = [&](const float4* x, uint32_t operand, int n, bool is_v) {
-#pragma unroll
-    for (int u = 0; u < kUnits; ++u) {
-      float y[8] = {x[2 * u].x, x[2 * u].y, x[2 * u].z, x[2 * u].w,
-                    x[2 * u + 1].x, x[2 * u + 1].y, x[2 * u + 1].z, x[2 * u + 1].w};
-      const int key = crow + 32 * u;
-      if (is_v && k0 + (n + 1) * kKeys > seq.ctx) {
-        // no infinity or NaN of a drafted row into a product with the zero
-        // probability of a row that does not see it
-        const int at = k0 + n * kKeys + key - seq.ctx;
-        bool bad = false;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (at >= 0 && (__float_as_uint(y[k]) & 0x7f800000u) == 0x7f800000u) {
-            y[k] = 0.f;
-            bad = true;
-          }
-        if (bad) atomicOr(odd + (at >> 5), 1u << (at & 31));
-      }
-      uint32_t w[3][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) split3(y[2 * k], y[2 * k + 1], w[0][k], w[1][k], w[2][k]);
-#pragma unroll
-      for (int t = 0; t < 3; ++t)
-        *reinterpret_cast<uint4*>(smem + operand + t * kOperand + sw128((uint32_t)key * 128u + c8 * 16u)) =
-            make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(is_v ? vfull : kfull);
-  };
-
-  if (warp >= L::kSoft && warp < L::kMmaWarp) {
-    if (warp == L::kSoft && lane == 0) {
-      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kfull[i], kF32 ? kConvWarps : 1);  // and vfull
-      for (int i = 0; i < 2 * kStages; ++i) mbar_init(&kempty[i], 1);                     // and vempty
-      mbar_init(&sfull[0], 1);
-      mbar_init(&sfull[1], 1);
-      mbar_init(&sread[0], L::kSoft);
-      mbar_init(&sread[1], L::kSoft);
-      mbar_init(pfull, L::kSoft);
-      mbar_init(odone, 1);
-      mbar_init(drain, 1);
-      fence_mbar_init();
+  if (warp == L::kTmaWarp) {
+    for (int i = lane; i < L::kNumBars; i += 32)
+      mbar_init(&kfull[i], &kfull[i] >= sread && &kfull[i] < odone ? L::kSoft : 1);  // sread and pfull: every softmax warp
+    fence_mbar_init();
+    if (lane == 0) {
       *abort_flag = 0;
       odd[0] = odd[1] = 0;
     }
     __syncwarp();
-    // The first tiles are on their way before the block has met.
-    if constexpr (kF32) {
-      entries = centry(0);
-      entries_next = centry(1);
-      fetch(a.k_pages, 0, entries, entries_next, 0, kx);
-      fetch(a.v_pages, 0, entries, entries_next, 0, vx);
-    } else {
-      entries = entry_at(0);
-      entries_next = entry_at(1);
-      load(&mk, kfull, 0, 0);
-      while (ahead < kStages - 1 && ahead < ntiles) load_next();
-    }
+    // The first tile is on its way before the block has met.
+    entries = first_entries;
+    entries_next = entry_at(1);
+    if (ntiles > 0) load(&mk, kfull, 0, 0);
   } else if (warp == L::kMmaWarp) {
     tmem_alloc(words, L::kTmem);
     tmem_relinquish();
@@ -319,41 +243,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = words[0];
 
-  if (warp >= L::kSoft && warp < L::kMmaWarp) {
-    if constexpr (kF32) {
-      // K(n) as soon as S(n - 1) has read the terms before it, then V(n - 1) after PV(n - 2).
-      for (int n = 0; n <= ntiles; ++n) {
-        if (n < ntiles) {
-          if (n > 0 && !wait.warp(kempty, (n - 1) & 1)) break;
-          split_out(kx, 0, n, false);
-          if (n + 1 < ntiles) fetch(a.k_pages, n + 1, entries, entries_next, group, kx);
-        }
-        if (n > 0) {
-          if (n > 1 && !wait.warp(vempty, n & 1)) break;
-          split_out(vx, kV, n - 1, true);
-          if (n < ntiles) fetch(a.v_pages, n, entries, entries_next, group, vx);
-          if ((n >> 3) != group) {  // V's next tile starts a group
-            group = n >> 3;
-            entries = entries_next;
-            entries_next = centry(group + 1);
-          }
-        }
-      }
-    } else {
-      while (ahead < ntiles && load_next()) {
-      }
-      if (*abort_flag) {
-        // Copies still in flight land before the block's shared memory is
-        // released (K up to ahead + 1, V up to ahead - 1 may have been issued).
-        for (int i = max(0, ahead - kStages); i < min(ahead + 2, ntiles); ++i)
-          mbar_wait(&kfull[i % kStages], (i / kStages) & 1, 1000000);
-        for (int i = max(0, ahead - kStages); i < ahead; ++i)
-          mbar_wait(&vfull[i % kStages], (i / kStages) & 1, 1000000);
-      }
+  if (warp == L::kTmaWarp) {
+    while (ahead < ntiles && load_next()) {
+    }
+    if (*abort_flag) {
+      // Copies still in flight land before the block's shared memory is
+      // released (K up to ahead + 1, V up to ahead - 1 may have been issued).
+      for (int i = max(0, ahead - kStages); i < min(ahead + 2, ntiles); ++i)
+        mbar_wait(&kfull[i % kStages], (i / kStages) & 1, 1000000);
+      for (int i = max(0, ahead - kStages); i < ahead; ++i)
+        mbar_wait(&vfull[i % kStages], (i / kStages) & 1, 1000000);
     }
     __syncwarp();
   } else if (warp == L::kMmaWarp) {
-    constexpr uint32_t kIdS = idesc_tree(128, R, false);
+    constexpr uint32_t kIdS = idesc_tree(128, R, false), kIdPV = idesc_tree(64, L::kN, true);
     const uint32_t base = smem_u32(smem);
     const uint64_t qd = sdesc_sw128(base + L::kSmemQ), pd = sdesc_sw128_mn(base + L::kSmemP, kOperand);
     auto issue_s = [&](int n) -> bool {
@@ -364,39 +267,31 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       const uint64_t kd = sdesc_sw128(base + st * kStageBytes);
       const uint32_t dst = tmem + L::kColS + (n & 1) * R;
       if (elect()) {
-        // Products of terms i + j <= 2, the smallest first: only the last four
-        // accumulations are at the score's own size.
+        // The smallest term first: only the last four accumulations are at the
+        // score's own size.
 #pragma unroll
-        for (int order = 2; order >= 0; --order)
+        for (int t = 2; t >= 0; --t)
 #pragma unroll
-          for (int kt = 0; kt < kTerms; ++kt)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (kt <= order)
-                mma_f16_ss(dst, kd + kt * (kOperand >> 4) + x * 2, qd + (order - kt) * (R * 8) + x * 2, kIdS,
-                           order < 2 || kt > 0 || x > 0);
+          for (int x = 0; x < 4; ++x)
+            mma_f16_ss(dst, kd + x * 2, qd + t * (R * 8) + x * 2, kIdS, t < 2 || x > 0);
         mma_commit(&sfull[n & 1]);
         mma_commit(&kempty[st]);
       }
       __syncwarp();
       return true;
     };
-    bool ok = issue_s(0);
+    bool ok = ntiles == 0 || issue_s(0);
     for (int n = 0; ok && n < ntiles; ++n) {
       if (n + 1 < ntiles && !(ok = issue_s(n + 1))) break;
       const int st = n % kStages;
       if (!(ok = wait.warp(pfull, n & 1) && wait.warp(&vfull[st], (n / kStages) & 1))) break;
       tc_fence_after();
-      const uint64_t vd = sdesc_sw128_mn(base + st * kStageBytes + kV);
+      const uint64_t vd = sdesc_sw128_mn(base + st * kStageBytes + kOperand);
       const uint32_t old = n > 0 && !fresh[n & 1];
       if (elect()) {
-        // V's term t takes the 3 - t largest terms of p, into their columns.
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-          for (int x = 0; x < 8; ++x)  // 16 keys a step: 2048 bytes of rows
-            mma_f16_ss(tmem + L::kColO, vd + t * (kOperand >> 4) + x * 128, pd + x * 128,
-                       idesc_tree(64, L::kN - t * R, true), t > 0 || x > 0 ? 1u : old);
+        for (int x = 0; x < 8; ++x)  // 16 keys a step: 2048 bytes of rows
+          mma_f16_ss(tmem + L::kColO, vd + x * 128, pd + x * 128, kIdPV, x > 0 ? 1u : old);
         mma_commit(&vempty[st]);
         mma_commit(odone);
       }
@@ -463,12 +358,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 #pragma unroll
             for (int i = 0; i < kCols / 4; ++i)
               if (!(masks[col0 / 4 + i] >> at & 1)) hidden |= 15u << (4 * i);
-          if constexpr (!kF32) {
+          {
             // The value row of this key: zeros past the last key (its slot may hold
             // anything), and no infinity or NaN of a drafted row into a product
             // with the zero probability of a row that does not see it.
             if (!wait(&vfull[n % kStages], (n / kStages) & 1)) failed = true;
-            uint8_t* v = smem + (n % kStages) * kStageBytes + kV;
+            uint8_t* v = smem + (n % kStages) * kStageBytes + kOperand;
             for (int c8 = part; c8 < 8; c8 += L::kParts) {
               uint4* p = reinterpret_cast<uint4*>(v + sw128((uint32_t)key * 128u + c8 * 16u));
               uint4 u = past ? make_uint4(0, 0, 0, 0) : *p;
@@ -553,7 +448,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             if (kept && lane < 16) {
               float old[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) old[j] = *acc_at<kF32, R>(smem, col0 + h + j, d);
+              for (int j = 0; j < 8; ++j) old[j] = *acc_at<R>(smem, col0 + h + j, d);
 #pragma unroll
               for (int j = 0; j < 8; ++j) o[j] += old[j];
             }
@@ -563,7 +458,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
             }
             if (lane < 16) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) *acc_at<kF32, R>(smem, col0 + h + j, d) = o[j];
+              for (int j = 0; j < 8; ++j) *acc_at<R>(smem, col0 + h + j, d) = o[j];
             }
           }
           kept = true;
@@ -586,7 +481,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
 
     // ------------------------------------------------------------ epilogue
-    if (!failed) failed = !wait.warp(odone, (ntiles - 1) & 1);
+    if (!failed && ntiles > 0) failed = !wait.warp(odone, (ntiles - 1) & 1);
     {
       // Sums over the warp's keys: halving the columns a lane holds each round,
       // lanes j and 16 + j end with column col0 + j.
@@ -610,7 +505,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       for (int h = 0; h < kCols; h += 8) read_o(h, reinterpret_cast<float (&)[8]>(o[h]));
       if (kept && lane < 16) {
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) o[j] += *acc_at<kF32, R>(smem, col0 + j, d);
+        for (int j = 0; j < kCols; ++j) o[j] += *acc_at<R>(smem, col0 + j, d);
       }
       unsigned long long rest = ((unsigned long long)odd[1] << 32) | odd[0];
       while (rest) {  // drafted values that are not finite reach the rows that see them
@@ -619,8 +514,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         const int page = __ldg(trow + (seq.ctx + j0) / ATTN_PAGE);
         if (lane < 16 && page >= 0 && page < a.num_pages) {
           const size_t at = (((size_t)page * ATTN_PAGE + (seq.ctx + j0) % ATTN_PAGE) * kHKV + head) * kD + d;
-          const float v = kF32 ? __ldg(static_cast<const float*>(a.v_pages) + at)
-                               : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.v_pages) + at) << 16);
+          const float v = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.v_pages) + at) << 16);
           if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u)
 #pragma unroll
             for (int j = 0; j < kCols; ++j)
@@ -629,10 +523,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       }
       // Rows to shared memory, so that they leave in 16-byte pieces. (p's atoms
       // are free, and so is what the tiles occupied.)
-      float* const rows = reinterpret_cast<float*>(smem);  // [R][68]
+      float* const rows = reinterpret_cast<float*>(smem);  // [R][kRowStride]
       if (lane < 16) {
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) rows[(col0 + j) * 68 + d] = o[j];
+        for (int j = 0; j < kCols; ++j) rows[(col0 + j) * kRowStride + d] = ntiles > 0 ? o[j] : 0.f;
       }
       if (quarter == 0 && lane < kCols) maxima[4 * R + c] = ref;
       meet(kMeet);
@@ -642,7 +536,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       for (int e = tid; e < nrows * kGroup * 16; e += kMeet) {  // (row, 4 dims)
         const int r = e >> 4, d4 = (e & 15) * 4;
         const float sl = (maxima[r] + maxima[R + r]) + (maxima[2 * R + r] + maxima[3 * R + r]);
-        float4 y = *reinterpret_cast<const float4*>(rows + r * 68 + d4);
+        if (a.cluster) {
+          if (d4 == 0) ends[r] = make_float2(maxima[4 * R + r] == kUnseen ? -INFINITY : maxima[4 * R + r], sl);
+          continue;
+        }
+        float4 y = *reinterpret_cast<const float4*>(rows + r * kRowStride + d4);
         const size_t at = at0 + (r >> 2) * kHQ + (r & 3);
         if (whole) {
           const float inv = sl == 0.f ? 0.f : 1.f / sl;  // no key: zeros
@@ -665,26 +563,29 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   __syncthreads();
   tc_fence_after();
   if (*abort_flag && !whole) {  // after a failed wait the segment counts as empty
-    float2* mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
-    for (int r = tid; r < nrows * kGroup; r += L::kThreads)
-      mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
-          make_float2(-INFINITY, 0.f);
+    float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+    for (int r = tid; r < nrows * kGroup; r += L::kThreads) {
+      if (a.cluster) ends[r] = make_float2(-INFINITY, 0.f);
+      else
+        mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
+            make_float2(-INFINITY, 0.f);
+    }
+    __syncthreads();
   }
   if (warp == L::kMmaWarp) tmem_dealloc(tmem, L::kTmem);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (a.cluster && warp < L::kSoft)
+    cluster_merge(a, seq.first + i0, nrows, head, reinterpret_cast<const float*>(smem), kRowStride, ends, tid,
+                  32 * L::kSoft);
 }
 
 }  // namespace
 
-template <bool kF32, int R>
+template <int R>
 TreeVariant variant() {
-  using L = Lay<kF32, R>;
-  return {tree_tc_kernel<kF32, R>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0};
+  using L = Lay<R>;
+  return {tree_tc_kernel<R>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0};
 }
 
-TreeVariant tree_tc_variant(bool bf16, int which) {
-  if (!bf16) return which == 0 ? variant<true, 16>() : variant<true, 32>();
-  return which == 0 ? variant<false, 16>() : which == 1 ? variant<false, 32>() : variant<false, 64>();
-}
+TreeVariant tree_tc_variant(int tokens) { return tokens == 4 ? variant<16>() : variant<32>(); }
 
 }  // namespace attn

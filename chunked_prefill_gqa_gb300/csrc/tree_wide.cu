@@ -42,6 +42,7 @@ constexpr int kKeys = 64;                  // keys of a tile
 constexpr int kPages = kKeys / ATTN_PAGE;
 constexpr int kSoft = 8;                   // softmax warps, two groups of four
 constexpr uint32_t kHalf = kKeys * 128;    // 64 rows of 128 bytes
+constexpr int kRowStride = kD + 4;         // floats, for rows written a row a thread
 
 template <bool kF32>
 struct Wide {
@@ -61,13 +62,16 @@ struct Wide {
   static constexpr uint32_t kColO = kColS + kBufs * kBufCols;
   static constexpr uint32_t kSmemMask = kStages * kStageBytes;
   static constexpr uint32_t kSmemMl = kSmemMask + kRows * 8;         // [2 groups][128 rows] (reference, sum)
-  static constexpr uint32_t kSmemBar = kSmemMl + 2 * 128 * 8;
+  static constexpr uint32_t kSmemEnds = kSmemMl + 2 * 128 * 8;       // [128 rows] the same of both groups together
+  static constexpr uint32_t kSmemBar = kSmemEnds + 128 * 8;
+  // In the ring once it is idle: the groups' exchange, then the block's rows.
+  static constexpr uint32_t kSmemRows = 2 * 128 * 32 * 4;
   static constexpr int kNumBars = 6 * kStages + 2 * kBufs + 4 + 3;
   static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2)
   static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
   static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
   static_assert(kColO + 2 * kD <= 512, "TMEM layout");
-  static_assert(2 * 128 * 32 * 4 <= kStages * kStageBytes, "the groups' exchange fits the ring");
+  static_assert(kSmemRows + 128 * kRowStride * 4 <= kStages * kStageBytes, "the exchange and the rows fit the ring");
 };
 
 template <bool kF32>
@@ -93,7 +97,9 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   const int k1 = min(k0 + a.split_len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   if (nrows <= 0) return;
-  if (k0 >= k1) {
+  // Early: the merge's blocks may take their places; they wait for all of this grid.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (k0 >= k1 && !a.cluster) {
     // Past the sequence: the merge counts its segments from the lengths. A
     // sequence without any key (only a refused one) gets zeros.
     if (s == 0)
@@ -101,8 +107,8 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         a.out[((size_t)(seq.first + i0 + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
     return;
   }
-  const bool whole = seq.keys <= a.split_len;  // one segment: the output is written here
-  const int ntiles = (k1 - k0 + kKeys - 1) / kKeys;
+  const bool whole = !a.cluster && seq.keys <= a.split_len;  // one segment: the output is written here
+  const int ntiles = max(0, (k1 - k0 + kKeys - 1) / kKeys);
   const int quarters = (nrows * kGroup + 31) / 32;  // lane quarters that hold rows
 
   uint64_t* const kfull = reinterpret_cast<uint64_t*>(smem + L::kSmemBar);  // [stage] K landed
@@ -121,6 +127,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
   uint32_t* const odd = words + 2;  // [2] drafted rows whose value is not finite
   unsigned long long* const masks = reinterpret_cast<unsigned long long*>(smem + L::kSmemMask);
+  float2* const ends = reinterpret_cast<float2*>(smem + L::kSmemEnds);
   const Wait wait{a.err, a.timeout_ns, abort_flag};
 
   // The TMA warps, one for K and one for V (a box of 16 rows costs its warp about
@@ -169,20 +176,21 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     // The first tiles are on their way before the block has met.
     entries = first_entries;
     entries_next = entry_at(1);
-    for (int n = 0; n < kStages && n < ntiles; ++n) load(&mk, kfull, 0, n);
+    if (ntiles > 0) load(&mk, kfull, 0, 0);
   } else if (warp == L::kVWarp) {
     entries = first_entries;
     entries_next = entry_at(1);
   } else if (warp == L::kQkWarp) {
     tmem_alloc(words, 512);
     tmem_relinquish();
-  } else if (tid < kRows) {
-    const int rows_left = seq.rows;  // bits past the sequence's rows see nothing
-    unsigned long long m = 0;
-    if (tid < nrows)
-      m = (a.masks ? (unsigned long long)__ldg(a.masks + seq.first + i0 + tid) : ~0ull >> (63 - (i0 + tid))) &
-          (~0ull >> (64 - rows_left));
-    masks[tid] = m;
+  } else if (warp < kSoft) {
+    if (tid < kRows) {
+      unsigned long long m = 0;
+      if (tid < nrows)
+        m = (a.masks ? (unsigned long long)__ldg(a.masks + seq.first + i0 + tid) : ~0ull >> (63 - (i0 + tid))) &
+            (~0ull >> (64 - seq.rows));  // bits past the sequence's rows see nothing
+      masks[tid] = m;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -200,7 +208,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       const bool is_k = warp == L::kKWarp;
       uint64_t* const full = is_k ? kfull : vfull;
       uint64_t* const empty = is_k ? kempty : vempty;
-      int n = is_k ? kStages : 0;
+      int n = is_k ? 1 : 0;
       for (; n < ntiles; ++n) {
         if (n >= kStages && !wait.warp(&empty[n % kStages], (n / kStages - 1) & 1)) break;
         load(is_k ? &mk : &mv, full, is_k ? 0 : L::kV, n);
@@ -214,7 +222,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       const bool qk = warp == L::kQkWarp;
       uint64_t* const go = (kF32 ? kready : kfull) + (qk ? 0 : kStages);  // K, or V, ready
       if (qk) {
-        bool ok = wait.warp(qready, 0);
+        bool ok = ntiles == 0 || wait.warp(qready, 0);
         for (int n = 0; ok && n < ntiles; ++n) {
           const int st = n % kStages, buf = n % L::kBufs;
           if (!(ok = wait.warp(&go[st], (n / kStages) & 1) &&
@@ -370,7 +378,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     for (int i = 0; i < kD; ++i) o[i] = 0.f;
     bool failed = false;
 
-    if (active) {
+    if (active && ntiles > 0) {
       {  // this thread's 32 dims (32 g ..) of its row of q, in its terms
         const int i = row >> 2;
         const float* src = a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (row & 3)) * kD + g * 32;
@@ -560,7 +568,9 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       const bool mine = active && (row >> 2) < nrows;
       const size_t at = (size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3);
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;  // no key: zeros
-      float* const dst = (whole ? a.out + at * kD : a.parts + (at * a.splits + s) * kD) + g * 32;
+      float* const dst = (a.cluster ? reinterpret_cast<float*>(smem + L::kSmemRows) + row * kRowStride
+                          : whole   ? a.out + at * kD
+                                    : a.parts + (at * a.splits + s) * kD) + g * 32;
       if (mine) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -572,7 +582,8 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
               make_float4(fmaf(w0, a0, w1 * y.x) * inv, fmaf(w0, a1, w1 * y.y) * inv, fmaf(w0, a2, w1 * y.z) * inv,
                           fmaf(w0, a3, w1 * y.w) * inv);
         }
-        if (!whole && g == 0) {
+        if (a.cluster && g == 0) ends[row] = make_float2(m == kUnseen ? -INFINITY : m, l);
+        if (!a.cluster && !whole && g == 0) {
           float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
           mls[at * a.splits + s] = make_float2(m == kUnseen ? -INFINITY : m, l);
         }
@@ -587,12 +598,19 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   tc_fence_after();
   if (*abort_flag && !whole) {  // after a failed wait the segment counts as empty
     float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
-    for (int r = tid; r < nrows * kGroup; r += L::kThreads)
-      mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
-          make_float2(-INFINITY, 0.f);
+    for (int r = tid; r < nrows * kGroup; r += L::kThreads) {
+      if (a.cluster) ends[r] = make_float2(-INFINITY, 0.f);
+      else
+        mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
+            make_float2(-INFINITY, 0.f);
+    }
+    __syncthreads();
   }
   if (warp == L::kQkWarp) tmem_dealloc(tmem, 512);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (The softmax warps: with fp32 pages the others have given their registers away.)
+  if (a.cluster && warp < kSoft)
+    cluster_merge(a, seq.first + i0, nrows, head, reinterpret_cast<const float*>(smem + L::kSmemRows), kRowStride, ends,
+                  tid, 32 * kSoft);
 }
 
 }  // namespace

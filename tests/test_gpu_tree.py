@@ -60,7 +60,7 @@ def test_sizes(cp, bf16, rows, ctx):
 
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("kind", ["tree", "chain", "self", "empty", "mixed", "null"])
-@pytest.mark.parametrize("splits", [0, 1, 3, 64])
+@pytest.mark.parametrize("splits", [0, 1, 3, 8, 64])
 def test_ragged_batch_masks_and_splits(cp, bf16, kind, splits):
     lens = [(700, 5), (0, 12), (33, 0), (1, 1), (2500, 12), (128, 7), (0, 1), (255, 2)]
     b = R.make_batch(lens, bf16=bf16, seed=11)
@@ -210,11 +210,11 @@ def test_workspace_is_checked(cp):
     lens = [(3000, 2)]
     b = R.make_batch(lens, seed=73)
     q, out = queries(2), torch.empty(2, 32, 64, device="cuda")
-    need = cp.attn_tree_workspace_bytes(1, 2, 2, 3000, 4)
+    need = cp.attn_tree_workspace_bytes(1, 2, 2, 3000, 20)
     assert need > 0
     for ws in (None, torch.empty(need - 16, dtype=torch.uint8, device="cuda")):
         with pytest.raises(cp.AttnError) as e:
-            cp.attn_tree_paged(q, b["kp"], b["vp"], b["table"], b["ctx"], b["starts"], None, out, 2, 3000, 4, ws)
+            cp.attn_tree_paged(q, b["kp"], b["vp"], b["table"], b["ctx"], b["starts"], None, out, 2, 3000, 20, ws)
         assert e.value.code == cp.ATTN_ESPACE
 
 
@@ -238,7 +238,8 @@ def test_pools_past_32_bit_offsets(cp):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
-def test_streams_and_graph_replay(cp, bf16):
+@pytest.mark.parametrize("splits", [0, 12])
+def test_streams_and_graph_replay(cp, bf16, splits):
     """Two captured graphs with a workspace each, replayed on two streams at once,
     after the inputs have changed; and an eager call on another stream."""
     lens = [(2000, 9), (700, 4)]
@@ -247,18 +248,18 @@ def test_streams_and_graph_replay(cp, bf16):
         b = R.make_batch(lens, bf16=bf16, seed=90 + s)
         masks = torch.from_numpy(R.tree_masks(lens, seed=s)).cuda()
         q, out = queries(13, seed=s), torch.empty(13, 32, 64, device="cuda")
-        need = cp.attn_tree_workspace_bytes(2, 13, 9, 2000)
-        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        need = cp.attn_tree_workspace_bytes(2, 13, 9, 2000, splits)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
         call = cp.attn_tree_paged_bf16kv if bf16 else cp.attn_tree_paged
         args = (q, b["kp"], b["vp"], b["table"], b["ctx"], b["starts"], masks, out, 9, 2000)
         st = torch.cuda.Stream()
         st.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(st):
-            call(*args, workspace=ws)
+            call(*args, num_splits=splits, workspace=ws)
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=st):
-            call(*args, workspace=ws)
+            call(*args, num_splits=splits, workspace=ws)
         q.copy_(queries(13, seed=s + 10))
         out.fill_(float("nan"))
         made.append((b, masks, q, out, g, st, ws))

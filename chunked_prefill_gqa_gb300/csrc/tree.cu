@@ -427,50 +427,59 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   if (a.cluster) cluster_merge(a, seq.first, nrows, head, rows, kRowStride, ends, tid, 32 * kWarps);
 }
 
-// Merge: block (drafted row, sequence), a warp per four heads in turn, two dims a lane.
-// Lane s holds segment s's maximum and sum, 32 segments at a time.
+// Merge of segments that are not one cluster: a warp per (drafted row, query
+// head), two dims a lane. Lane s holds segment s's maximum and sum, 32 segments at
+// a time; eight segments' rows are on their way at once.
 constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(32 * kMergeWarps)
 tree_merge_kernel(const TreeArgs a) {
-  const int b = blockIdx.y, i = blockIdx.x, lane = threadIdx.x & 31;
+  constexpr int kAhead = 8;
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int i = blockIdx.x / (kHQ / kMergeWarps);
+  const int h = (blockIdx.x % (kHQ / kMergeWarps)) * kMergeWarps + (threadIdx.x >> 5);
   const Seq seq = load_seq(a, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i >= seq.rows || seq.keys <= a.split_len) return;
   const int active = (seq.keys + a.split_len - 1) / a.split_len;
-  const float2* mls = reinterpret_cast<const float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
-  for (int h = threadIdx.x >> 5; h < kHQ; h += kMergeWarps) {
-    const size_t at = (size_t)(seq.first + i) * kHQ + h;
-    float2 p[kMaxSplits / 32];
-    float m = -INFINITY;
+  const size_t at = (size_t)(seq.first + i) * kHQ + h;
+  const float2* mls = reinterpret_cast<const float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD) + at * a.splits;
+  const float2* rows = reinterpret_cast<const float2*>(a.parts + at * a.splits * kD) + lane;
+  float2 p[kMaxSplits / 32];
+  float m = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kMaxSplits / 32; ++k) {
-      p[k] = make_float2(-INFINITY, 0.f);
-      if (k * 32 + lane < active) p[k] = mls[at * a.splits + k * 32 + lane];
-      m = fmaxf(m, p[k].x);
-    }
+  for (int k = 0; k < kMaxSplits / 32; ++k) {
+    p[k] = make_float2(-INFINITY, 0.f);
+    if (k * 32 + lane < active) p[k] = mls[k * 32 + lane];
+    m = fmaxf(m, p[k].x);
+  }
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
-    float den = 0.f;
-    float2 x = make_float2(0.f, 0.f);
+  for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+  float den = 0.f;
+  float2 x = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < kMaxSplits / 32; ++k) {
-      const float w = p[k].x == -INFINITY ? 0.f : ex2(p[k].x - m);
-      const int most = min(32, active - k * 32);
-      den = fmaf(w, p[k].y, den);
-      for (int t = 0; t < most; ++t) {
-        const float wt = __shfl_sync(kFull, w, t);
-        const float2 y = *reinterpret_cast<const float2*>(a.parts + (at * a.splits + k * 32 + t) * kD + 2 * lane);
-        if (wt != 0.f) {  // an empty segment's accumulator has no weight, whatever it holds
-          x.x = fmaf(wt, y.x, x.x);
-          x.y = fmaf(wt, y.y, x.y);
+  for (int k = 0; k < kMaxSplits / 32; ++k) {
+    const float w = p[k].x == -INFINITY ? 0.f : ex2(p[k].x - m);
+    const int most = min(32, active - k * 32);
+    den = fmaf(w, p[k].y, den);
+    for (int t = 0; t < most; t += kAhead) {
+      float2 y[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (t + u < most) y[u] = rows[(k * 32 + t + u) * (kD / 2)];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const float wt = __shfl_sync(kFull, w, (t + u) & 31);
+        if (t + u < most && wt != 0.f) {  // an empty segment's row has no weight, whatever it holds
+          x.x = fmaf(wt, y[u].x, x.x);
+          x.y = fmaf(wt, y[u].y, x.y);
         }
       }
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(kFull, den, off);
-    const float inv = den == 0.f ? 0.f : 1.f / den;  // no key: zeros
-    *reinterpret_cast<float2*>(a.out + at * kD + 2 * lane) = make_float2(x.x * inv, x.y * inv);
   }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(kFull, den, off);
+  const float inv = den == 0.f ? 0.f : 1.f / den;  // no key: zeros
+  *reinterpret_cast<float2*>(a.out + at * kD + 2 * lane) = make_float2(x.x * inv, x.y * inv);
 }
 
 // ---------------------------------------------------------------------------
@@ -544,6 +553,13 @@ int tree_device(TreeDevice** out) {
           if (cudaFuncGetAttributes(&fa, x.kernel) != cudaSuccess) return ATTN_ECUDA;
           if (fa.numRegs < x.regs) return ATTN_ELAUNCH;
         }
+        // The occupancy queries count one block an SM for any kernel that uses
+        // tensor memory; with half an SM's shared and tensor memory two run
+        // (measured: 256 blocks of tree_tc take the time of 128).
+        int counted = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&counted, x.kernel, x.threads, x.smem) != cudaSuccess)
+          return ATTN_ECUDA;
+        const int more = counted > 0 && counted < x.blocks ? x.blocks / counted : 1;
         d.slots[t][v] = sms * x.blocks;
         for (int size = 2; size <= kMaxCluster; ++size) {
           cudaLaunchConfig_t cfg = {};
@@ -562,7 +578,7 @@ int tree_device(TreeDevice** out) {
             (void)cudaGetLastError();
             n = 0;  // no such clusters: segments merge through memory
           }
-          d.clusters[t][v][size] = n;
+          d.clusters[t][v][size] = n * more;
         }
       }
     d.ready = true;
@@ -647,7 +663,7 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
     // The merge's blocks start as this grid's last ones run (programmatic
     // dependent launch) and wait for its end.
     cudaLaunchConfig_t mcfg = {};
-    mcfg.gridDim = dim3(c.max_rows, c.B);
+    mcfg.gridDim = dim3(c.max_rows * (kHQ / kMergeWarps), c.B);
     mcfg.blockDim = dim3(32 * kMergeWarps);
     mcfg.stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -59,15 +59,20 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b) {
   return s;
 }
 
-// Three bf16 terms of a pair: two truncated, the last rounded to nearest: 24
-// bits, all of an fp32 value whose last term does not underflow.
+// Three bf16 terms of a pair, each rounded to nearest: 24 bits, all of an fp32
+// value whose last term does not underflow. The remainders, exact, come from
+// fused products of bf16 operands into fp32 (t * -1 + x), one instruction where
+// unpacking the term first takes two.
 __device__ __forceinline__ void split3(float x, float y, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
-  t0 = tc::pack_bf16_trunc(x, y);
-  float rx, ry;
-  tc::fma2(rx, ry, tc::bf16_trunc(x), tc::bf16_trunc(y), -1.f, -1.f, x, y);  // exact
-  t1 = tc::pack_bf16_trunc(rx, ry);
-  tc::fma2(rx, ry, tc::bf16_trunc(rx), tc::bf16_trunc(ry), -1.f, -1.f, rx, ry);
-  t2 = tc::pack_bf16_rn(rx, ry);
+  asm("{\n\t.reg .b16 l, h, m;\n\t.reg .f32 rx, ry;\n\t"
+      "mov.b16 m, 0xBF80;\n\t"  // -1
+      "cvt.rn.bf16x2.f32 %0, %4, %3;\n\tmov.b32 {l, h}, %0;\n\t"
+      "fma.rn.f32.bf16 rx, l, m, %3;\n\tfma.rn.f32.bf16 ry, h, m, %4;\n\t"
+      "cvt.rn.bf16x2.f32 %1, ry, rx;\n\tmov.b32 {l, h}, %1;\n\t"
+      "fma.rn.f32.bf16 rx, l, m, rx;\n\tfma.rn.f32.bf16 ry, h, m, ry;\n\t"
+      "cvt.rn.bf16x2.f32 %2, ry, rx;\n\t}"
+      : "=&r"(t0), "=&r"(t1), "=r"(t2)
+      : "f"(x), "f"(y));
 }
 
 // ---- pieces of the tcgen05 kernels

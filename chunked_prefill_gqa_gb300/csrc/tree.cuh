@@ -161,38 +161,36 @@ __device__ __forceinline__ void cluster_merge(const TreeArgs& a, int first_row, 
                                               int threads) {
   __syncwarp();
   tc::cluster_sync_all();
-  for (int e = blockIdx.x * threads + tid; e < nrows * kGroup * 16; e += a.splits * threads) {  // (row, 4 dims)
-    const int r = e >> 4, d = (e & 15) * 4;
-    const uint32_t ml_at = tc::smem_u32(ml + r), row_at = tc::smem_u32(rows + r * stride + d);
-    float2 p[kMaxCluster];
-    float4 y[kMaxCluster];
-#pragma unroll
-    for (int s = 0; s < kMaxCluster; ++s)
-      if (s < a.splits) {
-        p[s] = ld_cluster2(tc::mapa_shared(ml_at, s));
-        y[s] = ld_cluster4(tc::mapa_shared(row_at, s));
-      }
-    float m = -INFINITY;
-#pragma unroll
-    for (int s = 0; s < kMaxCluster; ++s)
-      if (s < a.splits) m = fmaxf(m, p[s].x);
-    float den = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int s = 0; s < kMaxCluster; ++s)
-      if (s < a.splits) {
-        const float w = p[s].x == -INFINITY ? 0.f : ex2(p[s].x - m);
-        den = fmaf(w, p[s].y, den);
-        if (w != 0.f) {  // an empty segment's rows have no weight, whatever they hold
-          x.x = fmaf(w, y[s].x, x.x);
-          x.y = fmaf(w, y[s].y, x.y);
-          x.z = fmaf(w, y[s].z, x.z);
-          x.w = fmaf(w, y[s].w, x.w);
-        }
-      }
+  // A lane a segment, 2, 4 or 8 together an element (a row's 4 dims): the reads of
+  // other blocks' shared memory are what takes the time here.
+  const int bits = a.splits <= 2 ? 1 : a.splits <= 4 ? 2 : 3, lanes = 1 << bits;
+  const int s = tid & (lanes - 1), group = tid >> bits, groups = threads >> bits;
+  const int elements = nrows * kGroup * 16;
+  for (int e0 = blockIdx.x * groups; e0 < elements; e0 += a.splits * groups) {
+    const int e = min(e0 + group, elements - 1), r = e >> 4, d = (e & 15) * 4;
+    float2 p = make_float2(-INFINITY, 0.f);
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (s < a.splits) {
+      p = ld_cluster2(tc::mapa_shared(tc::smem_u32(ml + r), s));
+      y = ld_cluster4(tc::mapa_shared(tc::smem_u32(rows + r * stride + d), s));
+    }
+    float m = p.x;
+    for (int off = 1; off < lanes; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float w = p.x == -INFINITY ? 0.f : ex2(p.x - m);
+    float den = w * p.y;
+    // an empty segment's rows have no weight, whatever they hold
+    y = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(w * y.x, w * y.y, w * y.z, w * y.w);
+    for (int off = 1; off < lanes; off <<= 1) {
+      den += __shfl_xor_sync(0xffffffffu, den, off);
+      y.x += __shfl_xor_sync(0xffffffffu, y.x, off);
+      y.y += __shfl_xor_sync(0xffffffffu, y.y, off);
+      y.z += __shfl_xor_sync(0xffffffffu, y.z, off);
+      y.w += __shfl_xor_sync(0xffffffffu, y.w, off);
+    }
     const float inv = den == 0.f ? 0.f : 1.f / den;  // no key: zeros
-    *reinterpret_cast<float4*>(a.out + ((size_t)(first_row + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * kD + d) =
-        make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    if (s == 0 && e0 + group < elements)
+      *reinterpret_cast<float4*>(a.out + ((size_t)(first_row + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * kD + d) =
+          make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
   }
   __syncwarp();
   tc::cluster_sync_all();

@@ -395,16 +395,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         }
         return most;
       };
-      const float most = relative();
-      int over;
-      if (meet(kMeet, __any_sync(0xffffffffu, most > kTreeStale), failed, lane, &over)) {
-        failed = true;
-        break;
+      int over = 1;  // of the first tile it is known
+      if (n > 0) {
+        const float most = relative();
+        if (meet(kMeet, __any_sync(0xffffffffu, most > kTreeStale), failed, lane, &over)) {
+          failed = true;
+          break;
+        }
+        if (over) {
+          tmem_ld16(s_tmem, x);  // the scores again
+          tmem_wait_ld();
+        }
       }
       float alpha = 1.f;
       if (over) {
-        tmem_ld16(s_tmem, x);  // the scores again
-        tmem_wait_ld();
         float mine = -INFINITY;
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {
@@ -419,9 +423,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
         alpha = ex2(ref - next);
         ref = next;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) {
-          neg[j] = -__shfl_sync(0xffffffffu, next, j);
-          sum[j] *= __shfl_sync(0xffffffffu, alpha, j);
+        for (int j = 0; j < kCols; ++j) neg[j] = -__shfl_sync(0xffffffffu, next, j);
+        if (n > 0) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) sum[j] *= __shfl_sync(0xffffffffu, alpha, j);
         }
         relative();
       }
@@ -481,7 +486,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
 
     // ------------------------------------------------------------ epilogue
-    if (!failed && ntiles > 0) failed = !wait.warp(odone, (ntiles - 1) & 1);
     {
       // Sums over the warp's keys: halving the columns a lane holds each round,
       // lanes j and 16 + j end with column col0 + j.
@@ -496,6 +500,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       const float l = sum[0] + __shfl_xor_sync(0xffffffffu, sum[0], 16);
       const int c = col0 + (lane & 15);
       int over;
+      if (!failed && ntiles > 0) failed = !wait.warp(odone, (ntiles - 1) & 1);
       // The maxima of the last tile may still be read: meet before they become sums.
       if (meet(kMeet, false, failed, lane, &over)) goto done;
       if (lane < kCols) maxima[quarter * R + c] = l;

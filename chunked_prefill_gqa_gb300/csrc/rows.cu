@@ -145,9 +145,10 @@ rows_kernel(const RowArgs a) {
     int first = 0;
     const int b = find_sequence(a.row_start, a.B, n, lane, &first);
     if (b < 0 || b >= a.B) return;  // a row of no sequence: left as it is
-    token = (long long)__ldg(a.ctx_lens + b) + (n - first);
+    const long long row = (long long)n - first;
+    token = (long long)__ldg(a.ctx_lens + b) + row;
     slot = -1;
-    if (token >= n - first && token < (long long)a.max_blocks * ATTN_PAGE) {
+    if (token >= row && token < (long long)a.max_blocks * ATTN_PAGE) {
       const int page = __ldg(a.table + (size_t)b * a.max_blocks + token / ATTN_PAGE);
       if (page >= 0 && page < a.num_pages) slot = (long long)page * ATTN_PAGE + token % ATTN_PAGE;
     }

@@ -197,6 +197,18 @@ def test_append_skips_what_is_out_of_range(cp):
         assert torch.equal(pool.view(torch.int32), old.view(torch.int32))
 
 
+def test_append_with_a_row_start_far_below_zero(cp):
+    """Rows 2^31 and more behind their sequence's first: past the table, recorded, not stored."""
+    b = R.make_batch([(0, 3)])
+    before = b["kp"].clone()
+    k = torch.randn(3, 8, 64, device="cuda")
+    starts = torch.tensor([-2 ** 31, 3], dtype=torch.int32, device="cuda")
+    assert cp.attn_get_device_error() == 0
+    cp.attn_append_paged(k, k, b["kp"], b["vp"], b["table"], b["ctx"], starts)
+    assert cp.attn_get_device_error() == cp.ATTN_EBOUNDS
+    assert torch.equal(b["kp"].view(torch.int32), before.view(torch.int32))
+
+
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("lens", [[(0, 1)], [(5, 64), (16, 17), (0, 33), (100, 2), (7, 0)],
                                   [(40, 20)] * 37])

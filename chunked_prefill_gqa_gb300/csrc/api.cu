@@ -569,7 +569,7 @@ extern "C" int attn_append_paged_bf16kv(const void* q, const void* k, const void
 
 extern "C" size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxContext, int numSplits) {
   if (B <= 0 || N <= 0 || maxRows < 1 || maxRows > ATTN_TREE_ROWS || maxContext < 0 ||
-      maxContext > ATTN_MAX_TOKENS - maxRows || numSplits < 0 || B > 65535 || N > ATTN_MAX_TOKENS)
+      maxContext > ATTN_MAX_TOKENS || numSplits < 0 || B > 65535 || N > ATTN_MAX_TOKENS)
     return 0;
   size_t most = 0;
   for (int bf16 = 0; bf16 < 2; ++bf16) {  // either page type may be called with it

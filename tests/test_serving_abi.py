@@ -103,7 +103,7 @@ def test_tree(name, change, code):
 
 def test_tree_workspace_rejects_bad_sizes():
     for a in ((0, 3, 2, 60, 0), (2, 0, 2, 60, 0), (2, 3, 0, 60, 0), (2, 3, 65, 60, 0), (2, 3, 2, -1, 0),
-              (2, 3, 2, 60, -1), (70000, 3, 2, 60, 0), (2, 3, 2, cp.MAX_TOKENS, 0)):
+              (2, 3, 2, 60, -1), (70000, 3, 2, 60, 0), (2, 3, 2, cp.MAX_TOKENS + 1, 0)):
         assert cp.attn_tree_workspace_bytes(*a) == 0
 
 

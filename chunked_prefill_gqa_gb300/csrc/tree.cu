@@ -507,11 +507,19 @@ int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtenso
   const cuuint64_t dims[2] = {(cuuint64_t)kHKV * kD, (cuuint64_t)num_pages * ATTN_PAGE};
   const cuuint64_t strides[1] = {(cuuint64_t)kHKV * kD * (bf16 ? 2 : 4)};
   const cuuint32_t box[2] = {bf16 ? 64u : 32u, ATTN_PAGE};
-  if (enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base),
-          dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return ATTN_ETMA;
-  return ATTN_OK;
+  const auto encode = [&] {
+    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+               const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode();
+  int dev = 0;
+  // A thread whose first CUDA call this is has no context yet; a runtime call
+  // would bind one, the driver's encoder does not.
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
+    r = encode();
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ETMA;
 }
 
 // Variants by page type and drafted rows: up to 4, up to 8, more. Measured on 16

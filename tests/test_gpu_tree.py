@@ -82,6 +82,30 @@ def test_loose_bounds_change_nothing_but_the_segments(cp, bf16):
     check(run(cp, b, q, masks, bf16, max_rows=64, max_context=8000), *R.tree_reference(q, b, masks))
 
 
+LOOSE = {
+    "ragged": [((137 * i) % 900, (11 * i) % 65) for i in range(40)],
+    "short": [(3 * i, 1 + i % 7) for i in range(20)],
+    "one long": [(0, 0)] * 9 + [(9000, 33)] + [(1, 1), (0, 2)] * 6,
+    "alike": [(1024, 32)] * 24,
+}
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("kind", ["tree", "empty", "mixed"])
+@pytest.mark.parametrize("batch", list(LOOSE))
+def test_batches_far_below_their_bounds(cp, bf16, kind, batch):
+    """64 rows and 30000 tokens as bounds: most segments are empty, and a sequence
+    may end in any of them."""
+    lens = LOOSE[batch]
+    b = R.make_batch(lens, bf16=bf16, seed=17, extra_blocks=2000)
+    masks, q = R.tree_masks(lens, kind, seed=18), queries(b["n"], seed=19)
+    got = run(cp, b, q, masks, bf16, max_rows=64, max_context=30000, pad=2)
+    check(got, *R.tree_reference(q, b, masks))
+    again = run(cp, b, q, masks, bf16, max_rows=64, max_context=30000)
+    assert torch.equal(got, again)
+    assert cp.attn_get_device_error() == 0
+
+
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("rows", [1, 6, 20])
 def test_long_context(cp, bf16, rows):
@@ -151,17 +175,19 @@ def test_what_a_row_does_not_see_has_no_influence(cp, bf16, value, rows):
     check(got[blind], want[blind], tol[blind])
 
 
-def test_a_query_that_is_nan_stays_in_its_row(cp):
-    lens = [(300, 5)]
-    b = R.make_batch(lens, seed=62)
-    masks, q = R.tree_masks(lens, "chain"), queries(5, seed=5)
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("rows", [4, 5, 20])
+@pytest.mark.parametrize("splits", [1, 3, 20])
+def test_a_query_that_is_nan_stays_in_its_row(cp, bf16, rows, splits):
+    lens = [(3000, rows)]
+    b = R.make_batch(lens, bf16=bf16, seed=62)
+    masks, q = R.tree_masks(lens, "chain"), queries(rows, seed=5)
     want, tol = R.tree_reference(q, b, masks)
     q[3, 7, 0] = float("nan")
-    for splits in (1, 3):
-        got = run(cp, b, q, masks, False, splits)
-        assert torch.isnan(got[3, 7]).all()
-        got[3, 7] = want[3, 7].float()
-        check(got, want, tol + 1e-7)
+    got = run(cp, b, q, masks, bf16, splits)
+    assert torch.isnan(got[3, 7]).all()
+    got[3, 7] = want[3, 7].float()
+    check(got, want, tol + 1e-7)
 
 
 @pytest.mark.parametrize("bf16", [False, True])
@@ -218,6 +244,11 @@ def test_workspace_is_checked(cp):
         assert e.value.code == cp.ATTN_ESPACE
 
 
+def test_workspace_of_the_longest_context(cp):
+    """attn_tree_paged takes a bound of ATTN_MAX_TOKENS; the size is there for it too."""
+    assert cp.attn_tree_workspace_bytes(2, 9, 5, cp.MAX_TOKENS, 20) == 9 * 32 * 20 * 66 * 4
+
+
 def test_pools_past_32_bit_offsets(cp):
     """Pages whose bytes lie past 4 GiB of their pool."""
     lens = [(200, 5)]
@@ -272,6 +303,94 @@ def test_streams_and_graph_replay(cp, bf16, splits):
     for b, masks, q, out, *_ in made:
         check(out, *R.tree_reference(q, b, masks.cpu().numpy()))
     assert cp.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_calls_from_several_threads(cp, bf16):
+    """Four threads, each with its own stream, batch and workspace."""
+    import threading
+    lens = [(900, 6), (300, 3), (2500, 4)]
+    call = cp.attn_tree_paged_bf16kv if bf16 else cp.attn_tree_paged
+    need = cp.attn_tree_workspace_bytes(3, 13, 6, 2500, 12)
+    made = []
+    for s in range(4):
+        b, masks = R.make_batch(lens, bf16=bf16, seed=110 + s), R.tree_masks(lens, seed=s)
+        made.append((b, masks, torch.from_numpy(masks).cuda(), queries(13, seed=s),
+                     torch.empty(13, 32, 64, device="cuda"), torch.empty(need, dtype=torch.uint8, device="cuda"),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(b, m, q, out, ws, st):
+        for splits in (12, 0, 1, 12):
+            call(q, b["kp"], b["vp"], b["table"], b["ctx"], b["starts"], m, out, 6, 2500, splits, ws, stream=st)
+
+    threads = [threading.Thread(target=work, args=(b, *rest)) for b, _, *rest in made]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for b, masks, _, q, out, *_ in made:
+        check(out, *R.tree_reference(q, b, masks))
+    assert cp.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("rows", [2, 7, 20])
+def test_beside_a_prefill_on_another_stream(cp, rows):
+    """Blocks of the bf16 prefill and of the tree kernels share SMs, shared and tensor memory."""
+    lens = [(3000, rows)] * 3
+    b = R.make_batch(lens, bf16=True, seed=120)
+    masks, q = R.tree_masks(lens, seed=1), queries(3 * rows, seed=2)
+    m, out = torch.from_numpy(masks).cuda(), torch.empty_like(q)
+    need = cp.attn_tree_workspace_bytes(3, 3 * rows, rows, 3000, 0)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    pq = torch.randn(96, 32, 64, device="cuda")
+    pk, pv = (torch.randn(2096, 8, 64, device="cuda").bfloat16() for _ in range(2))
+    pout, want = torch.empty_like(pq), torch.empty_like(pq)
+    cp.attn_prefill_bf16kv(pq, pk, pv, want, 2000)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        cp.attn_prefill_bf16kv(pq, pk, pv, pout, 2000, stream=streams[0])
+        cp.attn_tree_paged_bf16kv(q, b["kp"], b["vp"], b["table"], b["ctx"], b["starts"], m, out, rows, 3000, 0, ws,
+                                  stream=streams[1])
+    torch.cuda.synchronize()
+    assert torch.equal(pout, want)
+    check(out, *R.tree_reference(q, b, masks))
+    assert cp.attn_get_device_error() == 0
+
+
+FIRST_CALLS = """
+import torch
+import chunked_prefill_gqa_gb300 as cp
+F, I = dict(device="cuda"), dict(device="cuda", dtype=torch.int32)
+k, q, out = torch.randn(4, 8, 64, **F), torch.randn(4, 32, 64, **F), torch.empty(4, 32, 64, **F)
+kp, vp = torch.zeros(6, 16, 8, 64, **F), torch.zeros(6, 16, 8, 64, **F)
+table, ctx, starts = torch.arange(6, **I).view(2, 3), torch.zeros(2, **I), torch.tensor([0, 1, 4], **I)
+keep, counts, cs = torch.zeros(2, 1, **I), torch.ones(2, **I), torch.empty(8, 64, **F)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    cp.attn_rope_table(cs)
+    cp.attn_append_paged(k, k, kp, vp, table, ctx, starts, cs, q=q, qOut=q)
+    cp.attn_tree_paged(q, kp, vp, table, ctx, starts, None, out, 3, 20)
+    cp.attn_compact_paged(kp, vp, table, ctx, keep, counts, 3)
+g.replay()
+torch.cuda.synchronize()
+v = k[0][:, None].expand(8, 4, 64)  # one key: its value, whose product keeps all but 2^-19 of it
+assert ((out[0].view(8, 4, 64) - v).abs() <= 2.0 ** -19 * v.abs()).all()
+assert cp.attn_get_device_error() == 0
+print("captured")
+"""
+
+
+def test_first_calls_inside_a_capture(cp):
+    """A process whose first calls of the library are captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
 
 
 @pytest.mark.parametrize("bf16", [False, True])

@@ -95,8 +95,8 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
 
   const Seq seq = load_seq(a, b);
   const int nrows = seq.rows;  // of at most four
-  const int k0 = s * a.split_len;
-  const int k1 = min(k0 + a.split_len, seq.keys);
+  const int len = segment_len(a, seq), k0 = s * len;
+  const int k1 = min(k0 + len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   if (nrows <= 0) return;
   // Early: the merge's blocks may take their places; they wait for all of this grid.

@@ -59,6 +59,16 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b) {
   return s;
 }
 
+// Keys of a segment. Where the segments of a unit are one cluster, which holds its
+// SMs until the last of them ends, a sequence's own keys are cut evenly (48
+// sequences of 1 to 4096 tokens: five rows on bf16 pages 72 to 59 us, one row on
+// fp32 pages 132 to 105); otherwise the call's length counts, and blocks past a
+// short sequence's end leave at once.
+__device__ __forceinline__ int segment_len(const TreeArgs& a, const Seq& s) {
+  if (!a.cluster) return a.split_len;
+  return ((s.keys + a.splits - 1) / a.splits + 127) / 128 * 128;
+}
+
 // Three bf16 terms of a pair, each rounded to nearest: 24 bits, all of an fp32
 // value whose last term does not underflow. The remainders, exact, come from
 // fused products of bf16 operands into fp32 (t * -1 + x), one instruction where
@@ -161,36 +171,37 @@ __device__ __forceinline__ void cluster_merge(const TreeArgs& a, int first_row, 
                                               int threads) {
   __syncwarp();
   tc::cluster_sync_all();
-  // A lane a segment, 2, 4 or 8 together an element (a row's 4 dims): the reads of
-  // other blocks' shared memory are what takes the time here.
-  const int bits = a.splits <= 2 ? 1 : a.splits <= 4 ? 2 : 3, lanes = 1 << bits;
-  const int s = tid & (lanes - 1), group = tid >> bits, groups = threads >> bits;
+  // A thread an element (4 dims of a row), all segments' loads on their way at once,
+  // a warp's from one block's shared memory each. (A lane a segment, in pieces of 64
+  // bytes a block, took 17.2 us where this takes 12.7: 32 drafted rows, 1000 tokens,
+  // eight segments; 9.4 and 9.0 with 8 rows.)
   const int elements = nrows * kGroup * 16;
-  for (int e0 = blockIdx.x * groups; e0 < elements; e0 += a.splits * groups) {
-    const int e = min(e0 + group, elements - 1), r = e >> 4, d = (e & 15) * 4;
-    float2 p = make_float2(-INFINITY, 0.f);
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (s < a.splits) {
-      p = ld_cluster2(tc::mapa_shared(tc::smem_u32(ml + r), s));
-      y = ld_cluster4(tc::mapa_shared(tc::smem_u32(rows + r * stride + d), s));
+  for (int e = blockIdx.x * threads + tid; e < elements; e += a.splits * threads) {
+    const int r = e >> 4, d = (e & 15) * 4;
+    float2 p[kMaxCluster];
+    float4 y[kMaxCluster];
+    float m = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s) {
+      p[s] = make_float2(-INFINITY, 0.f);
+      if (s < a.splits) {
+        p[s] = ld_cluster2(tc::mapa_shared(tc::smem_u32(ml + r), s));
+        y[s] = ld_cluster4(tc::mapa_shared(tc::smem_u32(rows + r * stride + d), s));
+      }
+      m = fmaxf(m, p[s].x);
     }
-    float m = p.x;
-    for (int off = 1; off < lanes; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float w = p.x == -INFINITY ? 0.f : ex2(p.x - m);
-    float den = w * p.y;
-    // an empty segment's rows have no weight, whatever they hold
-    y = w == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(w * y.x, w * y.y, w * y.z, w * y.w);
-    for (int off = 1; off < lanes; off <<= 1) {
-      den += __shfl_xor_sync(0xffffffffu, den, off);
-      y.x += __shfl_xor_sync(0xffffffffu, y.x, off);
-      y.y += __shfl_xor_sync(0xffffffffu, y.y, off);
-      y.z += __shfl_xor_sync(0xffffffffu, y.z, off);
-      y.w += __shfl_xor_sync(0xffffffffu, y.w, off);
+    float den = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kMaxCluster; ++s) {
+      const float w = p[s].x == -INFINITY ? 0.f : ex2(p[s].x - m);
+      den = fmaf(w, p[s].y, den);
+      if (w != 0.f)  // an empty segment's rows have no weight, whatever they hold
+        x = make_float4(fmaf(w, y[s].x, x.x), fmaf(w, y[s].y, x.y), fmaf(w, y[s].z, x.z), fmaf(w, y[s].w, x.w));
     }
     const float inv = den == 0.f ? 0.f : 1.f / den;  // no key: zeros
-    if (s == 0 && e0 + group < elements)
-      *reinterpret_cast<float4*>(a.out + ((size_t)(first_row + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * kD + d) =
-          make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);
+    *reinterpret_cast<float4*>(a.out + ((size_t)(first_row + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * kD + d) =
+        make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
   }
   __syncwarp();
   tc::cluster_sync_all();

@@ -110,8 +110,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: descriptors in uniform registers
   const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
 
-  // The table's first entries are on their way while the lengths are: an entry
-  // past the sequence is read and not used.
+  // The table's first entries are on their way while the lengths are, as of a
+  // sequence as long as the call allows: an entry past the sequence is read and not
+  // used.
   const int first_page = s * (a.split_len / ATTN_PAGE) + lane;
   int first_entries = -1;
   if (warp == L::kTmaWarp && first_page < a.max_blocks)
@@ -119,8 +120,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   const Seq seq = load_seq(a, b);
   const int i0 = rt * (R / 4);  // the block's first drafted row
   const int nrows = min(R / 4, seq.rows - i0);
-  const int k0 = s * a.split_len;
-  const int k1 = min(k0 + a.split_len, seq.keys);
+  const int len = segment_len(a, seq), k0 = s * len;
+  const int k1 = min(k0 + len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   if (nrows <= 0) return;
   // Early: the merge's blocks may take their places; they wait for all of this grid.
@@ -204,7 +205,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
     __syncwarp();
     // The first tile is on its way before the block has met.
-    entries = first_entries;
+    entries = len == a.split_len ? first_entries : entry_at(0);
     entries_next = entry_at(1);
     if (ntiles > 0) load(&mk, kfull, 0, 0);
   } else if (warp == L::kMmaWarp) {

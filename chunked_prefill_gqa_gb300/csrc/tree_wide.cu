@@ -85,16 +85,17 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
 
-  // The table's first entries are on their way while the lengths are: an entry
-  // past the sequence is read and not used.
+  // The table's first entries are on their way while the lengths are, as of a
+  // sequence as long as the call allows: an entry past the sequence is read and not
+  // used.
   const int first_page = s * (a.split_len / ATTN_PAGE) + lane;
   int first_entries = -1;
   if ((warp == L::kKWarp || warp == L::kVWarp) && first_page < a.max_blocks) first_entries = __ldg(a.table + (size_t)b * a.max_blocks + first_page);
   const Seq seq = load_seq(a, b);
   const int i0 = rt * kRows;  // the block's first drafted row
   const int nrows = min(kRows, seq.rows - i0);
-  const int k0 = s * a.split_len;
-  const int k1 = min(k0 + a.split_len, seq.keys);
+  const int len = segment_len(a, seq), k0 = s * len;
+  const int k1 = min(k0 + len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   if (nrows <= 0) return;
   // Early: the merge's blocks may take their places; they wait for all of this grid.
@@ -174,11 +175,11 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     }
     __syncwarp();
     // The first tiles are on their way before the block has met.
-    entries = first_entries;
+    entries = len == a.split_len ? first_entries : entry_at(0);
     entries_next = entry_at(1);
     if (ntiles > 0) load(&mk, kfull, 0, 0);
   } else if (warp == L::kVWarp) {
-    entries = first_entries;
+    entries = len == a.split_len ? first_entries : entry_at(0);
     entries_next = entry_at(1);
   } else if (warp == L::kQkWarp) {
     tmem_alloc(words, 512);

@@ -15,8 +15,12 @@
 // and stores are 16 bytes a lane (8 from or to bf16), the sum of squares is
 // four shuffles, a halves pair sits eight lanes away and a neighbours pair in
 // the lane itself. The cos and sin of a row are read once per warp. Nothing is
-// staged in shared memory: every byte is used once, so the bound is memory
-// (latency for a few rows).
+// staged in shared memory: every byte is used once, so the bound is memory, and
+// for a few rows the launch and a chain of dependent loads (the row's sequence, its
+// context, its page or angles). Measured, inputs in HBM: 8192 fp32 rows appended
+// with their queries 33.2 us (201 MB, 6.1 TB/s), normed and rotated alone 27.1
+// (168 MB, 6.2 TB/s); 2048 bf16 rows 9.4 and 7.5; 16 rows 3.0 and 2.4, nearly all
+// of it the launch.
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -25,7 +29,11 @@
 namespace attn {
 namespace {
 
-constexpr int kRowWarps = 8;
+// 12 blocks of 4 warps an SM (40 registers a thread): a chunk's rows wait for the
+// lookups of where they go, so as many warps as fit wait at once, with bf16 heads
+// held as loaded until then. (2048 bf16 rows appended with their queries: 9.4 us;
+// 10.8 with 44 registers and heads widened as they land, 11.0 in blocks of 8 warps.)
+constexpr int kRowWarps = 4, kRowBlocks = 12;
 constexpr int kHeadsPerWarp = 8;
 constexpr int kQChunks = kHQ / kHeadsPerWarp;  // 4 warps for a row's queries, one for its keys, one for its values
 constexpr unsigned kFull = 0xffffffffu;
@@ -39,10 +47,12 @@ struct Elem<true> {
   using type = __nv_bfloat16;
 };
 
-// Four consecutive values as fp32. Plain loads: a call may run in place.
+// Four consecutive values, and what they are in fp32. Plain loads: a call may run
+// in place.
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
+__device__ __forceinline__ uint2 load4(const __nv_bfloat16* p) { return *reinterpret_cast<const uint2*>(p); }
+__device__ __forceinline__ float4 widen(float4 v) { return v; }
+__device__ __forceinline__ float4 widen(uint2 u) {
   return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                      __uint_as_float(u.y & 0xffff0000u));
 }
@@ -121,13 +131,13 @@ struct RowArgs {
 };
 
 template <bool kInBf16, bool kOutBf16, bool kPaged>
-__global__ void __launch_bounds__(32 * kRowWarps)
+__global__ void __launch_bounds__(32 * kRowWarps, kRowBlocks)
 rows_kernel(const RowArgs a) {
   using In = typename Elem<kInBf16>::type;
   using Out = typename Elem<kOutBf16>::type;
-  const long long item = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+  const unsigned item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);  // 6 x ATTN_MAX_TOKENS at most
   const int lane = threadIdx.x & 31, sub = lane & 15, d = 4 * sub;
-  const int n = (int)(item / a.chunks), chunk = (int)(item % a.chunks);
+  const int n = (int)(item / (unsigned)a.chunks), chunk = (int)(item % (unsigned)a.chunks);
   if (n >= a.N) return;
 
   const bool is_q = chunk < a.q_chunks, is_k = chunk == a.q_chunks;
@@ -135,37 +145,39 @@ rows_kernel(const RowArgs a) {
   const In* src = is_q ? static_cast<const In*>(a.q) + (size_t)n * a.q_stride + chunk * kHeadsPerWarp * kD
                   : is_k ? static_cast<const In*>(a.k) + (size_t)n * a.k_stride
                          : static_cast<const In*>(a.v) + (size_t)n * a.v_stride;
-  float4 x[kHeadsPerWarp / 2];
+  src += (lane >> 4) * kD + d;
+  decltype(load4(src)) raw[kHeadsPerWarp / 2];
 #pragma unroll
-  for (int i = 0; i < kHeadsPerWarp / 2; ++i) x[i] = load4(src + (2 * i + (lane >> 4)) * kD + d);
+  for (int i = 0; i < kHeadsPerWarp / 2; ++i) raw[i] = load4(src + 2 * i * kD);
 
-  long long token = 0;
-  long long slot = n;  // row of the destination
+  int position = 0;  // where nothing else says: its token
+  int slot = n;      // row of the destination
   if (kPaged) {
     int first = 0;
     const int b = find_sequence(a.row_start, a.B, n, lane, &first);
     if (b < 0 || b >= a.B) return;  // a row of no sequence: left as it is
-    const long long row = (long long)n - first;
-    token = (long long)__ldg(a.ctx_lens + b) + row;
+    const long long row = (long long)n - first, token = __ldg(a.ctx_lens + b) + row;
     slot = -1;
     if (token >= row && token < (long long)a.max_blocks * ATTN_PAGE) {
       const int page = __ldg(a.table + (size_t)b * a.max_blocks + token / ATTN_PAGE);
-      if (page >= 0 && page < a.num_pages) slot = (long long)page * ATTN_PAGE + token % ATTN_PAGE;
+      if (page >= 0 && page < a.num_pages) slot = page * ATTN_PAGE + (int)token % ATTN_PAGE;
     }
+    position = (int)min(max(token, -1ll), (long long)ATTN_MAX_TOKENS);
     if (slot < 0 && lane == 0) record_error(a.err, kDevErrBounds);
   }
 
+  float4 x[kHeadsPerWarp / 2];
   if (is_q || is_k) {
     const float* weight = is_q ? a.q_weight : a.k_weight;
     const float4 w = weight ? __ldg(reinterpret_cast<const float4*>(weight + d)) : make_float4(1.f, 1.f, 1.f, 1.f);
     Angles t{};
     if (a.cos_sin) {
-      long long pos = a.positions ? (long long)__ldg(a.positions + n) : token;
-      if (pos < 0 || pos >= a.num_positions) {
+      if (a.positions) position = __ldg(a.positions + n);
+      if (position < 0 || position >= a.num_positions) {
         if (lane == 0) record_error(a.err, kDevErrBounds);
-        pos = pos < 0 ? 0 : a.num_positions - 1;
+        position = position < 0 ? 0 : a.num_positions - 1;
       }
-      const float* row = a.cos_sin + (size_t)pos * kD;
+      const float* row = a.cos_sin + (size_t)position * kD;
       if (a.pairing == ATTN_ROPE_PAIRS) {
         const float2 c = __ldg(reinterpret_cast<const float2*>(row + 2 * sub));
         const float2 s = __ldg(reinterpret_cast<const float2*>(row + kD / 2 + 2 * sub));
@@ -179,17 +191,20 @@ rows_kernel(const RowArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < kHeadsPerWarp / 2; ++i)
-      x[i] = norm_rotate(x[i], w, weight != nullptr, t, a.cos_sin != nullptr, a.pairing, a.eps);
+      x[i] = norm_rotate(widen(raw[i]), w, weight != nullptr, t, a.cos_sin != nullptr, a.pairing, a.eps);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kHeadsPerWarp / 2; ++i) x[i] = widen(raw[i]);
   }
 
   if (is_q) {
-    float* dst = a.q_out + ((size_t)n * kHQ + chunk * kHeadsPerWarp) * kD + d;
+    float* dst = a.q_out + ((size_t)n * kHQ + chunk * kHeadsPerWarp + (lane >> 4)) * kD + d;
 #pragma unroll
-    for (int i = 0; i < kHeadsPerWarp / 2; ++i) store4(dst + (2 * i + (lane >> 4)) * kD, x[i]);
+    for (int i = 0; i < kHeadsPerWarp / 2; ++i) store4(dst + 2 * i * kD, x[i]);
   } else if (slot >= 0) {
-    Out* dst = static_cast<Out*>(is_k ? a.k_out : a.v_out) + (size_t)slot * (kHKV * kD) + d;
+    Out* dst = static_cast<Out*>(is_k ? a.k_out : a.v_out) + ((size_t)slot * kHKV + (lane >> 4)) * kD + d;
 #pragma unroll
-    for (int i = 0; i < kHeadsPerWarp / 2; ++i) store4(dst + (2 * i + (lane >> 4)) * kD, x[i]);
+    for (int i = 0; i < kHeadsPerWarp / 2; ++i) store4(dst + 2 * i * kD, x[i]);
   }
 }
 
@@ -228,7 +243,8 @@ __global__ void rope_table_kernel(const __grid_constant__ Frequencies inv, float
 // moves to row i, for K (pool 0) or V (pool 1); a thread owns 16 bytes of every
 // row. keep rises strictly, so keep[i] >= i and a row is read before any store
 // reaches it, also with eight rows' loads in flight at once: their stores go to
-// rows below every later source.
+// rows below every later source. At most 64 rows of 2 or 4 KB a sequence: the
+// launch and three dependent loads are all of it (2.3 us for 16 sequences).
 constexpr int kKeepAhead = 8;
 
 __global__ void compact_kernel(uint4* k_pages, uint4* v_pages, int row_vecs, const int* table, const int* ctx_lens,

@@ -104,6 +104,7 @@ cudaError_t launch_compact(void* k_pages, void* v_pages, int type, const int* ta
 // Attention of drafted rows over a paged cache (tree.cu): how a call is cut into
 // key segments, the workspace of its partials, launch. int results are ATTN_* codes.
 struct TreePlan {
+  int variant;  // which kernel of the page type
   int splits, split_len;
   bool cluster;  // the segments of a unit are one cluster: no partials in memory
 };

@@ -43,7 +43,7 @@ constexpr int kMaxSplits = 64;
 
 constexpr int kWarps = 4;
 constexpr int kStages = 3;                       // pages of a warp in flight: 96 KB a block, two blocks an SM
-constexpr int kRows = 16;
+constexpr int kRows = 16, kTokens = kRows / kGroup;  // query rows, drafted rows
 constexpr int kRowStride = kD + 4;
 constexpr uint32_t kBox = ATTN_PAGE * 128;       // 32 dims of 16 tokens
 constexpr uint32_t kStage = 4 * kBox;            // a page of K, then of V
@@ -91,10 +91,11 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   uint8_t* const smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, c = lane & 3;  // fragment row (or key), fragment column
-  const int s = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
+  const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
 
   const Seq seq = load_seq(a, b);
-  const int nrows = seq.rows;  // of at most four
+  const int i0 = rt * kTokens;  // the block's first drafted row
+  const int nrows = min(kTokens, seq.rows - i0);
   const int len = segment_len(a, seq), k0 = s * len;
   const int k1 = min(k0 + len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
@@ -106,7 +107,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     // sequence without any key (only a refused one) gets zeros.
     if (s == 0)
       for (int e = tid; e < nrows * kGroup * kD; e += 32 * kWarps)
-        a.out[((size_t)(seq.first + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
+        a.out[((size_t)(seq.first + i0 + e / (kGroup * kD)) * kHQ + head * kGroup) * kD + e % (kGroup * kD)] = 0.f;
     return;
   }
   const bool whole = !a.cluster && seq.keys <= a.split_len;  // one segment: the output is written here
@@ -119,10 +120,10 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
     tc::fence_mbar_init();
   }
-  if (tid < 4)
+  if (tid < kTokens)
     masks[tid] = tid >= nrows ? 0ull
-                 : a.masks    ? (unsigned long long)__ldg(a.masks + seq.first + tid)
-                              : ~0ull >> (63 - tid);
+                 : a.masks    ? (unsigned long long)__ldg(a.masks + seq.first + i0 + tid)
+                              : ~0ull >> (63 - (i0 + tid));
   __syncwarp();
 
   // This warp's pages: pages warp, warp + kWarps, ... of the segment. Lane l
@@ -163,7 +164,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       const int i = 2 * h + (g >> 2);
       float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < nrows)
-        u = __ldg(reinterpret_cast<const float4*>(a.q + ((size_t)(seq.first + i) * kHQ + head * kGroup + (g & 3)) * kD +
+        u = __ldg(reinterpret_cast<const float4*>(a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (g & 3)) * kD +
                                                   16 * j + 4 * c));
       x[h][0] = u.x, x[h][1] = u.y, x[h][2] = u.z, x[h][3] = u.w;
     }
@@ -409,7 +410,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       x.z = fmaf(wt, y.z, x.z);
       x.w = fmaf(wt, y.w, x.w);
     }
-    const size_t at = (size_t)(seq.first + row / kGroup) * kHQ + head * kGroup + row % kGroup;
+    const size_t at = (size_t)(seq.first + i0 + row / kGroup) * kHQ + head * kGroup + row % kGroup;
     // after a failed wait the segment counts as empty
     const float2 end = any_failed ? make_float2(-INFINITY, 0.f) : make_float2(m, den);
     if (a.cluster) {
@@ -424,7 +425,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       if (d == 0) reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD)[at * a.splits + s] = end;
     }
   }
-  if (a.cluster) cluster_merge(a, seq.first, nrows, head, rows, kRowStride, ends, tid, 32 * kWarps);
+  if (a.cluster) cluster_merge(a, seq.first + i0, nrows, head, rows, kRowStride, ends, tid, 32 * kWarps);
 }
 
 // Merge of segments that are not one cluster: a warp per (drafted row, query
@@ -522,16 +523,24 @@ int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtenso
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ETMA;
 }
 
-// Variants by page type and drafted rows: up to 4, up to 8, more. Measured on 16
-// sequences of 16384 tokens: bf16 pages, 8 rows, tree_tc 101 us and tree_wide 140;
-// 16 rows, 175 (as two tiles of 8: 200) and 143. fp32 pages, 4 rows, the kernel here
-// 205 us and tree_wide 250; 8 rows, 312 and 250.
+// Variants by page type and the drafted rows of a block. Long calls take the least
+// that holds their rows. Measured on 16 sequences of 16384 tokens: bf16 pages, 8 rows,
+// tree_tc 99 us and tree_wide 140; 16 rows, 175 (as two tiles of 8: 200) and 142. fp32
+// pages, 4 rows, the kernel here 202 us and tree_wide 250; 8 rows, 312 and 251.
+// A small call is another matter: where a block for every 128 keys of every tile of
+// few rows has its place at once, reading a page for each of those tiles costs less
+// than the longer way through a wide block: one sequence of 1000 tokens with 8 rows
+// on fp32 pages 7.7 and 9.0 us, with 16 8.2 and 9.6; with 16 rows on bf16 pages 8.5
+// and 9.2. With four sequences more blocks than places: 11.1 and 11.3, 16.8 and 11.8,
+// 10.4 and 10.7. On bf16 pages a third more blocks than places still pay (384 of 304:
+// eight sequences of 300 tokens with 16 rows 7.9 and 9.4, one of 2000 with 24 10.0 and
+// 11.1; 576: two of 1000 with 32 12.1 and 11.2); on fp32 pages it depends (384: four
+// of 300 with 16 rows 9.1 and 11.0, sixteen of 60 11.4 and 8.2).
 using Variant = TreeVariant;
-const Variant kNarrow = {tree_narrow_kernel, 4, 32 * kWarps, kSmemAlloc, kBlocks, false, 0};
-const Variant kVariants[2][3] = {{kNarrow, tree_wide_variant(false), tree_wide_variant(false)},
+const Variant kNarrow = {tree_narrow_kernel, kTokens, 32 * kWarps, kSmemAlloc, kBlocks, false, 0};
+constexpr int kCount[2] = {2, 3};
+const Variant kVariants[2][3] = {{kNarrow, tree_wide_variant(false)},
                                  {tree_tc_variant(4), tree_tc_variant(8), tree_wide_variant(true)}};
-
-int variant_of(int max_rows) { return max_rows <= 4 ? 0 : max_rows <= 8 ? 1 : 2; }
 
 // Per device and variant: how many blocks fit at once, and how many clusters of
 // each size.
@@ -552,7 +561,7 @@ int tree_device(TreeDevice** out) {
     int sms = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return ATTN_ECUDA;
     for (int t = 0; t < 2; ++t)
-      for (int v = 0; v < 3; ++v) {
+      for (int v = 0; v < kCount[t]; ++v) {
         const Variant& x = kVariants[t][v];
         if (cudaFuncSetAttribute(x.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.smem) != cudaSuccess)
           return ATTN_ECUDA;
@@ -601,7 +610,17 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
   TreeDevice* d = nullptr;
   const int rc = tree_device(&d);
   if (rc != ATTN_OK) return rc;
-  const int v = variant_of(max_rows);
+  auto small = [&](int v) {  // a block for every 128 keys of every row tile, nearly all at once
+    const int tokens = kVariants[bf16][v].tokens, slots = d->slots[bf16][v];
+    return (long long)B * ((max_context + max_rows + 127) / 128) * kHKV * ((max_rows + tokens - 1) / tokens) <=
+           (bf16 ? slots + slots / 3 : slots);
+  };
+  int v = 0;
+  if (bf16)
+    v = max_rows <= kVariants[1][0].tokens ? 0 : max_rows <= kVariants[1][1].tokens || small(1) ? 1 : 2;
+  else
+    v = max_rows <= kTokens || small(0) ? 0 : 1;
+  plan->variant = v;
   const int* const clusters = d->clusters[bf16][v];
   const int keys = max_context + max_rows;
   int n = splits_hint < kMaxSplits ? splits_hint : kMaxSplits;
@@ -642,7 +661,7 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
   int rc = tree_device(&d);
   if (rc != ATTN_OK) return rc;
   const bool bf16 = c.type == ATTN_BF16;
-  const Variant& x = kVariants[bf16][variant_of(c.max_rows)];
+  const Variant& x = kVariants[bf16][c.plan.variant];
   alignas(64) CUtensorMap mk, mv;
   if ((rc = encode_pool(c.k_pages, c.num_pages, bf16, false, &mk)) != ATTN_OK ||
       (rc = encode_pool(c.v_pages, c.num_pages, bf16, x.v_atom32, &mv)) != ATTN_OK)

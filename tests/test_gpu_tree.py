@@ -59,6 +59,19 @@ def test_sizes(cp, bf16, rows, ctx):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("rows", [5, 8, 9, 16, 17, 31, 33, 64])
+@pytest.mark.parametrize("ctx", [0, 1, 15, 16, 129, 1000])
+@pytest.mark.parametrize("splits", [1, 5])
+def test_sizes_below_a_long_bound(cp, bf16, rows, ctx, splits):
+    """The kernels of calls that allow long contexts, at the short ones."""
+    lens = [(ctx, rows)]
+    b = R.make_batch(lens, bf16=bf16, seed=rows * 7 + ctx, extra_blocks=1100)
+    q, masks = queries(rows, seed=ctx), R.tree_masks(lens, seed=rows)
+    check(run(cp, b, q, masks, bf16, splits, max_context=17000), *R.tree_reference(q, b, masks))
+    assert cp.attn_get_device_error() == 0
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("kind", ["tree", "chain", "self", "empty", "mixed", "null"])
 @pytest.mark.parametrize("splits", [0, 1, 3, 8, 64])
 def test_ragged_batch_masks_and_splits(cp, bf16, kind, splits):

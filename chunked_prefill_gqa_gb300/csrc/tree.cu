@@ -11,6 +11,7 @@
 //   bf16 pages, up to 8 drafted rows: tree_tc.cu (keys on the M side of tcgen05)
 //   more rows, and fp32 pages from 5 on: tree_wide.cu (rows on the M side)
 //   fp32 pages, up to 4 rows: the kernel here
+// (small calls with more rows take several blocks of the first and last kind)
 // This file also holds what they share on the host: how a call is cut into key
 // segments, the launch, and the merge of segments that are not one cluster, with
 // the split-K rule m = max m_s, out = sum e^(m_s - m) O_s / sum e^(m_s - m) l_s.
@@ -25,6 +26,8 @@
 // registers. The reference maximum of a row moves only when a score passes it by
 // 2^8 (p stays below 2^8, far from fp32's range), so in the steady state a page
 // costs one vote instead of a reduction over lanes and a rescaled accumulator.
+// Bound: HBM, and the two blocks that 16 sequences of 16384 tokens leave each of 128
+// SMs: 1.07 GB in 200 us, 5.4 TB/s (4 rows: 201; the mma.sync pipe is 46% active).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -27,6 +27,10 @@
 // table, 8 boxes each of K and V a tile); one thread for the MMAs. S(n+1) is
 // issued as soon as S(n) has been read into registers, so it runs under the
 // softmax of tile n, and PV(n) under the first half of that of tile n + 1.
+//
+// Bound: HBM up to 4 rows; with 8 also the softmax's own instructions. 16 sequences of
+// 16384 tokens (537 MB): 1 to 4 rows 87 us (6.2 TB/s), 8 rows 99 us (5.4 TB/s; issue
+// slots 51% used, tensor pipe 36%), two blocks an SM in both.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

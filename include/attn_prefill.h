@@ -420,13 +420,15 @@ int attn_append_paged_bf16kv(const void *q, const void *k, const void *v, int in
  * its output not finite. Slots past a sequence's last row may hold anything.
  * q stays in fp32 precision on both caches (bf16 pages are used as stored, q and
  * the probabilities split into three bf16 terms).
- * numSplits: segments per sequence, 0 = chosen so that the blocks fill the
- * device (segments of at least 128 keys, at most 64 of them; larger hints count
- * as 64). With more than one segment the partials need `workspace`, a device
+ * numSplits: segments per sequence, 0 = chosen from the sizes and bounds so that
+ * the blocks fill the device (segments of at least 128 keys, at most 64 of them;
+ * larger hints count as 64). Up to eight segments run as one cluster of blocks and
+ * merge in shared memory; with more their partials need `workspace`, a device
  * buffer of at least attn_tree_workspace_bytes(B, N, maxRows, maxContext,
  * numSplits) bytes, 16-byte aligned, owned by the caller, overwritten by the
  * call; calls that may overlap (other streams, graphs that run at the same
- * time) need one each. Nothing in it needs to start at zero.
+ * time) need one each. Nothing in it needs to start at zero. Where that size is 0
+ * the workspace may be NULL.
  * A context length outside [0, maxContext], rows that run past N, 16 *
  * maxBlocks tokens or maxRows, and a page index outside [0, numPages) are
  * recorded as ATTN_EBOUNDS and clamped / read as zeros. Errors: ATTN_EINVAL
@@ -446,8 +448,8 @@ int attn_tree_paged_bf16kv(const float *q, const uint16_t *kPages, const uint16_
 
 /*
  * attn_tree_workspace_bytes -- the workspace the two calls above need for the
- * same sizes on the current device (enough for either); 0 when one segment
- * suffices (or for invalid arguments).
+ * same sizes on the current device (enough for either); 0 when none is needed
+ * (one segment, or segments that merge in shared memory) or for invalid arguments.
  */
 size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxContext, int numSplits);
 

@@ -79,6 +79,30 @@ int launch_tc_bf16x3(const Problem& p, cudaStream_t stream);
 // Paged K/V: p.k / p.v point at [num_pages * 16][8][64] page pools.
 int launch_tc_paged(const Problem& p, const int* table, int num_pages, cudaStream_t stream);
 
+#ifdef __CUDACC__
+// A launch that may be prepared while the kernel before it in the stream still runs
+// (programmatic dependent launch); the kernel calls follow() before anything else,
+// in every thread.
+template <typename... P, typename... A>
+cudaError_t launch_following(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+// Waits for the grid before this one to end, its writes visible; and lets the next
+// one be prepared.
+__device__ __forceinline__ void follow() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+#endif
+
 // Rows between the projections and attention (rows.cu): norm, rotation and the
 // store into a contiguous destination (table == nullptr) or a paged cache.
 struct RowCall {

@@ -133,6 +133,7 @@ struct RowArgs {
 template <bool kInBf16, bool kOutBf16, bool kPaged>
 __global__ void __launch_bounds__(32 * kRowWarps, kRowBlocks)
 rows_kernel(const RowArgs a) {
+  follow();
   using In = typename Elem<kInBf16>::type;
   using Out = typename Elem<kOutBf16>::type;
   const unsigned item = blockIdx.x * kRowWarps + (threadIdx.x >> 5);  // 6 x ATTN_MAX_TOKENS at most
@@ -210,15 +211,10 @@ rows_kernel(const RowArgs a) {
 
 template <bool kPaged>
 cudaError_t launch_rows_as(const RowArgs& a, bool in_bf16, bool out_bf16, cudaStream_t stream) {
-  const long long items = (long long)a.N * a.chunks;
-  const dim3 grid((unsigned)((items + kRowWarps - 1) / kRowWarps)), block(32 * kRowWarps);
-  if (in_bf16)
-    out_bf16 ? rows_kernel<true, true, kPaged><<<grid, block, 0, stream>>>(a)
-             : rows_kernel<true, false, kPaged><<<grid, block, 0, stream>>>(a);
-  else
-    out_bf16 ? rows_kernel<false, true, kPaged><<<grid, block, 0, stream>>>(a)
-             : rows_kernel<false, false, kPaged><<<grid, block, 0, stream>>>(a);
-  return cudaGetLastError();
+  const unsigned blocks = (unsigned)(((long long)a.N * a.chunks + kRowWarps - 1) / kRowWarps);
+  return launch_following(in_bf16 ? (out_bf16 ? rows_kernel<true, true, kPaged> : rows_kernel<true, false, kPaged>)
+                                  : (out_bf16 ? rows_kernel<false, true, kPaged> : rows_kernel<false, false, kPaged>),
+                          dim3(blocks), dim3(32 * kRowWarps), stream, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -251,6 +247,7 @@ __global__ void compact_kernel(uint4* k_pages, uint4* v_pages, int row_vecs, con
                                const int* keep, const int* counts, int max_keep, int max_rows, int max_blocks,
                                int num_pages, unsigned* err) {
   __shared__ long long from[ATTN_TREE_ROWS], to[ATTN_TREE_ROWS];
+  follow();
   const int b = blockIdx.x, tid = threadIdx.x;
   const int count = __ldg(counts + b);
   const int ctx = __ldg(ctx_lens + b);
@@ -336,10 +333,9 @@ cudaError_t launch_compact(void* k_pages, void* v_pages, int type, const int* ta
                            const int* keep, const int* counts, int B, int max_keep, int max_rows, int max_blocks,
                            int num_pages, unsigned* err, cudaStream_t stream) {
   const int vecs = kHKV * kD * (type == ATTN_BF16 ? 2 : 4) / 16;  // 16-byte words of a token's row: 64 or 128
-  compact_kernel<<<dim3(B, 2), vecs, 0, stream>>>(static_cast<uint4*>(k_pages), static_cast<uint4*>(v_pages), vecs,
-                                                  table, ctx_lens, keep, counts, max_keep, max_rows, max_blocks,
-                                                  num_pages, err);
-  return cudaGetLastError();
+  return launch_following(compact_kernel, dim3(B, 2), dim3(vecs), stream, static_cast<uint4*>(k_pages),
+                          static_cast<uint4*>(v_pages), vecs, table, ctx_lens, keep, counts, max_keep, max_rows,
+                          max_blocks, num_pages, err);
 }
 
 }  // namespace attn

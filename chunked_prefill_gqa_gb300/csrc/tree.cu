@@ -90,6 +90,7 @@ __device__ __forceinline__ int turn(int n) { return (n >> 1) | ((n & 1) << 2); }
 
 __global__ void __launch_bounds__(32 * kWarps, kBlocks)
 tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
+  follow();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -103,8 +104,6 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   const int k1 = min(k0 + len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   if (nrows <= 0) return;
-  // Early: the merge's blocks may take their places; they wait for all of this grid.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (k0 >= k1 && !a.cluster) {
     // Past the sequence: the merge counts its segments from the lengths. A
     // sequence without any key (only a refused one) gets zeros.
@@ -441,8 +440,8 @@ tree_merge_kernel(const TreeArgs a) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int i = blockIdx.x / (kHQ / kMergeWarps);
   const int h = (blockIdx.x % (kHQ / kMergeWarps)) * kMergeWarps + (threadIdx.x >> 5);
-  const Seq seq = load_seq(a, b);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Seq seq = load_seq(a, b);  // older than the kernel before, whose blocks have all waited
+  follow();
   if (i >= seq.rows || seq.keys <= a.split_len) return;
   const int active = (seq.keys + a.split_len - 1) / a.split_len;
   const size_t at = (size_t)(seq.first + i) * kHQ + h;
@@ -679,14 +678,17 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
   cfg.blockDim = dim3(x.threads);
   cfg.dynamicSmemBytes = x.smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.attrs = attr;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 1;
   if (p.cluster) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
   }
   if (cudaLaunchKernelEx(&cfg, x.kernel, mk, mv, a) != cudaSuccess) return ATTN_ELAUNCH;
   if (p.splits > 1 && !p.cluster) {

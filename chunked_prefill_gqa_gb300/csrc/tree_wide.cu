@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(Wide<kF32>::kThreads, 1)
 tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   using L = Wide<kF32>;
   constexpr int kStages = L::kStages;
+  follow();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -108,8 +109,6 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   const int k1 = min(k0 + len, seq.keys);
   if (!seq.ok && s == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   if (nrows <= 0) return;
-  // Early: the merge's blocks may take their places; they wait for all of this grid.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (k0 >= k1 && !a.cluster) {
     // Past the sequence: the merge counts its segments from the lengths. A
     // sequence without any key (only a refused one) gets zeros.

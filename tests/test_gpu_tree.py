@@ -318,6 +318,78 @@ def test_streams_and_graph_replay(cp, bf16, splits):
     assert cp.attn_get_device_error() == 0
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("rows,splits", [(3, 0), (7, 20), (20, 0)])
+def test_each_call_sees_what_ran_before_it(cp, captured, rows, splits):
+    """A call may be prepared while what is before it in the stream still runs: a
+    long kernel, a copy, a fill, another stream's work joined by an event, and its
+    own predecessors, whose results it reads and overwrites."""
+    lens = [(900, rows), (300, rows)]
+    n = 2 * rows
+    b = R.make_batch(lens, seed=130)
+    kp0, vp0 = b["kp"].clone(), b["vp"].clone()
+    masks = R.tree_masks(lens, "chain")
+    table = cp.attn_rope_table(torch.empty(1024, 64, device="cuda"))
+    sets = [[torch.randn(n, h, 64, device="cuda") for h in (32, 8, 8)] for _ in range(3)]
+    q, k, v, qo, out = (torch.empty(n, h, 64, device="cuda") for h in (32, 8, 8, 32, 32))
+    keep = torch.tensor([[rows - 1]] * 2, dtype=torch.int32, device="cuda")
+    cnt = torch.empty(2, dtype=torch.int32, device="cuda")
+    need = cp.attn_tree_workspace_bytes(2, n, rows, 900, splits)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    slow = torch.randn(2048, 2048, device="cuda")
+    outs, sides = [torch.empty_like(out) for _ in sets], torch.cuda.Stream()
+
+    def step():
+        for (q1, k1, v1), o in zip(sets, outs):
+            q.copy_(q1)                      # copies
+            x = slow @ slow                  # a kernel that takes a while
+            k.copy_(k1).add_(x[0, 0] * 0)
+            sides.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(sides):   # work of another stream
+                v.copy_((slow @ slow)[0, 0] * 0 + v1)
+            torch.cuda.current_stream().wait_stream(sides)
+            cp.attn_append_paged(k, v, b["kp"], b["vp"], b["table"], b["ctx"], b["starts"], table, q=q, qOut=qo)
+            cp.attn_tree_paged(qo, b["kp"], b["vp"], b["table"], b["ctx"], b["starts"], None, out, rows, 900, splits, ws)
+            o.copy_(out)                     # and what follows a call
+            out.zero_()
+            cnt.fill_(1)
+            cp.attn_compact_paged(b["kp"], b["vp"], b["table"], b["ctx"], keep, cnt, rows)
+            for pool in (q, k, v, qo, cnt):
+                pool.zero_()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    for o in outs:
+        o.zero_()
+    b["kp"].copy_(kp0), b["vp"].copy_(vp0)
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        g.replay()
+    else:
+        step()
+    torch.cuda.synchronize()
+    assert cp.attn_get_device_error() == 0
+    tok = torch.tensor([c + i for c, t in lens for i in range(t)], device="cuda")
+    for (q1, k1, v1), o in zip(sets, outs):
+        want = dict(b, kp=kp0.clone(), vp=vp0.clone())
+        kw, kt = R.norm_rotate_reference(k1, None, tok, table, 0, 1e-6)
+        qw, qt = R.norm_rotate_reference(q1, None, tok, table, 0, 1e-6)
+        seq = torch.tensor([0] * rows + [1] * rows, device="cuda")
+        page = b["table"].long()[seq, tok // 16]
+        want["kp"][page, tok % 16], want["vp"][page, tok % 16] = kw.float(), v1
+        ref, tol = R.tree_reference(qw.float(), want, masks)
+        # the rotated operands' own roundings (a few 2^-24 of values around 1) next to the tolerance's 2^-19
+        check(o, ref, 2 * tol)
+    last = torch.tensor([rows - 1, 2 * rows - 1], device="cuda")
+    first = torch.tensor([900, 300], device="cuda")
+    assert torch.equal(b["vp"][b["table"].long()[[0, 1], first // 16], first % 16], sets[-1][2][last])
+
+
 @pytest.mark.parametrize("bf16", [False, True])
 def test_calls_from_several_threads(cp, bf16):
     """Four threads, each with its own stream, batch and workspace."""

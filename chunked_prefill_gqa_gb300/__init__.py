@@ -393,7 +393,7 @@ def attn_decode_paged_noalloc(q, kPages, vPages, blockTable, contextLens, out, m
 
 
 def _native():
-    """The extension that checks and marshals the serving-step calls (binding.c):
+    """The extension that checks and marshals the serving-step calls (binding.cpp):
     they run once a layer, where doing that in Python would take longer than the
     launch. It raises TypeError or ValueError for a tensor of another type, shape,
     layout or device than stated; every tensor has to be on the current device."""
@@ -405,6 +405,8 @@ def _native():
             raise RuntimeError(f"{path} is missing: build it with `python -m chunked_prefill_gqa_gb300.build`")
         import importlib.machinery
         import importlib.util
+
+        import torch  # noqa: F401  (whose libraries the extension uses)
         loader = importlib.machinery.ExtensionFileLoader("_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
         loader.exec_module(module)

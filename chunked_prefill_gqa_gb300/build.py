@@ -1,7 +1,7 @@
 """Build libattnprefill.so in-tree with nvcc for sm_103a.
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then nvcc links the
-shared library (CUDA runtime linked statically), and gcc the small CPython
+shared library (CUDA runtime linked statically), and g++ the small CPython
 extension that marshals the serving-step calls to it. Run as a module
 (``python -m chunked_prefill_gqa_gb300.build``) or call :func:`build`.
 """
@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -38,7 +39,7 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(CSRC, "*.c"))) + \
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(CSRC, "*.cpp"))) + \
         [os.path.join(INCLUDE, "attn_prefill.h"), os.path.abspath(__file__)]
 
 
@@ -67,7 +68,9 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
 
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
+        binding = ex.submit(compile_binding, nvcc)
         results = list(ex.map(compile_one, srcs))
+        binding.result()
     if ptxas_verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -77,22 +80,41 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    build_binding(nvcc)
+    link_binding()
     return LIB
 
 
-def build_binding(nvcc: str) -> None:
-    """The CPython extension next to the library, which it finds by its own folder."""
-    tmp = BINDING + f".tmp{os.getpid()}"
-    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
-    cmd = [shutil.which("gcc") or "cc", "-O2", "-std=c11", "-Wall", "-fPIC", "-shared", "-I", INCLUDE, "-I", cuda,
-           "-I", sysconfig.get_paths()["include"], "-o", tmp, os.path.join(CSRC, "binding.c"), "-L", OUT,
-           "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+def _torch() -> str:
+    """PyTorch's folder, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found: its headers are required to build the binding")
+    return spec.submodule_search_locations[0]
+
+
+def _run(what: str, cmd: list) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on binding.c:\n{r.stderr}")
-    if r.stderr:
-        sys.stderr.write(r.stderr)
+        raise RuntimeError(f"{what}:\n{r.stderr}")
+
+
+def compile_binding(nvcc: str) -> None:
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    torch = os.path.join(_torch(), "include")
+    _run("g++ failed on binding.cpp",
+         [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", cuda, "-isystem", torch,
+          "-isystem", os.path.join(torch, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+          "-c", os.path.join(CSRC, "binding.cpp"), "-o", os.path.join(OUT, "binding.o")])
+
+
+def link_binding() -> None:
+    """The CPython extension next to the library, which it finds by its own folder; PyTorch's
+    own libraries are there by the time it is loaded."""
+    tmp = BINDING + f".tmp{os.getpid()}"
+    _run("the binding does not link",
+         [shutil.which("g++") or "c++", "-shared", "-o", tmp, os.path.join(OUT, "binding.o"), "-L", OUT,
+          "-l:" + os.path.basename(LIB), "-L", os.path.join(_torch(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, BINDING)
 
 

@@ -90,13 +90,25 @@ __device__ __forceinline__ int turn(int n) { return (n >> 1) | ((n & 1) << 2); }
 
 __global__ void __launch_bounds__(32 * kWarps, kBlocks)
 tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
-  follow();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + kSmemBar);
+  uint64_t* const full = bars + warp * kStages;
+  if (lane == 0) {
+    if (warp < 2) tc::tma_prefetch_desc(warp ? &mv : &mk);
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
+    tc::fence_mbar_init();
+  }
+  follow();
   const int g = lane >> 2, c = lane & 3;  // fragment row (or key), fragment column
   const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
 
+  // The table's first entries are on their way while the lengths are, as of a
+  // sequence as long as the call allows: an entry past the sequence is read and not
+  // used.
+  const int first_page = s * (a.split_len / ATTN_PAGE) + warp + lane * kWarps;
+  const int first_entries = first_page < a.max_blocks ? __ldg(a.table + (size_t)b * a.max_blocks + first_page) : 0;
   const Seq seq = load_seq(a, b);
   const int i0 = rt * kTokens;  // the block's first drafted row
   const int nrows = min(kTokens, seq.rows - i0);
@@ -114,14 +126,8 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   }
   const bool whole = !a.cluster && seq.keys <= a.split_len;  // one segment: the output is written here
 
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kSmemBar);
   unsigned long long* masks = reinterpret_cast<unsigned long long*>(smem + kSmemMask);
   uint8_t* const ring = smem + warp * (kStages * kStage);
-  uint64_t* const full = bars + warp * kStages;
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) tc::mbar_init(&full[i], 1);
-    tc::fence_mbar_init();
-  }
   if (tid < kTokens)
     masks[tid] = tid >= nrows ? 0ull
                  : a.masks    ? (unsigned long long)__ldg(a.masks + seq.first + i0 + tid)
@@ -135,7 +141,10 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   const int* trow = a.table + (size_t)b * a.max_blocks + k0 / ATTN_PAGE + warp;
   int entries = 0;
   auto issue = [&](int n) {
-    if ((n & 31) == 0) entries = n + lane < mine ? __ldg(trow + (size_t)(n + lane) * kWarps) : 0;
+    if ((n & 31) == 0)
+      entries = n == 0 && len == a.split_len ? first_entries
+                : n + lane < mine            ? __ldg(trow + (size_t)(n + lane) * kWarps)
+                                             : 0;
     int page = __shfl_sync(kFull, entries, n & 31);
     if (lane == 0) {
       if (page < 0 || page >= a.num_pages) {  // reads as zeros: past the pool's end
@@ -539,7 +548,7 @@ int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtenso
 // 11.1; 576: two of 1000 with 32 12.1 and 11.2); on fp32 pages it depends (384: four
 // of 300 with 16 rows 9.1 and 11.0, sixteen of 60 11.4 and 8.2).
 using Variant = TreeVariant;
-const Variant kNarrow = {tree_narrow_kernel, kTokens, 32 * kWarps, kSmemAlloc, kBlocks, false, 0};
+const Variant kNarrow = {tree_narrow_kernel, kTokens, 32 * kWarps, kSmemAlloc, kBlocks, false, 0, 2};
 constexpr int kCount[2] = {2, 3};
 const Variant kVariants[2][3] = {{kNarrow, tree_wide_variant(false)},
                                  {tree_tc_variant(4), tree_tc_variant(8), tree_wide_variant(true)}};
@@ -629,10 +638,13 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
   if (n <= 0) {
     // The segments that take the least time, counted in tiles of 128 keys: rounds
     // of resident blocks, each as long as its tiles and what a block costs besides
-    // them (measured: six tiles' time), and the merge (two in a cluster, five
-    // through memory and a second kernel).
-    const int tokens = kVariants[bf16][v].tokens, slots = d->slots[bf16][v];
-    const long long units = (long long)B * kHKV * ((max_rows + tokens - 1) / tokens);
+    // them, and the merge: one in a cluster; through memory two for the second kernel
+    // and what the partials take. One row on fp32 pages, 300 tokens: three segments
+    // 5.3 us, one 8.0; sixteen such sequences: three 11.6, one 8.2. 4000 tokens: 24
+    // segments 9.1 us, eight 12.4.
+    const Variant& x = kVariants[bf16][v];
+    const int slots = d->slots[bf16][v];
+    const long long units = (long long)B * kHKV * ((max_rows + x.tokens - 1) / x.tokens);
     const int tiles = (keys + 127) / 128;
     const int limit = tiles < kMaxSplits ? tiles : kMaxSplits;
     long long best = 0;
@@ -640,7 +652,8 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
     for (int s = 1; s <= limit; ++s) {
       const bool cluster = s > 1 && s <= kMaxCluster && clusters[s] > 0;
       const long long rounds = cluster ? (units + clusters[s] - 1) / clusters[s] : (units * s + slots - 1) / slots;
-      const long long cost = rounds * ((tiles + s - 1) / s + 6) + (s == 1 ? 0 : cluster ? 2 : 5);
+      const long long merge = s == 1 ? 0 : cluster ? 1 : 2 + (long long)B * max_rows * s / 440;
+      const long long cost = rounds * ((tiles + s - 1) / s + x.fixed) + merge;
       if (s == 1 || cost < best) {
         best = cost;
         n = s;

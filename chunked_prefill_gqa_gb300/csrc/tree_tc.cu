@@ -108,11 +108,12 @@ template <int R>
 __global__ void __launch_bounds__(Lay<R>::kThreads, Lay<R>::kBlocks)
 tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   using L = Lay<R>;
-  follow();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform: descriptors in uniform registers
+  if (warp == L::kTmaWarp && lane < 2) tma_prefetch_desc(lane ? &mv : &mk);
+  follow();
   const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
 
   // The table's first entries are on their way while the lengths are, as of a
@@ -592,7 +593,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 template <int R>
 TreeVariant variant() {
   using L = Lay<R>;
-  return {tree_tc_kernel<R>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0};
+  return {tree_tc_kernel<R>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0, 5};
 }
 
 TreeVariant tree_tc_variant(int tokens) { return tokens == 4 ? variant<16>() : variant<32>(); }

@@ -89,11 +89,13 @@ __global__ void __launch_bounds__(Wide<kF32>::kThreads, 1)
 tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   using L = Wide<kF32>;
   constexpr int kStages = L::kStages;
-  follow();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  if (warp == L::kKWarp && lane == 0) tma_prefetch_desc(&mk);
+  if (warp == L::kVWarp && lane == 0) tma_prefetch_desc(&mv);
+  follow();
   const int s = blockIdx.x, head = blockIdx.y % kHKV, rt = blockIdx.y / kHKV, b = blockIdx.z;
 
   // The table's first entries are on their way while the lengths are, as of a
@@ -200,6 +202,20 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         m = (a.masks ? (unsigned long long)__ldg(a.masks + seq.first + i0 + tid) : ~0ull >> (63 - (i0 + tid))) &
             (~0ull >> (64 - seq.rows));  // bits past the sequence's rows see nothing
       masks[tid] = m;
+    }
+  }
+  // A softmax thread's 32 dims (32 g ..) of its row of q are on their way before the
+  // block has met.
+  float x[32];
+  if (warp < kSoft) {
+    const int row = (warp & 3) * 32 + lane, i = row >> 2;
+    const float* src =
+        a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (row & 3)) * kD + (warp >> 2) * 32;
+#pragma unroll
+    for (int k = 0; k < 32; k += 4) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < nrows) v = __ldg(reinterpret_cast<const float4*>(src + k));
+      x[k] = v.x, x[k + 1] = v.y, x[k + 2] = v.z, x[k + 3] = v.w;
     }
   }
   tc_fence_before();
@@ -389,16 +405,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     bool failed = false;
 
     if (active && ntiles > 0) {
-      {  // this thread's 32 dims (32 g ..) of its row of q, in its terms
-        const int i = row >> 2;
-        const float* src = a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (row & 3)) * kD + g * 32;
-        float x[32];
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i < nrows) v = __ldg(reinterpret_cast<const float4*>(src + k));
-          x[k] = v.x, x[k + 1] = v.y, x[k + 2] = v.z, x[k + 3] = v.w;
-        }
+      {  // q in its terms
         if constexpr (kF32) {
           float hi[32];
 #pragma unroll

@@ -17,10 +17,10 @@
 // the lane itself. The cos and sin of a row are read once per warp. Nothing is
 // staged in shared memory: every byte is used once, so the bound is memory, and
 // for a few rows the launch and a chain of dependent loads (the row's sequence, its
-// context, its page or angles). Measured, inputs in HBM: 8192 fp32 rows appended
-// with their queries 33.2 us (201 MB, 6.1 TB/s), normed and rotated alone 27.1
-// (168 MB, 6.2 TB/s); 2048 bf16 rows 9.4 and 7.5; 16 rows 3.0 and 2.4, nearly all
-// of it the launch.
+// context, its page or angles). Measured in graphs, inputs in HBM: 8192 fp32 rows
+// appended with their queries 31.5 us (201 MB, 6.4 TB/s), normed and rotated alone
+// 26.6 (168 MB, 6.3 TB/s); 2048 bf16 rows 7.8 and 7.0; 16 rows 2.2 and 2.1, of which
+// 1.4 are a launch.
 #include <cstdint>
 #include <cuda_bf16.h>
 
@@ -31,8 +31,9 @@ namespace {
 
 // 12 blocks of 4 warps an SM (40 registers a thread): a chunk's rows wait for the
 // lookups of where they go, so as many warps as fit wait at once, with bf16 heads
-// held as loaded until then. (2048 bf16 rows appended with their queries: 9.4 us;
-// 10.8 with 44 registers and heads widened as they land, 11.0 in blocks of 8 warps.)
+// held as loaded until then, and each lookup starts as soon as it can. (2048 bf16 rows
+// appended with their queries: 7.8 us; 8.9 with a context, a page, a position and its
+// angles each after the other; 10.5 with 44 registers and heads widened as they land.)
 constexpr int kRowWarps = 4, kRowBlocks = 12;
 constexpr int kHeadsPerWarp = 8;
 constexpr int kQChunks = kHQ / kHeadsPerWarp;  // 4 warps for a row's queries, one for its keys, one for its values
@@ -151,20 +152,23 @@ rows_kernel(const RowArgs a) {
 #pragma unroll
   for (int i = 0; i < kHeadsPerWarp / 2; ++i) raw[i] = load4(src + 2 * i * kD);
 
-  int position = 0;  // where nothing else says: its token
-  int slot = n;      // row of the destination
+  // Then what the lookups need, as much of it at once as there is.
+  int position = a.positions ? __ldg(a.positions + n) : 0;
+  int slot = n;  // row of the destination
+  int page = 0;
   if (kPaged) {
+    int ctx = lane < a.B ? __ldg(a.ctx_lens + lane) : 0;  // of the first 32 sequences
     int first = 0;
     const int b = find_sequence(a.row_start, a.B, n, lane, &first);
     if (b < 0 || b >= a.B) return;  // a row of no sequence: left as it is
-    const long long row = (long long)n - first, token = __ldg(a.ctx_lens + b) + row;
-    slot = -1;
-    if (token >= row && token < (long long)a.max_blocks * ATTN_PAGE) {
-      const int page = __ldg(a.table + (size_t)b * a.max_blocks + token / ATTN_PAGE);
-      if (page >= 0 && page < a.num_pages) slot = page * ATTN_PAGE + (int)token % ATTN_PAGE;
+    ctx = b < 32 ? __shfl_sync(kFull, ctx, b) : __ldg(a.ctx_lens + b);
+    const long long row = (long long)n - first, token = ctx + row;
+    page = -1;
+    if (!is_q && token >= row && token < (long long)a.max_blocks * ATTN_PAGE) {
+      page = __ldg(a.table + (size_t)b * a.max_blocks + token / ATTN_PAGE);
+      slot = (int)token % ATTN_PAGE;
     }
-    position = (int)min(max(token, -1ll), (long long)ATTN_MAX_TOKENS);
-    if (slot < 0 && lane == 0) record_error(a.err, kDevErrBounds);
+    if (!a.positions) position = (int)min(max(token, -1ll), (long long)ATTN_MAX_TOKENS);
   }
 
   float4 x[kHeadsPerWarp / 2];
@@ -173,7 +177,6 @@ rows_kernel(const RowArgs a) {
     const float4 w = weight ? __ldg(reinterpret_cast<const float4*>(weight + d)) : make_float4(1.f, 1.f, 1.f, 1.f);
     Angles t{};
     if (a.cos_sin) {
-      if (a.positions) position = __ldg(a.positions + n);
       if (position < 0 || position >= a.num_positions) {
         if (lane == 0) record_error(a.err, kDevErrBounds);
         position = position < 0 ? 0 : a.num_positions - 1;
@@ -202,7 +205,14 @@ rows_kernel(const RowArgs a) {
     float* dst = a.q_out + ((size_t)n * kHQ + chunk * kHeadsPerWarp + (lane >> 4)) * kD + d;
 #pragma unroll
     for (int i = 0; i < kHeadsPerWarp / 2; ++i) store4(dst + 2 * i * kD, x[i]);
-  } else if (slot >= 0) {
+  } else {
+    if (kPaged) {
+      if (page < 0 || page >= a.num_pages) {
+        if (lane == 0) record_error(a.err, kDevErrBounds);
+        return;
+      }
+      slot += page * ATTN_PAGE;
+    }
     Out* dst = static_cast<Out*>(is_k ? a.k_out : a.v_out) + ((size_t)slot * kHKV + (lane >> 4)) * kD + d;
 #pragma unroll
     for (int i = 0; i < kHeadsPerWarp / 2; ++i) store4(dst + 2 * i * kD, x[i]);
@@ -236,54 +246,55 @@ __global__ void rope_table_kernel(const __grid_constant__ Frequencies inv, float
 
 // ---------------------------------------------------------------------------
 // Keeping an accepted path. Block (b, pool): row keep[b][i] of the drafted rows
-// moves to row i, for K (pool 0) or V (pool 1); a thread owns 16 bytes of every
-// row. keep rises strictly, so keep[i] >= i and a row is read before any store
-// reaches it, also with eight rows' loads in flight at once: their stores go to
-// rows below every later source. At most 64 rows of 2 or 4 KB a sequence: the
-// launch and three dependent loads are all of it (2.3 us for 16 sequences).
-constexpr int kKeepAhead = 8;
+// moves to row i, for K (pool 0) or V (pool 1). A thread owns 16 bytes of up to 16
+// rows (of one to four groups of threads, by maxKeep), and all rows are in registers
+// before any is stored, so the moves run in place whatever overlaps. At most 64 rows
+// of 2 or 4 KB a sequence: the launch and three dependent loads (list, table, rows)
+// are nearly all of it. 64 rows of 64 sequences 2.8 us in a graph; with one group,
+// eight rows at a time, and the list read after its length 6.2.
+constexpr int kKeepRows = 16, kKeepGroups = ATTN_TREE_ROWS / kKeepRows;
 
-__global__ void compact_kernel(uint4* k_pages, uint4* v_pages, int row_vecs, const int* table, const int* ctx_lens,
-                               const int* keep, const int* counts, int max_keep, int max_rows, int max_blocks,
-                               int num_pages, unsigned* err) {
-  __shared__ long long from[ATTN_TREE_ROWS], to[ATTN_TREE_ROWS];
+__global__ void __launch_bounds__(128 * kKeepGroups)
+compact_kernel(uint4* k_pages, uint4* v_pages, int row_vecs, const int* table, const int* ctx_lens,
+               const int* keep, const int* counts, int max_keep, int max_rows, int max_blocks, int num_pages,
+               unsigned* err) {
+  __shared__ int from[ATTN_TREE_ROWS], to[ATTN_TREE_ROWS];  // rows of the pool
   follow();
   const int b = blockIdx.x, tid = threadIdx.x;
   const int count = __ldg(counts + b);
   const int ctx = __ldg(ctx_lens + b);
+  const int r = tid < max_keep ? __ldg(keep + (size_t)b * max_keep + tid) : 0;
+  const int before = tid > 0 && tid < max_keep ? __ldg(keep + (size_t)b * max_keep + tid - 1) : -1;
   bool bad = count < 0 || count > max_keep || count > max_rows || ctx < 0;
-  if (!bad) {
-    for (int i = tid; i < count; i += blockDim.x) {
-      const int r = __ldg(keep + (size_t)b * max_keep + i);
-      const int before = i ? __ldg(keep + (size_t)b * max_keep + i - 1) : -1;
-      const long long src = (long long)ctx + r, dst = (long long)ctx + i;
-      if (r <= before || r >= max_rows || src >= (long long)max_blocks * ATTN_PAGE) {
-        bad = true;
-        break;
-      }
+  if (!bad && tid < count) {
+    const long long src = (long long)ctx + r, dst = (long long)ctx + tid;
+    if (r <= before || r >= max_rows || src >= (long long)max_blocks * ATTN_PAGE) {
+      bad = true;
+    } else {
       const int ps = __ldg(table + (size_t)b * max_blocks + src / ATTN_PAGE);
       const int pd = __ldg(table + (size_t)b * max_blocks + dst / ATTN_PAGE);
-      if (ps < 0 || ps >= num_pages || pd < 0 || pd >= num_pages) {
-        bad = true;
-        break;
-      }
-      from[i] = (long long)ps * ATTN_PAGE + src % ATTN_PAGE;
-      to[i] = (long long)pd * ATTN_PAGE + dst % ATTN_PAGE;
+      bad = ps < 0 || ps >= num_pages || pd < 0 || pd >= num_pages;
+      from[tid] = ps * ATTN_PAGE + (int)src % ATTN_PAGE;
+      to[tid] = pd * ATTN_PAGE + (int)dst % ATTN_PAGE;
     }
   }
   if (__syncthreads_or(bad)) {  // nothing of this sequence is moved
     if (tid == 0) record_error(err, kDevErrBounds);
     return;
   }
-  uint4* pool = (blockIdx.y ? v_pages : k_pages) + tid;
-  for (int i0 = 0; i0 < count; i0 += kKeepAhead) {
-    uint4 x[kKeepAhead];
+  const int group = tid / row_vecs, groups = blockDim.x / row_vecs;
+  uint4* pool = (blockIdx.y ? v_pages : k_pages) + tid % row_vecs;
+  uint4 x[kKeepRows];
 #pragma unroll
-    for (int i = 0; i < kKeepAhead; ++i)
-      if (i0 + i < count && from[i0 + i] != to[i0 + i]) x[i] = pool[(size_t)from[i0 + i] * row_vecs];
+  for (int k = 0; k < kKeepRows; ++k) {
+    const int i = k * groups + group;
+    if (i < count && from[i] != to[i]) x[k] = pool[(size_t)from[i] * row_vecs];
+  }
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kKeepAhead; ++i)
-      if (i0 + i < count && from[i0 + i] != to[i0 + i]) pool[(size_t)to[i0 + i] * row_vecs] = x[i];
+  for (int k = 0; k < kKeepRows; ++k) {
+    const int i = k * groups + group;
+    if (i < count && from[i] != to[i]) pool[(size_t)to[i] * row_vecs] = x[k];
   }
 }
 
@@ -333,7 +344,8 @@ cudaError_t launch_compact(void* k_pages, void* v_pages, int type, const int* ta
                            const int* keep, const int* counts, int B, int max_keep, int max_rows, int max_blocks,
                            int num_pages, unsigned* err, cudaStream_t stream) {
   const int vecs = kHKV * kD * (type == ATTN_BF16 ? 2 : 4) / 16;  // 16-byte words of a token's row: 64 or 128
-  return launch_following(compact_kernel, dim3(B, 2), dim3(vecs), stream, static_cast<uint4*>(k_pages),
+  const int groups = (max_keep + kKeepRows - 1) / kKeepRows;
+  return launch_following(compact_kernel, dim3(B, 2), dim3(vecs * groups), stream, static_cast<uint4*>(k_pages),
                           static_cast<uint4*>(v_pages), vecs, table, ctx_lens, keep, counts, max_keep, max_rows,
                           max_blocks, num_pages, err);
 }

@@ -459,7 +459,7 @@ size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxContext, int 
  * they lie at tokens contextLens[b] .. contextLens[b] + keepCounts[b] - 1 and
  * the next step's context is contextLens[b] + keepCounts[b].
  *   keep        int32 [B][maxKeep]: the accepted rows of sequence b, rising, each
- *               in [0, maxRows); entries from keepCounts[b] on are not read
+ *               in [0, maxRows); entries from keepCounts[b] on do not count
  *   keepCounts  int32 [B], each in [0, maxKeep]
  * keep[b][i] >= i, so the moves run in place. Tokens that no accepted row moves
  * to stay as they are. A sequence whose list is not as above, or whose tokens or

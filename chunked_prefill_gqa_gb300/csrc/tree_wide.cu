@@ -31,7 +31,7 @@
 // us (537 MB, 3.7 TB/s; 206 GFLOP of term products, 1.42 PFLOP/s; pipe active 74% on
 // those SMs), 16 rows on fp32 pages 254 us (pipe active 83%, half of its lanes without
 // rows). 64 rows of one sequence of 131071 tokens on bf16 pages: 144 blocks, 134 us.
-// Run back to back for long these meet the power limit and take a tenth more. A grid
+// Run back to back for long, full tiles meet the power limit and take a tenth more. A grid
 // of one block an SM that shares all tiles evenly, units cut where a block's share
 // ends, was built and ran 252 and 157 us: what a second unit costs a block (q again,
 // an empty pipeline, two partials through memory) is what the idle SMs gave.

@@ -101,6 +101,12 @@ cudaError_t launch_following(void (*kernel)(P...), dim3 grid, dim3 block, cudaSt
 __device__ __forceinline__ void follow() {
   asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
 }
+// What such a kernel reads may be written while it is already there, up to follow():
+// a plain load, which stays behind it, never one by the read-only path.
+template <typename T>
+__device__ __forceinline__ T fetch(const T* p) {
+  return *p;
+}
 #endif
 
 // Rows between the projections and attention (rows.cu): norm, rotation and the

@@ -102,7 +102,7 @@ __device__ __forceinline__ int find_sequence(const int* row_start, int B, int n,
   while (true) {
     const int step = (hi - lo + 31) / 32;
     const long long at = (long long)lo + (long long)lane * step;
-    const int v = at < hi ? __ldg(row_start + at) : 0x7fffffff;
+    const int v = at < hi ? fetch(row_start + at) : 0x7fffffff;
     const unsigned le = __ballot_sync(kFull, at < hi && v <= n);
     if (le == 0) return -1;
     const int last = 31 - __clz(le);
@@ -153,19 +153,19 @@ rows_kernel(const RowArgs a) {
   for (int i = 0; i < kHeadsPerWarp / 2; ++i) raw[i] = load4(src + 2 * i * kD);
 
   // Then what the lookups need, as much of it at once as there is.
-  int position = a.positions ? __ldg(a.positions + n) : 0;
+  int position = a.positions ? fetch(a.positions + n) : 0;
   int slot = n;  // row of the destination
   int page = 0;
   if (kPaged) {
-    int ctx = lane < a.B ? __ldg(a.ctx_lens + lane) : 0;  // of the first 32 sequences
+    int ctx = lane < a.B ? fetch(a.ctx_lens + lane) : 0;  // of the first 32 sequences
     int first = 0;
     const int b = find_sequence(a.row_start, a.B, n, lane, &first);
     if (b < 0 || b >= a.B) return;  // a row of no sequence: left as it is
-    ctx = b < 32 ? __shfl_sync(kFull, ctx, b) : __ldg(a.ctx_lens + b);
+    ctx = b < 32 ? __shfl_sync(kFull, ctx, b) : fetch(a.ctx_lens + b);
     const long long row = (long long)n - first, token = ctx + row;
     page = -1;
     if (!is_q && token >= row && token < (long long)a.max_blocks * ATTN_PAGE) {
-      page = __ldg(a.table + (size_t)b * a.max_blocks + token / ATTN_PAGE);
+      page = fetch(a.table + (size_t)b * a.max_blocks + token / ATTN_PAGE);
       slot = (int)token % ATTN_PAGE;
     }
     if (!a.positions) position = (int)min(max(token, -1ll), (long long)ATTN_MAX_TOKENS);
@@ -174,7 +174,7 @@ rows_kernel(const RowArgs a) {
   float4 x[kHeadsPerWarp / 2];
   if (is_q || is_k) {
     const float* weight = is_q ? a.q_weight : a.k_weight;
-    const float4 w = weight ? __ldg(reinterpret_cast<const float4*>(weight + d)) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 w = weight ? fetch(reinterpret_cast<const float4*>(weight + d)) : make_float4(1.f, 1.f, 1.f, 1.f);
     Angles t{};
     if (a.cos_sin) {
       if (position < 0 || position >= a.num_positions) {
@@ -183,13 +183,13 @@ rows_kernel(const RowArgs a) {
       }
       const float* row = a.cos_sin + (size_t)position * kD;
       if (a.pairing == ATTN_ROPE_PAIRS) {
-        const float2 c = __ldg(reinterpret_cast<const float2*>(row + 2 * sub));
-        const float2 s = __ldg(reinterpret_cast<const float2*>(row + kD / 2 + 2 * sub));
+        const float2 c = fetch(reinterpret_cast<const float2*>(row + 2 * sub));
+        const float2 s = fetch(reinterpret_cast<const float2*>(row + kD / 2 + 2 * sub));
         t.c = make_float4(c.x, c.y, 0.f, 0.f);
         t.s = make_float4(s.x, s.y, 0.f, 0.f);
       } else {
-        t.c = __ldg(reinterpret_cast<const float4*>(row + (d & 31)));
-        t.s = __ldg(reinterpret_cast<const float4*>(row + kD / 2 + (d & 31)));
+        t.c = fetch(reinterpret_cast<const float4*>(row + (d & 31)));
+        t.s = fetch(reinterpret_cast<const float4*>(row + kD / 2 + (d & 31)));
         if (sub < 8) t.s = make_float4(-t.s.x, -t.s.y, -t.s.z, -t.s.w);
       }
     }
@@ -261,18 +261,18 @@ compact_kernel(uint4* k_pages, uint4* v_pages, int row_vecs, const int* table, c
   __shared__ int from[ATTN_TREE_ROWS], to[ATTN_TREE_ROWS];  // rows of the pool
   follow();
   const int b = blockIdx.x, tid = threadIdx.x;
-  const int count = __ldg(counts + b);
-  const int ctx = __ldg(ctx_lens + b);
-  const int r = tid < max_keep ? __ldg(keep + (size_t)b * max_keep + tid) : 0;
-  const int before = tid > 0 && tid < max_keep ? __ldg(keep + (size_t)b * max_keep + tid - 1) : -1;
+  const int count = fetch(counts + b);
+  const int ctx = fetch(ctx_lens + b);
+  const int r = tid < max_keep ? fetch(keep + (size_t)b * max_keep + tid) : 0;
+  const int before = tid > 0 && tid < max_keep ? fetch(keep + (size_t)b * max_keep + tid - 1) : -1;
   bool bad = count < 0 || count > max_keep || count > max_rows || ctx < 0;
   if (!bad && tid < count) {
     const long long src = (long long)ctx + r, dst = (long long)ctx + tid;
     if (r <= before || r >= max_rows || src >= (long long)max_blocks * ATTN_PAGE) {
       bad = true;
     } else {
-      const int ps = __ldg(table + (size_t)b * max_blocks + src / ATTN_PAGE);
-      const int pd = __ldg(table + (size_t)b * max_blocks + dst / ATTN_PAGE);
+      const int ps = fetch(table + (size_t)b * max_blocks + src / ATTN_PAGE);
+      const int pd = fetch(table + (size_t)b * max_blocks + dst / ATTN_PAGE);
       bad = ps < 0 || ps >= num_pages || pd < 0 || pd >= num_pages;
       from[tid] = ps * ATTN_PAGE + (int)src % ATTN_PAGE;
       to[tid] = pd * ATTN_PAGE + (int)dst % ATTN_PAGE;

@@ -108,7 +108,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   // sequence as long as the call allows: an entry past the sequence is read and not
   // used.
   const int first_page = s * (a.split_len / ATTN_PAGE) + warp + lane * kWarps;
-  const int first_entries = first_page < a.max_blocks ? __ldg(a.table + (size_t)b * a.max_blocks + first_page) : 0;
+  const int first_entries = first_page < a.max_blocks ? fetch(a.table + (size_t)b * a.max_blocks + first_page) : 0;
   const Seq seq = load_seq(a, b);
   const int i0 = rt * kTokens;  // the block's first drafted row
   const int nrows = min(kTokens, seq.rows - i0);
@@ -130,7 +130,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   uint8_t* const ring = smem + warp * (kStages * kStage);
   if (tid < kTokens)
     masks[tid] = tid >= nrows ? 0ull
-                 : a.masks    ? (unsigned long long)__ldg(a.masks + seq.first + i0 + tid)
+                 : a.masks    ? (unsigned long long)fetch(a.masks + seq.first + i0 + tid)
                               : ~0ull >> (63 - (i0 + tid));
   __syncwarp();
 
@@ -143,7 +143,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   auto issue = [&](int n) {
     if ((n & 31) == 0)
       entries = n == 0 && len == a.split_len ? first_entries
-                : n + lane < mine            ? __ldg(trow + (size_t)(n + lane) * kWarps)
+                : n + lane < mine            ? fetch(trow + (size_t)(n + lane) * kWarps)
                                              : 0;
     int page = __shfl_sync(kFull, entries, n & 31);
     if (lane == 0) {
@@ -175,7 +175,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       const int i = 2 * h + (g >> 2);
       float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
       if (i < nrows)
-        u = __ldg(reinterpret_cast<const float4*>(a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (g & 3)) * kD +
+        u = fetch(reinterpret_cast<const float4*>(a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (g & 3)) * kD +
                                                   16 * j + 4 * c));
       x[h][0] = u.x, x[h][1] = u.y, x[h][2] = u.z, x[h][3] = u.w;
     }

@@ -35,9 +35,9 @@ struct Seq {
 };
 __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b) {
   Seq s;
-  s.ctx = __ldg(a.ctx_lens + b);
-  s.first = __ldg(a.row_start + b);
-  const int end = __ldg(a.row_start + b + 1);
+  s.ctx = fetch(a.ctx_lens + b);
+  s.first = fetch(a.row_start + b);
+  const int end = fetch(a.row_start + b + 1);
   s.ok = true;
   const int room = min((long long)a.max_blocks * ATTN_PAGE, (long long)ATTN_MAX_TOKENS);
   if (s.ctx < 0 || s.ctx > a.max_context) {

@@ -122,7 +122,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   const int first_page = s * (a.split_len / ATTN_PAGE) + lane;
   int first_entries = -1;
   if (warp == L::kTmaWarp && first_page < a.max_blocks)
-    first_entries = __ldg(a.table + (size_t)b * a.max_blocks + first_page);
+    first_entries = fetch(a.table + (size_t)b * a.max_blocks + first_page);
   const Seq seq = load_seq(a, b);
   const int i0 = rt * (R / 4);  // the block's first drafted row
   const int nrows = min(R / 4, seq.rows - i0);
@@ -166,7 +166,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   int entries = -1, entries_next = -1, group = 0, ahead = 0;
   auto entry_at = [&](int g) -> int {
     const int t = k0 + g * 4 * kKeys + lane * ATTN_PAGE;
-    return t < k1 ? __ldg(trow + t / ATTN_PAGE) : -1;
+    return t < k1 ? fetch(trow + t / ATTN_PAGE) : -1;
   };
   auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t operand, int n) {
     const int st = n % kStages;
@@ -223,7 +223,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       if (i < nrows) {
         const float4* src = reinterpret_cast<const float4*>(
             a.q + ((size_t)(seq.first + i0 + i) * kHQ + head * kGroup + (r & 3)) * kD + c8 * 8);
-        const float4 u = __ldg(src), v = __ldg(src + 1);
+        const float4 u = fetch(src), v = fetch(src + 1);
         x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
       } else {
 #pragma unroll
@@ -239,7 +239,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     }
     for (int i = tid; i < R / 4; i += 32 * L::kSoft)
       masks[i] = i >= nrows ? 0ull
-                 : a.masks  ? (unsigned long long)__ldg(a.masks + seq.first + i0 + i)
+                 : a.masks  ? (unsigned long long)fetch(a.masks + seq.first + i0 + i)
                             : ~0ull >> (63 - (i0 + i));
     fence_proxy_async_smem();
   }
@@ -521,10 +521,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       while (rest) {  // drafted values that are not finite reach the rows that see them
         const int j0 = __ffsll((long long)rest) - 1;
         rest &= rest - 1;
-        const int page = __ldg(trow + (seq.ctx + j0) / ATTN_PAGE);
+        const int page = fetch(trow + (seq.ctx + j0) / ATTN_PAGE);
         if (lane < 16 && page >= 0 && page < a.num_pages) {
           const size_t at = (((size_t)page * ATTN_PAGE + (seq.ctx + j0) % ATTN_PAGE) * kHKV + head) * kD + d;
-          const float v = __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.v_pages) + at) << 16);
+          const float v = __uint_as_float((uint32_t)fetch(static_cast<const uint16_t*>(a.v_pages) + at) << 16);
           if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u)
 #pragma unroll
             for (int j = 0; j < kCols; ++j)

@@ -103,7 +103,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   // used.
   const int first_page = s * (a.split_len / ATTN_PAGE) + lane;
   int first_entries = -1;
-  if ((warp == L::kKWarp || warp == L::kVWarp) && first_page < a.max_blocks) first_entries = __ldg(a.table + (size_t)b * a.max_blocks + first_page);
+  if ((warp == L::kKWarp || warp == L::kVWarp) && first_page < a.max_blocks) first_entries = fetch(a.table + (size_t)b * a.max_blocks + first_page);
   const Seq seq = load_seq(a, b);
   const int i0 = rt * kRows;  // the block's first drafted row
   const int nrows = min(kRows, seq.rows - i0);
@@ -149,7 +149,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   int entries = -1, entries_next = -1;
   auto entry_at = [&](int g) -> int {
     const int t = k0 + g * 8 * kKeys + lane * ATTN_PAGE;
-    return t < k1 ? __ldg(trow + t / ATTN_PAGE) : -1;
+    return t < k1 ? fetch(trow + t / ATTN_PAGE) : -1;
   };
   auto load = [&](const CUtensorMap* map, uint64_t* full, uint32_t operand, int n) {
     const int st = n % kStages, p = lane & (kPages - 1), half = lane / kPages;
@@ -199,7 +199,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     if (tid < kRows) {
       unsigned long long m = 0;
       if (tid < nrows)
-        m = (a.masks ? (unsigned long long)__ldg(a.masks + seq.first + i0 + tid) : ~0ull >> (63 - (i0 + tid))) &
+        m = (a.masks ? (unsigned long long)fetch(a.masks + seq.first + i0 + tid) : ~0ull >> (63 - (i0 + tid))) &
             (~0ull >> (64 - seq.rows));  // bits past the sequence's rows see nothing
       masks[tid] = m;
     }
@@ -214,7 +214,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
     for (int k = 0; k < 32; k += 4) {
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < nrows) v = __ldg(reinterpret_cast<const float4*>(src + k));
+      if (i < nrows) v = fetch(reinterpret_cast<const float4*>(src + k));
       x[k] = v.x, x[k + 1] = v.y, x[k + 2] = v.z, x[k + 3] = v.w;
     }
   }
@@ -571,13 +571,13 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       while (rest && g == 0) {  // drafted values that are not finite reach the rows that see them
         const int j0 = __ffsll((long long)rest) - 1;
         rest &= rest - 1;
-        const int page = __ldg(trow + (seq.ctx + j0) / ATTN_PAGE);
+        const int page = fetch(trow + (seq.ctx + j0) / ATTN_PAGE);
         if (!(mask >> j0 & 1) || page < 0 || page >= a.num_pages) continue;
         const size_t at = (((size_t)page * ATTN_PAGE + (seq.ctx + j0) % ATTN_PAGE) * kHKV + head) * kD;
 #pragma unroll
         for (int i = 0; i < kD; ++i) {
-          const float v = kF32 ? __ldg(static_cast<const float*>(a.v_pages) + at + i)
-                               : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.v_pages) + at + i) << 16);
+          const float v = kF32 ? fetch(static_cast<const float*>(a.v_pages) + at + i)
+                               : __uint_as_float((uint32_t)fetch(static_cast<const uint16_t*>(a.v_pages) + at + i) << 16);
           if ((__float_as_uint(v) & 0x7f800000u) == 0x7f800000u) o[i] += v;
         }
       }

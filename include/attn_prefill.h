@@ -409,7 +409,7 @@ int attn_append_paged_bf16kv(const void *q, const void *k, const void *v, int in
  * it (attn_append_paged). Row i of sequence b sees the contextLens[b] tokens
  * before the rows and, of the rows, those j whose bit is set in its mask:
  *   out[r][h][:] = sum_{j in K} softmax_j(q[r][h] . k_b[j][h/4] / 8) v_b[j][h/4][:]
- *   q, out     [N][32][64] fp32, the batch's packed rows
+ *   q, out     [N][32][64] fp32, the batch's packed rows; out may be q
  *   masks      int64 [N], bit j for row j of the same sequence (itself included
  *              or not, as set; bits past its rows are ignored). NULL: a chain,
  *              row i sees rows 0 .. i (one row a sequence: a decode step)

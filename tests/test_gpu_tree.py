@@ -204,6 +204,22 @@ def test_a_query_that_is_nan_stays_in_its_row(cp, bf16, rows, splits):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("rows", [3, 7, 40])
+@pytest.mark.parametrize("splits", [1, 4, 20])
+def test_out_may_be_q(cp, bf16, rows, splits):
+    lens = [(3000, rows), (200, rows)]
+    b = R.make_batch(lens, bf16=bf16, seed=65)
+    masks, q = R.tree_masks(lens, seed=1), queries(2 * rows, seed=6)
+    want = run(cp, b, q, masks, bf16, splits)
+    need = cp.attn_tree_workspace_bytes(2, 2 * rows, rows, 3000, splits)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    call = cp.attn_tree_paged_bf16kv if bf16 else cp.attn_tree_paged
+    call(q, b["kp"], b["vp"], b["table"], b["ctx"], b["starts"], torch.from_numpy(masks).cuda(), q, rows, 3000, splits,
+         ws)
+    assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("splits", [1, 3])
 def test_bad_pages_read_as_zeros(cp, bf16, splits):
     lens = [(500, 6), (40, 2)]

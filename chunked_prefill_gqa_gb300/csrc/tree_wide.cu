@@ -458,6 +458,8 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 
       int k = 0;  // the group's k-th tile
       for (int n = g; n < ntiles; n += 2, ++k) {
+        // With two buffers of S its next one waits for this product anyway.
+        if (kF32 && k > 0) add_o(k - 1);
         const int buf = n % L::kBufs;
         const uint32_t s_tmem = lane_tmem + L::kColS + buf * L::kBufCols;
         failed |= !wait.warp(&sfull[buf], (n / L::kBufs) & 1);
@@ -545,7 +547,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             for (int t = 0; t < 3; ++t) tmem_st16(s_tmem + t * 32 + h / 2, w[t]);
           }
         }
-        if (k > 0) add_o(k - 1);
+        if (!kF32 && k > 0) add_o(k - 1);
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
           for (int i = 0; i < kD; ++i) o[i] *= alpha;

@@ -338,10 +338,10 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         *reinterpret_cast<float4*>(at) = h;
         *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x.x - h.x, x.y - h.y, x.z - h.z, x.w - h.w);
       };
-      for (int n = 0; n < ntiles; ++n) {
+      auto convert_k = [&](int n) -> bool {
         const int st = n % kStages;
         uint8_t* const stage = smem + st * L::kStageBytes;
-        if (!wait.warp(&kfull[st], (n / kStages) & 1)) break;
+        if (!wait.warp(&kfull[st], (n / kStages) & 1)) return false;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           float4 x[4];
@@ -353,7 +353,16 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&kready[st]);
-        if (!wait.warp(&vfull[st], (n / kStages) & 1)) break;
+        return true;
+      };
+      // K of the next tile first: its stage is free before V's, and the scores that
+      // wait for it are what the softmax waits for.
+      bool ok = ntiles == 0 || convert_k(0);
+      for (int n = 0; ok && n < ntiles; ++n) {
+        if (n + 1 < ntiles && !(ok = convert_k(n + 1))) break;
+        const int st = n % kStages;
+        uint8_t* const stage = smem + st * L::kStageBytes;
+        if (!(ok = wait.warp(&vfull[st], (n / kStages) & 1))) break;
         const bool tail = k0 + (n + 1) * kKeys > seq.ctx;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -377,6 +386,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
                   y[k] = 0.f;
                   bad = true;
                 }
+              if (bad) *reinterpret_cast<float4*>(stage + L::kV + unit * 16) = x[i];
               if (bad && pos < k1) atomicOr(odd + (at >> 5), 1u << (at & 31));
             }
           }

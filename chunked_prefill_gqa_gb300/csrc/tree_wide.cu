@@ -76,7 +76,7 @@ struct Wide {
   static constexpr uint32_t kSmemBar = kSmemEnds + 128 * 8;
   // In the ring once it is idle: the groups' exchange, then the block's rows.
   static constexpr uint32_t kSmemRows = 2 * 128 * 32 * 4;
-  static constexpr int kNumBars = 6 * kStages + 2 * kBufs + 4 + 3;
+  static constexpr int kNumBars = 6 * kStages + 2 * kBufs + 4 + 4;
   static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2)
   static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
   static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
@@ -135,6 +135,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   uint64_t* const odone = pfull + 2;                                        // [group] PV complete
   uint64_t* const qready = odone + 2;                                       // q's terms in tensor memory
   uint64_t* const drain = qready + 1;                                       // [2] MMAs in flight on abort
+  uint64_t* const sissued = drain + 2;                                      // S of the next tile issued
   uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
   uint32_t* const odd = words + 2;  // [2] drafted rows whose value is not finite
@@ -279,6 +280,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
             mma_commit(&sfull[buf]);
             mma_commit(&kempty[st]);
+            if (kF32 && n > 0) mbar_arrive(sissued);
           }
           __syncwarp();
         }
@@ -286,6 +288,9 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         for (int n = 0; n < ntiles; ++n) {
           const int st = n % kStages, g = n & 1, buf = n % L::kBufs;
           if (!wait.warp(&go[st], (n / kStages) & 1) || !wait.warp(&pfull[g], (n >> 1) & 1)) break;
+          // fp32: O of a tile after S of the next, or the two buffers' products share
+          // the pipe, both end late and the pipe then waits for both softmaxes.
+          if (kF32 && n + 1 < ntiles && !wait.warp(sissued, n & 1)) break;
           tc_fence_after();
           const uint32_t d = tmem + L::kColO + g * kD, p = tmem + L::kColS + buf * L::kBufCols;
           const uint32_t vb = base + st * L::kStageBytes + L::kV;

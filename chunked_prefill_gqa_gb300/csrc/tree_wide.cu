@@ -63,24 +63,25 @@ struct Wide {
   static constexpr uint32_t kStageBytes = (kF32 ? 4 : 2) * kOperand; // K (K lo) V (V lo)
   static constexpr uint32_t kV = (kF32 ? 2 : 1) * kOperand;
   static constexpr int kStages = kF32 ? 3 : 8;
-  // Tensor memory: q's terms, then buffers of S (p overwrites it) and the rest of
-  // p, then the groups' O. With bf16 pages there is room for a third buffer, so
-  // S(n + 2) runs ahead of PV(n) and a group finds it ready; with fp32 pages it
-  // follows PV(n), whose p it overwrites.
-  static constexpr int kBufs = kF32 ? 2 : 3;
-  static constexpr uint32_t kColQ = 0, kColS = kF32 ? 128 : 96, kBufCols = kF32 ? 128 : 96;
-  static constexpr uint32_t kColO = kColS + kBufs * kBufCols;
+  // Tensor memory: q's terms, then three buffers of S (p overwrites it; with fp32
+  // pages its lo part lies beside them, a buffer a group), so S(n + 2) runs ahead of
+  // PV(n) and a group finds it ready; then O, one a group, or with fp32 pages one
+  // that a group reads as soon as it is complete, before the other's product.
+  static constexpr int kBufs = 3, kOs = kF32 ? 1 : 2;
+  static constexpr uint32_t kColQ = 0, kColS = kF32 ? 128 : 96, kBufCols = kF32 ? 64 : 96;
+  static constexpr uint32_t kColLo = kColS + kBufs * kBufCols;
+  static constexpr uint32_t kColO = kColLo + (kF32 ? 2 * kKeys : 0);
   static constexpr uint32_t kSmemMask = kStages * kStageBytes;
   static constexpr uint32_t kSmemMl = kSmemMask + kRows * 8;         // [2 groups][128 rows] (reference, sum)
   static constexpr uint32_t kSmemEnds = kSmemMl + 2 * 128 * 8;       // [128 rows] the same of both groups together
   static constexpr uint32_t kSmemBar = kSmemEnds + 128 * 8;
   // In the ring once it is idle: the groups' exchange, then the block's rows.
   static constexpr uint32_t kSmemRows = 2 * 128 * 32 * 4;
-  static constexpr int kNumBars = 6 * kStages + 2 * kBufs + 4 + 4;
+  static constexpr int kNumBars = 6 * kStages + 2 * kBufs + 4 + 6;
   static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2)
   static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
   static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
-  static_assert(kColO + 2 * kD <= 512, "TMEM layout");
+  static_assert(kColO + kOs * kD <= 512, "TMEM layout");
   static_assert(kSmemRows + 128 * kRowStride * 4 <= kStages * kStageBytes, "the exchange and the rows fit the ring");
 };
 
@@ -135,7 +136,8 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   uint64_t* const odone = pfull + 2;                                        // [group] PV complete
   uint64_t* const qready = odone + 2;                                       // q's terms in tensor memory
   uint64_t* const drain = qready + 1;                                       // [2] MMAs in flight on abort
-  uint64_t* const sissued = drain + 2;                                      // S of the next tile issued
+  uint64_t* const oread = drain + 2;                                        // (fp32) O read
+  uint64_t* const pissued = oread + 1;                                      // (fp32) [2] O of the group's tile issued
   uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
   uint32_t* const odd = words + 2;  // [2] drafted rows whose value is not finite
@@ -176,7 +178,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     for (int i = lane; i < L::kNumBars; i += 32) {
       const int kind = i / kStages;  // kfull, vfull, kready, vready, kempty, vempty, then the single ones
       mbar_init(&kfull[i], kind < 6 ? ((kind & ~1) == 2 && kF32 ? L::kConvWarps : 1)
-                           : &kfull[i] >= pfull && &kfull[i] < odone ? quarters
+                           : (&kfull[i] >= pfull && &kfull[i] < odone) || &kfull[i] == oread ? quarters
                            : &kfull[i] == qready                     ? kSoft
                                                                      : 1);
     }
@@ -244,7 +246,10 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         for (int i = max(0, min(n, ntiles) - kStages); i < min(n, ntiles); ++i)
           mbar_wait(&full[i % kStages], (i / kStages) & 1, 1000000);
     } else if (warp == L::kQkWarp || warp == L::kPvWarp) {
-      // Two issuers, so that one's waits and issue run under the other's.
+      // Two issuers, so that one's waits and issue run under the other's. With fp32
+      // pages S of a tile is issued after O of the one two before: in the pipe
+      // behind it, or both would end late, and one group's softmax runs under both
+      // (16 rows of 16 sequences of 16384 tokens: 219 us, and 238 in no order).
       const uint32_t base = smem_u32(smem);
       const bool qk = warp == L::kQkWarp;
       uint64_t* const go = (kF32 ? kready : kfull) + (qk ? 0 : kStages);  // K, or V, ready
@@ -253,7 +258,8 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         for (int n = 0; ok && n < ntiles; ++n) {
           const int st = n % kStages, buf = n % L::kBufs;
           if (!(ok = wait.warp(&go[st], (n / kStages) & 1) &&
-                     (n < L::kBufs || wait.warp(&sfree[buf], (n / L::kBufs - 1) & 1))))
+                     (n < L::kBufs || wait.warp(&sfree[buf], (n / L::kBufs - 1) & 1)) &&
+                     (!kF32 || n < 2 || wait.warp(&pissued[n & 1], ((n >> 1) - 1) & 1))))
             break;
           tc_fence_after();
           const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes);
@@ -280,7 +286,6 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             }
             mma_commit(&sfull[buf]);
             mma_commit(&kempty[st]);
-            if (kF32 && n > 0) mbar_arrive(sissued);
           }
           __syncwarp();
         }
@@ -288,11 +293,10 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         for (int n = 0; n < ntiles; ++n) {
           const int st = n % kStages, g = n & 1, buf = n % L::kBufs;
           if (!wait.warp(&go[st], (n / kStages) & 1) || !wait.warp(&pfull[g], (n >> 1) & 1)) break;
-          // fp32: O of a tile after S of the next, or the two buffers' products share
-          // the pipe, both end late and the pipe then waits for both softmaxes.
-          if (kF32 && n + 1 < ntiles && !wait.warp(sissued, n & 1)) break;
+          if (kF32 && n > 0 && !wait.warp(oread, (n - 1) & 1)) break;
           tc_fence_after();
-          const uint32_t d = tmem + L::kColO + g * kD, p = tmem + L::kColS + buf * L::kBufCols;
+          const uint32_t d = tmem + L::kColO + g % L::kOs * kD, p = tmem + L::kColS + buf * L::kBufCols;
+          const uint32_t p_lo = tmem + L::kColLo + g * kKeys;
           const uint32_t vb = base + st * L::kStageBytes + L::kV;
           if (elect()) {
             if constexpr (kF32) {
@@ -300,7 +304,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
               const uint64_t vd = sdesc_sw128a32_mn(vb, kHalf);
               constexpr uint64_t lo = L::kOperand >> 4;
 #pragma unroll
-              for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + 64 + x * 8, vd + x * 64, id, x > 0);
+              for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p_lo + x * 8, vd + x * 64, id, x > 0);
 #pragma unroll
               for (int x = 0; x < 8; ++x) mma_tf32_ts(d, p + x * 8, vd + lo + x * 64, id, 1);
 #pragma unroll
@@ -317,6 +321,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             mma_commit(&odone[g]);
             mma_commit(&sfree[buf]);
             mma_commit(&vempty[st]);
+            if (kF32) mbar_arrive(&pissued[g]);
           }
           __syncwarp();
         }
@@ -412,7 +417,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     const int row = quarter * 32 + lane;
     const bool active = quarter < quarters;
     const uint32_t lane_tmem = tmem + ((uint32_t)(quarter * 32) << 16);
-    const uint32_t o_tmem = lane_tmem + L::kColO + g * kD;
+    const uint32_t o_tmem = lane_tmem + L::kColO + g % L::kOs * kD;
     float ref = kUnseen, l0 = 0.f, l1 = 0.f;
     float o[kD];
 #pragma unroll
@@ -469,11 +474,16 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < 32; i += 2) add2(o[h + i], o[h + i + 1], o[h + i], o[h + i + 1], t[i], t[i + 1]);
         }
+        if (kF32) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(oread);
+        }
       };
 
       int k = 0;  // the group's k-th tile
       for (int n = g; n < ntiles; n += 2, ++k) {
-        // With two buffers of S its next one waits for this product anyway.
+        // fp32: at once, the other group's product waits for it.
         if (kF32 && k > 0) add_o(k - 1);
         const int buf = n % L::kBufs;
         const uint32_t s_tmem = lane_tmem + L::kColS + buf * L::kBufCols;
@@ -547,7 +557,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
               fma2(lo[i], lo[i + 1], tf32_hi(y[i]), tf32_hi(y[i + 1]), -1.f, -1.f, y[i], y[i + 1]);
             }
             tmem_st32(s_tmem + h, *reinterpret_cast<float(*)[32]>(y));
-            tmem_st32(s_tmem + 64 + h, lo);
+            tmem_st32(lane_tmem + L::kColLo + g * kKeys + h, lo);
           } else {
             uint32_t w[3][16];
 #pragma unroll

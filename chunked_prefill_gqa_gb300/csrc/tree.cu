@@ -536,8 +536,8 @@ int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtenso
 
 // Variants by page type and the drafted rows of a block. Long calls take the least
 // that holds their rows. Measured on 16 sequences of 16384 tokens: bf16 pages, 8 rows,
-// tree_tc 99 us and tree_wide 140; 16 rows, 175 (as two tiles of 8: 200) and 142. fp32
-// pages, 4 rows, the kernel here 202 us and tree_wide 250; 8 rows, 312 and 251.
+// tree_tc 98 us and tree_wide 130; 16 rows, 200 (as two tiles of 8) and 131. fp32 pages,
+// 4 rows, the kernel here 201 us and tree_wide 214; 8 rows, 312 and 215.
 // A small call is another matter: where a block for every 128 keys of every tile of
 // few rows has its place at once, reading a page for each of those tiles costs less
 // than the longer way through a wide block: one sequence of 1000 tokens with 8 rows

@@ -548,7 +548,7 @@ int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtenso
 // 11.1; 576: two of 1000 with 32 12.1 and 11.2); on fp32 pages it depends (384: four
 // of 300 with 16 rows 9.1 and 11.0, sixteen of 60 11.4 and 8.2).
 using Variant = TreeVariant;
-const Variant kNarrow = {tree_narrow_kernel, kTokens, 32 * kWarps, kSmemAlloc, kBlocks, false, 0, 2};
+const Variant kNarrow = {tree_narrow_kernel, kTokens, 32 * kWarps, kSmemAlloc, kBlocks, false, 0, 2, 1};
 constexpr int kCount[2] = {2, 3};
 const Variant kVariants[2][3] = {{kNarrow, tree_wide_variant(false)},
                                  {tree_tc_variant(4), tree_tc_variant(8), tree_wide_variant(true)}};
@@ -638,10 +638,10 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
   if (n <= 0) {
     // The segments that take the least time, counted in tiles of 128 keys: rounds
     // of resident blocks, each as long as its tiles and what a block costs besides
-    // them, and the merge: one in a cluster; through memory two for the second kernel
-    // and what the partials take. One row on fp32 pages, 300 tokens: three segments
-    // 5.3 us, one 8.0; sixteen such sequences: three 11.6, one 8.2. 4000 tokens: 24
-    // segments 9.1 us, eight 12.4.
+    // them, and the merge: one in a cluster; through memory a second kernel and what
+    // the partials take. One row on fp32 pages, 300 tokens: three segments
+    // 5.3 us, one 8.0; sixteen such sequences: three 11.6, one 8.2. 2000 tokens: 16
+    // segments 7.0 us, eight 8.2; 4000: 24 9.1, eight 12.4.
     const Variant& x = kVariants[bf16][v];
     const int slots = d->slots[bf16][v];
     const long long units = (long long)B * kHKV * ((max_rows + x.tokens - 1) / x.tokens);
@@ -652,7 +652,7 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
     for (int s = 1; s <= limit; ++s) {
       const bool cluster = s > 1 && s <= kMaxCluster && clusters[s] > 0;
       const long long rounds = cluster ? (units + clusters[s] - 1) / clusters[s] : (units * s + slots - 1) / slots;
-      const long long merge = s == 1 ? 0 : cluster ? 1 : 2 + (long long)B * max_rows * s / 440;
+      const long long merge = s == 1 ? 0 : cluster ? 1 : x.merge + (long long)B * max_rows * s / 440;
       const long long cost = rounds * ((tiles + s - 1) / s + x.fixed) + merge;
       if (s == 1 || cost < best) {
         best = cost;

@@ -208,8 +208,8 @@ __device__ __forceinline__ void cluster_merge(const TreeArgs& a, int first_row, 
 }
 
 // A kernel of the family: drafted rows a block takes, threads, shared memory,
-// resident blocks of an SM; and what a block costs besides its keys, in the time of
-// 128 keys.
+// resident blocks of an SM; and in the time of 128 keys, what a block costs besides
+// its keys and what the second kernel does that merges segments through memory.
 struct TreeVariant {
   void (*kernel)(CUtensorMap, CUtensorMap, TreeArgs);
   int tokens, threads;
@@ -217,7 +217,7 @@ struct TreeVariant {
   int blocks;
   bool v_atom32;  // fp32 V in the 128-byte swizzle of 32-byte chunks
   int regs;       // registers a thread at least at launch (what its register split adds up to)
-  int fixed;
+  int fixed, merge;
 };
 TreeVariant tree_tc_variant(int tokens);   // bf16 pages, 4 or 8 drafted rows a block
 TreeVariant tree_wide_variant(bool bf16);  // 32 drafted rows a block

@@ -593,7 +593,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 template <int R>
 TreeVariant variant() {
   using L = Lay<R>;
-  return {tree_tc_kernel<R>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0, 5};
+  return {tree_tc_kernel<R>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0, 5, 2};
 }
 
 TreeVariant tree_tc_variant(int tokens) { return tokens == 4 ? variant<16>() : variant<32>(); }

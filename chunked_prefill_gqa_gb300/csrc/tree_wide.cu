@@ -676,8 +676,8 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 }  // namespace
 
 TreeVariant tree_wide_variant(bool bf16) {
-  if (bf16) return {tree_wide_kernel<false>, kRows, Wide<false>::kThreads, Wide<false>::kSmemAlloc, 1, false, 0, 6};
-  return {tree_wide_kernel<true>, kRows, Wide<true>::kThreads, Wide<true>::kSmemAlloc, 1, true, 126, 6};
+  if (bf16) return {tree_wide_kernel<false>, kRows, Wide<false>::kThreads, Wide<false>::kSmemAlloc, 1, false, 0, 6, 2};
+  return {tree_wide_kernel<true>, kRows, Wide<true>::kThreads, Wide<true>::kSmemAlloc, 1, true, 126, 6, 2};
 }
 
 }  // namespace attn

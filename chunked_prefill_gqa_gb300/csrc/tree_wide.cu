@@ -4,9 +4,9 @@
 // one row, and nothing of the softmax crosses threads.
 //
 // Tiles of 64 keys go in turn to two softmax groups of four warps (tile n to
-// group n % 2), each with its own S, p and O in tensor memory and its own
-// reference maximum, sum and accumulator, so one group's softmax runs under the
-// other's products; the two partials merge at the end like two segments. The
+// group n % 2), each with its own reference maximum, sum and accumulator, so one
+// group's softmax runs under the other's products; the two partials merge at the
+// end like two segments. The
 // tensor core's accumulation does not round to nearest: O of a tile starts at
 // zero, and the row's thread adds it to fp32 registers, rounded to nearest. A
 // reference that moves therefore costs a product in registers and no trip to
@@ -15,8 +15,8 @@
 //   bf16 pages (K and V as stored, q and p in three bf16 terms):
 //     S  = (q3, q2, q1) K^T        3 x 4 MMAs of 128 x 64 x 16
 //     O  = (p3, p2, p1) V          3 x 4 MMAs of 128 x 64 x 16
-//   fp32 pages (x = hi + lo, hi what the tensor core reads of x as tf32; four
-//   converter warps write K lo and V lo next to each landed tile):
+//   fp32 pages (x = hi + lo, hi a tf32 value; of K and V four converter warps round
+//   it in place in each landed tile and write lo next to it):
 //     S  = q_lo K + q_hi K_lo + q_hi K       3 x 8 MMAs of 128 x 64 x 8
 //     O  = p_lo V + p_hi V_lo + p_hi V       3 x 8 MMAs of 128 x 64 x 8
 // q and p are tensor-memory operands (p overwrites the S it came from), K a

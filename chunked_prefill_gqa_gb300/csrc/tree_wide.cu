@@ -569,7 +569,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
               y[i] = ex2(y[i]);
               y[i + 1] = ex2(y[i + 1]);
               add2(l0, l1, l0, l1, y[i], y[i + 1]);
-              split3(y[i], y[i + 1], w[0][i / 2], w[1][i / 2], w[2][i / 2]);
+              split3_cut(y[i], y[i + 1], w[0][i / 2], w[1][i / 2], w[2][i / 2]);
             }
 #pragma unroll
             for (int t = 0; t < 3; ++t) tmem_st16(s_tmem + t * 32 + h / 2, w[t]);

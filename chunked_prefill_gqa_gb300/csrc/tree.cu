@@ -27,7 +27,8 @@
 // 2^8 (p stays below 2^8, far from fp32's range), so in the steady state a page
 // costs one vote instead of a reduction over lanes and a rescaled accumulator.
 // Bound: HBM, and the two blocks that 16 sequences of 16384 tokens leave each of 128
-// SMs: 1.07 GB in 200 us, 5.4 TB/s (4 rows: 201; the mma.sync pipe is 46% active).
+// SMs: 1.07 GB in 205 us, 5.2 TB/s (4 rows: 206; the mma.sync pipe is 46% active; 201
+// with first terms that round to infinity past 2^128 - 2^115).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -66,11 +67,11 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// The tf32 terms: hi rounded to nearest (half the remainder of a truncation,
-// and of either sign, so what the products drop does not lean one way), lo the
-// exact rest, of which the tensor core reads the upper 11 bits.
-__device__ __forceinline__ uint32_t hi_of(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
-__device__ __forceinline__ uint32_t lo_of(float x) { return __float_as_uint(x - __uint_as_float(hi_of(x))); }
+// The tf32 terms of an operand of any size: hi by tf32_near, lo the exact rest, of
+// which the tensor core reads the upper 11 bits. p stays below 2^8 and needs no limit.
+__device__ __forceinline__ uint32_t hi_of(float x) { return __float_as_uint(tf32_near(x)); }
+__device__ __forceinline__ uint32_t lo_of(float x) { return __float_as_uint(x - tf32_near(x)); }
+__device__ __forceinline__ uint32_t hi_of_p(float x) { return (__float_as_uint(x) + 0x1000u) & 0xffffe000u; }
 __device__ __forceinline__ bool finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 // The tensor core's own accumulation does not round to nearest: over a long key
@@ -321,8 +322,8 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
 #pragma unroll
         for (int e = 0; e < 4; ++e) {  // a0 a1: column 2c (key c), rows g, g + 8; a2 a3: column 2c + 1 (key c + 4)
           const float p = sc[nt][(e & 1) * 2 + (e >> 1)];
-          ph[nt][e] = hi_of(p);
-          pl[nt][e] = lo_of(p);
+          ph[nt][e] = hi_of_p(p);
+          pl[nt][e] = __float_as_uint(p - __uint_as_float(ph[nt][e]));
         }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {

@@ -69,6 +69,19 @@ __device__ __forceinline__ int segment_len(const TreeArgs& a, const Seq& s) {
   return ((s.keys + a.splits - 1) / a.splits + 127) / 128 * 128;
 }
 
+// The first tf32 term of an fp32 operand, rounded to nearest: half the remainder of a
+// truncation, and of either sign, so that what the products drop does not lean one
+// way. A finite value that would round to infinity takes the largest tf32 number
+// instead, with all of the rest in its second term, x - hi. (Of an infinity that rest
+// is infinite, of a NaN NaN.)
+__device__ __forceinline__ float tf32_near(float x) {
+  float y;
+  asm("min.xorsign.abs.f32 %0, %1, %2;"
+      : "=f"(y)
+      : "f"(__uint_as_float((__float_as_uint(x) + 0x1000u) & 0xffffe000u)), "f"(__uint_as_float(0x7f7fe000u)));
+  return y;
+}
+
 // Three bf16 terms of a pair, each rounded to nearest: 24 bits, all of an fp32
 // value whose last term does not underflow. The remainders, exact, come from
 // fused products of bf16 operands into fp32 (t * -1 + x), one instruction where

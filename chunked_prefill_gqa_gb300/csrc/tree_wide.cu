@@ -343,11 +343,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       // tensor core truncated: a remainder of twice the size and of x's own sign.)
       const int ctid = tid - 32 * L::kConvWarp;
       auto split = [&](uint8_t* at, float4 x) {
-        float4 h;
-        h.x = __uint_as_float((__float_as_uint(x.x) + 0x1000u) & 0xffffe000u);
-        h.y = __uint_as_float((__float_as_uint(x.y) + 0x1000u) & 0xffffe000u);
-        h.z = __uint_as_float((__float_as_uint(x.z) + 0x1000u) & 0xffffe000u);
-        h.w = __uint_as_float((__float_as_uint(x.w) + 0x1000u) & 0xffffe000u);
+        const float4 h = make_float4(tf32_near(x.x), tf32_near(x.y), tf32_near(x.z), tf32_near(x.w));
         *reinterpret_cast<float4*>(at) = h;
         *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x.x - h.x, x.y - h.y, x.z - h.z, x.w - h.w);
       };
@@ -446,7 +442,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
           float hi[32];
 #pragma unroll
           for (int k = 0; k < 32; ++k) {
-            hi[k] = __uint_as_float((__float_as_uint(x[k]) + 0x1000u) & 0xffffe000u);  // to nearest
+            hi[k] = tf32_near(x[k]);
             x[k] -= hi[k];
           }
           tmem_st32(lane_tmem + L::kColQ + g * 32, hi);

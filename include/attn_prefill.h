@@ -416,8 +416,11 @@ int attn_append_paged_bf16kv(const void *q, const void *k, const void *v, int in
  *   maxRows    at most 64, maxContext: bounds of the batch's row counts and
  *              context lengths
  * A row that sees nothing gets zeros. What a row does not see has no influence
- * on it, not even values that are infinite or NaN; one that it does see makes
- * its output not finite. Slots past a sequence's last row may hold anything.
+ * on it, not even values that are infinite or NaN; one that it does see has the
+ * effect that the formula gives it, or makes the output NaN. Finite operands may
+ * be as large as fp32's largest number; a sum of products past that is infinite
+ * (weights are up to 2^8 before they are divided by their sum). Slots past a
+ * sequence's last row may hold anything.
  * q stays in fp32 precision on both caches (bf16 pages are used as stored, q and
  * the probabilities split into three bf16 terms).
  * numSplits: segments per sequence, 0 = chosen from the sizes and bounds so that

@@ -85,7 +85,8 @@ __device__ __forceinline__ float tf32_near(float x) {
 // Three bf16 terms of a pair, each rounded to nearest: 24 bits, all of an fp32
 // value whose last term does not underflow. The remainders, exact, come from
 // fused products of bf16 operands into fp32 (t * -1 + x), one instruction where
-// unpacking the term first takes two.
+// unpacking the term first takes two. (For probabilities, which stay below 2^8: a
+// value next to fp32's largest would round to infinity.)
 __device__ __forceinline__ void split3(float x, float y, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
   asm("{\n\t.reg .b16 l, h, m;\n\t.reg .f32 rx, ry;\n\t"
       "mov.b16 m, 0xBF80;\n\t"  // -1
@@ -100,8 +101,9 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& t0, uint32_t&
 
 // The same with the first terms cut off instead of rounded, one byte permutation for
 // a conversion: the remainder is exact either way, the other two terms hold 16 bits
-// of it, 24 in all. (p of tree_wide, whose softmax is what takes the time: 16 rows of
-// 16 sequences of 16384 tokens 131 to 128 us.)
+// of it, 24 in all, and every finite value has finite terms, as a query needs. (Also
+// p of tree_wide, whose softmax is what takes the time: 16 rows of 16 sequences of
+// 16384 tokens 131 to 128 us.)
 __device__ __forceinline__ void split3_cut(float x, float y, uint32_t& t0, uint32_t& t1, uint32_t& t2) {
   asm("{\n\t.reg .b16 l, h, m;\n\t.reg .f32 rx, ry;\n\t"
       "mov.b16 m, 0xBF80;\n\t"  // -1

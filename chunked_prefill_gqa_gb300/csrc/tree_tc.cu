@@ -231,7 +231,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       }
       uint32_t w[3][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) split3(x[2 * k], x[2 * k + 1], w[0][k], w[1][k], w[2][k]);
+      for (int k = 0; k < 4; ++k) split3_cut(x[2 * k], x[2 * k + 1], w[0][k], w[1][k], w[2][k]);
 #pragma unroll
       for (int t = 0; t < 3; ++t)
         *reinterpret_cast<uint4*>(smem + L::kSmemQ + sw128((uint32_t)(t * R + r) * 128u + c8 * 16u)) =

@@ -450,7 +450,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         } else {
           uint32_t w[3][16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) split3(x[2 * k], x[2 * k + 1], w[0][k], w[1][k], w[2][k]);
+          for (int k = 0; k < 16; ++k) split3_cut(x[2 * k], x[2 * k + 1], w[0][k], w[1][k], w[2][k]);
 #pragma unroll
           for (int t = 0; t < 3; ++t) tmem_st16(lane_tmem + L::kColQ + t * 32 + g * 16, w[t]);
         }

@@ -82,7 +82,7 @@ def test_a_largest_key(cp, bf16, value, rows, bound, splits):
     assert cp.attn_get_device_error() == 0
 
 
-@pytest.mark.parametrize("bf16", [False])
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("value", [F32_MAX, -F32_MAX, 2.0 ** 128 - 2.0 ** 115, 2.0 ** 128 - 2.0 ** 119])
 @pytest.mark.parametrize("rows,bound,splits", SHAPES)
 def test_a_largest_query(cp, bf16, value, rows, bound, splits):

@@ -81,8 +81,8 @@ int launch_tc_paged(const Problem& p, const int* table, int num_pages, cudaStrea
 
 #ifdef __CUDACC__
 // A launch that may be prepared while the kernel before it in the stream still runs
-// (programmatic dependent launch); the kernel calls follow() before anything else,
-// in every thread.
+// (programmatic dependent launch); every thread of the kernel calls follow() before it
+// reads or writes anything that another launch may touch.
 template <typename... P, typename... A>
 cudaError_t launch_following(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};

@@ -450,8 +450,8 @@ tree_merge_kernel(const TreeArgs a) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int i = blockIdx.x / (kHQ / kMergeWarps);
   const int h = (blockIdx.x % (kHQ / kMergeWarps)) * kMergeWarps + (threadIdx.x >> 5);
-  const Seq seq = load_seq(a, b);  // older than the kernel before, whose blocks have all waited
-  follow();
+  follow();  // the lengths too may come from a kernel that only the one before has waited for
+  const Seq seq = load_seq(a, b);
   if (i >= seq.rows || seq.keys <= a.split_len) return;
   const int active = (seq.keys + a.split_len - 1) / a.split_len;
   const size_t at = (size_t)(seq.first + i) * kHQ + h;

@@ -79,6 +79,13 @@ int launch_tc_bf16x3(const Problem& p, cudaStream_t stream);
 // Paged K/V: p.k / p.v point at [num_pages * 16][8][64] page pools.
 int launch_tc_paged(const Problem& p, const int* table, int num_pages, cudaStream_t stream);
 
+// A refused launch is reported by its own call: the runtime would also hand it to the
+// next one that asks for the last error.
+inline cudaError_t launched(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return e;
+}
+
 #ifdef __CUDACC__
 // A launch that may be prepared while the kernel before it in the stream still runs
 // (programmatic dependent launch); every thread of the kernel calls follow() before it
@@ -94,7 +101,7 @@ cudaError_t launch_following(void (*kernel)(P...), dim3 grid, dim3 block, cudaSt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  return launched(cudaLaunchKernelEx(&cfg, kernel, P(args)...));
 }
 // Waits for the grid before this one to end, its writes visible; and lets the next
 // one be prepared.

@@ -486,7 +486,7 @@ int launch_decode(const float* q, const float* k_pages, const float* v_pages, co
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, decode_merge_kernel, a) != cudaSuccess) return ATTN_ELAUNCH;
+    if (launched(cudaLaunchKernelEx(&cfg, decode_merge_kernel, a)) != cudaSuccess) return ATTN_ELAUNCH;
   }
   return ATTN_OK;
 }

@@ -1245,7 +1245,7 @@ int tc_launch_impl(const Problem& p, cudaStream_t stream, unsigned long long tim
                : split == 3 ? tc_kernel<kTail3>
                : split == 12 ? tc_kernel<kTail12>
                             : tc_kernel<kTail>;
-  if (cudaLaunchKernelEx(&cfg, tail, mk, mv, tail_prm) != cudaSuccess) return ATTN_ELAUNCH;
+  if (launched(cudaLaunchKernelEx(&cfg, tail, mk, mv, tail_prm)) != cudaSuccess) return ATTN_ELAUNCH;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
 

@@ -1179,7 +1179,7 @@ int launch_impl(const Problem& p, cudaStream_t stream) {
                : split == 3 ? tc_bf16_kernel<kF32, 3>
                : split == 12 ? tc_bf16_kernel<kF32, 12>
                             : tc_bf16_kernel<kF32, 2>;
-  if (cudaLaunchKernelEx(&cfg, tail, mk, mv, tail_prm) != cudaSuccess) return ATTN_ELAUNCH;
+  if (launched(cudaLaunchKernelEx(&cfg, tail, mk, mv, tail_prm)) != cudaSuccess) return ATTN_ELAUNCH;
   return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
 }
 

@@ -704,7 +704,7 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  if (cudaLaunchKernelEx(&cfg, x.kernel, mk, mv, a) != cudaSuccess) return ATTN_ELAUNCH;
+  if (launched(cudaLaunchKernelEx(&cfg, x.kernel, mk, mv, a)) != cudaSuccess) return ATTN_ELAUNCH;
   if (p.splits > 1 && !p.cluster) {
     // The merge's blocks start as this grid's last ones run (programmatic
     // dependent launch) and wait for its end.
@@ -716,7 +716,7 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     mcfg.attrs = attr;
     mcfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&mcfg, tree_merge_kernel, a) != cudaSuccess) return ATTN_ELAUNCH;
+    if (launched(cudaLaunchKernelEx(&mcfg, tree_merge_kernel, a)) != cudaSuccess) return ATTN_ELAUNCH;
   }
   return ATTN_OK;
 }

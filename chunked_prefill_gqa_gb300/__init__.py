@@ -482,7 +482,9 @@ def attn_append_paged_bf16kv(k, v, kPages, vPages, blockTable, contextLens, rowS
 
 
 def attn_tree_workspace_bytes(B: int, N: int, max_rows: int, max_context: int, num_splits: int = 0) -> int:
-    """Bytes of workspace attn_tree_paged (either page type) needs on the current device."""
+    """Bytes of workspace that attn_tree_paged (either page type) makes use of on the
+    current device. A smaller batch may ask for more: its sequences are cut into more
+    segments."""
     return int(load().attn_tree_workspace_bytes(int(B), int(N), int(max_rows), int(max_context), int(num_splits)))
 
 
@@ -493,9 +495,10 @@ def attn_tree_paged(q, kPages, vPages, blockTable, contextLens, rowStart, masks,
     q, out fp32 [N][32][64]; masks int64 [N] (bit j: the row sees row j of its
     sequence) or None for a chain; the rows' keys and values are already in the
     pages at tokens contextLens[b] + i. max_rows (<= 64) and max_context bound
-    the batch. ``workspace``: a CUDA tensor of at least
-    attn_tree_workspace_bytes(B, N, max_rows, max_context, num_splits) bytes, or
-    None when none is needed."""
+    the batch. ``workspace``: a CUDA tensor of
+    attn_tree_workspace_bytes(B, N, max_rows, max_context, num_splits) bytes. With
+    num_splits 0 any smaller one, or None, does as well: the segments are then chosen
+    among those that it holds."""
     rc = (_binding or _native()).tree_paged(False, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out,
                                             max_rows, max_context, num_splits, workspace, stream)
     if rc:

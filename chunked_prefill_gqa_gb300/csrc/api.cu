@@ -456,7 +456,9 @@ int tree_paged(TreeCall c, int numSplits, void* workspace, size_t workspaceBytes
     return ATTN_EALIGN;
   DeviceState* st = nullptr;
   if ((rc = current_device(&st)) != ATTN_OK) return rc;
-  if ((rc = tree_plan(c.type == ATTN_BF16, c.B, c.max_rows, c.max_context, numSplits, &c.plan)) != ATTN_OK) return rc;
+  if ((rc = tree_plan(c.type == ATTN_BF16, c.B, c.N, c.max_rows, c.max_context, numSplits,
+                      workspace ? workspaceBytes : 0, &c.plan)) != ATTN_OK)
+    return rc;
   const size_t need = tree_workspace_bytes(c.N, c.plan);
   if (need > 0) {
     if (!workspace || workspaceBytes < need) return ATTN_ESPACE;
@@ -574,7 +576,7 @@ extern "C" size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxCo
   size_t most = 0;
   for (int bf16 = 0; bf16 < 2; ++bf16) {  // either page type may be called with it
     TreePlan plan{};
-    if (tree_plan(bf16 != 0, B, maxRows, maxContext, numSplits, &plan) != ATTN_OK) return 0;
+    if (tree_plan(bf16 != 0, B, N, maxRows, maxContext, numSplits, SIZE_MAX, &plan) != ATTN_OK) return 0;
     const size_t need = tree_workspace_bytes(N, plan);
     if (need > most) most = need;
   }

@@ -155,7 +155,8 @@ struct TreeCall {
   int B, N, max_rows, max_blocks, num_pages, max_context;
   TreePlan plan;
 };
-int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, TreePlan* plan);
+// room: bytes of workspace that a choice of segments (splits_hint 0) may take.
+int tree_plan(bool bf16, int B, int N, int max_rows, int max_context, int splits_hint, size_t room, TreePlan* plan);
 size_t tree_workspace_bytes(int N, const TreePlan& plan);
 int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream);
 

@@ -618,7 +618,7 @@ int tree_device(TreeDevice** out) {
 
 }  // namespace
 
-int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, TreePlan* plan) {
+int tree_plan(bool bf16, int B, int N, int max_rows, int max_context, int splits_hint, size_t room, TreePlan* plan) {
   TreeDevice* d = nullptr;
   const int rc = tree_device(&d);
   if (rc != ATTN_OK) return rc;
@@ -635,6 +635,12 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
   plan->variant = v;
   const int* const clusters = d->clusters[bf16][v];
   const int keys = max_context + max_rows;
+  auto cut = [&](int n) {  // into n segments, or as many of whole 128 keys as that leaves
+    const int per = (keys + n - 1) / n;
+    plan->split_len = (per + 127) / 128 * 128;
+    plan->splits = (keys + plan->split_len - 1) / plan->split_len;
+    plan->cluster = plan->splits > 1 && plan->splits <= kMaxCluster && clusters[plan->splits] > 0;
+  };
   int n = splits_hint < kMaxSplits ? splits_hint : kMaxSplits;
   if (n <= 0) {
     // The segments that take the least time, counted in tiles of 128 keys: rounds
@@ -642,7 +648,9 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
     // them, and the merge: one in a cluster; through memory a second kernel and what
     // the partials take. One row on fp32 pages, 300 tokens: three segments
     // 5.3 us, one 8.0; sixteen such sequences: three 11.6, one 8.2. 2000 tokens: 16
-    // segments 7.0 us, eight 8.2; 4000: 24 9.1, eight 12.4.
+    // segments 7.0 us, eight 8.2; 4000: 24 9.1, eight 12.4. Only what the workspace
+    // holds counts: fewer sequences may want more segments, and a buffer that was
+    // enough for the batch before is enough for every one, if not for the best cut.
     const Variant& x = kVariants[bf16][v];
     const int slots = d->slots[bf16][v];
     const long long units = (long long)B * kHKV * ((max_rows + x.tokens - 1) / x.tokens);
@@ -651,6 +659,10 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
     long long best = 0;
     n = 1;
     for (int s = 1; s <= limit; ++s) {
+      if ((size_t)N * kHQ * s * (kD + 2) * sizeof(float) > room) {  // unless a cluster, or fewer once cut
+        cut(s);
+        if (tree_workspace_bytes(N, *plan) > room) continue;  // never of one segment
+      }
       const bool cluster = s > 1 && s <= kMaxCluster && clusters[s] > 0;
       const long long rounds = cluster ? (units + clusters[s] - 1) / clusters[s] : (units * s + slots - 1) / slots;
       const long long merge = s == 1 ? 0 : cluster ? 1 : x.merge + (long long)B * max_rows * s / 440;
@@ -661,10 +673,7 @@ int tree_plan(bool bf16, int B, int max_rows, int max_context, int splits_hint, 
       }
     }
   }
-  const int per = (keys + n - 1) / n;
-  plan->split_len = (per + 127) / 128 * 128;
-  plan->splits = (keys + plan->split_len - 1) / plan->split_len;
-  plan->cluster = plan->splits > 1 && plan->splits <= kMaxCluster && clusters[plan->splits] > 0;
+  cut(n);
   return ATTN_OK;
 }
 

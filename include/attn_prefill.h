@@ -426,12 +426,16 @@ int attn_append_paged_bf16kv(const void *q, const void *k, const void *v, int in
  * numSplits: segments per sequence, 0 = chosen from the sizes and bounds so that
  * the blocks fill the device (segments of at least 128 keys, at most 64 of them;
  * larger hints count as 64). Up to eight segments run as one cluster of blocks and
- * merge in shared memory; with more their partials need `workspace`, a device
- * buffer of at least attn_tree_workspace_bytes(B, N, maxRows, maxContext,
- * numSplits) bytes, 16-byte aligned, owned by the caller, overwritten by the
- * call; calls that may overlap (other streams, graphs that run at the same
- * time) need one each. Nothing in it needs to start at zero. Where that size is 0
- * the workspace may be NULL.
+ * merge in shared memory; with more their partials go through `workspace`, a device
+ * buffer, 16-byte aligned, owned by the caller, overwritten by the call; calls that
+ * may overlap (other streams, graphs that run at the same time) need one each.
+ * Nothing in it needs to start at zero. With numSplits 0 any size is enough, NULL
+ * with 0 bytes too: segments are chosen among those whose partials it holds, and
+ * attn_tree_workspace_bytes(B, N, maxRows, maxContext, 0) is what the fastest of all
+ * take. A batch of fewer sequences is cut into more segments, so it may ask for MORE
+ * bytes than a larger one (one sequence of 16384 tokens with 32 rows 5 MB, sixteen
+ * none): a buffer for all batches of a program is the largest of their sizes, not
+ * the largest batch's. With numSplits above 0 that function's size is required.
  * A context length outside [0, maxContext], rows that run past N, 16 *
  * maxBlocks tokens or maxRows, and a page index outside [0, numPages) are
  * recorded as ATTN_EBOUNDS and clamped / read as zeros. Errors: ATTN_EINVAL
@@ -450,8 +454,8 @@ int attn_tree_paged_bf16kv(const float *q, const uint16_t *kPages, const uint16_
                            void *workspace, size_t workspaceBytes, cudaStream_t stream);
 
 /*
- * attn_tree_workspace_bytes -- the workspace the two calls above need for the
- * same sizes on the current device (enough for either); 0 when none is needed
+ * attn_tree_workspace_bytes -- the workspace that the two calls above make use of for
+ * the same sizes on the current device (enough for either); 0 when there is none
  * (one segment, or segments that merge in shared memory) or for invalid arguments.
  */
 size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxContext, int numSplits);

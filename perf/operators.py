@@ -351,7 +351,7 @@ def _own_run(s):
              eps=EPS, pairing=s["pairing"])
         return {"k": s["kPages"], "v": s["vPages"], "q": s["qOut"]}
     if s["op"] == "tree":
-        if "workspace" not in s:  # a program keeps one for its largest batch
+        if "workspace" not in s:  # a program keeps one for all of its batches, as large as any of them asks for
             need = cp.attn_tree_workspace_bytes(s["table"].shape[0], s["n"], s["max_rows"], s["max_context"])
             s["workspace"] = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
         call = cp.attn_tree_paged_bf16kv if bf16 else cp.attn_tree_paged

@@ -49,7 +49,7 @@ EXPORTS = ("attn_prefill", "attn_prefill_bf16x3", "attn_prefill_bf16kv", "attn_p
            "attn_compact_paged", "attn_compact_paged_bf16kv",
            "attn_naive_workspace_bytes", "attn_naive_scores", "attn_naive_softmax", "attn_naive_weighted_sum",
            "attn_naive_prefill", "attn_prefill_ffma", "attn_reference_prefill", "attn_selftest_timeout",
-           "attn_selftest_decode_timeout", "attn_tensor_peak", "attn_get_device_error", "attn_strerror",
+           "attn_selftest_decode_timeout", "attn_selftest_tree_timeout", "attn_tensor_peak", "attn_get_device_error", "attn_strerror",
            "attn_version")
 
 _lock = threading.Lock()
@@ -112,6 +112,8 @@ def load():
                 fn = getattr(lib, name)
                 fn.restype = ci
                 fn.argtypes = [vp] * 8 + [ci] * 7 + [vp, cs, vp]
+            lib.attn_selftest_tree_timeout.restype = ci
+            lib.attn_selftest_tree_timeout.argtypes = [vp] * 3 + [ci] + [vp] * 5 + [ci] * 8 + [vp, cs, vp]
             lib.attn_tree_workspace_bytes.restype = cs
             lib.attn_tree_workspace_bytes.argtypes = [ci] * 5
             for name in ("attn_compact_paged", "attn_compact_paged_bf16kv"):
@@ -513,6 +515,36 @@ def attn_tree_paged_bf16kv(q, kPages, vPages, blockTable, contextLens, rowStart,
                                             max_rows, max_context, num_splits, workspace, stream)
     if rc:
         raise AttnError(rc, "attn_tree_paged_bf16kv")
+    return out
+
+
+def attn_selftest_tree_timeout(q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows: int,
+                               max_context: int, num_splits: int = 0, workspace=None, withheld: int = 1, stream=None):
+    """Failure-path test of the drafted-tree kernels (arguments as attn_tree_paged, the
+    page type by kPages): the first keys of the first ``withheld`` segments never
+    arrive, their waits expire after 20 ms and ATTN_ETIMEOUT is recorded; read it with
+    attn_get_device_error(). The other segments' attention goes to out."""
+    import torch
+    floats, page = torch.float32, kPages.dtype
+    want = {"q": (q, floats), "out": (out, floats), "kPages": (kPages, page), "vPages": (vPages, page),
+            "blockTable": (blockTable, torch.int32), "contextLens": (contextLens, torch.int32),
+            "rowStart": (rowStart, torch.int32), "masks": (masks, torch.int64)}
+    for name, (t, dtype) in want.items():
+        if t is not None and (t.dtype != dtype or not t.is_cuda or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor")
+    B, N = contextLens.shape[0], q.shape[0]
+    if (page not in (torch.float32, torch.bfloat16) or tuple(q.shape) != (N, HQ, D) or out.shape != q.shape
+            or tuple(kPages.shape[1:]) != (PAGE, HKV, D) or vPages.shape != kPages.shape or blockTable.dim() != 2
+            or blockTable.shape[0] != B or tuple(rowStart.shape) != (B + 1,)
+            or (masks is not None and tuple(masks.shape) != (N,))):
+        raise ValueError("shapes or page type not as attn_tree_paged's")
+    rc = load().attn_selftest_tree_timeout(
+        _ptr(q), _ptr(kPages), _ptr(vPages), F32 if page == floats else BF16, _ptr(blockTable), _ptr(contextLens),
+        _ptr(rowStart), _ptr(masks), _ptr(out), B, N, int(max_rows), blockTable.shape[1], kPages.shape[0],
+        int(max_context), int(num_splits), int(withheld), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_selftest_tree_timeout")
     return out
 
 

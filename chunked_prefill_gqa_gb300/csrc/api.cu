@@ -588,7 +588,7 @@ extern "C" int attn_tree_paged(const float* q, const float* kPages, const float*
                                int N, int maxRows, int maxBlocks, int numPages, int maxContext, int numSplits,
                                void* workspace, size_t workspaceBytes, cudaStream_t stream) {
   return tree_paged(TreeCall{q, kPages, vPages, ATTN_F32, blockTable, contextLens, rowStart, masks, out, nullptr, B, N,
-                             maxRows, maxBlocks, numPages, maxContext, {}},
+                             maxRows, maxBlocks, numPages, maxContext, {}, 0},
                     numSplits, workspace, workspaceBytes, stream);
 }
 
@@ -598,7 +598,19 @@ extern "C" int attn_tree_paged_bf16kv(const float* q, const uint16_t* kPages, co
                                       int numPages, int maxContext, int numSplits, void* workspace,
                                       size_t workspaceBytes, cudaStream_t stream) {
   return tree_paged(TreeCall{q, kPages, vPages, ATTN_BF16, blockTable, contextLens, rowStart, masks, out, nullptr, B,
-                             N, maxRows, maxBlocks, numPages, maxContext, {}},
+                             N, maxRows, maxBlocks, numPages, maxContext, {}, 0},
+                    numSplits, workspace, workspaceBytes, stream);
+}
+
+extern "C" int attn_selftest_tree_timeout(const float* q, const void* kPages, const void* vPages, int pageType,
+                                          const int* blockTable, const int* contextLens, const int* rowStart,
+                                          const long long* masks, float* out, int B, int N, int maxRows, int maxBlocks,
+                                          int numPages, int maxContext, int numSplits, int withheld, void* workspace,
+                                          size_t workspaceBytes, cudaStream_t stream) {
+  if (B < 1 || N < 1 || withheld < 1) return ATTN_EINVAL;  // nothing to withhold
+  if (pageType != ATTN_F32 && pageType != ATTN_BF16) return ATTN_EINVAL;
+  return tree_paged(TreeCall{q, kPages, vPages, pageType, blockTable, contextLens, rowStart, masks, out, nullptr, B, N,
+                             maxRows, maxBlocks, numPages, maxContext, {}, withheld},
                     numSplits, workspace, workspaceBytes, stream);
 }
 

@@ -154,6 +154,7 @@ struct TreeCall {
   float *out, *parts;
   int B, N, max_rows, max_blocks, num_pages, max_context;
   TreePlan plan;
+  int withheld;  // failure test: segments whose first tile is never loaded, and every wait limited to 20 ms
 };
 // room: bytes of workspace that a choice of segments (splits_hint 0) may take.
 int tree_plan(bool bf16, int B, int N, int max_rows, int max_context, int splits_hint, size_t room, TreePlan* plan);

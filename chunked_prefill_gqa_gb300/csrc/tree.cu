@@ -89,6 +89,7 @@ __device__ __forceinline__ void add4(float (&o)[4], const float (&x)[4]) {
 // of a fragment touch all eight chunk positions of the swizzle once.
 __device__ __forceinline__ int turn(int n) { return (n >> 1) | ((n & 1) << 2); }
 
+template <bool kFault>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks)
 tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -155,6 +156,7 @@ tree_narrow_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       const int st = n % kStages;
       uint8_t* dst = ring + st * kStage;
       tc::mbar_arrive_expect_tx(&full[st], kStage);
+      if (withheld<kFault>(a, s, n)) return;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         tc::tma_load_2d(dst + x * kBox, &mk, &full[st], head * kD + x * 32, page * ATTN_PAGE);
@@ -549,7 +551,7 @@ int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtenso
 // 11.1; 576: two of 1000 with 32 12.1 and 11.2); on fp32 pages it depends (384: four
 // of 300 with 16 rows 9.1 and 11.0, sixteen of 60 11.4 and 8.2).
 using Variant = TreeVariant;
-const Variant kNarrow = {tree_narrow_kernel, kTokens, 32 * kWarps, kSmemAlloc, kBlocks, false, 0, 2, 1};
+const Variant kNarrow = {tree_narrow_kernel<false>, tree_narrow_kernel<true>, kTokens, 32 * kWarps, kSmemAlloc, kBlocks, false, 0, 2, 1};
 constexpr int kCount[2] = {2, 3};
 const Variant kVariants[2][3] = {{kNarrow, tree_wide_variant(false)},
                                  {tree_tc_variant(4), tree_tc_variant(8), tree_wide_variant(true)}};
@@ -575,12 +577,14 @@ int tree_device(TreeDevice** out) {
     for (int t = 0; t < 2; ++t)
       for (int v = 0; v < kCount[t]; ++v) {
         const Variant& x = kVariants[t][v];
-        if (cudaFuncSetAttribute(x.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.smem) != cudaSuccess)
-          return ATTN_ECUDA;
+        for (auto* kernel : {x.kernel, x.fault})
+          if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.smem) != cudaSuccess)
+            return ATTN_ECUDA;
         if (x.regs) {  // a split that adds up to more than the launch has would wait forever
-          cudaFuncAttributes fa;
-          if (cudaFuncGetAttributes(&fa, x.kernel) != cudaSuccess) return ATTN_ECUDA;
-          if (fa.numRegs < x.regs) return ATTN_ELAUNCH;
+          cudaFuncAttributes fa, fb;
+          if (cudaFuncGetAttributes(&fa, x.kernel) != cudaSuccess || cudaFuncGetAttributes(&fb, x.fault) != cudaSuccess)
+            return ATTN_ECUDA;
+          if (fa.numRegs < x.regs || fb.numRegs < x.regs) return ATTN_ELAUNCH;
         }
         // The occupancy queries count one block an SM for any kernel that uses
         // tensor memory; with half an SM's shared and tensor memory two run
@@ -694,7 +698,7 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
   const TreePlan& p = c.plan;
   const TreeArgs a{c.q, c.k_pages, c.v_pages, c.table, c.ctx_lens, c.row_start, c.masks, c.out, c.parts,
                    c.B, c.N, c.max_rows, c.max_blocks, c.num_pages, c.max_context, p.split_len, p.splits,
-                   p.cluster, err, 2000000000ull};
+                   p.cluster, err, c.withheld ? kFaultNs + c.withheld : kTimeoutNs};
   const int row_tiles = (c.max_rows + x.tokens - 1) / x.tokens;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.splits, kHKV * row_tiles, c.B);
@@ -713,7 +717,7 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  if (launched(cudaLaunchKernelEx(&cfg, x.kernel, mk, mv, a)) != cudaSuccess) return ATTN_ELAUNCH;
+  if (launched(cudaLaunchKernelEx(&cfg, c.withheld ? x.fault : x.kernel, mk, mv, a)) != cudaSuccess) return ATTN_ELAUNCH;
   if (p.splits > 1 && !p.cluster) {
     // The merge's blocks start as this grid's last ones run (programmatic
     // dependent launch) and wait for its end.

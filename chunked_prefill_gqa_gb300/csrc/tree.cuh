@@ -28,6 +28,15 @@ struct TreeArgs {
   unsigned long long timeout_ns;
 };
 
+// A failure test's waits are limited to 20 ms, and by as many nanoseconds more as there
+// are segments that never get their first tile. Its kernels are instantiations of their
+// own (kFault), so that the others hold nothing of it.
+constexpr unsigned long long kTimeoutNs = 2000000000ull, kFaultNs = 20000000ull;
+template <bool kFault>
+__device__ __forceinline__ bool withheld(const TreeArgs& a, int segment, int tile) {
+  return kFault && tile == 0 && segment < (int)(a.timeout_ns - kFaultNs);
+}
+
 // One sequence of the batch, its lengths checked.
 struct Seq {
   int ctx, first, rows, keys;
@@ -150,6 +159,11 @@ __device__ __forceinline__ bool elect() {
   return p != 0;
 }
 
+// Waits up to timeout_ns, or until another warp of the block has given up. A block in
+// which a wait ran out winds down: every warp leaves its loop at its next wait, all of
+// them meet, and only then, with the abort flag final, do the warps that started
+// copies and products wait for those still in flight. (One that looked earlier could
+// have started its last and left while another warp still waited for it.)
 struct Wait {
   unsigned* err;
   unsigned long long timeout_ns;
@@ -238,11 +252,26 @@ __device__ __forceinline__ void cluster_merge(const TreeArgs& a, int first_row, 
   tc::cluster_sync_all();
 }
 
+// Waits for the copies of the last `stages` of `issued` tiles to land.
+__device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int issued, uint64_t timeout_ns) {
+#pragma unroll 1
+  for (int i = max(0, issued - stages); i < issued; ++i) tc::mbar_wait(&full[i % stages], (i / stages) & 1, timeout_ns);
+}
+// Waits for every product the warp has issued; the whole warp comes here.
+__device__ __forceinline__ void drain_products(uint64_t* bar, uint64_t timeout_ns) {
+  if (elect()) {
+    tc::mma_commit(bar);
+    tc::mbar_wait(bar, 0, timeout_ns);
+  }
+  __syncwarp();
+}
+
 // A kernel of the family: drafted rows a block takes, threads, shared memory,
 // resident blocks of an SM; and in the time of 128 keys, what a block costs besides
 // its keys and what the second kernel does that merges segments through memory.
 struct TreeVariant {
   void (*kernel)(CUtensorMap, CUtensorMap, TreeArgs);
+  void (*fault)(CUtensorMap, CUtensorMap, TreeArgs);  // the failure test's
   int tokens, threads;
   uint32_t smem;
   int blocks;

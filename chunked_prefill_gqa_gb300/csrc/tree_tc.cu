@@ -79,7 +79,7 @@ struct Lay {
   static constexpr uint32_t kSmemEnds = kSmemMax + 5 * R * 4;        // [R] (log2 maximum, sum)
   static constexpr uint32_t kSmemBar = kSmemEnds + R * 8;
   static constexpr int kNumBars = 4 * kStages + 7;
-  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2), fresh (2)
+  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2), fresh (2), issued (2)
   static constexpr uint32_t kSmemAlloc = kSmemWords + 32 + 1024;
   static_assert(kBlocks * (kSmemAlloc + 1024) <= 233472, "shared memory of an SM");
   static_assert(kColO + kN <= kTmem && kBlocks * kTmem <= 512, "TMEM layout");
@@ -104,7 +104,7 @@ __device__ __forceinline__ float* acc_at(uint8_t* smem, int j, int d) {
   return reinterpret_cast<float*>(smem + Lay<R>::kSmemAcc + sw128(at / kFree * 128u + 128u - kFree + at % kFree));
 }
 
-template <int R>
+template <int R, bool kFault>
 __global__ void __launch_bounds__(Lay<R>::kThreads, Lay<R>::kBlocks)
 tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   using L = Lay<R>;
@@ -154,6 +154,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
   uint32_t* const odd = words + 2;                 // [2] drafted rows whose value is not finite
   volatile uint32_t* const fresh = words + 4;      // [2] tile n starts O anew, at n % 2
+  volatile uint32_t* const issued = words + 6;     // [2] tiles of K and of V loaded
   unsigned long long* const masks = reinterpret_cast<unsigned long long*>(smem + L::kSmemMask);
   float2* const ends = reinterpret_cast<float2*>(smem + L::kSmemEnds);
   const Wait wait{a.err, a.timeout_ns, abort_flag};
@@ -177,9 +178,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       page = a.num_pages;  // past the pool's end: reads as zeros
     }
     const unsigned boxes = __popc(__ballot_sync(0xffffffffu, has));
-    if (lane == 0) mbar_arrive_expect_tx(&full[st], boxes * kBox);
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[st], boxes * kBox);
+      issued[operand != 0] = n + 1;
+    }
     __syncwarp();
-    if (has)
+    if (has && !(operand == 0 && withheld<kFault>(a, s, n)))
       tma_load_2d(smem + st * kStageBytes + operand + lane * kBox, map, &full[st], head * kD, page * ATTN_PAGE);
   };
   auto load_next = [&]() -> bool {  // K(ahead + 1), whose stage is free earlier, then V(ahead)
@@ -206,6 +210,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
     if (lane == 0) {
       *abort_flag = 0;
       odd[0] = odd[1] = 0;
+      issued[0] = issued[1] = 0;
     }
     __syncwarp();
     // The first tile is on its way before the block has met.
@@ -251,14 +256,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   if (warp == L::kTmaWarp) {
     while (ahead < ntiles && load_next()) {
     }
-    if (*abort_flag) {
-      // Copies still in flight land before the block's shared memory is
-      // released (K up to ahead + 1, V up to ahead - 1 may have been issued).
-      for (int i = max(0, ahead - kStages); i < min(ahead + 2, ntiles); ++i)
-        mbar_wait(&kfull[i % kStages], (i / kStages) & 1, 1000000);
-      for (int i = max(0, ahead - kStages); i < ahead; ++i)
-        mbar_wait(&vfull[i % kStages], (i / kStages) & 1, 1000000);
-    }
     __syncwarp();
   } else if (warp == L::kMmaWarp) {
     constexpr uint32_t kIdS = idesc_tree(128, R, false), kIdPV = idesc_tree(64, L::kN, true);
@@ -302,15 +299,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
       }
       __syncwarp();
     }
-    if (*abort_flag) {
-      if (elect()) {
-        mma_commit(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < a.timeout_ns) {
-        }
-      }
-    }
-    __syncwarp();
   } else {
     // ------------------------------------------------------------- softmax
     const int quarter = warp & 3, part = warp >> 2;
@@ -572,13 +560,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (*abort_flag && !whole) {  // after a failed wait the segment counts as empty
-    float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
-    for (int r = tid; r < nrows * kGroup; r += L::kThreads) {
-      if (a.cluster) ends[r] = make_float2(-INFINITY, 0.f);
-      else
-        mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
-            make_float2(-INFINITY, 0.f);
+  if (*abort_flag) {
+    if (warp == L::kTmaWarp) {  // before the block's shared memory is released
+      drain_copies(kfull, kStages, issued[0], a.timeout_ns);
+      drain_copies(vfull, kStages, issued[1], a.timeout_ns);
+    } else if (warp == L::kMmaWarp) {
+      drain_products(drain, a.timeout_ns);
+    } else if (!whole) {  // after a failed wait the segment counts as empty
+      float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+      for (int r = tid; r < nrows * kGroup; r += 32 * L::kSoft) {
+        if (a.cluster) ends[r] = make_float2(-INFINITY, 0.f);
+        else
+          mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
+              make_float2(-INFINITY, 0.f);
+      }
     }
     __syncthreads();
   }
@@ -593,7 +588,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ C
 template <int R>
 TreeVariant variant() {
   using L = Lay<R>;
-  return {tree_tc_kernel<R>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0, 5, 2};
+  return {tree_tc_kernel<R, false>, tree_tc_kernel<R, true>, R / 4, L::kThreads, L::kSmemAlloc, L::kBlocks, false, 0, 5,
+          2};
 }
 
 TreeVariant tree_tc_variant(int tokens) { return tokens == 4 ? variant<16>() : variant<32>(); }

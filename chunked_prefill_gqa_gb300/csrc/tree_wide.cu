@@ -81,14 +81,14 @@ struct Wide {
   // In the ring once it is idle: the groups' exchange, then the block's rows.
   static constexpr uint32_t kSmemRows = 2 * 128 * 32 * 4;
   static constexpr int kNumBars = 6 * kStages + 2 * kBufs + 4 + 6;
-  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2)
-  static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
+  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;    // TMEM address, abort flag, odd rows (2), issued (2)
+  static constexpr uint32_t kSmemAlloc = kSmemWords + 24 + 1024;
   static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
   static_assert(kColO + kOs * kD <= 512, "TMEM layout");
   static_assert(kSmemRows + 128 * kRowStride * 4 <= kStages * kStageBytes, "the exchange and the rows fit the ring");
 };
 
-template <bool kF32>
+template <bool kF32, bool kFault>
 __global__ void __launch_bounds__(Wide<kF32>::kThreads, 1)
 tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const TreeArgs a) {
   using L = Wide<kF32>;
@@ -144,6 +144,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
   uint32_t* const odd = words + 2;  // [2] drafted rows whose value is not finite
+  volatile uint32_t* const issued = words + 4;  // [2] tiles of K and of V loaded
   unsigned long long* const masks = reinterpret_cast<unsigned long long*>(smem + L::kSmemMask);
   float2* const ends = reinterpret_cast<float2*>(smem + L::kSmemEnds);
   const Wait wait{a.err, a.timeout_ns, abort_flag};
@@ -166,9 +167,12 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
       record_error(a.err, kDevErrBounds);
       page = a.num_pages;  // past the pool's end: reads as zeros
     }
-    if (lane == 0) mbar_arrive_expect_tx(&full[st], pages * (kF32 ? 2 : 1) * (ATTN_PAGE * 128));
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[st], pages * (kF32 ? 2 : 1) * (ATTN_PAGE * 128));
+      issued[operand != 0] = n + 1;
+    }
     __syncwarp();
-    if (has)
+    if (has && !(operand == 0 && withheld<kFault>(a, s, n)))
       tma_load_2d(smem + st * L::kStageBytes + operand + half * kHalf + p * (ATTN_PAGE * 128), map, &full[st],
                   head * kD + half * 32, page * ATTN_PAGE);
     if ((n & 7) == 7) {
@@ -189,6 +193,7 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
     if (lane == 0) {
       *abort_flag = 0;
       odd[0] = odd[1] = 0;
+      issued[0] = issued[1] = 0;
     }
     __syncwarp();
     // The first tiles are on their way before the block has met.
@@ -245,9 +250,6 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
         if (n >= kStages && !wait.warp(&empty[n % kStages], (n / kStages - 1) & 1)) break;
         load(is_k ? &mk : &mv, full, is_k ? 0 : L::kV, n);
       }
-      if (*abort_flag)  // copies still in flight land before the block's shared memory is released
-        for (int i = max(0, min(n, ntiles) - kStages); i < min(n, ntiles); ++i)
-          mbar_wait(&full[i % kStages], (i / kStages) & 1, 1000000);
     } else if (warp == L::kQkWarp || warp == L::kPvWarp) {
       // Two issuers, so that one's waits and issue run under the other's. With fp32
       // pages S of a tile is issued after O of the one two before: in the pipe
@@ -327,14 +329,6 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
             if (kF32) mbar_arrive(&pissued[g]);
           }
           __syncwarp();
-        }
-      }
-      if (*abort_flag) {
-        if (elect()) {
-          mma_commit(&drain[!qk]);
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(&drain[!qk], 0) && globaltimer_ns() - t0 < a.timeout_ns) {
-          }
         }
       }
     } else if (kF32 && warp < L::kKWarp) {
@@ -652,13 +646,20 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (*abort_flag && !whole) {  // after a failed wait the segment counts as empty
-    float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
-    for (int r = tid; r < nrows * kGroup; r += L::kThreads) {
-      if (a.cluster) ends[r] = make_float2(-INFINITY, 0.f);
-      else
-        mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
-            make_float2(-INFINITY, 0.f);
+  if (*abort_flag) {
+    if (warp == L::kKWarp || warp == L::kVWarp) {  // before the block's memory is released
+      const bool is_v = warp == L::kVWarp;
+      drain_copies(is_v ? vfull : kfull, kStages, issued[is_v], a.timeout_ns);
+    } else if (warp == L::kQkWarp || warp == L::kPvWarp) {
+      drain_products(&drain[warp == L::kPvWarp], a.timeout_ns);
+    } else if (warp < kSoft && !whole) {  // after a failed wait the segment counts as empty
+      float2* const mls = reinterpret_cast<float2*>(a.parts + (size_t)a.N * kHQ * a.splits * kD);
+      for (int r = tid; r < nrows * kGroup; r += 32 * kSoft) {
+        if (a.cluster) ends[r] = make_float2(-INFINITY, 0.f);
+        else
+          mls[((size_t)(seq.first + i0 + (r >> 2)) * kHQ + head * kGroup + (r & 3)) * a.splits + s] =
+              make_float2(-INFINITY, 0.f);
+      }
     }
     __syncthreads();
   }
@@ -672,8 +673,11 @@ tree_wide_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__
 }  // namespace
 
 TreeVariant tree_wide_variant(bool bf16) {
-  if (bf16) return {tree_wide_kernel<false>, kRows, Wide<false>::kThreads, Wide<false>::kSmemAlloc, 1, false, 0, 6, 2};
-  return {tree_wide_kernel<true>, kRows, Wide<true>::kThreads, Wide<true>::kSmemAlloc, 1, true, 126, 6, 2};
+  if (bf16)
+    return {tree_wide_kernel<false, false>, tree_wide_kernel<false, true>, kRows, Wide<false>::kThreads,
+            Wide<false>::kSmemAlloc, 1, false, 0, 6, 2};
+  return {tree_wide_kernel<true, false>, tree_wide_kernel<true, true>, kRows, Wide<true>::kThreads,
+          Wide<true>::kSmemAlloc, 1, true, 126, 6, 2};
 }
 
 }  // namespace attn

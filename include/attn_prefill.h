@@ -567,6 +567,22 @@ int attn_selftest_decode_timeout(const float *q, const float *kPages, const floa
                                  cudaStream_t stream);
 
 /*
+ * attn_selftest_tree_timeout -- the same test for the drafted-tree kernels: the
+ * arguments, checks and workspace of attn_tree_paged (pageType ATTN_F32) or
+ * attn_tree_paged_bf16kv (ATTN_BF16), but the first `withheld` segments of every
+ * sequence never get their first keys and every bounded wait is limited to 20 ms.
+ * Their blocks record ATTN_ETIMEOUT, wind down and count as segments without keys:
+ * out is the attention over the other segments' keys, zeros where there is none; a
+ * sequence in one segment of its own (not one of a cluster) is left unwritten. The
+ * context stays usable. Requires B, N and withheld >= 1 (ATTN_EINVAL otherwise).
+ */
+int attn_selftest_tree_timeout(const float *q, const void *kPages, const void *vPages, int pageType,
+                               const int *blockTable, const int *contextLens, const int *rowStart,
+                               const long long *masks, float *out, int B, int N, int maxRows, int maxBlocks,
+                               int numPages, int maxContext, int numSplits, int withheld, void *workspace,
+                               size_t workspaceBytes, cudaStream_t stream);
+
+/*
  * attn_tensor_peak -- a measurement of this GPU's tensor pipe, not an
  * attention computation: the rate against which the prefill kernels'
  * contractions are judged compute-bound or not (page 1, "Inference Attention

@@ -22,12 +22,12 @@
 // segments with l_s = 0 (m_s = -inf). With one segment the split kernel writes
 // the output directly and no partials are stored.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <mutex>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace attn {
 namespace {
@@ -388,35 +388,9 @@ int decode_device(DecodeDevice** out) {
   return ATTN_OK;
 }
 
-// The driver's tensor-map encoder, looked up once (a function-local static is
-// initialised once even when the first calls come from several threads).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  return fn;
-}
-
-// A page pool [num_pages * 16][8][64] fp32 as the 2-D tensor (head * 64 + d,
-// row); a box is 32 floats (one 128-byte swizzle row) x the 16 rows of a page.
+// A page pool [num_pages * 16][8][64] fp32; a box is the 16 rows of a page.
 int encode_page_pool(const float* base, int num_pages, CUtensorMap* map) {
-  auto enc = tensor_map_encoder();
-  if (!enc) return ATTN_ETMA;
-  const cuuint32_t ones[2] = {1, 1};
-  const cuuint64_t dims[2] = {(cuuint64_t)kHKV * kD, (cuuint64_t)num_pages * ATTN_PAGE};
-  const cuuint64_t strides[1] = {(cuuint64_t)kHKV * kD * 4};
-  const cuuint32_t box[2] = {32, ATTN_PAGE};
-  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(base), dims, strides, box, ones,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return ATTN_ETMA;
-  return ATTN_OK;
+  return encode_rows_map(base, false, (long long)num_pages * ATTN_PAGE, ATTN_PAGE, CU_TENSOR_MAP_SWIZZLE_128B, map);
 }
 
 }  // namespace

@@ -50,12 +50,12 @@
 // Every wait is bounded; on expiry the kernel records ATTN_ETIMEOUT in the
 // device error word, all roles wind down, and TMEM is freed.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <mutex>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace attn {
 namespace {
@@ -1009,39 +1009,13 @@ tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUten
 // Host side
 // ---------------------------------------------------------------------------
 
-// The driver's tensor-map encoder, looked up once (a function-local static is
-// initialised once even when the first calls come from several threads).
-PFN_cuTensorMapEncodeTiled_v12000 get_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  return fn;
-}
-
-// k, v [rows][8][64] as a 2-D tensor (head * 64 + d, row); a box is 32 floats
-// (one 128-byte swizzle row) x box_rows rows: 64 keys of a contiguous cache, or
-// one 16-token page of a paged cache ([pages * 16][8][64]).
+// k, v [rows][8][64]; a box is 64 keys of a contiguous cache, or one 16-token page of a
+// paged cache ([pages * 16][8][64]).
 // K lands in the 128-byte swizzle of K-major operands; V, an MN-major tf32
 // operand, in the 128-byte swizzle of 32-byte chunks that the tensor core
 // requires of MN-major 32-bit operands.
 int encode_kv_map(const float* base, int rows, int box_rows, CUtensorMapSwizzle swizzle, CUtensorMap* map) {
-  auto enc = get_encoder();
-  if (!enc) return ATTN_ETMA;
-  const cuuint32_t ones[2] = {1, 1};
-  const cuuint64_t dims[2] = {(cuuint64_t)kHKV * kD, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kHKV * kD * 4};
-  const cuuint32_t box[2] = {32, (cuuint32_t)box_rows};
-  if (enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<float*>(base), dims, strides, box, ones,
-          CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return ATTN_ETMA;
-  return ATTN_OK;
+  return encode_rows_map(base, false, rows, box_rows, swizzle, map);
 }
 
 struct TcDeviceState {

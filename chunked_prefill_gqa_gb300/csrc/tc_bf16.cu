@@ -48,12 +48,12 @@
 // Three S buffers let QK run two tiles ahead of the softmax. Every wait is
 // bounded; on expiry the kernel records ATTN_ETIMEOUT, winds down and frees TMEM.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <mutex>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.cuh"
 
 namespace attn {
 namespace {
@@ -964,35 +964,9 @@ tc_bf16_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
 // Host side
 // ---------------------------------------------------------------------------
 
-// The driver's tensor-map encoder, looked up once (a function-local static is
-// initialised once even when the first calls come from several threads).
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  return fn;
-}
-
-// k or v [rows][8][64] as a 2-D tensor (head * 64 + d, row); a box is 128
-// bytes of one head's values (64 bf16, or 32 fp32: one swizzle row) x 128 rows.
+// k or v [rows][8][64]; a box is 128 rows.
 int encode_kv_tile_map(const void* base, int rows, bool f32, CUtensorMap* map) {
-  auto enc = encoder();
-  if (!enc) return ATTN_ETMA;
-  const cuuint32_t ones[2] = {1, 1};
-  const cuuint64_t dims[2] = {(cuuint64_t)kHKV * kD, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)kHKV * kD * (f32 ? 4 : 2)};
-  const cuuint32_t box[2] = {(cuuint32_t)(f32 ? 32 : 64), (cuuint32_t)kBc};
-  if (enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
-          dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return ATTN_ETMA;
-  return ATTN_OK;
+  return encode_rows_map(base, !f32, rows, kBc, CU_TENSOR_MAP_SWIZZLE_128B, map);
 }
 
 struct DevState {

@@ -30,12 +30,12 @@
 // SMs: 1.07 GB in 205 us, 5.2 TB/s (4 rows: 206; the mma.sync pipe is 46% active; 201
 // with first terms that round to infinity past 2^128 - 2^115).
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <mutex>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
+#include "tensor_map.cuh"
 #include "tree.cuh"
 
 namespace attn {
@@ -500,41 +500,10 @@ tree_merge_kernel(const TreeArgs a) {
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      ptr = nullptr;
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }();
-  return fn;
-}
-
-// A page pool [num_pages * 16][8][64] as the 2-D tensor (head * 64 + d, row); a
-// box is 128 bytes (64 bf16, or 32 fp32) of the 16 rows of a page.
+// A page pool [num_pages * 16][8][64]; a box is the 16 rows of a page.
 int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtensorMap* map) {
-  auto enc = encoder();
-  if (!enc) return ATTN_ETMA;
-  const cuuint32_t ones[2] = {1, 1};
-  const cuuint64_t dims[2] = {(cuuint64_t)kHKV * kD, (cuuint64_t)num_pages * ATTN_PAGE};
-  const cuuint64_t strides[1] = {(cuuint64_t)kHKV * kD * (bf16 ? 2 : 4)};
-  const cuuint32_t box[2] = {bf16 ? 64u : 32u, ATTN_PAGE};
-  const auto encode = [&] {
-    return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-               const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B : CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  };
-  CUresult r = encode();
-  int dev = 0;
-  // A thread whose first CUDA call this is has no context yet; a runtime call
-  // would bind one, the driver's encoder does not.
-  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess)
-    r = encode();
-  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ETMA;
+  return encode_rows_map(base, bf16, (long long)num_pages * ATTN_PAGE, ATTN_PAGE,
+                         atom32 ? CU_TENSOR_MAP_SWIZZLE_128B_ATOM_32B : CU_TENSOR_MAP_SWIZZLE_128B, map);
 }
 
 // Variants by page type and the drafted rows of a block. Long calls take the least

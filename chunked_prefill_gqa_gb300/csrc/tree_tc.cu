@@ -32,7 +32,6 @@
 // 16384 tokens (537 MB): 1 to 4 rows 87 us (6.2 TB/s), 8 rows 99 us (5.4 TB/s; issue
 // slots 51% used, tensor pipe 36%), two blocks an SM in both.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include <mutex>
 

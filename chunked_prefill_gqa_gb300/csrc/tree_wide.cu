@@ -39,7 +39,6 @@
 // SMs gave. 16 rows on all 128 lanes, p's hi on one half and its lo on the other, two
 // products instead of three for fp32 pages: 227 us, the softmax done twice.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"

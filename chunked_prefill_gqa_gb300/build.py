@@ -1,8 +1,9 @@
 """Build libattnprefill.so in-tree with nvcc for sm_103a.
 
 Each ``csrc/*.cu`` compiles to an object in parallel, then nvcc links the
-shared library (CUDA runtime linked statically), and g++ the small CPython
-extension that marshals the serving-step calls to it. Run as a module
+shared library (CUDA runtime linked statically). Then g++ builds the small CPython
+extension that marshals the serving-step calls to it, where PyTorch is installed: C
+hosts need the library alone. Run as a module
 (``python -m chunked_prefill_gqa_gb300.build``) or call :func:`build`.
 """
 from __future__ import annotations
@@ -39,22 +40,40 @@ def _sources():
 
 
 def _deps():
-    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + sorted(glob.glob(os.path.join(CSRC, "*.cpp"))) + \
+    return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
         [os.path.join(INCLUDE, "attn_prefill.h"), os.path.abspath(__file__)]
 
 
+def _binding_deps():
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "attn_prefill.h"), os.path.abspath(__file__)]
+
+
+def _newer(path: str, deps: list) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return _newer(LIB, _deps()) and (_torch() is None or _newer(BINDING, _binding_deps()))
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = None) -> str:
     """Compile every kernel translation unit and link the library; returns its path."""
-    if not force and up_to_date():
-        return LIB
     os.makedirs(OUT, exist_ok=True)
+    library, torch = force or not _newer(LIB, _deps()), _torch()
+    binding = torch is not None and (force or not _newer(BINDING, _binding_deps()))
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside the library, which it must not keep from being linked
+        compiled = ex.submit(compile_binding, torch) if binding else None
+        if library:
+            build_library(ptxas_verbose, jobs)
+        if compiled:
+            compiled.result()
+            link_binding(torch)
+    if library and torch is None:
+        sys.stderr.write("PyTorch is not installed: the binding of the serving-step calls is not built\n")
+    return LIB
+
+
+def build_library(ptxas_verbose: bool = False, jobs: int | None = None) -> None:
     nvcc = _nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 
@@ -68,9 +87,7 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
 
     srcs = _sources()
     with cf.ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
-        binding = ex.submit(compile_binding, nvcc)
         results = list(ex.map(compile_one, srcs))
-        binding.result()
     if ptxas_verbose:
         for _, log in results:
             sys.stderr.write(log)
@@ -80,16 +97,12 @@ def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = N
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    link_binding()
-    return LIB
 
 
-def _torch() -> str:
-    """PyTorch's folder, found without importing it."""
+def _torch() -> str | None:
+    """PyTorch's folder, found without importing it; None where it is not installed."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch not found: its headers are required to build the binding")
-    return spec.submodule_search_locations[0]
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
 def _run(what: str, cmd: list) -> None:
@@ -98,22 +111,22 @@ def _run(what: str, cmd: list) -> None:
         raise RuntimeError(f"{what}:\n{r.stderr}")
 
 
-def compile_binding(nvcc: str) -> None:
-    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
-    torch = os.path.join(_torch(), "include")
+def compile_binding(torch: str) -> None:
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    include = os.path.join(torch, "include")
     _run("g++ failed on binding.cpp",
-         [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", cuda, "-isystem", torch,
-          "-isystem", os.path.join(torch, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
+         [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-isystem", cuda, "-isystem", include,
+          "-isystem", os.path.join(include, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"],
           "-c", os.path.join(CSRC, "binding.cpp"), "-o", os.path.join(OUT, "binding.o")])
 
 
-def link_binding() -> None:
+def link_binding(torch: str) -> None:
     """The CPython extension next to the library, which it finds by its own folder; PyTorch's
     own libraries are there by the time it is loaded."""
     tmp = BINDING + f".tmp{os.getpid()}"
     _run("the binding does not link",
          [shutil.which("g++") or "c++", "-shared", "-o", tmp, os.path.join(OUT, "binding.o"), "-L", OUT,
-          "-l:" + os.path.basename(LIB), "-L", os.path.join(_torch(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, BINDING)
 

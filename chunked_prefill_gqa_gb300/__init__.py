@@ -402,13 +402,16 @@ def _native():
     global _binding
     if _binding is None:
         load()
-        path = os.path.join(_HERE, "_build", "_binding.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with `python -m chunked_prefill_gqa_gb300.build`")
         import importlib.machinery
         import importlib.util
 
         import torch  # noqa: F401  (whose libraries the extension uses)
+
+        from . import build
+        path = build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing (no binding for this Python and PyTorch): build it with "
+                               "`python -m chunked_prefill_gqa_gb300.build`")
         loader = importlib.machinery.ExtensionFileLoader("_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
         loader.exec_module(module)

@@ -12,6 +12,7 @@ import concurrent.futures as cf
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -21,7 +22,6 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libattnprefill.so")
-BINDING = os.path.join(OUT, "_binding.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -44,6 +44,19 @@ def _deps():
         [os.path.join(INCLUDE, "attn_prefill.h"), os.path.abspath(__file__)]
 
 
+def binding_path() -> str | None:
+    """The binding for this Python and the installed PyTorch, whose tensors it reads in
+    place: a layout that another build of either need not share, so both are in its
+    name. None without PyTorch."""
+    torch = _torch()
+    if torch is None:
+        return None
+    with open(os.path.join(torch, "version.py")) as f:
+        got = dict(re.findall(r"^(__version__|git_version)\s*(?::[^=]*)?=\s*['\"]([^'\"]+)", f.read(), re.M))
+    tag = "-".join([sysconfig.get_config_var("SOABI"), "torch", got["__version__"], got.get("git_version", "")[:8]])
+    return os.path.join(OUT, f"_binding.{tag}.so")
+
+
 def _binding_deps():
     return [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "attn_prefill.h"), os.path.abspath(__file__)]
 
@@ -53,14 +66,14 @@ def _newer(path: str, deps: list) -> bool:
 
 
 def up_to_date() -> bool:
-    return _newer(LIB, _deps()) and (_torch() is None or _newer(BINDING, _binding_deps()))
+    return _newer(LIB, _deps()) and (_torch() is None or _newer(binding_path(), _binding_deps()))
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, jobs: int | None = None) -> str:
     """Compile every kernel translation unit and link the library; returns its path."""
     os.makedirs(OUT, exist_ok=True)
     library, torch = force or not _newer(LIB, _deps()), _torch()
-    binding = torch is not None and (force or not _newer(BINDING, _binding_deps()))
+    binding = torch is not None and (force or not _newer(binding_path(), _binding_deps()))
     with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside the library, which it must not keep from being linked
         compiled = ex.submit(compile_binding, torch) if binding else None
         if library:
@@ -123,12 +136,13 @@ def compile_binding(torch: str) -> None:
 def link_binding(torch: str) -> None:
     """The CPython extension next to the library, which it finds by its own folder; PyTorch's
     own libraries are there by the time it is loaded."""
-    tmp = BINDING + f".tmp{os.getpid()}"
+    path = binding_path()
+    tmp = path + f".tmp{os.getpid()}"
     _run("the binding does not link",
          [shutil.which("g++") or "c++", "-shared", "-o", tmp, os.path.join(OUT, "binding.o"), "-L", OUT,
           "-l:" + os.path.basename(LIB), "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"])
-    os.replace(tmp, BINDING)
+    os.replace(tmp, path)
 
 
 if __name__ == "__main__":

@@ -10,6 +10,11 @@ from chunked_prefill_gqa_gb300 import build as B
 KERNEL = 'extern "C" int answer() { return 42; }\n__global__ void k(int* p) { *p = 1; }\n'
 
 
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    B.build()
+
+
 @pytest.fixture
 def tree(tmp_path, monkeypatch):
     """A source folder with one small kernel, and a folder for what is built from it."""
@@ -23,8 +28,6 @@ def tree(tmp_path, monkeypatch):
     monkeypatch.setattr(B, "INCLUDE", str(inc))
     monkeypatch.setattr(B, "OUT", str(out))
     monkeypatch.setattr(B, "LIB", str(out / "libattnprefill.so"))
-    if hasattr(B, "BINDING"):
-        monkeypatch.setattr(B, "BINDING", str(out / "_binding.so"))
     return tmp_path
 
 
@@ -51,3 +54,34 @@ def test_a_binding_that_does_not_compile_leaves_the_library(tree):
         B.build()
     assert answer() == 42
     assert not B.up_to_date()
+
+
+@pytest.mark.parametrize("what", ["version", "git_version", "python"])
+def test_a_binding_of_another_pytorch_or_python_does_not_count(tree, monkeypatch, what):
+    """After an upgrade the old binding is neither current nor the one that is loaded."""
+    pytest.importorskip("torch")
+    B.build()
+    old = B.binding_path()
+    assert B.up_to_date() and os.path.exists(old)
+    if what == "python":
+        config = B.sysconfig.get_config_var
+        monkeypatch.setattr(B.sysconfig, "get_config_var", lambda k: "cpython-399" if k == "SOABI" else config(k))
+    else:
+        other = tree / "torch"
+        other.mkdir()
+        with open(os.path.join(B._torch(), "version.py")) as f:
+            lines = f.read().splitlines()
+        key = {"version": "__version__", "git_version": "git_version"}[what]
+        (other / "version.py").write_text("\n".join(f"{key} = '99.0'" if x.startswith(key) else x for x in lines))
+        monkeypatch.setattr(B, "_torch", lambda: str(other))
+    assert not B.up_to_date()
+    assert B.binding_path() != old and not os.path.exists(B.binding_path())
+
+
+def test_a_missing_binding_is_named(tree, monkeypatch):
+    pytest.importorskip("torch")
+    import chunked_prefill_gqa_gb300 as cp
+    cp.load()
+    monkeypatch.setattr(cp, "_binding", None)
+    with pytest.raises(RuntimeError, match="no binding for this Python and PyTorch"):
+        cp._native()

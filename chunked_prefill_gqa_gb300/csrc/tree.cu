@@ -507,18 +507,18 @@ int encode_pool(const void* base, int num_pages, bool bf16, bool atom32, CUtenso
 }
 
 // Variants by page type and the drafted rows of a block. Long calls take the least
-// that holds their rows. Measured on 16 sequences of 16384 tokens: bf16 pages, 8 rows,
-// tree_tc 98 us and tree_wide 130; 16 rows, 200 (as two tiles of 8) and 131. fp32 pages,
-// 4 rows, the kernel here 201 us and tree_wide 214; 8 rows, 312 and 215.
+// that holds their rows. Measured on 16 sequences of 16384 tokens, in graphs: bf16
+// pages, 8 rows, tree_tc 99 us and tree_wide 129; 16 rows, 184 (as two tiles of 8) and
+// 129. fp32 pages, 4 rows, the kernel here 205 us and tree_wide 216; 8 rows, 395 and 216.
 // A small call is another matter: where a block for every 128 keys of every tile of
 // few rows has its place at once, reading a page for each of those tiles costs less
 // than the longer way through a wide block: one sequence of 1000 tokens with 8 rows
-// on fp32 pages 7.7 and 9.0 us, with 16 8.2 and 9.6; with 16 rows on bf16 pages 8.5
-// and 9.2. With four sequences more blocks than places: 11.1 and 11.3, 16.8 and 11.8,
-// 10.4 and 10.7. On bf16 pages a third more blocks than places still pay (384 of 304:
-// eight sequences of 300 tokens with 16 rows 7.9 and 9.4, one of 2000 with 24 10.0 and
-// 11.1; 576: two of 1000 with 32 12.1 and 11.2); on fp32 pages it depends (384: four
-// of 300 with 16 rows 9.1 and 11.0, sixteen of 60 11.4 and 8.2).
+// on fp32 pages 7.6 and 9.0 us, with 16 8.2 and 9.4; with 16 rows on bf16 pages 8.3
+// and 8.6. With four sequences more blocks than places: 11.5 and 10.9, 17.3 and 11.4,
+// 10.1 and 10.0. On bf16 pages a third more blocks than places still pay (384 of 304:
+// eight sequences of 300 tokens with 16 rows 7.6 and 8.7, one of 2000 with 24 10.0 and
+// 10.5; 576: two of 1000 with 32 11.8 and 10.7); on fp32 pages it depends (384: four
+// of 300 with 16 rows 9.1 and 9.4, sixteen of 60 11.5 and 8.1).
 using Variant = TreeVariant;
 const Variant kNarrow = {tree_narrow_kernel<false>, tree_narrow_kernel<true>, kTokens, 32 * kWarps, kSmemAlloc, kBlocks, false, 0, 2, 1};
 constexpr int kCount[2] = {2, 3};
@@ -620,8 +620,8 @@ int tree_plan(bool bf16, int B, int N, int max_rows, int max_context, int splits
     // of resident blocks, each as long as its tiles and what a block costs besides
     // them, and the merge: one in a cluster; through memory a second kernel and what
     // the partials take. One row on fp32 pages, 300 tokens: three segments
-    // 5.3 us, one 8.0; sixteen such sequences: three 11.6, one 8.2. 2000 tokens: 16
-    // segments 7.0 us, eight 8.2; 4000: 24 9.1, eight 12.4. Only what the workspace
+    // 5.8 us, one 8.4; sixteen such sequences: three 12.3, one 8.8. 2000 tokens: 16
+    // segments 7.3 us, eight 8.6; 4000: 24 9.3, eight 13.0. Only what the workspace
     // holds counts: fewer sequences may want more segments, and a buffer that was
     // enough for the batch before is enough for every one, if not for the best cut.
     const Variant& x = kVariants[bf16][v];

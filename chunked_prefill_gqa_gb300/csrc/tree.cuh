@@ -72,7 +72,8 @@ __device__ __forceinline__ Seq load_seq(const TreeArgs& a, int b) {
 // SMs until the last of them ends, a sequence's own keys are cut evenly (48
 // sequences of 1 to 4096 tokens: five rows on bf16 pages 72 to 59 us, one row on
 // fp32 pages 132 to 105); otherwise the call's length counts, and blocks past a
-// short sequence's end leave at once.
+// short sequence's end leave at once. (So a call whose bound is far above its lengths
+// and whose segments merge through memory leaves most of its blocks without keys.)
 __device__ __forceinline__ int segment_len(const TreeArgs& a, const Seq& s) {
   if (!a.cluster) return a.split_len;
   return ((s.keys + a.splits - 1) / a.splits + 127) / 128 * 128;

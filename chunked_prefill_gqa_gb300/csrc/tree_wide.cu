@@ -28,16 +28,19 @@
 //
 // Bound: the tensor pipe, at 31.5 cycles an MMA, on as many SMs as there are blocks.
 // 16 sequences of 16384 tokens are 128 blocks of 152 places: 32 rows on bf16 pages 140
-// us (537 MB, 3.8 TB/s; 206 GFLOP of term products, 1.47 PFLOP/s; pipe active 75% on
-// those SMs, the softmax of a tile as long as its products), 16 rows on fp32 pages 219
+// us (537 MB, 3.8 TB/s; 206 GFLOP of term products, 1.47 PFLOP/s; pipe active 77% on
+// those SMs, the softmax of a tile as long as its products), 16 rows on fp32 pages 221
 // us (4.9 TB/s; pipe active 95%, half of its lanes without rows). 64 rows of one
-// sequence of 131071 tokens on bf16 pages: 144 blocks, 130 us. Run back to back for
-// long, full tiles meet the power limit and take a tenth more. A grid of one block an
-// SM that shares all tiles evenly, units cut where a block's share ends, was built on
-// an earlier form and ran 252 and 157 us for its 254 and 146: what a second unit costs
-// a block (q again, an empty pipeline, two partials through memory) is what the idle
-// SMs gave. 16 rows on all 128 lanes, p's hi on one half and its lo on the other, two
-// products instead of three for fp32 pages: 227 us, the softmax done twice.
+// sequence of 131071 tokens on bf16 pages: 144 blocks, 132 us. Those are short bursts:
+// back to back for long they meet the power limit and take 154, 235 and 144 us, and up
+// to 4 % more on another card. (Registers are full: the bf16 kernel, at 168, stores 36
+// bytes a thread to local memory and loads 68, the fp32 one, launched with 128, 12 and
+// 20.) A grid of one block an SM that shares all tiles evenly, units cut where a
+// block's share ends, was built on an earlier form and ran 252 and 157 us for its 254
+// and 146: what a second unit costs a block (q again, an empty pipeline, two partials
+// through memory) is what the idle SMs gave. 16 rows on all 128 lanes, p's hi on one
+// half and its lo on the other, two products instead of three for fp32 pages: 227 us,
+// the softmax done twice.
 #include <cuda.h>
 
 #include "common.cuh"

@@ -346,8 +346,9 @@ int attn_rope_table(const double *invFreq, float *cosSin, int numPositions, cuda
  *   y[d] = x[d] w[d] / sqrt(sum_e x[e]^2 / 64 + eps)
  *   (y[a], y[b]) -> (y[a] cos - y[b] sin, y[b] cos + y[a] sin)
  * (a, b) = (i, i + 32) for ATTN_ROPE_HALVES, (2 i, 2 i + 1) for ATTN_ROPE_PAIRS,
- * cos and sin of frequency i from row positions[n] of cosSin. fp32 arithmetic,
- * one rounding at the store.
+ * cos and sin of frequency i from row positions[n] of cosSin. fp32 arithmetic
+ * (under a norm, a head whose squares sum past fp32's range, values of 2^61 and more,
+ * comes out as zeros), one rounding at the store.
  *   q, k       N rows of 32 and 8 heads of 64, fp32 or bf16 (inType), qStride
  *              and kStride elements between rows (views into a wider projection
  *              are fine; every row starts on 16 bytes). q may be NULL.
@@ -422,7 +423,10 @@ int attn_append_paged_bf16kv(const void *q, const void *k, const void *v, int in
  * (weights are up to 2^8 before they are divided by their sum). Slots past a
  * sequence's last row may hold anything.
  * q stays in fp32 precision on both caches (bf16 pages are used as stored, q and
- * the probabilities split into three bf16 terms).
+ * the probabilities split into three bf16 terms). For one row a sequence on fp32
+ * pages attn_decode_paged is the faster call (16 sequences of 16384 tokens: 162 us,
+ * and 205 here); maxContext close to the longest context makes this one faster where
+ * its segments merge through memory.
  * numSplits: segments per sequence, 0 = chosen from the sizes and bounds so that
  * the blocks fill the device (segments of at least 128 keys, at most 64 of them;
  * larger hints count as 64). Up to eight segments run as one cluster of blocks and
@@ -470,7 +474,9 @@ size_t attn_tree_workspace_bytes(int B, int N, int maxRows, int maxContext, int 
  *   keepCounts  int32 [B], each in [0, maxKeep]
  * keep[b][i] >= i, so the moves run in place. Tokens that no accepted row moves
  * to stay as they are. A sequence whose list is not as above, or whose tokens or
- * pages are out of range, is recorded as ATTN_EBOUNDS and left as it is. Pages
+ * pages are out of range, is recorded as ATTN_EBOUNDS and left as it is. The call
+ * does not see how many rows each sequence has: an entry at or past a sequence's own
+ * rows, but below maxRows, moves whatever its slot holds. Pages
  * and table as attn_append_paged; sequences must not share the pages of their
  * rows. Errors: ATTN_EINVAL (NULL pointer, negative size, maxRows, maxBlocks or
  * numPages < 1), ATTN_ERANGE (maxRows above 64, maxKeep above maxRows, the

@@ -609,6 +609,7 @@ extern "C" int attn_selftest_tree_timeout(const float* q, const void* kPages, co
                                           size_t workspaceBytes, cudaStream_t stream) {
   if (B < 1 || N < 1 || withheld < 1) return ATTN_EINVAL;  // nothing to withhold
   if (pageType != ATTN_F32 && pageType != ATTN_BF16) return ATTN_EINVAL;
+  if (withheld > 64) withheld = 64;  // no call has more segments
   return tree_paged(TreeCall{q, kPages, vPages, pageType, blockTable, contextLens, rowStart, masks, out, nullptr, B, N,
                              maxRows, maxBlocks, numPages, maxContext, {}, withheld},
                     numSplits, workspace, workspaceBytes, stream);

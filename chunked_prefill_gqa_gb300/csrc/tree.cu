@@ -532,6 +532,16 @@ struct TreeDevice {
   int slots[2][3] = {};
   int clusters[2][3][kMaxCluster + 1] = {};
 };
+int set_up(const Variant& x, decltype(x.kernel) kernel) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.smem) != cudaSuccess)
+    return ATTN_ECUDA;
+  if (x.regs) {  // a split that adds up to more than the launch has would wait forever
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return ATTN_ECUDA;
+    if (fa.numRegs < x.regs) return ATTN_ELAUNCH;
+  }
+  return ATTN_OK;
+}
 int tree_device(TreeDevice** out) {
   constexpr int kMaxDev = 64;
   static std::mutex mu;
@@ -546,15 +556,7 @@ int tree_device(TreeDevice** out) {
     for (int t = 0; t < 2; ++t)
       for (int v = 0; v < kCount[t]; ++v) {
         const Variant& x = kVariants[t][v];
-        for (auto* kernel : {x.kernel, x.fault})
-          if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)x.smem) != cudaSuccess)
-            return ATTN_ECUDA;
-        if (x.regs) {  // a split that adds up to more than the launch has would wait forever
-          cudaFuncAttributes fa, fb;
-          if (cudaFuncGetAttributes(&fa, x.kernel) != cudaSuccess || cudaFuncGetAttributes(&fb, x.fault) != cudaSuccess)
-            return ATTN_ECUDA;
-          if (fa.numRegs < x.regs || fb.numRegs < x.regs) return ATTN_ELAUNCH;
-        }
+        if (const int rc = set_up(x, x.kernel); rc != ATTN_OK) return rc;
         // The occupancy queries count one block an SM for any kernel that uses
         // tensor memory; with half an SM's shared and tensor memory two run
         // (measured: 256 blocks of tree_tc take the time of 128).
@@ -660,6 +662,7 @@ int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream) {
   if (rc != ATTN_OK) return rc;
   const bool bf16 = c.type == ATTN_BF16;
   const Variant& x = kVariants[bf16][c.plan.variant];
+  if (c.withheld && (rc = set_up(x, x.fault)) != ATTN_OK) return rc;
   alignas(64) CUtensorMap mk, mv;
   if ((rc = encode_pool(c.k_pages, c.num_pages, bf16, false, &mk)) != ATTN_OK ||
       (rc = encode_pool(c.v_pages, c.num_pages, bf16, x.v_atom32, &mv)) != ATTN_OK)

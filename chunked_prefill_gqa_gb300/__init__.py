@@ -38,6 +38,8 @@ MAX_TOKENS = 1 << 24
 PAGE = 16
 TREE_ROWS = 64     # drafted rows of one sequence
 F32, BF16 = 0, 1   # element types of the calls that take more than one
+ROPE_AXES = 4      # positions of one row
+WEIGH_ROWS = 65536  # rows of one sequence in a weighing window
 ROPE_HALVES, ROPE_PAIRS = 0, 1   # the rotation turns dims (i, i + 32), or (2 i, 2 i + 1)
 
 # Every symbol the header declares (the CPU tests check the library exports them).
@@ -45,8 +47,12 @@ EXPORTS = ("attn_prefill", "attn_prefill_bf16x3", "attn_prefill_bf16kv", "attn_p
            "attn_prefill_bf16x3_host", "attn_prefill_bf16kv_host", "attn_full_causal", "attn_prefill_paged", "attn_decode_paged",
            "attn_decode_workspace_bytes", "attn_decode_paged_noalloc",
            "attn_rope_table", "attn_qk_norm_rope", "attn_append_paged", "attn_append_paged_bf16kv",
+           "attn_qk_norm_rope_axes", "attn_append_paged_axes", "attn_append_paged_axes_bf16kv",
            "attn_tree_paged", "attn_tree_paged_bf16kv", "attn_tree_workspace_bytes",
            "attn_compact_paged", "attn_compact_paged_bf16kv",
+           "attn_decode_weigh_paged", "attn_decode_weigh_paged_bf16kv", "attn_decode_weigh_workspace_bytes",
+           "attn_weigh_paged", "attn_weigh_paged_bf16kv", "attn_weigh_workspace_bytes",
+           "attn_evict_paged", "attn_evict_paged_bf16kv", "attn_evict_workspace_bytes",
            "attn_naive_workspace_bytes", "attn_naive_scores", "attn_naive_softmax", "attn_naive_weighted_sum",
            "attn_naive_prefill", "attn_prefill_ffma", "attn_reference_prefill", "attn_selftest_timeout",
            "attn_selftest_decode_timeout", "attn_selftest_tree_timeout", "attn_tensor_peak", "attn_get_device_error", "attn_strerror",
@@ -120,6 +126,31 @@ def load():
                 fn = getattr(lib, name)
                 fn.restype = ci
                 fn.argtypes = [vp] * 6 + [ci] * 5 + [vp]
+            axes = [cl, ci, vp]  # positionsStride, numAxes, axes
+            lib.attn_qk_norm_rope_axes.restype = ci
+            lib.attn_qk_norm_rope_axes.argtypes = [vp, vp, ci, cl, cl, vp, vp, cf, vp, vp, *axes, ci, ci, vp, vp, ci, ci, vp]
+            for name in ("attn_append_paged_axes", "attn_append_paged_axes_bf16kv"):
+                fn = getattr(lib, name)
+                fn.restype = ci
+                fn.argtypes = [vp, vp, vp, ci, cl, cl, cl, vp, vp, cf, vp, vp, *axes, ci, ci, vp, vp, vp, vp, vp, vp,
+                               ci, ci, ci, ci, vp]
+            for name in ("attn_decode_weigh_paged", "attn_decode_weigh_paged_bf16kv"):
+                fn = getattr(lib, name)
+                fn.restype = ci
+                fn.argtypes = [vp] * 7 + [cf, vp] + [ci] * 4 + [vp, cs, vp]
+            for name in ("attn_weigh_paged", "attn_weigh_paged_bf16kv"):
+                fn = getattr(lib, name)
+                fn.restype = ci
+                fn.argtypes = [vp] * 7 + [cf] + [ci] * 6 + [vp, cs, vp]
+            for name in ("attn_evict_paged", "attn_evict_paged_bf16kv"):
+                fn = getattr(lib, name)
+                fn.restype = ci
+                fn.argtypes = [vp] * 6 + [ci] * 6 + [vp, cs, vp]
+            for name, sizes in (("attn_decode_weigh_workspace_bytes", 2), ("attn_weigh_workspace_bytes", 4),
+                                ("attn_evict_workspace_bytes", 2)):
+                fn = getattr(lib, name)
+                fn.restype = cs
+                fn.argtypes = [ci] * sizes
             lib.attn_naive_workspace_bytes.restype = ctypes.c_size_t
             lib.attn_naive_workspace_bytes.argtypes = [ci, ci]
             lib.attn_naive_scores.restype = ci
@@ -486,6 +517,43 @@ def attn_append_paged_bf16kv(k, v, kPages, vPages, blockTable, contextLens, rowS
     return qOut
 
 
+def attn_qk_norm_rope_axes(q, k, positions, axes, cosSin, qOut, kOut, qWeight=None, kWeight=None, eps: float = 1e-6,
+                           pairing: int = ROPE_HALVES, stream=None):
+    """attn_qk_norm_rope for rows whose position has several axes (time, height, width).
+
+    positions int32 [A][N], A at most 4, each axis's packed (an expanded tensor will
+    do); axes: of each of the 32 frequencies the axis whose position turns it, for
+    instance ``[0] * 8 + [1] * 12 + [2] * 12`` or ``[i % 3 for i in range(32)]``.
+    cosSin (attn_rope_table) serves all axes. Returns (qOut, kOut)."""
+    rc = (_binding or _native()).qk_norm_rope_axes(q, k, positions, axes, cosSin, qOut, kOut, qWeight, kWeight, eps,
+                                                   pairing, stream)
+    if rc:
+        raise AttnError(rc, "attn_qk_norm_rope_axes")
+    return qOut, kOut
+
+
+def attn_append_paged_axes(k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin, positions, axes, kWeight=None,
+                           q=None, qOut=None, qWeight=None, eps: float = 1e-6, pairing: int = ROPE_HALVES, stream=None):
+    """attn_append_paged for rows whose position has several axes: positions int32
+    [A][N] and axes as attn_qk_norm_rope_axes. Slots go by the row as ever."""
+    rc = (_binding or _native()).append_paged_axes(False, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin,
+                                                   positions, axes, kWeight, q, qOut, qWeight, eps, pairing, stream)
+    if rc:
+        raise AttnError(rc, "attn_append_paged_axes")
+    return qOut
+
+
+def attn_append_paged_axes_bf16kv(k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin, positions, axes,
+                                  kWeight=None, q=None, qOut=None, qWeight=None, eps: float = 1e-6,
+                                  pairing: int = ROPE_HALVES, stream=None):
+    """attn_append_paged_axes into bfloat16 pages."""
+    rc = (_binding or _native()).append_paged_axes(True, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin,
+                                                   positions, axes, kWeight, q, qOut, qWeight, eps, pairing, stream)
+    if rc:
+        raise AttnError(rc, "attn_append_paged_axes_bf16kv")
+    return qOut
+
+
 def attn_tree_workspace_bytes(B: int, N: int, max_rows: int, max_context: int, num_splits: int = 0) -> int:
     """Bytes of workspace that attn_tree_paged (either page type) makes use of on the
     current device. A smaller batch may ask for more: its sequences are cut into more
@@ -567,6 +635,97 @@ def attn_compact_paged_bf16kv(kPages, vPages, blockTable, contextLens, keep, kee
                                                max_rows, stream)
     if rc:
         raise AttnError(rc, "attn_compact_paged_bf16kv")
+
+
+def attn_decode_weigh_workspace_bytes(B: int, max_context: int) -> int:
+    """Bytes of workspace attn_decode_weigh_paged (either page type) needs on the current device."""
+    return int(load().attn_decode_weigh_workspace_bytes(int(B), int(max_context)))
+
+
+def attn_decode_weigh_paged(q, kPages, vPages, weights, blockTable, contextLens, out, max_context: int,
+                            decay: float = 1.0, weighedLens=None, workspace=None, stream=None):
+    """attn_decode_paged which also adds the probabilities that every cached token was
+    given to its weight.
+
+    weights fp32 [numPages][8][16], beside the pages: W = decay W + the sum over the
+    head's four queries, and for tokens from weighedLens[b] on (int32 [B]; None:
+    contextLens[b] - 1) that sum alone. contextLens counts the new token.
+    ``workspace``: a CUDA tensor of attn_decode_weigh_workspace_bytes(B, max_context)
+    bytes. Returns out."""
+    rc = (_binding or _native()).decode_weigh_paged(False, q, kPages, vPages, weights, blockTable, contextLens, out,
+                                                    max_context, decay, weighedLens, workspace, stream)
+    if rc:
+        raise AttnError(rc, "attn_decode_weigh_paged")
+    return out
+
+
+def attn_decode_weigh_paged_bf16kv(q, kPages, vPages, weights, blockTable, contextLens, out, max_context: int,
+                                   decay: float = 1.0, weighedLens=None, workspace=None, stream=None):
+    """attn_decode_weigh_paged against bfloat16 pages, used exactly as stored."""
+    rc = (_binding or _native()).decode_weigh_paged(True, q, kPages, vPages, weights, blockTable, contextLens, out,
+                                                    max_context, decay, weighedLens, workspace, stream)
+    if rc:
+        raise AttnError(rc, "attn_decode_weigh_paged_bf16kv")
+    return out
+
+
+def attn_weigh_workspace_bytes(B: int, N: int, max_rows: int, max_context: int) -> int:
+    """Bytes of workspace attn_weigh_paged (either page type) needs on the current device."""
+    return int(load().attn_weigh_workspace_bytes(int(B), int(N), int(max_rows), int(max_context)))
+
+
+def attn_weigh_paged(q, kPages, weights, blockTable, contextLens, rowStart, max_rows: int, max_context: int,
+                     decay: float = 1.0, weighedLens=None, workspace=None, stream=None):
+    """Add what a window of rows (a prompt's last ones, say) gives to the cached tokens to
+    their weights, without the rows' attention.
+
+    q fp32 [N][32][64]; row i of sequence b stands at token contextLens[b] + i, whose
+    key is in the cache, and sees the tokens up to it. weights as
+    attn_decode_weigh_paged; weighedLens None: contextLens, all but the rows' own.
+    max_rows and max_context bound the batch. ``workspace``: a CUDA tensor of
+    attn_weigh_workspace_bytes(B, N, max_rows, max_context) bytes. Returns weights."""
+    rc = (_binding or _native()).weigh_paged(False, q, kPages, weights, blockTable, contextLens, rowStart, max_rows,
+                                             max_context, decay, weighedLens, workspace, stream)
+    if rc:
+        raise AttnError(rc, "attn_weigh_paged")
+    return weights
+
+
+def attn_weigh_paged_bf16kv(q, kPages, weights, blockTable, contextLens, rowStart, max_rows: int, max_context: int,
+                            decay: float = 1.0, weighedLens=None, workspace=None, stream=None):
+    """attn_weigh_paged against bfloat16 pages, used exactly as stored."""
+    rc = (_binding or _native()).weigh_paged(True, q, kPages, weights, blockTable, contextLens, rowStart, max_rows,
+                                             max_context, decay, weighedLens, workspace, stream)
+    if rc:
+        raise AttnError(rc, "attn_weigh_paged_bf16kv")
+    return weights
+
+
+def attn_evict_workspace_bytes(B: int, max_context: int) -> int:
+    """Bytes of workspace attn_evict_paged (either page type) needs."""
+    return int(load().attn_evict_workspace_bytes(int(B), int(max_context)))
+
+
+def attn_evict_paged(kPages, vPages, weights, blockTable, contextLens, keepLens, max_context: int, keep_first: int = 0,
+                     keep_last: int = 0, workspace=None, stream=None):
+    """Cut every sequence to keepLens[b] tokens (int32 [B]): each key/value head keeps its
+    first keep_first, its last keep_last and, of those between, the ones of the largest
+    weights, which close up (keys, values and weights; not in their old order). The
+    context is min(contextLens, keepLens) afterwards. ``workspace``: a CUDA tensor of
+    attn_evict_workspace_bytes(B, max_context) bytes."""
+    rc = (_binding or _native()).evict_paged(False, kPages, vPages, weights, blockTable, contextLens, keepLens,
+                                             max_context, keep_first, keep_last, workspace, stream)
+    if rc:
+        raise AttnError(rc, "attn_evict_paged")
+
+
+def attn_evict_paged_bf16kv(kPages, vPages, weights, blockTable, contextLens, keepLens, max_context: int,
+                            keep_first: int = 0, keep_last: int = 0, workspace=None, stream=None):
+    """attn_evict_paged on bfloat16 pages."""
+    rc = (_binding or _native()).evict_paged(True, kPages, vPages, weights, blockTable, contextLens, keepLens,
+                                             max_context, keep_first, keep_last, workspace, stream)
+    if rc:
+        raise AttnError(rc, "attn_evict_paged_bf16kv")
 
 
 def attn_naive_workspace_bytes(C: int, P: int) -> int:

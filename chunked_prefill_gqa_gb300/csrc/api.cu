@@ -539,10 +539,70 @@ RowCall append_call(const void* q, const void* k, const void* v, int inType, lon
                     int maxBlocks, int numPages) {
   return RowCall{q,        k,       v,         qStride,   kStride,      vStride, inType,  pageType,
                  qWeight,  kWeight, eps,       cosSin,    positions,    numPositions, pairing, qOut,
-                 kPages,   vPages,  blockTable, contextLens, rowStart,  B,       N,       maxBlocks, numPages};
+                 kPages,   vPages,  blockTable, contextLens, rowStart,  B,       N,       maxBlocks, numPages,
+                 0,        0,       0};
+}
+
+// The axes of a row's positions, checked and added to its call.
+int with_axes(RowCall* c, const int* positions, long long positionsStride, int numAxes, const int* axes) {
+  if (numAxes < 1 || positionsStride < 0) return ATTN_EINVAL;
+  if (numAxes > ATTN_ROPE_AXES) return ATTN_ERANGE;
+  if (c->N <= 0) return ATTN_OK;
+  if (!c->cos_sin || !positions || !axes) return ATTN_EINVAL;
+  for (int i = 0; i < ATTN_D / 2; ++i) {
+    if (axes[i] < 0 || axes[i] >= numAxes) return ATTN_EINVAL;
+    c->axis_of |= (unsigned long long)axes[i] << (2 * i);
+  }
+  c->num_axes = numAxes;
+  c->pos_stride = positionsStride;
+  return ATTN_OK;
 }
 }  // namespace
 }  // namespace attn
+
+extern "C" int attn_qk_norm_rope_axes(const void* q, const void* k, int inType, long long qStride, long long kStride,
+                                      const float* qWeight, const float* kWeight, float eps, const float* cosSin,
+                                      const int* positions, long long positionsStride, int numAxes, const int* axes,
+                                      int numPositions, int pairing, float* qOut, void* kOut, int kOutType, int N,
+                                      cudaStream_t stream) {
+  RowCall c = append_call(q, k, nullptr, inType, qStride, kStride, 0, qWeight, kWeight, eps, cosSin, positions,
+                          numPositions, pairing, qOut, kOut, nullptr, kOutType, nullptr, nullptr, nullptr, 0, N, 0, 0);
+  int rc = rows_ok(c);
+  if (rc == ATTN_OK) rc = with_axes(&c, positions, positionsStride, numAxes, axes);
+  if (rc != ATTN_OK || N == 0) return rc;
+  DeviceState* st = nullptr;
+  if ((rc = current_device(&st)) != ATTN_OK) return rc;
+  return from_cuda(launch_rows(c, st->err, stream));
+}
+
+extern "C" int attn_append_paged_axes(const void* q, const void* k, const void* v, int inType, long long qStride,
+                                      long long kStride, long long vStride, const float* qWeight, const float* kWeight,
+                                      float eps, const float* cosSin, const int* positions, long long positionsStride,
+                                      int numAxes, const int* axes, int numPositions, int pairing, float* qOut,
+                                      float* kPages, float* vPages, const int* blockTable, const int* contextLens,
+                                      const int* rowStart, int B, int N, int maxBlocks, int numPages,
+                                      cudaStream_t stream) {
+  RowCall c = append_call(q, k, v, inType, qStride, kStride, vStride, qWeight, kWeight, eps, cosSin, positions,
+                          numPositions, pairing, qOut, kPages, vPages, ATTN_F32, blockTable, contextLens, rowStart, B, N,
+                          maxBlocks, numPages);
+  const int rc = with_axes(&c, positions, positionsStride, numAxes, axes);
+  return rc != ATTN_OK ? rc : append_paged(c, stream);
+}
+
+extern "C" int attn_append_paged_axes_bf16kv(const void* q, const void* k, const void* v, int inType,
+                                             long long qStride, long long kStride, long long vStride,
+                                             const float* qWeight, const float* kWeight, float eps,
+                                             const float* cosSin, const int* positions, long long positionsStride,
+                                             int numAxes, const int* axes, int numPositions, int pairing, float* qOut,
+                                             uint16_t* kPages, uint16_t* vPages, const int* blockTable,
+                                             const int* contextLens, const int* rowStart, int B, int N, int maxBlocks,
+                                             int numPages, cudaStream_t stream) {
+  RowCall c = append_call(q, k, v, inType, qStride, kStride, vStride, qWeight, kWeight, eps, cosSin, positions,
+                          numPositions, pairing, qOut, kPages, vPages, ATTN_BF16, blockTable, contextLens, rowStart, B,
+                          N, maxBlocks, numPages);
+  const int rc = with_axes(&c, positions, positionsStride, numAxes, axes);
+  return rc != ATTN_OK ? rc : append_paged(c, stream);
+}
 
 extern "C" int attn_append_paged(const void* q, const void* k, const void* v, int inType, long long qStride,
                                  long long kStride, long long vStride, const float* qWeight, const float* kWeight,
@@ -627,6 +687,149 @@ extern "C" int attn_compact_paged_bf16kv(uint16_t* kPages, uint16_t* vPages, con
                                          int maxKeep, int maxRows, int maxBlocks, int numPages, cudaStream_t stream) {
   return compact_paged(kPages, vPages, ATTN_BF16, blockTable, contextLens, keep, keepCounts, B, maxKeep, maxRows,
                        maxBlocks, numPages, stream);
+}
+
+namespace attn {
+namespace {
+
+int decay_ok(float decay) { return decay >= 0.f && decay <= 1.f ? ATTN_OK : ATTN_EINVAL; }
+
+int decode_weigh_paged(const DecodeWeighCall& c, size_t workspaceBytes, cudaStream_t stream) {
+  int rc = decode_shape_ok(c.B, c.max_blocks, c.num_pages, c.max_context, 0);
+  if (rc == ATTN_OK) rc = decay_ok(c.decay);
+  if (rc != ATTN_OK || c.B == 0) return rc;
+  if (!c.q || !c.k_pages || !c.v_pages || !c.weights || !c.table || !c.ctx_lens || !c.out) return ATTN_EINVAL;
+  if (!aligned16(c.q) || !aligned16(c.k_pages) || !aligned16(c.v_pages) || !aligned16(c.weights) || !aligned16(c.out) ||
+      !aligned4(c.table) || !aligned4(c.ctx_lens) || !aligned4(c.weighed_lens))
+    return ATTN_EALIGN;
+  DeviceState* st = nullptr;
+  if ((rc = current_device(&st)) != ATTN_OK) return rc;
+  size_t need = 0;
+  if ((rc = decode_weigh_workspace_bytes(c.B, c.max_context, &need)) != ATTN_OK) return rc;
+  if (need > 0) {
+    if (!c.workspace || workspaceBytes < need) return ATTN_ESPACE;
+    if (!aligned16(c.workspace)) return ATTN_EALIGN;
+  }
+  return launch_decode_weigh(c, st->err, stream);
+}
+
+int weigh_shape_ok(int B, int N, int maxRows, int maxContext) {
+  if (B < 0 || N < 0 || maxRows < 1 || maxContext < 0) return ATTN_EINVAL;
+  if (B > 65535 || N > ATTN_MAX_TOKENS || maxRows > ATTN_WEIGH_ROWS || maxContext > ATTN_MAX_TOKENS) return ATTN_ERANGE;
+  return ATTN_OK;
+}
+
+int weigh_paged(const WeighCall& c, size_t workspaceBytes, cudaStream_t stream) {
+  int rc = batch_ok(c.B, c.N, c.max_blocks, c.num_pages);
+  if (rc == ATTN_OK) rc = weigh_shape_ok(c.B, c.N, c.max_rows, c.max_context);
+  if (rc == ATTN_OK && c.max_context > c.max_blocks * ATTN_PAGE) rc = ATTN_ERANGE;
+  if (rc == ATTN_OK) rc = decay_ok(c.decay);
+  if (rc != ATTN_OK || c.B == 0 || c.N == 0) return rc;
+  if (!c.q || !c.k_pages || !c.weights || !c.table || !c.ctx_lens || !c.row_start) return ATTN_EINVAL;
+  if (!aligned16(c.q) || !aligned16(c.k_pages) || !aligned16(c.weights) || !aligned4(c.table) || !aligned4(c.ctx_lens) ||
+      !aligned4(c.row_start) || !aligned4(c.weighed_lens))
+    return ATTN_EALIGN;
+  DeviceState* st = nullptr;
+  if ((rc = current_device(&st)) != ATTN_OK) return rc;
+  size_t need = 0;
+  if ((rc = weigh_workspace_bytes(c.B, c.N, c.max_rows, c.max_context, &need)) != ATTN_OK) return rc;
+  if (!c.workspace || workspaceBytes < need) return ATTN_ESPACE;
+  if (!aligned16(c.workspace)) return ATTN_EALIGN;
+  return launch_weigh(c, st->err, stream);
+}
+
+int evict_paged(const EvictCall& c, size_t workspaceBytes, cudaStream_t stream) {
+  int rc = batch_ok(c.B, 0, c.max_blocks, c.num_pages);
+  if (rc != ATTN_OK) return rc;
+  if (c.max_context < 0 || c.first < 0 || c.last < 0) return ATTN_EINVAL;
+  if (c.max_context > c.max_blocks * ATTN_PAGE || c.first > ATTN_MAX_TOKENS || c.last > ATTN_MAX_TOKENS) return ATTN_ERANGE;
+  if (c.B == 0 || c.max_context == 0) return ATTN_OK;
+  if (!c.k_pages || !c.v_pages || !c.weights || !c.table || !c.ctx_lens || !c.keep_lens) return ATTN_EINVAL;
+  if (!aligned16(c.k_pages) || !aligned16(c.v_pages) || !aligned16(c.weights) || !aligned4(c.table) ||
+      !aligned4(c.ctx_lens) || !aligned4(c.keep_lens))
+    return ATTN_EALIGN;
+  DeviceState* st = nullptr;
+  if ((rc = current_device(&st)) != ATTN_OK) return rc;
+  if (!c.workspace || workspaceBytes < evict_workspace_bytes(c.B, c.max_context)) return ATTN_ESPACE;
+  if (!aligned16(c.workspace)) return ATTN_EALIGN;
+  int sms = 0;
+  if ((rc = sm_count(&sms)) != ATTN_OK) return rc;
+  return from_cuda(launch_evict(c, sms, st->err, stream));
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" size_t attn_decode_weigh_workspace_bytes(int B, int maxContext) {
+  size_t bytes = 0;
+  if (B <= 0 || B > 65535 || maxContext < 0 || maxContext > ATTN_MAX_TOKENS) return 0;
+  return decode_weigh_workspace_bytes(B, maxContext, &bytes) == ATTN_OK ? bytes : 0;
+}
+
+extern "C" int attn_decode_weigh_paged(const float* q, const float* kPages, const float* vPages, float* weights,
+                                       const int* blockTable, const int* contextLens, const int* weighedLens,
+                                       float decay, float* out, int B, int maxBlocks, int numPages, int maxContext,
+                                       void* workspace, size_t workspaceBytes, cudaStream_t stream) {
+  return decode_weigh_paged(DecodeWeighCall{q, kPages, vPages, ATTN_F32, weights, blockTable, contextLens, weighedLens, out,
+                                            workspace, B, maxBlocks, numPages, maxContext, decay},
+                            workspaceBytes, stream);
+}
+
+extern "C" int attn_decode_weigh_paged_bf16kv(const float* q, const uint16_t* kPages, const uint16_t* vPages,
+                                              float* weights, const int* blockTable, const int* contextLens,
+                                              const int* weighedLens, float decay, float* out, int B, int maxBlocks,
+                                              int numPages, int maxContext, void* workspace, size_t workspaceBytes,
+                                              cudaStream_t stream) {
+  return decode_weigh_paged(DecodeWeighCall{q, kPages, vPages, ATTN_BF16, weights, blockTable, contextLens, weighedLens,
+                                            out, workspace, B, maxBlocks, numPages, maxContext, decay},
+                            workspaceBytes, stream);
+}
+
+extern "C" size_t attn_weigh_workspace_bytes(int B, int N, int maxRows, int maxContext) {
+  size_t bytes = 0;
+  if (B <= 0 || N <= 0 || weigh_shape_ok(B, N, maxRows, maxContext) != ATTN_OK) return 0;
+  return weigh_workspace_bytes(B, N, maxRows, maxContext, &bytes) == ATTN_OK ? bytes : 0;
+}
+
+extern "C" int attn_weigh_paged(const float* q, const float* kPages, float* weights, const int* blockTable,
+                                const int* contextLens, const int* rowStart, const int* weighedLens, float decay, int B,
+                                int N, int maxRows, int maxBlocks, int numPages, int maxContext, void* workspace,
+                                size_t workspaceBytes, cudaStream_t stream) {
+  return weigh_paged(WeighCall{q, kPages, ATTN_F32, weights, blockTable, contextLens, rowStart, weighedLens, workspace, B, N,
+                               maxRows, maxBlocks, numPages, maxContext, decay},
+                     workspaceBytes, stream);
+}
+
+extern "C" int attn_weigh_paged_bf16kv(const float* q, const uint16_t* kPages, float* weights, const int* blockTable,
+                                       const int* contextLens, const int* rowStart, const int* weighedLens, float decay,
+                                       int B, int N, int maxRows, int maxBlocks, int numPages, int maxContext,
+                                       void* workspace, size_t workspaceBytes, cudaStream_t stream) {
+  return weigh_paged(WeighCall{q, kPages, ATTN_BF16, weights, blockTable, contextLens, rowStart, weighedLens, workspace, B,
+                               N, maxRows, maxBlocks, numPages, maxContext, decay},
+                     workspaceBytes, stream);
+}
+
+extern "C" size_t attn_evict_workspace_bytes(int B, int maxContext) {
+  if (B <= 0 || B > 65535 || maxContext <= 0 || maxContext > ATTN_MAX_TOKENS) return 0;
+  return evict_workspace_bytes(B, maxContext);
+}
+
+extern "C" int attn_evict_paged(float* kPages, float* vPages, float* weights, const int* blockTable,
+                                const int* contextLens, const int* keepLens, int keepFirst, int keepLast, int B,
+                                int maxBlocks, int numPages, int maxContext, void* workspace, size_t workspaceBytes,
+                                cudaStream_t stream) {
+  return evict_paged(EvictCall{kPages, vPages, ATTN_F32, weights, blockTable, contextLens, keepLens, workspace, B,
+                               maxBlocks, numPages, maxContext, keepFirst, keepLast},
+                     workspaceBytes, stream);
+}
+
+extern "C" int attn_evict_paged_bf16kv(uint16_t* kPages, uint16_t* vPages, float* weights, const int* blockTable,
+                                       const int* contextLens, const int* keepLens, int keepFirst, int keepLast, int B,
+                                       int maxBlocks, int numPages, int maxContext, void* workspace,
+                                       size_t workspaceBytes, cudaStream_t stream) {
+  return evict_paged(EvictCall{kPages, vPages, ATTN_BF16, weights, blockTable, contextLens, keepLens, workspace, B,
+                               maxBlocks, numPages, maxContext, keepFirst, keepLast},
+                     workspaceBytes, stream);
 }
 
 extern "C" size_t attn_naive_workspace_bytes(int C, int P) {
@@ -717,7 +920,8 @@ extern "C" const char* attn_strerror(int code) {
     case ATTN_EALIGN: return "a tensor pointer is not 16-byte aligned";
     case ATTN_ERANGE:
       return "a size is out of range (C, N or P + C above ATTN_MAX_TOKENS, numPages above ATTN_MAX_TOKENS / 16, "
-             "B above 65535, maxContext above 16 * maxBlocks, maxRows above ATTN_TREE_ROWS, or maxKeep above maxRows)";
+             "B above 65535, maxContext above 16 * maxBlocks, maxRows above ATTN_TREE_ROWS or ATTN_WEIGH_ROWS, maxKeep "
+             "above maxRows, or more than ATTN_ROPE_AXES axes)";
     case ATTN_ELAUNCH: return "kernel launch failed";
     case ATTN_ETIMEOUT: return "a device-side bounded wait expired";
     case ATTN_EBOUNDS: return "a device-side bounds check failed";
@@ -725,7 +929,7 @@ extern "C" const char* attn_strerror(int code) {
     case ATTN_ETMA: return "a TMA tensor map could not be encoded";
     case ATTN_ECUDA: return "a CUDA runtime call failed";
     case ATTN_ESPACE:
-      return "the workspace is missing or smaller than attn_decode_workspace_bytes() or attn_tree_workspace_bytes()";
+      return "the workspace is missing or smaller than the call's attn_*_workspace_bytes()";
     case ATTN_ESCRATCH:
       return "the decode partials exceed the library's fixed scratch (ATTN_DECODE_SCRATCH_BYTES): "
              "use fewer splits or attn_decode_paged with a workspace";
@@ -734,5 +938,5 @@ extern "C" const char* attn_strerror(int code) {
 }
 
 extern "C" const char* attn_version(void) {
-  return "libattnprefill: tcgen05 split-TF32 prefill (contiguous and paged), tcgen05 bf16-K/V prefill, split-KV GQA decode, drafted-tree attention, norm/rotation/append rows, FFMA, score-matrix and reference kernels, sm_103a";
+  return "libattnprefill: tcgen05 split-TF32 prefill (contiguous and paged), tcgen05 bf16-K/V prefill, split-KV GQA decode, drafted-tree attention, norm/rotation/append rows, cache weights and eviction, FFMA, score-matrix and reference kernels, sm_103a";
 }

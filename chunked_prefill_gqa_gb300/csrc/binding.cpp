@@ -167,17 +167,82 @@ void rows(Call* c, Rows* r, PyObject* q, PyObject* k, PyObject* positions, PyObj
   if (PyErr_Occurred()) c->failed = true;
 }
 
+// A row's positions on several axes, and the axis of each frequency.
+struct Axes {
+  const int* positions = nullptr;
+  long long stride = 0;
+  int count = 0, of[ATTN_D / 2] = {};
+};
+
+void axes_of(Call* c, Axes* x, long long n, PyObject* positions, PyObject* axes) {
+  const at::Tensor* p = unpack(c, "positions", positions);
+  if (!p) return;
+  if (p->scalar_type() != kI32 || !p->is_cuda()) {
+    fail(c, "positions must be a %s CUDA tensor", name_of(kI32));
+    return;
+  }
+  if (c->dev < 0) c->dev = c10::cuda::current_device();
+  if (p->get_device() != c->dev) {
+    fail(c, "positions is on CUDA device %d, the current device is %d", (int)p->get_device(), c->dev);
+    return;
+  }
+  if (p->dim() != 2 || p->size(1) != n) {
+    fail(c, "positions must be [axes][%lld]", n);
+    return;
+  }
+  if (n > 1 && p->stride(1) != 1) {
+    fail(c, "positions: those of an axis must be packed");
+    return;
+  }
+  x->positions = (const int*)p->data_ptr();
+  x->count = extent(c, "positions", p->size(0));
+  x->stride = x->count > 1 ? p->stride(0) : 0;
+  PyObject* seq = PySequence_Fast(axes, "axes must be a sequence of 32 ints");
+  if (!seq) {
+    c->failed = true;
+    return;
+  }
+  if (PySequence_Fast_GET_SIZE(seq) != ATTN_D / 2) fail(c, "axes must hold %d axes", ATTN_D / 2);
+  for (int i = 0; i < ATTN_D / 2 && !c->failed; ++i) x->of[i] = integer(c, "axes", PySequence_Fast_GET_ITEM(seq, i));
+  Py_DECREF(seq);
+}
+
+// Any tensor of the call's device, as bytes; None: none.
+void* workspace_of(Call* c, PyObject* t, size_t* bytes) {
+  *bytes = 0;
+  if (t == Py_None) return nullptr;
+  const at::Tensor* w = unpack(c, "workspace", t);
+  if (!w) return nullptr;
+  long long any[8] = {kAny, kAny, kAny, kAny, kAny, kAny, kAny, kAny};
+  if (w->dim() > 8) return fail(c, "workspace has too many dimensions");
+  void* p = tensor(c, "workspace", t, w->scalar_type(), (int)w->dim(), any);
+  if (!c->failed) *bytes = w->nbytes();
+  return p;
+}
+
+float real(Call* c, PyObject* v) {
+  if (c->failed) return 0.f;
+  const double x = PyFloat_AsDouble(v);
+  if (PyErr_Occurred()) c->failed = true;
+  return (float)x;
+}
+
 // A paged batch: pages, table, lengths.
 struct Batch {
   void *k_pages, *v_pages, *table, *ctx;
+  float* weights;
   int B, max_blocks, num_pages;
 };
 
-void batch(Call* c, Batch* x, bool bf16, PyObject* k_pages, PyObject* v_pages, PyObject* table, PyObject* ctx) {
+// v_pages or weights nullptr: the call has none.
+void batch(Call* c, Batch* x, bool bf16, PyObject* k_pages, PyObject* v_pages, PyObject* table, PyObject* ctx,
+           PyObject* weights = nullptr) {
   long long pool[4] = {kAny, ATTN_PAGE, ATTN_HKV, ATTN_D}, len[1] = {kAny};
   const at::ScalarType dtype = bf16 ? kBF16 : kF32;
   x->k_pages = tensor(c, "kPages", k_pages, dtype, 4, pool);
-  x->v_pages = tensor(c, "vPages", v_pages, dtype, 4, pool);
+  x->v_pages = v_pages ? tensor(c, "vPages", v_pages, dtype, 4, pool) : nullptr;
+  long long by_page[3] = {pool[0], ATTN_HKV, ATTN_PAGE};
+  x->weights = weights ? (float*)tensor(c, "weights", weights, kF32, 3, by_page) : nullptr;
   x->ctx = tensor(c, "contextLens", ctx, kI32, 1, len);
   long long tab[2] = {len[0], kAny};
   x->table = tensor(c, "blockTable", table, kI32, 2, tab);
@@ -255,6 +320,142 @@ PyObject* append_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// q, k, positions, axes, cosSin, qOut, kOut, qWeight, kWeight, eps, pairing, stream
+PyObject* qk_norm_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("qk_norm_rope_axes", n, 12, [&]() -> PyObject* {
+    Call c;
+    Rows r;
+    rows(&c, &r, a[0], a[1], Py_None, a[4], a[5], a[7], a[8], a[9]);
+    Axes x;
+    axes_of(&c, &x, r.n, a[2], a[3]);
+    const at::Tensor* ko = unpack(&c, "kOut", a[6]);
+    if (!ko) return nullptr;
+    const bool bf16 = ko->scalar_type() == kBF16;
+    long long ks[3] = {r.n, ATTN_HKV, ATTN_D};
+    void* k_out = tensor(&c, "kOut", a[6], bf16 ? kBF16 : kF32, 3, ks);
+    const int pairing = integer(&c, "pairing", a[10]);
+    const cudaStream_t st = stream_of(&c, a[11]);
+    return call(c, [&] {
+      return attn_qk_norm_rope_axes(r.q, r.k, r.type, r.q_stride, r.k_stride, (const float*)r.q_weight,
+                                    (const float*)r.k_weight, r.eps, (const float*)r.cos_sin, x.positions, x.stride,
+                                    x.count, x.of, r.num_positions, pairing, (float*)r.q_out, k_out,
+                                    bf16 ? ATTN_BF16 : ATTN_F32, r.n, st);
+    });
+  });
+}
+
+// bf16 pages, k, v, kPages, vPages, blockTable, contextLens, rowStart, cosSin, positions, axes, kWeight, q, qOut,
+// qWeight, eps, pairing, stream
+PyObject* append_paged_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("append_paged_axes", n, 18, [&]() -> PyObject* {
+    Call c;
+    const bool bf16 = a[0] == Py_True;
+    Rows r;
+    rows(&c, &r, a[12], a[1], Py_None, a[8], a[13], a[14], a[11], a[15]);
+    long long vs[3] = {r.n, ATTN_HKV, ATTN_D}, v_stride = 0;
+    void* v = tensor(&c, "v", a[2], r.dtype, 3, vs, &v_stride);
+    Axes p;
+    axes_of(&c, &p, r.n, a[9], a[10]);
+    Batch x;
+    batch(&c, &x, bf16, a[3], a[4], a[5], a[6]);
+    long long st1[1] = {(long long)x.B + 1};
+    const int* starts = (const int*)tensor(&c, "rowStart", a[7], kI32, 1, st1);
+    const int pairing = integer(&c, "pairing", a[16]);
+    const cudaStream_t st = stream_of(&c, a[17]);
+    return call(c, [&] {
+      const auto go = [&](auto fn, auto* k_pages, auto* v_pages) {
+        return fn(r.q, r.k, v, r.type, r.q_stride, r.k_stride, v_stride, (const float*)r.q_weight,
+                  (const float*)r.k_weight, r.eps, (const float*)r.cos_sin, p.positions, p.stride, p.count, p.of,
+                  r.num_positions, pairing, (float*)r.q_out, k_pages, v_pages, (const int*)x.table, (const int*)x.ctx,
+                  starts, x.B, r.n, x.max_blocks, x.num_pages, st);
+      };
+      return bf16 ? go(attn_append_paged_axes_bf16kv, (uint16_t*)x.k_pages, (uint16_t*)x.v_pages)
+                  : go(attn_append_paged_axes, (float*)x.k_pages, (float*)x.v_pages);
+    });
+  });
+}
+
+// bf16 pages, q, kPages, vPages, weights, blockTable, contextLens, out, max_context, decay, weighedLens, workspace, stream
+PyObject* decode_weigh_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("decode_weigh_paged", n, 13, [&]() -> PyObject* {
+    Call c;
+    const bool bf16 = a[0] == Py_True;
+    Batch x;
+    batch(&c, &x, bf16, a[2], a[3], a[5], a[6], a[4]);
+    long long qs[3] = {x.B, ATTN_HQ, ATTN_D}, len[1] = {x.B};
+    const float* q = (const float*)tensor(&c, "q", a[1], kF32, 3, qs);
+    float* out = (float*)tensor(&c, "out", a[7], kF32, 3, qs);
+    const int max_context = integer(&c, "max_context", a[8]);
+    const float decay = real(&c, a[9]);
+    const int* weighed = (const int*)optional(&c, "weighedLens", a[10], kI32, 1, len);
+    size_t bytes = 0;
+    void* ws = workspace_of(&c, a[11], &bytes);
+    const cudaStream_t st = stream_of(&c, a[12]);
+    return call(c, [&] {
+      const auto go = [&](auto fn, auto* k_pages, auto* v_pages) {
+        return fn(q, k_pages, v_pages, x.weights, (const int*)x.table, (const int*)x.ctx, weighed, decay, out, x.B,
+                  x.max_blocks, x.num_pages, max_context, ws, bytes, st);
+      };
+      return bf16 ? go(attn_decode_weigh_paged_bf16kv, (const uint16_t*)x.k_pages, (const uint16_t*)x.v_pages)
+                  : go(attn_decode_weigh_paged, (const float*)x.k_pages, (const float*)x.v_pages);
+    });
+  });
+}
+
+// bf16 pages, q, kPages, weights, blockTable, contextLens, rowStart, max_rows, max_context, decay, weighedLens, workspace,
+// stream
+PyObject* weigh_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("weigh_paged", n, 13, [&]() -> PyObject* {
+    Call c;
+    const bool bf16 = a[0] == Py_True;
+    Batch x;
+    batch(&c, &x, bf16, a[2], nullptr, a[4], a[5], a[3]);
+    long long qs[3] = {kAny, ATTN_HQ, ATTN_D}, len[1] = {x.B}, st1[1] = {(long long)x.B + 1};
+    const float* q = (const float*)tensor(&c, "q", a[1], kF32, 3, qs);
+    const int rows_n = extent(&c, "q", qs[0]);
+    const int* starts = (const int*)tensor(&c, "rowStart", a[6], kI32, 1, st1);
+    const int max_rows = integer(&c, "max_rows", a[7]), max_context = integer(&c, "max_context", a[8]);
+    const float decay = real(&c, a[9]);
+    const int* weighed = (const int*)optional(&c, "weighedLens", a[10], kI32, 1, len);
+    size_t bytes = 0;
+    void* ws = workspace_of(&c, a[11], &bytes);
+    const cudaStream_t st = stream_of(&c, a[12]);
+    return call(c, [&] {
+      const auto go = [&](auto fn, auto* k_pages) {
+        return fn(q, k_pages, x.weights, (const int*)x.table, (const int*)x.ctx, starts, weighed, decay, x.B, rows_n,
+                  max_rows, x.max_blocks, x.num_pages, max_context, ws, bytes, st);
+      };
+      return bf16 ? go(attn_weigh_paged_bf16kv, (const uint16_t*)x.k_pages) : go(attn_weigh_paged, (const float*)x.k_pages);
+    });
+  });
+}
+
+// bf16 pages, kPages, vPages, weights, blockTable, contextLens, keepLens, max_context, keep_first, keep_last, workspace,
+// stream
+PyObject* evict_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return entry("evict_paged", n, 12, [&]() -> PyObject* {
+    Call c;
+    const bool bf16 = a[0] == Py_True;
+    Batch x;
+    batch(&c, &x, bf16, a[1], a[2], a[4], a[5], a[3]);
+    long long len[1] = {x.B};
+    const int* keep = (const int*)tensor(&c, "keepLens", a[6], kI32, 1, len);
+    const int max_context = integer(&c, "max_context", a[7]), first = integer(&c, "keep_first", a[8]),
+              last = integer(&c, "keep_last", a[9]);
+    size_t bytes = 0;
+    void* ws = workspace_of(&c, a[10], &bytes);
+    const cudaStream_t st = stream_of(&c, a[11]);
+    return call(c, [&] {
+      const auto go = [&](auto fn, auto* k_pages, auto* v_pages) {
+        return fn(k_pages, v_pages, x.weights, (const int*)x.table, (const int*)x.ctx, keep, first, last, x.B,
+                  x.max_blocks, x.num_pages, max_context, ws, bytes, st);
+      };
+      return bf16 ? go(attn_evict_paged_bf16kv, (uint16_t*)x.k_pages, (uint16_t*)x.v_pages)
+                  : go(attn_evict_paged, (float*)x.k_pages, (float*)x.v_pages);
+    });
+  });
+}
+
 // bf16 pages, q, kPages, vPages, blockTable, contextLens, rowStart, masks, out, max_rows, max_context, num_splits,
 // workspace, stream
 PyObject* tree_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -272,16 +473,8 @@ PyObject* tree_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long* masks = (const long long*)optional(&c, "masks", a[7], kI64, 1, ms);
     const int max_rows = integer(&c, "max_rows", a[9]), max_context = integer(&c, "max_context", a[10]),
               splits = integer(&c, "num_splits", a[11]);
-    void* ws = nullptr;
     size_t bytes = 0;
-    if (a[12] != Py_None) {  // any type and shape
-      const at::Tensor* w = unpack(&c, "workspace", a[12]);
-      if (!w) return nullptr;
-      long long any[8] = {kAny, kAny, kAny, kAny, kAny, kAny, kAny, kAny};
-      if (w->dim() > 8) fail(&c, "workspace has too many dimensions");
-      ws = tensor(&c, "workspace", a[12], w->scalar_type(), (int)w->dim(), any);
-      if (!c.failed) bytes = w->nbytes();
-    }
+    void* ws = workspace_of(&c, a[12], &bytes);
     const cudaStream_t st = stream_of(&c, a[13]);
     return call(c, [&] {
       const auto go = [&](auto fn, auto* k_pages, auto* v_pages) {
@@ -320,6 +513,11 @@ PyObject* compact_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyMethodDef methods[] = {
     {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, "attn_qk_norm_rope"},
     {"append_paged", (PyCFunction)(void (*)(void))append_paged, METH_FASTCALL, "attn_append_paged(_bf16kv)"},
+    {"qk_norm_rope_axes", (PyCFunction)(void (*)(void))qk_norm_rope_axes, METH_FASTCALL, "attn_qk_norm_rope_axes"},
+    {"append_paged_axes", (PyCFunction)(void (*)(void))append_paged_axes, METH_FASTCALL, "attn_append_paged_axes(_bf16kv)"},
+    {"decode_weigh_paged", (PyCFunction)(void (*)(void))decode_weigh_paged, METH_FASTCALL, "attn_decode_weigh_paged(_bf16kv)"},
+    {"weigh_paged", (PyCFunction)(void (*)(void))weigh_paged, METH_FASTCALL, "attn_weigh_paged(_bf16kv)"},
+    {"evict_paged", (PyCFunction)(void (*)(void))evict_paged, METH_FASTCALL, "attn_evict_paged(_bf16kv)"},
     {"tree_paged", (PyCFunction)(void (*)(void))tree_paged, METH_FASTCALL, "attn_tree_paged(_bf16kv)"},
     {"compact_paged", (PyCFunction)(void (*)(void))compact_paged, METH_FASTCALL, "attn_compact_paged(_bf16kv)"},
     {nullptr, nullptr, 0, nullptr}};

@@ -131,6 +131,11 @@ struct RowCall {
   void *k_out, *v_out;
   const int *table, *ctx_lens, *row_start;
   int B, N, max_blocks, num_pages;
+  // Several positions a row (num_axes > 0): axis x of row n at positions[x * pos_stride +
+  // n], and the axis of frequency i in bits 2 i and 2 i + 1.
+  int num_axes;
+  long long pos_stride;
+  unsigned long long axis_of;
 };
 cudaError_t launch_rows(const RowCall& c, unsigned* err, cudaStream_t stream);
 cudaError_t launch_rope_table(const double* inv_freq, float* table, int num_positions, cudaStream_t stream);
@@ -160,6 +165,48 @@ struct TreeCall {
 int tree_plan(bool bf16, int B, int N, int max_rows, int max_context, int splits_hint, size_t room, TreePlan* plan);
 size_t tree_workspace_bytes(int N, const TreePlan& plan);
 int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream);
+
+// A decode step that also adds what each cached token was given to its weight
+// (decode_weigh.cu): resident blocks of the device, workspace bytes, launch.
+struct DecodeWeighCall {
+  const float* q;
+  const void *k_pages, *v_pages;
+  int type;  // ATTN_F32 or ATTN_BF16 pages
+  float* weights;
+  const int *table, *ctx_lens, *weighed_lens;  // weighed_lens may be nullptr
+  float* out;
+  void* workspace;
+  int B, max_blocks, num_pages, max_context;
+  float decay;
+};
+int decode_weigh_workspace_bytes(int B, int max_context, size_t* bytes);
+int launch_decode_weigh(const DecodeWeighCall& c, unsigned* err, cudaStream_t stream);
+
+// The same weights from a window of rows, without their attention (weigh.cu).
+struct WeighCall {
+  const float* q;
+  const void* k_pages;
+  int type;
+  float* weights;
+  const int *table, *ctx_lens, *row_start, *weighed_lens;
+  void* workspace;
+  int B, N, max_rows, max_blocks, num_pages, max_context;
+  float decay;
+};
+int weigh_workspace_bytes(int B, int N, int max_rows, int max_context, size_t* bytes);
+int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream);
+
+// Tokens of least weight leave a cache (evict.cu).
+struct EvictCall {
+  void *k_pages, *v_pages;
+  int type;
+  float* weights;
+  const int *table, *ctx_lens, *keep_lens;
+  void* workspace;
+  int B, max_blocks, num_pages, max_context, first, last;
+};
+size_t evict_workspace_bytes(int B, int max_context);
+cudaError_t launch_evict(const EvictCall& c, int sms, unsigned* err, cudaStream_t stream);
 
 // Tensor-pipe rate measurement (peak.cu): `ctas` CTAs each issue `iters`
 // dense M = 128, N = n MMAs (kind::tf32, or kind::f16 with bf16 operands).

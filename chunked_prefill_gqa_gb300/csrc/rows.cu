@@ -125,6 +125,12 @@ struct RowArgs {
   const float* cos_sin;  // [num_positions][64], or nullptr: not rotated
   const int* positions;  // [N], or nullptr: consecutive after the sequence's context
   int num_positions, pairing;
+  // Several positions a row: axis x of row n at positions[x * pos_stride + n], and two
+  // bits of axis_of for each frequency. grouped: a lane's frequencies share an axis.
+  long long pos_stride;
+  unsigned long long axis_of;
+  int num_axes;
+  bool grouped;
   float* q_out;          // [N][32][64]
   void *k_out, *v_out;   // contiguous: k_out [N][8][64]; paged: the page pools
   const int *table, *ctx_lens, *row_start;  // paged
@@ -133,7 +139,41 @@ struct RowArgs {
   unsigned* err;
 };
 
-template <bool kInBf16, bool kOutBf16, bool kPaged>
+// This lane's cosines and sines where each frequency goes by one of several positions:
+// lane x holds the row's position on axis x, checked by axis_position(). Where a lane's
+// frequencies (four of a halves pairing, two of a neighbours one) share an axis they come
+// as one vector each; otherwise one by one, from table rows that L1 holds (2048 rows of
+// bf16, with queries: XXX us grouped, XXX one by one).
+__device__ __forceinline__ Angles axis_angles(const RowArgs& a, int position, int sub) {
+  const bool pairs = a.pairing == ATTN_ROPE_PAIRS;
+  const int f0 = pairs ? 2 * sub : (4 * sub) & 31;
+  float c[4] = {}, s[4] = {};
+  if (a.grouped) {
+    const int p = __shfl_sync(kFull, position, (int)(a.axis_of >> (2 * f0)) & 3);
+    const float* row = a.cos_sin + (size_t)p * kD + f0;
+    if (pairs) {
+      const float2 x = fetch(reinterpret_cast<const float2*>(row)), y = fetch(reinterpret_cast<const float2*>(row + kD / 2));
+      c[0] = x.x, c[1] = x.y, s[0] = y.x, s[1] = y.y;
+    } else {
+      const float4 x = fetch(reinterpret_cast<const float4*>(row)), y = fetch(reinterpret_cast<const float4*>(row + kD / 2));
+      c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w, s[0] = y.x, s[1] = y.y, s[2] = y.z, s[3] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int f = pairs ? f0 + (j & 1) : f0 + j;
+      const int p = __shfl_sync(kFull, position, (int)(a.axis_of >> (2 * f)) & 3);
+      if (j < 2 || !pairs) {
+        const float* row = a.cos_sin + (size_t)p * kD + f;
+        c[j] = fetch(row), s[j] = fetch(row + kD / 2);
+      }
+    }
+  }
+  const float sign = !pairs && sub < 8 ? -1.f : 1.f;
+  return Angles{make_float4(c[0], c[1], c[2], c[3]), make_float4(sign * s[0], sign * s[1], sign * s[2], sign * s[3])};
+}
+
+template <bool kInBf16, bool kOutBf16, bool kPaged, bool kAxes>
 __global__ void __launch_bounds__(32 * kRowWarps, kRowBlocks)
 rows_kernel(const RowArgs a) {
   follow();
@@ -155,7 +195,12 @@ rows_kernel(const RowArgs a) {
   for (int i = 0; i < kHeadsPerWarp / 2; ++i) raw[i] = load4(src + 2 * i * kD);
 
   // Then what the lookups need, as much of it at once as there is.
-  int position = a.positions ? fetch(a.positions + n) : 0;
+  int position = 0;
+  if constexpr (kAxes) {
+    if (lane < a.num_axes) position = fetch(a.positions + lane * a.pos_stride + n);
+  } else {
+    position = a.positions ? fetch(a.positions + n) : 0;
+  }
   int slot = n;  // row of the destination
   int page = 0;
   if (kPaged) {
@@ -170,7 +215,7 @@ rows_kernel(const RowArgs a) {
       page = fetch(a.table + (size_t)b * a.max_blocks + token / ATTN_PAGE);
       slot = (int)token % ATTN_PAGE;
     }
-    if (!a.positions) position = (int)min(max(token, -1ll), (long long)ATTN_MAX_TOKENS);
+    if (!kAxes && !a.positions) position = (int)min(max(token, -1ll), (long long)ATTN_MAX_TOKENS);
   }
 
   float4 x[kHeadsPerWarp / 2];
@@ -178,7 +223,13 @@ rows_kernel(const RowArgs a) {
     const float* weight = is_q ? a.q_weight : a.k_weight;
     const float4 w = weight ? fetch(reinterpret_cast<const float4*>(weight + d)) : make_float4(1.f, 1.f, 1.f, 1.f);
     Angles t{};
-    if (a.cos_sin) {
+    if constexpr (kAxes) {
+      if (position < 0 || position >= a.num_positions) {  // lanes without an axis hold 0
+        record_error(a.err, kDevErrBounds);
+        position = position < 0 ? 0 : a.num_positions - 1;
+      }
+      t = axis_angles(a, position, sub);
+    } else if (a.cos_sin) {
       if (position < 0 || position >= a.num_positions) {
         if (lane == 0) record_error(a.err, kDevErrBounds);
         position = position < 0 ? 0 : a.num_positions - 1;
@@ -197,7 +248,7 @@ rows_kernel(const RowArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < kHeadsPerWarp / 2; ++i)
-      x[i] = norm_rotate(widen(raw[i]), w, weight != nullptr, t, a.cos_sin != nullptr, a.pairing, a.eps);
+      x[i] = norm_rotate(widen(raw[i]), w, weight != nullptr, t, kAxes || a.cos_sin != nullptr, a.pairing, a.eps);
   } else {
 #pragma unroll
     for (int i = 0; i < kHeadsPerWarp / 2; ++i) x[i] = widen(raw[i]);
@@ -221,12 +272,13 @@ rows_kernel(const RowArgs a) {
   }
 }
 
-template <bool kPaged>
+template <bool kPaged, bool kAxes>
 cudaError_t launch_rows_as(const RowArgs& a, bool in_bf16, bool out_bf16, cudaStream_t stream) {
   const unsigned blocks = (unsigned)(((long long)a.N * a.chunks + kRowWarps - 1) / kRowWarps);
-  return launch_following(in_bf16 ? (out_bf16 ? rows_kernel<true, true, kPaged> : rows_kernel<true, false, kPaged>)
-                                  : (out_bf16 ? rows_kernel<false, true, kPaged> : rows_kernel<false, false, kPaged>),
-                          dim3(blocks), dim3(32 * kRowWarps), stream, a);
+  return launch_following(
+      in_bf16 ? (out_bf16 ? rows_kernel<true, true, kPaged, kAxes> : rows_kernel<true, false, kPaged, kAxes>)
+              : (out_bf16 ? rows_kernel<false, true, kPaged, kAxes> : rows_kernel<false, false, kPaged, kAxes>),
+      dim3(blocks), dim3(32 * kRowWarps), stream, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -330,8 +382,16 @@ cudaError_t launch_rows(const RowCall& c, unsigned* err, cudaStream_t stream) {
   a.q_chunks = c.q ? kQChunks : 0;
   a.chunks = a.q_chunks + (c.k ? 1 : 0) + (c.v ? 1 : 0);
   a.err = err;
-  return c.table ? launch_rows_as<true>(a, c.in_type == ATTN_BF16, c.out_type == ATTN_BF16, stream)
-                 : launch_rows_as<false>(a, c.in_type == ATTN_BF16, c.out_type == ATTN_BF16, stream);
+  const bool in = c.in_type == ATTN_BF16, out = c.out_type == ATTN_BF16;
+  if (c.num_axes == 0) return c.table ? launch_rows_as<true, false>(a, in, out, stream) : launch_rows_as<false, false>(a, in, out, stream);
+  a.num_axes = c.num_axes;
+  a.pos_stride = c.pos_stride;
+  a.axis_of = c.axis_of;
+  const int per_lane = c.pairing == ATTN_ROPE_PAIRS ? 2 : 4;
+  a.grouped = true;
+  for (int f = 1; f < kD / 2; ++f)
+    if (f % per_lane && ((c.axis_of >> (2 * f)) & 3) != ((c.axis_of >> (2 * f - 2)) & 3)) a.grouped = false;
+  return c.table ? launch_rows_as<true, true>(a, in, out, stream) : launch_rows_as<false, true>(a, in, out, stream);
 }
 
 cudaError_t launch_rope_table(const double* inv_freq, float* table, int num_positions, cudaStream_t stream) {

@@ -1,0 +1,549 @@
+// weigh.cu -- what a window of rows gives to every cached token, without the rows'
+// attention: the weights by which a prompt's cache is cut down.
+//   s_rhj = q_rh . k_j / 8,  p_rhj = softmax over the tokens j that row r sees,
+//   W[j][g] = (decay W[j][g], or 0 for a token without a weight yet) + sum of p_rhj over rows r
+//             and the 4 heads h of g; row i of a sequence sees its tokens j <= context + i
+//
+// p needs its row's sum over all keys first, and a window's scores (up to 8 KB a token) cost
+// more to keep than to compute again: two passes over K, one kernel with its operands
+// exchanged. A block has the 128 (row, head) pairs of 32 rows and a KV head, their terms in
+// shared memory, and streams tiles of 128 keys past them; both are K-major operands of 128
+// rows, so the tensor core takes either one on its M side:
+//   rows pass  S [rows][keys]: a thread owns a row, its maximum and sum never cross threads
+//   keys pass  S [keys][rows]: a thread owns a key and adds up its column of p's
+// The rows pass leaves (log2 maximum, sum) of every row and segment of keys; the keys pass
+// merges them, so that p = 2^(s - lse), with no maximum to watch. Windows of more than 32
+// rows: more blocks in the rows pass, one after another in the keys pass, whose threads add to
+// weights that they alone write.
+//   bf16 pages: S = K (q3, q2, q1), K as stored: 3 x 4 MMAs of 128 x 128 x 16 a tile
+//   fp32 pages: S = K q_lo + K_lo q + K q, tf32 terms: 3 x 8 MMAs of 128 x 128 x 8
+//
+// Roles: warps 0-3 and 4-7 take the tiles in turn; (fp32) 8-11 split K into its terms; one
+// warp for TMA (16-token pages through the block table), one to issue the products.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "common.cuh"
+#include "tc_ptx.cuh"
+#include "tensor_map.cuh"
+#include "tree.cuh"
+
+namespace attn {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 32;                  // rows of a block: 128 (row, head) pairs
+constexpr int kKeys = 128;                 // keys of a tile
+constexpr int kPages = kKeys / ATTN_PAGE;
+constexpr int kSoft = 8;                   // warps that read S, two groups of four
+constexpr uint32_t kHalf = 128 * 128;      // 128 rows of 128 bytes
+constexpr uint32_t kBox = ATTN_PAGE * 128;
+constexpr int kMaxSplits = 64;
+constexpr unsigned kFull = 0xffffffffu;
+
+struct WeighArgs {
+  const float* q;          // [N][32][64]
+  float* weights;          // [num_pages][8][16]
+  const int *table, *ctx_lens, *row_start, *weighed_lens;
+  float2* stats;           // [N][32][splits]: log2 maximum, sum (both 0 of a segment without keys)
+  int B, N, max_rows, max_blocks, num_pages, max_context;
+  int splits;              // of the rows pass
+  int key_splits;          // of the keys pass
+  float decay;
+  unsigned* err;
+  unsigned long long timeout_ns;
+};
+
+template <bool kF32>
+struct Lay {
+  static constexpr int kConvWarp = kSoft, kConvWarps = kF32 ? 4 : 0;
+  static constexpr int kTmaWarp = kSoft + kConvWarps, kMmaWarp = kTmaWarp + 1;
+  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr uint32_t kOperand = kF32 ? 2 * kHalf : kHalf;      // a tile of K, or a term of q
+  static constexpr uint32_t kStageBytes = (kF32 ? 2 : 1) * kOperand;  // K (, K lo)
+  static constexpr int kStages = kF32 ? 2 : 8;
+  static constexpr int kTerms = kF32 ? 2 : 3;
+  static constexpr uint32_t kSmemQ = kStages * kStageBytes;
+  static constexpr uint32_t kSmemLse = kSmemQ + kTerms * kOperand;    // [128] floats; at the end of the rows pass [128] float2
+  static constexpr uint32_t kSmemBar = kSmemLse + 128 * 8;
+  static constexpr int kBufs = 4;                                     // of S, two a group
+  static constexpr int kNumBars = 3 * kStages + 2 * kBufs + 2;
+  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;     // TMEM address, abort flag, copies issued
+  static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
+  static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
+};
+
+// The lengths of a sequence, checked as those of drafted rows are.
+__device__ __forceinline__ Seq load_window(const WeighArgs& a, int b) {
+  TreeArgs t;
+  t.ctx_lens = a.ctx_lens;
+  t.row_start = a.row_start;
+  t.max_blocks = a.max_blocks;
+  t.max_context = a.max_context;
+  t.N = a.N;
+  t.max_rows = a.max_rows;
+  return load_seq(t, b);
+}
+
+template <bool kF32, bool kByKey>
+__global__ void __launch_bounds__(Lay<kF32>::kThreads, 1)
+weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
+  using L = Lay<kF32>;
+  constexpr int kStages = L::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);
+  if (warp == L::kTmaWarp && lane == 0) tma_prefetch_desc(&mk);
+  follow();
+  const int s = blockIdx.x, head = blockIdx.y % kHKV, b = blockIdx.z;
+  const Seq seq = load_window(a, b);
+  if (!seq.ok && s == 0 && !kByKey && blockIdx.y == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+  // The rows of this block: a tile of 32 of them, or by key all tiles one after another.
+  const int rt0 = kByKey ? 0 : blockIdx.y / kHKV, rt1 = kByKey ? (seq.rows + kRows - 1) / kRows : rt0 + 1;
+  if (seq.rows - rt0 * kRows <= 0) return;
+  // The sequence's own keys, cut evenly into segments of whole tiles.
+  const int splits = kByKey ? a.key_splits : a.splits;
+  const int len = ((seq.keys + splits - 1) / splits + kKeys - 1) / kKeys * kKeys;
+  const int k0 = min((long long)s * len, (long long)seq.keys), k1 = min((long long)k0 + len, (long long)seq.keys);
+  // Keys that some row of row tile rt sees, and the tiles that hold them.
+  const auto visible = [&](int rt) { return min(k1, seq.ctx + min(seq.rows, (rt + 1) * kRows)); };
+  const auto tiles = [&](int rt) { return max(0, (visible(rt) - k0 + kKeys - 1) / kKeys); };
+  if (kByKey && k0 >= k1) return;
+
+  uint64_t* const kfull = reinterpret_cast<uint64_t*>(smem + L::kSmemBar);  // [stage] K landed
+  uint64_t* const kready = kfull + kStages;                                 // [stage] K's terms written (fp32)
+  uint64_t* const kempty = kready + kStages;                                // [stage] products done with K
+  uint64_t* const sfull = kempty + kStages;                                 // [buffer] S written
+  uint64_t* const sfree = sfull + L::kBufs;                                 // [buffer] S read
+  uint64_t* const qready = sfree + L::kBufs;                                // q's terms of a row tile written
+  uint64_t* const drain = qready + 1;
+  uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
+  volatile uint32_t* const issued = words + 2;
+  float* const lse = reinterpret_cast<float*>(smem + L::kSmemLse);
+  const Wait wait{a.err, a.timeout_ns, abort_flag};
+  const int* const trow = a.table + (size_t)b * a.max_blocks;
+
+  if (warp == L::kTmaWarp) {
+    for (int i = lane; i < L::kNumBars; i += 32) {
+      const bool by_conv = &kfull[i] >= kready && &kfull[i] < kempty;
+      const bool by_soft = &kfull[i] >= sfree && &kfull[i] < qready;
+      mbar_init(&kfull[i], by_conv && kF32 ? L::kConvWarps : by_soft ? 4 : &kfull[i] == qready ? kSoft : 1);
+    }
+    fence_mbar_init();
+    if (lane == 0) {
+      *abort_flag = 0;
+      *issued = 0;
+    }
+  } else if (warp == L::kMmaWarp) {
+    tmem_alloc(words, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = words[0];
+
+  if (warp == L::kTmaWarp) {
+    int it = 0;
+    bool ok = true;
+    for (int rt = rt0; ok && rt < rt1; ++rt) {
+      const int end = visible(rt), count = tiles(rt);
+      // Lane l holds the table's entry of page l of a group of four tiles.
+      const auto entry_at = [&](int g) -> int {
+        const int t = k0 + g * 4 * kKeys + lane * ATTN_PAGE;
+        return t < end ? fetch(trow + t / ATTN_PAGE) : -1;
+      };
+      int entries = entry_at(0), entries_next = entry_at(1);
+      for (int n = 0; n < count; ++n, ++it) {
+        const int st = it % kStages;
+        if (it >= kStages && !(ok = wait.warp(&kempty[st], (it / kStages - 1) & 1))) break;
+        const int p = lane & (kPages - 1), half = lane / kPages;
+        int page = __shfl_sync(kFull, entries, (n & 3) * kPages + p);
+        const int pages = min(kPages, (end - k0 - n * kKeys + ATTN_PAGE - 1) / ATTN_PAGE);
+        const bool has = half < (kF32 ? 2 : 1) && p < pages;
+        if (has && (page < 0 || page >= a.num_pages)) {
+          record_error(a.err, kDevErrBounds);
+          page = a.num_pages;  // past the pool's end: reads as zeros
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&kfull[st], pages * (kF32 ? 2 : 1) * kBox);
+          *issued = it + 1;
+        }
+        __syncwarp();
+        if (has)
+          tma_load_2d(smem + st * L::kStageBytes + half * kHalf + p * kBox, &mk, &kfull[st], head * kD + half * 32,
+                      page * ATTN_PAGE);
+        if ((n & 3) == 3) {
+          entries = entries_next;
+          entries_next = entry_at((n >> 2) + 2);
+        }
+      }
+    }
+  } else if (warp == L::kMmaWarp) {
+    const uint32_t base = smem_u32(smem);
+    int it = 0, used[2] = {0, 0};  // tiles in all, and each group's
+    bool ok = true;
+    for (int rt = rt0; ok && rt < rt1; ++rt) {
+      const int count = tiles(rt);
+      ok = wait.warp(qready, (rt - rt0) & 1);
+      for (int n = 0; ok && n < count; ++n, ++it) {
+        const int st = it % kStages, g = n & 1, k = used[g], buf = 2 * g + (k & 1);
+        ++used[g];
+        if (!(ok = wait.warp(kF32 ? &kready[st] : &kfull[st], (it / kStages) & 1) &&
+                   (k < 2 || wait.warp(&sfree[buf], ((k >> 1) - 1) & 1))))
+          break;
+        tc_fence_after();
+        const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes), qd = sdesc_sw128(base + L::kSmemQ);
+        const uint32_t d = tmem + buf * kKeys;
+        if (elect()) {
+          const auto product = [&](uint64_t kt, uint64_t qt, bool first) {
+            if constexpr (kF32) {
+              constexpr uint32_t id = idesc_tf32(128, 128);
+#pragma unroll
+              for (int x = 0; x < 8; ++x) {
+                const uint64_t at = (x >> 2) * (kHalf >> 4) + (x & 3) * 2;
+                mma_tf32_ss(d, (kByKey ? kt : qt) + at, (kByKey ? qt : kt) + at, id, !first || x > 0);
+              }
+            } else {
+              constexpr uint32_t id = idesc_bf16(128, 128, false);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                mma_f16_ss(d, (kByKey ? kt : qt) + x * 2, (kByKey ? qt : kt) + x * 2, id, !first || x > 0);
+            }
+          };
+          constexpr uint64_t next = L::kOperand >> 4;
+          if constexpr (kF32) {
+            product(kd, qd + next, true);
+            product(kd + next, qd, false);
+            product(kd, qd, false);
+          } else {
+            product(kd, qd + 2 * next, true);
+            product(kd, qd + next, false);
+            product(kd, qd, false);
+          }
+          mma_commit(&sfull[buf]);
+          mma_commit(&kempty[st]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (kF32 && warp >= L::kConvWarp && warp < L::kTmaWarp) {
+    // hi(x), rounded to nearest, in place and lo = x - hi(x) at the same offset of the next region.
+    const int ctid = tid - 32 * L::kConvWarp;
+    int total = 0;
+    for (int rt = rt0; rt < rt1; ++rt) total += tiles(rt);
+    for (int it = 0; it < total; ++it) {
+      const int st = it % kStages;
+      uint8_t* const stage = smem + st * L::kStageBytes;
+      if (!wait.warp(&kfull[st], (it / kStages) & 1)) break;
+#pragma unroll 2
+      for (int h = 0; h < 4; ++h) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(stage + (ctid + (4 * h + i) * 128) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint8_t* const at = stage + (ctid + (4 * h + i) * 128) * 16;
+          const float4 y = make_float4(tf32_near(x[i].x), tf32_near(x[i].y), tf32_near(x[i].z), tf32_near(x[i].w));
+          *reinterpret_cast<float4*>(at) = y;
+          *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x[i].x - y.x, x[i].y - y.y, x[i].z - y.z, x[i].w - y.w);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&kready[st]);
+    }
+  } else if (warp < kSoft) {
+    constexpr int kMeet = 32 * kSoft;
+    const int quarter = warp & 3, g = warp >> 2, row = quarter * 32 + lane;  // lane of tensor memory
+    const uint32_t lane_tmem = tmem + ((uint32_t)(quarter * 32) << 16);
+    bool failed = false;
+    float ref = kUnseen, l0 = 0.f, l1 = 0.f;
+    const int weighed = kByKey ? (a.weighed_lens ? fetch(a.weighed_lens + b) : seq.ctx) : 0;
+    int k = 0;  // the group's k-th tile
+    for (int rt = rt0; rt < rt1; ++rt) {
+      const int i0 = rt * kRows, nrows = min(kRows, seq.rows - i0);
+      if (rt > rt0) {  // q and lse of the tile before are still in use
+        int over;
+        if (meet(kMeet, false, failed, lane, &over)) break;
+      }
+      {  // q in its terms: thread (row, half g) 32 dims of (row tile's row, head); rows past the last are zeros
+        const float* const src = a.q + ((size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3)) * kD + g * 32;
+        uint8_t* const dst = smem + L::kSmemQ;
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          float x[8];
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if ((row >> 2) < nrows) v = fetch(reinterpret_cast<const float4*>(src + i + j));
+            x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+          }
+          if constexpr (kF32) {
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              uint8_t* const at = dst + g * kHalf + sw128((uint32_t)row * 128u + (i + j) * 4u);
+              const float4 h = make_float4(tf32_near(x[j]), tf32_near(x[j + 1]), tf32_near(x[j + 2]), tf32_near(x[j + 3]));
+              *reinterpret_cast<float4*>(at) = h;
+              *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x[j] - h.x, x[j + 1] - h.y, x[j + 2] - h.z, x[j + 3] - h.w);
+            }
+          } else {
+            uint32_t w[3][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split3_cut(x[2 * j], x[2 * j + 1], w[0][j], w[1][j], w[2][j]);
+            uint8_t* const at = dst + sw128((uint32_t)row * 128u + (g * 32 + i) * 2u);
+#pragma unroll
+            for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(at + t * L::kOperand) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+          }
+        }
+        fence_proxy_async_smem();
+        if (kByKey && g == 0) {  // the row's log2 of its sum over all keys, from the segments
+          float top = kUnseen, sum = 0.f;
+          if ((row >> 2) < nrows) {
+            const float2* const st = a.stats + ((size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3)) * a.splits;
+            for (int x = 0; x < a.splits; ++x) top = fmaxf(top, fetch(st + x).x);
+            for (int x = 0; x < a.splits; ++x) {
+              const float2 p = fetch(st + x);
+              sum = fmaf(ex2(p.x - top), p.y, sum);
+            }
+          }
+          // a row whose scores are all -inf, or no row: gives nothing
+          lse[row] = sum == 0.f ? INFINITY : top + log2f(sum);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(qready);
+        if (kByKey) {  // lse of all rows is written
+          int over;
+          if (meet(kMeet, false, failed, lane, &over)) break;
+        }
+      }
+      const int count = tiles(rt);
+      for (int n = g; n < count; n += 2, ++k) {
+        const int buf = 2 * g + (k & 1), t0 = k0 + n * kKeys;
+        const uint32_t s_tmem = lane_tmem + buf * kKeys;
+        if constexpr (kByKey) {
+          const int t = t0 + row, end = visible(rt);
+          // The key's weight so far, on its way while the products run. Row tile (t - context) /
+          // 32 is the first that sees a token of the rows themselves, 0 any other.
+          float* w = nullptr;
+          float old = 0.f;
+          if (t < end) {
+            const int page = fetch(trow + t / ATTN_PAGE);
+            if (page >= 0 && page < a.num_pages) {
+              w = a.weights + ((size_t)page * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;
+              if (rt > max(0, t - seq.ctx) / kRows) old = *w;
+              else if (a.decay != 0.f && t < weighed) old = a.decay * *w;
+            }
+          }
+          failed |= !wait.warp(&sfull[buf], (k >> 1) & 1);
+          tc_fence_after();
+          float sum0 = 0.f, sum1 = 0.f;
+          const int late = t - seq.ctx - i0;  // rows before it do not see the key
+#pragma unroll
+          for (int h = 0; h < 128; h += 32) {
+            float x[32];
+            tmem_ld32(s_tmem + h, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 e = *reinterpret_cast<const float4*>(lse + h + i);
+              fma2(x[i], x[i + 1], x[i], x[i + 1], kTreeC, kTreeC, -e.x, -e.y);
+              fma2(x[i + 2], x[i + 3], x[i + 2], x[i + 3], kTreeC, kTreeC, -e.z, -e.w);
+            }
+            if (t0 + kKeys > seq.ctx + i0) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((h + i) / 4 < late) x[i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) add2(sum0, sum1, sum0, sum1, ex2(x[i]), ex2(x[i + 1]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sfree[buf]);
+          if (w && !failed) *w = old + (sum0 + sum1);
+        } else {
+          failed |= !wait.warp(&sfull[buf], (k >> 1) & 1);
+          tc_fence_after();
+          const int sees = seq.ctx + i0 + (row >> 2) + 1 - t0;  // keys of the tile that the row sees
+          const int limit = min(sees, k1 - t0);
+#pragma unroll
+          for (int h = 0; h < 128; h += 64) {
+            float x[64];
+            tmem_ld32(s_tmem + h, *reinterpret_cast<float(*)[32]>(&x[0]));
+            tmem_ld32(s_tmem + h + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
+            tmem_wait_ld();
+            if (h == 64) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sfree[buf]);
+            }
+            if (t0 + kKeys > min(seq.ctx + i0, k1)) {
+#pragma unroll
+              for (int i = 0; i < 64; ++i)
+                if (h + i >= limit) x[i] = -INFINITY;
+            }
+            float top[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              top[c] = fmaxf(x[c], x[c + 4]);
+#pragma unroll
+              for (int i = 8; i < 64; i += 8) top[c] = max3(top[c], x[i + c], x[i + c + 4]);
+            }
+            const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * kTreeC;
+            if (most > ref + kTreeStale) {
+              const float alpha = ex2(ref - most);
+              ref = most;
+              l0 *= alpha;
+              l1 *= alpha;
+            }
+            const float neg = -ref;
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+              fma2(x[i], x[i + 1], x[i], x[i + 1], kTreeC, kTreeC, neg, neg);
+              add2(l0, l1, l0, l1, ex2(x[i]), ex2(x[i + 1]));
+            }
+          }
+        }
+      }
+    }
+    if constexpr (!kByKey) {
+      float2* const other = reinterpret_cast<float2*>(smem + L::kSmemLse);
+      if (g == 1) other[row] = make_float2(ref, l0 + l1);
+      int over;
+      const bool lost = meet(kMeet, false, failed, lane, &over);
+      const int i = rt0 * kRows + (row >> 2);
+      if (g == 0 && i < seq.rows) {
+        const float2 o = other[row];
+        const float top = fmaxf(ref, o.x);
+        const float sum = fmaf(ex2(ref - top), l0 + l1, ex2(o.x - top) * o.y);
+        a.stats[((size_t)(seq.first + i) * kHQ + head * kGroup + (row & 3)) * a.splits + s] =
+            lost ? make_float2(kUnseen, 0.f) : make_float2(top, sum);
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (*abort_flag) {
+    if (warp == L::kTmaWarp) drain_copies(kfull, kStages, *issued, a.timeout_ns);
+    else if (warp == L::kMmaWarp) drain_products(drain, a.timeout_ns);
+    __syncthreads();
+  }
+  if (warp == L::kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+struct Device {
+  bool ready = false;
+  int sms = 0;
+};
+template <bool kF32, bool kByKey>
+bool set_up() {
+  return cudaFuncSetAttribute(weigh_kernel<kF32, kByKey>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)Lay<kF32>::kSmemAlloc) == cudaSuccess;
+}
+int device(Device** out) {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static Device devs[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return ATTN_ECUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  Device& d = devs[dev];
+  if (!d.ready) {
+    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !set_up<false, false>() ||
+        !set_up<false, true>() || !set_up<true, false>() || !set_up<true, true>()) {
+      (void)cudaGetLastError();
+      return ATTN_ECUDA;
+    }
+    d.ready = true;
+  }
+  *out = &d;
+  return ATTN_OK;
+}
+
+// Segments of the keys for `units` blocks each: the number whose rounds of one block an SM
+// take the least time, a block costing its tiles (each of them `passes` times) and as long
+// as four tiles besides.
+int plan(long long units, int max_keys, int passes, int sms) {
+  const int tiles = (max_keys + kKeys - 1) / kKeys;
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
+    const long long rounds = (units * s + sms - 1) / sms;
+    const double time = (double)rounds * ((double)((tiles + s - 1) / s) * passes + 4.0 * passes);
+    if (time < least * 0.999) least = time, best = s;
+  }
+  return best;
+}
+
+int max_keys(int max_context, int max_rows) {
+  return max_context > ATTN_MAX_TOKENS - max_rows ? ATTN_MAX_TOKENS : max_context + max_rows;
+}
+
+}  // namespace
+
+int weigh_workspace_bytes(int B, int N, int max_rows, int max_context, size_t* bytes) {
+  Device* d = nullptr;
+  const int rc = device(&d);
+  if (rc != ATTN_OK) return rc;
+  const int tiles = (max_rows + kRows - 1) / kRows;
+  *bytes = (size_t)N * kHQ * plan((long long)B * kHKV * tiles, max_keys(max_context, max_rows), 1, d->sms) * sizeof(float2);
+  return ATTN_OK;
+}
+
+int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
+  Device* d = nullptr;
+  int rc = device(&d);
+  if (rc != ATTN_OK) return rc;
+  const bool bf16 = c.type == ATTN_BF16;
+  alignas(64) CUtensorMap mk;
+  if ((rc = encode_rows_map(c.k_pages, bf16, (long long)c.num_pages * ATTN_PAGE, ATTN_PAGE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            &mk)) != ATTN_OK)
+    return rc;
+  const int tiles = (c.max_rows + kRows - 1) / kRows;
+  const int keys = max_keys(c.max_context, c.max_rows);
+  WeighArgs a{};
+  a.q = c.q;
+  a.weights = c.weights;
+  a.table = c.table;
+  a.ctx_lens = c.ctx_lens;
+  a.row_start = c.row_start;
+  a.weighed_lens = c.weighed_lens;
+  a.stats = static_cast<float2*>(c.workspace);
+  a.B = c.B;
+  a.N = c.N;
+  a.max_rows = c.max_rows;
+  a.max_blocks = c.max_blocks;
+  a.num_pages = c.num_pages;
+  a.max_context = c.max_context;
+  a.splits = plan((long long)c.B * kHKV * tiles, keys, 1, d->sms);
+  a.key_splits = plan((long long)c.B * kHKV, keys, tiles, d->sms);
+  a.decay = c.decay;
+  a.err = err;
+  a.timeout_ns = kTimeoutNs;
+  for (int pass = 0; pass < 2; ++pass) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = pass ? dim3(a.key_splits, kHKV, c.B) : dim3(a.splits, kHKV * tiles, c.B);
+    cfg.blockDim = dim3(bf16 ? Lay<false>::kThreads : Lay<true>::kThreads);
+    cfg.dynamicSmemBytes = bf16 ? Lay<false>::kSmemAlloc : Lay<true>::kSmemAlloc;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const auto kernel = bf16 ? (pass ? weigh_kernel<false, true> : weigh_kernel<false, false>)
+                             : (pass ? weigh_kernel<true, true> : weigh_kernel<true, false>);
+    if (launched(cudaLaunchKernelEx(&cfg, kernel, mk, a)) != cudaSuccess) return ATTN_ELAUNCH;
+  }
+  return ATTN_OK;
+}
+
+}  // namespace attn

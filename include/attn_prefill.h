@@ -64,6 +64,8 @@ extern "C" {
 #define ATTN_MAX_TOKENS (1 << 24)
 #define ATTN_PAGE 16        /* tokens per page of a paged K/V cache */
 #define ATTN_TREE_ROWS 64   /* drafted rows of one sequence: bits of a row's mask */
+#define ATTN_ROPE_AXES 4    /* positions of one row: time, height, width and one more */
+#define ATTN_WEIGH_ROWS 65536  /* rows of one sequence in a weighing window */
 
 /* Element types of the calls that take more than one. */
 #define ATTN_F32 0
@@ -405,6 +407,47 @@ int attn_append_paged_bf16kv(const void *q, const void *k, const void *v, int in
                              cudaStream_t stream);
 
 /*
+ * attn_qk_norm_rope_axes, attn_append_paged_axes, attn_append_paged_axes_bf16kv --
+ * attn_qk_norm_rope and the appends for rows whose position has several axes, as
+ * those of an image or a video have (time, height, width): frequency i of a row is
+ * turned by its position on axis axes[i],
+ *   angle_i = positions[axes[i] * positionsStride + n] * invFreq[i],
+ * cos and sin from column i (and 32 + i) of that position's row of cosSin, so one
+ * table serves all axes, sections of frequencies and interleaved ones alike, and
+ * axes with frequencies of their own too (column i belongs to its axis alone). A
+ * row of text has the same position on every axis and comes out as by the calls
+ * above.
+ *   positions        int32, numAxes arrays of N, positionsStride elements from one
+ *                    to the next (0: all axes share one array). Each outside [0,
+ *                    numPositions) is recorded as ATTN_EBOUNDS and clamped
+ *   axes             HOST array of 32 ints in [0, numAxes), read before the call
+ *                    returns
+ * cosSin, positions and axes are required (there is no default position: a row's
+ * slot says nothing about its place in an image). numAxes from 1 to 4
+ * (ATTN_ROPE_AXES). Everything else as attn_qk_norm_rope and attn_append_paged.
+ * Errors: theirs, ATTN_EINVAL (cosSin, positions or axes NULL, an axis out of range,
+ * numAxes < 1, a negative positionsStride), ATTN_ERANGE (numAxes above 4).
+ */
+int attn_qk_norm_rope_axes(const void *q, const void *k, int inType, long long qStride, long long kStride,
+                           const float *qWeight, const float *kWeight, float eps, const float *cosSin,
+                           const int *positions, long long positionsStride, int numAxes, const int *axes,
+                           int numPositions, int pairing, float *qOut, void *kOut, int kOutType, int N,
+                           cudaStream_t stream);
+int attn_append_paged_axes(const void *q, const void *k, const void *v, int inType, long long qStride,
+                           long long kStride, long long vStride, const float *qWeight, const float *kWeight, float eps,
+                           const float *cosSin, const int *positions, long long positionsStride, int numAxes,
+                           const int *axes, int numPositions, int pairing, float *qOut, float *kPages, float *vPages,
+                           const int *blockTable, const int *contextLens, const int *rowStart, int B, int N,
+                           int maxBlocks, int numPages, cudaStream_t stream);
+int attn_append_paged_axes_bf16kv(const void *q, const void *k, const void *v, int inType, long long qStride,
+                                  long long kStride, long long vStride, const float *qWeight, const float *kWeight,
+                                  float eps, const float *cosSin, const int *positions, long long positionsStride,
+                                  int numAxes, const int *axes, int numPositions, int pairing, float *qOut,
+                                  uint16_t *kPages, uint16_t *vPages, const int *blockTable, const int *contextLens,
+                                  const int *rowStart, int B, int N, int maxBlocks, int numPages,
+                                  cudaStream_t stream);
+
+/*
  * attn_tree_paged, attn_tree_paged_bf16kv -- attention of up to 64 drafted rows
  * per sequence over its paged cache, the rows' own keys and values already in
  * it (attn_append_paged). Row i of sequence b sees the contextLens[b] tokens
@@ -488,6 +531,139 @@ int attn_compact_paged(float *kPages, float *vPages, const int *blockTable, cons
 int attn_compact_paged_bf16kv(uint16_t *kPages, uint16_t *vPages, const int *blockTable, const int *contextLens,
                               const int *keep, const int *keepCounts, int B, int maxKeep, int maxRows,
                               int maxBlocks, int numPages, cudaStream_t stream);
+
+/*
+ * Weights of cached tokens, and eviction by them. A pool beside the pages,
+ *   weights  [numPages][8][16] fp32: at [p][g][s] the weight of slot s of page p for
+ *            key/value head g,
+ * holds of every cached token and head the sum, over the rows that attended to it
+ * and the head's four query heads, of the probabilities that it was given. The calls
+ * below add to it, in a decode step (attn_decode_weigh_paged) or from a window of
+ * rows, a prompt's last ones for instance (attn_weigh_paged); attn_evict_paged takes
+ * the tokens of least weight out, each head its own. A cache kept within bounds is:
+ *   attn_append_paged, attn_prefill_paged, ...           as ever
+ *   attn_weigh_paged        after a prompt (window: its last rows; weighedLens: 0)
+ *   attn_decode_weigh_paged in every decode step
+ *   attn_evict_paged        when a sequence has grown past its bound; its context is
+ *                           then min(contextLens[b], keepLens[b])
+ * After an eviction a token's slot no longer says its position: appends take
+ * `positions` (or are the *_axes ones). All of it is enqueued on `stream`, allocates
+ * nothing and may be captured into a graph; calls that may overlap need a workspace
+ * each (and must not share sequences).
+ *
+ * weighedLens, int32 [B] or NULL, is how many of a sequence's tokens have a weight
+ * already: the weights of tokens from there on are set, not added to, and what was
+ * there before is not read, so the pool needs no clearing, whoever had its pages
+ * before. decay, from 0 to 1, multiplies the old weights first; with 0 none is read.
+ *
+ * attn_decode_weigh_paged, attn_decode_weigh_paged_bf16kv -- attn_decode_paged (q,
+ * pages, table, contextLens with the new token counted, out) on fp32 or bf16 pages,
+ * which adds its probabilities to the weights:
+ *   out[b][h][:] = sum_j p_hj v_j[h/4][:],  p_hj = softmax_j(q[b][h] . k_j[h/4] / 8)
+ *   W_b[j][g]    = decay W_b[j][g] + sum_{h in 4 g .. 4 g + 3} p_hj,  j < contextLens[b]
+ * weighedLens NULL: contextLens[b] - 1, all tokens but the new one. q and p keep fp32
+ * precision on both page types; bf16 pages are used as stored. A sequence of context
+ * 0, and a head whose scores are all -inf, get zeros. A key or value that is
+ * infinite or NaN has the effect that the formula gives it, or makes the outputs and
+ * weights that it reaches NaN; slots past the context may hold anything. `workspace`:
+ * attn_decode_weigh_workspace_bytes(B, maxContext) bytes, 16-byte aligned,
+ * overwritten (16 bytes a token and head, which the weights are made of, and the
+ * segments' partials). A context length outside [0, maxContext] or a page index
+ * outside [0, numPages) is recorded as ATTN_EBOUNDS and clamped / read as zeros (its
+ * tokens' weights stay). Two sequences of a call must not share pages (weights are
+ * written). Errors: as attn_decode_paged, ATTN_EINVAL (NULL weights, decay outside
+ * [0, 1]). B == 0 is a no-op.
+ */
+int attn_decode_weigh_paged(const float *q, const float *kPages, const float *vPages, float *weights,
+                            const int *blockTable, const int *contextLens, const int *weighedLens, float decay,
+                            float *out, int B, int maxBlocks, int numPages, int maxContext, void *workspace,
+                            size_t workspaceBytes, cudaStream_t stream);
+int attn_decode_weigh_paged_bf16kv(const float *q, const uint16_t *kPages, const uint16_t *vPages, float *weights,
+                                   const int *blockTable, const int *contextLens, const int *weighedLens, float decay,
+                                   float *out, int B, int maxBlocks, int numPages, int maxContext, void *workspace,
+                                   size_t workspaceBytes, cudaStream_t stream);
+
+/*
+ * attn_decode_weigh_workspace_bytes -- the workspace of the two calls above for the
+ * same sizes on the current device; 0 for invalid arguments. A batch of fewer
+ * sequences may be cut into more segments: a buffer for all batches of a program is
+ * the largest of their sizes.
+ */
+size_t attn_decode_weigh_workspace_bytes(int B, int maxContext);
+
+/*
+ * attn_weigh_paged, attn_weigh_paged_bf16kv -- what a window of rows gives to the
+ * tokens of its sequences, without the rows' attention (V is not read). Row i of
+ * sequence b stands at token contextLens[b] + i, its key is in the cache, and it
+ * sees the tokens up to its own:
+ *   p_rhj = softmax_{j <= contextLens[b] + i}(q[r][h] . k_j[h/4] / 8)
+ *   W_b[j][g] = decay W_b[j][g] + sum over the sequence's rows r and h in 4 g .. 4 g
+ *               + 3 of p_rhj,  j < contextLens[b] + rows
+ *   q         [N][32][64] fp32, the batch's packed rows (attn_append_paged's qOut)
+ *   maxRows   bound of the rows of a sequence, at most 65536 (ATTN_WEIGH_ROWS);
+ *             maxContext: of its context. A window may be any number of rows, up to
+ *             a whole prompt; its work is rows x keys
+ * weighedLens NULL: contextLens[b], all tokens but the rows' own. After a prompt of
+ * which only the last rows are weighed it is what was weighed before (0 at first).
+ * A sequence without rows is left as it is; rows behind the last sequence are not
+ * read. `workspace`: attn_weigh_workspace_bytes(B, N, maxRows, maxContext) bytes,
+ * 16-byte aligned, overwritten. Pages, bounds, clamping and errors as
+ * attn_tree_paged, ATTN_EINVAL (NULL weights, decay outside [0, 1]), ATTN_ERANGE
+ * (maxRows above 65536). Two sequences of a call must not share pages. B == 0 or N ==
+ * 0 is a no-op.
+ */
+int attn_weigh_paged(const float *q, const float *kPages, float *weights, const int *blockTable,
+                     const int *contextLens, const int *rowStart, const int *weighedLens, float decay, int B, int N,
+                     int maxRows, int maxBlocks, int numPages, int maxContext, void *workspace, size_t workspaceBytes,
+                     cudaStream_t stream);
+int attn_weigh_paged_bf16kv(const float *q, const uint16_t *kPages, float *weights, const int *blockTable,
+                            const int *contextLens, const int *rowStart, const int *weighedLens, float decay, int B,
+                            int N, int maxRows, int maxBlocks, int numPages, int maxContext, void *workspace,
+                            size_t workspaceBytes, cudaStream_t stream);
+
+/*
+ * attn_weigh_workspace_bytes -- the workspace of the two calls above for the same
+ * sizes on the current device; 0 for invalid arguments. Not monotone in the batch, as
+ * above.
+ */
+size_t attn_weigh_workspace_bytes(int B, int N, int maxRows, int maxContext);
+
+/*
+ * attn_evict_paged, attn_evict_paged_bf16kv -- sequence b cut from contextLens[b] to
+ * keepLens[b] tokens (nothing happens to one that has no more than that). Every
+ * key/value head keeps its own: its first keepFirst tokens, its last keepLast, and of
+ * those between the keepLens[b] - keepFirst - keepLast of the largest weights, of
+ * equal ones the lower token. (A NaN counts as less than every number.) Keys, values
+ * and weights move together, within the head's column of the pages:
+ *   the kept tokens from keepLens[b] - keepLast on fill the gaps before it, the i-th
+ *   of them (rising) the i-th gap (rising);
+ *   the last keepLast follow in their order, up to keepLens[b] - 1.
+ * The order of the others is not kept: attention does not go by it, since a key
+ * carries its rotation. Slots from keepLens[b] on hold leftovers; pages past
+ * ceil(keepLens[b] / 16) are free to be given to others.
+ *   keepLens  int32 [B] (device); keepFirst, keepLast: the same for all sequences
+ * A sequence whose context is outside [0, maxContext], whose keepLens is negative or,
+ * where tokens have to leave, below keepFirst + keepLast, or one of whose pages is
+ * outside [0, numPages) is recorded as ATTN_EBOUNDS and left as it is. Sequences must
+ * not share pages. `workspace`: attn_evict_workspace_bytes(B, maxContext) bytes, 16-byte
+ * aligned, overwritten. Errors: ATTN_EINVAL (NULL pointer, negative size or keep
+ * count, maxBlocks or numPages < 1), ATTN_ERANGE (maxContext above 16 * maxBlocks,
+ * keepFirst or keepLast above ATTN_MAX_TOKENS, the bounds of attn_append_paged),
+ * ATTN_EALIGN, ATTN_ESPACE. B == 0 or maxContext == 0 is a no-op.
+ */
+int attn_evict_paged(float *kPages, float *vPages, float *weights, const int *blockTable, const int *contextLens,
+                     const int *keepLens, int keepFirst, int keepLast, int B, int maxBlocks, int numPages,
+                     int maxContext, void *workspace, size_t workspaceBytes, cudaStream_t stream);
+int attn_evict_paged_bf16kv(uint16_t *kPages, uint16_t *vPages, float *weights, const int *blockTable,
+                            const int *contextLens, const int *keepLens, int keepFirst, int keepLast, int B,
+                            int maxBlocks, int numPages, int maxContext, void *workspace, size_t workspaceBytes,
+                            cudaStream_t stream);
+
+/*
+ * attn_evict_workspace_bytes -- the workspace of the two calls above: it grows with B
+ * and with maxContext; 0 for invalid arguments.
+ */
+size_t attn_evict_workspace_bytes(int B, int maxContext);
 
 /*
  * The score-matrix pipeline ("Inference Attention 1: The Full Score Matrix",

@@ -11,8 +11,9 @@
 // rows, so the tensor core takes either one on its M side:
 //   rows pass  S [rows][keys]: a thread owns a row, its maximum and sum never cross threads
 //   keys pass  S [keys][rows]: a thread owns a key and adds up its column of p's
-// The rows pass leaves (log2 maximum, sum) of every row and segment of keys; the keys pass
-// merges them, so that p = 2^(s - lse), with no maximum to watch. Windows of more than 32
+// The rows pass leaves (log2 reference, sum) of every row and segment of keys; the keys pass
+// merges them, so that p = 2^(s - reference) / sum, with no maximum to watch. (As 2^(s -
+// lse) a score of a few thousand would round both passes differently.) Windows of more than 32
 // rows: more blocks in the rows pass, one after another in the keys pass, whose threads add to
 // weights that they alone write.
 //   bf16 pages: S = K (q3, q2, q1), K as stored: 3 x 4 MMAs of 128 x 128 x 16 a tile
@@ -66,8 +67,8 @@ struct Lay {
   static constexpr int kStages = kF32 ? 2 : 8;
   static constexpr int kTerms = kF32 ? 2 : 3;
   static constexpr uint32_t kSmemQ = kStages * kStageBytes;
-  static constexpr uint32_t kSmemLse = kSmemQ + kTerms * kOperand;    // [128] floats; at the end of the rows pass [128] float2
-  static constexpr uint32_t kSmemBar = kSmemLse + 128 * 8;
+  static constexpr uint32_t kSmemEnds = kSmemQ + kTerms * kOperand;   // keys pass: [128] references, [128] 1 / sums; rows: [128] float2
+  static constexpr uint32_t kSmemBar = kSmemEnds + 128 * 8;
   static constexpr int kBufs = 4;                                     // of S, two a group
   static constexpr int kNumBars = 3 * kStages + 2 * kBufs + 2;
   static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;     // TMEM address, abort flag, copies issued
@@ -123,7 +124,8 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
   volatile uint32_t* const issued = words + 2;
-  float* const lse = reinterpret_cast<float*>(smem + L::kSmemLse);
+  float* const tops = reinterpret_cast<float*>(smem + L::kSmemEnds);
+  float* const invs = tops + 128;
   const Wait wait{a.err, a.timeout_ns, abort_flag};
   const int* const trow = a.table + (size_t)b * a.max_blocks;
 
@@ -267,7 +269,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
     int k = 0;  // the group's k-th tile
     for (int rt = rt0; rt < rt1; ++rt) {
       const int i0 = rt * kRows, nrows = min(kRows, seq.rows - i0);
-      if (rt > rt0) {  // q and lse of the tile before are still in use
+      if (rt > rt0) {  // what the tile before needs is still in use
         int over;
         if (meet(kMeet, false, failed, lane, &over)) break;
       }
@@ -301,7 +303,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           }
         }
         fence_proxy_async_smem();
-        if (kByKey && g == 0) {  // the row's log2 of its sum over all keys, from the segments
+        if (kByKey && g == 0) {  // the row's reference and sum over all keys, from the segments
           float top = kUnseen, sum = 0.f;
           if ((row >> 2) < nrows) {
             const float2* const st = a.stats + ((size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3)) * a.splits;
@@ -312,11 +314,12 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             }
           }
           // a row whose scores are all -inf, or no row: gives nothing
-          lse[row] = sum == 0.f ? INFINITY : top + log2f(sum);
+          tops[row] = sum == 0.f ? INFINITY : top;
+          invs[row] = sum == 0.f ? 0.f : 1.f / sum;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(qready);
-        if (kByKey) {  // lse of all rows is written
+        if (kByKey) {  // those of all rows are written
           int over;
           if (meet(kMeet, false, failed, lane, &over)) break;
         }
@@ -350,7 +353,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 e = *reinterpret_cast<const float4*>(lse + h + i);
+              const float4 e = *reinterpret_cast<const float4*>(tops + h + i);
               fma2(x[i], x[i + 1], x[i], x[i + 1], kTreeC, kTreeC, -e.x, -e.y);
               fma2(x[i + 2], x[i + 3], x[i + 2], x[i + 3], kTreeC, kTreeC, -e.z, -e.w);
             }
@@ -360,7 +363,11 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
                 if ((h + i) / 4 < late) x[i] = -INFINITY;
             }
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) add2(sum0, sum1, sum0, sum1, ex2(x[i]), ex2(x[i + 1]));
+            for (int i = 0; i < 32; i += 4) {
+              const float4 e = *reinterpret_cast<const float4*>(invs + h + i);
+              fma2(sum0, sum1, ex2(x[i]), ex2(x[i + 1]), e.x, e.y, sum0, sum1);
+              fma2(sum0, sum1, ex2(x[i + 2]), ex2(x[i + 3]), e.z, e.w, sum0, sum1);
+            }
           }
           tc_fence_before();
           __syncwarp();
@@ -412,7 +419,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
       }
     }
     if constexpr (!kByKey) {
-      float2* const other = reinterpret_cast<float2*>(smem + L::kSmemLse);
+      float2* const other = reinterpret_cast<float2*>(smem + L::kSmemEnds);
       if (g == 1) other[row] = make_float2(ref, l0 + l1);
       int over;
       const bool lost = meet(kMeet, false, failed, lane, &over);

@@ -5,22 +5,25 @@
 //             and the 4 heads h of g; row i of a sequence sees its tokens j <= context + i
 //
 // p needs its row's sum over all keys first, and a window's scores (up to 8 KB a token) cost
-// more to keep than to compute again: two passes over K, one kernel with its operands
-// exchanged. A block has the 128 (row, head) pairs of 32 rows and a KV head, their terms in
-// shared memory, and streams tiles of 128 keys past them; both are K-major operands of 128
-// rows, so the tensor core takes either one on its M side:
-//   rows pass  S [rows][keys]: a thread owns a row, its maximum and sum never cross threads
-//   keys pass  S [keys][rows]: a thread owns a key and adds up its column of p's
-// The rows pass leaves (log2 reference, sum) of every row and segment of keys; the keys pass
-// merges them, so that p = 2^(s - reference) / sum, with no maximum to watch. (As 2^(s -
-// lse) a score of a few thousand would round both passes differently.) Windows of more than 32
-// rows: more blocks in the rows pass, one after another in the keys pass, whose threads add to
-// weights that they alone write.
-//   bf16 pages: S = K (q3, q2, q1), K as stored: 3 x 4 MMAs of 128 x 128 x 16 a tile
-//   fp32 pages: S = K q_lo + K_lo q + K q, tf32 terms: 3 x 8 MMAs of 128 x 128 x 8
+// more to keep than to compute again: two passes over K with their operands exchanged. A
+// block has the 128 (row, head) pairs of 32 rows and a KV head and streams tiles of 128 keys:
+//   rows pass  S [rows][keys], q in tensor memory: a thread owns a row, its maximum and sum
+//              never cross threads
+//   keys pass  S [keys][rows], K in tensor memory: a thread owns a key and adds up its p's
+// The rows pass leaves (reference, sum) of every row and segment of keys; the keys pass merges
+// them and has the tensor core subtract them too, by one more K step (1 .. 1) . (reference and
+// log2 of the sum, in three terms each), so that what a thread reads is log2 p and all it does
+// is 2^x and an addition. (Read from shared memory, 8 bytes a column and thread, they took as
+// long as the products.) q is scaled by log2(e) / 8 before it is split. Windows of more than 32
+// rows: more blocks in the rows pass, one row tile after another in the keys pass, whose
+// block adds to weights that it alone writes.
+//   bf16 pages: K as stored, q in three bf16 terms: 3 x 4 MMAs of 128 x 128 x 16 a tile
+//   fp32 pages: q_lo K + q K_lo + q K, tf32 terms, in halves of 32 dims: 3 x 8 of 128 x 128 x 8
+// (K is read truncated; K_lo is the remainder rounded to tf32, q's first term rounded too.)
 //
-// Roles: warps 0-3 and 4-7 take the tiles in turn; (fp32) 8-11 split K into its terms; one
-// warp for TMA (16-token pages through the block table), one to issue the products.
+// Roles: four groups of four warps take the tiles in turn; four warps that write K_lo (fp32,
+// rows) or move K to tensor memory (keys); one warp for TMA (16-token pages through the block
+// table), one to issue the products.
 #include <cuda.h>
 
 #include <mutex>
@@ -38,10 +41,11 @@ using namespace tc;
 constexpr int kRows = 32;                  // rows of a block: 128 (row, head) pairs
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kPages = kKeys / ATTN_PAGE;
-constexpr int kSoft = 8;                   // warps that read S, two groups of four
+constexpr int kGroups = 4, kSoft = 4 * kGroups;  // warps that read S
 constexpr uint32_t kHalf = 128 * 128;      // 128 rows of 128 bytes
 constexpr uint32_t kBox = ATTN_PAGE * 128;
 constexpr int kMaxSplits = 64;
+constexpr float kNothing = 1e30f;          // reference of a row that gives nothing
 constexpr unsigned kFull = 0xffffffffu;
 
 struct WeighArgs {
@@ -57,23 +61,30 @@ struct WeighArgs {
   unsigned long long timeout_ns;
 };
 
-template <bool kF32>
+template <bool kF32, bool kByKey>
 struct Lay {
-  static constexpr int kConvWarp = kSoft, kConvWarps = kF32 ? 4 : 0;
+  static constexpr int kConvWarp = kSoft, kConvWarps = kF32 || kByKey ? 4 : 0;
   static constexpr int kTmaWarp = kSoft + kConvWarps, kMmaWarp = kTmaWarp + 1;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  static constexpr uint32_t kOperand = kF32 ? 2 * kHalf : kHalf;      // a tile of K, or a term of q
-  static constexpr uint32_t kStageBytes = (kF32 ? 2 : 1) * kOperand;  // K (, K lo)
-  static constexpr int kStages = kF32 ? 2 : 8;
+  static constexpr uint32_t kOperand = kF32 ? 2 * kHalf : kHalf;     // a tile of K, or a term of q
+  static constexpr uint32_t kStageBytes = (kF32 && !kByKey ? 2 : 1) * kOperand;  // K (, K lo)
+  static constexpr int kStages = kF32 ? 3 : 8;
   static constexpr int kTerms = kF32 ? 2 : 3;
-  static constexpr uint32_t kSmemQ = kStages * kStageBytes;
-  static constexpr uint32_t kSmemEnds = kSmemQ + kTerms * kOperand;   // keys pass: [128] references, [128] 1 / sums; rows: [128] float2
-  static constexpr uint32_t kSmemBar = kSmemEnds + 128 * 8;
-  static constexpr int kBufs = 4;                                     // of S, two a group
-  static constexpr int kNumBars = 3 * kStages + 2 * kBufs + 2;
+  // Keys pass: q's terms and the references' tile.
+  static constexpr uint32_t kSmemQ = kStages * kStageBytes, kSmemRef = kSmemQ + (kByKey ? kTerms * kOperand : 0);
+  static constexpr uint32_t kSmemEnds = kSmemRef + (kByKey ? kHalf : 0);         // rows pass: [groups][128] (reference, sum)
+  static constexpr uint32_t kSmemBar = kSmemEnds + kGroups * 128 * 8;
+  // Tensor memory. Rows: q's terms, then S. Keys: parts of K (fp32 halves, hi and lo), ones, S.
+  static constexpr int kParts = kF32 && kByKey ? 2 : 1, kSlots = 3;
+  static constexpr uint32_t kSlotCols = kF32 ? 64 : 32;
+  static constexpr uint32_t kColK = 0, kColOnes = kSlots * kSlotCols;
+  static constexpr uint32_t kColQ = 0, kColS = kByKey ? kColOnes + 16 : kF32 ? 128 : 96;
+  static constexpr int kBufs = kF32 && kByKey ? 2 : 3;
+  static constexpr int kNumBars = 3 * kStages + 2 * kSlots + kGroups + kBufs + 2;
   static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;     // TMEM address, abort flag, copies issued
   static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
   static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
+  static_assert(kColS + kBufs * kKeys <= 512, "TMEM layout");
 };
 
 // The lengths of a sequence, checked as those of drafted rows are.
@@ -88,10 +99,27 @@ __device__ __forceinline__ Seq load_window(const WeighArgs& a, int b) {
   return load_seq(t, b);
 }
 
+// Three terms of x that the tensor core takes exactly: bf16, or tf32 (of fp32 pages).
+template <bool kF32>
+__device__ __forceinline__ void three_terms(float x, float (&t)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    t[i] = kF32 ? tf32_hi(x) : bf16_trunc(x);
+    x -= t[i];
+  }
+}
+
+// tcgen05.st of 8 columns.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&u)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(u[0]), "r"(u[1]),
+               "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+
 template <bool kF32, bool kByKey>
-__global__ void __launch_bounds__(Lay<kF32>::kThreads, 1)
+__global__ void __launch_bounds__(Lay<kF32, kByKey>::kThreads, 1)
 weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
-  using L = Lay<kF32>;
+  using L = Lay<kF32, kByKey>;
   constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -115,25 +143,27 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   if (kByKey && k0 >= k1) return;
 
   uint64_t* const kfull = reinterpret_cast<uint64_t*>(smem + L::kSmemBar);  // [stage] K landed
-  uint64_t* const kready = kfull + kStages;                                 // [stage] K's terms written (fp32)
-  uint64_t* const kempty = kready + kStages;                                // [stage] products done with K
-  uint64_t* const sfull = kempty + kStages;                                 // [buffer] S written
-  uint64_t* const sfree = sfull + L::kBufs;                                 // [buffer] S read
+  uint64_t* const kready = kfull + kStages;                                 // [stage] K lo written (fp32, rows)
+  uint64_t* const kempty = kready + kStages;                                // [stage] K read
+  uint64_t* const tfull = kempty + kStages;                                 // [slot] K in tensor memory (keys)
+  uint64_t* const tempty = tfull + L::kSlots;                               // [slot] products done with it
+  // A group's next S: a barrier a group, since the buffers go round in another time; the group
+  // has waited for its tile before the buffer's next product, and so its own, is issued.
+  uint64_t* const sfull = tempty + L::kSlots;                               // [group] S written
+  uint64_t* const sfree = sfull + kGroups;                                  // [buffer] S read
   uint64_t* const qready = sfree + L::kBufs;                                // q's terms of a row tile written
   uint64_t* const drain = qready + 1;
   uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
   volatile uint32_t* const issued = words + 2;
-  float* const tops = reinterpret_cast<float*>(smem + L::kSmemEnds);
-  float* const invs = tops + 128;
   const Wait wait{a.err, a.timeout_ns, abort_flag};
   const int* const trow = a.table + (size_t)b * a.max_blocks;
 
   if (warp == L::kTmaWarp) {
     for (int i = lane; i < L::kNumBars; i += 32) {
-      const bool by_conv = &kfull[i] >= kready && &kfull[i] < kempty;
-      const bool by_soft = &kfull[i] >= sfree && &kfull[i] < qready;
-      mbar_init(&kfull[i], by_conv && kF32 ? L::kConvWarps : by_soft ? 4 : &kfull[i] == qready ? kSoft : 1);
+      uint64_t* const bar = &kfull[i];
+      const bool by_four = (bar >= kready && bar < kempty) || (kByKey && bar >= kempty && bar < tempty) || (bar >= sfree && bar < qready);
+      mbar_init(bar, by_four ? 4 : bar == qready ? kSoft : 1);
     }
     fence_mbar_init();
     if (lane == 0) {
@@ -187,54 +217,81 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
     }
   } else if (warp == L::kMmaWarp) {
     const uint32_t base = smem_u32(smem);
-    int it = 0, used[2] = {0, 0};  // tiles in all, and each group's
+    int it = 0;
     bool ok = true;
     for (int rt = rt0; ok && rt < rt1; ++rt) {
       const int count = tiles(rt);
       ok = wait.warp(qready, (rt - rt0) & 1);
       for (int n = 0; ok && n < count; ++n, ++it) {
-        const int st = it % kStages, g = n & 1, k = used[g], buf = 2 * g + (k & 1);
-        ++used[g];
-        if (!(ok = wait.warp(kF32 ? &kready[st] : &kfull[st], (it / kStages) & 1) &&
-                   (k < 2 || wait.warp(&sfree[buf], ((k >> 1) - 1) & 1))))
-          break;
-        tc_fence_after();
-        const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes), qd = sdesc_sw128(base + L::kSmemQ);
-        const uint32_t d = tmem + buf * kKeys;
-        if (elect()) {
-          const auto product = [&](uint64_t kt, uint64_t qt, bool first) {
+        const int buf = it % L::kBufs;
+        const uint32_t d = tmem + L::kColS + buf * kKeys;
+        if (it >= L::kBufs && !(ok = wait.warp(&sfree[buf], (it / L::kBufs - 1) & 1))) break;
+        constexpr uint32_t id = kF32 ? idesc_tf32(128, 128) : idesc_bf16(128, 128, false);
+        constexpr uint64_t lo = L::kOperand >> 4;
+        if constexpr (!kByKey) {
+          const int st = it % kStages;
+          if (!(ok = wait.warp(kF32 ? &kready[st] : &kfull[st], (it / kStages) & 1))) break;
+          tc_fence_after();
+          const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes);
+          const uint32_t q = tmem + L::kColQ;
+          if (elect()) {
             if constexpr (kF32) {
-              constexpr uint32_t id = idesc_tf32(128, 128);
 #pragma unroll
-              for (int x = 0; x < 8; ++x) {
-                const uint64_t at = (x >> 2) * (kHalf >> 4) + (x & 3) * 2;
-                mma_tf32_ss(d, (kByKey ? kt : qt) + at, (kByKey ? qt : kt) + at, id, !first || x > 0);
+              for (int h = 0; h < 2; ++h) {
+                const uint64_t kh = kd + h * (kHalf >> 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, q + 64 + h * 32 + x * 8, kh + x * 2, id, h + x > 0);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, q + h * 32 + x * 8, kh + lo + x * 2, id, 1);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, q + h * 32 + x * 8, kh + x * 2, id, 1);
               }
             } else {
-              constexpr uint32_t id = idesc_bf16(128, 128, false);
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                mma_f16_ss(d, (kByKey ? kt : qt) + x * 2, (kByKey ? qt : kt) + x * 2, id, !first || x > 0);
+              for (int t = 2; t >= 0; --t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + t * 32 + x * 8, kd + x * 2, id, t < 2 || x > 0);
             }
-          };
-          constexpr uint64_t next = L::kOperand >> 4;
-          if constexpr (kF32) {
-            product(kd, qd + next, true);
-            product(kd + next, qd, false);
-            product(kd, qd, false);
-          } else {
-            product(kd, qd + 2 * next, true);
-            product(kd, qd + next, false);
-            product(kd, qd, false);
+            mma_commit(&sfull[it % kGroups]);
+            mma_commit(&kempty[st]);
           }
-          mma_commit(&sfull[buf]);
-          mma_commit(&kempty[st]);
+          __syncwarp();
+        } else {
+          const uint64_t qd = sdesc_sw128(base + L::kSmemQ), rd = sdesc_sw128(base + L::kSmemRef);
+#pragma unroll 1
+          for (int h = 0; ok && h < L::kParts; ++h) {
+            const int part = it * L::kParts + h, slot = part % L::kSlots;
+            if (!(ok = wait.warp(&tfull[slot], (part / L::kSlots) & 1))) break;
+            tc_fence_after();
+            const uint32_t k = tmem + L::kColK + slot * L::kSlotCols;
+            if (elect()) {
+              if constexpr (kF32) {
+                const uint64_t qh = qd + h * (kHalf >> 4);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, k + x * 8, qh + lo + x * 2, id, h + x > 0);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, k + 32 + x * 8, qh + x * 2, id, 1);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, k + x * 8, qh + x * 2, id, 1);
+              } else {
+#pragma unroll
+                for (int t = 2; t >= 0; --t)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) mma_f16_ts(d, k + x * 8, qd + t * lo + x * 2, id, t < 2 || x > 0);
+              }
+              mma_commit(&tempty[slot]);
+              if (h == L::kParts - 1) {
+                if constexpr (kF32) mma_tf32_ts(d, tmem + L::kColOnes, rd, id, 1);
+                else mma_f16_ts(d, tmem + L::kColOnes, rd, id, 1);
+                mma_commit(&sfull[it % kGroups]);
+              }
+            }
+            __syncwarp();
+          }
         }
-        __syncwarp();
       }
     }
-  } else if (kF32 && warp >= L::kConvWarp && warp < L::kTmaWarp) {
-    // hi(x), rounded to nearest, in place and lo = x - hi(x) at the same offset of the next region.
+  } else if (warp >= L::kConvWarp && warp < L::kTmaWarp) {
     const int ctid = tid - 32 * L::kConvWarp;
     int total = 0;
     for (int rt = rt0; rt < rt1; ++rt) total += tiles(rt);
@@ -242,22 +299,53 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
       const int st = it % kStages;
       uint8_t* const stage = smem + st * L::kStageBytes;
       if (!wait.warp(&kfull[st], (it / kStages) & 1)) break;
+      if constexpr (!kByKey) {
+        // K lo, at the same offset of the next region.
 #pragma unroll 2
-      for (int h = 0; h < 4; ++h) {
-        float4 x[4];
+        for (int h = 0; h < 4; ++h) {
+          float4 x[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(stage + (ctid + (4 * h + i) * 128) * 16);
+          for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(stage + (ctid + (4 * h + i) * 128) * 16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint8_t* const at = stage + (ctid + (4 * h + i) * 128) * 16;
-          const float4 y = make_float4(tf32_near(x[i].x), tf32_near(x[i].y), tf32_near(x[i].z), tf32_near(x[i].w));
-          *reinterpret_cast<float4*>(at) = y;
-          *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x[i].x - y.x, x[i].y - y.y, x[i].z - y.z, x[i].w - y.w);
+          for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<float4*>(stage + (ctid + (4 * h + i) * 128) * 16 + L::kOperand) =
+                make_float4(tf32_near(x[i].x - tf32_hi(x[i].x)), tf32_near(x[i].y - tf32_hi(x[i].y)),
+                            tf32_near(x[i].z - tf32_hi(x[i].z)), tf32_near(x[i].w - tf32_hi(x[i].w)));
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kready[st]);
+      } else {
+        // A thread's key, row ctid of the tile, to its lane of tensor memory.
+        bool ok = true;
+#pragma unroll
+        for (int h = 0; ok && h < L::kParts; ++h) {
+          const int part = it * L::kParts + h, slot = part % L::kSlots;
+          float x[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(x + 4 * i) =
+                *reinterpret_cast<const float4*>(stage + h * kHalf + sw128((uint32_t)ctid * 128u + i * 16u));
+          if (h == L::kParts - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kempty[st]);
+          }
+          if (part >= L::kSlots && !(ok = wait.warp(&tempty[slot], (part / L::kSlots - 1) & 1))) break;
+          tc_fence_after();
+          const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + L::kColK + slot * L::kSlotCols;
+          tmem_st32(at, x);
+          if constexpr (kF32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = tf32_near(x[i] - tf32_hi(x[i]));
+            tmem_st32(at + 32, x);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tfull[slot]);
+        }
+        if (!ok) break;
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&kready[st]);
     }
   } else if (warp < kSoft) {
     constexpr int kMeet = 32 * kSoft;
@@ -266,75 +354,107 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
     bool failed = false;
     float ref = kUnseen, l0 = 0.f, l1 = 0.f;
     const int weighed = kByKey ? (a.weighed_lens ? fetch(a.weighed_lens + b) : seq.ctx) : 0;
-    int k = 0;  // the group's k-th tile
+    int done = 0;  // tiles of the row tiles before
     for (int rt = rt0; rt < rt1; ++rt) {
       const int i0 = rt * kRows, nrows = min(kRows, seq.rows - i0);
-      if (rt > rt0) {  // what the tile before needs is still in use
+      const bool in = (row >> 2) < nrows;
+      const size_t pair = (size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3);
+      if (rt > rt0) {  // what the tile before needs is still in use; its weights are written
         int over;
         if (meet(kMeet, false, failed, lane, &over)) break;
       }
-      {  // q in its terms: thread (row, half g) 32 dims of (row tile's row, head); rows past the last are zeros
-        const float* const src = a.q + ((size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3)) * kD + g * 32;
-        uint8_t* const dst = smem + L::kSmemQ;
+      // q in its terms; rows past the last are zeros.
+      {
+        float x[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 8) {
-          float x[8];
+        for (int i = 0; i < 16; i += 4) {
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (in) v = fetch(reinterpret_cast<const float4*>(a.q + pair * kD + g * 16 + i));
+          x[i] = v.x * kTreeC, x[i + 1] = v.y * kTreeC, x[i + 2] = v.z * kTreeC, x[i + 3] = v.w * kTreeC;
+        }
+        if constexpr (!kByKey && kF32) {
+          uint32_t w[2][16];
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if ((row >> 2) < nrows) v = fetch(reinterpret_cast<const float4*>(src + i + j));
-            x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+          for (int i = 0; i < 16; ++i) {
+            const float h = tf32_near(x[i]);
+            w[0][i] = __float_as_uint(h), w[1][i] = __float_as_uint(x[i] - h);
           }
-          if constexpr (kF32) {
 #pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-              uint8_t* const at = dst + g * kHalf + sw128((uint32_t)row * 128u + (i + j) * 4u);
-              const float4 h = make_float4(tf32_near(x[j]), tf32_near(x[j + 1]), tf32_near(x[j + 2]), tf32_near(x[j + 3]));
-              *reinterpret_cast<float4*>(at) = h;
-              *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x[j] - h.x, x[j + 1] - h.y, x[j + 2] - h.z, x[j + 3] - h.w);
-            }
-          } else {
+          for (int t = 0; t < 2; ++t) tmem_st16(lane_tmem + L::kColQ + t * 64 + g * 16, w[t]);
+        } else if constexpr (!kByKey) {
+          uint32_t w[3][8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) split3_cut(x[2 * i], x[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+#pragma unroll
+          for (int t = 0; t < 3; ++t) tmem_st8(lane_tmem + L::kColQ + t * 32 + g * 8, w[t]);
+        } else if constexpr (kF32) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            uint8_t* const at = smem + L::kSmemQ + (g >> 1) * kHalf + sw128((uint32_t)row * 128u + (g & 1) * 64u + i * 4u);
+            const float4 h = make_float4(tf32_near(x[i]), tf32_near(x[i + 1]), tf32_near(x[i + 2]), tf32_near(x[i + 3]));
+            *reinterpret_cast<float4*>(at) = h;
+            *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x[i] - h.x, x[i + 1] - h.y, x[i + 2] - h.z, x[i + 3] - h.w);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; i += 8) {
             uint32_t w[3][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split3_cut(x[2 * j], x[2 * j + 1], w[0][j], w[1][j], w[2][j]);
-            uint8_t* const at = dst + sw128((uint32_t)row * 128u + (g * 32 + i) * 2u);
+            for (int j = 0; j < 4; ++j) split3_cut(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j], w[2][j]);
+            uint8_t* const at = smem + L::kSmemQ + sw128((uint32_t)row * 128u + g * 32u + i * 2u);
 #pragma unroll
             for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(at + t * L::kOperand) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
           }
         }
-        fence_proxy_async_smem();
-        if (kByKey && g == 0) {  // the row's reference and sum over all keys, from the segments
+        if (kByKey && g == 0) {
+          // The row's reference and the logarithm of its sum over all keys, from the segments.
           float top = kUnseen, sum = 0.f;
-          if ((row >> 2) < nrows) {
-            const float2* const st = a.stats + ((size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3)) * a.splits;
-            for (int x = 0; x < a.splits; ++x) top = fmaxf(top, fetch(st + x).x);
-            for (int x = 0; x < a.splits; ++x) {
-              const float2 p = fetch(st + x);
+          if (in) {
+            const float2* const st = a.stats + pair * a.splits;
+#pragma unroll 4
+            for (int i = 0; i < a.splits; ++i) top = fmaxf(top, fetch(st + i).x);
+#pragma unroll 4
+            for (int i = 0; i < a.splits; ++i) {
+              const float2 p = fetch(st + i);
               sum = fmaf(ex2(p.x - top), p.y, sum);
             }
           }
-          // a row whose scores are all -inf, or no row: gives nothing
-          tops[row] = sum == 0.f ? INFINITY : top;
-          invs[row] = sum == 0.f ? 0.f : 1.f / sum;
+          // A row whose scores are all -inf, or none: 2^x is 0 whatever x is.
+          float t[6];
+          three_terms<kF32>(sum == 0.f ? -kNothing : -top, *reinterpret_cast<float(*)[3]>(t));
+          three_terms<kF32>(sum == 0.f ? 0.f : -log2f(sum), *reinterpret_cast<float(*)[3]>(t + 3));
+          uint4 u0, u1 = make_uint4(0, 0, 0, 0);
+          if constexpr (kF32) {
+            u0 = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
+            u1.x = __float_as_uint(t[4]), u1.y = __float_as_uint(t[5]);
+          } else {
+            u0 = make_uint4(pack_bf16_trunc(t[0], t[1]), pack_bf16_trunc(t[2], t[3]), pack_bf16_trunc(t[4], t[5]), 0u);
+          }
+          *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u)) = u0;
+          *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u + 16u)) = u1;
+          if (rt == rt0) {
+            constexpr uint32_t kOne = kF32 ? 0x3f800000u : 0x3f803f80u;
+            const uint32_t ones[8] = {kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne};
+            tmem_st8(lane_tmem + L::kColOnes, ones);
+          }
         }
+        if (kByKey) fence_proxy_async_smem();
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(qready);
-        if (kByKey) {  // those of all rows are written
-          int over;
-          if (meet(kMeet, false, failed, lane, &over)) break;
-        }
       }
       const int count = tiles(rt);
-      for (int n = g; n < count; n += 2, ++k) {
-        const int buf = 2 * g + (k & 1), t0 = k0 + n * kKeys;
-        const uint32_t s_tmem = lane_tmem + buf * kKeys;
+      for (int n = (g - done) & (kGroups - 1); n < count; n += kGroups) {
+        const int it = done + n, buf = it % L::kBufs, t0 = k0 + n * kKeys;
+        const uint32_t s_tmem = lane_tmem + L::kColS + buf * kKeys;
         if constexpr (kByKey) {
-          const int t = t0 + row, end = visible(rt);
+          const int t = t0 + row;
           // The key's weight so far, on its way while the products run. Row tile (t - context) /
           // 32 is the first that sees a token of the rows themselves, 0 any other.
           float* w = nullptr;
           float old = 0.f;
-          if (t < end) {
+          if (t < visible(rt)) {
             const int page = fetch(trow + t / ATTN_PAGE);
             if (page >= 0 && page < a.num_pages) {
               w = a.weights + ((size_t)page * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;
@@ -342,7 +462,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
               else if (a.decay != 0.f && t < weighed) old = a.decay * *w;
             }
           }
-          failed |= !wait.warp(&sfull[buf], (k >> 1) & 1);
+          failed |= !wait.warp(&sfull[g], (it / kGroups) & 1);
           tc_fence_after();
           float sum0 = 0.f, sum1 = 0.f;
           const int late = t - seq.ctx - i0;  // rows before it do not see the key
@@ -351,11 +471,10 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             float x[32];
             tmem_ld32(s_tmem + h, x);
             tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 e = *reinterpret_cast<const float4*>(tops + h + i);
-              fma2(x[i], x[i + 1], x[i], x[i + 1], kTreeC, kTreeC, -e.x, -e.y);
-              fma2(x[i + 2], x[i + 3], x[i + 2], x[i + 3], kTreeC, kTreeC, -e.z, -e.w);
+            if (h == 96) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sfree[buf]);
             }
             if (t0 + kKeys > seq.ctx + i0) {
 #pragma unroll
@@ -363,35 +482,26 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
                 if ((h + i) / 4 < late) x[i] = -INFINITY;
             }
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 e = *reinterpret_cast<const float4*>(invs + h + i);
-              fma2(sum0, sum1, ex2(x[i]), ex2(x[i + 1]), e.x, e.y, sum0, sum1);
-              fma2(sum0, sum1, ex2(x[i + 2]), ex2(x[i + 3]), e.z, e.w, sum0, sum1);
-            }
+            for (int i = 0; i < 32; i += 2) add2(sum0, sum1, sum0, sum1, ex2(x[i]), ex2(x[i + 1]));
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sfree[buf]);
           if (w && !failed) *w = old + (sum0 + sum1);
         } else {
-          failed |= !wait.warp(&sfull[buf], (k >> 1) & 1);
+          failed |= !wait.warp(&sfull[g], (it / kGroups) & 1);
           tc_fence_after();
-          const int sees = seq.ctx + i0 + (row >> 2) + 1 - t0;  // keys of the tile that the row sees
-          const int limit = min(sees, k1 - t0);
+          const int limit = min(seq.ctx + i0 + (row >> 2) + 1, k1) - t0;  // keys of the tile that the row sees
 #pragma unroll
-          for (int h = 0; h < 128; h += 64) {
-            float x[64];
-            tmem_ld32(s_tmem + h, *reinterpret_cast<float(*)[32]>(&x[0]));
-            tmem_ld32(s_tmem + h + 32, *reinterpret_cast<float(*)[32]>(&x[32]));
+          for (int h = 0; h < 128; h += 32) {
+            float x[32];
+            tmem_ld32(s_tmem + h, x);
             tmem_wait_ld();
-            if (h == 64) {
+            if (h == 96) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&sfree[buf]);
             }
             if (t0 + kKeys > min(seq.ctx + i0, k1)) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i)
+              for (int i = 0; i < 32; ++i)
                 if (h + i >= limit) x[i] = -INFINITY;
             }
             float top[4];
@@ -399,9 +509,9 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             for (int c = 0; c < 4; ++c) {
               top[c] = fmaxf(x[c], x[c + 4]);
 #pragma unroll
-              for (int i = 8; i < 64; i += 8) top[c] = max3(top[c], x[i + c], x[i + c + 4]);
+              for (int i = 8; i < 32; i += 8) top[c] = max3(top[c], x[i + c], x[i + c + 4]);
             }
-            const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]) * kTreeC;
+            const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]);
             if (most > ref + kTreeStale) {
               const float alpha = ex2(ref - most);
               ref = most;
@@ -410,24 +520,28 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             }
             const float neg = -ref;
 #pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-              fma2(x[i], x[i + 1], x[i], x[i + 1], kTreeC, kTreeC, neg, neg);
+            for (int i = 0; i < 32; i += 2) {
+              add2(x[i], x[i + 1], x[i], x[i + 1], neg, neg);
               add2(l0, l1, l0, l1, ex2(x[i]), ex2(x[i + 1]));
             }
           }
         }
       }
+      done += count;
     }
     if constexpr (!kByKey) {
-      float2* const other = reinterpret_cast<float2*>(smem + L::kSmemEnds);
-      if (g == 1) other[row] = make_float2(ref, l0 + l1);
+      float2* const ends = reinterpret_cast<float2*>(smem + L::kSmemEnds);
+      if (g > 0) ends[g * 128 + row] = make_float2(ref, l0 + l1);
       int over;
       const bool lost = meet(kMeet, false, failed, lane, &over);
       const int i = rt0 * kRows + (row >> 2);
       if (g == 0 && i < seq.rows) {
-        const float2 o = other[row];
-        const float top = fmaxf(ref, o.x);
-        const float sum = fmaf(ex2(ref - top), l0 + l1, ex2(o.x - top) * o.y);
+        float top = ref;
+#pragma unroll
+        for (int x = 1; x < kGroups; ++x) top = fmaxf(top, ends[x * 128 + row].x);
+        float sum = ex2(ref - top) * (l0 + l1);
+#pragma unroll
+        for (int x = 1; x < kGroups; ++x) sum = fmaf(ex2(ends[x * 128 + row].x - top), ends[x * 128 + row].y, sum);
         a.stats[((size_t)(seq.first + i) * kHQ + head * kGroup + (row & 3)) * a.splits + s] =
             lost ? make_float2(kUnseen, 0.f) : make_float2(top, sum);
       }
@@ -453,7 +567,7 @@ struct Device {
 template <bool kF32, bool kByKey>
 bool set_up() {
   return cudaFuncSetAttribute(weigh_kernel<kF32, kByKey>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Lay<kF32>::kSmemAlloc) == cudaSuccess;
+                              (int)Lay<kF32, kByKey>::kSmemAlloc) == cudaSuccess;
 }
 int device(Device** out) {
   constexpr int kMaxDev = 64;
@@ -538,8 +652,9 @@ int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
   for (int pass = 0; pass < 2; ++pass) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = pass ? dim3(a.key_splits, kHKV, c.B) : dim3(a.splits, kHKV * tiles, c.B);
-    cfg.blockDim = dim3(bf16 ? Lay<false>::kThreads : Lay<true>::kThreads);
-    cfg.dynamicSmemBytes = bf16 ? Lay<false>::kSmemAlloc : Lay<true>::kSmemAlloc;
+    cfg.blockDim = dim3(bf16 ? (pass ? Lay<false, true>::kThreads : Lay<false, false>::kThreads) : Lay<true, false>::kThreads);
+    cfg.dynamicSmemBytes = bf16 ? (pass ? Lay<false, true>::kSmemAlloc : Lay<false, false>::kSmemAlloc)
+                                : (pass ? Lay<true, true>::kSmemAlloc : Lay<true, false>::kSmemAlloc);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -42,9 +42,11 @@ constexpr int kRows = 32;                  // rows of a block: 128 (row, head) p
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kPages = kKeys / ATTN_PAGE;
 constexpr int kGroups = 4, kSoft = 4 * kGroups;  // warps that read S
+constexpr int kTmaWarps = 2;               // tiles in turn: a box of 16 rows costs its warp about 100 cycles
 constexpr uint32_t kHalf = 128 * 128;      // 128 rows of 128 bytes
 constexpr uint32_t kBox = ATTN_PAGE * 128;
 constexpr int kMaxSplits = 64;
+constexpr int kWideRows = 8;               // windows from which on operands have two bf16 terms
 constexpr float kNothing = 1e30f;          // reference of a row that gives nothing
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -54,34 +56,40 @@ struct WeighArgs {
   const int *table, *ctx_lens, *row_start, *weighed_lens;
   float2* stats;           // [N][32][splits]: log2 maximum, sum (both 0 of a segment without keys)
   int B, N, max_rows, max_blocks, num_pages, max_context;
-  int splits;              // of the rows pass
+  int row_tiles, splits;   // of the rows pass
   int key_splits;          // of the keys pass
   float decay;
   unsigned* err;
   unsigned long long timeout_ns;
 };
 
-template <bool kF32, bool kByKey>
+template <bool kF32, bool kByKey, bool kWide>
 struct Lay {
-  static constexpr int kConvWarp = kSoft, kConvWarps = kF32 || kByKey ? 4 : 0;
-  static constexpr int kTmaWarp = kSoft + kConvWarps, kMmaWarp = kTmaWarp + 1;
+  static constexpr bool kTf32 = kF32 && !kWide;  // else bf16 operands
+  static constexpr bool kDirect = !kF32 && !kByKey;  // the tensor core reads K as it landed
+  static constexpr bool kSlotted = kByKey || (kF32 && kWide);  // K goes on to slots, in tensor memory (keys) or shared (rows)
+  static constexpr int kConvWarp = kSoft, kConvWarps = kDirect ? 0 : 4;
+  static constexpr int kTmaWarp = kSoft + kConvWarps, kMmaWarp = kTmaWarp + kTmaWarps;
   static constexpr int kThreads = 32 * (kMmaWarp + 1);
-  static constexpr uint32_t kOperand = kF32 ? 2 * kHalf : kHalf;     // a tile of K, or a term of q
-  static constexpr uint32_t kStageBytes = (kF32 && !kByKey ? 2 : 1) * kOperand;  // K (, K lo)
-  static constexpr int kStages = kF32 ? 3 : 8;
-  static constexpr int kTerms = kF32 ? 2 : 3;
-  // Keys pass: q's terms and the references' tile.
-  static constexpr uint32_t kSmemQ = kStages * kStageBytes, kSmemRef = kSmemQ + (kByKey ? kTerms * kOperand : 0);
+  static constexpr uint32_t kRaw = kF32 ? 2 * kHalf : kHalf;          // a tile of K as it lands
+  static constexpr uint32_t kOperand = kTf32 ? 2 * kHalf : kHalf;     // an operand of 128 rows
+  static constexpr uint32_t kStageBytes = kRaw + (kTf32 && !kByKey ? kOperand : 0);  // K (, K lo)
+  static constexpr int kStages = kTf32 ? 3 : kF32 ? 4 : 8;
+  static constexpr int kTerms = kTf32 || kWide ? 2 : 3;               // of q
+  static constexpr int kSlots = kF32 && kWide && !kByKey ? 2 : 3;
+  static constexpr uint32_t kSmemSlots = kStages * kStageBytes;       // rows pass of wide windows: K's two terms
+  static constexpr uint32_t kSmemQ = kSmemSlots + (kSlotted && !kByKey ? kSlots * 2 * kOperand : 0);  // keys pass: q's terms
+  static constexpr uint32_t kSmemRef = kSmemQ + (kByKey ? kTerms * kOperand : 0);                    // and the references' tile
   static constexpr uint32_t kSmemEnds = kSmemRef + (kByKey ? kHalf : 0);         // rows pass: [groups][128] (reference, sum)
   static constexpr uint32_t kSmemBar = kSmemEnds + kGroups * 128 * 8;
-  // Tensor memory. Rows: q's terms, then S. Keys: parts of K (fp32 halves, hi and lo), ones, S.
-  static constexpr int kParts = kF32 && kByKey ? 2 : 1, kSlots = 3;
+  // Tensor memory. Rows: q's terms, then S. Keys: parts of K (tf32: halves, hi and lo), ones, S.
+  static constexpr int kParts = kTf32 && kByKey ? 2 : 1;
   static constexpr uint32_t kSlotCols = kF32 ? 64 : 32;
   static constexpr uint32_t kColK = 0, kColOnes = kSlots * kSlotCols;
-  static constexpr uint32_t kColQ = 0, kColS = kByKey ? kColOnes + 16 : kF32 ? 128 : 96;
+  static constexpr uint32_t kColQ = 0, kTermCols = kTf32 ? 64 : 32, kColS = kByKey ? kColOnes + 16 : kTerms * kTermCols;
   static constexpr int kBufs = kF32 && kByKey ? 2 : 3;
   static constexpr int kNumBars = 3 * kStages + 2 * kSlots + kGroups + kBufs + 2;
-  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;     // TMEM address, abort flag, copies issued
+  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;     // TMEM address, abort flag
   static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
   static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
   static_assert(kColS + kBufs * kKeys <= 512, "TMEM layout");
@@ -100,13 +108,24 @@ __device__ __forceinline__ Seq load_window(const WeighArgs& a, int b) {
 }
 
 // Three terms of x that the tensor core takes exactly: bf16, or tf32 (of fp32 pages).
-template <bool kF32>
+template <bool kTf32>
 __device__ __forceinline__ void three_terms(float x, float (&t)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    t[i] = kF32 ? tf32_hi(x) : bf16_trunc(x);
+    t[i] = kTf32 ? tf32_hi(x) : bf16_trunc(x);
     x -= t[i];
   }
+}
+
+// Two bf16 terms of a pair, each rounded to nearest: 16 bits and a sign, 2^-18 of x left out.
+// (A finite value that would round to infinity takes the largest bf16 number.)
+__device__ __forceinline__ void split2(float x, float y, uint32_t& t0, uint32_t& t1) {
+  const float most = __uint_as_float(0x7f7f0000u);
+  float cx, cy, hx, hy;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(cx) : "f"(x), "f"(most));
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(cy) : "f"(y), "f"(most));
+  t0 = pack_bf16_rn_keep(cx, cy, hx, hy);
+  t1 = pack_bf16_rn(x - hx, y - hy);
 }
 
 // tcgen05.st of 8 columns.
@@ -116,10 +135,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&u)[8])
                : "memory");
 }
 
-template <bool kF32, bool kByKey>
-__global__ void __launch_bounds__(Lay<kF32, kByKey>::kThreads, 1)
+template <bool kF32, bool kByKey, bool kWide>
+__global__ void __launch_bounds__(Lay<kF32, kByKey, kWide>::kThreads, 1)
 weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
-  using L = Lay<kF32, kByKey>;
+  using L = Lay<kF32, kByKey, kWide>;
   constexpr int kStages = L::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -127,11 +146,14 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
   if (warp == L::kTmaWarp && lane == 0) tma_prefetch_desc(&mk);
   follow();
-  const int s = blockIdx.x, head = blockIdx.y % kHKV, b = blockIdx.z;
+  // Rows pass: the row tiles of a segment are neighbours in the grid and read its keys at
+  // about the same time, all but one from L2.
+  const int row_tiles = kByKey ? 1 : a.row_tiles;
+  const int s = blockIdx.x / row_tiles, head = blockIdx.y, b = blockIdx.z;
   const Seq seq = load_window(a, b);
-  if (!seq.ok && s == 0 && !kByKey && blockIdx.y == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+  if (!seq.ok && !kByKey && blockIdx.x == 0 && head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
   // The rows of this block: a tile of 32 of them, or by key all tiles one after another.
-  const int rt0 = kByKey ? 0 : blockIdx.y / kHKV, rt1 = kByKey ? (seq.rows + kRows - 1) / kRows : rt0 + 1;
+  const int rt0 = kByKey ? 0 : blockIdx.x % row_tiles, rt1 = kByKey ? (seq.rows + kRows - 1) / kRows : rt0 + 1;
   if (seq.rows - rt0 * kRows <= 0) return;
   // The sequence's own keys, cut evenly into segments of whole tiles.
   const int splits = kByKey ? a.key_splits : a.splits;
@@ -143,9 +165,9 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   if (kByKey && k0 >= k1) return;
 
   uint64_t* const kfull = reinterpret_cast<uint64_t*>(smem + L::kSmemBar);  // [stage] K landed
-  uint64_t* const kready = kfull + kStages;                                 // [stage] K lo written (fp32, rows)
+  uint64_t* const kready = kfull + kStages;                                 // [stage] K lo written (tf32, rows)
   uint64_t* const kempty = kready + kStages;                                // [stage] K read
-  uint64_t* const tfull = kempty + kStages;                                 // [slot] K in tensor memory (keys)
+  uint64_t* const tfull = kempty + kStages;                                 // [slot] K written there
   uint64_t* const tempty = tfull + L::kSlots;                               // [slot] products done with it
   // A group's next S: a barrier a group, since the buffers go round in another time; the group
   // has waited for its tile before the buffer's next product, and so its own, is issued.
@@ -155,21 +177,17 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   uint64_t* const drain = qready + 1;
   uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
-  volatile uint32_t* const issued = words + 2;
   const Wait wait{a.err, a.timeout_ns, abort_flag};
   const int* const trow = a.table + (size_t)b * a.max_blocks;
 
   if (warp == L::kTmaWarp) {
     for (int i = lane; i < L::kNumBars; i += 32) {
       uint64_t* const bar = &kfull[i];
-      const bool by_four = (bar >= kready && bar < kempty) || (kByKey && bar >= kempty && bar < tempty) || (bar >= sfree && bar < qready);
+      const bool by_four = (bar >= kready && bar < kempty) || (L::kSlotted && bar >= kempty && bar < tempty) || (bar >= sfree && bar < qready);
       mbar_init(bar, by_four ? 4 : bar == qready ? kSoft : 1);
     }
     fence_mbar_init();
-    if (lane == 0) {
-      *abort_flag = 0;
-      *issued = 0;
-    }
+    if (lane == 0) *abort_flag = 0;
   } else if (warp == L::kMmaWarp) {
     tmem_alloc(words, 512);
     tmem_relinquish();
@@ -178,8 +196,10 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = words[0];
+  int last = -1;  // the last tile that a TMA warp has asked for
 
-  if (warp == L::kTmaWarp) {
+  if (warp >= L::kTmaWarp && warp < L::kMmaWarp) {
+    const int mine = warp - L::kTmaWarp;  // this warp's tiles: every second one
     int it = 0;
     bool ok = true;
     for (int rt = rt0; ok && rt < rt1; ++rt) {
@@ -191,24 +211,24 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
       };
       int entries = entry_at(0), entries_next = entry_at(1);
       for (int n = 0; n < count; ++n, ++it) {
-        const int st = it % kStages;
-        if (it >= kStages && !(ok = wait.warp(&kempty[st], (it / kStages - 1) & 1))) break;
-        const int p = lane & (kPages - 1), half = lane / kPages;
-        int page = __shfl_sync(kFull, entries, (n & 3) * kPages + p);
-        const int pages = min(kPages, (end - k0 - n * kKeys + ATTN_PAGE - 1) / ATTN_PAGE);
-        const bool has = half < (kF32 ? 2 : 1) && p < pages;
-        if (has && (page < 0 || page >= a.num_pages)) {
-          record_error(a.err, kDevErrBounds);
-          page = a.num_pages;  // past the pool's end: reads as zeros
+        if ((it & (kTmaWarps - 1)) == mine) {
+          const int st = it % kStages;
+          if (it >= kStages && !(ok = wait.warp(&kempty[st], (it / kStages - 1) & 1))) break;
+          const int p = lane & (kPages - 1), half = lane / kPages;
+          int page = __shfl_sync(kFull, entries, (n & 3) * kPages + p);
+          const int pages = min(kPages, (end - k0 - n * kKeys + ATTN_PAGE - 1) / ATTN_PAGE);
+          const bool has = half < (kF32 ? 2 : 1) && p < pages;
+          if (has && (page < 0 || page >= a.num_pages)) {
+            record_error(a.err, kDevErrBounds);
+            page = a.num_pages;  // past the pool's end: reads as zeros
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&kfull[st], pages * (kF32 ? 2 : 1) * kBox);
+          last = it;
+          __syncwarp();
+          if (has)
+            tma_load_2d(smem + st * L::kStageBytes + half * kHalf + p * kBox, &mk, &kfull[st], head * kD + half * 32,
+                        page * ATTN_PAGE);
         }
-        if (lane == 0) {
-          mbar_arrive_expect_tx(&kfull[st], pages * (kF32 ? 2 : 1) * kBox);
-          *issued = it + 1;
-        }
-        __syncwarp();
-        if (has)
-          tma_load_2d(smem + st * L::kStageBytes + half * kHalf + p * kBox, &mk, &kfull[st], head * kD + half * 32,
-                      page * ATTN_PAGE);
         if ((n & 3) == 3) {
           entries = entries_next;
           entries_next = entry_at((n >> 2) + 2);
@@ -226,16 +246,18 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
         const int buf = it % L::kBufs;
         const uint32_t d = tmem + L::kColS + buf * kKeys;
         if (it >= L::kBufs && !(ok = wait.warp(&sfree[buf], (it / L::kBufs - 1) & 1))) break;
-        constexpr uint32_t id = kF32 ? idesc_tf32(128, 128) : idesc_bf16(128, 128, false);
+        constexpr uint32_t id = L::kTf32 ? idesc_tf32(128, 128) : idesc_bf16(128, 128, false);
         constexpr uint64_t lo = L::kOperand >> 4;
         if constexpr (!kByKey) {
-          const int st = it % kStages;
-          if (!(ok = wait.warp(kF32 ? &kready[st] : &kfull[st], (it / kStages) & 1))) break;
+          const int st = it % kStages, slot = it % L::kSlots;
+          if (!(ok = L::kSlotted ? wait.warp(&tfull[slot], (it / L::kSlots) & 1)
+                                 : wait.warp(kF32 ? &kready[st] : &kfull[st], (it / kStages) & 1)))
+            break;
           tc_fence_after();
-          const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes);
+          const uint64_t kd = sdesc_sw128(base + (L::kSlotted ? L::kSmemSlots + slot * 2 * L::kOperand : st * L::kStageBytes));
           const uint32_t q = tmem + L::kColQ;
           if (elect()) {
-            if constexpr (kF32) {
+            if constexpr (L::kTf32) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 const uint64_t kh = kd + h * (kHalf >> 4);
@@ -247,13 +269,17 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
                 for (int x = 0; x < 4; ++x) mma_tf32_ts(d, q + h * 32 + x * 8, kh + x * 2, id, 1);
               }
             } else {
+              if constexpr (kF32) {
 #pragma unroll
-              for (int t = 2; t >= 0; --t)
+                for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + x * 8, kd + lo + x * 2, id, x > 0);
+              }
 #pragma unroll
-                for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + t * 32 + x * 8, kd + x * 2, id, t < 2 || x > 0);
+              for (int t = L::kTerms - 1; t >= 0; --t)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + t * 32 + x * 8, kd + x * 2, id, kF32 || t < L::kTerms - 1 || x > 0);
             }
             mma_commit(&sfull[it % kGroups]);
-            mma_commit(&kempty[st]);
+            mma_commit(L::kSlotted ? &tempty[slot] : &kempty[st]);
           }
           __syncwarp();
         } else {
@@ -265,7 +291,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             tc_fence_after();
             const uint32_t k = tmem + L::kColK + slot * L::kSlotCols;
             if (elect()) {
-              if constexpr (kF32) {
+              if constexpr (L::kTf32) {
                 const uint64_t qh = qd + h * (kHalf >> 4);
 #pragma unroll
                 for (int x = 0; x < 4; ++x) mma_tf32_ts(d, k + x * 8, qh + lo + x * 2, id, h + x > 0);
@@ -274,14 +300,19 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) mma_tf32_ts(d, k + x * 8, qh + x * 2, id, 1);
               } else {
+                if constexpr (kF32) {
 #pragma unroll
-                for (int t = 2; t >= 0; --t)
+                  for (int x = 0; x < 4; ++x) mma_f16_ts(d, k + 32 + x * 8, qd + x * 2, id, x > 0);
+                }
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) mma_f16_ts(d, k + x * 8, qd + t * lo + x * 2, id, t < 2 || x > 0);
+                for (int t = L::kTerms - 1; t >= 0; --t)
+#pragma unroll
+                  for (int x = 0; x < 4; ++x)
+                    mma_f16_ts(d, k + x * 8, qd + t * lo + x * 2, id, kF32 || t < L::kTerms - 1 || x > 0);
               }
               mma_commit(&tempty[slot]);
               if (h == L::kParts - 1) {
-                if constexpr (kF32) mma_tf32_ts(d, tmem + L::kColOnes, rd, id, 1);
+                if constexpr (L::kTf32) mma_tf32_ts(d, tmem + L::kColOnes, rd, id, 1);
                 else mma_f16_ts(d, tmem + L::kColOnes, rd, id, 1);
                 mma_commit(&sfull[it % kGroups]);
               }
@@ -299,7 +330,34 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
       const int st = it % kStages;
       uint8_t* const stage = smem + st * L::kStageBytes;
       if (!wait.warp(&kfull[st], (it / kStages) & 1)) break;
-      if constexpr (!kByKey) {
+      if constexpr (kF32 && kWide && !kByKey) {
+        // K's two terms, a tile of bf16 each. A thread takes 8 dims (two 16-byte words of fp32,
+        // one of bf16) of a key, a quarter-warp's 8 one after another.
+        const int slot = it % L::kSlots;
+        if (it >= L::kSlots && !wait.warp(&tempty[slot], (it / L::kSlots - 1) & 1)) break;
+        uint8_t* const to = smem + L::kSmemSlots + slot * 2 * L::kOperand;
+#pragma unroll 2
+        for (int h = 0; h < 8; ++h) {
+          const uint32_t key = (uint32_t)(ctid >> 3) + 16u * h, oct = ctid & 7;
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float4*>(x + 4 * i) =
+                *reinterpret_cast<const float4*>(stage + (oct >> 2) * kHalf + sw128(key * 128u + ((oct & 3) * 2 + i) * 16u));
+          uint32_t w0[4], w1[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], w0[i], w1[i]);
+          uint8_t* const at = to + sw128(key * 128u + oct * 16u);
+          *reinterpret_cast<uint4*>(at) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+          *reinterpret_cast<uint4*>(at + L::kOperand) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&kempty[st]);
+          mbar_arrive(&tfull[slot]);
+        }
+      } else if constexpr (!kByKey) {
         // K lo, at the same offset of the next region.
 #pragma unroll 2
         for (int h = 0; h < 4; ++h) {
@@ -326,18 +384,37 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           for (int i = 0; i < 8; ++i)
             *reinterpret_cast<float4*>(x + 4 * i) =
                 *reinterpret_cast<const float4*>(stage + h * kHalf + sw128((uint32_t)ctid * 128u + i * 16u));
-          if (h == L::kParts - 1) {
+          if (h == L::kParts - 1 && !(kF32 && kWide)) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&kempty[st]);
           }
           if (part >= L::kSlots && !(ok = wait.warp(&tempty[slot], (part / L::kSlots - 1) & 1))) break;
           tc_fence_after();
           const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + L::kColK + slot * L::kSlotCols;
-          tmem_st32(at, x);
-          if constexpr (kF32) {
+          if constexpr (kF32 && kWide) {
+            // Two bf16 terms of the 32 dims; the other half of the row follows.
+            uint32_t w0[16], w1[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = tf32_near(x[i] - tf32_hi(x[i]));
-            tmem_st32(at + 32, x);
+            for (int i = 0; i < 16; ++i) split2(x[2 * i], x[2 * i + 1], w0[i], w1[i]);
+            tmem_st16(at, w0);
+            tmem_st16(at + 32, w1);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(x + 4 * i) =
+                  *reinterpret_cast<const float4*>(stage + kHalf + sw128((uint32_t)ctid * 128u + i * 16u));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kempty[st]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) split2(x[2 * i], x[2 * i + 1], w0[i], w1[i]);
+            tmem_st16(at + 16, w0);
+            tmem_st16(at + 48, w1);
+          } else {
+            tmem_st32(at, x);
+            if constexpr (kF32) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = tf32_near(x[i] - tf32_hi(x[i]));
+              tmem_st32(at + 32, x);
+            }
           }
           tmem_wait_st();
           tc_fence_before();
@@ -372,7 +449,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           if (in) v = fetch(reinterpret_cast<const float4*>(a.q + pair * kD + g * 16 + i));
           x[i] = v.x * kTreeC, x[i + 1] = v.y * kTreeC, x[i + 2] = v.z * kTreeC, x[i + 3] = v.w * kTreeC;
         }
-        if constexpr (!kByKey && kF32) {
+        if constexpr (!kByKey && L::kTf32) {
           uint32_t w[2][16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -384,10 +461,13 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
         } else if constexpr (!kByKey) {
           uint32_t w[3][8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) split3_cut(x[2 * i], x[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+          for (int i = 0; i < 8; ++i) {
+            if (kWide) split2(x[2 * i], x[2 * i + 1], w[0][i], w[1][i]);
+            else split3_cut(x[2 * i], x[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+          }
 #pragma unroll
-          for (int t = 0; t < 3; ++t) tmem_st8(lane_tmem + L::kColQ + t * 32 + g * 8, w[t]);
-        } else if constexpr (kF32) {
+          for (int t = 0; t < L::kTerms; ++t) tmem_st8(lane_tmem + L::kColQ + t * 32 + g * 8, w[t]);
+        } else if constexpr (L::kTf32) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             uint8_t* const at = smem + L::kSmemQ + (g >> 1) * kHalf + sw128((uint32_t)row * 128u + (g & 1) * 64u + i * 4u);
@@ -400,10 +480,13 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           for (int i = 0; i < 16; i += 8) {
             uint32_t w[3][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split3_cut(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j], w[2][j]);
+            for (int j = 0; j < 4; ++j) {
+              if (kWide) split2(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j]);
+              else split3_cut(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j], w[2][j]);
+            }
             uint8_t* const at = smem + L::kSmemQ + sw128((uint32_t)row * 128u + g * 32u + i * 2u);
 #pragma unroll
-            for (int t = 0; t < 3; ++t) *reinterpret_cast<uint4*>(at + t * L::kOperand) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+            for (int t = 0; t < L::kTerms; ++t) *reinterpret_cast<uint4*>(at + t * L::kOperand) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
           }
         }
         if (kByKey && g == 0) {
@@ -421,10 +504,10 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           }
           // A row whose scores are all -inf, or none: 2^x is 0 whatever x is.
           float t[6];
-          three_terms<kF32>(sum == 0.f ? -kNothing : -top, *reinterpret_cast<float(*)[3]>(t));
-          three_terms<kF32>(sum == 0.f ? 0.f : -log2f(sum), *reinterpret_cast<float(*)[3]>(t + 3));
+          three_terms<L::kTf32>(sum == 0.f ? -kNothing : -top, *reinterpret_cast<float(*)[3]>(t));
+          three_terms<L::kTf32>(sum == 0.f ? 0.f : -log2f(sum), *reinterpret_cast<float(*)[3]>(t + 3));
           uint4 u0, u1 = make_uint4(0, 0, 0, 0);
-          if constexpr (kF32) {
+          if constexpr (L::kTf32) {
             u0 = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
             u1.x = __float_as_uint(t[4]), u1.y = __float_as_uint(t[5]);
           } else {
@@ -433,7 +516,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u)) = u0;
           *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u + 16u)) = u1;
           if (rt == rt0) {
-            constexpr uint32_t kOne = kF32 ? 0x3f800000u : 0x3f803f80u;
+            constexpr uint32_t kOne = L::kTf32 ? 0x3f800000u : 0x3f803f80u;
             const uint32_t ones[8] = {kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne};
             tmem_st8(lane_tmem + L::kColOnes, ones);
           }
@@ -553,8 +636,9 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   __syncthreads();
   tc_fence_after();
   if (*abort_flag) {
-    if (warp == L::kTmaWarp) drain_copies(kfull, kStages, *issued, a.timeout_ns);
-    else if (warp == L::kMmaWarp) drain_products(drain, a.timeout_ns);
+    if (warp >= L::kTmaWarp && warp < L::kMmaWarp)  // its copies still in flight
+      for (int i = last; i >= 0 && i > last - kStages; i -= kTmaWarps) mbar_wait(&kfull[i % kStages], (i / kStages) & 1, a.timeout_ns);
+    if (warp == L::kMmaWarp) drain_products(drain, a.timeout_ns);
     __syncthreads();
   }
   if (warp == L::kMmaWarp) tmem_dealloc(tmem, 512);
@@ -564,11 +648,22 @@ struct Device {
   bool ready = false;
   int sms = 0;
 };
-template <bool kF32, bool kByKey>
-bool set_up() {
-  return cudaFuncSetAttribute(weigh_kernel<kF32, kByKey>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)Lay<kF32, kByKey>::kSmemAlloc) == cudaSuccess;
+// A pass of the call: its kernel, threads and shared memory.
+struct Pass {
+  void (*kernel)(CUtensorMap, WeighArgs);
+  int threads;
+  uint32_t smem;
+};
+template <bool kF32, bool kWide>
+Pass pass_of(bool by_key) {
+  if (by_key) return {weigh_kernel<kF32, true, kWide>, Lay<kF32, true, kWide>::kThreads, Lay<kF32, true, kWide>::kSmemAlloc};
+  return {weigh_kernel<kF32, false, kWide>, Lay<kF32, false, kWide>::kThreads, Lay<kF32, false, kWide>::kSmemAlloc};
 }
+Pass pass_of(bool f32, bool wide, bool by_key) {
+  return f32 ? (wide ? pass_of<true, true>(by_key) : pass_of<true, false>(by_key))
+             : (wide ? pass_of<false, true>(by_key) : pass_of<false, false>(by_key));
+}
+
 int device(Device** out) {
   constexpr int kMaxDev = 64;
   static std::mutex mu;
@@ -578,8 +673,12 @@ int device(Device** out) {
   std::lock_guard<std::mutex> lock(mu);
   Device& d = devs[dev];
   if (!d.ready) {
-    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !set_up<false, false>() ||
-        !set_up<false, true>() || !set_up<true, false>() || !set_up<true, true>()) {
+    bool ok = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+    for (int i = 0; i < 8; ++i) {
+      const Pass p = pass_of(i & 1, i & 2, i & 4);
+      ok = ok && cudaFuncSetAttribute(p.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) == cudaSuccess;
+    }
+    if (!ok) {
       (void)cudaGetLastError();
       return ATTN_ECUDA;
     }
@@ -644,26 +743,25 @@ int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
   a.max_blocks = c.max_blocks;
   a.num_pages = c.num_pages;
   a.max_context = c.max_context;
+  a.row_tiles = tiles;
   a.splits = plan((long long)c.B * kHKV * tiles, keys, 1, d->sms);
   a.key_splits = plan((long long)c.B * kHKV, keys, tiles, d->sms);
   a.decay = c.decay;
   a.err = err;
   a.timeout_ns = kTimeoutNs;
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int by_key = 0; by_key < 2; ++by_key) {
+    const Pass p = pass_of(!bf16, c.max_rows >= kWideRows, by_key);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = pass ? dim3(a.key_splits, kHKV, c.B) : dim3(a.splits, kHKV * tiles, c.B);
-    cfg.blockDim = dim3(bf16 ? (pass ? Lay<false, true>::kThreads : Lay<false, false>::kThreads) : Lay<true, false>::kThreads);
-    cfg.dynamicSmemBytes = bf16 ? (pass ? Lay<false, true>::kSmemAlloc : Lay<false, false>::kSmemAlloc)
-                                : (pass ? Lay<true, true>::kSmemAlloc : Lay<true, false>::kSmemAlloc);
+    cfg.gridDim = dim3(by_key ? a.key_splits : a.splits * tiles, kHKV, c.B);
+    cfg.blockDim = dim3(p.threads);
+    cfg.dynamicSmemBytes = p.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const auto kernel = bf16 ? (pass ? weigh_kernel<false, true> : weigh_kernel<false, false>)
-                             : (pass ? weigh_kernel<true, true> : weigh_kernel<true, false>);
-    if (launched(cudaLaunchKernelEx(&cfg, kernel, mk, a)) != cudaSuccess) return ATTN_ELAUNCH;
+    if (launched(cudaLaunchKernelEx(&cfg, p.kernel, mk, a)) != cudaSuccess) return ATTN_ELAUNCH;
   }
   return ATTN_OK;
 }

@@ -21,7 +21,7 @@
 //   fp32 pages: q_lo K + q K_lo + q K, tf32 terms, in halves of 32 dims: 3 x 8 of 128 x 128 x 8
 // (K is read truncated; K_lo is the remainder rounded to tf32, q's first term rounded too.)
 //
-// Roles: four groups of four warps take the tiles in turn; four warps that write K_lo (fp32,
+// Roles: three groups of four warps take the tiles in turn; four warps that write K_lo (fp32,
 // rows) or move K to tensor memory (keys); one warp for TMA (16-token pages through the block
 // table), one to issue the products.
 #include <cuda.h>
@@ -41,7 +41,8 @@ using namespace tc;
 constexpr int kRows = 32;                  // rows of a block: 128 (row, head) pairs
 constexpr int kKeys = 128;                 // keys of a tile
 constexpr int kPages = kKeys / ATTN_PAGE;
-constexpr int kGroups = 4, kSoft = 4 * kGroups;  // warps that read S
+constexpr int kGroups = 3, kSoft = 4 * kGroups;  // warps that read S
+constexpr int kChunk = 64;                 // columns of S that a thread has in registers
 constexpr int kTmaWarps = 2;               // tiles in turn: a box of 16 rows costs its warp about 100 cycles
 constexpr uint32_t kHalf = 128 * 128;      // 128 rows of 128 bytes
 constexpr uint32_t kBox = ATTN_PAGE * 128;
@@ -332,24 +333,33 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
       if (!wait.warp(&kfull[st], (it / kStages) & 1)) break;
       if constexpr (kF32 && kWide && !kByKey) {
         // K's two terms, a tile of bf16 each. A thread takes 8 dims (two 16-byte words of fp32,
-        // one of bf16) of a key, a quarter-warp's 8 one after another.
+        // one of bf16) of a key.
         const int slot = it % L::kSlots;
         if (it >= L::kSlots && !wait.warp(&tempty[slot], (it / L::kSlots - 1) & 1)) break;
         uint8_t* const to = smem + L::kSmemSlots + slot * 2 * L::kOperand;
-#pragma unroll 2
-        for (int h = 0; h < 8; ++h) {
-          const uint32_t key = (uint32_t)(ctid >> 3) + 16u * h, oct = ctid & 7;
-          float x[8];
+        const uint32_t oct = ctid & 7, odd = oct >> 2;  // half a row apart, words of the other parity first: no bank twice
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            *reinterpret_cast<float4*>(x + 4 * i) =
-                *reinterpret_cast<const float4*>(stage + (oct >> 2) * kHalf + sw128(key * 128u + ((oct & 3) * 2 + i) * 16u));
-          uint32_t w0[4], w1[4];
+        for (int h = 0; h < 8; h += 4) {
+          float4 x[4][2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) split2(x[2 * i], x[2 * i + 1], w0[i], w1[i]);
-          uint8_t* const at = to + sw128(key * 128u + oct * 16u);
-          *reinterpret_cast<uint4*>(at) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-          *reinterpret_cast<uint4*>(at + L::kOperand) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t key = (uint32_t)(ctid >> 3) + 16u * (h + j);
+            x[j][0] = *reinterpret_cast<const float4*>(stage + odd * kHalf + sw128(key * 128u + ((oct & 3) * 2 + odd) * 16u));
+            x[j][1] = *reinterpret_cast<const float4*>(stage + odd * kHalf + sw128(key * 128u + ((oct & 3) * 2 + 1 - odd) * 16u));
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t key = (uint32_t)(ctid >> 3) + 16u * (h + j);
+            const float4 u = odd ? x[j][1] : x[j][0], v = odd ? x[j][0] : x[j][1];
+            uint4 w0, w1;
+            split2(u.x, u.y, w0.x, w1.x);
+            split2(u.z, u.w, w0.y, w1.y);
+            split2(v.x, v.y, w0.z, w1.z);
+            split2(v.z, v.w, w0.w, w1.w);
+            uint8_t* const at = to + sw128(key * 128u + oct * 16u);
+            *reinterpret_cast<uint4*>(at) = w0;
+            *reinterpret_cast<uint4*>(at + L::kOperand) = w1;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -441,12 +451,13 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
         if (meet(kMeet, false, failed, lane, &over)) break;
       }
       // q in its terms; rows past the last are zeros.
-      {
+#pragma unroll 1
+      for (int c = g; g < 2 && c < 4; c += 2) {  // 16 dims at a time, by the first two groups
         float x[16];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (in) v = fetch(reinterpret_cast<const float4*>(a.q + pair * kD + g * 16 + i));
+          if (in) v = fetch(reinterpret_cast<const float4*>(a.q + pair * kD + c * 16 + i));
           x[i] = v.x * kTreeC, x[i + 1] = v.y * kTreeC, x[i + 2] = v.z * kTreeC, x[i + 3] = v.w * kTreeC;
         }
         if constexpr (!kByKey && L::kTf32) {
@@ -457,7 +468,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             w[0][i] = __float_as_uint(h), w[1][i] = __float_as_uint(x[i] - h);
           }
 #pragma unroll
-          for (int t = 0; t < 2; ++t) tmem_st16(lane_tmem + L::kColQ + t * 64 + g * 16, w[t]);
+          for (int t = 0; t < 2; ++t) tmem_st16(lane_tmem + L::kColQ + t * 64 + c * 16, w[t]);
         } else if constexpr (!kByKey) {
           uint32_t w[3][8];
 #pragma unroll
@@ -466,11 +477,11 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             else split3_cut(x[2 * i], x[2 * i + 1], w[0][i], w[1][i], w[2][i]);
           }
 #pragma unroll
-          for (int t = 0; t < L::kTerms; ++t) tmem_st8(lane_tmem + L::kColQ + t * 32 + g * 8, w[t]);
+          for (int t = 0; t < L::kTerms; ++t) tmem_st8(lane_tmem + L::kColQ + t * 32 + c * 8, w[t]);
         } else if constexpr (L::kTf32) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
-            uint8_t* const at = smem + L::kSmemQ + (g >> 1) * kHalf + sw128((uint32_t)row * 128u + (g & 1) * 64u + i * 4u);
+            uint8_t* const at = smem + L::kSmemQ + (c >> 1) * kHalf + sw128((uint32_t)row * 128u + (c & 1) * 64u + i * 4u);
             const float4 h = make_float4(tf32_near(x[i]), tf32_near(x[i + 1]), tf32_near(x[i + 2]), tf32_near(x[i + 3]));
             *reinterpret_cast<float4*>(at) = h;
             *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x[i] - h.x, x[i + 1] - h.y, x[i + 2] - h.z, x[i + 3] - h.w);
@@ -484,51 +495,51 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
               if (kWide) split2(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j]);
               else split3_cut(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j], w[2][j]);
             }
-            uint8_t* const at = smem + L::kSmemQ + sw128((uint32_t)row * 128u + g * 32u + i * 2u);
+            uint8_t* const at = smem + L::kSmemQ + sw128((uint32_t)row * 128u + c * 32u + i * 2u);
 #pragma unroll
             for (int t = 0; t < L::kTerms; ++t) *reinterpret_cast<uint4*>(at + t * L::kOperand) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
           }
         }
-        if (kByKey && g == 0) {
-          // The row's reference and the logarithm of its sum over all keys, from the segments.
-          float top = kUnseen, sum = 0.f;
-          if (in) {
-            const float2* const st = a.stats + pair * a.splits;
-#pragma unroll 4
-            for (int i = 0; i < a.splits; ++i) top = fmaxf(top, fetch(st + i).x);
-#pragma unroll 4
-            for (int i = 0; i < a.splits; ++i) {
-              const float2 p = fetch(st + i);
-              sum = fmaf(ex2(p.x - top), p.y, sum);
-            }
-          }
-          // A row whose scores are all -inf, or none: 2^x is 0 whatever x is.
-          float t[6];
-          three_terms<L::kTf32>(sum == 0.f ? -kNothing : -top, *reinterpret_cast<float(*)[3]>(t));
-          three_terms<L::kTf32>(sum == 0.f ? 0.f : -log2f(sum), *reinterpret_cast<float(*)[3]>(t + 3));
-          uint4 u0, u1 = make_uint4(0, 0, 0, 0);
-          if constexpr (L::kTf32) {
-            u0 = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
-            u1.x = __float_as_uint(t[4]), u1.y = __float_as_uint(t[5]);
-          } else {
-            u0 = make_uint4(pack_bf16_trunc(t[0], t[1]), pack_bf16_trunc(t[2], t[3]), pack_bf16_trunc(t[4], t[5]), 0u);
-          }
-          *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u)) = u0;
-          *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u + 16u)) = u1;
-          if (rt == rt0) {
-            constexpr uint32_t kOne = L::kTf32 ? 0x3f800000u : 0x3f803f80u;
-            const uint32_t ones[8] = {kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne};
-            tmem_st8(lane_tmem + L::kColOnes, ones);
-          }
-        }
-        if (kByKey) fence_proxy_async_smem();
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qready);
       }
+              if (kByKey && g == kGroups - 1) {
+                // The row's reference and the logarithm of its sum over all keys, from the segments.
+                float top = kUnseen, sum = 0.f;
+                if (in) {
+                  const float2* const st = a.stats + pair * a.splits;
+      #pragma unroll 4
+                  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, fetch(st + i).x);
+      #pragma unroll 4
+                  for (int i = 0; i < a.splits; ++i) {
+                    const float2 p = fetch(st + i);
+                    sum = fmaf(ex2(p.x - top), p.y, sum);
+                  }
+                }
+                // A row whose scores are all -inf, or none: 2^x is 0 whatever x is.
+                float t[6];
+                three_terms<L::kTf32>(sum == 0.f ? -kNothing : -top, *reinterpret_cast<float(*)[3]>(t));
+                three_terms<L::kTf32>(sum == 0.f ? 0.f : -log2f(sum), *reinterpret_cast<float(*)[3]>(t + 3));
+                uint4 u0, u1 = make_uint4(0, 0, 0, 0);
+                if constexpr (L::kTf32) {
+                  u0 = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
+                  u1.x = __float_as_uint(t[4]), u1.y = __float_as_uint(t[5]);
+                } else {
+                  u0 = make_uint4(pack_bf16_trunc(t[0], t[1]), pack_bf16_trunc(t[2], t[3]), pack_bf16_trunc(t[4], t[5]), 0u);
+                }
+                *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u)) = u0;
+                *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u + 16u)) = u1;
+                if (rt == rt0) {
+                  constexpr uint32_t kOne = L::kTf32 ? 0x3f800000u : 0x3f803f80u;
+                  const uint32_t ones[8] = {kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne};
+                  tmem_st8(lane_tmem + L::kColOnes, ones);
+                }
+              }
+      if (kByKey) fence_proxy_async_smem();
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qready);
       const int count = tiles(rt);
-      for (int n = (g - done) & (kGroups - 1); n < count; n += kGroups) {
+      for (int n = (g + kGroups - done % kGroups) % kGroups; n < count; n += kGroups) {
         const int it = done + n, buf = it % L::kBufs, t0 = k0 + n * kKeys;
         const uint32_t s_tmem = lane_tmem + L::kColS + buf * kKeys;
         if constexpr (kByKey) {
@@ -550,22 +561,23 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           float sum0 = 0.f, sum1 = 0.f;
           const int late = t - seq.ctx - i0;  // rows before it do not see the key
 #pragma unroll
-          for (int h = 0; h < 128; h += 32) {
-            float x[32];
-            tmem_ld32(s_tmem + h, x);
+          for (int h = 0; h < 128; h += kChunk) {
+            float x[kChunk];
+#pragma unroll
+            for (int i = 0; i < kChunk; i += 32) tmem_ld32(s_tmem + h + i, *reinterpret_cast<float(*)[32]>(&x[i]));
             tmem_wait_ld();
-            if (h == 96) {
+            if (h == 128 - kChunk) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&sfree[buf]);
             }
             if (t0 + kKeys > seq.ctx + i0) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < kChunk; ++i)
                 if ((h + i) / 4 < late) x[i] = -INFINITY;
             }
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) add2(sum0, sum1, sum0, sum1, ex2(x[i]), ex2(x[i + 1]));
+            for (int i = 0; i < kChunk; i += 2) add2(sum0, sum1, sum0, sum1, ex2(x[i]), ex2(x[i + 1]));
           }
           if (w && !failed) *w = old + (sum0 + sum1);
         } else {
@@ -573,18 +585,19 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           tc_fence_after();
           const int limit = min(seq.ctx + i0 + (row >> 2) + 1, k1) - t0;  // keys of the tile that the row sees
 #pragma unroll
-          for (int h = 0; h < 128; h += 32) {
-            float x[32];
-            tmem_ld32(s_tmem + h, x);
+          for (int h = 0; h < 128; h += kChunk) {
+            float x[kChunk];
+#pragma unroll
+            for (int i = 0; i < kChunk; i += 32) tmem_ld32(s_tmem + h + i, *reinterpret_cast<float(*)[32]>(&x[i]));
             tmem_wait_ld();
-            if (h == 96) {
+            if (h == 128 - kChunk) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(&sfree[buf]);
             }
             if (t0 + kKeys > min(seq.ctx + i0, k1)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < kChunk; ++i)
                 if (h + i >= limit) x[i] = -INFINITY;
             }
             float top[4];
@@ -592,7 +605,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             for (int c = 0; c < 4; ++c) {
               top[c] = fmaxf(x[c], x[c + 4]);
 #pragma unroll
-              for (int i = 8; i < 32; i += 8) top[c] = max3(top[c], x[i + c], x[i + c + 4]);
+              for (int i = 8; i < kChunk; i += 8) top[c] = max3(top[c], x[i + c], x[i + c + 4]);
             }
             const float most = fmaxf(max3(top[0], top[1], top[2]), top[3]);
             if (most > ref + kTreeStale) {
@@ -603,7 +616,7 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             }
             const float neg = -ref;
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < kChunk; i += 2) {
               add2(x[i], x[i + 1], x[i], x[i + 1], neg, neg);
               add2(l0, l1, l0, l1, ex2(x[i]), ex2(x[i + 1]));
             }

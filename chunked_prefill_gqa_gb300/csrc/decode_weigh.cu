@@ -94,19 +94,45 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-// The weight of token t of (b, head): given the scores of its four heads and those heads'
-// log2 maxima and inverse sums.
-__device__ __forceinline__ void add_weight(const DecodeWeighArgs& a, int b, int head, int t, int weighed, float4 s,
-                                           const float* m, const float* inv) {
-  const int page = fetch(a.table + (size_t)b * a.max_blocks + t / ATTN_PAGE);
-  if (page < 0 || page >= a.num_pages) return;  // recorded where its keys were read
-  float* const w = a.weights + ((size_t)page * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;
-  const float old = a.decay != 0.f && t < weighed ? a.decay * *w : 0.f;
-  // a head whose scores are all -inf gives nothing (inv 0)
-  const float g0 = inv[0] == 0.f ? 0.f : ex2(s.x - m[0]) * inv[0], g1 = inv[1] == 0.f ? 0.f : ex2(s.y - m[1]) * inv[1];
-  const float g2 = inv[2] == 0.f ? 0.f : ex2(s.z - m[2]) * inv[2], g3 = inv[3] == 0.f ? 0.f : ex2(s.w - m[3]) * inv[3];
-  *w = old + ((g0 + g1) + (g2 + g3));
+// What a (sequence, head)'s four query heads have in common over all keys.
+struct Heads {
+  float top[kGroup], inv[kGroup];  // log2 maximum, inverse sum (0: all scores -inf, which give nothing)
+};
+__device__ __forceinline__ float given(float4 s, const Heads& x) {
+  const float g0 = x.inv[0] == 0.f ? 0.f : ex2(s.x - x.top[0]) * x.inv[0];
+  const float g1 = x.inv[1] == 0.f ? 0.f : ex2(s.y - x.top[1]) * x.inv[1];
+  const float g2 = x.inv[2] == 0.f ? 0.f : ex2(s.z - x.top[2]) * x.inv[2];
+  const float g3 = x.inv[3] == 0.f ? 0.f : ex2(s.w - x.top[3]) * x.inv[3];
+  return (g0 + g1) + (g2 + g3);
 }
+
+// Tokens t, t + kThreads, ... of (b, head), their scores, places and old weights all on their
+// way before any is used (while the segments' partials are merged).
+template <int kTokens>
+struct Tokens {
+  float4 s[kTokens];
+  float* w[kTokens];  // nullptr: no such token, or on a page that is none (recorded where its keys were read)
+  float old[kTokens];
+  __device__ __forceinline__ void load(const DecodeWeighArgs& a, const float4* scores, int b, int head, int t, int end, int weighed) {
+    int page[kTokens];
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const int at = t + i * kThreads;
+      page[i] = at < end ? fetch(a.table + (size_t)b * a.max_blocks + at / ATTN_PAGE) : -1;
+      if (at < end) s[i] = fetch(scores + at);
+    }
+#pragma unroll
+    for (int i = 0; i < kTokens; ++i) {
+      const int at = t + i * kThreads;
+      w[i] = page[i] >= 0 && page[i] < a.num_pages
+                 ? a.weights + ((size_t)page[i] * kHKV + head) * ATTN_PAGE + at % ATTN_PAGE : nullptr;
+      old[i] = w[i] && a.decay != 0.f && at < weighed ? a.decay * *w[i] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void store(const Heads& x, int i) const {
+    if (w[i]) *w[i] = old[i] + given(s[i], x);
+  }
+};
 
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -378,32 +404,44 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   *reinterpret_cast<float2*>(a.out + ((size_t)b * kHQ + head * kGroup + h) * kD + 2 * lane) = make_float2(y.x * inv, y.y * inv);
   if (lane == 0) ml[kWarps * kGroup + h] = make_float2(top, inv);
   __syncthreads();  // and the block's scores are visible to it
-  float tops[kGroup], invs[kGroup];
+  Heads heads;
 #pragma unroll
-  for (int i = 0; i < kGroup; ++i) tops[i] = ml[kWarps * kGroup + i].x, invs[i] = ml[kWarps * kGroup + i].y;
+  for (int i = 0; i < kGroup; ++i) heads.top[i] = ml[kWarps * kGroup + i].x, heads.inv[i] = ml[kWarps * kGroup + i].y;
   const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
-  for (int t = tid; t < ctx; t += kThreads) add_weight(a, b, head, t, weighed, scores[t], tops, invs);
+  for (int t = tid; t < ctx; t += 2 * kThreads) {
+    Tokens<2> x;
+    x.load(a, scores, b, head, t, ctx, weighed);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x.store(heads, i);
+  }
 }
 
-// Merges the segments of (sequence, head) and adds the weights of a stretch of its tokens.
-constexpr int kStretch = 512;
+// Merges the segments of (sequence, head): the last block of a row of the grid writes the
+// output, each of the others adds the weights of a stretch of tokens.
+constexpr int kAtOnce = 4, kStretch = kAtOnce * kThreads;
 __global__ void __launch_bounds__(kThreads) decode_weigh_merge_kernel(const DecodeWeighArgs a) {
-  __shared__ float tops[kGroup], invs[kGroup];
+  __shared__ Heads heads;
   __shared__ unsigned lost[2];
   follow();
   const int head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, h = tid >> 5;
   const int ctx = checked_ctx(a, b, false);
-  if (blockIdx.x > 0 && (long long)blockIdx.x * kStretch >= ctx) return;
+  const bool output = blockIdx.x == gridDim.x - 1;
+  if (!output && (long long)blockIdx.x * kStretch >= ctx) return;
   const float* const part = a.parts + ((size_t)b * kHKV + head) * a.splits * kPartFloats;
   // Warp h: head h, a lane two segments (at most 64 of them).
   float m[2] = {kUnseen, kUnseen}, sum[2] = {0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int s = lane + 32 * i;
-    if (s < a.splits) {
-      m[i] = fetch(part + (size_t)s * kPartFloats + kGroup * kD + h);
-      sum[i] = fetch(part + (size_t)s * kPartFloats + kGroup * kD + kGroup + h);
+  for (int i = 0; i < 2; ++i)
+    if (lane + 32 * i < a.splits) {
+      m[i] = fetch(part + (size_t)(lane + 32 * i) * kPartFloats + kGroup * kD + h);
+      sum[i] = fetch(part + (size_t)(lane + 32 * i) * kPartFloats + kGroup * kD + kGroup + h);
     }
+  const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
+  const int t0 = blockIdx.x * kStretch + tid;
+  Tokens<kAtOnce> x;
+  if (!output) x.load(a, a.scores + ((size_t)b * kHKV + head) * a.stride, b, head, t0, ctx, weighed);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
     const unsigned gone = __ballot_sync(kFull, sum[i] == kFailed);
     if (tid == 0) lost[i] = gone;  // all heads of a segment alike
     if (sum[i] == kFailed) m[i] = kUnseen, sum[i] = 0.f;
@@ -416,31 +454,32 @@ __global__ void __launch_bounds__(kThreads) decode_weigh_merge_kernel(const Deco
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) total += __shfl_xor_sync(kFull, total, off);
   const float inv = total == 0.f ? 0.f : 1.f / total;
-  if (lane == 0) tops[h] = top, invs[h] = inv;
+  if (lane == 0) heads.top[h] = top, heads.inv[h] = inv;
   __syncthreads();
   const unsigned long long gone = (unsigned long long)lost[1] << 32 | lost[0];
-  if (blockIdx.x == 0) {  // the output: two dims of head h a lane
+  if (output) {  // two dims of head h a lane
     float2 y = make_float2(0.f, 0.f);
-    for (int s = 0; s < a.splits; ++s) {
-      const float f = __shfl_sync(kFull, s < 32 ? f0 : f1, s & 31);
-      if (gone >> s & 1) continue;
-      const float2 v = fetch(reinterpret_cast<const float2*>(part + (size_t)s * kPartFloats + h * kD + 2 * lane));
-      y.x = fmaf(f, v.x, y.x);
-      y.y = fmaf(f, v.y, y.y);
+    for (int s = 0; s < a.splits; s += 8) {
+      float2 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (s + i < a.splits) v[i] = fetch(reinterpret_cast<const float2*>(part + (size_t)(s + i) * kPartFloats + h * kD + 2 * lane));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = __shfl_sync(kFull, s < 32 ? f0 : f1, (s + i) & 31);
+        if (s + i >= a.splits || (gone >> (s + i) & 1)) continue;
+        y.x = fmaf(f, v[i].x, y.x);
+        y.y = fmaf(f, v[i].y, y.y);
+      }
     }
     *reinterpret_cast<float2*>(a.out + ((size_t)b * kHQ + head * kGroup + h) * kD + 2 * lane) = make_float2(y.x * inv, y.y * inv);
+    return;
   }
-  const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
-  const float4* const scores = a.scores + ((size_t)b * kHKV + head) * a.stride;
   const int per = ((ctx + ATTN_PAGE - 1) / ATTN_PAGE + a.splits - 1) / a.splits * ATTN_PAGE;
-  float tp[kGroup], iv[kGroup];
+  const Heads all = heads;
 #pragma unroll
-  for (int i = 0; i < kGroup; ++i) tp[i] = tops[i], iv[i] = invs[i];
-#pragma unroll
-  for (int i = 0; i < kStretch / kThreads; ++i) {
-    const int t = blockIdx.x * kStretch + i * kThreads + tid;
-    if (t < ctx && !(gone >> (t / per) & 1)) add_weight(a, b, head, t, weighed, fetch(scores + t), tp, iv);
-  }
+  for (int i = 0; i < kAtOnce; ++i)
+    if (!(gone && gone >> ((t0 + i * kThreads) / per) & 1)) x.store(all, i);
 }
 
 struct Device {
@@ -531,8 +570,8 @@ int launch_decode_weigh(const DecodeWeighCall& c, unsigned* err, cudaStream_t st
   if (launched(cudaLaunchKernelEx(&cfg, bf16 ? decode_weigh_kernel<false> : decode_weigh_kernel<true>, mk, mv, a)) != cudaSuccess)
     return ATTN_ELAUNCH;
   if (a.splits > 1) {
-    const unsigned stretches = c.max_context > 0 ? (c.max_context + kStretch - 1) / kStretch : 1;
-    if (launch_following(decode_weigh_merge_kernel, dim3(stretches, kHKV, c.B), dim3(kThreads), stream, a) != cudaSuccess)
+    const unsigned stretches = (c.max_context + kStretch - 1) / kStretch;
+    if (launch_following(decode_weigh_merge_kernel, dim3(stretches + 1, kHKV, c.B), dim3(kThreads), stream, a) != cudaSuccess)
       return ATTN_ELAUNCH;
   }
   return ATTN_OK;

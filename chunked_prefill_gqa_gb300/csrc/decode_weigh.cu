@@ -3,12 +3,16 @@
 //   s_hj = q_h . k_j / 8,  p_hj = softmax_j(s_hj),  out_h = sum_j p_hj v_j
 //   W[j][g] = (decay W[j][g], or 0 for a token without a weight yet) + sum of p_hj, the 4 heads h of g
 //
-// p needs the maximum and sum over all keys, which are known at the end. So the split
-// kernel, which reads K and V once, keeps the scores (16 bytes a token and KV head, where
-// K and V are 256 or 512), and the weights are added from them afterwards: by the same
-// block where it has the whole sequence, else by the kernel that merges the segments.
+// p needs the maximum and sum over all keys, which are known at the end. So the kernel that
+// reads K and V once keeps the scores (16 bytes a token and KV head, where K and V are 256 or
+// 512), and the weights are added from them afterwards. Two forms:
+//   cluster  up to eight segments of a (sequence, KV head) are one cluster of blocks. Each
+//            keeps its scores in shared memory (up to 2560 tokens), they exchange maxima and
+//            sums through distributed shared memory, and each adds its own tokens' weights:
+//            one launch, nothing through memory but what the call is about
+//   memory   longer contexts: scores and partials in the workspace, a second kernel merges
 //
-// Split kernel: a block owns (segment, KV head, sequence), each of its four warps every
+// A block owns (segment, KV head, sequence), each of its four warps every
 // fourth 16-token page, which arrives by TMA in a ring of the warp's own; warps meet only
 // at the end. A page is exactly the 16 rows of mma.sync, keys on the M side, and the 8
 // columns of N hold the four query heads in two terms each, so a thread ends with the
@@ -37,18 +41,21 @@ constexpr int kPartFloats = kGroup * kD + 2 * kGroup;  // O of 4 heads, then the
 constexpr float kFailed = -1.f;                        // sum of a segment whose tiles never came
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint32_t kBox = ATTN_PAGE * 128;             // 16 rows of 128 bytes
+constexpr int kMaxKept = 2560;                         // tokens of a segment whose scores a block keeps
 
-template <bool kF32>
+template <bool kF32, bool kCluster>
 struct Pages {
   static constexpr uint32_t kOperand = kF32 ? 2 * kBox : kBox;  // a page of K or V of a head; fp32 in halves of 32 dims
   static constexpr uint32_t kStageBytes = 2 * kOperand;
-  static constexpr int kStages = kF32 ? 3 : 6;                  // 24 KB a warp, 192 KB on an SM of two blocks
+  static constexpr int kStages = (kF32 ? 1 : 2) * (kCluster ? 2 : 3);  // 16 or 24 KB a warp, two blocks an SM
   static constexpr uint32_t kRing = kStages * kStageBytes;
   static constexpr uint32_t kSmemAcc = kWarps * kRing;                        // [warps][4][64] floats
   static constexpr uint32_t kSmemMl = kSmemAcc + kWarps * kGroup * kD * 4;    // [warps][4] (maximum, sum), then [4] of all
-  static constexpr uint32_t kSmemBar = kSmemMl + (kWarps + 1) * kGroup * 8;
-  static constexpr uint32_t kSmemAlloc = kSmemBar + kWarps * kStages * 8 + 1024;
-  static_assert(2 * (kSmemAlloc + 1024) <= 233472, "shared memory of an SM");
+  static constexpr uint32_t kSmemOut = kSmemMl + (kWarps + 1) * kGroup * 8;   // cluster: [4][64] floats, [4] (maximum, sum)
+  static constexpr uint32_t kSmemBar = kSmemOut + (kCluster ? kGroup * kD * 4 + kGroup * 8 : 0);
+  static constexpr uint32_t kSmemScores = (kSmemBar + kWarps * kStages * 8 + 15) / 16 * 16;  // cluster: float4 a token
+  static constexpr uint32_t kSmemAlloc = kSmemScores + 1024;                  // and the scores
+  static_assert(2 * (kSmemAlloc + 1024 + (kCluster ? kMaxKept * 16 : 0)) <= 233472, "shared memory of an SM");
 };
 
 struct DecodeWeighArgs {
@@ -94,6 +101,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+// A score that waits in L2 for the second kernel, while 16 times as many bytes of K and V go
+// through (16 sequences of 16384 tokens on bf16 pages: 110 to 108 us).
+__device__ __forceinline__ void store_kept(float* p, float x, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.f32 [%0], %1, %2;" ::"l"(p), "f"(x), "l"(policy) : "memory");
+}
+
 // What a (sequence, head)'s four query heads have in common over all keys.
 struct Heads {
   float top[kGroup], inv[kGroup];  // log2 maximum, inverse sum (0: all scores -inf, which give nothing)
@@ -106,24 +119,25 @@ __device__ __forceinline__ float given(float4 s, const Heads& x) {
   return (g0 + g1) + (g2 + g3);
 }
 
-// Tokens t, t + kThreads, ... of (b, head), their scores, places and old weights all on their
-// way before any is used (while the segments' partials are merged).
+// Tokens first + t, first + t + kThreads, ... of (b, head) with their scores (of first on),
+// places and old weights, all on their way before any is used (while partial sums are merged).
 template <int kTokens>
 struct Tokens {
   float4 s[kTokens];
   float* w[kTokens];  // nullptr: no such token, or on a page that is none (recorded where its keys were read)
   float old[kTokens];
-  __device__ __forceinline__ void load(const DecodeWeighArgs& a, const float4* scores, int b, int head, int t, int end, int weighed) {
+  __device__ __forceinline__ void load(const DecodeWeighArgs& a, const float4* scores, int b, int head, int first, int t, int count,
+                                       int weighed) {
     int page[kTokens];
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
       const int at = t + i * kThreads;
-      page[i] = at < end ? fetch(a.table + (size_t)b * a.max_blocks + at / ATTN_PAGE) : -1;
-      if (at < end) s[i] = fetch(scores + at);
+      page[i] = at < count ? fetch(a.table + (size_t)b * a.max_blocks + (first + at) / ATTN_PAGE) : -1;
+      if (at < count) s[i] = fetch(scores + at);
     }
 #pragma unroll
     for (int i = 0; i < kTokens; ++i) {
-      const int at = t + i * kThreads;
+      const int at = first + t + i * kThreads;
       w[i] = page[i] >= 0 && page[i] < a.num_pages
                  ? a.weights + ((size_t)page[i] * kHKV + head) * ATTN_PAGE + at % ATTN_PAGE : nullptr;
       old[i] = w[i] && a.decay != 0.f && at < weighed ? a.decay * *w[i] : 0.f;
@@ -134,11 +148,11 @@ struct Tokens {
   }
 };
 
-template <bool kF32>
+template <bool kF32, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2)
 decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                     const DecodeWeighArgs a) {
-  using L = Pages<kF32>;
+  using L = Pages<kF32, kCluster>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
@@ -151,12 +165,16 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   __syncwarp();
   follow();
 
+  uint64_t policy = 0;
+  if (!kCluster) asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
   const int ctx = checked_ctx(a, b, s == 0 && head == 0 && tid == 0);
   const int pages = (ctx + ATTN_PAGE - 1) / ATTN_PAGE, per = (pages + a.splits - 1) / a.splits;
   const int p0 = s * per, p1 = min(p0 + per, pages);  // the segment's pages
   const int count = max(0, (p1 - p0 - warp + kWarps - 1) / kWarps);  // this warp's: p0 + warp, + 4, ...
   uint8_t* const ring = smem + warp * L::kRing;
-  float4* const scores = a.scores + ((size_t)b * kHKV + head) * a.stride;
+  // Of the segment's first token on.
+  float4* const scores = kCluster ? reinterpret_cast<float4*>(smem + L::kSmemScores)
+                                  : a.scores + ((size_t)b * kHKV + head) * a.stride + (size_t)p0 * ATTN_PAGE;
 
   // Lane l holds the table's entry of the warp's page l of a group of 32.
   const int* const trow = a.table + (size_t)b * a.max_blocks;
@@ -280,9 +298,14 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     }
     const float s0 = key0 < valid ? (x[0] + x[1]) * kTreeC : -INFINITY;
     const float s1 = key0 + 8 < valid ? (x[2] + x[3]) * kTreeC : -INFINITY;
-    float* const keep = reinterpret_cast<float*>(scores + t0 + key0) + c;
-    keep[0] = s0;
-    keep[8 * 4] = s1;
+    float* const keep = reinterpret_cast<float*>(scores + (t0 - p0 * ATTN_PAGE) + key0) + c;
+    if constexpr (kCluster) {
+      keep[0] = s0;
+      keep[8 * 4] = s1;
+    } else {
+      store_kept(keep, s0, policy);
+      store_kept(keep + 8 * 4, s1, policy);
+    }
     if (__any_sync(kFull, fmaxf(s0, s1) > ref + kTreeStale)) {
       float most = fmaxf(s0, s1);
 #pragma unroll
@@ -390,6 +413,67 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     y.x = fmaf(f, v.x, y.x);
     y.y = fmaf(f, v.y, y.y);
   }
+  const int first = p0 * ATTN_PAGE, end = min(p1 * ATTN_PAGE, ctx);  // the segment's tokens
+  const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
+  Heads heads;
+  float2* const all = ml + kWarps * kGroup;
+  if constexpr (kCluster) {
+    // Every block's sums to all: lane x of warp h looks at head h of block x.
+    float* const mine = reinterpret_cast<float*>(smem + L::kSmemOut);
+    float2* const ends = reinterpret_cast<float2*>(mine + kGroup * kD);
+    *reinterpret_cast<float2*>(mine + h * kD + 2 * lane) = y;
+    if (lane == 0) ends[h] = make_float2(top, lost ? kFailed : sum);
+    Tokens<4> x;  // its first tokens' places and weights meanwhile
+    x.load(a, scores, b, head, first, tid, end - first, weighed);
+    __syncwarp();
+    cluster_sync_all();
+    float2 p = make_float2(kUnseen, 0.f);
+    if (lane < a.splits) p = ld_cluster2(mapa_shared(smem_u32(ends + h), lane));
+    const bool none = p.y == kFailed;
+    if (none) p = make_float2(kUnseen, 0.f);
+    float m = p.x;
+#pragma unroll
+    for (int off = 1; off < kMaxCluster; off <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+    m = __shfl_sync(kFull, m, 0);
+    const float f = ex2(p.x - m);
+    float total = f * p.y;
+#pragma unroll
+    for (int off = 1; off < kMaxCluster; off <<= 1) total += __shfl_xor_sync(kFull, total, off);
+    total = __shfl_sync(kFull, total, 0);
+    const float inv = total == 0.f ? 0.f : 1.f / total;  // no key: zeros
+    // Block s writes every a.splits-th pair of dims.
+    const unsigned gone = __ballot_sync(kFull, none);
+    const bool writes = tid % a.splits == s;
+    float2 z = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) {
+      const float w = __shfl_sync(kFull, f, i);
+      if (!writes || i >= a.splits || (gone >> i & 1)) continue;
+      const float2 v = ld_cluster2(mapa_shared(smem_u32(mine + h * kD + 2 * lane), i));
+      z.x = fmaf(w, v.x, z.x);
+      z.y = fmaf(w, v.y, z.y);
+    }
+    if (writes)
+      *reinterpret_cast<float2*>(a.out + ((size_t)b * kHQ + head * kGroup + h) * kD + 2 * lane) = make_float2(z.x * inv, z.y * inv);
+    if (lane == 0) all[h] = make_float2(m, inv);
+    __syncwarp();
+    cluster_arrive();  // the others' shared memory has been read
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) heads.top[i] = all[i].x, heads.inv[i] = all[i].y;
+    if (!lost) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.store(heads, i);
+      for (int t = tid + 4 * kThreads; t < end - first; t += 4 * kThreads) {
+        x.load(a, scores, b, head, first, t, end - first, weighed);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.store(heads, i);
+      }
+    }
+    __syncwarp();
+    cluster_wait();
+    return;
+  }
   if (a.splits > 1) {
     float* const part = a.parts + (((size_t)b * kHKV + head) * a.splits + s) * kPartFloats;
     *reinterpret_cast<float2*>(part + h * kD + 2 * lane) = y;
@@ -402,32 +486,47 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   if (lost) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
   *reinterpret_cast<float2*>(a.out + ((size_t)b * kHQ + head * kGroup + h) * kD + 2 * lane) = make_float2(y.x * inv, y.y * inv);
-  if (lane == 0) ml[kWarps * kGroup + h] = make_float2(top, inv);
+  if (lane == 0) all[h] = make_float2(top, inv);
   __syncthreads();  // and the block's scores are visible to it
-  Heads heads;
 #pragma unroll
-  for (int i = 0; i < kGroup; ++i) heads.top[i] = ml[kWarps * kGroup + i].x, heads.inv[i] = ml[kWarps * kGroup + i].y;
-  const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
+  for (int i = 0; i < kGroup; ++i) heads.top[i] = all[i].x, heads.inv[i] = all[i].y;
   for (int t = tid; t < ctx; t += 2 * kThreads) {
     Tokens<2> x;
-    x.load(a, scores, b, head, t, ctx, weighed);
+    x.load(a, scores, b, head, 0, t, ctx, weighed);
 #pragma unroll
     for (int i = 0; i < 2; ++i) x.store(heads, i);
   }
 }
 
 // Merges the segments of (sequence, head): the last block of a row of the grid writes the
-// output, each of the others adds the weights of a stretch of tokens.
-constexpr int kAtOnce = 4, kStretch = kAtOnce * kThreads;
-__global__ void __launch_bounds__(kThreads) decode_weigh_merge_kernel(const DecodeWeighArgs a) {
+// output, each of the others adds the weights of a stretch of tokens, whose scores arrive as one
+// copy (held in registers they would leave an SM half of its blocks).
+constexpr int kAtOnce = 8, kStretch = kAtOnce * kThreads;
+__global__ void __launch_bounds__(kThreads, 12) decode_weigh_merge_kernel(const DecodeWeighArgs a) {
+  __shared__ __align__(16) float4 scores[kStretch];
+  __shared__ uint64_t full;
   __shared__ Heads heads;
   __shared__ unsigned lost[2];
-  follow();
   const int head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, h = tid >> 5;
+  if (tid == 0) {
+    mbar_init(&full, 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  follow();
   const int ctx = checked_ctx(a, b, false);
   const bool output = blockIdx.x == gridDim.x - 1;
-  if (!output && (long long)blockIdx.x * kStretch >= ctx) return;
+  const long long first = (long long)blockIdx.x * kStretch;
+  if (!output && first >= ctx) return;
   const float* const part = a.parts + ((size_t)b * kHKV + head) * a.splits * kPartFloats;
+  const int count = output ? 0 : (int)min((long long)kStretch, ctx - first);
+  if (!output && tid == 0) {
+    const uint32_t bytes = (count + ATTN_PAGE - 1) / ATTN_PAGE * ATTN_PAGE * (uint32_t)sizeof(float4);  // scores of whole pages are there
+    mbar_arrive_expect_tx(&full, bytes);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(scores)),
+                 "l"(a.scores + ((size_t)b * kHKV + head) * a.stride + first), "r"(bytes), "r"(smem_u32(&full))
+                 : "memory");
+  }
   // Warp h: head h, a lane two segments (at most 64 of them).
   float m[2] = {kUnseen, kUnseen}, sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -437,9 +536,20 @@ __global__ void __launch_bounds__(kThreads) decode_weigh_merge_kernel(const Deco
       sum[i] = fetch(part + (size_t)(lane + 32 * i) * kPartFloats + kGroup * kD + kGroup + h);
     }
   const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
-  const int t0 = blockIdx.x * kStretch + tid;
-  Tokens<kAtOnce> x;
-  if (!output) x.load(a, a.scores + ((size_t)b * kHKV + head) * a.stride, b, head, t0, ctx, weighed);
+  int slot[kAtOnce];   // of the weights' pool, in heads' rows of a page; negative: no such token, or no such page
+  float old[kAtOnce];
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    const int t = (int)first + i * kThreads + tid;
+    slot[i] = i * kThreads + tid < count ? fetch(a.table + (size_t)b * a.max_blocks + t / ATTN_PAGE) : -1;
+    if (slot[i] >= a.num_pages) slot[i] = -1;  // recorded where its keys were read
+  }
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    const int t = (int)first + i * kThreads + tid;
+    if (slot[i] >= 0) slot[i] = (slot[i] * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;  // 2^27 at most
+    old[i] = slot[i] >= 0 && a.decay != 0.f && t < weighed ? a.decay * a.weights[slot[i]] : 0.f;
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const unsigned gone = __ballot_sync(kFull, sum[i] == kFailed);
@@ -475,17 +585,23 @@ __global__ void __launch_bounds__(kThreads) decode_weigh_merge_kernel(const Deco
     *reinterpret_cast<float2*>(a.out + ((size_t)b * kHQ + head * kGroup + h) * kD + 2 * lane) = make_float2(y.x * inv, y.y * inv);
     return;
   }
+  if (__syncthreads_or(!mbar_wait(&full, 0, a.timeout_ns))) {  // nothing was copied: the weights stay
+    if (tid == 0) record_error(a.err, kDevErrTimeout);
+    return;
+  }
   const int per = ((ctx + ATTN_PAGE - 1) / ATTN_PAGE + a.splits - 1) / a.splits * ATTN_PAGE;
   const Heads all = heads;
 #pragma unroll
   for (int i = 0; i < kAtOnce; ++i)
-    if (!(gone && gone >> ((t0 + i * kThreads) / per) & 1)) x.store(all, i);
+    if (slot[i] >= 0 && !(gone && gone >> (((int)first + i * kThreads + tid) / per) & 1))
+      a.weights[slot[i]] = old[i] + given(scores[i * kThreads + tid], all);
 }
 
 struct Device {
   bool ready = false;
   int sms = 0;
 };
+constexpr size_t kKeptBytes = (size_t)kMaxKept * sizeof(float4);
 int device(Device** out) {
   constexpr int kMaxDev = 64;
   static std::mutex mu;
@@ -495,11 +611,14 @@ int device(Device** out) {
   std::lock_guard<std::mutex> lock(mu);
   Device& d = devs[dev];
   if (!d.ready) {
+    const auto room = [](auto kernel, size_t bytes) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+    };
     if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaFuncSetAttribute(decode_weigh_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Pages<false>::kSmemAlloc) != cudaSuccess ||
-        cudaFuncSetAttribute(decode_weigh_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)Pages<true>::kSmemAlloc) != cudaSuccess) {
+        !room(decode_weigh_kernel<false, false>, Pages<false, false>::kSmemAlloc) ||
+        !room(decode_weigh_kernel<true, false>, Pages<true, false>::kSmemAlloc) ||
+        !room(decode_weigh_kernel<false, true>, Pages<false, true>::kSmemAlloc + kKeptBytes) ||
+        !room(decode_weigh_kernel<true, true>, Pages<true, true>::kSmemAlloc + kKeptBytes)) {
       (void)cudaGetLastError();
       return ATTN_ECUDA;
     }
@@ -511,10 +630,25 @@ int device(Device** out) {
 
 long long score_stride(int max_context) { return ((long long)max_context + ATTN_PAGE - 1) / ATTN_PAGE * ATTN_PAGE; }
 
-// Segments: as decode's, two blocks on an SM.
-int plan(int B, int max_context, const Device& d) {
+// How a call is cut: as clusters where one round of two blocks an SM holds them all and a
+// segment's scores fit, of as many segments as that allows (one sequence of 1000 tokens 6.0
+// us, through memory 8.0); else as decode's segments, through memory. (More rounds of clusters
+// were slower: they hold their places until the last of them ends. 16 sequences of 16384
+// tokens on bf16 pages 132 us, 110 through memory; 48 of 1 to 4096 on fp32 pages 91 and 85.)
+struct Plan {
+  bool cluster;
+  int splits, kept;  // kept: tokens of a segment at most (cluster)
+};
+Plan plan(int B, int max_context, const Device& d) {
+  const long long pages = score_stride(max_context) / ATTN_PAGE;
+  for (int s = kMaxCluster; s >= 1; --s) {
+    const long long per = (pages + s - 1) / s;
+    if (per * ATTN_PAGE > kMaxKept) break;
+    if ((long long)B * kHKV * s > 2 * d.sms || (s > 1 && per < kWarps)) continue;  // a page a warp at least
+    return Plan{true, s, (int)per * ATTN_PAGE};
+  }
   int len = 0;
-  return decode_splits(B, max_context, 0, 2 * d.sms, &len);
+  return Plan{false, decode_splits(B, max_context, 0, 2 * d.sms, &len), 0};
 }
 
 }  // namespace
@@ -523,9 +657,10 @@ int decode_weigh_workspace_bytes(int B, int max_context, size_t* bytes) {
   Device* d = nullptr;
   const int rc = device(&d);
   if (rc != ATTN_OK) return rc;
-  const int splits = plan(B, max_context, *d);
-  *bytes = (size_t)B * kHKV * ((size_t)score_stride(max_context) * sizeof(float4) +
-                               (splits > 1 ? splits * kPartFloats * sizeof(float) : 0));
+  const Plan p = plan(B, max_context, *d);
+  *bytes = p.cluster ? 0
+                     : (size_t)B * kHKV * ((size_t)score_stride(max_context) * sizeof(float4) +
+                                           (p.splits > 1 ? p.splits * kPartFloats * sizeof(float) : 0));
   return ATTN_OK;
 }
 
@@ -539,6 +674,7 @@ int launch_decode_weigh(const DecodeWeighCall& c, unsigned* err, cudaStream_t st
   if ((rc = encode_rows_map(c.k_pages, bf16, rows, ATTN_PAGE, CU_TENSOR_MAP_SWIZZLE_128B, &mk)) != ATTN_OK ||
       (rc = encode_rows_map(c.v_pages, bf16, rows, ATTN_PAGE, CU_TENSOR_MAP_SWIZZLE_128B, &mv)) != ATTN_OK)
     return rc;
+  const Plan p = plan(c.B, c.max_context, *d);
   DecodeWeighArgs a{};
   a.q = c.q;
   a.weights = c.weights;
@@ -550,26 +686,33 @@ int launch_decode_weigh(const DecodeWeighCall& c, unsigned* err, cudaStream_t st
   a.max_blocks = c.max_blocks;
   a.num_pages = c.num_pages;
   a.max_context = c.max_context;
-  a.splits = plan(c.B, c.max_context, *d);
+  a.splits = p.splits;
   a.stride = score_stride(c.max_context);
-  a.scores = static_cast<float4*>(c.workspace);
-  a.parts = reinterpret_cast<float*>(a.scores + (size_t)c.B * kHKV * a.stride);
+  if (!p.cluster) {
+    a.scores = static_cast<float4*>(c.workspace);
+    a.parts = reinterpret_cast<float*>(a.scores + (size_t)c.B * kHKV * a.stride);
+  }
   a.decay = c.decay;
   a.err = err;
   a.timeout_ns = kTimeoutNs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.splits, kHKV, c.B);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = bf16 ? Pages<false>::kSmemAlloc : Pages<true>::kSmemAlloc;
+  cfg.dynamicSmemBytes = p.cluster ? (bf16 ? Pages<false, true>::kSmemAlloc : Pages<true, true>::kSmemAlloc) + p.kept * sizeof(float4)
+                                   : (bf16 ? Pages<false, false>::kSmemAlloc : Pages<true, false>::kSmemAlloc);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.splits;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (launched(cudaLaunchKernelEx(&cfg, bf16 ? decode_weigh_kernel<false> : decode_weigh_kernel<true>, mk, mv, a)) != cudaSuccess)
-    return ATTN_ELAUNCH;
-  if (a.splits > 1) {
+  cfg.numAttrs = p.cluster ? 2 : 1;
+  const auto kernel = p.cluster ? (bf16 ? decode_weigh_kernel<false, true> : decode_weigh_kernel<true, true>)
+                                : (bf16 ? decode_weigh_kernel<false, false> : decode_weigh_kernel<true, false>);
+  if (launched(cudaLaunchKernelEx(&cfg, kernel, mk, mv, a)) != cudaSuccess) return ATTN_ELAUNCH;
+  if (!p.cluster && a.splits > 1) {
     const unsigned stretches = (c.max_context + kStretch - 1) / kStretch;
     if (launch_following(decode_weigh_merge_kernel, dim3(stretches + 1, kHKV, c.B), dim3(kThreads), stream, a) != cudaSuccess)
       return ATTN_ELAUNCH;

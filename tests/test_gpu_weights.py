@@ -69,17 +69,18 @@ def ints(v):
 
 CONTEXTS = {
     "one": [1], "none": [0, 5, 0], "page": [15, 16, 17], "warps": [63, 64, 65, 48, 49],
-    "segment": [255, 256, 257], "uneven": [1000, 3, 517], "long": [4097], "many": [int(x) % 300 for x in
+    "segment": [255, 256, 257], "uneven": [1000, 3, 517], "long": [4097], "longer": [19999, 21, 7000], "many": [int(x) % 300 for x in
                                                                                 np.random.default_rng(2).integers(0, 10 ** 6, 70)],
 }
 
 
 @pytest.mark.parametrize("name", CONTEXTS)
 @pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("decay,bound", [(1.0, None), (0.9, 9000), (0.0, None)])
+@pytest.mark.parametrize("decay,bound", [(1.0, None), (0.9, 9000), (0.0, None), (0.9, 30000)])
 def test_decode(cp, name, bf16, decay, bound):
     lens = [(c, 0) for c in CONTEXTS[name]]
-    b = R.make_batch(lens, bf16=bf16, seed=4, extra_blocks=563 if bound else 0)
+    bound = bound and max([bound] + CONTEXTS[name])  # of the longest context at least
+    b = R.make_batch(lens, bf16=bf16, seed=4, extra_blocks=bound // 16 + 1 if bound else 0)
     weighed = [c - 1 for c, _ in lens]
     w = W.weight_pool(b, known=[max(0, n) for n in weighed]) if decay else torch.full_like(W.weight_pool(b), float("nan"))
     before = w.clone()
@@ -247,12 +248,12 @@ def test_bad_pages_and_lengths_are_recorded(cp):
 
 def test_refusals(cp):
     lens = [(100, 2), (60, 1)]
-    b, q = R.make_batch(lens, seed=13), torch.randn(3, 32, 64, device="cuda")
+    b, q = R.make_batch(lens, seed=13, extra_blocks=1900), torch.randn(3, 32, 64, device="cuda")
     w, out = W.weight_pool(b), torch.empty(2, 32, 64, device="cuda")
-    need = cp.attn_decode_weigh_workspace_bytes(2, 100)
+    need = cp.attn_decode_weigh_workspace_bytes(2, 30000)
     for ws in (None, torch.empty(need - 1, dtype=torch.uint8, device="cuda")):
         with pytest.raises(cp.AttnError) as e:
-            cp.attn_decode_weigh_paged(q[:2], b["kp"], b["vp"], w, b["table"], b["ctx"], out, 100, workspace=ws)
+            cp.attn_decode_weigh_paged(q[:2], b["kp"], b["vp"], w, b["table"], b["ctx"], out, 30000, workspace=ws)
         assert e.value.code == cp.ATTN_ESPACE
     need = cp.attn_weigh_workspace_bytes(2, 3, 2, 100)
     for ws in (None, torch.empty(need - 1, dtype=torch.uint8, device="cuda")):

@@ -513,13 +513,31 @@ __global__ void __launch_bounds__(kThreads, 12) decode_weigh_merge_kernel(const 
     fence_mbar_init();
   }
   __syncthreads();
-  follow();
+  // Before the wait for the grid that reads K and V: what that grid only reads or does not
+  // touch. It is there, because this one is launched when all blocks of that one have passed
+  // their own wait for whatever came before.
   const int ctx = checked_ctx(a, b, false);
   const bool output = blockIdx.x == gridDim.x - 1;
   const long long first = (long long)blockIdx.x * kStretch;
-  if (!output && first >= ctx) return;
+  const int count = output || first >= ctx ? 0 : (int)min((long long)kStretch, ctx - first);
+  const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
+  int slot[kAtOnce];   // of the weights' pool, in heads' rows of a page; negative: no such token, or no such page
+  float old[kAtOnce];
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    const int t = (int)first + i * kThreads + tid;
+    slot[i] = i * kThreads + tid < count ? fetch(a.table + (size_t)b * a.max_blocks + t / ATTN_PAGE) : -1;
+    if (slot[i] >= a.num_pages) slot[i] = -1;  // recorded where its keys were read
+  }
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    const int t = (int)first + i * kThreads + tid;
+    if (slot[i] >= 0) slot[i] = (slot[i] * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;  // 2^27 at most
+    old[i] = slot[i] >= 0 && a.decay != 0.f && t < weighed ? a.decay * fetch(a.weights + slot[i]) : 0.f;
+  }
+  follow();
+  if (!output && count == 0) return;
   const float* const part = a.parts + ((size_t)b * kHKV + head) * a.splits * kPartFloats;
-  const int count = output ? 0 : (int)min((long long)kStretch, ctx - first);
   if (!output && tid == 0) {
     const uint32_t bytes = (count + ATTN_PAGE - 1) / ATTN_PAGE * ATTN_PAGE * (uint32_t)sizeof(float4);  // scores of whole pages are there
     mbar_arrive_expect_tx(&full, bytes);
@@ -535,21 +553,6 @@ __global__ void __launch_bounds__(kThreads, 12) decode_weigh_merge_kernel(const 
       m[i] = fetch(part + (size_t)(lane + 32 * i) * kPartFloats + kGroup * kD + h);
       sum[i] = fetch(part + (size_t)(lane + 32 * i) * kPartFloats + kGroup * kD + kGroup + h);
     }
-  const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
-  int slot[kAtOnce];   // of the weights' pool, in heads' rows of a page; negative: no such token, or no such page
-  float old[kAtOnce];
-#pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) {
-    const int t = (int)first + i * kThreads + tid;
-    slot[i] = i * kThreads + tid < count ? fetch(a.table + (size_t)b * a.max_blocks + t / ATTN_PAGE) : -1;
-    if (slot[i] >= a.num_pages) slot[i] = -1;  // recorded where its keys were read
-  }
-#pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) {
-    const int t = (int)first + i * kThreads + tid;
-    if (slot[i] >= 0) slot[i] = (slot[i] * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;  // 2^27 at most
-    old[i] = slot[i] >= 0 && a.decay != 0.f && t < weighed ? a.decay * a.weights[slot[i]] : 0.f;
-  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const unsigned gone = __ballot_sync(kFull, sum[i] == kFailed);

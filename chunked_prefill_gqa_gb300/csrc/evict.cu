@@ -36,7 +36,8 @@ struct EvictArgs {
   void *k_pages, *v_pages;
   float* weights;             // [num_pages][8][16]
   const int *table, *ctx_lens, *keep_lens;
-  int *counts, *holes, *movers;  // [B][8]; [B][8][cap] each
+  int2* counts;               // [B][8]: pairs of a hole and its mover (-1: nothing to do); those whose mover lies below new
+  int *holes, *movers;        // [B][8][cap] each: slots of the pool, page * 16 + slot
   int B, max_blocks, num_pages, max_context, first, last, cap, cached;
   unsigned* err;
 };
@@ -69,7 +70,7 @@ struct Shared {
   uint32_t hist[2][kBins];
   uint32_t warp_sums[kWarps];
   uint32_t warp_gt[kWarps], warp_eq[kWarps];
-  uint32_t totals[4];  // this block's: above, equal, and both below edge
+  uint32_t totals[6];  // this block's keys above and equal to the m-th: all, below edge, below new
   uint32_t bin, need;
   int bad;
 };
@@ -80,18 +81,34 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, int rank) {
   return v;
 }
 
+// One more of a digit for every lane that has one; the same digit in the whole warp (weights
+// of zero, above all) counts at once.
+__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit, bool in, int lane) {
+  const unsigned some = __ballot_sync(kFull, in);
+  if (!some) return;
+  const uint32_t one = __shfl_sync(kFull, digit, __ffs(some) - 1);
+  if (__ballot_sync(kFull, in && digit == one) == some) {
+    if (lane == 0) atomicAdd(hist + one, __popc(some));
+  } else if (in) {
+    atomicAdd(hist + digit, 1u);
+  }
+}
+
+// Four tokens' keys, a quarter of a page, are looked at together.
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
-  extern __shared__ uint32_t cache[];
+  extern __shared__ __align__(16) uint32_t cache[];
   __shared__ Shared sh;
-  follow();
   const int rank = blockIdx.x, ranks = gridDim.x, head = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
+  if (tid == 0) sh.bad = 0;
+  follow();
   const Cut cut = load_cut(a, b);
-  int* const count = a.counts + b * kHKV + head;
+  int2* const count = a.counts + b * kHKV + head;
   if (!cut.live) {  // for every block of the cluster
     if (rank == 0 && tid == 0) {
       if (!cut.ok) record_error(a.err, kDevErrBounds);
-      *count = -1;
+      *count = make_int2(-1, 0);
     }
     return;
   }
@@ -99,22 +116,44 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   // This block's tokens: whole pages, the sequence's own length cut evenly.
   const int span = ((cut.ctx + ATTN_PAGE - 1) / ATTN_PAGE + ranks - 1) / ranks * ATTN_PAGE;
   const int t0 = min((long long)rank * span, (long long)cut.ctx), t1 = min((long long)t0 + span, (long long)cut.ctx);
-  if (tid == 0) sh.bad = 0;
-  for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
-  __syncthreads();
-  auto key_of = [&](int t) -> uint32_t {
-    const int page = fetch(trow + t / ATTN_PAGE);
-    if (page < 0 || page >= a.num_pages) {
-      sh.bad = 1;
-      return 0;
-    }
-    return ordered(fetch(a.weights + ((size_t)page * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE));
-  };
-  if (a.cached)
-    for (int t = t0 + tid; t < t1; t += kThreads) cache[t - t0] = key_of(t);
-  const auto key_at = [&](int t) -> uint32_t { return a.cached ? cache[t - t0] : key_of(t); };
-  const int lo = max(t0, a.first), hi = min(t1, cut.end);  // the middle's part of them
+  const int quads = (t1 - t0 + 3) / 4;
+  const int lo = max(t0, a.first), hi = min(t1, cut.end);  // the middle's part of the tokens
   const uint32_t m = cut.now - a.first - a.last;
+  __syncthreads();
+  const auto page_of = [&](int quad) {
+    const int page = fetch(trow + (t0 + 4 * quad) / ATTN_PAGE);
+    if (page >= 0 && page < a.num_pages) return page;
+    sh.bad = 1;
+    return -1;
+  };
+  const auto keys_at = [&](int quad, int page) {  // slots past the last token of a page may hold anything
+    if (page < 0) return make_uint4(0, 0, 0, 0);
+    const float4 w = fetch(reinterpret_cast<const float4*>(a.weights + ((size_t)page * kHKV + head) * ATTN_PAGE) + (t0 / 4 + quad) % 4);
+    return make_uint4(ordered(w.x), ordered(w.y), ordered(w.z), ordered(w.w));
+  };
+  const auto quad_at = [&](int quad) -> uint4 {
+    return a.cached ? reinterpret_cast<const uint4*>(cache)[quad] : keys_at(quad, page_of(quad));
+  };
+  const auto inside = [&](int t) { return t >= lo && t < hi; };
+  // All keys once, with the first digit's histogram; several quads' lookups on their way at once.
+  constexpr int kAhead = 4;
+  for (int q0 = warp * 32; q0 < quads; q0 += kAhead * kThreads) {
+    int page[kAhead];
+    uint4 key[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) page[i] = q0 + i * kThreads + lane < quads ? page_of(q0 + i * kThreads + lane) : -1;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) key[i] = keys_at(q0 + i * kThreads + lane, page[i]);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int q = q0 + i * kThreads + lane, t = t0 + 4 * q;
+      if (q - lane >= quads) break;
+      if (a.cached && q < quads) reinterpret_cast<uint4*>(cache)[q] = key[i];
+      const uint32_t k[4] = {key[i].x, key[i].y, key[i].z, key[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) count_digit(sh.hist[0], k[j] >> 21, q < quads && inside(t + j), lane);
+    }
+  }
 
   // The m-th largest key, digit by digit from the top.
   uint32_t prefix = 0, need = m;
@@ -124,23 +163,14 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     const int bits = pass == 2 ? 10 : 11, above = shift;
     shift -= bits;
     uint32_t* const hist = sh.hist[pass & 1];
-    __syncthreads();
-    for (int t = lo + tid; t - lane < hi; t += kThreads) {
-      uint32_t key = 0;
-      bool in = t < hi;
-      if (in) {
-        key = key_at(t);
-        in = pass == 0 || key >> above == prefix;
-      }
-      const uint32_t digit = key >> shift & ((1u << bits) - 1);
-      // Equal digits of a whole warp (weights of zero, above all) count at once.
-      const unsigned some = __ballot_sync(kFull, in);
-      if (!some) continue;
-      const uint32_t one = __shfl_sync(kFull, digit, __ffs(some) - 1);
-      if (__ballot_sync(kFull, in && digit == one) == some) {
-        if (lane == 0) atomicAdd(hist + one, __popc(some));
-      } else if (in) {
-        atomicAdd(hist + digit, 1u);
+    if (pass > 0) {
+      __syncthreads();
+      for (int q = tid; q - lane < quads; q += kThreads) {
+        const uint4 key = q < quads ? quad_at(q) : make_uint4(0, 0, 0, 0);
+        const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          count_digit(hist, k[j] >> shift & ((1u << bits) - 1), q < quads && inside(t0 + 4 * q + j) && k[j] >> above == prefix, lane);
       }
     }
     if (ranks > 1) tc::cluster_sync_all();
@@ -148,13 +178,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     // Thread i owns bins kBins - 1 - 4 i and the three below: counts from the top.
     uint32_t n[kPerThread], sum = 0;
 #pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      const uint32_t* at = hist + (kBins - 1 - (tid * kPerThread + j));
-      n[j] = ranks > 1 ? 0 : *at;
-      if (ranks > 1)
-        for (int r = 0; r < ranks; ++r) n[j] += ld_cluster(at, r);
-      sum += n[j];
-    }
+    for (int j = 0; j < kPerThread; ++j) n[j] = ranks > 1 ? 0 : hist[kBins - 1 - (tid * kPerThread + j)];
+    for (int r = 0; ranks > 1 && r < ranks; ++r)
+#pragma unroll
+      for (int j = 0; j < kPerThread; ++j) n[j] += ld_cluster(hist + (kBins - 1 - (tid * kPerThread + j)), r);
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) sum += n[j];
     uint32_t up = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -165,7 +194,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     for (int i = tid; i < kBins; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;  // read by nobody since the last meeting
     __syncthreads();
     uint32_t before = up - sum;
-    for (int w = 0; w < warp; ++w) before += sh.warp_sums[w];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) before += w < warp ? sh.warp_sums[w] : 0;
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) {
       if (before < need && need <= before + n[j]) {
@@ -181,34 +211,36 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   // Stays: key > top, or one of the first `need` equal to it.
   const uint32_t top = m > 0 ? prefix : kFull;
 
-  // A warp's tokens are consecutive, so that ranks follow from counts.
-  const int per = ((max(hi - lo, 0) + kWarps - 1) / kWarps + 31) / 32 * 32;
-  const int w0 = lo + warp * per, w1 = min(w0 + per, hi);
-  uint32_t gt = 0, eq = 0, gt_in = 0, eq_in = 0;
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const uint32_t key = t < w1 ? key_at(t) : 0;
-    const bool g = t < w1 && key > top, e = t < w1 && key == top;
-    gt += __popc(__ballot_sync(kFull, g));
-    eq += __popc(__ballot_sync(kFull, e));
-    gt_in += __popc(__ballot_sync(kFull, g && t < cut.edge));
-    eq_in += __popc(__ballot_sync(kFull, e && t < cut.edge));
+  // A warp's quads are consecutive, so that ranks follow from counts.
+  const int per = (quads + 32 * kWarps - 1) / (32 * kWarps) * 32;
+  const int w0 = min(warp * per, quads), w1 = min(w0 + per, quads);
+  uint32_t c[6] = {};
+  for (int q = w0 + lane; q < w1; q += 32) {
+    const uint4 key = quad_at(q);
+    const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = t0 + 4 * q + j;
+      const uint32_t g = inside(t) && k[j] > top, e = inside(t) && k[j] == top;
+      c[0] += g, c[1] += e;
+      if (t < cut.edge) c[2] += g, c[3] += e;
+      if (t < cut.now) c[4] += g, c[5] += e;
+    }
   }
-  if (!a.cached)  // the pages of what stays in any case count too
-    for (int t = t0 + tid; t < t1; t += kThreads)
-      if (t < lo || t >= hi) key_of(t);
-  if (tid < 4) sh.totals[tid] = 0;
+  if (tid < 6) sh.totals[tid] = 0;
   __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 6; ++i) c[i] = __reduce_add_sync(kFull, c[i]);
   if (lane == 0) {
-    sh.warp_gt[warp] = gt;
-    sh.warp_eq[warp] = eq;
-    atomicAdd(sh.totals + 0, gt);
-    atomicAdd(sh.totals + 1, eq);
-    atomicAdd(sh.totals + 2, gt_in);
-    atomicAdd(sh.totals + 3, eq_in);
+    sh.warp_gt[warp] = c[0];
+    sh.warp_eq[warp] = c[1];
   }
+#pragma unroll
+  for (int i = 0; i < 6; ++i)
+    if (lane == i) atomicAdd(sh.totals + i, c[i]);
   if (ranks > 1) tc::cluster_sync_all();
   else __syncthreads();
-  uint32_t gt_before = 0, eq_before = 0, in_gt = 0, in_eq = 0;
+  uint32_t gt_before = 0, eq_before = 0, in_gt = 0, in_eq = 0, now_gt = 0, now_eq = 0;
   int bad = 0;
   for (int r = 0; r < ranks; ++r) {
     if (r < rank) {
@@ -217,34 +249,61 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     }
     in_gt += ld_cluster(sh.totals + 2, r);
     in_eq += ld_cluster(sh.totals + 3, r);
+    now_gt += ld_cluster(sh.totals + 4, r);
+    now_eq += ld_cluster(sh.totals + 5, r);
     bad |= (int)ld_cluster(reinterpret_cast<const uint32_t*>(&sh.bad), r);
   }
-  if (ranks > 1) tc::cluster_sync_all();  // nobody's shared memory is read past here
-  if (bad) {  // of every block of every head of the sequence
-    if (rank == 0 && tid == 0) {
-      record_error(a.err, kDevErrBounds);
-      *count = -1;
-    }
-    return;
+  if (ranks > 1) {
+    __syncwarp();
+    tc::cluster_arrive();  // nobody's shared memory is read past here
   }
   const uint32_t kept_in = in_gt + min(in_eq, need);  // middle tokens that stay below edge
-  if (rank == 0 && tid == 0) *count = (int)(m - kept_in);
-  for (int w = 0; w < warp; ++w) gt_before += sh.warp_gt[w], eq_before += sh.warp_eq[w];
-  const size_t base = ((size_t)b * kHKV + head) * a.cap;
-  const unsigned below = (1u << lane) - 1;
-  for (int t = w0 + lane; t - lane < w1; t += 32) {
-    const uint32_t key = t < w1 ? key_at(t) : 0;
-    const bool g = t < w1 && key > top, e = t < w1 && key == top;
-    const unsigned gs = __ballot_sync(kFull, g), es = __ballot_sync(kFull, e);
-    const uint32_t g_rank = gt_before + __popc(gs & below), e_rank = eq_before + __popc(es & below);
-    if (t < w1) {
-      const uint32_t kept_before = g_rank + min(e_rank, need);
-      const bool stays = g || (e && e_rank < need);
-      if (t < cut.edge && !stays) a.holes[base + (t - a.first) - kept_before] = t;
-      if (t >= cut.edge && stays) a.movers[base + kept_before - kept_in] = t;
+  if (rank == 0 && tid == 0) {
+    if (bad) record_error(a.err, kDevErrBounds);
+    *count = bad ? make_int2(-1, 0) : make_int2((int)(m - kept_in), (int)(now_gt + min(now_eq, need) - kept_in));
+  }
+  if (!bad) {  // else of every block of every head of the sequence
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) gt_before += w < warp ? sh.warp_gt[w] : 0, eq_before += w < warp ? sh.warp_eq[w] : 0;
+    const size_t base = ((size_t)b * kHKV + head) * a.cap;
+    for (int q = w0 + lane; q - lane < w1; q += 32) {
+      const uint4 key = q < w1 ? quad_at(q) : make_uint4(0, 0, 0, 0);
+      const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+      uint32_t g[4], e[4], own = 0;  // own: keys above in the upper half, equal ones in the lower
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = q < w1 && inside(t0 + 4 * q + j);
+        g[j] = in && k[j] > top, e[j] = in && k[j] == top;
+        own += g[j] << 16 | e[j];
+      }
+      uint32_t up = own;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t x = __shfl_up_sync(kFull, up, off);
+        if (lane >= off) up += x;
+      }
+      const uint32_t all = __shfl_sync(kFull, up, 31);
+      uint32_t g_rank = gt_before + ((up - own) >> 16), e_rank = eq_before + ((up - own) & 0xffffu);
+      const int page = q < w1 ? fetch(trow + (t0 + 4 * q) / ATTN_PAGE) : 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = t0 + 4 * q + j, slot = page * ATTN_PAGE + t % ATTN_PAGE;
+        if (q < w1 && inside(t)) {
+          const uint32_t kept_before = g_rank + min(e_rank, need);
+          const bool stays = g[j] || (e[j] && e_rank < need);
+          if (t < cut.edge && !stays) a.holes[base + (t - a.first) - kept_before] = slot;
+          if (t >= cut.edge && stays) a.movers[base + kept_before - kept_in] = slot;
+        }
+        g_rank += g[j];
+        e_rank += e[j];
+      }
+      gt_before += all >> 16;
+      eq_before += all & 0xffffu;
     }
-    gt_before += __popc(gs);
-    eq_before += __popc(es);
+  }
+  if (ranks > 1) {
+    __syncwarp();
+    tc::cluster_wait();
   }
 }
 
@@ -254,33 +313,31 @@ constexpr int kMoveThreads = 128, kMoveWarps = kMoveThreads / 32;
 // kVecs: 16-byte words of a head's row (8 or 16).
 template <int kVecs>
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
-  follow();
+  // Lengths and table are there before the selection that this follows has ended: that grid
+  // has waited for whatever came before.
   const int head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
-  const int pairs = fetch(a.counts + b * kHKV + head);
-  if (pairs < 0) return;
   const Cut cut = load_cut(a, b);
   const int* const trow = a.table + (size_t)b * a.max_blocks;
+  follow();
+  const int2 counts = fetch(a.counts + b * kHKV + head);
+  const int pairs = counts.x, near = counts.y;
+  if (pairs < 0) return;
   const size_t base = ((size_t)b * kHKV + head) * a.cap;
   uint4* const kp = static_cast<uint4*>(a.k_pages);
   uint4* const vp = static_cast<uint4*>(a.v_pages);
-  // The row of the pool, in heads' rows, that holds token t of this head; and its weight.
-  const auto row_of = [&](int t) { return (fetch(trow + t / ATTN_PAGE) * ATTN_PAGE + t % ATTN_PAGE) * kHKV + head; };
-  const auto weight_of = [&](int t) {
-    return a.weights + ((size_t)fetch(trow + t / ATTN_PAGE) * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;
-  };
-  // A warp moves 32 pairs: a lane looks one up, then the rows go several at once.
+  const auto slot_of = [&](int t) { return fetch(trow + t / ATTN_PAGE) * ATTN_PAGE + t % ATTN_PAGE; };
+  // A slot's row of this head, in rows of heads; and its weight.
+  const auto row_of = [&](int slot) { return (size_t)slot * kHKV + head; };
+  const auto weight_of = [&](int slot) { return a.weights + ((size_t)(slot / ATTN_PAGE) * kHKV + head) * ATTN_PAGE + slot % ATTN_PAGE; };
+  // A warp moves the pairs i .. i + 31 below end: a lane looks one up, then the rows go several at once.
   constexpr int kAtOnce = 32 / kVecs;  // rows of one pool that a warp's load covers
-  const auto fill = [&](int i, bool near) {
+  const auto fill = [&](int i, int end) {
     int src = 0, dst = 0;
-    bool in = i + lane < pairs;
+    const bool in = i + lane < end;
     if (in) {
-      const int from = fetch(a.movers + base + i + lane);
-      in = (from < cut.now) == near;
-      if (in) {
-        const int to = fetch(a.holes + base + i + lane);
-        src = row_of(from), dst = row_of(to);
-        *weight_of(to) = *weight_of(from);
-      }
+      src = fetch(a.movers + base + i + lane);
+      dst = fetch(a.holes + base + i + lane);
+      *weight_of(dst) = *weight_of(src);
     }
     const unsigned some = __ballot_sync(kFull, in);
     if (!some) return;
@@ -293,8 +350,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
         const int q = p + u * kAtOnce + lane / kVecs;
         const int s = __shfl_sync(kFull, src, q);
         if (some >> q & 1) {
-          x[u] = kp[(size_t)s * kVecs + lane % kVecs];
-          y[u] = vp[(size_t)s * kVecs + lane % kVecs];
+          x[u] = kp[row_of(s) * kVecs + lane % kVecs];
+          y[u] = vp[row_of(s) * kVecs + lane % kVecs];
         }
       }
 #pragma unroll
@@ -302,42 +359,43 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
         const int q = p + u * kAtOnce + lane / kVecs;
         const int d = __shfl_sync(kFull, dst, q);
         if (some >> q & 1) {
-          kp[(size_t)d * kVecs + lane % kVecs] = x[u];
-          vp[(size_t)d * kVecs + lane % kVecs] = y[u];
+          kp[row_of(d) * kVecs + lane % kVecs] = x[u];
+          vp[row_of(d) * kVecs + lane % kVecs] = y[u];
         }
       }
     }
   };
   if (blockIdx.x > 0) {
-    for (int i = ((blockIdx.x - 1) * kMoveWarps + (tid >> 5)) * 32; i < pairs; i += (gridDim.x - 1) * kMoveThreads) fill(i, false);
+    for (int i = near + ((blockIdx.x - 1) * kMoveWarps + (tid >> 5)) * 32; i < pairs; i += (gridDim.x - 1) * kMoveThreads)
+      fill(i, pairs);
     return;
   }
   // What leaves the places of the last ones, then those: in rising batches, each read
   // before it is written (a source is never below its destination).
-  for (int i = (tid >> 5) * 32; i < pairs && i <= a.last; i += kMoveThreads) fill(i, true);
+  for (int i = (tid >> 5) * 32; i < near; i += kMoveThreads) fill(i, near);
   const int shift = cut.ctx - cut.now;
   constexpr int kRows = 4 * kMoveThreads / kVecs;  // of a batch
   for (int i0 = 0; i0 < a.last; i0 += kRows) {
     uint4 x[4], y[4];
     float w = 0.f;
     const bool weigh = tid < kRows && i0 + tid < a.last;
-    if (weigh) w = *weight_of(cut.edge + shift + i0 + tid);
+    if (weigh) w = *weight_of(slot_of(cut.edge + shift + i0 + tid));
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + (tid + u * kMoveThreads) / kVecs;
       if (i < a.last) {
-        const size_t s = (size_t)row_of(cut.edge + shift + i) * kVecs + tid % kVecs;
+        const size_t s = row_of(slot_of(cut.edge + shift + i)) * kVecs + tid % kVecs;
         x[u] = kp[s];
         y[u] = vp[s];
       }
     }
     __syncthreads();
-    if (weigh) *weight_of(cut.edge + i0 + tid) = w;
+    if (weigh) *weight_of(slot_of(cut.edge + i0 + tid)) = w;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int i = i0 + (tid + u * kMoveThreads) / kVecs;
       if (i < a.last) {
-        const size_t d = (size_t)row_of(cut.edge + i) * kVecs + tid % kVecs;
+        const size_t d = row_of(slot_of(cut.edge + i)) * kVecs + tid % kVecs;
         kp[d] = x[u];
         vp[d] = y[u];
       }
@@ -351,7 +409,7 @@ int list_cap(int max_context) { return max_context / 2 + 1; }
 }  // namespace
 
 size_t evict_workspace_bytes(int B, int max_context) {
-  return ((size_t)B * kHKV * sizeof(int) + 15) / 16 * 16 + 2 * (size_t)B * kHKV * list_cap(max_context) * sizeof(int);
+  return (size_t)B * kHKV * sizeof(int2) + 2 * (size_t)B * kHKV * list_cap(max_context) * sizeof(int);
 }
 
 cudaError_t launch_evict(const EvictCall& c, int sms, unsigned* err, cudaStream_t stream) {
@@ -369,8 +427,8 @@ cudaError_t launch_evict(const EvictCall& c, int sms, unsigned* err, cudaStream_
   a.first = c.first;
   a.last = c.last;
   a.cap = list_cap(c.max_context);
-  a.counts = static_cast<int*>(c.workspace);
-  a.holes = a.counts + ((size_t)c.B * kHKV + 3) / 4 * 4;
+  a.counts = static_cast<int2*>(c.workspace);
+  a.holes = reinterpret_cast<int*>(a.counts + (size_t)c.B * kHKV);
   a.movers = a.holes + (size_t)c.B * kHKV * a.cap;
   a.err = err;
 

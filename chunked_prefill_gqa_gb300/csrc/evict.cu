@@ -30,7 +30,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kPerThread = kBins / kThreads;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxCached = 40960;  // tokens of a block whose keys stay in shared memory (160 KB)
+constexpr int kMaxCached = 40960;  // tokens of a block whose keys stay in shared memory (160 KB of its 227)
 
 struct EvictArgs {
   void *k_pages, *v_pages;
@@ -66,12 +66,16 @@ __device__ __forceinline__ uint32_t ordered(float w) {
   return w != w ? 0u : u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+constexpr int kListed = 2048;  // keys of the first digit's bin that a block keeps apart
+
 struct Shared {
   uint32_t hist[2][kBins];
+  uint32_t keys[kListed], places[kListed];  // and their tokens, from the block's first on
+  uint32_t listed;
   uint32_t warp_sums[kWarps];
   uint32_t warp_gt[kWarps], warp_eq[kWarps];
   uint32_t totals[6];  // this block's keys above and equal to the m-th: all, below edge, below new
-  uint32_t bin, need;
+  uint32_t bin, need, whole;
   int bad;
 };
 
@@ -81,27 +85,16 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, int rank) {
   return v;
 }
 
-// One more of a digit for every lane that has one; the same digit in the whole warp (weights
-// of zero, above all) counts at once.
-__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit, bool in, int lane) {
-  const unsigned some = __ballot_sync(kFull, in);
-  if (!some) return;
-  const uint32_t one = __shfl_sync(kFull, digit, __ffs(some) - 1);
-  if (__ballot_sync(kFull, in && digit == one) == some) {
-    if (lane == 0) atomicAdd(hist + one, __popc(some));
-  } else if (in) {
-    atomicAdd(hist + digit, 1u);
-  }
-}
-
-// Four tokens' keys, a quarter of a page, are looked at together.
+// Four tokens' keys, a quarter of a page, are looked at together. (16 sequences of 16384 tokens:
+// XXX us; 32 with every digit counted over all keys, 250 instructions for each 32 of them.)
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   extern __shared__ __align__(16) uint32_t cache[];
   __shared__ Shared sh;
   const int rank = blockIdx.x, ranks = gridDim.x, head = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
-  if (tid == 0) sh.bad = 0;
+  if (tid < 6) sh.totals[tid] = 0;
+  if (tid == 0) sh.bad = 0, sh.listed = 0;
   follow();
   const Cut cut = load_cut(a, b);
   int2* const count = a.counts + b * kHKV + head;
@@ -136,43 +129,31 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   };
   const auto inside = [&](int t) { return t >= lo && t < hi; };
   // All keys once, with the first digit's histogram; several quads' lookups on their way at once.
-  constexpr int kAhead = 4;
-  for (int q0 = warp * 32; q0 < quads; q0 += kAhead * kThreads) {
+  constexpr int kAhead = 4, kFirst = 21;  // the first digit: 11 bits from there up
+  for (int q0 = tid; q0 < quads; q0 += kAhead * kThreads) {
     int page[kAhead];
     uint4 key[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) page[i] = q0 + i * kThreads + lane < quads ? page_of(q0 + i * kThreads + lane) : -1;
+    for (int i = 0; i < kAhead; ++i) page[i] = q0 + i * kThreads < quads ? page_of(q0 + i * kThreads) : -1;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) key[i] = keys_at(q0 + i * kThreads + lane, page[i]);
+    for (int i = 0; i < kAhead; ++i) key[i] = keys_at(q0 + i * kThreads, page[i]);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int q = q0 + i * kThreads + lane, t = t0 + 4 * q;
-      if (q - lane >= quads) break;
-      if (a.cached && q < quads) reinterpret_cast<uint4*>(cache)[q] = key[i];
+      const int q = q0 + i * kThreads, t = t0 + 4 * q;
+      if (q >= quads) break;
+      if (a.cached) reinterpret_cast<uint4*>(cache)[q] = key[i];
       const uint32_t k[4] = {key[i].x, key[i].y, key[i].z, key[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) count_digit(sh.hist[0], k[j] >> 21, q < quads && inside(t + j), lane);
+      for (int j = 0; j < 4; ++j)
+        if (inside(t + j)) atomicAdd(sh.hist[0] + (k[j] >> kFirst), 1u);
     }
   }
 
-  // The m-th largest key, digit by digit from the top.
-  uint32_t prefix = 0, need = m;
-  int shift = 32;
-#pragma unroll 1
-  for (int pass = 0; pass < 3 && m > 0; ++pass) {
-    const int bits = pass == 2 ? 10 : 11, above = shift;
-    shift -= bits;
+  // The bin of a digit that holds the cluster's need-th key from the top, how many of the bin's
+  // are needed, and whether that is all of them. Zeroes the other histogram, which nobody has
+  // read since the last meeting.
+  const auto choose = [&](int pass, uint32_t need) {
     uint32_t* const hist = sh.hist[pass & 1];
-    if (pass > 0) {
-      __syncthreads();
-      for (int q = tid; q - lane < quads; q += kThreads) {
-        const uint4 key = q < quads ? quad_at(q) : make_uint4(0, 0, 0, 0);
-        const uint32_t k[4] = {key.x, key.y, key.z, key.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          count_digit(hist, k[j] >> shift & ((1u << bits) - 1), q < quads && inside(t0 + 4 * q + j) && k[j] >> above == prefix, lane);
-      }
-    }
     if (ranks > 1) tc::cluster_sync_all();
     else __syncthreads();
     // Thread i owns bins kBins - 1 - 4 i and the three below: counts from the top.
@@ -191,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
       if (lane >= off) up += x;
     }
     if (lane == 31) sh.warp_sums[warp] = up;
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;  // read by nobody since the last meeting
+    for (int i = tid; i < kBins; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;
     __syncthreads();
     uint32_t before = up - sum;
 #pragma unroll
@@ -201,43 +182,107 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
       if (before < need && need <= before + n[j]) {
         sh.bin = kBins - 1 - (tid * kPerThread + j);
         sh.need = need - before;
+        sh.whole = need == before + n[j];
       }
       before += n[j];
     }
     __syncthreads();
-    prefix = prefix << bits | sh.bin;
-    need = sh.need;
-  }
-  // Stays: key > top, or one of the first `need` equal to it.
-  const uint32_t top = m > 0 ? prefix : kFull;
+  };
 
-  // A warp's quads are consecutive, so that ranks follow from counts.
+  // Stays: key > top, or one of the first `need` equal to it. A warp's quads are consecutive, so
+  // that ranks follow from counts.
+  uint32_t top = kFull, need = 0;
   const int per = (quads + 32 * kWarps - 1) / (32 * kWarps) * 32;
   const int w0 = min(warp * per, quads), w1 = min(w0 + per, quads);
-  uint32_t c[6] = {};
-  for (int q = w0 + lane; q < w1; q += 32) {
-    const uint4 key = quad_at(q);
-    const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+  uint32_t c[6] = {};  // as totals, of this thread
+  const auto tally = [&](uint32_t g, uint32_t e, int t) {
+    c[0] += g, c[1] += e;
+    if (t < cut.edge) c[2] += g, c[3] += e;
+    if (t < cut.now) c[4] += g, c[5] += e;
+  };
+  bool listed = false;
+  if (m > 0) {
+    choose(0, m);
+    uint32_t prefix = sh.bin;
+    need = sh.need;
+    // Keys above the bin are counted, those in it (a few in a hundred) listed: the other
+    // digits and what goes by them look at the list alone, if it holds them all.
+    for (int q = w0 + lane; q < w1; q += 32) {
+      const uint4 key = quad_at(q);
+      const uint32_t k[4] = {key.x, key.y, key.z, key.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = t0 + 4 * q + j;
-      const uint32_t g = inside(t) && k[j] > top, e = inside(t) && k[j] == top;
-      c[0] += g, c[1] += e;
-      if (t < cut.edge) c[2] += g, c[3] += e;
-      if (t < cut.now) c[4] += g, c[5] += e;
+      for (int j = 0; j < 4; ++j) {
+        const int t = t0 + 4 * q + j;
+        if (!inside(t) || k[j] >> kFirst < prefix) continue;
+        if (k[j] >> kFirst > prefix) {
+          tally(1, 0, t);
+        } else {
+          const uint32_t at = atomicAdd(&sh.listed, 1u);
+          if (at < kListed) sh.keys[at] = k[j], sh.places[at] = t - t0;
+        }
+      }
+    }
+    uint32_t gt = __reduce_add_sync(kFull, c[0]);
+    if (lane == 0) sh.warp_gt[warp] = gt, sh.warp_eq[warp] = 0;
+    bool whole = sh.whole;
+    __syncthreads();
+    listed = sh.listed <= kListed;
+    const int entries = sh.listed;
+    int shift = kFirst;
+#pragma unroll 1
+    for (int pass = 1; pass < 3 && !whole; ++pass) {
+      const int bits = pass == 2 ? 10 : 11, above = shift;
+      shift -= bits;
+      const auto count_digit = [&](uint32_t key) {
+        if (key >> above == prefix) atomicAdd(sh.hist[pass & 1] + (key >> shift & ((1u << bits) - 1)), 1u);
+      };
+      if (listed) {
+        for (int i = tid; i < entries; i += kThreads) count_digit(sh.keys[i]);
+      } else {
+        for (int q = tid; q < quads; q += kThreads) {
+          const uint4 key = quad_at(q);
+          const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (inside(t0 + 4 * q + j)) count_digit(k[j]);
+        }
+      }
+      choose(pass, need);
+      prefix = prefix << bits | sh.bin;
+      need = sh.need;
+      whole = sh.whole;
+    }
+    // Where all of the last bin stay (never all tokens: prefix is not 0 then) any above its border do.
+    top = prefix << shift;
+    if (whole) --top, need = 0;
+    if (listed) {
+      for (int i = tid; i < entries; i += kThreads) {
+        const int place = sh.places[i];
+        const uint32_t g = sh.keys[i] > top, e = sh.keys[i] == top;
+        tally(g, e, t0 + place);
+        if (g) atomicAdd(&sh.warp_gt[place / 4 / per], 1u);
+        if (e) atomicAdd(&sh.warp_eq[place / 4 / per], 1u);
+      }
     }
   }
-  if (tid < 6) sh.totals[tid] = 0;
-  __syncthreads();
+  if (!listed) {
 #pragma unroll
-  for (int i = 0; i < 6; ++i) c[i] = __reduce_add_sync(kFull, c[i]);
-  if (lane == 0) {
-    sh.warp_gt[warp] = c[0];
-    sh.warp_eq[warp] = c[1];
+    for (int i = 0; i < 6; ++i) c[i] = 0;
+    for (int q = w0 + lane; q < w1; q += 32) {
+      const uint4 key = quad_at(q);
+      const uint32_t k[4] = {key.x, key.y, key.z, key.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (inside(t0 + 4 * q + j)) tally(k[j] > top, k[j] == top, t0 + 4 * q + j);
+    }
+    const uint32_t gt = __reduce_add_sync(kFull, c[0]), eq = __reduce_add_sync(kFull, c[1]);
+    if (lane == 0) sh.warp_gt[warp] = gt, sh.warp_eq[warp] = eq;
   }
 #pragma unroll
-  for (int i = 0; i < 6; ++i)
-    if (lane == i) atomicAdd(sh.totals + i, c[i]);
+  for (int i = 0; i < 6; ++i) {
+    const uint32_t sum = __reduce_add_sync(kFull, c[i]);
+    if (lane == i && sum) atomicAdd(sh.totals + i, sum);
+  }
   if (ranks > 1) tc::cluster_sync_all();
   else __syncthreads();
   uint32_t gt_before = 0, eq_before = 0, in_gt = 0, in_eq = 0, now_gt = 0, now_eq = 0;
@@ -441,7 +486,7 @@ cudaError_t launch_evict(const EvictCall& c, int sms, unsigned* err, cudaStream_
   const int span = ((c.max_context + ATTN_PAGE - 1) / ATTN_PAGE + ranks - 1) / ranks * ATTN_PAGE;
   a.cached = span <= kMaxCached;
   const size_t smem = a.cached ? (size_t)span * sizeof(uint32_t) : 0;
-  if (smem > 24576) {  // past 48 KB with the block's own
+  if (smem > 8192) {  // past 48 KB with the block's own
     const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
     if (e != cudaSuccess) return launched(e);
   }

@@ -752,9 +752,7 @@ int evict_paged(const EvictCall& c, size_t workspaceBytes, cudaStream_t stream) 
   if ((rc = current_device(&st)) != ATTN_OK) return rc;
   if (!c.workspace || workspaceBytes < evict_workspace_bytes(c.B, c.max_context)) return ATTN_ESPACE;
   if (!aligned16(c.workspace)) return ATTN_EALIGN;
-  int sms = 0;
-  if ((rc = sm_count(&sms)) != ATTN_OK) return rc;
-  return from_cuda(launch_evict(c, sms, st->err, stream));
+  return launch_evict(c, st->err, stream);
 }
 
 }  // namespace

@@ -206,7 +206,7 @@ struct EvictCall {
   int B, max_blocks, num_pages, max_context, first, last;
 };
 size_t evict_workspace_bytes(int B, int max_context);
-cudaError_t launch_evict(const EvictCall& c, int sms, unsigned* err, cudaStream_t stream);
+int launch_evict(const EvictCall& c, unsigned* err, cudaStream_t stream);
 
 // Tensor-pipe rate measurement (peak.cu): `ctas` CTAs each issue `iters`
 // dense M = 128, N = n MMAs (kind::tf32, or kind::f16 with bf16 operands).

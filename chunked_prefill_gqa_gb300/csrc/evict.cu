@@ -12,13 +12,14 @@
 // 4 rows a head instead of n / 2 kept in order.
 //
 // Two launches. select_kernel: a cluster of blocks per (sequence, head) finds the m-th
-// largest weight by its digits (11, 11 and 10 bits of the weights mapped to ordered
+// largest weight by its digits (12, 10 and 10 bits of the weights mapped to ordered
 // integers, a histogram in shared memory, the cluster's added up through distributed
 // shared memory), then walks its tokens once more and writes both lists. move_kernel moves
 // the rows: sources at or past new are written by nobody, so those go in any order; what
 // lies between edge and new is read (as sources of holes) before one block per (sequence,
 // head) writes the last ones there, batch by batch.
 #include <cstdint>
+#include <mutex>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -27,10 +28,11 @@ namespace attn {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = 2048, kPerThread = kBins / kThreads;
+// Digits of 12, 10 and 10 bits: with three bits of the fraction in the first one, the weights of
+// a warp (within a few powers of two) seldom meet in a bin (XXX).
+constexpr int kBins = 4096, kFirst = 20, kDigit = 10;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxCached = 40960;  // tokens of a block whose keys stay in shared memory (160 KB of its 227)
+constexpr int kMaxCached = 40960;  // tokens of a block whose keys stay in shared memory (160 KB of its 227; the rest takes 50)
 
 struct EvictArgs {
   void *k_pages, *v_pages;
@@ -68,7 +70,9 @@ __device__ __forceinline__ uint32_t ordered(float w) {
 
 constexpr int kListed = 2048;  // keys of the first digit's bin that a block keeps apart
 
-struct Shared {
+template <int kThreads>
+struct alignas(16) Shared {  // the keys follow
+  static constexpr int kWarps = kThreads / 32;
   uint32_t hist[2][kBins];
   uint32_t keys[kListed], places[kListed];  // and their tokens, from the block's first on
   uint32_t listed;
@@ -85,11 +89,17 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, int rank) {
   return v;
 }
 
+// The lowest n of a quad's four bits.
+__device__ __forceinline__ uint32_t lowest(int n) { return (1u << min(max(n, 0), 4)) - 1; }
+
 // Four tokens' keys, a quarter of a page, are looked at together. (16 sequences of 16384 tokens:
 // XXX us; 32 with every digit counted over all keys, 250 instructions for each 32 of them.)
+template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
-  extern __shared__ __align__(16) uint32_t cache[];
-  __shared__ Shared sh;
+  constexpr int kWarps = kThreads / 32, kPerThread = kBins / kThreads;
+  extern __shared__ __align__(16) uint8_t select_smem[];
+  Shared<kThreads>& sh = *reinterpret_cast<Shared<kThreads>*>(select_smem);
+  uint4* const cache = reinterpret_cast<uint4*>(select_smem + sizeof(Shared<kThreads>));  // the keys, if they fit
   const int rank = blockIdx.x, ranks = gridDim.x, head = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
@@ -125,11 +135,17 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     return make_uint4(ordered(w.x), ordered(w.y), ordered(w.z), ordered(w.w));
   };
   const auto quad_at = [&](int quad) -> uint4 {
-    return a.cached ? reinterpret_cast<const uint4*>(cache)[quad] : keys_at(quad, page_of(quad));
+    return a.cached ? cache[quad] : keys_at(quad, page_of(quad));
   };
-  const auto inside = [&](int t) { return t >= lo && t < hi; };
+  const auto middle = [&](int t) { return lowest(hi - t) & ~lowest(lo - t); };  // of a quad's tokens
+  // Of a quad, the keys above and equal to a border.
+  const auto above_equal = [&](uint4 k, int t, uint32_t border, uint32_t* g, uint32_t* e) {
+    const uint32_t in = middle(t);
+    *g = in & ((uint32_t)(k.x > border) | (uint32_t)(k.y > border) << 1 | (uint32_t)(k.z > border) << 2 | (uint32_t)(k.w > border) << 3);
+    *e = in & ((uint32_t)(k.x == border) | (uint32_t)(k.y == border) << 1 | (uint32_t)(k.z == border) << 2 | (uint32_t)(k.w == border) << 3);
+  };
   // All keys once, with the first digit's histogram; several quads' lookups on their way at once.
-  constexpr int kAhead = 4, kFirst = 21;  // the first digit: 11 bits from there up
+  constexpr int kAhead = 4;
   for (int q0 = tid; q0 < quads; q0 += kAhead * kThreads) {
     int page[kAhead];
     uint4 key[kAhead];
@@ -141,11 +157,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     for (int i = 0; i < kAhead; ++i) {
       const int q = q0 + i * kThreads, t = t0 + 4 * q;
       if (q >= quads) break;
-      if (a.cached) reinterpret_cast<uint4*>(cache)[q] = key[i];
-      const uint32_t k[4] = {key[i].x, key[i].y, key[i].z, key[i].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (inside(t + j)) atomicAdd(sh.hist[0] + (k[j] >> kFirst), 1u);
+      if (a.cached) cache[q] = key[i];
+      const uint32_t in = middle(t);
+      if (in & 1) atomicAdd(sh.hist[0] + (key[i].x >> kFirst), 1u);
+      if (in & 2) atomicAdd(sh.hist[0] + (key[i].y >> kFirst), 1u);
+      if (in & 4) atomicAdd(sh.hist[0] + (key[i].z >> kFirst), 1u);
+      if (in & 8) atomicAdd(sh.hist[0] + (key[i].w >> kFirst), 1u);
     }
   }
 
@@ -156,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     uint32_t* const hist = sh.hist[pass & 1];
     if (ranks > 1) tc::cluster_sync_all();
     else __syncthreads();
-    // Thread i owns bins kBins - 1 - 4 i and the three below: counts from the top.
+    // Thread i owns kPerThread bins from kBins - 1 - kPerThread i down: counts from the top.
     uint32_t n[kPerThread], sum = 0;
 #pragma unroll
     for (int j = 0; j < kPerThread; ++j) n[j] = ranks > 1 ? 0 : hist[kBins - 1 - (tid * kPerThread + j)];
@@ -195,10 +212,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   const int per = (quads + 32 * kWarps - 1) / (32 * kWarps) * 32;
   const int w0 = min(warp * per, quads), w1 = min(w0 + per, quads);
   uint32_t c[6] = {};  // as totals, of this thread
-  const auto tally = [&](uint32_t g, uint32_t e, int t) {
-    c[0] += g, c[1] += e;
-    if (t < cut.edge) c[2] += g, c[3] += e;
-    if (t < cut.now) c[4] += g, c[5] += e;
+  const auto tally = [&](uint32_t g, uint32_t e, int t) {  // bits of tokens t .. t + 3
+    const uint32_t in = lowest(cut.edge - t), now = lowest(cut.now - t);
+    c[0] += __popc(g), c[1] += __popc(e);
+    c[2] += __popc(g & in), c[3] += __popc(e & in);
+    c[4] += __popc(g & now), c[5] += __popc(e & now);
   };
   bool listed = false;
   if (m > 0) {
@@ -209,17 +227,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     // digits and what goes by them look at the list alone, if it holds them all.
     for (int q = w0 + lane; q < w1; q += 32) {
       const uint4 key = quad_at(q);
-      const uint32_t k[4] = {key.x, key.y, key.z, key.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = t0 + 4 * q + j;
-        if (!inside(t) || k[j] >> kFirst < prefix) continue;
-        if (k[j] >> kFirst > prefix) {
-          tally(1, 0, t);
-        } else {
-          const uint32_t at = atomicAdd(&sh.listed, 1u);
-          if (at < kListed) sh.keys[at] = k[j], sh.places[at] = t - t0;
-        }
+      const int t = t0 + 4 * q;
+      uint32_t g, e;
+      above_equal(make_uint4(key.x >> kFirst, key.y >> kFirst, key.z >> kFirst, key.w >> kFirst), t, prefix, &g, &e);
+      tally(g, 0, t);
+      while (e) {
+        const int j = __ffs(e) - 1;
+        e &= e - 1;
+        const uint32_t at = atomicAdd(&sh.listed, 1u);
+        if (at < kListed) sh.keys[at] = j == 0 ? key.x : j == 1 ? key.y : j == 2 ? key.z : key.w, sh.places[at] = t + j - t0;
       }
     }
     uint32_t gt = __reduce_add_sync(kFull, c[0]);
@@ -231,24 +247,25 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     int shift = kFirst;
 #pragma unroll 1
     for (int pass = 1; pass < 3 && !whole; ++pass) {
-      const int bits = pass == 2 ? 10 : 11, above = shift;
-      shift -= bits;
-      const auto count_digit = [&](uint32_t key) {
-        if (key >> above == prefix) atomicAdd(sh.hist[pass & 1] + (key >> shift & ((1u << bits) - 1)), 1u);
+      const int above = shift;
+      shift -= kDigit;
+      const auto count_digit = [&](uint32_t key, bool in) {
+        if (in && key >> above == prefix) atomicAdd(sh.hist[pass & 1] + (key >> shift & ((1u << kDigit) - 1)), 1u);
       };
       if (listed) {
-        for (int i = tid; i < entries; i += kThreads) count_digit(sh.keys[i]);
+        for (int i = tid; i < entries; i += kThreads) count_digit(sh.keys[i], true);
       } else {
         for (int q = tid; q < quads; q += kThreads) {
           const uint4 key = quad_at(q);
-          const uint32_t k[4] = {key.x, key.y, key.z, key.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (inside(t0 + 4 * q + j)) count_digit(k[j]);
+          const uint32_t in = middle(t0 + 4 * q);
+          count_digit(key.x, in & 1);
+          count_digit(key.y, in & 2);
+          count_digit(key.z, in & 4);
+          count_digit(key.w, in & 8);
         }
       }
       choose(pass, need);
-      prefix = prefix << bits | sh.bin;
+      prefix = prefix << kDigit | sh.bin;
       need = sh.need;
       whole = sh.whole;
     }
@@ -269,11 +286,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
 #pragma unroll
     for (int i = 0; i < 6; ++i) c[i] = 0;
     for (int q = w0 + lane; q < w1; q += 32) {
-      const uint4 key = quad_at(q);
-      const uint32_t k[4] = {key.x, key.y, key.z, key.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (inside(t0 + 4 * q + j)) tally(k[j] > top, k[j] == top, t0 + 4 * q + j);
+      uint32_t g, e;
+      above_equal(quad_at(q), t0 + 4 * q, top, &g, &e);
+      tally(g, e, t0 + 4 * q);
     }
     const uint32_t gt = __reduce_add_sync(kFull, c[0]), eq = __reduce_add_sync(kFull, c[1]);
     if (lane == 0) sh.warp_gt[warp] = gt, sh.warp_eq[warp] = eq;
@@ -311,16 +326,16 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) gt_before += w < warp ? sh.warp_gt[w] : 0, eq_before += w < warp ? sh.warp_eq[w] : 0;
     const size_t base = ((size_t)b * kHKV + head) * a.cap;
+    int page = w0 + lane < w1 ? fetch(trow + (t0 + 4 * (w0 + lane)) / ATTN_PAGE) : 0;
     for (int q = w0 + lane; q - lane < w1; q += 32) {
-      const uint4 key = q < w1 ? quad_at(q) : make_uint4(0, 0, 0, 0);
-      const uint32_t k[4] = {key.x, key.y, key.z, key.w};
-      uint32_t g[4], e[4], own = 0;  // own: keys above in the upper half, equal ones in the lower
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = q < w1 && inside(t0 + 4 * q + j);
-        g[j] = in && k[j] > top, e[j] = in && k[j] == top;
-        own += g[j] << 16 | e[j];
+      const int t = t0 + 4 * q, slot = page * ATTN_PAGE + t % ATTN_PAGE;
+      if (q + 32 < w1) page = fetch(trow + (t + 128) / ATTN_PAGE);
+      uint32_t g = 0, e = 0, in = 0;
+      if (q < w1) {
+        above_equal(quad_at(q), t, top, &g, &e);
+        in = middle(t);
       }
+      const uint32_t own = __popc(g) << 16 | __popc(e);  // keys above in the upper half, equal ones in the lower
       uint32_t up = own;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -328,19 +343,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
         if (lane >= off) up += x;
       }
       const uint32_t all = __shfl_sync(kFull, up, 31);
-      uint32_t g_rank = gt_before + ((up - own) >> 16), e_rank = eq_before + ((up - own) & 0xffffu);
-      const int page = q < w1 ? fetch(trow + (t0 + 4 * q) / ATTN_PAGE) : 0;
+      const uint32_t g_rank = gt_before + ((up - own) >> 16), e_rank = eq_before + ((up - own) & 0xffffu);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int t = t0 + 4 * q + j, slot = page * ATTN_PAGE + t % ATTN_PAGE;
-        if (q < w1 && inside(t)) {
-          const uint32_t kept_before = g_rank + min(e_rank, need);
-          const bool stays = g[j] || (e[j] && e_rank < need);
-          if (t < cut.edge && !stays) a.holes[base + (t - a.first) - kept_before] = slot;
-          if (t >= cut.edge && stays) a.movers[base + kept_before - kept_in] = slot;
-        }
-        g_rank += g[j];
-        e_rank += e[j];
+        if (!(in >> j & 1)) continue;
+        const uint32_t eq = e_rank + __popc(e & ((1u << j) - 1));
+        const uint32_t kept_before = g_rank + __popc(g & ((1u << j) - 1)) + min(eq, need);
+        const bool stays = (g >> j & 1) || ((e >> j & 1) && eq < need);
+        if (t + j < cut.edge && !stays) a.holes[base + (t + j - a.first) - kept_before] = slot + j;
+        if (t + j >= cut.edge && stays) a.movers[base + kept_before - kept_in] = slot + j;
       }
       gt_before += all >> 16;
       eq_before += all & 0xffffu;
@@ -449,6 +460,33 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
   }
 }
 
+static_assert(sizeof(Shared<512>) % 16 == 0 && sizeof(Shared<1024>) % 16 == 0, "the keys start on 16 bytes");
+static_assert(sizeof(Shared<1024>) + (size_t)kMaxCached * sizeof(uint32_t) <= 232448, "exceeds the 227 KB per-block shared memory limit");
+
+// Once per device: the shared-memory opt-in, and how many SMs there are.
+int device(int* sms) {
+  constexpr int kMaxDev = 64;
+  static std::mutex mu;
+  static int devs[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return ATTN_ECUDA;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!devs[dev]) {
+    int n = 0;
+    const auto room = [](auto kernel) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) == cudaSuccess;
+    };
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !room(select_kernel<512>) ||
+        !room(select_kernel<1024>)) {
+      (void)cudaGetLastError();
+      return ATTN_ECUDA;
+    }
+    devs[dev] = n;
+  }
+  *sms = devs[dev];
+  return ATTN_OK;
+}
+
 int list_cap(int max_context) { return max_context / 2 + 1; }
 
 }  // namespace
@@ -457,7 +495,10 @@ size_t evict_workspace_bytes(int B, int max_context) {
   return (size_t)B * kHKV * sizeof(int2) + 2 * (size_t)B * kHKV * list_cap(max_context) * sizeof(int);
 }
 
-cudaError_t launch_evict(const EvictCall& c, int sms, unsigned* err, cudaStream_t stream) {
+int launch_evict(const EvictCall& c, unsigned* err, cudaStream_t stream) {
+  int sms = 0;
+  const int rc = device(&sms);
+  if (rc != ATTN_OK) return rc;
   EvictArgs a{};
   a.k_pages = c.k_pages;
   a.v_pages = c.v_pages;
@@ -477,22 +518,21 @@ cudaError_t launch_evict(const EvictCall& c, int sms, unsigned* err, cudaStream_
   a.movers = a.holes + (size_t)c.B * kHKV * a.cap;
   a.err = err;
 
-  // Blocks of a cluster: as many as have a place on two blocks an SM, with 1024 tokens each
-  // at least; and so many that a block's keys fit its shared memory, if they can.
+  // Blocks of a cluster: as many as have an SM each, with 1024 tokens at least; and so many that a block's keys fit its shared memory, if they can.
   int ranks = 1;
-  while (ranks < kMaxCluster && ((long long)c.B * kHKV * 2 * ranks <= 2 * sms ? c.max_context / (2 * ranks) >= 1024
+  while (ranks < kMaxCluster && ((long long)c.B * kHKV * 2 * ranks <= sms ? c.max_context / (2 * ranks) >= 1024
                                                                               : c.max_context / ranks > kMaxCached))
     ranks *= 2;
   const int span = ((c.max_context + ATTN_PAGE - 1) / ATTN_PAGE + ranks - 1) / ranks * ATTN_PAGE;
   a.cached = span <= kMaxCached;
-  const size_t smem = a.cached ? (size_t)span * sizeof(uint32_t) : 0;
-  if (smem > 8192) {  // past 48 KB with the block's own
-    const cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxCached * 4);
-    if (e != cudaSuccess) return launched(e);
-  }
+  // Threads by a block's tokens: few wait less for each other (1000 tokens: 512 threads XXX us,
+  // 1024 XXX), many have more under way (16384 tokens: XXX and XXX).
+  const bool wide = span > 4096;
+  const auto kernel = wide ? select_kernel<1024> : select_kernel<512>;
+  const size_t smem = (wide ? sizeof(Shared<1024>) : sizeof(Shared<512>)) + (a.cached ? (size_t)span * sizeof(uint32_t) : 0);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks, kHKV, c.B);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(wide ? 1024 : 512);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -503,14 +543,14 @@ cudaError_t launch_evict(const EvictCall& c, int sms, unsigned* err, cudaStream_
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  const cudaError_t e = launched(cudaLaunchKernelEx(&cfg, select_kernel, a));
-  if (e != cudaSuccess) return e;
+  if (launched(cudaLaunchKernelEx(&cfg, kernel, a)) != cudaSuccess) return ATTN_ELAUNCH;
   // Blocks for the pairs: one for 128 of them, at most 32 resident rounds of all SMs.
   const long long most = 32LL * 16 * sms / ((long long)c.B * kHKV);
   long long blocks = (a.cap + kMoveThreads - 1) / kMoveThreads;
   if (blocks > most) blocks = most < 1 ? 1 : most;
   const dim3 grid((unsigned)blocks + 1, kHKV, c.B);
-  return launch_following(c.type == ATTN_BF16 ? move_kernel<8> : move_kernel<16>, grid, dim3(kMoveThreads), stream, a);
+  return launch_following(c.type == ATTN_BF16 ? move_kernel<8> : move_kernel<16>, grid, dim3(kMoveThreads), stream, a) == cudaSuccess
+             ? ATTN_OK : ATTN_ELAUNCH;
 }
 
 }  // namespace attn

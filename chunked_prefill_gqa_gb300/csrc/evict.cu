@@ -92,6 +92,10 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, int rank) {
 // The lowest n of a quad's four bits.
 __device__ __forceinline__ uint32_t lowest(int n) { return (1u << min(max(n, 0), 4)) - 1; }
 
+// Of four bits, how many are set up to each, in a byte each (the last one: in all). POPC would
+// take four times as long.
+__device__ __forceinline__ uint32_t running(uint32_t bits) { return ((bits * 0x00204081u) & 0x01010101u) * 0x01010101u; }
+
 // Four tokens' keys, a quarter of a page, are looked at together. (16 sequences of 16384 tokens:
 // XXX us; 32 with every digit counted over all keys, 250 instructions for each 32 of them.)
 template <int kThreads>
@@ -212,11 +216,11 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   const int per = (quads + 32 * kWarps - 1) / (32 * kWarps) * 32;
   const int w0 = min(warp * per, quads), w1 = min(w0 + per, quads);
   uint32_t c[6] = {};  // as totals, of this thread
-  const auto tally = [&](uint32_t g, uint32_t e, int t) {  // bits of tokens t .. t + 3
-    const uint32_t in = lowest(cut.edge - t), now = lowest(cut.now - t);
-    c[0] += __popc(g), c[1] += __popc(e);
-    c[2] += __popc(g & in), c[3] += __popc(e & in);
-    c[4] += __popc(g & now), c[5] += __popc(e & now);
+  const auto tally = [&](int i, uint32_t bits, int t) {  // of tokens t .. t + 3, to c[i], c[i + 2] and c[i + 4]
+    const uint32_t n = running(bits) >> 24;
+    c[i] += n;
+    c[i + 2] += t + 4 <= cut.edge ? n : t >= cut.edge ? 0 : running(bits & lowest(cut.edge - t)) >> 24;
+    c[i + 4] += t + 4 <= cut.now ? n : t >= cut.now ? 0 : running(bits & lowest(cut.now - t)) >> 24;
   };
   bool listed = false;
   if (m > 0) {
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
       const int t = t0 + 4 * q;
       uint32_t g, e;
       above_equal(make_uint4(key.x >> kFirst, key.y >> kFirst, key.z >> kFirst, key.w >> kFirst), t, prefix, &g, &e);
-      tally(g, 0, t);
+      tally(0, g, t);
       while (e) {
         const int j = __ffs(e) - 1;
         e &= e - 1;
@@ -276,7 +280,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
       for (int i = tid; i < entries; i += kThreads) {
         const int place = sh.places[i];
         const uint32_t g = sh.keys[i] > top, e = sh.keys[i] == top;
-        tally(g, e, t0 + place);
+        tally(0, g, t0 + place);
+        tally(1, e, t0 + place);
         if (g) atomicAdd(&sh.warp_gt[place / 4 / per], 1u);
         if (e) atomicAdd(&sh.warp_eq[place / 4 / per], 1u);
       }
@@ -288,7 +293,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     for (int q = w0 + lane; q < w1; q += 32) {
       uint32_t g, e;
       above_equal(quad_at(q), t0 + 4 * q, top, &g, &e);
-      tally(g, e, t0 + 4 * q);
+      tally(0, g, t0 + 4 * q);
+      tally(1, e, t0 + 4 * q);
     }
     const uint32_t gt = __reduce_add_sync(kFull, c[0]), eq = __reduce_add_sync(kFull, c[1]);
     if (lane == 0) sh.warp_gt[warp] = gt, sh.warp_eq[warp] = eq;
@@ -335,7 +341,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
         above_equal(quad_at(q), t, top, &g, &e);
         in = middle(t);
       }
-      const uint32_t own = __popc(g) << 16 | __popc(e);  // keys above in the upper half, equal ones in the lower
+      // Keys above in the upper half, equal ones (few, as a rule none) in the lower.
+      const uint32_t eqs = running(e), own = (running(g) >> 24) << 16 | eqs >> 24;
       uint32_t up = own;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -344,14 +351,20 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
       }
       const uint32_t all = __shfl_sync(kFull, up, 31);
       const uint32_t g_rank = gt_before + ((up - own) >> 16), e_rank = eq_before + ((up - own) & 0xffffu);
+      uint32_t stays = g;
+      if (e)  // the first `need` of them
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if ((e >> j & 1) && e_rank + (eqs >> 8 * j & 255u) <= need) stays |= 1u << j;
+      const uint32_t kept_before = g_rank + min(e_rank, need), kept = running(stays) << 8;  // up to each token, without it
+      const uint32_t ahead = lowest(cut.edge - t), out = in & ~stays & ahead, move = stays & ~ahead;
+      int* const hole = a.holes + base + (t - a.first) - (int)kept_before;
+      int* const mover = a.movers + base + (int)(kept_before - kept_in);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (!(in >> j & 1)) continue;
-        const uint32_t eq = e_rank + __popc(e & ((1u << j) - 1));
-        const uint32_t kept_before = g_rank + __popc(g & ((1u << j) - 1)) + min(eq, need);
-        const bool stays = (g >> j & 1) || ((e >> j & 1) && eq < need);
-        if (t + j < cut.edge && !stays) a.holes[base + (t + j - a.first) - kept_before] = slot + j;
-        if (t + j >= cut.edge && stays) a.movers[base + kept_before - kept_in] = slot + j;
+        const int n = kept >> 8 * j & 255u;
+        if (out >> j & 1) hole[j - n] = slot + j;
+        if (move >> j & 1) mover[n] = slot + j;
       }
       gt_before += all >> 16;
       eq_before += all & 0xffffu;

@@ -750,8 +750,11 @@ int evict_paged(const EvictCall& c, size_t workspaceBytes, cudaStream_t stream) 
     return ATTN_EALIGN;
   DeviceState* st = nullptr;
   if ((rc = current_device(&st)) != ATTN_OK) return rc;
-  if (!c.workspace || workspaceBytes < evict_workspace_bytes(c.B, c.max_context)) return ATTN_ESPACE;
-  if (!aligned16(c.workspace)) return ATTN_EALIGN;
+  const size_t need = evict_workspace_bytes(c.B, c.max_context);
+  if (need > 0) {
+    if (!c.workspace || workspaceBytes < need) return ATTN_ESPACE;
+    if (!aligned16(c.workspace)) return ATTN_EALIGN;
+  }
   return launch_evict(c, st->err, stream);
 }
 

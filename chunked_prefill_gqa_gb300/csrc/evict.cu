@@ -96,6 +96,49 @@ __device__ __forceinline__ uint32_t lowest(int n) { return (1u << min(max(n, 0),
 // take four times as long.
 __device__ __forceinline__ uint32_t running(uint32_t bits) { return ((bits * 0x00204081u) & 0x01010101u) * 0x01010101u; }
 
+// The bin of a digit that holds the cluster's need-th key from the top, how many of the bin's
+// are needed, and whether that is all of them. Zeroes the other histogram, which nobody has
+// read since the last meeting.
+template <int kThreads>
+__device__ __forceinline__ void choose(Shared<kThreads>& sh, int ranks, int pass, uint32_t need) {
+  constexpr int kWarps = kThreads / 32, kPerThread = kBins / kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t* const hist = sh.hist[pass & 1];
+  if (ranks > 1) tc::cluster_sync_all();
+  else __syncthreads();
+  // Thread i owns kPerThread bins from kBins - 1 - kPerThread i down: counts from the top.
+  uint32_t n[kPerThread], sum = 0;
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) n[j] = ranks > 1 ? 0 : hist[kBins - 1 - (tid * kPerThread + j)];
+  for (int r = 0; ranks > 1 && r < ranks; ++r)
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) n[j] += ld_cluster(hist + (kBins - 1 - (tid * kPerThread + j)), r);
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) sum += n[j];
+  uint32_t up = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t x = __shfl_up_sync(kFull, up, off);
+    if (lane >= off) up += x;
+  }
+  if (lane == 31) sh.warp_sums[warp] = up;
+  for (int i = tid; i < kBins; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;
+  __syncthreads();
+  uint32_t before = up - sum;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) before += w < warp ? sh.warp_sums[w] : 0;
+#pragma unroll
+  for (int j = 0; j < kPerThread; ++j) {
+    if (before < need && need <= before + n[j]) {
+      sh.bin = kBins - 1 - (tid * kPerThread + j);
+      sh.need = need - before;
+      sh.whole = need == before + n[j];
+    }
+    before += n[j];
+  }
+  __syncthreads();
+}
+
 // Four tokens' keys, a quarter of a page, are looked at together. (16 sequences of 16384 tokens:
 // XXX us; 32 with every digit counted over all keys, 250 instructions for each 32 of them.)
 template <int kThreads>
@@ -170,46 +213,6 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     }
   }
 
-  // The bin of a digit that holds the cluster's need-th key from the top, how many of the bin's
-  // are needed, and whether that is all of them. Zeroes the other histogram, which nobody has
-  // read since the last meeting.
-  const auto choose = [&](int pass, uint32_t need) {
-    uint32_t* const hist = sh.hist[pass & 1];
-    if (ranks > 1) tc::cluster_sync_all();
-    else __syncthreads();
-    // Thread i owns kPerThread bins from kBins - 1 - kPerThread i down: counts from the top.
-    uint32_t n[kPerThread], sum = 0;
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j) n[j] = ranks > 1 ? 0 : hist[kBins - 1 - (tid * kPerThread + j)];
-    for (int r = 0; ranks > 1 && r < ranks; ++r)
-#pragma unroll
-      for (int j = 0; j < kPerThread; ++j) n[j] += ld_cluster(hist + (kBins - 1 - (tid * kPerThread + j)), r);
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j) sum += n[j];
-    uint32_t up = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t x = __shfl_up_sync(kFull, up, off);
-      if (lane >= off) up += x;
-    }
-    if (lane == 31) sh.warp_sums[warp] = up;
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;
-    __syncthreads();
-    uint32_t before = up - sum;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) before += w < warp ? sh.warp_sums[w] : 0;
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j) {
-      if (before < need && need <= before + n[j]) {
-        sh.bin = kBins - 1 - (tid * kPerThread + j);
-        sh.need = need - before;
-        sh.whole = need == before + n[j];
-      }
-      before += n[j];
-    }
-    __syncthreads();
-  };
-
   // Stays: key > top, or one of the first `need` equal to it. A warp's quads are consecutive, so
   // that ranks follow from counts.
   uint32_t top = kFull, need = 0;
@@ -224,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   };
   bool listed = false;
   if (m > 0) {
-    choose(0, m);
+    choose<kThreads>(sh, ranks, 0, m);
     uint32_t prefix = sh.bin;
     need = sh.need;
     // Keys above the bin are counted, those in it (a few in a hundred) listed: the other
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
           count_digit(key.w, in & 8);
         }
       }
-      choose(pass, need);
+      choose<kThreads>(sh, ranks, pass, need);
       prefix = prefix << kDigit | sh.bin;
       need = sh.need;
       whole = sh.whole;
@@ -377,100 +380,306 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-constexpr int kMoveThreads = 128, kMoveWarps = kMoveThreads / 32;
+// Where a head's rows and weights lie. A slot is page * 16 + its place there.
+template <int kVecs>  // 16-byte words of a head's row (8 or 16)
+struct Rows {
+  uint4 *k, *v;
+  float* weights;
+  const int* trow;
+  int head;
+  __device__ __forceinline__ Rows(const EvictArgs& a, int b, int h)
+      : k(static_cast<uint4*>(a.k_pages)), v(static_cast<uint4*>(a.v_pages)), weights(a.weights),
+        trow(a.table + (size_t)b * a.max_blocks), head(h) {}
+  __device__ __forceinline__ int slot(int t) const { return fetch(trow + t / ATTN_PAGE) * ATTN_PAGE + t % ATTN_PAGE; }
+  __device__ __forceinline__ size_t row(int slot) const { return ((size_t)slot * kHKV + head) * kVecs; }
+  __device__ __forceinline__ float* weight(int slot) const {
+    return weights + ((size_t)(slot / ATTN_PAGE) * kHKV + head) * ATTN_PAGE + slot % ATTN_PAGE;
+  }
 
-// kVecs: 16-byte words of a head's row (8 or 16).
-template <int kVecs>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
-  // Lengths and table are there before the selection that this follows has ended: that grid
-  // has waited for whatever came before.
-  const int head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31;
-  const Cut cut = load_cut(a, b);
-  const int* const trow = a.table + (size_t)b * a.max_blocks;
-  follow();
-  const int2 counts = fetch(a.counts + b * kHKV + head);
-  const int pairs = counts.x, near = counts.y;
-  if (pairs < 0) return;
-  const size_t base = ((size_t)b * kHKV + head) * a.cap;
-  uint4* const kp = static_cast<uint4*>(a.k_pages);
-  uint4* const vp = static_cast<uint4*>(a.v_pages);
-  const auto slot_of = [&](int t) { return fetch(trow + t / ATTN_PAGE) * ATTN_PAGE + t % ATTN_PAGE; };
-  // A slot's row of this head, in rows of heads; and its weight.
-  const auto row_of = [&](int slot) { return (size_t)slot * kHKV + head; };
-  const auto weight_of = [&](int slot) { return a.weights + ((size_t)(slot / ATTN_PAGE) * kHKV + head) * ATTN_PAGE + slot % ATTN_PAGE; };
   // A warp moves the pairs i .. i + 31 below end: a lane looks one up, then the rows go several at once.
-  constexpr int kAtOnce = 32 / kVecs;  // rows of one pool that a warp's load covers
-  const auto fill = [&](int i, int end) {
+  __device__ __forceinline__ void fill(const int* holes, const int* movers, int i, int end, int lane) const {
+    constexpr int kAtOnce = 32 / kVecs, kUnroll = 4;  // rows of one pool that a warp's load covers
     int src = 0, dst = 0;
     const bool in = i + lane < end;
     if (in) {
-      src = fetch(a.movers + base + i + lane);
-      dst = fetch(a.holes + base + i + lane);
-      *weight_of(dst) = *weight_of(src);
+      src = fetch(movers + i + lane);
+      dst = fetch(holes + i + lane);
+      *weight(dst) = *weight(src);
     }
-    const unsigned some = __ballot_sync(kFull, in);
-    if (!some) return;
-    constexpr int kUnroll = 4;
+    const int pairs = min(end - i, 32);
 #pragma unroll 1
-    for (int p = 0; p < 32; p += kAtOnce * kUnroll) {
+    for (int p = 0; p < pairs; p += kAtOnce * kUnroll) {
       uint4 x[kUnroll], y[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int q = p + u * kAtOnce + lane / kVecs;
-        const int s = __shfl_sync(kFull, src, q);
-        if (some >> q & 1) {
-          x[u] = kp[row_of(s) * kVecs + lane % kVecs];
-          y[u] = vp[row_of(s) * kVecs + lane % kVecs];
-        }
+        const size_t s = row(__shfl_sync(kFull, src, q)) + lane % kVecs;
+        if (q < pairs) x[u] = k[s], y[u] = v[s];
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int q = p + u * kAtOnce + lane / kVecs;
-        const int d = __shfl_sync(kFull, dst, q);
-        if (some >> q & 1) {
-          kp[row_of(d) * kVecs + lane % kVecs] = x[u];
-          vp[row_of(d) * kVecs + lane % kVecs] = y[u];
+        const size_t d = row(__shfl_sync(kFull, dst, q)) + lane % kVecs;
+        if (q < pairs) k[d] = x[u], v[d] = y[u];
+      }
+    }
+  }
+
+  // A block moves the last tokens to their places, in rising batches, each read before it is
+  // written (a source is never below its destination). What leaves those places has left them
+  // by the first batch's barrier.
+  template <int kThreads>
+  __device__ __forceinline__ void follow_up(const Cut& cut, int last, int tid) const {
+    const int shift = cut.ctx - cut.now;
+    constexpr int kRows = 4 * kThreads / kVecs;  // of a batch
+    for (int i0 = 0; i0 < last; i0 += kRows) {
+      uint4 x[4], y[4];
+      float w = 0.f;
+      const bool weigh = tid < kRows && i0 + tid < last;
+      if (weigh) w = *weight(slot(cut.edge + shift + i0 + tid));
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + (tid + u * kThreads) / kVecs;
+        if (i < last) {
+          const size_t s = row(slot(cut.edge + shift + i)) + tid % kVecs;
+          x[u] = k[s], y[u] = v[s];
+        }
+      }
+      __syncthreads();
+      if (weigh) *weight(slot(cut.edge + i0 + tid)) = w;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + (tid + u * kThreads) / kVecs;
+        if (i < last) {
+          const size_t d = row(slot(cut.edge + i)) + tid % kVecs;
+          k[d] = x[u], v[d] = y[u];
+        }
+      }
+      __syncthreads();
+    }
+  }
+};
+
+constexpr int kMoveThreads = 128, kMoveWarps = kMoveThreads / 32;
+
+template <int kVecs>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
+  // Lengths are there before the selection that this follows has ended: that grid has waited
+  // for whatever came before.
+  const int head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Cut cut = load_cut(a, b);
+  follow();
+  const int2 counts = fetch(a.counts + b * kHKV + head);
+  const int pairs = counts.x, near = counts.y;
+  if (pairs < 0) return;
+  const Rows<kVecs> rows(a, b, head);
+  const int* const holes = a.holes + ((size_t)b * kHKV + head) * a.cap;
+  const int* const movers = a.movers + ((size_t)b * kHKV + head) * a.cap;
+  if (blockIdx.x > 0) {
+    for (int i = near + ((blockIdx.x - 1) * kMoveWarps + warp) * 32; i < pairs; i += (gridDim.x - 1) * kMoveThreads)
+      rows.fill(holes, movers, i, pairs, lane);
+    return;
+  }
+  // What leaves the places of the last ones, then those.
+  for (int i = warp * 32; i < near; i += kMoveThreads) rows.fill(holes, movers, i, near, lane);
+  rows.template follow_up<kMoveThreads>(cut, a.last, tid);
+}
+
+// ---------------------------------------------------------------------------
+// Both steps by one block a (sequence, head), for contexts of up to kSmall tokens: a thread has
+// two quads' keys in registers, the first digit's bin settles all but a few keys, whose ranks
+// are counted among themselves (or, of many equal ones, by further digits), and what stays is a
+// bit a token. XXX measured
+constexpr int kSmall = 4096, kSmallThreads = 512, kQuads = kSmall / 4 / kSmallThreads, kWords = kSmall / 32;
+constexpr int kRanked = 256;  // listed keys whose ranks are counted
+
+struct alignas(16) Small {
+  Shared<kSmallThreads> sh;
+  uint32_t stays[kWords], equal[kWords];
+  int hole_at[kWords], mover_at[kWords];  // places in the lists of a word's first
+  int holes[kSmall / 2 + 1], movers[kSmall / 2 + 1];
+  int pairs;
+};
+
+template <int kVecs>
+__global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a) {
+  extern __shared__ __align__(16) uint8_t small_smem[];
+  Small& sm = *reinterpret_cast<Small*>(small_smem);
+  Shared<kSmallThreads>& sh = sm.sh;
+  const int head = blockIdx.x, b = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kBins; i += kSmallThreads) sh.hist[0][i] = 0;
+  if (tid < kWords) sm.stays[tid] = sm.equal[tid] = 0;
+  if (tid == 0) sh.bad = 0, sh.listed = 0;
+  follow();
+  const Cut cut = load_cut(a, b);
+  if (!cut.live) {
+    if (!cut.ok && head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+    return;
+  }
+  const Rows<kVecs> rows(a, b, head);
+  const uint32_t m = cut.now - a.first - a.last;
+  const auto middle = [&](int t) { return lowest(cut.end - t) & ~lowest(a.first - t); };  // of a quad's tokens
+  __syncthreads();
+  int page[kQuads];
+  uint4 key[kQuads];
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    const int t = 4 * (tid + i * kSmallThreads);
+    page[i] = t < cut.ctx ? fetch(rows.trow + t / ATTN_PAGE) : 0;
+    if (page[i] < 0 || page[i] >= a.num_pages) sh.bad = 1, page[i] = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    const int t = 4 * (tid + i * kSmallThreads);
+    key[i] = make_uint4(0, 0, 0, 0);
+    if (t >= cut.ctx) continue;
+    const float4 w = fetch(reinterpret_cast<const float4*>(a.weights + ((size_t)page[i] * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE));
+    key[i] = make_uint4(ordered(w.x), ordered(w.y), ordered(w.z), ordered(w.w));
+    const uint32_t in = middle(t);
+    if (in & 1) atomicAdd(sh.hist[0] + (key[i].x >> kFirst), 1u);
+    if (in & 2) atomicAdd(sh.hist[0] + (key[i].y >> kFirst), 1u);
+    if (in & 4) atomicAdd(sh.hist[0] + (key[i].z >> kFirst), 1u);
+    if (in & 8) atomicAdd(sh.hist[0] + (key[i].w >> kFirst), 1u);
+  }
+  if (m > 0) {
+    choose<kSmallThreads>(sh, 1, 0, m);
+    uint32_t prefix = sh.bin, need = sh.need;
+    bool whole = sh.whole;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) {
+      const int t = 4 * (tid + i * kSmallThreads);
+      const uint32_t in = middle(t), k[4] = {key[i].x, key[i].y, key[i].z, key[i].w};
+      uint32_t bits = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!(in >> j & 1)) continue;
+        const uint32_t bin = k[j] >> kFirst;
+        if (bin > prefix || (whole && bin == prefix)) bits |= 1u << j;
+        else if (bin == prefix) {
+          const uint32_t at = atomicAdd(&sh.listed, 1u);
+          if (at < kListed) sh.keys[at] = k[j], sh.places[at] = t + j;
+        }
+      }
+      bits <<= 4 * (lane & 7);
+#pragma unroll
+      for (int off = 1; off < 8; off <<= 1) bits |= __shfl_xor_sync(kFull, bits, off);
+      if ((lane & 7) == 0) sm.stays[t / 32] = bits;
+    }
+    __syncthreads();
+    const int entries = sh.listed;
+    if (!whole && entries <= kRanked) {
+      // The rank of each among them, equal ones by their token.
+      for (int i = tid; i < entries; i += kSmallThreads) {
+        const uint32_t mine = sh.keys[i], place = sh.places[i];
+        uint32_t rank = 0;
+        for (int j = 0; j < entries; ++j) rank += sh.keys[j] > mine || (sh.keys[j] == mine && sh.places[j] < place);
+        if (rank < need) atomicOr(sm.stays + place / 32, 1u << (place & 31));
+      }
+    } else if (!whole) {
+      // The other digits, over all keys (they may be too many for the list).
+      int shift = kFirst;
+#pragma unroll 1
+      for (int pass = 1; pass < 3 && !whole; ++pass) {
+        const int above = shift;
+        shift -= kDigit;
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+          const uint32_t in = middle(4 * (tid + i * kSmallThreads)), k[4] = {key[i].x, key[i].y, key[i].z, key[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((in >> j & 1) && k[j] >> above == prefix) atomicAdd(sh.hist[pass & 1] + (k[j] >> shift & ((1u << kDigit) - 1)), 1u);
+        }
+        choose<kSmallThreads>(sh, 1, pass, need);
+        prefix = prefix << kDigit | sh.bin;
+        need = sh.need;
+        whole = sh.whole;
+      }
+      // Those above stay, and of the equal ones the first `need` (all, where the last bin is).
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) {
+        const int t = 4 * (tid + i * kSmallThreads);
+        const uint32_t in = middle(t), k[4] = {key[i].x, key[i].y, key[i].z, key[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (!(in >> j & 1) || k[j] >> kFirst != prefix >> (kFirst - shift)) continue;
+          const uint32_t digits = k[j] >> shift;
+          if (digits > prefix || (whole && digits == prefix)) atomicOr(sm.stays + (t + j) / 32, 1u << ((t + j) & 31));
+          else if (digits == prefix) atomicOr(sm.equal + (t + j) / 32, 1u << ((t + j) & 31));
+        }
+      }
+      __syncthreads();
+      if (!whole && warp == 0) {
+        uint32_t before = 0;
+        for (int w0 = 0; w0 < kWords; w0 += 32) {
+          const uint32_t e = sm.equal[w0 + lane];
+          uint32_t up = __popc(e);
+          const uint32_t own = up;
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t x = __shfl_up_sync(kFull, up, off);
+            if (lane >= off) up += x;
+          }
+          uint32_t left = need > before + up - own ? need - (before + up - own) : 0, keep = 0, rest = e;
+          for (; left > 0 && rest; --left, rest &= rest - 1) keep |= rest & -rest;
+          sm.stays[w0 + lane] |= keep;
+          before += __shfl_sync(kFull, up, 31);
         }
       }
     }
-  };
-  if (blockIdx.x > 0) {
-    for (int i = near + ((blockIdx.x - 1) * kMoveWarps + (tid >> 5)) * 32; i < pairs; i += (gridDim.x - 1) * kMoveThreads)
-      fill(i, pairs);
+  }
+  __syncthreads();
+  if (sh.bad) {  // seen by the blocks of all heads: nothing of the sequence is moved
+    if (head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
     return;
   }
-  // What leaves the places of the last ones, then those: in rising batches, each read
-  // before it is written (a source is never below its destination).
-  for (int i = (tid >> 5) * 32; i < near; i += kMoveThreads) fill(i, near);
-  const int shift = cut.ctx - cut.now;
-  constexpr int kRows = 4 * kMoveThreads / kVecs;  // of a batch
-  for (int i0 = 0; i0 < a.last; i0 += kRows) {
-    uint4 x[4], y[4];
-    float w = 0.f;
-    const bool weigh = tid < kRows && i0 + tid < a.last;
-    if (weigh) w = *weight_of(slot_of(cut.edge + shift + i0 + tid));
+  // The lists: warp 0 counts what leaves below edge and what stays from there on, word by word.
+  const auto split = [&](int word, uint32_t* out, uint32_t* move) {
+    const int t = 32 * word;
+    const auto below = [&](int n) { return n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1; };
+    const uint32_t in = below(cut.end - t) & ~below(a.first - t), ahead = below(cut.edge - t);
+    *out = in & ~sm.stays[word] & ahead;
+    *move = sm.stays[word] & ~ahead;
+  };
+  if (warp == 0) {
+    int holes = 0, movers = 0;
+    for (int w0 = 0; w0 * 32 < cut.end; w0 += 32) {
+      uint32_t out, move;
+      split(w0 + lane, &out, &move);
+      const uint32_t own = __popc(out) << 16 | __popc(move);  // 1024 at most
+      uint32_t up = own;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + (tid + u * kMoveThreads) / kVecs;
-      if (i < a.last) {
-        const size_t s = row_of(slot_of(cut.edge + shift + i)) * kVecs + tid % kVecs;
-        x[u] = kp[s];
-        y[u] = vp[s];
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t x = __shfl_up_sync(kFull, up, off);
+        if (lane >= off) up += x;
       }
+      sm.hole_at[w0 + lane] = holes + (int)((up - own) >> 16);
+      sm.mover_at[w0 + lane] = movers + (int)((up - own) & 0xffffu);
+      const uint32_t all = __shfl_sync(kFull, up, 31);
+      holes += (int)(all >> 16);
+      movers += (int)(all & 0xffffu);
     }
-    __syncthreads();
-    if (weigh) *weight_of(slot_of(cut.edge + i0 + tid)) = w;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int i = i0 + (tid + u * kMoveThreads) / kVecs;
-      if (i < a.last) {
-        const size_t d = row_of(slot_of(cut.edge + i)) * kVecs + tid % kVecs;
-        kp[d] = x[u];
-        vp[d] = y[u];
-      }
-    }
-    __syncthreads();
+    if (lane == 0) sm.pairs = movers;
   }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    const int t = 4 * (tid + i * kSmallThreads);
+    if (t >= cut.end) continue;
+    uint32_t out, move;
+    split(t / 32, &out, &move);
+    const uint32_t before = (1u << (t & 31)) - 1;
+    int hole = sm.hole_at[t / 32] + __popc(out & before), mover = sm.mover_at[t / 32] + __popc(move & before);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int slot = page[i] * ATTN_PAGE + (t + j) % ATTN_PAGE;
+      if (out >> (t + j & 31) & 1) sm.holes[hole++] = slot;
+      if (move >> (t + j & 31) & 1) sm.movers[mover++] = slot;
+    }
+  }
+  __syncthreads();
+  for (int i = warp * 32; i < sm.pairs; i += kSmallThreads) rows.fill(sm.holes, sm.movers, i, sm.pairs, lane);
+  rows.template follow_up<kSmallThreads>(cut, a.last, tid);
 }
 
 static_assert(sizeof(Shared<512>) % 16 == 0 && sizeof(Shared<1024>) % 16 == 0, "the keys start on 16 bytes");
@@ -490,7 +699,7 @@ int device(int* sms) {
       return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) == cudaSuccess;
     };
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !room(select_kernel<512>) ||
-        !room(select_kernel<1024>)) {
+        !room(select_kernel<1024>) || !room(small_kernel<8>) || !room(small_kernel<16>)) {
       (void)cudaGetLastError();
       return ATTN_ECUDA;
     }
@@ -505,6 +714,7 @@ int list_cap(int max_context) { return max_context / 2 + 1; }
 }  // namespace
 
 size_t evict_workspace_bytes(int B, int max_context) {
+  if (max_context <= kSmall) return 0;
   return (size_t)B * kHKV * sizeof(int2) + 2 * (size_t)B * kHKV * list_cap(max_context) * sizeof(int);
 }
 
@@ -530,6 +740,21 @@ int launch_evict(const EvictCall& c, unsigned* err, cudaStream_t stream) {
   a.holes = reinterpret_cast<int*>(a.counts + (size_t)c.B * kHKV);
   a.movers = a.holes + (size_t)c.B * kHKV * a.cap;
   a.err = err;
+
+  if (c.max_context <= kSmall) {
+    const auto kernel = c.type == ATTN_BF16 ? small_kernel<8> : small_kernel<16>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kHKV, c.B);
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = sizeof(Small);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return launched(cudaLaunchKernelEx(&cfg, kernel, a)) == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
+  }
 
   // Blocks of a cluster: as many as have an SM each, with 1024 tokens at least; and so many that a block's keys fit its shared memory, if they can.
   int ranks = 1;

@@ -75,17 +75,18 @@ CASES = {
 
 @pytest.mark.parametrize("name", CASES)
 @pytest.mark.parametrize("bf16", [False, True])
-def test_evict(cp, name, bf16):
+@pytest.mark.parametrize("bound", [None, 5000, 40000])  # one block a head; a cluster and a second kernel
+def test_evict(cp, name, bf16, bound):
     contexts, keep, first, last = CASES[name]
-    b = R.make_batch([(c, 0) for c in contexts], bf16=bf16, seed=3)
+    b = R.make_batch([(c, 0) for c in contexts], bf16=bf16, seed=3, extra_blocks=2500 if bound else 0)
     # A sequence that has to give up tokens and cannot hold the first and last ones is refused.
     refused = [s for s, c in enumerate(contexts) if keep[s] < c and keep[s] < first + last]
-    check(cp, b, W.weight_pool(b), keep, first, last, untouched=refused)
+    check(cp, b, W.weight_pool(b), keep, first, last, bound=bound, untouched=refused)
     assert cp.attn_get_device_error() == (cp.ATTN_EBOUNDS if refused else 0)
 
 
 @pytest.mark.parametrize("kind", ["zeros", "few values", "half zeros", "nan", "signs", "infinite"])
-@pytest.mark.parametrize("context,keep", [(700, 300), (5000, 4500)])
+@pytest.mark.parametrize("context,keep", [(700, 300), (4096, 3500), (5000, 4500)])
 def test_equal_and_unusual_weights(cp, kind, context, keep):
     b = R.make_batch([(context, 0), (90, 0)], bf16=True, seed=4)
     rng, w = np.random.default_rng(5), W.weight_pool(b)
@@ -123,11 +124,14 @@ def test_a_bound_far_above_the_lengths(cp):
     assert cp.attn_get_device_error() == 0
 
 
-def test_refused_sequences_are_recorded_and_left(cp):
+@pytest.mark.parametrize("far", [0, 500])  # by a bound of 8000 through lists in memory
+def test_refused_sequences_are_recorded_and_left(cp, far):
     lens = [(100, 0), (200, 0), (300, 0), (80, 0)]
 
     def fresh():
-        b = R.make_batch(lens, seed=8)
+        b = R.make_batch(lens, seed=8, extra_blocks=far)
+        if far:
+            b["max_context"] = 8000
         return b, W.weight_pool(b)
     b, w = fresh()
     assert cp.attn_get_device_error() == 0
@@ -151,10 +155,13 @@ def test_refused_sequences_are_recorded_and_left(cp):
             for pool, before in zip((b["kp"], b["vp"]), old):
                 assert torch.equal(bits(rows_of(pool, b, 1, 200)), bits(rows_of(before, b, 1, 200)))
                 assert not torch.equal(bits(rows_of(pool, b, 0, 50)), bits(rows_of(before, b, 0, 50)))
-    b, w = fresh()
-    with pytest.raises(cp.AttnError) as e:
-        evict(cp, b, w, [50, 60, 100, 30], ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
-    assert e.value.code == cp.ATTN_ESPACE
+    b = R.make_batch(lens, seed=8, extra_blocks=500)
+    w = W.weight_pool(b)
+    for ws, code in ((torch.empty(64, dtype=torch.uint8, device="cuda"), cp.ATTN_ESPACE),
+                     (workspace(1 << 20)[8:], cp.ATTN_EALIGN)):
+        with pytest.raises(cp.AttnError) as e:
+            evict(cp, b, w, [50, 60, 100, 30], bound=8000, ws=ws)
+        assert e.value.code == code
     with pytest.raises(cp.AttnError) as e:
         evict(cp, b, w, [50, 60, 100, 30], first=-1)
     assert e.value.code == cp.ATTN_EINVAL

@@ -133,7 +133,9 @@ def test_workspaces_reject_bad_sizes():
 
 
 def test_eviction_workspace_holds_both_lists():
-    for b, n in ((1, 1), (1, 7), (3, 1000), (65535, 16), (1, cp.MAX_TOKENS)):
+    for b, n in ((1, 1), (3, 1000), (65535, 4096)):  # one block a head: lists in shared memory
+        assert cp.attn_evict_workspace_bytes(b, n) == 0
+    for b, n in ((1, 4097), (3, 10001), (65535, 5000), (1, cp.MAX_TOKENS)):
         # counts, and for every head a list of at most half the tokens of each kind
         assert cp.attn_evict_workspace_bytes(b, n) >= b * 8 * 4 * (1 + 2 * (n // 2))
         assert cp.attn_evict_workspace_bytes(b, n) % 4 == 0

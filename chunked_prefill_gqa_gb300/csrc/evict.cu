@@ -486,10 +486,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Both steps by one block a (sequence, head), for contexts of up to kSmall tokens: a thread has
-// two quads' keys in registers, the first digit's bin settles all but a few keys, whose ranks
-// are counted among themselves (or, of many equal ones, by further digits), and what stays is a
-// bit a token. XXX measured
+// Both steps in one launch, for contexts of up to kSmall tokens: a thread has two quads' keys in
+// registers, the first digit's bin settles all but a few keys, whose ranks are counted among
+// themselves (or, of many equal ones, by further digits), and what stays is a bit a token. A
+// cluster's blocks all find the same lists, in shared memory, and share the moves. XXX measured
 constexpr int kSmall = 4096, kSmallThreads = 512, kQuads = kSmall / 4 / kSmallThreads, kWords = kSmall / 32;
 constexpr int kRanked = 256;  // listed keys whose ranks are counted
 
@@ -498,7 +498,7 @@ struct alignas(16) Small {
   uint32_t stays[kWords], equal[kWords];
   int hole_at[kWords], mover_at[kWords];  // places in the lists of a word's first
   int holes[kSmall / 2 + 1], movers[kSmall / 2 + 1];
-  int pairs;
+  int pairs, near;
 };
 
 template <int kVecs>
@@ -506,15 +506,15 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
   extern __shared__ __align__(16) uint8_t small_smem[];
   Small& sm = *reinterpret_cast<Small*>(small_smem);
   Shared<kSmallThreads>& sh = sm.sh;
-  const int head = blockIdx.x, b = blockIdx.y;
+  const int rank = blockIdx.x, ranks = gridDim.x, head = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kBins; i += kSmallThreads) sh.hist[0][i] = 0;
   if (tid < kWords) sm.stays[tid] = sm.equal[tid] = 0;
   if (tid == 0) sh.bad = 0, sh.listed = 0;
   follow();
   const Cut cut = load_cut(a, b);
-  if (!cut.live) {
-    if (!cut.ok && head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+  if (!cut.live) {  // for every block of the cluster
+    if (!cut.ok && rank == 0 && head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
     return;
   }
   const Rows<kVecs> rows(a, b, head);
@@ -541,6 +541,10 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
     if (in & 2) atomicAdd(sh.hist[0] + (key[i].y >> kFirst), 1u);
     if (in & 4) atomicAdd(sh.hist[0] + (key[i].z >> kFirst), 1u);
     if (in & 8) atomicAdd(sh.hist[0] + (key[i].w >> kFirst), 1u);
+  }
+  if (ranks > 1) {
+    __syncwarp();
+    tc::cluster_arrive();  // this block has read the weights, which are moved too
   }
   if (m > 0) {
     choose<kSmallThreads>(sh, 1, 0, m);
@@ -629,20 +633,24 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
     }
   }
   __syncthreads();
+  if (ranks > 1) {
+    __syncwarp();
+    tc::cluster_wait();
+  }
   if (sh.bad) {  // seen by the blocks of all heads: nothing of the sequence is moved
-    if (head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+    if (rank == 0 && head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
     return;
   }
   // The lists: warp 0 counts what leaves below edge and what stays from there on, word by word.
+  const auto below = [&](int n) { return n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1; };
   const auto split = [&](int word, uint32_t* out, uint32_t* move) {
     const int t = 32 * word;
-    const auto below = [&](int n) { return n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1; };
     const uint32_t in = below(cut.end - t) & ~below(a.first - t), ahead = below(cut.edge - t);
     *out = in & ~sm.stays[word] & ahead;
     *move = sm.stays[word] & ~ahead;
   };
   if (warp == 0) {
-    int holes = 0, movers = 0;
+    int holes = 0, movers = 0, near = 0;
     for (int w0 = 0; w0 * 32 < cut.end; w0 += 32) {
       uint32_t out, move;
       split(w0 + lane, &out, &move);
@@ -658,8 +666,9 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
       const uint32_t all = __shfl_sync(kFull, up, 31);
       holes += (int)(all >> 16);
       movers += (int)(all & 0xffffu);
+      near += (int)__reduce_add_sync(kFull, __popc(move & below(cut.now - 32 * (w0 + lane))));
     }
-    if (lane == 0) sm.pairs = movers;
+    if (lane == 0) sm.pairs = movers, sm.near = near;
   }
   __syncthreads();
 #pragma unroll
@@ -678,8 +687,12 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
     }
   }
   __syncthreads();
-  for (int i = warp * 32; i < sm.pairs; i += kSmallThreads) rows.fill(sm.holes, sm.movers, i, sm.pairs, lane);
-  rows.template follow_up<kSmallThreads>(cut, a.last, tid);
+  // The first block moves what lies where the last ones go, then those; all share the others.
+  const int near = sm.near, pairs = sm.pairs;
+  if (rank == 0)
+    for (int i = warp * 32; i < near; i += kSmallThreads) rows.fill(sm.holes, sm.movers, i, near, lane);
+  for (int i = near + (rank + warp * ranks) * 32; i < pairs; i += kSmallThreads * ranks) rows.fill(sm.holes, sm.movers, i, pairs, lane);
+  if (rank == 0) rows.template follow_up<kSmallThreads>(cut, a.last, tid);
 }
 
 static_assert(sizeof(Shared<512>) % 16 == 0 && sizeof(Shared<1024>) % 16 == 0, "the keys start on 16 bytes");
@@ -742,17 +755,23 @@ int launch_evict(const EvictCall& c, unsigned* err, cudaStream_t stream) {
   a.err = err;
 
   if (c.max_context <= kSmall) {
+    // Blocks to share the moves: as many as have an SM each, with 128 tokens at least.
+    int ranks = 1;
+    while (ranks < kMaxCluster && (long long)c.B * kHKV * 2 * ranks <= sms && c.max_context / (2 * ranks) >= 128) ranks *= 2;
     const auto kernel = c.type == ATTN_BF16 ? small_kernel<8> : small_kernel<16>;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kHKV, c.B);
+    cfg.gridDim = dim3(ranks, kHKV, c.B);
     cfg.blockDim = dim3(kSmallThreads);
     cfg.dynamicSmemBytes = sizeof(Small);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return launched(cudaLaunchKernelEx(&cfg, kernel, a)) == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
   }
 

@@ -366,8 +366,9 @@ def _plain_evict(s):
 # ---------------------------------------------------------------------------
 # The framework's calls
 # ---------------------------------------------------------------------------
-def _workspace(s, need):
-    if "workspace" not in s:  # a program keeps one for all of its steps
+def _workspace(s, bytes_of, *sizes):
+    if "workspace" not in s:  # a program asks once and keeps one for all of its steps
+        need = bytes_of(*sizes)
         s["workspace"] = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
     return s["workspace"]
 
@@ -388,18 +389,18 @@ def _own_run(s):
         return {"q": s["qOut"], "k": s["kPages"], "v": s["vPages"]}
     batch = s["table"].shape[0]
     if op == "decode":
-        ws = _workspace(s, cp.attn_decode_weigh_workspace_bytes(batch, s["max_context"]))
+        ws = _workspace(s, cp.attn_decode_weigh_workspace_bytes, batch, s["max_context"])
         call = cp.attn_decode_weigh_paged_bf16kv if bf16 else cp.attn_decode_weigh_paged
         call(s["q"], s["kPages"], s["vPages"], s["weights"], s["table"], s["ctx"], s["out"], s["max_context"],
              decay=s["decay"], workspace=ws)
         return {"out": s["out"], "weights": s["weights"]}
     if op == "weigh":
-        ws = _workspace(s, cp.attn_weigh_workspace_bytes(batch, s["n"], s["max_rows"], s["max_context"]))
+        ws = _workspace(s, cp.attn_weigh_workspace_bytes, batch, s["n"], s["max_rows"], s["max_context"])
         call = cp.attn_weigh_paged_bf16kv if bf16 else cp.attn_weigh_paged
         return call(s["q"], s["kPages"], s["weights"], s["table"], s["ctx"], s["rowStart"], s["max_rows"],
                     s["max_context"], decay=s["decay"], workspace=ws)
     s["weights"].copy_(s["before"])
-    ws = _workspace(s, cp.attn_evict_workspace_bytes(batch, s["max_context"]))
+    ws = _workspace(s, cp.attn_evict_workspace_bytes, batch, s["max_context"])
     call = cp.attn_evict_paged_bf16kv if bf16 else cp.attn_evict_paged
     call(s["kPages"], s["vPages"], s["weights"], s["table"], s["ctx"], s["keep"], s["max_context"],
          keep_first=s["first"], keep_last=s["last"], workspace=ws)

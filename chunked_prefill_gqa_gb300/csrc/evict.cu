@@ -89,6 +89,13 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* p, int rank) {
   return v;
 }
 
+__device__ __forceinline__ uint4 ld_cluster4u(const uint32_t* p, int rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(tc::mapa_shared(tc::smem_u32(p), rank)) : "memory");
+  return v;
+}
+
 // The lowest n of a quad's four bits.
 __device__ __forceinline__ uint32_t lowest(int n) { return (1u << min(max(n, 0), 4)) - 1; }
 
@@ -106,13 +113,15 @@ __device__ __forceinline__ void choose(Shared<kThreads>& sh, int ranks, int pass
   uint32_t* const hist = sh.hist[pass & 1];
   if (ranks > 1) tc::cluster_sync_all();
   else __syncthreads();
-  // Thread i owns kPerThread bins from kBins - 1 - kPerThread i down: counts from the top.
-  uint32_t n[kPerThread], sum = 0;
+  // Thread i owns kPerThread bins, the last thread the lowest ones: counts from the top.
+  const int low = kBins - kPerThread * (tid + 1);
+  uint32_t n[kPerThread] = {}, sum = 0;
+  for (int r = 0; r < ranks; ++r)
 #pragma unroll
-  for (int j = 0; j < kPerThread; ++j) n[j] = ranks > 1 ? 0 : hist[kBins - 1 - (tid * kPerThread + j)];
-  for (int r = 0; ranks > 1 && r < ranks; ++r)
-#pragma unroll
-    for (int j = 0; j < kPerThread; ++j) n[j] += ld_cluster(hist + (kBins - 1 - (tid * kPerThread + j)), r);
+    for (int j = 0; j < kPerThread; j += 4) {
+      const uint4 x = ranks > 1 ? ld_cluster4u(hist + low + j, r) : *reinterpret_cast<const uint4*>(hist + low + j);
+      n[j] += x.x, n[j + 1] += x.y, n[j + 2] += x.z, n[j + 3] += x.w;
+    }
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) sum += n[j];
   uint32_t up = sum;
@@ -122,15 +131,17 @@ __device__ __forceinline__ void choose(Shared<kThreads>& sh, int ranks, int pass
     if (lane >= off) up += x;
   }
   if (lane == 31) sh.warp_sums[warp] = up;
-  for (int i = tid; i < kBins; i += kThreads) sh.hist[(pass + 1) & 1][i] = 0;
+#pragma unroll
+  for (int i = 0; i < kBins / 4; i += kThreads)
+    reinterpret_cast<uint4*>(sh.hist[(pass + 1) & 1])[i + tid] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   uint32_t before = up - sum;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) before += w < warp ? sh.warp_sums[w] : 0;
 #pragma unroll
-  for (int j = 0; j < kPerThread; ++j) {
+  for (int j = kPerThread - 1; j >= 0; --j) {
     if (before < need && need <= before + n[j]) {
-      sh.bin = kBins - 1 - (tid * kPerThread + j);
+      sh.bin = low + j;
       sh.need = need - before;
       sh.whole = need == before + n[j];
     }
@@ -149,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   uint4* const cache = reinterpret_cast<uint4*>(select_smem + sizeof(Shared<kThreads>));  // the keys, if they fit
   const int rank = blockIdx.x, ranks = gridDim.x, head = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
+  for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist[0])[i] = make_uint4(0, 0, 0, 0);
   if (tid < 6) sh.totals[tid] = 0;
   if (tid == 0) sh.bad = 0, sh.listed = 0;
   follow();
@@ -396,19 +407,20 @@ struct Rows {
     return weights + ((size_t)(slot / ATTN_PAGE) * kHKV + head) * ATTN_PAGE + slot % ATTN_PAGE;
   }
 
-  // A warp moves the pairs i .. i + 31 below end: a lane looks one up, then the rows go several at once.
+  // A warp moves the pairs i .. i + kMost - 1 below end: a lane looks one up, then the rows go, all
+  // of kStep pairs at once.
+  static constexpr int kAtOnce = 32 / kVecs, kUnroll = 4, kStep = kAtOnce * kUnroll;  // kAtOnce: rows that a warp's load covers
+  template <int kMost>
   __device__ __forceinline__ void fill(const int* holes, const int* movers, int i, int end, int lane) const {
-    constexpr int kAtOnce = 32 / kVecs, kUnroll = 4;  // rows of one pool that a warp's load covers
     int src = 0, dst = 0;
-    const bool in = i + lane < end;
-    if (in) {
+    if (lane < kMost && i + lane < end) {
       src = fetch(movers + i + lane);
       dst = fetch(holes + i + lane);
       *weight(dst) = *weight(src);
     }
-    const int pairs = min(end - i, 32);
+    const int pairs = min(end - i, kMost);
 #pragma unroll 1
-    for (int p = 0; p < pairs; p += kAtOnce * kUnroll) {
+    for (int p = 0; p < pairs; p += kStep) {
       uint4 x[kUnroll], y[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
@@ -477,11 +489,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
   const int* const movers = a.movers + ((size_t)b * kHKV + head) * a.cap;
   if (blockIdx.x > 0) {
     for (int i = near + ((blockIdx.x - 1) * kMoveWarps + warp) * 32; i < pairs; i += (gridDim.x - 1) * kMoveThreads)
-      rows.fill(holes, movers, i, pairs, lane);
+      rows.template fill<32>(holes, movers, i, pairs, lane);
     return;
   }
   // What leaves the places of the last ones, then those.
-  for (int i = warp * 32; i < near; i += kMoveThreads) rows.fill(holes, movers, i, near, lane);
+  for (int i = warp * Rows<kVecs>::kStep; i < near; i += kMoveWarps * Rows<kVecs>::kStep) rows.template fill<Rows<kVecs>::kStep>(holes, movers, i, near, lane);
   rows.template follow_up<kMoveThreads>(cut, a.last, tid);
 }
 
@@ -508,7 +520,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
   Shared<kSmallThreads>& sh = sm.sh;
   const int rank = blockIdx.x, ranks = gridDim.x, head = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kBins; i += kSmallThreads) sh.hist[0][i] = 0;
+  for (int i = tid; i < kBins / 4; i += kSmallThreads) reinterpret_cast<uint4*>(sh.hist[0])[i] = make_uint4(0, 0, 0, 0);
   if (tid < kWords) sm.stays[tid] = sm.equal[tid] = 0;
   if (tid == 0) sh.bad = 0, sh.listed = 0;
   follow();
@@ -577,6 +589,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
       for (int i = tid; i < entries; i += kSmallThreads) {
         const uint32_t mine = sh.keys[i], place = sh.places[i];
         uint32_t rank = 0;
+#pragma unroll 8
         for (int j = 0; j < entries; ++j) rank += sh.keys[j] > mine || (sh.keys[j] == mine && sh.places[j] < place);
         if (rank < need) atomicOr(sm.stays + place / 32, 1u << (place & 31));
       }
@@ -688,10 +701,13 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
   }
   __syncthreads();
   // The first block moves what lies where the last ones go, then those; all share the others.
+  constexpr int kStep = Rows<kVecs>::kStep, kWarps = kSmallThreads / 32;
   const int near = sm.near, pairs = sm.pairs;
   if (rank == 0)
-    for (int i = warp * 32; i < near; i += kSmallThreads) rows.fill(sm.holes, sm.movers, i, near, lane);
-  for (int i = near + (rank + warp * ranks) * 32; i < pairs; i += kSmallThreads * ranks) rows.fill(sm.holes, sm.movers, i, pairs, lane);
+    for (int i = warp * kStep; i < near; i += kWarps * kStep) rows.template fill<kStep>(sm.holes, sm.movers, i, near, lane);
+  // (from the last block and warp on, which have no near ones)
+  for (int i = near + ((ranks - 1 - rank) + (kWarps - 1 - warp) * ranks) * kStep; i < pairs; i += kWarps * kStep * ranks)
+    rows.template fill<kStep>(sm.holes, sm.movers, i, pairs, lane);
   if (rank == 0) rows.template follow_up<kSmallThreads>(cut, a.last, tid);
 }
 

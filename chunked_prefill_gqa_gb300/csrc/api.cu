@@ -733,8 +733,10 @@ int weigh_paged(const WeighCall& c, size_t workspaceBytes, cudaStream_t stream) 
   if ((rc = current_device(&st)) != ATTN_OK) return rc;
   size_t need = 0;
   if ((rc = weigh_workspace_bytes(c.B, c.N, c.max_rows, c.max_context, &need)) != ATTN_OK) return rc;
-  if (!c.workspace || workspaceBytes < need) return ATTN_ESPACE;
-  if (!aligned16(c.workspace)) return ATTN_EALIGN;
+  if (need > 0) {
+    if (!c.workspace || workspaceBytes < need) return ATTN_ESPACE;
+    if (!aligned16(c.workspace)) return ATTN_EALIGN;
+  }
   return launch_weigh(c, st->err, stream);
 }
 

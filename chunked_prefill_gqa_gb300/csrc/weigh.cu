@@ -18,8 +18,12 @@
 // rows: more blocks in the rows pass, one row tile after another in the keys pass, whose
 // block adds to weights that it alone writes.
 //   bf16 pages: K as stored, q in three bf16 terms: 3 x 4 MMAs of 128 x 128 x 16 a tile
-//   fp32 pages: q_lo K + q K_lo + q K, tf32 terms, in halves of 32 dims: 3 x 8 of 128 x 128 x 8
-// (K is read truncated; K_lo is the remainder rounded to tf32, q's first term rounded too.)
+//   fp32 pages: q K_lo + q_lo K + q K, tf32 terms: 3 x 8 of 128 x 128 x 8
+// (K is read truncated; K_lo is the remainder rounded to tf32, q's first term rounded too.) By
+// key, windows of fewer rows take fewer columns. Fewer terms were measured and not kept: with two
+// bf16 terms in both passes 64 rows of 131071 tokens (bf16 pages) took 119 us for XXX, 32 rows of
+// 16 sequences of 16384 (fp32) 205 for XXX, but weights were off by 2e-6 to 4e-6 where a plain
+// fp32 computation is by 5e-7; in the rows pass alone, as much.
 //
 // Roles: three groups of four warps take the tiles in turn; four warps that write K_lo (fp32,
 // rows) or move K to tensor memory (keys); one warp for TMA (16-token pages through the block
@@ -27,6 +31,7 @@
 #include <cuda.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
@@ -47,7 +52,6 @@ constexpr int kTmaWarps = 2;               // tiles in turn: a box of 16 rows co
 constexpr uint32_t kHalf = 128 * 128;      // 128 rows of 128 bytes
 constexpr uint32_t kBox = ATTN_PAGE * 128;
 constexpr int kMaxSplits = 64;
-constexpr int kWideRows = 8;               // windows from which on operands have two bf16 terms
 constexpr float kNothing = 1e30f;          // reference of a row that gives nothing
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -64,36 +68,52 @@ struct WeighArgs {
   unsigned long long timeout_ns;
 };
 
-template <bool kF32, bool kByKey, bool kWide>
+template <bool kF32, bool kByKey>
 struct Lay {
-  static constexpr bool kTf32 = kF32 && !kWide;  // else bf16 operands
   static constexpr bool kDirect = !kF32 && !kByKey;  // the tensor core reads K as it landed
-  static constexpr bool kSlotted = kByKey || (kF32 && kWide);  // K goes on to slots, in tensor memory (keys) or shared (rows)
-  static constexpr int kConvWarp = kSoft, kConvWarps = kDirect ? 0 : 4;
-  static constexpr int kTmaWarp = kSoft + kConvWarps, kMmaWarp = kTmaWarp + kTmaWarps;
-  static constexpr int kThreads = 32 * (kMmaWarp + 1);
+  static constexpr bool kSlotted = kByKey;           // K goes on to slots in tensor memory
   static constexpr uint32_t kRaw = kF32 ? 2 * kHalf : kHalf;          // a tile of K as it lands
-  static constexpr uint32_t kOperand = kTf32 ? 2 * kHalf : kHalf;     // an operand of 128 rows
-  static constexpr uint32_t kStageBytes = kRaw + (kTf32 && !kByKey ? kOperand : 0);  // K (, K lo)
-  static constexpr int kStages = kTf32 ? 3 : kF32 ? 4 : 8;
-  static constexpr int kTerms = kTf32 || kWide ? 2 : 3;               // of q
-  static constexpr int kSlots = kF32 && kWide && !kByKey ? 2 : 3;
-  static constexpr uint32_t kSmemSlots = kStages * kStageBytes;       // rows pass of wide windows: K's two terms
-  static constexpr uint32_t kSmemQ = kSmemSlots + (kSlotted && !kByKey ? kSlots * 2 * kOperand : 0);  // keys pass: q's terms
+  static constexpr uint32_t kOperand = kRaw;                          // an operand of 128 rows
+  static constexpr uint32_t kStageBytes = kRaw + (kF32 && !kByKey ? kOperand : 0);  // K (, K lo)
+  static constexpr int kStages = kF32 ? 3 : 8;
+  static constexpr int kTerms = kF32 ? 2 : 3;               // of q
+  static constexpr int kSlots = 3;
+  static constexpr uint32_t kSmemQ = kStages * kStageBytes;           // keys pass: q's terms
   static constexpr uint32_t kSmemRef = kSmemQ + (kByKey ? kTerms * kOperand : 0);                    // and the references' tile
   static constexpr uint32_t kSmemEnds = kSmemRef + (kByKey ? kHalf : 0);         // rows pass: [groups][128] (reference, sum)
-  static constexpr uint32_t kSmemBar = kSmemEnds + kGroups * 128 * 8;
-  // Tensor memory. Rows: q's terms, then S. Keys: parts of K (tf32: halves, hi and lo), ones, S.
-  static constexpr int kParts = kTf32 && kByKey ? 2 : 1;
+  static constexpr uint32_t kSmemEnd = kSmemEnds + (kByKey ? 0 : kGroups * 128 * 8);
+  // Tensor memory. Rows: q's terms, then S. Keys: K (fp32: its lo and itself, one after the other), ones, S.
+  static constexpr int kParts = kF32 && kByKey ? 2 : 1;
   static constexpr uint32_t kSlotCols = kF32 ? 64 : 32;
   static constexpr uint32_t kColK = 0, kColOnes = kSlots * kSlotCols;
-  static constexpr uint32_t kColQ = 0, kTermCols = kTf32 ? 64 : 32, kColS = kByKey ? kColOnes + 16 : kTerms * kTermCols;
+  static constexpr uint32_t kColQ = 0, kTermCols = kF32 ? 64 : 32, kColS = kByKey ? kColOnes + 16 : kTerms * kTermCols;
   static constexpr int kBufs = kF32 && kByKey ? 2 : 3;
   static constexpr int kNumBars = 3 * kStages + 2 * kSlots + kGroups + kBufs + 2;
-  static constexpr uint32_t kSmemWords = kSmemBar + kNumBars * 8;     // TMEM address, abort flag
+  static_assert(kColS + kBufs * kKeys <= 512, "TMEM layout");
+};
+
+// Warps: those that read S, four that pass K on, TMA, products. (The first four of them have
+// nothing to do where the tensor core reads K as it landed.)
+constexpr int kConvWarp = kSoft, kTmaWarp = kConvWarp + 4, kMmaWarp = kTmaWarp + kTmaWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+
+// A kernel runs one pass, or both (kFused) one after the other over the same segment of keys:
+// the passes' operands lie in the same bytes, their barriers beside each other.
+constexpr int kRowsPass = 0, kKeysPass = 1, kFused = 2;
+constexpr int kFusedTiles = 2;  // row tiles of a fused window, whose sums stay in shared memory
+template <bool kF32, int kPass>
+struct Kernel {
+  using R = Lay<kF32, false>;
+  using K = Lay<kF32, true>;
+  static constexpr bool kRows = kPass != kKeysPass, kKeys = kPass != kRowsPass;
+  static constexpr uint32_t kEnd = kPass == kRowsPass ? R::kSmemEnd : kPass == kKeysPass ? K::kSmemEnd
+                                   : R::kSmemEnd > K::kSmemEnd ? R::kSmemEnd : K::kSmemEnd;
+  static constexpr uint32_t kSmemKept = kEnd;  // fused: [row tiles][128] (reference, sum) of this block's keys
+  static constexpr uint32_t kSmemBarR = kSmemKept + (kPass == kFused ? kFusedTiles * 128 * 8 : 0);
+  static constexpr uint32_t kSmemBarK = kSmemBarR + (kRows ? R::kNumBars * 8 : 0);
+  static constexpr uint32_t kSmemWords = kSmemBarK + (kKeys ? K::kNumBars * 8 : 0);  // TMEM address, abort flag
   static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
   static_assert(kSmemAlloc <= 232448, "exceeds the 227 KB per-block shared memory limit");
-  static_assert(kColS + kBufs * kKeys <= 512, "TMEM layout");
 };
 
 // The lengths of a sequence, checked as those of drafted rows are.
@@ -109,24 +129,13 @@ __device__ __forceinline__ Seq load_window(const WeighArgs& a, int b) {
 }
 
 // Three terms of x that the tensor core takes exactly: bf16, or tf32 (of fp32 pages).
-template <bool kTf32>
+template <bool kF32>
 __device__ __forceinline__ void three_terms(float x, float (&t)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    t[i] = kTf32 ? tf32_hi(x) : bf16_trunc(x);
+    t[i] = kF32 ? tf32_hi(x) : bf16_trunc(x);
     x -= t[i];
   }
-}
-
-// Two bf16 terms of a pair, each rounded to nearest: 16 bits and a sign, 2^-18 of x left out.
-// (A finite value that would round to infinity takes the largest bf16 number.)
-__device__ __forceinline__ void split2(float x, float y, uint32_t& t0, uint32_t& t1) {
-  const float most = __uint_as_float(0x7f7f0000u);
-  float cx, cy, hx, hy;
-  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(cx) : "f"(x), "f"(most));
-  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(cy) : "f"(y), "f"(most));
-  t0 = pack_bf16_rn_keep(cx, cy, hx, hy);
-  t1 = pack_bf16_rn(x - hx, y - hy);
 }
 
 // tcgen05.st of 8 columns.
@@ -136,71 +145,75 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&u)[8])
                : "memory");
 }
 
-template <bool kF32, bool kByKey, bool kWide>
-__global__ void __launch_bounds__(Lay<kF32, kByKey, kWide>::kThreads, 1)
-weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
-  using L = Lay<kF32, kByKey, kWide>;
-  constexpr int kStages = L::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(kFull, tid >> 5, 0);
-  if (warp == L::kTmaWarp && lane == 0) tma_prefetch_desc(&mk);
-  follow();
-  // Rows pass: the row tiles of a segment are neighbours in the grid and read its keys at
-  // about the same time, all but one from L2.
-  const int row_tiles = kByKey ? 1 : a.row_tiles;
-  const int s = blockIdx.x / row_tiles, head = blockIdx.y, b = blockIdx.z;
-  const Seq seq = load_window(a, b);
-  if (!seq.ok && !kByKey && blockIdx.x == 0 && head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
-  // The rows of this block: a tile of 32 of them, or by key all tiles one after another.
-  const int rt0 = kByKey ? 0 : blockIdx.x % row_tiles, rt1 = kByKey ? (seq.rows + kRows - 1) / kRows : rt0 + 1;
-  if (seq.rows - rt0 * kRows <= 0) return;
-  // The sequence's own keys, cut evenly into segments of whole tiles.
-  const int splits = kByKey ? a.key_splits : a.splits;
-  const int len = ((seq.keys + splits - 1) / splits + kKeys - 1) / kKeys * kKeys;
-  const int k0 = min((long long)s * len, (long long)seq.keys), k1 = min((long long)k0 + len, (long long)seq.keys);
+// What a block works on.
+struct Work {
+  uint8_t* smem;
+  uint32_t tmem;
+  Seq seq;
+  int head, b, s;    // s: its segment
+  int k0, k1;        // of these keys
+  int rt0, rt1;      // and row tiles
+  int ranks;         // fused: segments, the blocks of the cluster
+  float2* kept;      // fused: the rows' (reference, sum) over this block's keys
+  volatile int* abort_flag;
   // Keys that some row of row tile rt sees, and the tiles that hold them.
-  const auto visible = [&](int rt) { return min(k1, seq.ctx + min(seq.rows, (rt + 1) * kRows)); };
-  const auto tiles = [&](int rt) { return max(0, (visible(rt) - k0 + kKeys - 1) / kKeys); };
-  if (kByKey && k0 >= k1) return;
+  __device__ __forceinline__ int visible(int rt) const { return min(k1, seq.ctx + min(seq.rows, (rt + 1) * kRows)); }
+  // Columns of S by key: the row tile's (row, head) pairs, in steps of 32.
+  __device__ __forceinline__ int cols(int rt) const { return (min(seq.rows - rt * kRows, kRows) * kGroup + 31) / 32 * 32; }
+  __device__ __forceinline__ int tiles(int rt) const { return max(0, (visible(rt) - k0 + kKeys - 1) / kKeys); }
+};
 
-  uint64_t* const kfull = reinterpret_cast<uint64_t*>(smem + L::kSmemBar);  // [stage] K landed
-  uint64_t* const kready = kfull + kStages;                                 // [stage] K lo written (tf32, rows)
-  uint64_t* const kempty = kready + kStages;                                // [stage] K read
-  uint64_t* const tfull = kempty + kStages;                                 // [slot] K written there
-  uint64_t* const tempty = tfull + L::kSlots;                               // [slot] products done with it
-  // A group's next S: a barrier a group, since the buffers go round in another time; the group
-  // has waited for its tile before the buffer's next product, and so its own, is issued.
-  uint64_t* const sfull = tempty + L::kSlots;                               // [group] S written
-  uint64_t* const sfree = sfull + kGroups;                                  // [buffer] S read
-  uint64_t* const qready = sfree + L::kBufs;                                // q's terms of a row tile written
-  uint64_t* const drain = qready + 1;
-  uint32_t* const words = reinterpret_cast<uint32_t*>(smem + L::kSmemWords);
-  volatile int* const abort_flag = reinterpret_cast<volatile int*>(words + 1);
-  const Wait wait{a.err, a.timeout_ns, abort_flag};
-  const int* const trow = a.table + (size_t)b * a.max_blocks;
-
-  if (warp == L::kTmaWarp) {
+// A pass's barriers.
+template <class L>
+struct Bars {
+  uint64_t *kfull, *kready, *kempty, *tfull, *tempty, *sfull, *sfree, *qready, *drain;
+  __device__ __forceinline__ explicit Bars(uint64_t* at) {
+    kfull = at;                       // [stage] K landed
+    kready = kfull + L::kStages;      // [stage] K lo written (tf32, rows)
+    kempty = kready + L::kStages;     // [stage] K read
+    tfull = kempty + L::kStages;      // [slot] K written there
+    tempty = tfull + L::kSlots;       // [slot] products done with it
+    // A group's next S: a barrier a group, since the buffers go round in another time; the group
+    // has waited for its tile before the buffer's next product, and so its own, is issued.
+    sfull = tempty + L::kSlots;       // [group] S written
+    sfree = sfull + kGroups;          // [buffer] S read
+    qready = sfree + L::kBufs;        // q's terms of a row tile written
+    drain = qready + 1;
+  }
+  __device__ __forceinline__ void init(int lane) const {
     for (int i = lane; i < L::kNumBars; i += 32) {
       uint64_t* const bar = &kfull[i];
       const bool by_four = (bar >= kready && bar < kempty) || (L::kSlotted && bar >= kempty && bar < tempty) || (bar >= sfree && bar < qready);
       mbar_init(bar, by_four ? 4 : bar == qready ? kSoft : 1);
     }
-    fence_mbar_init();
-    if (lane == 0) *abort_flag = 0;
-  } else if (warp == L::kMmaWarp) {
-    tmem_alloc(words, 512);
-    tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = words[0];
+};
+
+// One pass of the block, every warp in its role. All warps meet at the end; after a wait that
+// ran out those that started copies and products have waited for them.
+template <bool kF32, bool kByKey>
+__device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs& a, const Work& x_, uint64_t* bars) {
+  using L = Lay<kF32, kByKey>;
+  constexpr int kStages = L::kStages;
+  uint8_t* const smem = x_.smem;
+  const Seq& seq = x_.seq;
+  const int head = x_.head, b = x_.b, s = x_.s, k0 = x_.k0, k1 = x_.k1, rt0 = x_.rt0, rt1 = x_.rt1;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);
+  const auto visible = [&](int rt) { return x_.visible(rt); };
+  const auto tiles = [&](int rt) { return x_.tiles(rt); };
+  const Bars<L> bar_(bars);
+  uint64_t *const kfull = bar_.kfull, *const kready = bar_.kready, *const kempty = bar_.kempty, *const tfull = bar_.tfull,
+           *const tempty = bar_.tempty, *const sfull = bar_.sfull, *const sfree = bar_.sfree, *const qready = bar_.qready,
+           *const drain = bar_.drain;
+  volatile int* const abort_flag = x_.abort_flag;
+  const Wait wait{a.err, a.timeout_ns, abort_flag};
+  const int* const trow = a.table + (size_t)b * a.max_blocks;
+  const uint32_t tmem = x_.tmem;
   int last = -1;  // the last tile that a TMA warp has asked for
 
-  if (warp >= L::kTmaWarp && warp < L::kMmaWarp) {
-    const int mine = warp - L::kTmaWarp;  // this warp's tiles: every second one
+  if (warp >= kTmaWarp && warp < kMmaWarp) {
+    const int mine = warp - kTmaWarp;  // this warp's tiles: every second one
     int it = 0;
     bool ok = true;
     for (int rt = rt0; ok && rt < rt1; ++rt) {
@@ -236,51 +249,42 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
         }
       }
     }
-  } else if (warp == L::kMmaWarp) {
+  } else if (warp == kMmaWarp) {
     const uint32_t base = smem_u32(smem);
     int it = 0;
     bool ok = true;
     for (int rt = rt0; ok && rt < rt1; ++rt) {
-      const int count = tiles(rt);
+      const int count = tiles(rt), cols = kByKey ? x_.cols(rt) : kKeys;
       ok = wait.warp(qready, (rt - rt0) & 1);
       for (int n = 0; ok && n < count; ++n, ++it) {
         const int buf = it % L::kBufs;
         const uint32_t d = tmem + L::kColS + buf * kKeys;
         if (it >= L::kBufs && !(ok = wait.warp(&sfree[buf], (it / L::kBufs - 1) & 1))) break;
-        constexpr uint32_t id = L::kTf32 ? idesc_tf32(128, 128) : idesc_bf16(128, 128, false);
+        const uint32_t id = kF32 ? idesc_tf32(128, cols) : idesc_bf16(128, cols, false);
         constexpr uint64_t lo = L::kOperand >> 4;
         if constexpr (!kByKey) {
-          const int st = it % kStages, slot = it % L::kSlots;
-          if (!(ok = L::kSlotted ? wait.warp(&tfull[slot], (it / L::kSlots) & 1)
-                                 : wait.warp(kF32 ? &kready[st] : &kfull[st], (it / kStages) & 1)))
-            break;
+          const int st = it % kStages;
+          if (!(ok = wait.warp(kF32 ? &kready[st] : &kfull[st], (it / kStages) & 1))) break;
           tc_fence_after();
-          const uint64_t kd = sdesc_sw128(base + (L::kSlotted ? L::kSmemSlots + slot * 2 * L::kOperand : st * L::kStageBytes));
+          const uint64_t kd = sdesc_sw128(base + st * L::kStageBytes);
           const uint32_t q = tmem + L::kColQ;
           if (elect()) {
-            if constexpr (L::kTf32) {
+            if constexpr (kF32) {  // the small products first, as by key
+              const auto product = [&](uint32_t qt, uint64_t kt, bool first) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint64_t kh = kd + h * (kHalf >> 4);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, q + 64 + h * 32 + x * 8, kh + x * 2, id, h + x > 0);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, q + h * 32 + x * 8, kh + lo + x * 2, id, 1);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, q + h * 32 + x * 8, kh + x * 2, id, 1);
-              }
+                for (int x = 0; x < 8; ++x) mma_tf32_ts(d, qt + x * 8, kt + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, !first || x > 0);
+              };
+              product(q, kd + lo, true);
+              product(q + 64, kd, false);
+              product(q, kd, false);
             } else {
-              if constexpr (kF32) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + x * 8, kd + lo + x * 2, id, x > 0);
-              }
 #pragma unroll
               for (int t = L::kTerms - 1; t >= 0; --t)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + t * 32 + x * 8, kd + x * 2, id, kF32 || t < L::kTerms - 1 || x > 0);
+                for (int x = 0; x < 4; ++x) mma_f16_ts(d, q + t * 32 + x * 8, kd + x * 2, id, t < L::kTerms - 1 || x > 0);
             }
             mma_commit(&sfull[it % kGroups]);
-            mma_commit(L::kSlotted ? &tempty[slot] : &kempty[st]);
+            mma_commit(&kempty[st]);
           }
           __syncwarp();
         } else {
@@ -292,28 +296,22 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
             tc_fence_after();
             const uint32_t k = tmem + L::kColK + slot * L::kSlotCols;
             if (elect()) {
-              if constexpr (L::kTf32) {
-                const uint64_t qh = qd + h * (kHalf >> 4);
+              if constexpr (kF32) {  // K lo, then K
+                const auto product = [&](uint64_t qt, bool first) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, k + x * 8, qh + lo + x * 2, id, h + x > 0);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, k + 32 + x * 8, qh + x * 2, id, 1);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) mma_tf32_ts(d, k + x * 8, qh + x * 2, id, 1);
+                  for (int x = 0; x < 8; ++x) mma_tf32_ts(d, k + x * 8, qt + (x >> 2) * (kHalf >> 4) + (x & 3) * 2, id, !first || x > 0);
+                };
+                if (h == 1) product(qd + lo, false);
+                product(qd, h == 0);
               } else {
-                if constexpr (kF32) {
-#pragma unroll
-                  for (int x = 0; x < 4; ++x) mma_f16_ts(d, k + 32 + x * 8, qd + x * 2, id, x > 0);
-                }
 #pragma unroll
                 for (int t = L::kTerms - 1; t >= 0; --t)
 #pragma unroll
-                  for (int x = 0; x < 4; ++x)
-                    mma_f16_ts(d, k + x * 8, qd + t * lo + x * 2, id, kF32 || t < L::kTerms - 1 || x > 0);
+                  for (int x = 0; x < 4; ++x) mma_f16_ts(d, k + x * 8, qd + t * lo + x * 2, id, t < L::kTerms - 1 || x > 0);
               }
               mma_commit(&tempty[slot]);
               if (h == L::kParts - 1) {
-                if constexpr (L::kTf32) mma_tf32_ts(d, tmem + L::kColOnes, rd, id, 1);
+                if constexpr (kF32) mma_tf32_ts(d, tmem + L::kColOnes, rd, id, 1);
                 else mma_f16_ts(d, tmem + L::kColOnes, rd, id, 1);
                 mma_commit(&sfull[it % kGroups]);
               }
@@ -323,51 +321,15 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
         }
       }
     }
-  } else if (warp >= L::kConvWarp && warp < L::kTmaWarp) {
-    const int ctid = tid - 32 * L::kConvWarp;
+  } else if (warp >= kConvWarp && warp < kTmaWarp) {
+    const int ctid = tid - 32 * kConvWarp;
     int total = 0;
-    for (int rt = rt0; rt < rt1; ++rt) total += tiles(rt);
+    for (int rt = rt0; !L::kDirect && rt < rt1; ++rt) total += tiles(rt);
     for (int it = 0; it < total; ++it) {
       const int st = it % kStages;
       uint8_t* const stage = smem + st * L::kStageBytes;
       if (!wait.warp(&kfull[st], (it / kStages) & 1)) break;
-      if constexpr (kF32 && kWide && !kByKey) {
-        // K's two terms, a tile of bf16 each. A thread takes 8 dims (two 16-byte words of fp32,
-        // one of bf16) of a key.
-        const int slot = it % L::kSlots;
-        if (it >= L::kSlots && !wait.warp(&tempty[slot], (it / L::kSlots - 1) & 1)) break;
-        uint8_t* const to = smem + L::kSmemSlots + slot * 2 * L::kOperand;
-        const uint32_t oct = ctid & 7, odd = oct >> 2;  // half a row apart, words of the other parity first: no bank twice
-#pragma unroll
-        for (int h = 0; h < 8; h += 4) {
-          float4 x[4][2];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t key = (uint32_t)(ctid >> 3) + 16u * (h + j);
-            x[j][0] = *reinterpret_cast<const float4*>(stage + odd * kHalf + sw128(key * 128u + ((oct & 3) * 2 + odd) * 16u));
-            x[j][1] = *reinterpret_cast<const float4*>(stage + odd * kHalf + sw128(key * 128u + ((oct & 3) * 2 + 1 - odd) * 16u));
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t key = (uint32_t)(ctid >> 3) + 16u * (h + j);
-            const float4 u = odd ? x[j][1] : x[j][0], v = odd ? x[j][0] : x[j][1];
-            uint4 w0, w1;
-            split2(u.x, u.y, w0.x, w1.x);
-            split2(u.z, u.w, w0.y, w1.y);
-            split2(v.x, v.y, w0.z, w1.z);
-            split2(v.z, v.w, w0.w, w1.w);
-            uint8_t* const at = to + sw128(key * 128u + oct * 16u);
-            *reinterpret_cast<uint4*>(at) = w0;
-            *reinterpret_cast<uint4*>(at + L::kOperand) = w1;
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&kempty[st]);
-          mbar_arrive(&tfull[slot]);
-        }
-      } else if constexpr (!kByKey) {
+      if constexpr (!kByKey) {
         // K lo, at the same offset of the next region.
 #pragma unroll 2
         for (int h = 0; h < 4; ++h) {
@@ -389,42 +351,25 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
 #pragma unroll
         for (int h = 0; ok && h < L::kParts; ++h) {
           const int part = it * L::kParts + h, slot = part % L::kSlots;
-          float x[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(x + 4 * i) =
-                *reinterpret_cast<const float4*>(stage + h * kHalf + sw128((uint32_t)ctid * 128u + i * 16u));
-          if (h == L::kParts - 1 && !(kF32 && kWide)) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kempty[st]);
-          }
           if (part >= L::kSlots && !(ok = wait.warp(&tempty[slot], (part / L::kSlots - 1) & 1))) break;
           tc_fence_after();
           const uint32_t at = tmem + ((uint32_t)((warp & 3) * 32) << 16) + L::kColK + slot * L::kSlotCols;
-          if constexpr (kF32 && kWide) {
-            // Two bf16 terms of the 32 dims; the other half of the row follows.
-            uint32_t w0[16], w1[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) split2(x[2 * i], x[2 * i + 1], w0[i], w1[i]);
-            tmem_st16(at, w0);
-            tmem_st16(at + 32, w1);
+          for (int half = 0; half < (kF32 ? 2 : 1); ++half) {
+            float x[32];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *reinterpret_cast<float4*>(x + 4 * i) =
-                  *reinterpret_cast<const float4*>(stage + kHalf + sw128((uint32_t)ctid * 128u + i * 16u));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kempty[st]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) split2(x[2 * i], x[2 * i + 1], w0[i], w1[i]);
-            tmem_st16(at + 16, w0);
-            tmem_st16(at + 48, w1);
-          } else {
-            tmem_st32(at, x);
-            if constexpr (kF32) {
+                  *reinterpret_cast<const float4*>(stage + half * kHalf + sw128((uint32_t)ctid * 128u + i * 16u));
+            if (kF32 && h == 0) {  // K lo first
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] = tf32_near(x[i] - tf32_hi(x[i]));
-              tmem_st32(at + 32, x);
             }
+            tmem_st32(at + half * 32, x);
+          }
+          if (h == L::kParts - 1) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kempty[st]);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -460,129 +405,161 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
           if (in) v = fetch(reinterpret_cast<const float4*>(a.q + pair * kD + c * 16 + i));
           x[i] = v.x * kTreeC, x[i + 1] = v.y * kTreeC, x[i + 2] = v.z * kTreeC, x[i + 3] = v.w * kTreeC;
         }
-        if constexpr (!kByKey && L::kTf32) {
+        if constexpr (!kByKey && kF32) {
           uint32_t w[2][16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float h = tf32_near(x[i]);
-            w[0][i] = __float_as_uint(h), w[1][i] = __float_as_uint(x[i] - h);
+            w[0][i] = __float_as_uint(h), w[1][i] = __float_as_uint(tf32_near(x[i] - h));
           }
 #pragma unroll
           for (int t = 0; t < 2; ++t) tmem_st16(lane_tmem + L::kColQ + t * 64 + c * 16, w[t]);
         } else if constexpr (!kByKey) {
           uint32_t w[3][8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if (kWide) split2(x[2 * i], x[2 * i + 1], w[0][i], w[1][i]);
-            else split3_cut(x[2 * i], x[2 * i + 1], w[0][i], w[1][i], w[2][i]);
-          }
+          for (int i = 0; i < 8; ++i) split3_cut(x[2 * i], x[2 * i + 1], w[0][i], w[1][i], w[2][i]);
 #pragma unroll
           for (int t = 0; t < L::kTerms; ++t) tmem_st8(lane_tmem + L::kColQ + t * 32 + c * 8, w[t]);
-        } else if constexpr (L::kTf32) {
+        } else if constexpr (kF32) {
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             uint8_t* const at = smem + L::kSmemQ + (c >> 1) * kHalf + sw128((uint32_t)row * 128u + (c & 1) * 64u + i * 4u);
             const float4 h = make_float4(tf32_near(x[i]), tf32_near(x[i + 1]), tf32_near(x[i + 2]), tf32_near(x[i + 3]));
             *reinterpret_cast<float4*>(at) = h;
-            *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(x[i] - h.x, x[i + 1] - h.y, x[i + 2] - h.z, x[i + 3] - h.w);
+            *reinterpret_cast<float4*>(at + L::kOperand) = make_float4(tf32_near(x[i] - h.x), tf32_near(x[i + 1] - h.y), tf32_near(x[i + 2] - h.z), tf32_near(x[i + 3] - h.w));
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 16; i += 8) {
             uint32_t w[3][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (kWide) split2(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j]);
-              else split3_cut(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j], w[2][j]);
-            }
+            for (int j = 0; j < 4; ++j) split3_cut(x[i + 2 * j], x[i + 2 * j + 1], w[0][j], w[1][j], w[2][j]);
             uint8_t* const at = smem + L::kSmemQ + sw128((uint32_t)row * 128u + c * 32u + i * 2u);
 #pragma unroll
             for (int t = 0; t < L::kTerms; ++t) *reinterpret_cast<uint4*>(at + t * L::kOperand) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
           }
         }
       }
-              if (kByKey && g == kGroups - 1) {
-                // The row's reference and the logarithm of its sum over all keys, from the segments.
-                float top = kUnseen, sum = 0.f;
-                if (in) {
-                  const float2* const st = a.stats + pair * a.splits;
-      #pragma unroll 4
-                  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, fetch(st + i).x);
-      #pragma unroll 4
-                  for (int i = 0; i < a.splits; ++i) {
-                    const float2 p = fetch(st + i);
-                    sum = fmaf(ex2(p.x - top), p.y, sum);
-                  }
-                }
-                // A row whose scores are all -inf, or none: 2^x is 0 whatever x is.
-                float t[6];
-                three_terms<L::kTf32>(sum == 0.f ? -kNothing : -top, *reinterpret_cast<float(*)[3]>(t));
-                three_terms<L::kTf32>(sum == 0.f ? 0.f : -log2f(sum), *reinterpret_cast<float(*)[3]>(t + 3));
-                uint4 u0, u1 = make_uint4(0, 0, 0, 0);
-                if constexpr (L::kTf32) {
-                  u0 = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
-                  u1.x = __float_as_uint(t[4]), u1.y = __float_as_uint(t[5]);
-                } else {
-                  u0 = make_uint4(pack_bf16_trunc(t[0], t[1]), pack_bf16_trunc(t[2], t[3]), pack_bf16_trunc(t[4], t[5]), 0u);
-                }
-                *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u)) = u0;
-                *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u + 16u)) = u1;
-                if (rt == rt0) {
-                  constexpr uint32_t kOne = L::kTf32 ? 0x3f800000u : 0x3f803f80u;
-                  const uint32_t ones[8] = {kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne};
-                  tmem_st8(lane_tmem + L::kColOnes, ones);
-                }
-              }
+      if (kByKey && g == kGroups - 1) {
+        // The row's reference and the logarithm of its sum over all keys, from the segments.
+        float top = kUnseen, sum = 0.f;
+        if (in && x_.kept) {  // the cluster's
+          float2 p[kMaxCluster];
+#pragma unroll
+          for (int i = 0; i < kMaxCluster; ++i) {
+            p[i] = make_float2(kUnseen, 0.f);
+            if (i < x_.ranks) p[i] = ld_cluster2(mapa_shared(smem_u32(x_.kept + (rt - rt0) * 128 + row), i));
+            top = fmaxf(top, p[i].x);
+          }
+#pragma unroll
+          for (int i = 0; i < kMaxCluster; ++i) sum = fmaf(ex2(p[i].x - top), p[i].y, sum);
+        } else if (in) {
+          const float2* const st = a.stats + pair * a.splits;
+#pragma unroll 4
+          for (int i = 0; i < a.splits; ++i) top = fmaxf(top, fetch(st + i).x);
+#pragma unroll 4
+          for (int i = 0; i < a.splits; ++i) {
+            const float2 p = fetch(st + i);
+            sum = fmaf(ex2(p.x - top), p.y, sum);
+          }
+        }
+        // A row whose scores are all -inf, or none: 2^x is 0 whatever x is.
+        float t[6];
+        three_terms<kF32>(sum == 0.f ? -kNothing : -top, *reinterpret_cast<float(*)[3]>(t));
+        three_terms<kF32>(sum == 0.f ? 0.f : -log2f(sum), *reinterpret_cast<float(*)[3]>(t + 3));
+        uint4 u0, u1 = make_uint4(0, 0, 0, 0);
+        if constexpr (kF32) {
+          u0 = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
+          u1.x = __float_as_uint(t[4]), u1.y = __float_as_uint(t[5]);
+        } else {
+          u0 = make_uint4(pack_bf16_trunc(t[0], t[1]), pack_bf16_trunc(t[2], t[3]), pack_bf16_trunc(t[4], t[5]), 0u);
+        }
+        *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u)) = u0;
+        *reinterpret_cast<uint4*>(smem + L::kSmemRef + sw128((uint32_t)row * 128u + 16u)) = u1;
+        if (rt == rt0) {
+          constexpr uint32_t kOne = kF32 ? 0x3f800000u : 0x3f803f80u;
+          const uint32_t ones[8] = {kOne, kOne, kOne, kOne, kOne, kOne, kOne, kOne};
+          tmem_st8(lane_tmem + L::kColOnes, ones);
+        }
+      }
       if (kByKey) fence_proxy_async_smem();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(qready);
       const int count = tiles(rt);
-      for (int n = (g + kGroups - done % kGroups) % kGroups; n < count; n += kGroups) {
+      const int cols = x_.cols(rt);
+      const int first = (g + kGroups - done % kGroups) % kGroups;  // the group's first tile
+      // By key: the page of a thread's key, looked up a tile ahead.
+      const int seen = visible(rt);
+      const auto page_at = [&](int n) {
+        const int t = k0 + n * kKeys + row;
+        return kByKey && t < seen ? fetch(trow + t / ATTN_PAGE) : -1;
+      };
+      int page_next = page_at(first);
+      for (int n = first; n < count; n += kGroups) {
         const int it = done + n, buf = it % L::kBufs, t0 = k0 + n * kKeys;
         const uint32_t s_tmem = lane_tmem + L::kColS + buf * kKeys;
         if constexpr (kByKey) {
-          const int t = t0 + row;
+          const int t = t0 + row, page = page_next;
+          page_next = page_at(n + kGroups);
           // The key's weight so far, on its way while the products run. Row tile (t - context) /
           // 32 is the first that sees a token of the rows themselves, 0 any other.
           float* w = nullptr;
           float old = 0.f;
-          if (t < visible(rt)) {
-            const int page = fetch(trow + t / ATTN_PAGE);
-            if (page >= 0 && page < a.num_pages) {
-              w = a.weights + ((size_t)page * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;
-              if (rt > max(0, t - seq.ctx) / kRows) old = *w;
-              else if (a.decay != 0.f && t < weighed) old = a.decay * *w;
-            }
+          if (page >= 0 && page < a.num_pages) {
+            w = a.weights + ((size_t)page * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;
+            if (rt > max(0, t - seq.ctx) / kRows) old = *w;
+            else if (a.decay != 0.f && t < weighed) old = a.decay * *w;
           }
           failed |= !wait.warp(&sfull[g], (it / kGroups) & 1);
           tc_fence_after();
           float sum0 = 0.f, sum1 = 0.f;
           const int late = t - seq.ctx - i0;  // rows before it do not see the key
-#pragma unroll
-          for (int h = 0; h < 128; h += kChunk) {
-            float x[kChunk];
-#pragma unroll
-            for (int i = 0; i < kChunk; i += 32) tmem_ld32(s_tmem + h + i, *reinterpret_cast<float(*)[32]>(&x[i]));
-            tmem_wait_ld();
-            if (h == 128 - kChunk) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sfree[buf]);
-            }
+          const auto add = [&](int h, float* x, auto width) {
+            constexpr int kWidth = decltype(width)::value;
             if (t0 + kKeys > seq.ctx + i0) {
 #pragma unroll
-              for (int i = 0; i < kChunk; ++i)
+              for (int i = 0; i < kWidth; ++i)
                 if ((h + i) / 4 < late) x[i] = -INFINITY;
             }
 #pragma unroll
-            for (int i = 0; i < kChunk; i += 2) add2(sum0, sum1, sum0, sum1, ex2(x[i]), ex2(x[i + 1]));
+            for (int i = 0; i < kWidth; i += 2) add2(sum0, sum1, sum0, sum1, ex2(x[i]), ex2(x[i + 1]));
+          };
+          const auto read = [&] {  // the buffer is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfree[buf]);
+          };
+          if (cols == kKeys) {
+#pragma unroll
+            for (int h = 0; h < 128; h += kChunk) {
+              float x[kChunk];
+#pragma unroll
+              for (int i = 0; i < kChunk; i += 32) tmem_ld32(s_tmem + h + i, *reinterpret_cast<float(*)[32]>(&x[i]));
+              tmem_wait_ld();
+              if (h == 128 - kChunk) read();
+              add(h, x, std::integral_constant<int, kChunk>());
+            }
+          } else {
+#pragma unroll 1
+            for (int h = 0; h < cols; h += 32) {
+              float x[32];
+              tmem_ld32(s_tmem + h, x);
+              tmem_wait_ld();
+              if (h == cols - 32) read();
+              add(h, x, std::integral_constant<int, 32>());
+            }
           }
           if (w && !failed) *w = old + (sum0 + sum1);
         } else {
           failed |= !wait.warp(&sfull[g], (it / kGroups) & 1);
           tc_fence_after();
+          if (quarter * 8 >= nrows) {  // no row in this warp's lanes
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfree[buf]);
+            continue;
+          }
           const int limit = min(seq.ctx + i0 + (row >> 2) + 1, k1) - t0;  // keys of the tile that the row sees
 #pragma unroll
           for (int h = 0; h < 128; h += kChunk) {
@@ -624,22 +601,23 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
         }
       }
       done += count;
-    }
-    if constexpr (!kByKey) {
-      float2* const ends = reinterpret_cast<float2*>(smem + L::kSmemEnds);
-      if (g > 0) ends[g * 128 + row] = make_float2(ref, l0 + l1);
-      int over;
-      const bool lost = meet(kMeet, false, failed, lane, &over);
-      const int i = rt0 * kRows + (row >> 2);
-      if (g == 0 && i < seq.rows) {
-        float top = ref;
+      if constexpr (!kByKey) {  // the groups' sums
+        float2* const ends = reinterpret_cast<float2*>(smem + L::kSmemEnds);
+        if (g > 0) ends[g * 128 + row] = make_float2(ref, l0 + l1);
+        int over;
+        const bool lost = meet(kMeet, false, failed, lane, &over);
+        if (g == 0) {
+          float top = ref;
 #pragma unroll
-        for (int x = 1; x < kGroups; ++x) top = fmaxf(top, ends[x * 128 + row].x);
-        float sum = ex2(ref - top) * (l0 + l1);
+          for (int x = 1; x < kGroups; ++x) top = fmaxf(top, ends[x * 128 + row].x);
+          float sum = ex2(ref - top) * (l0 + l1);
 #pragma unroll
-        for (int x = 1; x < kGroups; ++x) sum = fmaf(ex2(ends[x * 128 + row].x - top), ends[x * 128 + row].y, sum);
-        a.stats[((size_t)(seq.first + i) * kHQ + head * kGroup + (row & 3)) * a.splits + s] =
-            lost ? make_float2(kUnseen, 0.f) : make_float2(top, sum);
+          for (int x = 1; x < kGroups; ++x) sum = fmaf(ex2(ends[x * 128 + row].x - top), ends[x * 128 + row].y, sum);
+          const float2 all = lost ? make_float2(kUnseen, 0.f) : make_float2(top, sum);
+          if (x_.kept) x_.kept[(rt - rt0) * 128 + row] = all;
+          else if (in) a.stats[pair * a.splits + s] = all;
+        }
+        ref = kUnseen, l0 = l1 = 0.f;
       }
     }
   }
@@ -649,32 +627,88 @@ weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   __syncthreads();
   tc_fence_after();
   if (*abort_flag) {
-    if (warp >= L::kTmaWarp && warp < L::kMmaWarp)  // its copies still in flight
+    if (warp >= kTmaWarp && warp < kMmaWarp)  // its copies still in flight
       for (int i = last; i >= 0 && i > last - kStages; i -= kTmaWarps) mbar_wait(&kfull[i % kStages], (i / kStages) & 1, a.timeout_ns);
-    if (warp == L::kMmaWarp) drain_products(drain, a.timeout_ns);
+    if (warp == kMmaWarp) drain_products(drain, a.timeout_ns);
     __syncthreads();
   }
-  if (warp == L::kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+template <bool kF32, int kPass>
+__global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
+  using K = Kernel<kF32, kPass>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(kFull, tid >> 5, 0);
+  if (warp == kTmaWarp && lane == 0) tma_prefetch_desc(&mk);
+  follow();
+  // Rows pass: the row tiles of a segment are neighbours in the grid and read its keys at
+  // about the same time, all but one from L2.
+  const int row_tiles = kPass == kRowsPass ? a.row_tiles : 1, splits = kPass == kKeysPass ? a.key_splits : a.splits;
+  Work x;
+  x.smem = smem;
+  x.s = blockIdx.x / row_tiles;
+  x.head = blockIdx.y;
+  x.b = blockIdx.z;
+  x.seq = load_window(a, x.b);
+  if (!x.seq.ok && K::kRows && blockIdx.x == 0 && x.head == 0 && tid == 0) record_error(a.err, kDevErrBounds);
+  // The rows of this block: a tile of 32 of them, or all tiles one after another.
+  x.rt0 = kPass == kRowsPass ? blockIdx.x % row_tiles : 0;
+  x.rt1 = kPass == kRowsPass ? x.rt0 + 1 : (x.seq.rows + kRows - 1) / kRows;
+  if (x.seq.rows - x.rt0 * kRows <= 0) return;  // of a cluster all blocks
+  // The sequence's own keys, cut evenly into segments of whole tiles.
+  const int len = ((x.seq.keys + splits - 1) / splits + kKeys - 1) / kKeys * kKeys;
+  x.k0 = min((long long)x.s * len, (long long)x.seq.keys);
+  x.k1 = min((long long)x.k0 + len, (long long)x.seq.keys);
+  if (kPass == kKeysPass && x.k0 >= x.k1) return;
+  x.ranks = splits;
+  x.kept = kPass == kFused ? reinterpret_cast<float2*>(smem + K::kSmemKept) : nullptr;
+  uint64_t* const rbars = reinterpret_cast<uint64_t*>(smem + K::kSmemBarR);
+  uint64_t* const kbars = reinterpret_cast<uint64_t*>(smem + K::kSmemBarK);
+  uint32_t* const words = reinterpret_cast<uint32_t*>(smem + K::kSmemWords);
+  x.abort_flag = reinterpret_cast<volatile int*>(words + 1);
+
+  if (warp == kTmaWarp) {
+    if constexpr (K::kRows) Bars<typename K::R>(rbars).init(lane);
+    if constexpr (K::kKeys) Bars<typename K::K>(kbars).init(lane);
+    fence_mbar_init();
+    if (lane == 0) *x.abort_flag = 0;
+  } else if (warp == kMmaWarp) {
+    tmem_alloc(words, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  x.tmem = words[0];
+
+  if constexpr (K::kRows) run_pass<kF32, false>(mk, a, x, rbars);
+  if constexpr (kPass == kFused) cluster_sync_all();  // the rows' sums are written
+  if constexpr (K::kKeys) {
+    if (!*x.abort_flag) run_pass<kF32, true>(mk, a, x, kbars);
+  }
+  if (warp == kMmaWarp) tmem_dealloc(x.tmem, 512);
+  if constexpr (kPass == kFused) {
+    __syncwarp();
+    cluster_sync_all();  // and read by all
+  }
 }
 
 struct Device {
   bool ready = false;
   int sms = 0;
 };
-// A pass of the call: its kernel, threads and shared memory.
-struct Pass {
+// A kernel of the call and its shared memory.
+struct Choice {
   void (*kernel)(CUtensorMap, WeighArgs);
-  int threads;
   uint32_t smem;
 };
-template <bool kF32, bool kWide>
-Pass pass_of(bool by_key) {
-  if (by_key) return {weigh_kernel<kF32, true, kWide>, Lay<kF32, true, kWide>::kThreads, Lay<kF32, true, kWide>::kSmemAlloc};
-  return {weigh_kernel<kF32, false, kWide>, Lay<kF32, false, kWide>::kThreads, Lay<kF32, false, kWide>::kSmemAlloc};
-}
-Pass pass_of(bool f32, bool wide, bool by_key) {
-  return f32 ? (wide ? pass_of<true, true>(by_key) : pass_of<true, false>(by_key))
-             : (wide ? pass_of<false, true>(by_key) : pass_of<false, false>(by_key));
+template <bool kF32>
+Choice choice(int pass) {
+  if (pass == kRowsPass) return {weigh_kernel<kF32, kRowsPass>, Kernel<kF32, kRowsPass>::kSmemAlloc};
+  if (pass == kKeysPass) return {weigh_kernel<kF32, kKeysPass>, Kernel<kF32, kKeysPass>::kSmemAlloc};
+  return {weigh_kernel<kF32, kFused>, Kernel<kF32, kFused>::kSmemAlloc};
 }
 
 int device(Device** out) {
@@ -687,8 +721,8 @@ int device(Device** out) {
   Device& d = devs[dev];
   if (!d.ready) {
     bool ok = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
-    for (int i = 0; i < 8; ++i) {
-      const Pass p = pass_of(i & 1, i & 2, i & 4);
+    for (int i = 0; i < 6; ++i) {
+      const Choice p = i & 1 ? choice<true>(i >> 1) : choice<false>(i >> 1);
       ok = ok && cudaFuncSetAttribute(p.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) == cudaSuccess;
     }
     if (!ok) {
@@ -704,16 +738,43 @@ int device(Device** out) {
 // Segments of the keys for `units` blocks each: the number whose rounds of one block an SM
 // take the least time, a block costing its tiles (each of them `passes` times) and as long
 // as four tiles besides.
-int plan(long long units, int max_keys, int passes, int sms) {
+int segments(long long units, int max_keys, int passes, int sms, double* least) {
   const int tiles = (max_keys + kKeys - 1) / kKeys;
   int best = 1;
-  double least = 1e300;
+  *least = 1e300;
   for (int s = 1; s <= kMaxSplits && s <= tiles; ++s) {
     const long long rounds = (units * s + sms - 1) / sms;
     const double time = (double)rounds * ((double)((tiles + s - 1) / s) * passes + 4.0 * passes);
-    if (time < least * 0.999) least = time, best = s;
+    if (time < *least * 0.999) *least = time, best = s;
   }
   return best;
+}
+
+// How a call runs: as one launch, with the rows' sums in shared memory, or as two launches with
+// the sums through memory. One launch where a block has a sequence's keys alone (44 sequences of
+// 5 rows at 320 to 3213, bf16 pages: 71 us, and 79 as two) or a cluster's blocks exchange their
+// sums and all have an SM at once (8 rows at 1000: 9.0 and 9.5); not in several rounds of
+// clusters (8 windows of 64 rows at 16384, bf16 pages: 217 us in clusters of seven, 126).
+struct Plan {
+  bool fused;
+  int splits, key_splits;
+};
+Plan plan(int B, int max_rows, int max_keys, int sms) {
+  const int tiles = (max_rows + kRows - 1) / kRows;
+  double rows = 0, keys = 0;
+  Plan p{};
+  p.splits = segments((long long)B * kHKV * tiles, max_keys, 1, sms, &rows);
+  p.key_splits = segments((long long)B * kHKV, max_keys, tiles, sms, &keys);
+  if (tiles > kFusedTiles) return p;
+  const int key_tiles = (max_keys + kKeys - 1) / kKeys;
+  double least = rows + keys;
+  for (int s = 1; s <= kMaxCluster && s <= key_tiles; ++s) {
+    const long long rounds = ((long long)B * kHKV * s + sms - 1) / sms;
+    if (s > 1 && rounds > 1) break;
+    const double time = (double)rounds * (2.0 * tiles * ((key_tiles + s - 1) / s) + 4.0 + 2.0 * tiles);
+    if (time < least * 0.999) least = time, p.fused = true, p.splits = s;
+  }
+  return p;
 }
 
 int max_keys(int max_context, int max_rows) {
@@ -726,8 +787,8 @@ int weigh_workspace_bytes(int B, int N, int max_rows, int max_context, size_t* b
   Device* d = nullptr;
   const int rc = device(&d);
   if (rc != ATTN_OK) return rc;
-  const int tiles = (max_rows + kRows - 1) / kRows;
-  *bytes = (size_t)N * kHQ * plan((long long)B * kHKV * tiles, max_keys(max_context, max_rows), 1, d->sms) * sizeof(float2);
+  const Plan p = plan(B, max_rows, max_keys(max_context, max_rows), d->sms);
+  *bytes = p.fused ? 0 : (size_t)N * kHQ * p.splits * sizeof(float2);
   return ATTN_OK;
 }
 
@@ -740,8 +801,7 @@ int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
   if ((rc = encode_rows_map(c.k_pages, bf16, (long long)c.num_pages * ATTN_PAGE, ATTN_PAGE, CU_TENSOR_MAP_SWIZZLE_128B,
                             &mk)) != ATTN_OK)
     return rc;
-  const int tiles = (c.max_rows + kRows - 1) / kRows;
-  const int keys = max_keys(c.max_context, c.max_rows);
+  const Plan p = plan(c.B, c.max_rows, max_keys(c.max_context, c.max_rows), d->sms);
   WeighArgs a{};
   a.q = c.q;
   a.weights = c.weights;
@@ -756,25 +816,28 @@ int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
   a.max_blocks = c.max_blocks;
   a.num_pages = c.num_pages;
   a.max_context = c.max_context;
-  a.row_tiles = tiles;
-  a.splits = plan((long long)c.B * kHKV * tiles, keys, 1, d->sms);
-  a.key_splits = plan((long long)c.B * kHKV, keys, tiles, d->sms);
+  a.row_tiles = (c.max_rows + kRows - 1) / kRows;
+  a.splits = p.splits;
+  a.key_splits = p.key_splits;
   a.decay = c.decay;
   a.err = err;
   a.timeout_ns = kTimeoutNs;
-  for (int by_key = 0; by_key < 2; ++by_key) {
-    const Pass p = pass_of(!bf16, c.max_rows >= kWideRows, by_key);
+  for (int pass = p.fused ? kFused : kRowsPass; pass <= (p.fused ? kFused : kKeysPass); ++pass) {
+    const Choice k = bf16 ? choice<false>(pass) : choice<true>(pass);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(by_key ? a.key_splits : a.splits * tiles, kHKV, c.B);
-    cfg.blockDim = dim3(p.threads);
-    cfg.dynamicSmemBytes = p.smem;
+    cfg.gridDim = dim3(pass == kRowsPass ? a.splits * a.row_tiles : pass == kKeysPass ? a.key_splits : a.splits, kHKV, c.B);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = k.smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    if (launched(cudaLaunchKernelEx(&cfg, p.kernel, mk, a)) != cudaSuccess) return ATTN_ELAUNCH;
+    cfg.numAttrs = pass == kFused ? 2 : 1;
+    if (launched(cudaLaunchKernelEx(&cfg, k.kernel, mk, a)) != cudaSuccess) return ATTN_ELAUNCH;
   }
   return ATTN_OK;
 }

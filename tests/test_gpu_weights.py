@@ -255,13 +255,13 @@ def test_refusals(cp):
         with pytest.raises(cp.AttnError) as e:
             cp.attn_decode_weigh_paged(q[:2], b["kp"], b["vp"], w, b["table"], b["ctx"], out, 30000, workspace=ws)
         assert e.value.code == cp.ATTN_ESPACE
-    need = cp.attn_weigh_workspace_bytes(2, 3, 2, 100)
+    need = cp.attn_weigh_workspace_bytes(2, 3, 65, 100)  # too many rows for their sums to stay on chip
     for ws in (None, torch.empty(need - 1, dtype=torch.uint8, device="cuda")):
         with pytest.raises(cp.AttnError) as e:
-            cp.attn_weigh_paged(q, b["kp"], w, b["table"], b["ctx"], b["starts"], 2, 100, workspace=ws)
+            cp.attn_weigh_paged(q, b["kp"], w, b["table"], b["ctx"], b["starts"], 65, 100, workspace=ws)
         assert e.value.code == cp.ATTN_ESPACE
     with pytest.raises(cp.AttnError) as e:
-        cp.attn_weigh_paged(q, b["kp"], w, b["table"], b["ctx"], b["starts"], 2, 100, workspace=workspace(need + 16)[8:])
+        cp.attn_weigh_paged(q, b["kp"], w, b["table"], b["ctx"], b["starts"], 65, 100, workspace=workspace(need + 16)[8:])
     assert e.value.code == cp.ATTN_EALIGN
     for bad in (w[:, :, :8], w.half(), w.cpu(), w[1:], w.transpose(1, 2)):
         with pytest.raises(ValueError):

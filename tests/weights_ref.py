@@ -38,7 +38,7 @@ def get_weights(pool, batch, b, n):
     return pool[page[:, None], torch.arange(HKV, device="cuda")[None], (tok % PAGE)[:, None]]
 
 
-def softmax_reference(q, k, seen, wide=False):
+def softmax_reference(q, k, seen):
     """(p, relative error of a row's p's) of one head in fp64: q [t][64], k [n][64], seen [t][n].
 
     As for attention of drafted rows: a product keeps all but 2^-19 of |x y|, a score's
@@ -47,15 +47,12 @@ def softmax_reference(q, k, seen, wide=False):
     joins partial sums lie within 2^-21 each: eps_j, in the numerator and in the sum.
     The sum's own chains are at most n / 4 + 100 rounded additions of positive terms, and
     where it is kept as a logarithm, m log2 e + log2 sum <= 1.45 |m| + 20, that rounds
-    twice at 2^-24 of it, in the exponent again.
-    wide: a window of at least 8 rows, whose operands are kept in two bf16 terms: q, and k of
-    fp32 pages, to 2^-18 each (two roundings of 2^-9), and the product of the two second terms,
-    at most 2^-18 of |x y|, is left out: 3 2^-18 instead of 2^-19."""
+    twice at 2^-24 of it, in the exponent again."""
     s = (q @ k.T / 8).masked_fill(~seen, float("-inf"))
     m = s.amax(-1, keepdim=True)
     p = torch.softmax(s, -1)
     A = (q.abs() @ k.abs().T / 8).masked_fill(~seen, 0.0)
-    eps = ((3 * 2.0 ** -18 if wide else 2.0 ** -19) + 24 * 2.0 ** -23) * A + 3 * 2.0 ** -24 * 1.45 * (s.masked_fill(~seen, 0.0).abs() + m.abs()) + 2.0 ** -21
+    eps = (2.0 ** -19 + 24 * 2.0 ** -23) * A + 3 * 2.0 ** -24 * 1.45 * (s.masked_fill(~seen, 0.0).abs() + m.abs()) + 2.0 ** -21
     n = k.shape[0]
     rel = 2 * eps.amax(-1, keepdim=True) + (n / 4 + 100) * 2.0 ** -24 + 2.0 ** -23 * (1.45 * m.abs() + 20)
     return p, rel
@@ -80,8 +77,7 @@ def weigh_reference(q, batch, weights, weighed, decay, decode=False):
         had = torch.where((tok < weighed[b])[:, None], old * decay if decay else torch.zeros_like(old), torch.zeros_like(old))
         w, tol = had.clone(), torch.zeros_like(had)
         for h in range(HQ):
-            p, rel = softmax_reference(q[r:r + rows, h].double(), k[:, h // GROUP], seen.expand(rows, n),
-                                       not decode and batch["max_rows"] >= 8)
+            p, rel = softmax_reference(q[r:r + rows, h].double(), k[:, h // GROUP], seen.expand(rows, n))
             w[:, h // GROUP] += p.sum(0)
             tol[:, h // GROUP] += (p * rel).sum(0)
             if decode:

@@ -55,8 +55,8 @@ EXPORTS = ("attn_prefill", "attn_prefill_bf16x3", "attn_prefill_bf16kv", "attn_p
            "attn_evict_paged", "attn_evict_paged_bf16kv", "attn_evict_workspace_bytes",
            "attn_naive_workspace_bytes", "attn_naive_scores", "attn_naive_softmax", "attn_naive_weighted_sum",
            "attn_naive_prefill", "attn_prefill_ffma", "attn_reference_prefill", "attn_selftest_timeout",
-           "attn_selftest_decode_timeout", "attn_selftest_tree_timeout", "attn_tensor_peak", "attn_get_device_error", "attn_strerror",
-           "attn_version")
+           "attn_selftest_decode_timeout", "attn_selftest_tree_timeout", "attn_selftest_decode_weigh_timeout",
+           "attn_selftest_weigh_timeout", "attn_tensor_peak", "attn_get_device_error", "attn_strerror", "attn_version")
 
 _lock = threading.Lock()
 _lib = None
@@ -157,6 +157,11 @@ def load():
             lib.attn_naive_scores.argtypes = [vp, vp, vp, ci, ci, vp]
             lib.attn_naive_softmax.restype = ci
             lib.attn_naive_softmax.argtypes = [vp, ci, ci, vp]
+            cf = ctypes.c_float
+            lib.attn_selftest_decode_weigh_timeout.restype = ci
+            lib.attn_selftest_decode_weigh_timeout.argtypes = [vp] * 3 + [ci] + [vp] * 4 + [cf, vp] + [ci] * 5 + [vp, cs, vp]
+            lib.attn_selftest_weigh_timeout.restype = ci
+            lib.attn_selftest_weigh_timeout.argtypes = [vp, vp, ci] + [vp] * 5 + [cf] + [ci] * 7 + [vp, cs, vp]
             lib.attn_naive_weighted_sum.restype = ci
             lib.attn_naive_weighted_sum.argtypes = [vp, vp, vp, ci, ci, vp]
             lib.attn_naive_prefill.restype = ci
@@ -638,7 +643,8 @@ def attn_compact_paged_bf16kv(kPages, vPages, blockTable, contextLens, keep, kee
 
 
 def attn_decode_weigh_workspace_bytes(B: int, max_context: int) -> int:
-    """Bytes of workspace attn_decode_weigh_paged (either page type) needs on the current device."""
+    """Bytes of workspace attn_decode_weigh_paged (either page type) needs on the current
+    device: 0 for calls small enough to run as one launch."""
     return int(load().attn_decode_weigh_workspace_bytes(int(B), int(max_context)))
 
 
@@ -651,7 +657,7 @@ def attn_decode_weigh_paged(q, kPages, vPages, weights, blockTable, contextLens,
     head's four queries, and for tokens from weighedLens[b] on (int32 [B]; None:
     contextLens[b] - 1) that sum alone. contextLens counts the new token.
     ``workspace``: a CUDA tensor of attn_decode_weigh_workspace_bytes(B, max_context)
-    bytes. Returns out."""
+    bytes, or None where that is 0. Returns out."""
     rc = (_binding or _native()).decode_weigh_paged(False, q, kPages, vPages, weights, blockTable, contextLens, out,
                                                     max_context, decay, weighedLens, workspace, stream)
     if rc:
@@ -670,7 +676,8 @@ def attn_decode_weigh_paged_bf16kv(q, kPages, vPages, weights, blockTable, conte
 
 
 def attn_weigh_workspace_bytes(B: int, N: int, max_rows: int, max_context: int) -> int:
-    """Bytes of workspace attn_weigh_paged (either page type) needs on the current device."""
+    """Bytes of workspace attn_weigh_paged (either page type) needs on the current device: 0 for
+    windows that run as one launch."""
     return int(load().attn_weigh_workspace_bytes(int(B), int(N), int(max_rows), int(max_context)))
 
 
@@ -683,7 +690,8 @@ def attn_weigh_paged(q, kPages, weights, blockTable, contextLens, rowStart, max_
     key is in the cache, and sees the tokens up to it. weights as
     attn_decode_weigh_paged; weighedLens None: contextLens, all but the rows' own.
     max_rows and max_context bound the batch. ``workspace``: a CUDA tensor of
-    attn_weigh_workspace_bytes(B, N, max_rows, max_context) bytes. Returns weights."""
+    attn_weigh_workspace_bytes(B, N, max_rows, max_context) bytes, or None where that is 0.
+    Returns weights."""
     rc = (_binding or _native()).weigh_paged(False, q, kPages, weights, blockTable, contextLens, rowStart, max_rows,
                                              max_context, decay, weighedLens, workspace, stream)
     if rc:
@@ -701,8 +709,64 @@ def attn_weigh_paged_bf16kv(q, kPages, weights, blockTable, contextLens, rowStar
     return weights
 
 
+def _selftest_pages(kPages, tensors):
+    """The page type of a failure-path test's calls, its tensors (name: (tensor, dtype)) checked."""
+    import torch
+    page = kPages.dtype
+    if (page not in (torch.float32, torch.bfloat16) or kPages.dim() != 4 or tuple(kPages.shape[1:]) != (16, HKV, D)
+            or any(not t.is_cuda or not t.is_contiguous() or t.dtype != (page if want is None else want)
+                   for t, want in tensors.values() if t is not None)):
+        raise ValueError("shapes, types or pages not as those of the call that is tested")
+    return F32 if page == torch.float32 else BF16
+
+
+def attn_selftest_decode_weigh_timeout(q, kPages, vPages, weights, blockTable, contextLens, out, max_context: int,
+                                       decay: float = 1.0, weighedLens=None, workspace=None, withheld: int = 1, stream=None):
+    """Failure-path test of the decode step that weighs (arguments as
+    attn_decode_weigh_paged, the page type by kPages): the first keys of the first
+    ``withheld`` segments never arrive, their waits expire after 20 ms and ATTN_ETIMEOUT is
+    recorded; read it with attn_get_device_error(). Their tokens' weights stay."""
+    import torch
+    f, i = torch.float32, torch.int32
+    page = _selftest_pages(kPages, {"q": (q, f), "k": (kPages, None), "v": (vPages, None), "w": (weights, f), "out": (out, f),
+                                    "table": (blockTable, i), "ctx": (contextLens, i), "weighed": (weighedLens, i)})
+    B = q.shape[0]
+    if (tuple(q.shape[1:]) != (HQ, D) or out.shape != q.shape or vPages.shape != kPages.shape or blockTable.dim() != 2
+            or blockTable.shape[0] != B or tuple(weights.shape) != (kPages.shape[0], HKV, 16)
+            or any(t is not None and tuple(t.shape) != (B,) for t in (contextLens, weighedLens))):
+        raise ValueError("shapes not as attn_decode_weigh_paged's")
+    rc = load().attn_selftest_decode_weigh_timeout(
+        _ptr(q), _ptr(kPages), _ptr(vPages), page, _ptr(weights), _ptr(blockTable), _ptr(contextLens), _ptr(weighedLens),
+        float(decay), _ptr(out), B, blockTable.shape[1], kPages.shape[0], int(max_context), int(withheld), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_selftest_decode_weigh_timeout")
+    return out
+
+
+def attn_selftest_weigh_timeout(q, kPages, weights, blockTable, contextLens, rowStart, max_rows: int, max_context: int,
+                                decay: float = 1.0, weighedLens=None, workspace=None, withheld: int = 1, stream=None):
+    """The same test of attn_weigh_paged."""
+    import torch
+    f, i = torch.float32, torch.int32
+    page = _selftest_pages(kPages, {"q": (q, f), "k": (kPages, None), "w": (weights, f), "table": (blockTable, i),
+                                    "ctx": (contextLens, i), "starts": (rowStart, i), "weighed": (weighedLens, i)})
+    B = blockTable.shape[0]
+    if (tuple(q.shape[1:]) != (HQ, D) or blockTable.dim() != 2 or tuple(weights.shape) != (kPages.shape[0], HKV, 16)
+            or tuple(rowStart.shape) != (B + 1,)
+            or any(t is not None and tuple(t.shape) != (B,) for t in (contextLens, weighedLens))):
+        raise ValueError("shapes not as attn_weigh_paged's")
+    rc = load().attn_selftest_weigh_timeout(
+        _ptr(q), _ptr(kPages), page, _ptr(weights), _ptr(blockTable), _ptr(contextLens), _ptr(rowStart), _ptr(weighedLens),
+        float(decay), B, q.shape[0], int(max_rows), blockTable.shape[1], kPages.shape[0], int(max_context), int(withheld),
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_selftest_weigh_timeout")
+    return weights
+
+
 def attn_evict_workspace_bytes(B: int, max_context: int) -> int:
-    """Bytes of workspace attn_evict_paged (either page type) needs."""
+    """Bytes of workspace attn_evict_paged (either page type) needs: 0 up to a max_context of 4096."""
     return int(load().attn_evict_workspace_bytes(int(B), int(max_context)))
 
 
@@ -712,7 +776,7 @@ def attn_evict_paged(kPages, vPages, weights, blockTable, contextLens, keepLens,
     first keep_first, its last keep_last and, of those between, the ones of the largest
     weights, which close up (keys, values and weights; not in their old order). The
     context is min(contextLens, keepLens) afterwards. ``workspace``: a CUDA tensor of
-    attn_evict_workspace_bytes(B, max_context) bytes."""
+    attn_evict_workspace_bytes(B, max_context) bytes, or None where that is 0."""
     rc = (_binding or _native()).evict_paged(False, kPages, vPages, weights, blockTable, contextLens, keepLens,
                                              max_context, keep_first, keep_last, workspace, stream)
     if rc:

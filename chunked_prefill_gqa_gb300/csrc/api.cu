@@ -774,7 +774,7 @@ extern "C" int attn_decode_weigh_paged(const float* q, const float* kPages, cons
                                        float decay, float* out, int B, int maxBlocks, int numPages, int maxContext,
                                        void* workspace, size_t workspaceBytes, cudaStream_t stream) {
   return decode_weigh_paged(DecodeWeighCall{q, kPages, vPages, ATTN_F32, weights, blockTable, contextLens, weighedLens, out,
-                                            workspace, B, maxBlocks, numPages, maxContext, decay},
+                                            workspace, B, maxBlocks, numPages, maxContext, decay, 0},
                             workspaceBytes, stream);
 }
 
@@ -784,7 +784,19 @@ extern "C" int attn_decode_weigh_paged_bf16kv(const float* q, const uint16_t* kP
                                               int numPages, int maxContext, void* workspace, size_t workspaceBytes,
                                               cudaStream_t stream) {
   return decode_weigh_paged(DecodeWeighCall{q, kPages, vPages, ATTN_BF16, weights, blockTable, contextLens, weighedLens,
-                                            out, workspace, B, maxBlocks, numPages, maxContext, decay},
+                                            out, workspace, B, maxBlocks, numPages, maxContext, decay, 0},
+                            workspaceBytes, stream);
+}
+
+extern "C" int attn_selftest_decode_weigh_timeout(const float* q, const void* kPages, const void* vPages, int pageType,
+                                                  float* weights, const int* blockTable, const int* contextLens,
+                                                  const int* weighedLens, float decay, float* out, int B, int maxBlocks,
+                                                  int numPages, int maxContext, int withheld, void* workspace,
+                                                  size_t workspaceBytes, cudaStream_t stream) {
+  if (B < 1 || withheld < 1) return ATTN_EINVAL;  // nothing to withhold
+  if (pageType != ATTN_F32 && pageType != ATTN_BF16) return ATTN_EINVAL;
+  return decode_weigh_paged(DecodeWeighCall{q, kPages, vPages, pageType, weights, blockTable, contextLens, weighedLens, out,
+                                            workspace, B, maxBlocks, numPages, maxContext, decay, withheld},
                             workspaceBytes, stream);
 }
 
@@ -799,7 +811,7 @@ extern "C" int attn_weigh_paged(const float* q, const float* kPages, float* weig
                                 int N, int maxRows, int maxBlocks, int numPages, int maxContext, void* workspace,
                                 size_t workspaceBytes, cudaStream_t stream) {
   return weigh_paged(WeighCall{q, kPages, ATTN_F32, weights, blockTable, contextLens, rowStart, weighedLens, workspace, B, N,
-                               maxRows, maxBlocks, numPages, maxContext, decay},
+                               maxRows, maxBlocks, numPages, maxContext, decay, 0},
                      workspaceBytes, stream);
 }
 
@@ -808,7 +820,19 @@ extern "C" int attn_weigh_paged_bf16kv(const float* q, const uint16_t* kPages, f
                                        int B, int N, int maxRows, int maxBlocks, int numPages, int maxContext,
                                        void* workspace, size_t workspaceBytes, cudaStream_t stream) {
   return weigh_paged(WeighCall{q, kPages, ATTN_BF16, weights, blockTable, contextLens, rowStart, weighedLens, workspace, B,
-                               N, maxRows, maxBlocks, numPages, maxContext, decay},
+                               N, maxRows, maxBlocks, numPages, maxContext, decay, 0},
+                     workspaceBytes, stream);
+}
+
+extern "C" int attn_selftest_weigh_timeout(const float* q, const void* kPages, int pageType, float* weights,
+                                           const int* blockTable, const int* contextLens, const int* rowStart,
+                                           const int* weighedLens, float decay, int B, int N, int maxRows, int maxBlocks,
+                                           int numPages, int maxContext, int withheld, void* workspace,
+                                           size_t workspaceBytes, cudaStream_t stream) {
+  if (B < 1 || N < 1 || withheld < 1) return ATTN_EINVAL;
+  if (pageType != ATTN_F32 && pageType != ATTN_BF16) return ATTN_EINVAL;
+  return weigh_paged(WeighCall{q, kPages, pageType, weights, blockTable, contextLens, rowStart, weighedLens, workspace, B, N,
+                               maxRows, maxBlocks, numPages, maxContext, decay, withheld},
                      workspaceBytes, stream);
 }
 

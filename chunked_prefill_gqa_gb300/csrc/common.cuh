@@ -178,6 +178,7 @@ struct DecodeWeighCall {
   void* workspace;
   int B, max_blocks, num_pages, max_context;
   float decay;
+  int withheld;  // failure test: segments that never get their first keys, and every wait limited to 20 ms
 };
 int decode_weigh_workspace_bytes(int B, int max_context, size_t* bytes);
 int launch_decode_weigh(const DecodeWeighCall& c, unsigned* err, cudaStream_t stream);
@@ -192,6 +193,7 @@ struct WeighCall {
   void* workspace;
   int B, N, max_rows, max_blocks, num_pages, max_context;
   float decay;
+  int withheld;  // as above
 };
 int weigh_workspace_bytes(int B, int N, int max_rows, int max_context, size_t* bytes);
 int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream);

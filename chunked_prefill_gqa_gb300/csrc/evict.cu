@@ -11,13 +11,18 @@
 // - first = m places are below edge). A cache cut from n to n / 2 tokens so moves about n /
 // 4 rows a head instead of n / 2 kept in order.
 //
-// Two launches. select_kernel: a cluster of blocks per (sequence, head) finds the m-th
-// largest weight by its digits (12, 10 and 10 bits of the weights mapped to ordered
-// integers, a histogram in shared memory, the cluster's added up through distributed
-// shared memory), then walks its tokens once more and writes both lists. move_kernel moves
-// the rows: sources at or past new are written by nobody, so those go in any order; what
-// lies between edge and new is read (as sources of holes) before one block per (sequence,
-// head) writes the last ones there, batch by batch.
+// Up to kSmall tokens a block does both steps from registers and shared memory, in one launch
+// (small_kernel). Longer contexts take two. select_kernel: a cluster of blocks per (sequence,
+// head) finds the m-th largest weight by its digits (12, 10 and 10 bits of the weights mapped to
+// ordered integers, a histogram in shared memory, the cluster's added up through distributed
+// shared memory), then walks its tokens once more and writes both lists. move_kernel moves the
+// rows: sources at or past new are written by nobody, so those go in any order; what lies between
+// edge and new is read (as sources of holes) before one block per (sequence, head) writes the
+// last ones there, batch by batch.
+//
+// Bound by the moves' latency and bytes: 16 sequences of 16384 tokens to half (bf16 pages) read and
+// write 287 MB in the 81 us of the call with its 6 us of restored weights: select 20, move 45 (their
+// floor 43 together). Rows of 128 bytes at random places move at 6.2 TB/s.
 #include <cstdint>
 #include <mutex>
 
@@ -29,11 +34,10 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 // Digits of 12, 10 and 10 bits: with three bits of the fraction in the first one, the weights of
-// a warp (within a few powers of two) seldom meet in a bin (XXX).
+// a warp (within a few powers of two) seldom meet in a bin.
 constexpr int kBins = 4096, kFirst = 20, kDigit = 10;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxCached = 40960;  // tokens of a block whose keys stay in shared memory (160 KB of its 227; the rest takes 50)
-
 struct EvictArgs {
   void *k_pages, *v_pages;
   float* weights;             // [num_pages][8][16]
@@ -151,7 +155,7 @@ __device__ __forceinline__ void choose(Shared<kThreads>& sh, int ranks, int pass
 }
 
 // Four tokens' keys, a quarter of a page, are looked at together. (16 sequences of 16384 tokens:
-// XXX us; 32 with every digit counted over all keys, 250 instructions for each 32 of them.)
+// 20 us; 32 with every digit counted over all keys, 250 instructions for each 32 of them.)
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   constexpr int kWarps = kThreads / 32, kPerThread = kBins / kThreads;
@@ -501,7 +505,9 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
 // Both steps in one launch, for contexts of up to kSmall tokens: a thread has two quads' keys in
 // registers, the first digit's bin settles all but a few keys, whose ranks are counted among
 // themselves (or, of many equal ones, by further digits), and what stays is a bit a token. A
-// cluster's blocks all find the same lists, in shared memory, and share the moves. XXX measured
+// cluster's blocks all find the same lists, in shared memory, and share the moves.
+// (One sequence of 1000 tokens: 8.5 us in a graph; 11.7 with the copy that restores its weights, 14.4 as two
+// launches; one of 4000, bf16 pages: 14.3 and 17.8; 64 of 4000: 76 and 85.)
 constexpr int kSmall = 4096, kSmallThreads = 512, kQuads = kSmall / 4 / kSmallThreads, kWords = kSmall / 32;
 constexpr int kRanked = 256;  // listed keys whose ranks are counted
 
@@ -798,11 +804,14 @@ int launch_evict(const EvictCall& c, unsigned* err, cudaStream_t stream) {
     ranks *= 2;
   const int span = ((c.max_context + ATTN_PAGE - 1) / ATTN_PAGE + ranks - 1) / ranks * ATTN_PAGE;
   a.cached = span <= kMaxCached;
-  // Threads by a block's tokens: few wait less for each other (1000 tokens: 512 threads XXX us,
-  // 1024 XXX), many have more under way (16384 tokens: XXX and XXX).
-  const bool wide = span > 4096;
+  // Threads by a block's tokens. Blocks of 512 share an SM, and one counts while the other waits
+  // (40 sequences of 6000 tokens: 82 us for the call, 96 with 1024; 30 of 10000: 91 and 102);
+  // with 1024 more is under way where an SM holds one or two such blocks' keys (60 of up to
+  // 14000: 165 and 157; 16 of 16384: 92 and 81).
+  const bool wide = span > 12288;
+  const size_t keys = a.cached ? (size_t)span * sizeof(uint32_t) : 0;
   const auto kernel = wide ? select_kernel<1024> : select_kernel<512>;
-  const size_t smem = (wide ? sizeof(Shared<1024>) : sizeof(Shared<512>)) + (a.cached ? (size_t)span * sizeof(uint32_t) : 0);
+  const size_t smem = (wide ? sizeof(Shared<1024>) : sizeof(Shared<512>)) + keys;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ranks, kHKV, c.B);
   cfg.blockDim = dim3(wide ? 1024 : 512);

@@ -21,9 +21,11 @@
 //   fp32 pages: q K_lo + q_lo K + q K, tf32 terms: 3 x 8 of 128 x 128 x 8
 // (K is read truncated; K_lo is the remainder rounded to tf32, q's first term rounded too.) By
 // key, windows of fewer rows take fewer columns. Fewer terms were measured and not kept: with two
-// bf16 terms in both passes 64 rows of 131071 tokens (bf16 pages) took 119 us for XXX, 32 rows of
-// 16 sequences of 16384 (fp32) 205 for XXX, but weights were off by 2e-6 to 4e-6 where a plain
-// fp32 computation is by 5e-7; in the rows pass alone, as much.
+// bf16 terms in both passes 64 rows of 131071 tokens (bf16 pages) took 119 us for 144, 32 rows of
+// 16 sequences of 16384 (fp32) 205 for 278, but weights were off by 2e-6 to 4e-6 where a plain
+// fp32 computation is by 5e-7; in the rows pass alone, as much. Bound by the products: those 278
+// us are 1.37 PFLOP/s of tf32 terms at the rate of 174 us, and K's bytes, read twice, are 83 us;
+// the 144 are 112 of bf16 terms at the rate of a library product.
 //
 // Roles: three groups of four warps take the tiles in turn; four warps that write K_lo (fp32,
 // rows) or move K to tensor memory (keys); one warp for TMA (16-token pages through the block
@@ -64,6 +66,7 @@ struct WeighArgs {
   int row_tiles, splits;   // of the rows pass
   int key_splits;          // of the keys pass
   float decay;
+  int withheld;            // failure test: segments whose first tile is never loaded
   unsigned* err;
   unsigned long long timeout_ns;
 };
@@ -239,7 +242,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs&
           if (lane == 0) mbar_arrive_expect_tx(&kfull[st], pages * (kF32 ? 2 : 1) * kBox);
           last = it;
           __syncwarp();
-          if (has)
+          if (has && !(it == 0 && s < a.withheld))
             tma_load_2d(smem + st * L::kStageBytes + half * kHalf + p * kBox, &mk, &kfull[st], head * kD + half * 32,
                         page * ATTN_PAGE);
         }
@@ -393,7 +396,10 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs&
       const size_t pair = (size_t)(seq.first + i0 + (row >> 2)) * kHQ + head * kGroup + (row & 3);
       if (rt > rt0) {  // what the tile before needs is still in use; its weights are written
         int over;
-        if (meet(kMeet, false, failed, lane, &over)) break;
+        if (meet(kMeet, false, failed, lane, &over)) {
+          for (int x = rt; !kByKey && g == 0 && x_.kept && x < rt1; ++x) x_.kept[(x - rt0) * 128 + row] = make_float2(kUnseen, 0.f);
+          break;
+        }
       }
       // q in its terms; rows past the last are zeros.
 #pragma unroll 1
@@ -821,7 +827,8 @@ int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
   a.key_splits = p.key_splits;
   a.decay = c.decay;
   a.err = err;
-  a.timeout_ns = kTimeoutNs;
+  a.withheld = c.withheld;
+  a.timeout_ns = c.withheld ? kFaultNs : kTimeoutNs;
   for (int pass = p.fused ? kFused : kRowsPass; pass <= (p.fused ? kFused : kKeysPass); ++pass) {
     const Choice k = bf16 ? choice<false>(pass) : choice<true>(pass);
     cudaLaunchConfig_t cfg = {};

@@ -22,9 +22,9 @@
  * call. The
  * prefill entry points take no workspace: there is no score matrix anywhere
  * (the contract has no workspace argument). q, kCache and vCache are only
- * read. Two families outside that contract take a caller-owned workspace,
- * described with them: split-KV decode (its segment partials) and the
- * score-matrix pipeline (the matrix itself).
+ * read. Some families outside that contract take a caller-owned workspace,
+ * described with them: split-KV decode and drafted trees (their segment partials),
+ * the calls on cache weights, and the score-matrix pipeline (the matrix itself).
  *
  * Execution. Every compute entry point validates its arguments on the host,
  * enqueues its kernel(s) on `stream` and returns; completion is observed by
@@ -568,7 +568,7 @@ int attn_compact_paged_bf16kv(uint16_t *kPages, uint16_t *vPages, const int *blo
  * weights that it reaches NaN; slots past the context may hold anything. `workspace`:
  * attn_decode_weigh_workspace_bytes(B, maxContext) bytes, 16-byte aligned,
  * overwritten (16 bytes a token and head, which the weights are made of, and the
- * segments' partials). A context length outside [0, maxContext] or a page index
+ * segments' partials; small calls need none, and the pointer may be NULL). A context length outside [0, maxContext] or a page index
  * outside [0, numPages) is recorded as ATTN_EBOUNDS and clamped / read as zeros (its
  * tokens' weights stay). Two sequences of a call must not share pages (weights are
  * written). Errors: as attn_decode_paged, ATTN_EINVAL (NULL weights, decay outside
@@ -585,9 +585,10 @@ int attn_decode_weigh_paged_bf16kv(const float *q, const uint16_t *kPages, const
 
 /*
  * attn_decode_weigh_workspace_bytes -- the workspace of the two calls above for the
- * same sizes on the current device; 0 for invalid arguments. A batch of fewer
- * sequences may be cut into more segments: a buffer for all batches of a program is
- * the largest of their sizes.
+ * same sizes on the current device; 0 where none is needed (a call that a cluster of
+ * up to eight blocks a sequence and head takes in one launch) and for invalid arguments.
+ * A batch of fewer sequences may be cut into more segments: a buffer for all batches
+ * of a program is the largest of their sizes.
  */
 size_t attn_decode_weigh_workspace_bytes(int B, int maxContext);
 
@@ -607,7 +608,8 @@ size_t attn_decode_weigh_workspace_bytes(int B, int maxContext);
  * which only the last rows are weighed it is what was weighed before (0 at first).
  * A sequence without rows is left as it is; rows behind the last sequence are not
  * read. `workspace`: attn_weigh_workspace_bytes(B, N, maxRows, maxContext) bytes,
- * 16-byte aligned, overwritten. Pages, bounds, clamping and errors as
+ * 16-byte aligned, overwritten (none for windows of up to 64 rows that run as one
+ * launch; the pointer may then be NULL). Pages, bounds, clamping and errors as
  * attn_tree_paged, ATTN_EINVAL (NULL weights, decay outside [0, 1]), ATTN_ERANGE
  * (maxRows above 65536). Two sequences of a call must not share pages. B == 0 or N ==
  * 0 is a no-op.
@@ -623,8 +625,8 @@ int attn_weigh_paged_bf16kv(const float *q, const uint16_t *kPages, float *weigh
 
 /*
  * attn_weigh_workspace_bytes -- the workspace of the two calls above for the same
- * sizes on the current device; 0 for invalid arguments. Not monotone in the batch, as
- * above.
+ * sizes on the current device; 0 where none is needed and for invalid arguments. Not
+ * monotone in the batch, as above.
  */
 size_t attn_weigh_workspace_bytes(int B, int N, int maxRows, int maxContext);
 
@@ -646,7 +648,8 @@ size_t attn_weigh_workspace_bytes(int B, int N, int maxRows, int maxContext);
  * where tokens have to leave, below keepFirst + keepLast, or one of whose pages is
  * outside [0, numPages) is recorded as ATTN_EBOUNDS and left as it is. Sequences must
  * not share pages. `workspace`: attn_evict_workspace_bytes(B, maxContext) bytes, 16-byte
- * aligned, overwritten. Errors: ATTN_EINVAL (NULL pointer, negative size or keep
+ * aligned, overwritten (none up to a maxContext of 4096; the pointer may then be NULL).
+ * Errors: ATTN_EINVAL (NULL pointer, negative size or keep
  * count, maxBlocks or numPages < 1), ATTN_ERANGE (maxContext above 16 * maxBlocks,
  * keepFirst or keepLast above ATTN_MAX_TOKENS, the bounds of attn_append_paged),
  * ATTN_EALIGN, ATTN_ESPACE. B == 0 or maxContext == 0 is a no-op.
@@ -661,7 +664,7 @@ int attn_evict_paged_bf16kv(uint16_t *kPages, uint16_t *vPages, float *weights, 
 
 /*
  * attn_evict_workspace_bytes -- the workspace of the two calls above: it grows with B
- * and with maxContext; 0 for invalid arguments.
+ * and with maxContext; 0 up to a maxContext of 4096 and for invalid arguments.
  */
 size_t attn_evict_workspace_bytes(int B, int maxContext);
 
@@ -763,6 +766,28 @@ int attn_selftest_tree_timeout(const float *q, const void *kPages, const void *v
                                const long long *masks, float *out, int B, int N, int maxRows, int maxBlocks,
                                int numPages, int maxContext, int numSplits, int withheld, void *workspace,
                                size_t workspaceBytes, cudaStream_t stream);
+
+/*
+ * attn_selftest_decode_weigh_timeout, attn_selftest_weigh_timeout -- the same test for
+ * attn_decode_weigh_paged and attn_weigh_paged (pageType ATTN_F32) or their _bf16kv
+ * forms (ATTN_BF16): the first `withheld` segments of every (sequence, head) never get
+ * their first keys and every bounded wait is limited to 20 ms. Their blocks record
+ * ATTN_ETIMEOUT, wind down and count as segments without keys: the outputs and the
+ * weights that the other segments' tokens are given are of those segments alone, the
+ * withheld ones' weights stay; out stays unwritten where all of a context lies in one
+ * segment of its own, and is zeros where every segment of several is withheld. The
+ * context stays usable. Requires B, N and withheld >= 1 (ATTN_EINVAL otherwise).
+ */
+int attn_selftest_decode_weigh_timeout(const float *q, const void *kPages, const void *vPages, int pageType,
+                                       float *weights, const int *blockTable, const int *contextLens,
+                                       const int *weighedLens, float decay, float *out, int B, int maxBlocks,
+                                       int numPages, int maxContext, int withheld, void *workspace,
+                                       size_t workspaceBytes, cudaStream_t stream);
+int attn_selftest_weigh_timeout(const float *q, const void *kPages, int pageType, float *weights,
+                                const int *blockTable, const int *contextLens, const int *rowStart,
+                                const int *weighedLens, float decay, int B, int N, int maxRows, int maxBlocks,
+                                int numPages, int maxContext, int withheld, void *workspace, size_t workspaceBytes,
+                                cudaStream_t stream);
 
 /*
  * attn_tensor_peak -- a measurement of this GPU's tensor pipe, not an

@@ -7,13 +7,15 @@
 // reads K and V once keeps the scores (16 bytes a token and KV head, where K and V are 256 or
 // 512), and the weights are added from them afterwards. Two forms:
 //   cluster  up to eight segments of a (sequence, KV head) are one cluster of blocks. Each
-//            keeps its scores in shared memory (up to 2560 tokens), they exchange maxima and
+//            keeps its scores in shared memory (up to 2448 tokens), they exchange maxima and
 //            sums through distributed shared memory, and each adds its own tokens' weights:
 //            one launch, nothing through memory but what the call is about
 //   memory   longer contexts: scores and partials in the workspace, a second kernel merges
+// (Clusters whose scores wait in tensor memory, 8192 tokens a block, were built: 16 sequences of
+// 16384 tokens, bf16 pages, 98 us for 101, lengths of 1600 to 16384 63 for 60.)
 //
-// A block owns (segment, KV head, sequence), each of its four warps every
-// fourth 16-token page, which arrives by TMA in a ring of the warp's own; warps meet only
+// A block owns (segment, KV head, sequence), each of its warps (eight, four on fp32 pages) every
+// eighth (fourth) 16-token page, which arrives by TMA in a ring of the warp's own; warps meet only
 // at the end. A page is exactly the 16 rows of mma.sync, keys on the M side, and the 8
 // columns of N hold the four query heads in two terms each, so a thread ends with the
 // scores of two keys and one head, already summed over the terms:
@@ -23,8 +25,10 @@
 // fp32 precision. A page's products start at zero and join the fp32 sums rounded to
 // nearest. A head's reference maximum moves when a score passes it by 2^8.
 //
-// Bound by reading K and V: 16 sequences of 16384 tokens (bf16 pages, 551 MB) 104 us, 5.3 TB/s; one
-// of 131071 (bf16, 274 MB) 58 us; 48 of 410 to 4096 (fp32, 453 MB) 82 us, 5.5 TB/s; one of 1000
+// (Two pages at a time a warp, with twice the registers, made no difference; eight warps for four,
+// each with half the ring: 104 to 102 us for 16 sequences of 16384 tokens, bf16 pages.)
+// Bound by reading K and V: those 16 sequences (554 MB) 102 us, 5.4 TB/s; one
+// of 131071 (bf16, 277 MB) 52 us; 48 of 410 to 4096 (fp32, 453 MB) 82 us, 5.5 TB/s; one of 1000
 // (fp32, 4 MB), cluster form, 6.0 us, of which 2.5 are an empty call.
 #include <cuda.h>
 
@@ -40,18 +44,19 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kPartFloats = kGroup * kD + 2 * kGroup;  // O of 4 heads, then their log2 maxima and sums
 constexpr float kFailed = -1.f;                        // sum of a segment whose tiles never came
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxSplits = 64;                         // a lane of the merge has two segments
 constexpr uint32_t kBox = ATTN_PAGE * 128;             // 16 rows of 128 bytes
-constexpr int kMaxKept = 2560;                         // tokens of a segment whose scores a block keeps
+constexpr int kMaxKept = 2448;                         // tokens of a segment whose scores a block keeps
 
 template <bool kF32, bool kCluster>
 struct Pages {
+  static constexpr int kWarps = kF32 ? 4 : 8, kThreads = 32 * kWarps;
   static constexpr uint32_t kOperand = kF32 ? 2 * kBox : kBox;  // a page of K or V of a head; fp32 in halves of 32 dims
   static constexpr uint32_t kStageBytes = 2 * kOperand;
-  static constexpr int kStages = (kF32 ? 1 : 2) * (kCluster ? 2 : 3);  // 16 or 24 KB a warp, two blocks an SM
+  static constexpr int kStages = kCluster ? 2 : 3;  // 64 or 96 KB a block, two blocks an SM
   static constexpr uint32_t kRing = kStages * kStageBytes;
   static constexpr uint32_t kSmemAcc = kWarps * kRing;                        // [warps][4][64] floats
   static constexpr uint32_t kSmemMl = kSmemAcc + kWarps * kGroup * kD * 4;    // [warps][4] (maximum, sum), then [4] of all
@@ -126,7 +131,7 @@ __device__ __forceinline__ float given(float4 s, const Heads& x) {
 
 // Tokens first + t, first + t + kThreads, ... of (b, head) with their scores (of first on),
 // places and old weights, all on their way before any is used (while partial sums are merged).
-template <int kTokens>
+template <int kThreads, int kTokens>
 struct Tokens {
   float4 s[kTokens];
   float* w[kTokens];  // nullptr: no such token, or on a page that is none (recorded where its keys were read)
@@ -154,10 +159,11 @@ struct Tokens {
 };
 
 template <bool kF32, bool kCluster>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(Pages<kF32, kCluster>::kThreads, 2)
 decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                     const DecodeWeighArgs a) {
   using L = Pages<kF32, kCluster>;
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
@@ -175,7 +181,7 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   const int ctx = checked_ctx(a, b, s == 0 && head == 0 && tid == 0);
   const int pages = (ctx + ATTN_PAGE - 1) / ATTN_PAGE, per = (pages + a.splits - 1) / a.splits;
   const int p0 = s * per, p1 = min(p0 + per, pages);  // the segment's pages
-  const int count = max(0, (p1 - p0 - warp + kWarps - 1) / kWarps);  // this warp's: p0 + warp, + 4, ...
+  const int count = max(0, (p1 - p0 - warp + kWarps - 1) / kWarps);  // this warp's: p0 + warp, then every kWarps-th
   uint8_t* const ring = smem + warp * L::kRing;
   // Of the segment's first token on.
   float4* const scores = kCluster ? reinterpret_cast<float4*>(smem + L::kSmemScores)
@@ -394,7 +400,7 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(kFull, l, off);
 
-  // The four warps' sums.
+  // The warps' sums.
   float* const acc = reinterpret_cast<float*>(smem + L::kSmemAcc);
   float2* const ml = reinterpret_cast<float2*>(smem + L::kSmemMl);
   if (r == 0) ml[warp * kGroup + c] = make_float2(ref, l);
@@ -405,7 +411,8 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     acc[(warp * kGroup + c) * kD + d1] = o[2 * m + 1];
   }
   const bool lost = __syncthreads_or(failed);
-  const int h = tid >> 5;
+  const int h = warp % kGroup;  // (with eight warps, two do the same and one writes)
+  const bool writer = warp < kGroup;
   float top = kUnseen;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w * kGroup + h].x);
@@ -427,9 +434,9 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     // Every block's sums to all: lane x of warp h looks at head h of block x.
     float* const mine = reinterpret_cast<float*>(smem + L::kSmemOut);
     float2* const ends = reinterpret_cast<float2*>(mine + kGroup * kD);
-    *reinterpret_cast<float2*>(mine + h * kD + 2 * lane) = y;
-    if (lane == 0) ends[h] = make_float2(top, lost ? kFailed : sum);
-    Tokens<4> x;  // its first tokens' places and weights meanwhile
+    if (writer) *reinterpret_cast<float2*>(mine + h * kD + 2 * lane) = y;
+    if (writer && lane == 0) ends[h] = make_float2(top, lost ? kFailed : sum);
+    Tokens<kThreads, 4> x;  // its first tokens' places and weights meanwhile
     x.load(a, scores, b, head, first, tid, end - first, weighed);
     __syncwarp();
     cluster_sync_all();
@@ -449,7 +456,7 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     const float inv = total == 0.f ? 0.f : 1.f / total;  // no key: zeros
     // Block s writes every a.splits-th pair of dims.
     const unsigned gone = __ballot_sync(kFull, none);
-    const bool writes = tid % a.splits == s;
+    const bool writes = writer && tid % a.splits == s;
     float2 z = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kMaxCluster; ++i) {
@@ -461,7 +468,7 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
     }
     if (writes)
       *reinterpret_cast<float2*>(a.out + ((size_t)b * kHQ + head * kGroup + h) * kD + 2 * lane) = make_float2(z.x * inv, z.y * inv);
-    if (lane == 0) all[h] = make_float2(m, inv);
+    if (writer && lane == 0) all[h] = make_float2(m, inv);
     __syncwarp();
     cluster_arrive();  // the others' shared memory has been read
     __syncthreads();
@@ -482,8 +489,8 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   }
   if (a.splits > 1) {
     float* const part = a.parts + (((size_t)b * kHKV + head) * a.splits + s) * kPartFloats;
-    *reinterpret_cast<float2*>(part + h * kD + 2 * lane) = y;
-    if (lane == 0) {
+    if (writer) *reinterpret_cast<float2*>(part + h * kD + 2 * lane) = y;
+    if (writer && lane == 0) {
       part[kGroup * kD + h] = top;
       part[kGroup * kD + kGroup + h] = lost ? kFailed : sum;
     }
@@ -491,13 +498,13 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
   }
   if (lost) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
-  *reinterpret_cast<float2*>(a.out + ((size_t)b * kHQ + head * kGroup + h) * kD + 2 * lane) = make_float2(y.x * inv, y.y * inv);
-  if (lane == 0) all[h] = make_float2(top, inv);
+  if (writer) *reinterpret_cast<float2*>(a.out + ((size_t)b * kHQ + head * kGroup + h) * kD + 2 * lane) = make_float2(y.x * inv, y.y * inv);
+  if (writer && lane == 0) all[h] = make_float2(top, inv);
   __syncthreads();  // and the block's scores are visible to it
 #pragma unroll
   for (int i = 0; i < kGroup; ++i) heads.top[i] = all[i].x, heads.inv[i] = all[i].y;
   for (int t = tid; t < ctx; t += 2 * kThreads) {
-    Tokens<2> x;
+    Tokens<kThreads, 2> x;
     x.load(a, scores, b, head, 0, t, ctx, weighed);
 #pragma unroll
     for (int i = 0; i < 2; ++i) x.store(heads, i);
@@ -507,8 +514,8 @@ decode_weigh_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constan
 // Merges the segments of (sequence, head): the last block of a row of the grid writes the
 // output, each of the others adds the weights of a stretch of tokens, whose scores arrive as one
 // copy (held in registers they would leave an SM half of its blocks).
-constexpr int kAtOnce = 8, kStretch = kAtOnce * kThreads;
-__global__ void __launch_bounds__(kThreads, 12) decode_weigh_merge_kernel(const DecodeWeighArgs a) {
+constexpr int kPerThread = 8, kMergeThreads = 32 * kGroup, kStretch = kPerThread * kMergeThreads;
+__global__ void __launch_bounds__(kMergeThreads, 12) decode_weigh_merge_kernel(const DecodeWeighArgs a) {
   __shared__ __align__(16) float4 scores[kStretch];
   __shared__ uint64_t full;
   __shared__ Heads heads;
@@ -527,17 +534,17 @@ __global__ void __launch_bounds__(kThreads, 12) decode_weigh_merge_kernel(const 
   const long long first = (long long)blockIdx.x * kStretch;
   const int count = output || first >= ctx ? 0 : (int)min((long long)kStretch, ctx - first);
   const int weighed = a.weighed_lens ? fetch(a.weighed_lens + b) : ctx - 1;
-  int slot[kAtOnce];   // of the weights' pool, in heads' rows of a page; negative: no such token, or no such page
-  float old[kAtOnce];
+  int slot[kPerThread];   // of the weights' pool, in heads' rows of a page; negative: no such token, or no such page
+  float old[kPerThread];
 #pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) {
-    const int t = (int)first + i * kThreads + tid;
-    slot[i] = i * kThreads + tid < count ? fetch(a.table + (size_t)b * a.max_blocks + t / ATTN_PAGE) : -1;
+  for (int i = 0; i < kPerThread; ++i) {
+    const int t = (int)first + i * kMergeThreads + tid;
+    slot[i] = i * kMergeThreads + tid < count ? fetch(a.table + (size_t)b * a.max_blocks + t / ATTN_PAGE) : -1;
     if (slot[i] >= a.num_pages) slot[i] = -1;  // recorded where its keys were read
   }
 #pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) {
-    const int t = (int)first + i * kThreads + tid;
+  for (int i = 0; i < kPerThread; ++i) {
+    const int t = (int)first + i * kMergeThreads + tid;
     if (slot[i] >= 0) slot[i] = (slot[i] * kHKV + head) * ATTN_PAGE + t % ATTN_PAGE;  // 2^27 at most
     old[i] = slot[i] >= 0 && a.decay != 0.f && t < weighed ? a.decay * fetch(a.weights + slot[i]) : 0.f;
   }
@@ -601,16 +608,29 @@ __global__ void __launch_bounds__(kThreads, 12) decode_weigh_merge_kernel(const 
   const int per = ((ctx + ATTN_PAGE - 1) / ATTN_PAGE + a.splits - 1) / a.splits * ATTN_PAGE;
   const Heads all = heads;
 #pragma unroll
-  for (int i = 0; i < kAtOnce; ++i)
-    if (slot[i] >= 0 && !(gone && gone >> (((int)first + i * kThreads + tid) / per) & 1))
-      a.weights[slot[i]] = old[i] + given(scores[i * kThreads + tid], all);
+  for (int i = 0; i < kPerThread; ++i)
+    if (slot[i] >= 0 && !(gone && gone >> (((int)first + i * kMergeThreads + tid) / per) & 1))
+      a.weights[slot[i]] = old[i] + given(scores[i * kMergeThreads + tid], all);
 }
 
 struct Device {
   bool ready = false;
   int sms = 0;
 };
-constexpr size_t kKeptBytes = (size_t)kMaxKept * sizeof(float4);
+// A call's kernel, the shared memory that it takes, scores apart, and its threads.
+struct Choice {
+  void (*kernel)(CUtensorMap, CUtensorMap, DecodeWeighArgs);
+  size_t smem;
+  int threads;
+};
+template <bool kF32, bool kCluster>
+Choice choice() {
+  using L = Pages<kF32, kCluster>;
+  return {decode_weigh_kernel<kF32, kCluster>, L::kSmemAlloc, L::kThreads};
+}
+Choice choice(bool f32, bool cluster) {
+  return f32 ? cluster ? choice<true, true>() : choice<true, false>() : cluster ? choice<false, true>() : choice<false, false>();
+}
 int device(Device** out) {
   constexpr int kMaxDev = 64;
   static std::mutex mu;
@@ -620,14 +640,14 @@ int device(Device** out) {
   std::lock_guard<std::mutex> lock(mu);
   Device& d = devs[dev];
   if (!d.ready) {
-    const auto room = [](auto kernel, size_t bytes) {
-      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
-    };
-    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        !room(decode_weigh_kernel<false, false>, Pages<false, false>::kSmemAlloc) ||
-        !room(decode_weigh_kernel<true, false>, Pages<true, false>::kSmemAlloc) ||
-        !room(decode_weigh_kernel<false, true>, Pages<false, true>::kSmemAlloc + kKeptBytes) ||
-        !room(decode_weigh_kernel<true, true>, Pages<true, true>::kSmemAlloc + kKeptBytes)) {
+    bool ok = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+    for (int i = 0; i < 4; ++i) {
+      const bool cluster = i & 1;
+      const Choice x = choice(i >> 1, cluster);
+      ok = ok && cudaFuncSetAttribute(x.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)(x.smem + (cluster ? kMaxKept * sizeof(float4) : 0))) == cudaSuccess;
+    }
+    if (!ok) {
       (void)cudaGetLastError();
       return ATTN_ECUDA;
     }
@@ -641,9 +661,15 @@ long long score_stride(int max_context) { return ((long long)max_context + ATTN_
 
 // How a call is cut: as clusters where one round of two blocks an SM holds them all and a
 // segment's scores fit, of as many segments as that allows (one sequence of 1000 tokens 6.0
-// us, through memory 8.0); else as decode's segments, through memory. (More rounds of clusters
-// were slower: they hold their places until the last of them ends. 16 sequences of 16384
-// tokens on bf16 pages 132 us, 110 through memory; 48 of 1 to 4096 on fp32 pages 91 and 85.)
+// us, through memory 8.0); else through memory. (More rounds of clusters were slower: they hold
+// their places until the last of them ends. 16 sequences of 16384 tokens on bf16 pages 132 us,
+// 110 through memory; 48 of 1 to 4096 on fp32 pages 91 and 85.) There, segments as decode has
+// them, two blocks an SM and several rounds, but for
+//   one or two sequences: a block an SM, since all begin and end together and a second one only adds
+//     its own start (131071 tokens, bf16 pages: 52 us in 19 segments, 55 in 38; 30000: 16.6 and 18.7)
+//   more than 1536 tokens: two segments at least, since a block that has a sequence alone adds its
+//     weights at the end by itself (32 sequences of 8192, bf16 pages: 101 us, 112 in one segment;
+//     64 of up to 2000, fp32: 59 and 69; 64 of 1000, bf16: 34 and 30)
 struct Plan {
   bool cluster;
   int splits, kept;  // kept: tokens of a segment at most (cluster)
@@ -653,11 +679,14 @@ Plan plan(int B, int max_context, const Device& d) {
   for (int s = kMaxCluster; s >= 1; --s) {
     const long long per = (pages + s - 1) / s;
     if (per * ATTN_PAGE > kMaxKept) break;
-    if ((long long)B * kHKV * s > 2 * d.sms || (s > 1 && per < kWarps)) continue;  // a page a warp at least
+    if ((long long)B * kHKV * s > 2 * d.sms || (s > 1 && per < 4)) continue;  // four pages at least
     return Plan{true, s, (int)per * ATTN_PAGE};
   }
+  const int each = d.sms / (B * kHKV);
+  if (each >= 9) return Plan{false, each < kMaxSplits ? each : kMaxSplits, 0};  // 19584 tokens and more
   int len = 0;
-  return Plan{false, decode_splits(B, max_context, 0, 2 * d.sms, &len), 0};
+  const int splits = decode_splits(B, max_context, 0, 2 * d.sms, &len);
+  return Plan{false, splits == 1 && max_context > 1536 ? 2 : splits, 0};
 }
 
 }  // namespace
@@ -669,7 +698,7 @@ int decode_weigh_workspace_bytes(int B, int max_context, size_t* bytes) {
   const Plan p = plan(B, max_context, *d);
   *bytes = p.cluster ? 0
                      : (size_t)B * kHKV * ((size_t)score_stride(max_context) * sizeof(float4) +
-                                           (p.splits > 1 ? p.splits * kPartFloats * sizeof(float) : 0));
+                                                   (p.splits > 1 ? p.splits * kPartFloats * sizeof(float) : 0));
   return ATTN_OK;
 }
 
@@ -705,11 +734,11 @@ int launch_decode_weigh(const DecodeWeighCall& c, unsigned* err, cudaStream_t st
   a.err = err;
   a.withheld = c.withheld;
   a.timeout_ns = c.withheld ? kFaultNs : kTimeoutNs;
+  const Choice k = choice(!bf16, p.cluster);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.splits, kHKV, c.B);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = p.cluster ? (bf16 ? Pages<false, true>::kSmemAlloc : Pages<true, true>::kSmemAlloc) + p.kept * sizeof(float4)
-                                   : (bf16 ? Pages<false, false>::kSmemAlloc : Pages<true, false>::kSmemAlloc);
+  cfg.blockDim = dim3(k.threads);
+  cfg.dynamicSmemBytes = k.smem + p.kept * sizeof(float4);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -719,12 +748,10 @@ int launch_decode_weigh(const DecodeWeighCall& c, unsigned* err, cudaStream_t st
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster ? 2 : 1;
-  const auto kernel = p.cluster ? (bf16 ? decode_weigh_kernel<false, true> : decode_weigh_kernel<true, true>)
-                                : (bf16 ? decode_weigh_kernel<false, false> : decode_weigh_kernel<true, false>);
-  if (launched(cudaLaunchKernelEx(&cfg, kernel, mk, mv, a)) != cudaSuccess) return ATTN_ELAUNCH;
+  if (launched(cudaLaunchKernelEx(&cfg, k.kernel, mk, mv, a)) != cudaSuccess) return ATTN_ELAUNCH;
   if (!p.cluster && a.splits > 1) {
     const unsigned stretches = (c.max_context + kStretch - 1) / kStretch;
-    if (launch_following(decode_weigh_merge_kernel, dim3(stretches + 1, kHKV, c.B), dim3(kThreads), stream, a) != cudaSuccess)
+    if (launch_following(decode_weigh_merge_kernel, dim3(stretches + 1, kHKV, c.B), dim3(kMergeThreads), stream, a) != cudaSuccess)
       return ATTN_ELAUNCH;
   }
   return ATTN_OK;

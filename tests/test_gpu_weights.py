@@ -129,6 +129,24 @@ def test_window(cp, name, bf16, decay, bound):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,bound", [([9000, 3, 0, 515, 8999] + [100 * i for i in range(11)], None),
+                                        ([8192, 8191, 8177] + [31 * i for i in range(27)], None),
+                                        ([16384, 16383, 12000, 5, 16000, 64, 65], 40000),
+                                        ([20480, 20481, 300], 60000)])
+def test_decode_of_uneven_lengths(cp, bf16, lens, bound):
+    b = R.make_batch([(c, 0) for c in lens], bf16=bf16, seed=14, extra_blocks=(bound or 0) // 16)
+    bound = max(lens) if bound is None else bound
+    weighed = [max(0, c - 1 - 7 * (i % 3)) for i, c in enumerate(lens)]
+    w, q = W.weight_pool(b, known=weighed), torch.randn(len(lens), 32, 64, device="cuda") * 2
+    before = w.clone()
+    out = decode(cp, b, q, w, 0.9, ints(weighed), bound=bound)
+    assert cp.attn_get_device_error() == 0
+    want, o, tol = W.weigh_reference(q, b, before, weighed, 0.9, decode=True)
+    check_weights(w, before, b, want)
+    inside(out, o, tol)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 def test_window_of_tokens_without_weights(cp, bf16):
     """A prompt's last rows weigh all of it for the first time."""
     lens = [(260, 40), (100, 3), (1000, 64)]

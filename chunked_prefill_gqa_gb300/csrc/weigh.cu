@@ -16,7 +16,8 @@
 // is 2^x and an addition. (Read from shared memory, 8 bytes a column and thread, they took as
 // long as the products.) q is scaled by log2(e) / 8 before it is split. Windows of more than 32
 // rows: more blocks in the rows pass, one row tile after another in the keys pass, whose
-// block adds to weights that it alone writes.
+// block adds to weights that it alone writes. Windows of up to 32 rows over so few keys that all
+// products stay in tensor memory need no second pass: weights_of_products().
 //   bf16 pages: K as stored, q in three bf16 terms: 3 x 4 MMAs of 128 x 128 x 16 a tile
 //   fp32 pages: q K_lo + q_lo K + q K, tf32 terms: 3 x 8 of 128 x 128 x 8
 // (K is read truncated; K_lo is the remainder rounded to tf32, q's first term rounded too.) By
@@ -101,18 +102,20 @@ constexpr int kConvWarp = kSoft, kTmaWarp = kConvWarp + 4, kMmaWarp = kTmaWarp +
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 
 // A kernel runs one pass, or both (kFused) one after the other over the same segment of keys:
-// the passes' operands lie in the same bytes, their barriers beside each other.
-constexpr int kRowsPass = 0, kKeysPass = 1, kFused = 2;
+// the passes' operands lie in the same bytes, their barriers beside each other. kOnce: the
+// rows pass alone, whose products stay in tensor memory until the sums are known.
+constexpr int kRowsPass = 0, kKeysPass = 1, kFused = 2, kOnce = 3;
+constexpr int kHeld = 3;        // tiles of S that a block's tensor memory holds
 constexpr int kFusedTiles = 2;  // row tiles of a fused window, whose sums stay in shared memory
 template <bool kF32, int kPass>
 struct Kernel {
   using R = Lay<kF32, false>;
   using K = Lay<kF32, true>;
-  static constexpr bool kRows = kPass != kKeysPass, kKeys = kPass != kRowsPass;
-  static constexpr uint32_t kEnd = kPass == kRowsPass ? R::kSmemEnd : kPass == kKeysPass ? K::kSmemEnd
+  static constexpr bool kRows = kPass != kKeysPass, kKeys = kPass == kKeysPass || kPass == kFused;
+  static constexpr uint32_t kEnd = !kKeys ? R::kSmemEnd : kPass == kKeysPass ? K::kSmemEnd
                                    : R::kSmemEnd > K::kSmemEnd ? R::kSmemEnd : K::kSmemEnd;
-  static constexpr uint32_t kSmemKept = kEnd;  // fused: [row tiles][128] (reference, sum) of this block's keys
-  static constexpr uint32_t kSmemBarR = kSmemKept + (kPass == kFused ? kFusedTiles * 128 * 8 : 0);
+  static constexpr uint32_t kSmemKept = kEnd;  // one launch: [row tiles][128] (reference, sum) of this block's keys
+  static constexpr uint32_t kSmemBarR = kSmemKept + (kPass == kFused ? kFusedTiles * 128 * 8 : kPass == kOnce ? 128 * 8 : 0);
   static constexpr uint32_t kSmemBarK = kSmemBarR + (kRows ? R::kNumBars * 8 : 0);
   static constexpr uint32_t kSmemWords = kSmemBarK + (kKeys ? K::kNumBars * 8 : 0);  // TMEM address, abort flag
   static constexpr uint32_t kSmemAlloc = kSmemWords + 16 + 1024;
@@ -640,6 +643,84 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs&
   }
 }
 
+// The weights from a rows pass whose tiles all have a buffer of S of their own: p by row as the
+// pass had it, and its sums over the rows, 32 keys at a time, by exchanging halves of them
+// between the lanes (31 shuffles) and adding the quarters up in shared memory. It spares the second
+// load of K and its products, for more work a key than the keys pass has.
+template <bool kF32>
+__device__ __forceinline__ void weights_of_products(const WeighArgs& a, const Work& x) {
+  using L = Lay<kF32, false>;
+  static_assert(kHeld == L::kBufs && kHeld == kGroups, "a buffer and a group for each tile");
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kFull, threadIdx.x >> 5, 0);
+  const int quarter = warp & 3, g = warp >> 2, row = quarter * 32 + lane, count = x.tiles(0);
+  const bool soft = warp < kSoft, lost = *x.abort_flag;
+  float* const sums = reinterpret_cast<float*>(x.smem);  // [tiles][quarters][128], where K was
+  // A thread's key, of tile g, and its weight so far.
+  const int t = x.k0 + g * kKeys + row;
+  float* w = nullptr;
+  float old = 0.f;
+  if (soft && t < x.visible(0)) {
+    const int page = fetch(a.table + (size_t)x.b * a.max_blocks + t / ATTN_PAGE);
+    if (page >= 0 && page < a.num_pages) {
+      w = a.weights + ((size_t)page * kHKV + x.head) * ATTN_PAGE + t % ATTN_PAGE;
+      if (a.decay != 0.f && t < (a.weighed_lens ? fetch(a.weighed_lens + x.b) : x.seq.ctx)) old = a.decay * *w;
+    }
+  }
+  __syncwarp();
+  cluster_sync_all();  // the rows' sums are written
+  float top = kUnseen, sum = 0.f;
+  const bool in = soft && (row >> 2) < x.seq.rows;
+  if (in) {
+    float2 p[kMaxCluster];
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) {
+      p[i] = make_float2(kUnseen, 0.f);
+      if (i < x.ranks) p[i] = ld_cluster2(mapa_shared(smem_u32(x.kept + row), i));
+      top = fmaxf(top, p[i].x);
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxCluster; ++i) sum = fmaf(ex2(p[i].x - top), p[i].y, sum);
+  }
+  __syncwarp();
+  cluster_arrive();  // and read
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int quarters = (x.seq.rows + 7) / 8;
+  if (soft && !lost) {
+    if (quarter < quarters) {
+#pragma unroll 1
+      for (int i = g; i < 4 * count; i += kGroups) {  // tile i / 4, its columns 32 (i % 4) and on
+        const int n = i >> 2, c = (i & 3) * 32;
+        const int limit = min(x.seq.ctx + (row >> 2) + 1, x.k1) - x.k0 - n * kKeys - c;  // of the columns, those that the row sees
+        float p[32];
+        tmem_ld32(x.tmem + ((uint32_t)(quarter * 32) << 16) + L::kColS + n * kKeys + c, p);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) p[j] = inv == 0.f || j >= limit ? 0.f : ex2(p[j] - top) * inv;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+          for (int j = 0; j < off; ++j) {
+            const bool upper = lane & off;
+            p[j] = (upper ? p[j + off] : p[j]) + __shfl_xor_sync(kFull, upper ? p[j] : p[j + off], off);
+          }
+        sums[(n * 4 + quarter) * kKeys + c + lane] = p[0];
+      }
+    }
+    meet(32 * kSoft);
+    if (w) {
+      float all = 0.f;
+      for (int i = 0; i < quarters; ++i) all += sums[(g * 4 + i) * kKeys + row];
+      *w = old + all;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(x.tmem, 512);
+  __syncwarp();
+  cluster_wait();
+}
+
 template <bool kF32, int kPass>
 __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const __grid_constant__ CUtensorMap mk, const WeighArgs a) {
   using K = Kernel<kF32, kPass>;
@@ -669,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const __grid_constan
   x.k1 = min((long long)x.k0 + len, (long long)x.seq.keys);
   if (kPass == kKeysPass && x.k0 >= x.k1) return;
   x.ranks = splits;
-  x.kept = kPass == kFused ? reinterpret_cast<float2*>(smem + K::kSmemKept) : nullptr;
+  x.kept = kPass == kFused || kPass == kOnce ? reinterpret_cast<float2*>(smem + K::kSmemKept) : nullptr;
   uint64_t* const rbars = reinterpret_cast<uint64_t*>(smem + K::kSmemBarR);
   uint64_t* const kbars = reinterpret_cast<uint64_t*>(smem + K::kSmemBarK);
   uint32_t* const words = reinterpret_cast<uint32_t*>(smem + K::kSmemWords);
@@ -690,6 +771,10 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const __grid_constan
   x.tmem = words[0];
 
   if constexpr (K::kRows) run_pass<kF32, false>(mk, a, x, rbars);
+  if constexpr (kPass == kOnce) {
+    weights_of_products<kF32>(a, x);
+    return;
+  }
   if constexpr (kPass == kFused) cluster_sync_all();  // the rows' sums are written
   if constexpr (K::kKeys) {
     if (!*x.abort_flag) run_pass<kF32, true>(mk, a, x, kbars);
@@ -704,6 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const __grid_constan
 struct Device {
   bool ready = false;
   int sms = 0;
+  int clusters[kMaxCluster + 1] = {};  // of each size, that the device holds at once
 };
 // A kernel of the call and its shared memory.
 struct Choice {
@@ -714,6 +800,7 @@ template <bool kF32>
 Choice choice(int pass) {
   if (pass == kRowsPass) return {weigh_kernel<kF32, kRowsPass>, Kernel<kF32, kRowsPass>::kSmemAlloc};
   if (pass == kKeysPass) return {weigh_kernel<kF32, kKeysPass>, Kernel<kF32, kKeysPass>::kSmemAlloc};
+  if (pass == kOnce) return {weigh_kernel<kF32, kOnce>, Kernel<kF32, kOnce>::kSmemAlloc};
   return {weigh_kernel<kF32, kFused>, Kernel<kF32, kFused>::kSmemAlloc};
 }
 
@@ -727,13 +814,31 @@ int device(Device** out) {
   Device& d = devs[dev];
   if (!d.ready) {
     bool ok = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
-    for (int i = 0; i < 6; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const Choice p = i & 1 ? choice<true>(i >> 1) : choice<false>(i >> 1);
       ok = ok && cudaFuncSetAttribute(p.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) == cudaSuccess;
     }
     if (!ok) {
       (void)cudaGetLastError();
       return ATTN_ECUDA;
+    }
+    d.clusters[1] = d.sms;
+    const Choice k = choice<true>(kFused);  // all have an SM to themselves
+    for (int size = 2; size <= kMaxCluster; ++size) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(size, kHKV);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = k.smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = size;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&d.clusters[size], k.kernel, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        d.clusters[size] = 0;
+      }
     }
     d.ready = true;
   }
@@ -756,17 +861,20 @@ int segments(long long units, int max_keys, int passes, int sms, double* least) 
   return best;
 }
 
-// How a call runs: as one launch, with the rows' sums in shared memory, or as two launches with
-// the sums through memory. One launch where a block has a sequence's keys alone (44 sequences of
-// 5 rows at 320 to 3213, bf16 pages: 71 us, and 79 as two) or a cluster's blocks exchange their
-// sums and all have an SM at once (8 rows at 1000: 9.0 and 9.5); not in several rounds of
-// clusters (8 windows of 64 rows at 16384, bf16 pages: 217 us in clusters of seven, 126).
+// How a call runs. Once, where a window's 32 rows and the keys of each block of one round of
+// clusters fit tensor memory (8 rows at 1000, fp32 pages: 8.5 us, 9.8 with both passes; 32 rows at
+// 2900: 13.0, 15.8 as two launches). Else as one launch, with the rows' sums in shared memory, or as
+// two launches with the sums through memory. One launch where a block has a sequence's keys alone
+// (44 sequences of 5 rows at 320 to 3213, bf16 pages: 71 us, and 79 as two) or a cluster's blocks
+// exchange their sums and all have an SM at once; not in several rounds of clusters (8 windows of
+// 64 rows at 16384, bf16 pages: 217 us in clusters of seven, 126; 2 of 16 rows at 2000: 10.4 us in
+// clusters of seven, and 17 of eight, of which the device does not hold the 16 at once).
 struct Plan {
-  bool fused;
+  bool fused, once;
   int splits, key_splits;
 };
-Plan plan(int B, int max_rows, int max_keys, int sms) {
-  const int tiles = (max_rows + kRows - 1) / kRows;
+Plan plan(int B, int max_rows, int max_keys, const Device& d) {
+  const int tiles = (max_rows + kRows - 1) / kRows, sms = d.sms;
   double rows = 0, keys = 0;
   Plan p{};
   p.splits = segments((long long)B * kHKV * tiles, max_keys, 1, sms, &rows);
@@ -775,11 +883,18 @@ Plan plan(int B, int max_rows, int max_keys, int sms) {
   const int key_tiles = (max_keys + kKeys - 1) / kKeys;
   double least = rows + keys;
   for (int s = 1; s <= kMaxCluster && s <= key_tiles; ++s) {
+    const bool one_round = (long long)B * kHKV <= d.clusters[s];
+    if (s > 1 && !one_round) continue;
+    const int each = (key_tiles + s - 1) / s;
+    if (tiles == 1 && one_round && each <= kHeld) {
+      if (!p.once || each < (key_tiles + p.splits - 1) / p.splits) p.once = true, p.splits = s;
+      continue;
+    }
     const long long rounds = ((long long)B * kHKV * s + sms - 1) / sms;
-    if (s > 1 && rounds > 1) break;
-    const double time = (double)rounds * (2.0 * tiles * ((key_tiles + s - 1) / s) + 4.0 + 2.0 * tiles);
-    if (time < least * 0.999) least = time, p.fused = true, p.splits = s;
+    const double time = (double)rounds * (2.0 * tiles * each + 4.0 + 2.0 * tiles);
+    if (!p.once && time < least * 0.999) least = time, p.fused = true, p.splits = s;
   }
+  p.fused &= !p.once;
   return p;
 }
 
@@ -793,8 +908,8 @@ int weigh_workspace_bytes(int B, int N, int max_rows, int max_context, size_t* b
   Device* d = nullptr;
   const int rc = device(&d);
   if (rc != ATTN_OK) return rc;
-  const Plan p = plan(B, max_rows, max_keys(max_context, max_rows), d->sms);
-  *bytes = p.fused ? 0 : (size_t)N * kHQ * p.splits * sizeof(float2);
+  const Plan p = plan(B, max_rows, max_keys(max_context, max_rows), *d);
+  *bytes = p.fused || p.once ? 0 : (size_t)N * kHQ * p.splits * sizeof(float2);
   return ATTN_OK;
 }
 
@@ -807,7 +922,7 @@ int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
   if ((rc = encode_rows_map(c.k_pages, bf16, (long long)c.num_pages * ATTN_PAGE, ATTN_PAGE, CU_TENSOR_MAP_SWIZZLE_128B,
                             &mk)) != ATTN_OK)
     return rc;
-  const Plan p = plan(c.B, c.max_rows, max_keys(c.max_context, c.max_rows), d->sms);
+  const Plan p = plan(c.B, c.max_rows, max_keys(c.max_context, c.max_rows), *d);
   WeighArgs a{};
   a.q = c.q;
   a.weights = c.weights;
@@ -829,7 +944,8 @@ int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
   a.err = err;
   a.withheld = c.withheld;
   a.timeout_ns = c.withheld ? kFaultNs : kTimeoutNs;
-  for (int pass = p.fused ? kFused : kRowsPass; pass <= (p.fused ? kFused : kKeysPass); ++pass) {
+  const int first = p.once ? kOnce : p.fused ? kFused : kRowsPass, last = p.once ? kOnce : p.fused ? kFused : kKeysPass;
+  for (int pass = first; pass <= last; ++pass) {
     const Choice k = bf16 ? choice<false>(pass) : choice<true>(pass);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(pass == kRowsPass ? a.splits * a.row_tiles : pass == kKeysPass ? a.key_splits : a.splits, kHKV, c.B);
@@ -843,7 +959,7 @@ int launch_weigh(const WeighCall& c, unsigned* err, cudaStream_t stream) {
     attr[1].val.clusterDim.x = a.splits;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pass == kFused ? 2 : 1;
+    cfg.numAttrs = pass >= kFused ? 2 : 1;
     if (launched(cudaLaunchKernelEx(&cfg, k.kernel, mk, a)) != cudaSuccess) return ATTN_ELAUNCH;
   }
   return ATTN_OK;

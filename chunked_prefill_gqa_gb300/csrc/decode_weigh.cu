@@ -616,6 +616,7 @@ __global__ void __launch_bounds__(kMergeThreads, 12) decode_weigh_merge_kernel(c
 struct Device {
   bool ready = false;
   int sms = 0;
+  int clusters[kMaxCluster + 1] = {};  // of each size, that the device holds at once on either page type
 };
 // A call's kernel, the shared memory that it takes, scores apart, and its threads.
 struct Choice {
@@ -651,6 +652,28 @@ int device(Device** out) {
       (void)cudaGetLastError();
       return ATTN_ECUDA;
     }
+    for (int size = 1; size <= kMaxCluster; ++size) {
+      d.clusters[size] = 1 << 30;
+      for (int f32 = 0; f32 < 2; ++f32) {
+        const Choice x = choice(f32, true);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(size, kHKV);
+        cfg.blockDim = dim3(x.threads);
+        cfg.dynamicSmemBytes = x.smem + kMaxKept * sizeof(float4);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = size;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, x.kernel, &cfg) != cudaSuccess) {
+          (void)cudaGetLastError();
+          n = 0;
+        }
+        if (n < d.clusters[size]) d.clusters[size] = n;
+      }
+    }
     d.ready = true;
   }
   *out = &d;
@@ -659,11 +682,13 @@ int device(Device** out) {
 
 long long score_stride(int max_context) { return ((long long)max_context + ATTN_PAGE - 1) / ATTN_PAGE * ATTN_PAGE; }
 
-// How a call is cut: as clusters where one round of two blocks an SM holds them all and a
+// How a call is cut: as clusters where the device holds them all at once and a
 // segment's scores fit, of as many segments as that allows (one sequence of 1000 tokens 6.0
 // us, through memory 8.0); else through memory. (More rounds of clusters were slower: they hold
 // their places until the last of them ends. 16 sequences of 16384 tokens on bf16 pages 132 us,
-// 110 through memory; 48 of 1 to 4096 on fp32 pages 91 and 85.) There, segments as decode has
+// 110 through memory; 48 of 1 to 4096 on fp32 pages 91 and 85. Of three blocks and more the last few
+// that the device is said to hold wait as well: 12 sequences of 4000 in 96 clusters of three, of
+// 97, 32 us, in clusters of two 24; 7 in 56 of five, of 58, 21.5, of four 15.7.) There, segments as decode has
 // them, two blocks an SM and several rounds, but for
 //   one or two sequences: a block an SM, since all begin and end together and a second one only adds
 //     its own start (131071 tokens, bf16 pages: 52 us in 19 segments, 55 in 38; 30000: 16.6 and 18.7)
@@ -679,7 +704,7 @@ Plan plan(int B, int max_context, const Device& d) {
   for (int s = kMaxCluster; s >= 1; --s) {
     const long long per = (pages + s - 1) / s;
     if (per * ATTN_PAGE > kMaxKept) break;
-    if ((long long)B * kHKV * s > 2 * d.sms || (s > 1 && per < 4)) continue;  // four pages at least
+    if (B * kHKV > (s > 2 ? d.clusters[s] * 19 / 20 : d.clusters[s]) || (s > 1 && per < 4)) continue;  // four pages at least
     return Plan{true, s, (int)per * ATTN_PAGE};
   }
   const int each = d.sms / (B * kHKV);

@@ -23,6 +23,7 @@
 // Bound by the moves' latency and bytes: 16 sequences of 16384 tokens to half (bf16 pages) read and
 // write 287 MB in the 81 us of the call with its 6 us of restored weights: select 20, move 45 (their
 // floor 43 together). Rows of 128 bytes at random places move at 6.2 TB/s.
+#include <cstddef>
 #include <cstdint>
 #include <mutex>
 
@@ -77,12 +78,15 @@ constexpr int kListed = 2048;  // keys of the first digit's bin that a block kee
 template <int kThreads>
 struct alignas(16) Shared {  // the keys follow
   static constexpr int kWarps = kThreads / 32;
-  uint32_t hist[2][kBins];
+  uint32_t hist[2][kBins];     // these two in vectors of 16 bytes
+  uint32_t slice[kBins / 2];   // the cluster's counts of this block's share of the bins
+  uint32_t in_slice[3];        // and their sum, in each pass
   uint32_t keys[kListed], places[kListed];  // and their tokens, from the block's first on
   uint32_t listed;
   uint32_t warp_sums[kWarps];
   uint32_t warp_gt[kWarps], warp_eq[kWarps];
-  uint32_t totals[6];  // this block's keys above and equal to the m-th: all, below edge, below new
+  uint32_t totals[8];  // this block's keys above and equal to the m-th: all, below edge, below new; bad
+  uint32_t others[kMaxCluster][8];      // the cluster's
   uint32_t bin, need, whole;
   int bad;
 };
@@ -109,23 +113,50 @@ __device__ __forceinline__ uint32_t running(uint32_t bits) { return ((bits * 0x0
 
 // The bin of a digit that holds the cluster's need-th key from the top, how many of the bin's
 // are needed, and whether that is all of them. Zeroes the other histogram, which nobody has
-// read since the last meeting.
+// read since the last meeting. A cluster's blocks add up a share of the bins each, and then look at
+// the one share that the key is in. (Every block adding up all: eight times the distant reads, one
+// sequence of 20000 tokens 51 us for the call, 27 this way.)
 template <int kThreads>
-__device__ __forceinline__ void choose(Shared<kThreads>& sh, int ranks, int pass, uint32_t need) {
+__device__ __forceinline__ void choose(Shared<kThreads>& sh, int ranks, int rank, int pass, uint32_t need) {
   constexpr int kWarps = kThreads / 32, kPerThread = kBins / kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t* const hist = sh.hist[pass & 1];
-  if (ranks > 1) tc::cluster_sync_all();
-  else __syncthreads();
-  // Thread i owns kPerThread bins, the last thread the lowest ones: counts from the top.
-  const int low = kBins - kPerThread * (tid + 1);
-  uint32_t n[kPerThread] = {}, sum = 0;
-  for (int r = 0; r < ranks; ++r)
+  uint32_t n[kPerThread] = {}, sum = 0, passed = 0;
+  int base = 0, per = kPerThread, low = kBins - kPerThread * (tid + 1);  // this thread's bins, from low on; the last thread's are the lowest
+  if (ranks > 1) {
+    tc::cluster_sync_all();
+    const int share = kBins / ranks;  // block r has bins share * r and on
+    if (4 * tid < share) {
+      uint4 all = make_uint4(0, 0, 0, 0);
+      for (int r = 0; r < ranks; ++r) {
+        const uint4 x = ld_cluster4u(hist + rank * share + 4 * tid, r);
+        all.x += x.x, all.y += x.y, all.z += x.z, all.w += x.w;
+      }
+      *reinterpret_cast<uint4*>(sh.slice + 4 * tid) = all;
+      atomicAdd(sh.in_slice + pass, all.x + all.y + all.z + all.w);
+    }
+    __syncwarp();
+    tc::cluster_sync_all();
+    int owner = ranks - 1;
+    for (; owner > 0; --owner) {
+      const uint32_t in = ld_cluster(sh.in_slice + pass, owner);
+      if (need <= passed + in) break;
+      passed += in;
+    }
+    per = share >= kThreads ? share / kThreads : 1;
+    low = share - per * (tid + 1);
+    base = share * owner;
+#pragma unroll
+    for (int j = 0; j < kPerThread / 2; ++j)
+      if (j < per && low >= 0) n[j] = ld_cluster(sh.slice + low + j, owner);
+  } else {
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < kPerThread; j += 4) {
-      const uint4 x = ranks > 1 ? ld_cluster4u(hist + low + j, r) : *reinterpret_cast<const uint4*>(hist + low + j);
-      n[j] += x.x, n[j + 1] += x.y, n[j + 2] += x.z, n[j + 3] += x.w;
+      const uint4 x = *reinterpret_cast<const uint4*>(hist + low + j);
+      n[j] = x.x, n[j + 1] = x.y, n[j + 2] = x.z, n[j + 3] = x.w;
     }
+  }
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) sum += n[j];
   uint32_t up = sum;
@@ -139,13 +170,13 @@ __device__ __forceinline__ void choose(Shared<kThreads>& sh, int ranks, int pass
   for (int i = 0; i < kBins / 4; i += kThreads)
     reinterpret_cast<uint4*>(sh.hist[(pass + 1) & 1])[i + tid] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  uint32_t before = up - sum;
+  uint32_t before = passed + up - sum;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) before += w < warp ? sh.warp_sums[w] : 0;
 #pragma unroll
   for (int j = kPerThread - 1; j >= 0; --j) {
     if (before < need && need <= before + n[j]) {
-      sh.bin = low + j;
+      sh.bin = base + low + j;
       sh.need = need - before;
       sh.whole = need == before + n[j];
     }
@@ -165,7 +196,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   const int rank = blockIdx.x, ranks = gridDim.x, head = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kBins / 4; i += kThreads) reinterpret_cast<uint4*>(sh.hist[0])[i] = make_uint4(0, 0, 0, 0);
-  if (tid < 6) sh.totals[tid] = 0;
+  if (tid < 8) sh.totals[tid] = 0;
+  if (tid < 3) sh.in_slice[tid] = 0;
   if (tid == 0) sh.bad = 0, sh.listed = 0;
   follow();
   const Cut cut = load_cut(a, b);
@@ -242,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
   };
   bool listed = false;
   if (m > 0) {
-    choose<kThreads>(sh, ranks, 0, m);
+    choose<kThreads>(sh, ranks, rank, 0, m);
     uint32_t prefix = sh.bin;
     need = sh.need;
     // Keys above the bin are counted, those in it (a few in a hundred) listed: the other
@@ -286,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
           count_digit(key.w, in & 8);
         }
       }
-      choose<kThreads>(sh, ranks, pass, need);
+      choose<kThreads>(sh, ranks, rank, pass, need);
       prefix = prefix << kDigit | sh.bin;
       need = sh.need;
       whole = sh.whole;
@@ -322,24 +354,23 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const EvictArgs a) {
     const uint32_t sum = __reduce_add_sync(kFull, c[i]);
     if (lane == i && sum) atomicAdd(sh.totals + i, sum);
   }
+  __syncthreads();
+  if (tid == 0) sh.totals[6] = sh.bad;
   if (ranks > 1) tc::cluster_sync_all();
   else __syncthreads();
-  uint32_t gt_before = 0, eq_before = 0, in_gt = 0, in_eq = 0, now_gt = 0, now_eq = 0;
-  int bad = 0;
-  for (int r = 0; r < ranks; ++r) {
-    if (r < rank) {
-      gt_before += ld_cluster(sh.totals + 0, r);
-      eq_before += ld_cluster(sh.totals + 1, r);
-    }
-    in_gt += ld_cluster(sh.totals + 2, r);
-    in_eq += ld_cluster(sh.totals + 3, r);
-    now_gt += ld_cluster(sh.totals + 4, r);
-    now_eq += ld_cluster(sh.totals + 5, r);
-    bad |= (int)ld_cluster(reinterpret_cast<const uint32_t*>(&sh.bad), r);
-  }
+  if (tid < 8 * ranks) sh.others[tid >> 3][tid & 7] = ld_cluster(sh.totals + (tid & 7), tid >> 3);
   if (ranks > 1) {
     __syncwarp();
     tc::cluster_arrive();  // nobody's shared memory is read past here
+  }
+  __syncthreads();
+  uint32_t gt_before = 0, eq_before = 0, in_gt = 0, in_eq = 0, now_gt = 0, now_eq = 0;
+  int bad = 0;
+  for (int r = 0; r < ranks; ++r) {
+    const uint32_t* const x = sh.others[r];
+    if (r < rank) gt_before += x[0], eq_before += x[1];
+    in_gt += x[2], in_eq += x[3], now_gt += x[4], now_eq += x[5];
+    bad |= (int)x[6];
   }
   const uint32_t kept_in = in_gt + min(in_eq, need);  // middle tokens that stay below edge
   if (rank == 0 && tid == 0) {
@@ -565,7 +596,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
     tc::cluster_arrive();  // this block has read the weights, which are moved too
   }
   if (m > 0) {
-    choose<kSmallThreads>(sh, 1, 0, m);
+    choose<kSmallThreads>(sh, 1, 0, 0, m);
     uint32_t prefix = sh.bin, need = sh.need;
     bool whole = sh.whole;
 #pragma unroll
@@ -613,7 +644,7 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
           for (int j = 0; j < 4; ++j)
             if ((in >> j & 1) && k[j] >> above == prefix) atomicAdd(sh.hist[pass & 1] + (k[j] >> shift & ((1u << kDigit) - 1)), 1u);
         }
-        choose<kSmallThreads>(sh, 1, pass, need);
+        choose<kSmallThreads>(sh, 1, 0, pass, need);
         prefix = prefix << kDigit | sh.bin;
         need = sh.need;
         whole = sh.whole;
@@ -717,30 +748,54 @@ __global__ void __launch_bounds__(kSmallThreads) small_kernel(const EvictArgs a)
   if (rank == 0) rows.template follow_up<kSmallThreads>(cut, a.last, tid);
 }
 
+static_assert(offsetof(Shared<512>, slice) % 16 == 0 && offsetof(Shared<1024>, slice) % 16 == 0 && offsetof(Small, sh) % 16 == 0,
+              "histograms in vectors of 16 bytes");
 static_assert(sizeof(Shared<512>) % 16 == 0 && sizeof(Shared<1024>) % 16 == 0, "the keys start on 16 bytes");
 static_assert(sizeof(Shared<1024>) + (size_t)kMaxCached * sizeof(uint32_t) <= 232448, "exceeds the 227 KB per-block shared memory limit");
 
-// Once per device: the shared-memory opt-in, and how many SMs there are.
-int device(int* sms) {
+// Once per device: the shared-memory opt-in, how many SMs there are, and how many clusters
+// of each size whose blocks have an SM each.
+struct Device {
+  bool ready = false;
+  int sms = 0, clusters[kMaxCluster + 1] = {};
+};
+int device(Device** out) {
   constexpr int kMaxDev = 64;
+  constexpr int kAll = 232448;
   static std::mutex mu;
-  static int devs[kMaxDev];
+  static Device devs[kMaxDev];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return ATTN_ECUDA;
   std::lock_guard<std::mutex> lock(mu);
-  if (!devs[dev]) {
-    int n = 0;
+  Device& d = devs[dev];
+  if (!d.ready) {
     const auto room = [](auto kernel) {
-      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) == cudaSuccess;
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAll) == cudaSuccess;
     };
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !room(select_kernel<512>) ||
+    if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || !room(select_kernel<512>) ||
         !room(select_kernel<1024>) || !room(small_kernel<8>) || !room(small_kernel<16>)) {
       (void)cudaGetLastError();
       return ATTN_ECUDA;
     }
-    devs[dev] = n;
+    for (int size = 1; size <= kMaxCluster; size *= 2) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(size, kHKV);
+      cfg.blockDim = dim3(1024);
+      cfg.dynamicSmemBytes = kAll;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = size;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&d.clusters[size], select_kernel<1024>, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();
+        d.clusters[size] = 0;
+      }
+    }
+    d.ready = true;
   }
-  *sms = devs[dev];
+  *out = &d;
   return ATTN_OK;
 }
 
@@ -754,9 +809,10 @@ size_t evict_workspace_bytes(int B, int max_context) {
 }
 
 int launch_evict(const EvictCall& c, unsigned* err, cudaStream_t stream) {
-  int sms = 0;
-  const int rc = device(&sms);
+  Device* d = nullptr;
+  const int rc = device(&d);
   if (rc != ATTN_OK) return rc;
+  const int sms = d->sms;
   EvictArgs a{};
   a.k_pages = c.k_pages;
   a.v_pages = c.v_pages;
@@ -797,10 +853,11 @@ int launch_evict(const EvictCall& c, unsigned* err, cudaStream_t stream) {
     return launched(cudaLaunchKernelEx(&cfg, kernel, a)) == cudaSuccess ? ATTN_OK : ATTN_ELAUNCH;
   }
 
-  // Blocks of a cluster: as many as have an SM each, with 1024 tokens at least; and so many that a block's keys fit its shared memory, if they can.
+  // Blocks of a cluster: as many as have an SM each at once, with 1024 tokens at least; and so many that
+  // a block's keys fit its shared memory, if they can.
   int ranks = 1;
-  while (ranks < kMaxCluster && ((long long)c.B * kHKV * 2 * ranks <= sms ? c.max_context / (2 * ranks) >= 1024
-                                                                              : c.max_context / ranks > kMaxCached))
+  while (ranks < kMaxCluster && (c.B * kHKV <= d->clusters[2 * ranks] ? c.max_context / (2 * ranks) >= 1024
+                                                                      : c.max_context / ranks > kMaxCached))
     ranks *= 2;
   const int span = ((c.max_context + ATTN_PAGE - 1) / ATTN_PAGE + ranks - 1) / ranks * ATTN_PAGE;
   a.cached = span <= kMaxCached;

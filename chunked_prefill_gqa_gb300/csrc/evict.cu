@@ -21,7 +21,7 @@
 // last ones there, batch by batch.
 //
 // Bound by the moves' latency and bytes: 16 sequences of 16384 tokens to half (bf16 pages) read and
-// write 287 MB in the 81 us of the call with its 6 us of restored weights: select 20, move 45 (their
+// write 287 MB in the 80 us of the call with its 6 us of restored weights: select 20, move 45 (their
 // floor 43 together). Rows of 128 bytes at random places move at 6.2 TB/s.
 #include <cstddef>
 #include <cstdint>

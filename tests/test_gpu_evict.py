@@ -111,6 +111,25 @@ def test_equal_and_unusual_weights(cp, kind, context, keep):
     check(cp, b, w, [keep, 45], 3, 20)
 
 
+@pytest.mark.parametrize("kind", ["zeros", "few values", "half zeros"])
+@pytest.mark.parametrize("contexts,keep", [([20000], 9000), ([40000, 30, 17000], 8000)])
+def test_more_equal_weights_than_are_listed(cp, kind, contexts, keep):
+    """So many in the first digit's bin that a block's list of them overflows: all of its keys are looked at again."""
+    b = R.make_batch([(c, 0) for c in contexts], bf16=True, seed=8)
+    rng, w = np.random.default_rng(9), W.weight_pool(b)
+    for s, c in enumerate(contexts):
+        x = np.exp(rng.standard_normal((c, 8))).astype(np.float32)
+        if kind == "zeros":
+            x[:] = 0
+        elif kind == "few values":
+            x = rng.integers(0, 3, (c, 8)).astype(np.float32)
+        else:
+            x[rng.random((c, 8)) < 0.7] = 0.0
+        W.put_weights(w, b, s, x)
+    check(cp, b, w, [keep] * len(contexts), 4, 20)
+    assert cp.attn_get_device_error() == 0
+
+
 @pytest.mark.parametrize("contexts,keep", [([20000], 9000), ([70001], 60000), ([9000, 300, 12345], 4000)])
 def test_several_blocks_a_head(cp, contexts, keep):
     b = R.make_batch([(c, 0) for c in contexts], bf16=True, seed=6)

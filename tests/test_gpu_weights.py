@@ -129,6 +129,22 @@ def test_window(cp, name, bf16, decay, bound):
 
 
 @pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("lens,bound", [([(0, 1)], None), ([(100, 28)], None), ([(100, 29)], None), ([(1023, 1)], None), ([(1024, 32)], None),
+                                        ([(3039, 32)], None), ([(3045, 32)], None), ([(3000, 33)], None), ([(5, 9), (0, 32), (700, 17)], 1500),
+                                        ([(40 * i, 1 + i) for i in range(15)], 350), ([(0, 3), (2, 0), (1900, 8), (1300, 31)], None)])
+def test_windows_whose_products_are_kept(cp, bf16, lens, bound):
+    """As many keys as a cluster's tensor memory holds the products of, and a few more; segments without any."""
+    bound = max(c for c, _ in lens) if bound is None else max(bound, max(c for c, _ in lens))
+    b = R.make_batch(lens, bf16=bf16, seed=15, extra_blocks=bound // 16 + 2)
+    weighed = [max(0, c - 5) for c, _ in lens]
+    w, q = W.weight_pool(b, known=weighed), torch.randn(b["n"], 32, 64, device="cuda") * 2
+    before = w.clone()
+    weigh(cp, b, q, w, 0.9, ints(weighed), bound=bound)
+    assert cp.attn_get_device_error() == 0
+    check_weights(w, before, b, W.weigh_reference(q, b, before, weighed, 0.9))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("lens,bound", [([9000, 3, 0, 515, 8999] + [100 * i for i in range(11)], None),
                                         ([8192, 8191, 8177] + [31 * i for i in range(27)], None),
                                         ([16384, 16383, 12000, 5, 16000, 64, 65], 40000),

@@ -40,14 +40,15 @@
 #include "tc_ptx.cuh"
 #include "tensor_map.cuh"
 #include "tree.cuh"
+#include "weigh_tiles.cuh"
 
 namespace attn {
 namespace {
 
 using namespace tc;
 
-constexpr int kRows = 32;                  // rows of a block: 128 (row, head) pairs
-constexpr int kKeys = 128;                 // keys of a tile
+using weigh_tiles::kKeys;
+using weigh_tiles::kRows;
 constexpr int kPages = kKeys / ATTN_PAGE;
 constexpr int kGroups = 3, kSoft = 4 * kGroups;  // warps that read S
 constexpr int kChunk = 64;                 // columns of S that a thread has in registers
@@ -160,13 +161,13 @@ struct Work {
   int k0, k1;        // of these keys
   int rt0, rt1;      // and row tiles
   int ranks;         // fused: segments, the blocks of the cluster
-  float2* kept;      // fused: the rows' (reference, sum) over this block's keys
+  float2* kept;      // fused: [row tiles][128], the rows' (reference, sum) over this block's keys
   volatile int* abort_flag;
   // Keys that some row of row tile rt sees, and the tiles that hold them.
-  __device__ __forceinline__ int visible(int rt) const { return min(k1, seq.ctx + min(seq.rows, (rt + 1) * kRows)); }
+  __device__ __forceinline__ int visible(int rt) const { return weigh_tiles::visible(seq.ctx, seq.rows, k1, rt); }
   // Columns of S by key: the row tile's (row, head) pairs, in steps of 32.
   __device__ __forceinline__ int cols(int rt) const { return (min(seq.rows - rt * kRows, kRows) * kGroup + 31) / 32 * 32; }
-  __device__ __forceinline__ int tiles(int rt) const { return max(0, (visible(rt) - k0 + kKeys - 1) / kKeys); }
+  __device__ __forceinline__ int tiles(int rt) const { return weigh_tiles::tiles(seq.ctx, seq.rows, k0, k1, rt); }
 };
 
 // A pass's barriers.
@@ -197,13 +198,19 @@ struct Bars {
 
 // One pass of the block, every warp in its role. All warps meet at the end; after a wait that
 // ran out those that started copies and products have waited for them.
+//
+// It begins at the first row tile that sees a key of the segment, in every role. `qready` has one
+// phase a row tile, told apart by its parity alone, and what keeps the warps that write q from
+// completing two of them before the issuing warp has looked is that they wait for S of the tile
+// between: each row tile that is gone through has one.
 template <bool kF32, bool kByKey>
 __device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs& a, const Work& x_, uint64_t* bars) {
   using L = Lay<kF32, kByKey>;
   constexpr int kStages = L::kStages;
   uint8_t* const smem = x_.smem;
   const Seq& seq = x_.seq;
-  const int head = x_.head, b = x_.b, s = x_.s, k0 = x_.k0, k1 = x_.k1, rt0 = x_.rt0, rt1 = x_.rt1;
+  const int head = x_.head, b = x_.b, s = x_.s, k0 = x_.k0, k1 = x_.k1, rt1 = x_.rt1;
+  const int rt0 = weigh_tiles::first_seeing(seq.ctx, k0, k1, x_.rt0, rt1);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(kFull, tid >> 5, 0);
   const auto visible = [&](int rt) { return x_.visible(rt); };
@@ -393,6 +400,14 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs&
     float ref = kUnseen, l0 = 0.f, l1 = 0.f;
     const int weighed = kByKey ? (a.weighed_lens ? fetch(a.weighed_lens + b) : seq.ctx) : 0;
     int done = 0;  // tiles of the row tiles before
+    // What the rows pass leaves of a row tile, by the threads of one group.
+    const auto leave = [&](int rt, float2 all) {
+      if (x_.kept) x_.kept[rt * 128 + row] = all;
+      else if (rt * kRows + (row >> 2) < seq.rows)
+        a.stats[((size_t)(seq.first + rt * kRows + (row >> 2)) * kHQ + head * kGroup + (row & 3)) * a.splits + s] = all;
+    };
+    if (!kByKey && g == 0)
+      for (int rt = x_.rt0; rt < rt0; ++rt) leave(rt, make_float2(kUnseen, 0.f));
     for (int rt = rt0; rt < rt1; ++rt) {
       const int i0 = rt * kRows, nrows = min(kRows, seq.rows - i0);
       const bool in = (row >> 2) < nrows;
@@ -400,7 +415,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs&
       if (rt > rt0) {  // what the tile before needs is still in use; its weights are written
         int over;
         if (meet(kMeet, false, failed, lane, &over)) {
-          for (int x = rt; !kByKey && g == 0 && x_.kept && x < rt1; ++x) x_.kept[(x - rt0) * 128 + row] = make_float2(kUnseen, 0.f);
+          for (int x = rt; !kByKey && g == 0 && x < rt1; ++x) leave(x, make_float2(kUnseen, 0.f));
           break;
         }
       }
@@ -457,7 +472,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs&
 #pragma unroll
           for (int i = 0; i < kMaxCluster; ++i) {
             p[i] = make_float2(kUnseen, 0.f);
-            if (i < x_.ranks) p[i] = ld_cluster2(mapa_shared(smem_u32(x_.kept + (rt - rt0) * 128 + row), i));
+            if (i < x_.ranks) p[i] = ld_cluster2(mapa_shared(smem_u32(x_.kept + rt * 128 + row), i));
             top = fmaxf(top, p[i].x);
           }
 #pragma unroll
@@ -622,9 +637,7 @@ __device__ __forceinline__ void run_pass(const CUtensorMap& mk, const WeighArgs&
           float sum = ex2(ref - top) * (l0 + l1);
 #pragma unroll
           for (int x = 1; x < kGroups; ++x) sum = fmaf(ex2(ends[x * 128 + row].x - top), ends[x * 128 + row].y, sum);
-          const float2 all = lost ? make_float2(kUnseen, 0.f) : make_float2(top, sum);
-          if (x_.kept) x_.kept[(rt - rt0) * 128 + row] = all;
-          else if (in) a.stats[pair * a.splits + s] = all;
+          leave(rt, lost ? make_float2(kUnseen, 0.f) : make_float2(top, sum));
         }
         ref = kUnseen, l0 = l1 = 0.f;
       }
@@ -745,9 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_kernel(const __grid_constan
   x.rt1 = kPass == kRowsPass ? x.rt0 + 1 : (x.seq.rows + kRows - 1) / kRows;
   if (x.seq.rows - x.rt0 * kRows <= 0) return;  // of a cluster all blocks
   // The sequence's own keys, cut evenly into segments of whole tiles.
-  const int len = ((x.seq.keys + splits - 1) / splits + kKeys - 1) / kKeys * kKeys;
-  x.k0 = min((long long)x.s * len, (long long)x.seq.keys);
-  x.k1 = min((long long)x.k0 + len, (long long)x.seq.keys);
+  weigh_tiles::segment(x.seq.keys, splits, x.s, &x.k0, &x.k1);
   if (kPass == kKeysPass && x.k0 >= x.k1) return;
   x.ranks = splits;
   x.kept = kPass == kFused || kPass == kOnce ? reinterpret_cast<float2*>(smem + K::kSmemKept) : nullptr;

@@ -157,7 +157,6 @@ def load():
             lib.attn_naive_scores.argtypes = [vp, vp, vp, ci, ci, vp]
             lib.attn_naive_softmax.restype = ci
             lib.attn_naive_softmax.argtypes = [vp, ci, ci, vp]
-            cf = ctypes.c_float
             lib.attn_selftest_decode_weigh_timeout.restype = ci
             lib.attn_selftest_decode_weigh_timeout.argtypes = [vp] * 3 + [ci] + [vp] * 4 + [cf, vp] + [ci] * 5 + [vp, cs, vp]
             lib.attn_selftest_weigh_timeout.restype = ci

@@ -167,7 +167,7 @@ size_t tree_workspace_bytes(int N, const TreePlan& plan);
 int launch_tree(const TreeCall& c, unsigned* err, cudaStream_t stream);
 
 // A decode step that also adds what each cached token was given to its weight
-// (decode_weigh.cu): resident blocks of the device, workspace bytes, launch.
+// (decode_weigh.cu): workspace bytes, launch.
 struct DecodeWeighCall {
   const float* q;
   const void *k_pages, *v_pages;

@@ -21,8 +21,8 @@
 // last ones there, batch by batch.
 //
 // Bound by the moves' latency and bytes: 16 sequences of 16384 tokens to half (bf16 pages) read and
-// write 287 MB in the 80 us of the call with its 6 us of restored weights: select 20, move 45 (their
-// floor 43 together). Rows of 128 bytes at random places move at 6.2 TB/s.
+// write 287 MB in 80 us, the copy that restores their weights among them: select 21, move 50 (their
+// floor 43 together). Rows of 128 bytes at random places move at 5.5 TB/s.
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -38,7 +38,7 @@ constexpr unsigned kFull = 0xffffffffu;
 // a warp (within a few powers of two) seldom meet in a bin.
 constexpr int kBins = 4096, kFirst = 20, kDigit = 10;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxCached = 40960;  // tokens of a block whose keys stay in shared memory (160 KB of its 227; the rest takes 50)
+constexpr int kMaxCached = 40960;  // tokens of a block whose keys stay in shared memory: 160 KB of its 227, with Shared's 57
 struct EvictArgs {
   void *k_pages, *v_pages;
   float* weights;             // [num_pages][8][16]
@@ -537,8 +537,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictArgs a) {
 // registers, the first digit's bin settles all but a few keys, whose ranks are counted among
 // themselves (or, of many equal ones, by further digits), and what stays is a bit a token. A
 // cluster's blocks all find the same lists, in shared memory, and share the moves.
-// (One sequence of 1000 tokens: 8.5 us in a graph; 11.7 with the copy that restores its weights, 14.4 as two
-// launches; one of 4000, bf16 pages: 14.3 and 17.8; 64 of 4000: 76 and 85.)
+// (With the copy that restores its weights, one sequence of 1000 tokens: 9.6 us in a graph, of which the
+// copy is 1.0; call by call 12.2, as two launches 14.4. One of 4000, bf16 pages: 14.3 and 17.8; 64 of 4000: 76 and 85.)
 constexpr int kSmall = 4096, kSmallThreads = 512, kQuads = kSmall / 4 / kSmallThreads, kWords = kSmall / 32;
 constexpr int kRanked = 256;  // listed keys whose ranks are counted
 

@@ -24,9 +24,14 @@
 // key, windows of fewer rows take fewer columns. Fewer terms were measured and not kept: with two
 // bf16 terms in both passes 64 rows of 131071 tokens (bf16 pages) took 119 us for 144, 32 rows of
 // 16 sequences of 16384 (fp32) 205 for 278, but weights were off by 2e-6 to 4e-6 where a plain
-// fp32 computation is by 5e-7; in the rows pass alone, as much. Bound by the products: those 278
-// us are 1.37 PFLOP/s of tf32 terms at the rate of 174 us, and K's bytes, read twice, are 83 us;
-// the 144 are 112 of bf16 terms at the rate of a library product.
+// fp32 computation is by 5e-7; in the rows pass alone, as much.
+//
+// Bound by the products and by shared memory, neither full: those fp32 windows take 274 us in short
+// runs (2070 MHz) and 309 in long ones, which meet the power limit (1630 MHz). Their 206 GFLOP of
+// tf32 terms are 174 us at the rate of a dense loop, K's bytes, read twice, 83. In a short run the
+// tensor pipe is active for 70 % of the cycles and shared memory's data path for 65 (35 the products'
+// operand there, 30 the warps' loads and stores), K's landings not counted. The 64 rows on bf16
+// pages take 140 and 159 us, 112 of bf16 terms at the rate of a library product.
 //
 // Roles: three groups of four warps take the tiles in turn; four warps that write K_lo (fp32,
 // rows) or move K to tensor memory (keys); one warp for TMA (16-token pages through the block
@@ -63,7 +68,7 @@ struct WeighArgs {
   const float* q;          // [N][32][64]
   float* weights;          // [num_pages][8][16]
   const int *table, *ctx_lens, *row_start, *weighed_lens;
-  float2* stats;           // [N][32][splits]: log2 maximum, sum (both 0 of a segment without keys)
+  float2* stats;           // [N][32][splits]: log2 maximum, sum (kUnseen and 0 of a segment without keys)
   int B, N, max_rows, max_blocks, num_pages, max_context;
   int row_tiles, splits;   // of the rows pass
   int key_splits;          // of the keys pass
